@@ -18,7 +18,10 @@
  * or in two, with mt_tree_accept_commit doing the last two in one launch.
  * mt_tree_accept_typical replaces greedy acceptance by typical acceptance
  * (a tempered-probability threshold), and mt_tree_candidates builds the tree's
- * tokens from the Medusa heads before the step.
+ * tokens from the Medusa heads before the step.  Around the step:
+ * mt_qk_norm_rope normalises and rotates queries and keys, mt_kv_append_paged
+ * fills the cache, mt_tree_attn_paged_block8 attends over an 8-bit cache with
+ * block scales, and mt_sample_tokens draws a token.
  *
  * What the pages fix, per call:
  *  - vLLM issue 1171 "[Discussion] Will vLLM consider using Speculative
@@ -80,7 +83,8 @@ typedef enum {
   MT_ERR_TREE = -3,         /* (device) parents or depths violate the node-order rule */
   MT_ERR_PAGES = -4,        /* (device) page id out of range or block table too short */
   MT_ERR_CUDA = -5,         /* a CUDA runtime call failed */
-  MT_ERR_TIMEOUT = -6       /* (device) a bounded pipeline wait gave up */
+  MT_ERR_TIMEOUT = -6,      /* (device) a bounded pipeline wait gave up */
+  MT_ERR_POSITION = -7      /* (device) a position at or past the RoPE table's end */
 } mt_status;
 
 /* MT_E4M3 is a cache element type only (see mt_attn_desc.cache_dtype). */
@@ -323,6 +327,151 @@ int mt_tree_candidates(int batch, int tree_size, int heads, int vocab, mt_dtype 
                        const void* root_logits, const void* head_logits,
                        const int32_t* tree_parents, int32_t* tree_tokens, void* status_ws,
                        cudaStream_t stream);
+
+/* ---- Norms of queries and keys with the rotation ------------------------------
+ * Not on the pages; for models whose attention normalises every query and key
+ * head, and for the calls below, which take rotated rows.  For each token i and
+ * each head row x of q and k, in fp32 with one rounding to the act dtype:
+ *   y = x * rsqrt(mean(x^2) + eps) * weight   (weight act [D]; skipped when both
+ *                                              weights are null)
+ *   y rotated at positions[i] as defined above (skipped when rope is null).
+ * positions int32 [num_tokens] (may be null without rope): a negative entry
+ * marks a place without a token, whose rows of the outputs are left as they
+ * were; one at or past the table's end is recorded as MT_ERR_POSITION in
+ * status_ws (at least 256 bytes) and its rows are left as they were.
+ * Strides are in elements, (token, head); each a whole number of 16 bytes, the
+ * D elements of a row dense.  An output may be its own input (the same pointer
+ * and strides); other overlaps are not supported. */
+typedef struct {
+  int num_tokens;
+  int num_q_heads;
+  int num_kv_heads;
+  int head_dim;            /* 64 or 128 */
+  mt_dtype dtype;
+  float eps;
+  long long q_stride[2];
+  long long k_stride[2];
+  long long q_out_stride[2];
+  long long k_out_stride[2];
+} mt_norm_rope_desc;
+int mt_qk_norm_rope(const mt_norm_rope_desc* desc, const void* q, const void* k, const int32_t* positions,
+                    const void* q_weight, const void* k_weight, const mt_rope* rope, void* q_out,
+                    void* k_out, void* status_ws, cudaStream_t stream);
+
+/* ---- Appending keys and values to the paged cache ------------------------------
+ * How a prompt's rows, or an accepted path's, get into the pages.  New row i of
+ * sequence b goes to logical slot seq_lens[b] + i; its key is rotated at that
+ * position when rope is given (rounded once to the act dtype, the same
+ * arithmetic as mt_tree_attn_paged), its value is stored as given.  seq_lens
+ * and block_tables are read only: a model's layers append with the same lengths,
+ * and the caller grows them once.
+ *   mt_kv_append_paged     sequence b's new rows are k/v rows row_offsets[b] ..
+ *                          row_offsets[b + 1] - 1 (int32 [B + 1], never falling,
+ *                          within [0, num_rows]; other rows are ignored);
+ *   mt_kv_append_accepted  k and v are the tree's rows [B][T] (num_rows = B * T)
+ *                          and row i is node accept_path[b][i], i = 0 ..
+ *                          accept_len[b] (as mt_tree_accept_greedy gives them):
+ *                          the commit of a cache that mt_tree_attn_paged_block8
+ *                          reads.
+ * The cache holds the act dtype (cache_dtype 0), E4M3 codes of value / k_scale
+ * and value / v_scale (MT_E4M3 without scale arrays), or E4M3 codes with a scale
+ * for each block, one page of one KV head (MT_E4M3 with k_scales and v_scales,
+ * fp32 [num_pages][Hkv]):
+ *   scale = the smallest power of two 2^k, -64 <= k <= 119, with
+ *           largest |value| of the block <= 448 * 2^k;
+ *   a page that already holds older rows of its sequence keeps the larger of
+ *   its scale and the new rows'; when that grows, the older rows' codes become
+ *   the codes of (their value / the new scale), rounded to nearest even.
+ * A NaN is stored as the NaN code and does not enter the scale; an infinity
+ * makes the scale 2^119 and saturates.
+ * A sequence with seq_lens[b] < 0 is no sequence: nothing is written for it.
+ * Device status (status_ws, at least 256 bytes): MT_ERR_PAGES for offsets or
+ * nodes out of range, a table that does not cover the slots (nothing of that
+ * sequence is written), a page id out of range (nothing of that page is
+ * written); MT_ERR_POSITION for a slot past the RoPE table (nothing of that
+ * page is written).  Two sequences must not append to the same page.
+ * Strides of k and v in elements, (row, head), whole numbers of 16 bytes. */
+typedef struct {
+  int batch;
+  int num_rows;
+  int num_kv_heads;
+  int head_dim;            /* 64 or 128 */
+  int page_size;           /* 16 */
+  int max_blocks_per_seq;
+  int num_pages;
+  mt_dtype dtype;
+  int cache_dtype;         /* 0 or MT_E4M3 */
+  float k_scale;           /* MT_E4M3 without scale arrays */
+  float v_scale;
+  long long k_stride[2];
+  long long v_stride[2];
+} mt_append_desc;
+int mt_kv_append_paged(const mt_append_desc* desc, const void* k, const void* v,
+                       const int32_t* row_offsets, const mt_rope* rope, void* k_cache, void* v_cache,
+                       float* k_scales, float* v_scales, const int32_t* block_tables,
+                       const int32_t* seq_lens, void* status_ws, cudaStream_t stream);
+int mt_kv_append_accepted(const mt_append_desc* desc, int tree_size, int max_depth, const void* k,
+                          const void* v, const int32_t* accept_path, const int32_t* accept_len,
+                          const mt_rope* rope, void* k_cache, void* v_cache, float* k_scales,
+                          float* v_scales, const int32_t* block_tables, const int32_t* seq_lens,
+                          void* status_ws, cudaStream_t stream);
+
+/* ---- Tree attention over a block-scaled 8-bit cache ----------------------------
+ * As mt_tree_attn_paged, with three differences:
+ *   - the cache holds E4M3 codes with a scale for each (page, KV head), as
+ *     mt_kv_append_paged writes them, and is only read: no scratch slots, and the
+ *     table need cover slots 0 .. seq_lens[b] - 1 only;
+ *   - q and k_new are rows as they attend (rotated by mt_qk_norm_rope);
+ *   - the tree's own keys and values are seen as they will be stored, as E4M3
+ *     codes in blocks of 16 nodes (nodes 16j .. 16j + 15 of one KV head) with the
+ *     block scale above.
+ * T = 1 is a decoding step (tree_parents null, or -1); tree_parents null is a
+ * chain, each node the child of the one before it.
+ *   q [B][T][Hq][D], k_new, v_new [B][T][Hkv][D], out [B][T][Hq][D]  act (fp16 or bf16)
+ *   k_cache, v_cache [num_pages][Hkv][16][D] codes; k_scales, v_scales fp32
+ *   [num_pages][Hkv], finite and positive
+ * A sequence with seq_lens[b] < 0 is no sequence: its rows of out are left as
+ * they were.  desc: dtype MT_F16 or MT_BF16, cache_dtype MT_E4M3; num_splits,
+ * kernel, k_scale and v_scale are not used; any number of query heads per KV
+ * head.  Accumulation in fp32; queries keep their bits, softmax weights are
+ * rounded to fp16, and a split segment's pieces to the act dtype.
+ * workspace: mt_tree_attn_block8_workspace_size(desc) bytes, zero-filled before
+ * its first use (status word, schedule, partial results); calls that share one
+ * must not overlap.  Device status: MT_ERR_PAGES (length past the table, page id
+ * out of range), MT_ERR_TREE (a parent that is not earlier); the outputs of an
+ * affected sequence are unspecified. */
+size_t mt_tree_attn_block8_workspace_size(const mt_attn_desc* desc);
+int mt_tree_attn_paged_block8(const mt_attn_desc* desc, const void* q, const void* k_new,
+                              const void* v_new, const void* k_cache, const void* v_cache,
+                              const float* k_scales, const float* v_scales,
+                              const int32_t* block_tables, const int32_t* seq_lens,
+                              const int32_t* tree_parents, void* out, void* workspace,
+                              size_t ws_bytes, cudaStream_t stream);
+
+/* ---- Sampling --------------------------------------------------------------------
+ * A drawn token beside the argmax that greedy and typical acceptance return (the
+ * bonus token of an accepted path's last row, or a decoding step's).  For each i,
+ * with x the logits row row_index[i] (row i when row_index is null), m its
+ * maximum and t = temperature[i]:
+ *   w_v = exp((x_v - m) / t); the tokens are ordered by larger x, then lower
+ *   index; kept are those among the first top_k[i], with (mass before them) <
+ *   top_p[i] * (mass of the first top_k[i]), and with w_v >= min_p[i]; the first
+ *   is always kept; tokens[i] = the lowest v for which the kept mass of tokens
+ *   0 .. v exceeds uniforms[i] * (kept mass).
+ * t <= 0: the argmax (lowest index among equals).  top_k <= 0 or >= vocab,
+ * top_p >= 1, min_p <= 0: off.  A null parameter array: temperature 1, filters
+ * off.  uniforms: numbers of [0, 1), others are clamped.  A NaN logit counts as
+ * -inf; a row without anything above -inf gives -1; entries of +inf share the
+ * whole mass.  Sums are exact integers of weights good to 1e-9, so the token is
+ * that of the definition unless u lies that close to a border.  Weights below
+ * 2^-41 of the largest count as 0.
+ * row_index[i] < 0: no row, tokens[i] is left as it was; >= num_logit_rows: -1.
+ * row_stride in elements; rows need no alignment.  vocab <= 500000
+ * (MT_ERR_UNSUPPORTED above).  No workspace and no device status. */
+int mt_sample_tokens(int num_rows, int vocab, mt_dtype logits_dtype, const void* logits,
+                     int num_logit_rows, long long row_stride, const int32_t* row_index,
+                     const float* uniforms, const float* temperature, const int32_t* top_k,
+                     const float* top_p, const float* min_p, int32_t* tokens, cudaStream_t stream);
 
 /* ---- Status ------------------------------------------------------------------
  * Waits for `stream`, then reads and clears the device status word at the start

@@ -12,6 +12,11 @@ Calls (same names as the C ABI without the ``mt_`` prefix):
   kv_commit          move accepted K/V into place, grow lengths, release pages
   tree_accept_commit the last two in one launch
   tree_candidates    the tree's tokens from the base and Medusa-head logits
+  qk_norm_rope       norms of query and key heads, with the rotation in the same pass
+  kv_append_paged    new keys and values into the paged cache (prompts, decoding steps)
+  kv_append_accepted an accepted path's keys and values into the paged cache
+  tree_attn_paged_block8  tree attention over an 8-bit cache with a scale per page and head
+  sample_tokens      temperature, top-k, top-p and min-p from given uniform numbers
 """
 from __future__ import annotations
 
@@ -47,6 +52,23 @@ class AttnDesc(ctypes.Structure):
                 ("v_scale", ctypes.c_float)]
 
 
+class NormRopeDesc(ctypes.Structure):
+    _fields_ = [("num_tokens", ctypes.c_int), ("num_q_heads", ctypes.c_int),
+                ("num_kv_heads", ctypes.c_int), ("head_dim", ctypes.c_int), ("dtype", ctypes.c_int),
+                ("eps", ctypes.c_float), ("q_stride", ctypes.c_longlong * 2),
+                ("k_stride", ctypes.c_longlong * 2), ("q_out_stride", ctypes.c_longlong * 2),
+                ("k_out_stride", ctypes.c_longlong * 2)]
+
+
+class AppendDesc(ctypes.Structure):
+    _fields_ = [("batch", ctypes.c_int), ("num_rows", ctypes.c_int), ("num_kv_heads", ctypes.c_int),
+                ("head_dim", ctypes.c_int), ("page_size", ctypes.c_int),
+                ("max_blocks_per_seq", ctypes.c_int), ("num_pages", ctypes.c_int),
+                ("dtype", ctypes.c_int), ("cache_dtype", ctypes.c_int), ("k_scale", ctypes.c_float),
+                ("v_scale", ctypes.c_float), ("k_stride", ctypes.c_longlong * 2),
+                ("v_stride", ctypes.c_longlong * 2)]
+
+
 _lib = None
 
 
@@ -75,6 +97,15 @@ def _load():
         lib.mt_kv_commit.argtypes = [D, I] + [P] * 8 + [P]
         lib.mt_tree_accept_commit.argtypes = [D, I, I, I] + [P] * 12 + [P, Z, P]
         lib.mt_tree_candidates.argtypes = [I, I, I, I, I] + [P] * 5 + [P]
+        L = ctypes.c_longlong
+        lib.mt_qk_norm_rope.argtypes = [ctypes.POINTER(NormRopeDesc)] + [P] * 10
+        A = ctypes.POINTER(AppendDesc)
+        lib.mt_kv_append_paged.argtypes = [A] + [P] * 12
+        lib.mt_kv_append_accepted.argtypes = [A, I, I] + [P] * 13
+        lib.mt_tree_attn_block8_workspace_size.argtypes = [D]
+        lib.mt_tree_attn_block8_workspace_size.restype = Z
+        lib.mt_tree_attn_paged_block8.argtypes = [D] + [P] * 12 + [Z, P]
+        lib.mt_sample_tokens.argtypes = [I, I, I, P, I, L] + [P] * 7 + [P]
         lib.mt_read_status.argtypes = [P, P, ctypes.POINTER(I)]
         lib.mt_profile_enable.argtypes = [I]
         lib.mt_profile_read.argtypes = [ctypes.POINTER(ctypes.c_float), I, ctypes.POINTER(I)]
@@ -430,6 +461,279 @@ def tree_candidates(root_logits, head_logits, tree_parents, tree_tokens, *, stat
                                     _ptr(status_ws), _stream(stream))
     _check(st, "mt_tree_candidates")
     return tree_tokens
+
+
+# ---- the serving operators around the step ----------------------------------
+#
+# One check per argument (dtype, shape, device, layout), then the call on the
+# arguments' device: a decoding step makes a dozen of these calls per layer, so
+# the checks are kept short.
+
+_E4M3 = torch.float8_e4m3fn
+
+
+def _arg(t, name, dtype, shape, dev):
+    """A dense CUDA tensor of this dtype, shape and device; its address."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype is not dtype:
+        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    if t.device != dev:
+        raise ValueError(f"{name} is on {t.device}, the other tensors on {dev}")
+    return t.data_ptr()
+
+
+def _rows_arg(t, name, dtype, shape, dev):
+    """A CUDA tensor [rows, heads, D] whose head rows are dense and 16-byte
+    aligned (a view of a projection's output, say); its address and strides."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype is not dtype:
+        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    if t.device != dev:
+        raise ValueError(f"{name} is on {t.device}, the other tensors on {dev}")
+    st = t.stride()
+    s0, s1 = st[0] if shape[0] > 1 else 0, st[1] if shape[1] > 1 else 0
+    unit = 16 // t.element_size()
+    if st[2] != 1 or s0 % unit or s1 % unit or t.data_ptr() % 16:
+        raise ValueError(f"{name} must have dense, 16-byte aligned head rows, got strides {st}")
+    return t.data_ptr(), (s0, s1)
+
+
+def _cuda_device(t, name):
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be on a CUDA device, got {t.device}")
+    return t.device
+
+
+def _act(t, name, kinds=_DTYPES):
+    if t.dtype not in kinds:
+        raise ValueError(f"{name} must be one of {sorted(str(k) for k in kinds)}, got {t.dtype}")
+    return _DTYPES[t.dtype]
+
+
+def _status_arg(t, name, dev, nbytes=256):
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.device != dev or not t.is_contiguous() or t.numel() * t.element_size() < nbytes:
+        raise ValueError(f"{name} must be a dense tensor of at least {nbytes} bytes on {dev}")
+    return t.data_ptr()
+
+
+def _invoke(fn, what, dev, stream, *args):
+    """The call on its tensors' device: on `stream`, or that device's current one."""
+    if torch.cuda.current_device() == dev.index:
+        if stream is None:
+            stream = torch.cuda.current_stream()
+        st = fn(*args, stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream))
+    else:
+        with torch.cuda.device(dev):
+            if stream is None:
+                stream = torch.cuda.current_stream()
+            st = fn(*args, stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream))
+    if st != MT_OK:
+        raise MedusaTreeError(st, what)
+
+
+def qk_norm_rope(q, k, positions, q_out, k_out, *, rope: Optional[Rope] = None, q_weight=None,
+                 k_weight=None, eps: float = 1e-6, status_ws: torch.Tensor, stream=None):
+    """Norms every head row of q [N,Hq,D] and k [N,Hkv,D] (with weights [D]) and
+    rotates it at positions[i] (with rope), into q_out and k_out (which may be q
+    and k).  A negative position leaves its rows as they were.  q, k and the
+    outputs may be views with dense head rows."""
+    dev = _cuda_device(q, "q")
+    dt = _act(q, "q")
+    if q.dim() != 3 or not isinstance(k, torch.Tensor) or k.dim() != 3:
+        raise ValueError("q and k must have 3 dims (tokens, heads, head_dim)")
+    n, hq, d = q.shape
+    hkv = k.shape[1]
+    qp, qs = _rows_arg(q, "q", q.dtype, (n, hq, d), dev)
+    kp, ks = _rows_arg(k, "k", q.dtype, (n, hkv, d), dev)
+    qop, qos = _rows_arg(q_out, "q_out", q.dtype, (n, hq, d), dev)
+    kop, kos = _rows_arg(k_out, "k_out", q.dtype, (n, hkv, d), dev)
+    if (n > 1 and not (qos[0] and kos[0])) or (hq > 1 and not qos[1]) or (hkv > 1 and not kos[1]):
+        raise ValueError("q_out and k_out must not be expanded views")
+    pos = None if positions is None else _arg(positions, "positions", torch.int32, (n,), dev)
+    if rope is not None and positions is None:
+        raise ValueError("a rotation needs positions")
+    if (q_weight is None) != (k_weight is None):
+        raise ValueError("q_weight and k_weight go together")
+    if q_weight is None and rope is None:
+        raise ValueError("nothing to do: neither weights nor rope")
+    qw = None if q_weight is None else _arg(q_weight, "q_weight", q.dtype, (d,), dev)
+    kw = None if k_weight is None else _arg(k_weight, "k_weight", q.dtype, (d,), dev)
+    desc = NormRopeDesc(n, hq, hkv, d, dt, eps, qs, ks, qos, kos)
+    _invoke(_load().mt_qk_norm_rope, "mt_qk_norm_rope", dev, stream, desc, qp, kp, pos, qw, kw,
+            None if rope is None else rope.handle, qop, kop, _status_arg(status_ws, "status_ws", dev))
+    return q_out, k_out
+
+
+def _append_args(k, v, k_cache, v_cache, block_tables, seq_lens, k_scales, v_scales, k_scale, v_scale):
+    """Checks shared by the appends: the descriptor and the addresses."""
+    dev = _cuda_device(k, "k")
+    dt = _act(k, "k")
+    n, hkv, d = k.shape
+    kp, ks = _rows_arg(k, "k", k.dtype, (n, hkv, d), dev)
+    vp, vs = _rows_arg(v, "v", k.dtype, (n, hkv, d), dev)
+    if not isinstance(k_cache, torch.Tensor) or k_cache.dim() != 4:
+        raise ValueError("k_cache must have 4 dims (pages, heads, slots, head_dim)")
+    cdt = k_cache.dtype
+    if cdt is not k.dtype and cdt is not _E4M3:
+        raise ValueError(f"k_cache must be {k.dtype} or {_E4M3}, got {cdt}")
+    pages, page = k_cache.shape[0], k_cache.shape[2]
+    kcp = _arg(k_cache, "k_cache", cdt, (pages, hkv, page, d), dev)
+    vcp = _arg(v_cache, "v_cache", cdt, (pages, hkv, page, d), dev)
+    if not isinstance(block_tables, torch.Tensor) or block_tables.dim() != 2:
+        raise ValueError("block_tables must have 2 dims")
+    b, blocks = block_tables.shape
+    btp = _arg(block_tables, "block_tables", torch.int32, (b, blocks), dev)
+    slp = _arg(seq_lens, "seq_lens", torch.int32, (b,), dev)
+    if (k_scales is None) != (v_scales is None):
+        raise ValueError("k_scales and v_scales go together")
+    ksp = vsp = None
+    if k_scales is not None:
+        if cdt is not _E4M3:
+            raise ValueError(f"block scales need a cache of {_E4M3}")
+        ksp = _arg(k_scales, "k_scales", torch.float32, (pages, hkv), dev)
+        vsp = _arg(v_scales, "v_scales", torch.float32, (pages, hkv), dev)
+    desc = AppendDesc(b, n, hkv, d, page, blocks, pages, dt, MT_E4M3 if cdt is _E4M3 else 0, k_scale,
+                      v_scale, ks, vs)
+    return dev, desc, (kp, vp), (kcp, vcp, ksp, vsp, btp, slp)
+
+
+def kv_append_paged(k, v, k_cache, v_cache, block_tables, seq_lens, row_offsets, *,
+                    status_ws: torch.Tensor, rope: Optional[Rope] = None, k_scales=None, v_scales=None,
+                    k_scale: float = 1.0, v_scale: float = 1.0, stream=None):
+    """New keys and values k, v [N,Hkv,D] into the paged cache: rows
+    row_offsets[b] .. row_offsets[b+1]-1 go to sequence b's slots from
+    seq_lens[b] on, the keys rotated at their slots (with rope).  The cache holds
+    k's dtype, E4M3 codes under k_scale / v_scale, or E4M3 codes under
+    k_scales / v_scales [pages,Hkv] (updated).  seq_lens is not changed."""
+    if not isinstance(k, torch.Tensor) or k.dim() != 3:
+        raise ValueError("k must have 3 dims (rows, heads, head_dim)")
+    dev, desc, kv, rest = _append_args(k, v, k_cache, v_cache, block_tables, seq_lens, k_scales,
+                                       v_scales, k_scale, v_scale)
+    off = _arg(row_offsets, "row_offsets", torch.int32, (desc.batch + 1,), dev)
+    _invoke(_load().mt_kv_append_paged, "mt_kv_append_paged", dev, stream, desc, *kv, off,
+            None if rope is None else rope.handle, *rest, _status_arg(status_ws, "status_ws", dev))
+
+
+def kv_append_accepted(k_new, v_new, accept_path, accept_len, k_cache, v_cache, block_tables, seq_lens,
+                       *, status_ws: torch.Tensor, rope: Optional[Rope] = None, k_scales=None,
+                       v_scales=None, k_scale: float = 1.0, v_scale: float = 1.0, stream=None):
+    """The accepted path's keys and values into the paged cache: row i of
+    sequence b is node accept_path[b,i] of k_new, v_new [B,T,Hkv,D], i up to
+    accept_len[b].  Otherwise as kv_append_paged; seq_lens is not changed (it
+    grows by accept_len + 1 once every layer has appended)."""
+    if not isinstance(k_new, torch.Tensor) or k_new.dim() != 4:
+        raise ValueError("k_new must have 4 dims (batch, tree, heads, head_dim)")
+    if not isinstance(v_new, torch.Tensor) or v_new.shape != k_new.shape:
+        raise ValueError("v_new must have k_new's shape")
+    if not k_new.is_contiguous() or not v_new.is_contiguous():
+        raise ValueError("k_new and v_new must be contiguous")
+    b, t, hkv, d = k_new.shape
+    dev, desc, kv, rest = _append_args(k_new.view(b * t, hkv, d), v_new.view(b * t, hkv, d), k_cache,
+                                       v_cache, block_tables, seq_lens, k_scales, v_scales, k_scale,
+                                       v_scale)
+    if desc.batch != b:
+        raise ValueError("block_tables must have one row per sequence")
+    if not isinstance(accept_path, torch.Tensor) or accept_path.dim() != 2:
+        raise ValueError("accept_path must have 2 dims")
+    path = _arg(accept_path, "accept_path", torch.int32, (b, accept_path.shape[1]), dev)
+    length = _arg(accept_len, "accept_len", torch.int32, (b,), dev)
+    _invoke(_load().mt_kv_append_accepted, "mt_kv_append_accepted", dev, stream, desc, t,
+            accept_path.shape[1] - 1, *kv, path, length, None if rope is None else rope.handle, *rest,
+            _status_arg(status_ws, "status_ws", dev))
+
+
+def _block8_desc(q, k_cache, block_tables, sm_scale=0.0):
+    b, t, hq, d = q.shape
+    pages, hkv, page = k_cache.shape[:3]
+    return AttnDesc(b, t, hq, hkv, d, page, block_tables.shape[1], pages, 0, _DTYPES[q.dtype], sm_scale,
+                    0, MT_E4M3, 1.0, 1.0)
+
+
+def alloc_block8_workspace(q, k_cache, block_tables) -> torch.Tensor:
+    """The workspace of tree_attn_paged_block8 for these sizes, on q's device."""
+    dev = _cuda_device(q, "q")
+    _act(q, "q", (torch.float16, torch.bfloat16))
+    with torch.cuda.device(dev):
+        n = int(_load().mt_tree_attn_block8_workspace_size(ctypes.byref(_block8_desc(q, k_cache, block_tables))))
+    if n == 0:
+        raise MedusaTreeError(-1, "mt_tree_attn_block8_workspace_size")
+    return torch.zeros(n, dtype=torch.uint8, device=dev)
+
+
+def tree_attn_paged_block8(q, k_cache, v_cache, k_scales, v_scales, block_tables, seq_lens,
+                           tree_parents, out, *, k_new, v_new, workspace: torch.Tensor,
+                           sm_scale: float = 0.0, stream=None):
+    """out[b,i,h] = attention of new token i (head h) over the cached slots
+    0 .. seq_lens[b]-1 and its tree ancestors, itself included (tree_parents
+    None: the tokens are a chain; T = 1: a decoding step).
+
+    The cache holds E4M3 codes under k_scales / v_scales [pages,Hkv] and is only
+    read; q and k_new are rotated already (qk_norm_rope); the new keys and values
+    are seen as kv_append_paged would store them, in blocks of 16 tokens.  A
+    sequence with seq_lens[b] < 0 leaves its rows of out as they were."""
+    dev = _cuda_device(q, "q")
+    dt = q.dtype
+    _act(q, "q", (torch.float16, torch.bfloat16))
+    if q.dim() != 4 or not isinstance(k_cache, torch.Tensor) or k_cache.dim() != 4:
+        raise ValueError("q and k_cache must have 4 dims")
+    b, t, hq, d = q.shape
+    pages, hkv, page = k_cache.shape[:3]
+    if not isinstance(block_tables, torch.Tensor) or block_tables.dim() != 2:
+        raise ValueError("block_tables must have 2 dims")
+    cache, scales, new = (pages, hkv, page, d), (pages, hkv), (b, t, hkv, d)
+    desc = _block8_desc(q, k_cache, block_tables, sm_scale)
+    _invoke(_load().mt_tree_attn_paged_block8, "mt_tree_attn_paged_block8", dev, stream, desc,
+            _arg(q, "q", dt, (b, t, hq, d), dev), _arg(k_new, "k_new", dt, new, dev),
+            _arg(v_new, "v_new", dt, new, dev), _arg(k_cache, "k_cache", _E4M3, cache, dev),
+            _arg(v_cache, "v_cache", _E4M3, cache, dev),
+            _arg(k_scales, "k_scales", torch.float32, scales, dev),
+            _arg(v_scales, "v_scales", torch.float32, scales, dev),
+            _arg(block_tables, "block_tables", torch.int32, (b, block_tables.shape[1]), dev),
+            _arg(seq_lens, "seq_lens", torch.int32, (b,), dev),
+            None if tree_parents is None else _arg(tree_parents, "tree_parents", torch.int32, (b, t), dev),
+            _arg(out, "out", dt, (b, t, hq, d), dev), _status_arg(workspace, "workspace", dev),
+            workspace.numel() * workspace.element_size())
+    return out
+
+
+def sample_tokens(logits, uniforms, tokens, *, temperature=None, top_k=None, top_p=None, min_p=None,
+                  row_index=None, stream=None):
+    """Draws tokens[i] from row row_index[i] (row i without it) of logits [R,V]
+    with the given uniforms [N]: temperature (<= 0: the argmax), top_k, top_p and
+    min_p are tensors [N] or None.  Rows of logits may be strided; a negative
+    row_index leaves its token as it was."""
+    dev = _cuda_device(logits, "logits")
+    dt = _act(logits, "logits")
+    if logits.dim() != 2:
+        raise ValueError("logits must have 2 dims")
+    r, v = logits.shape
+    st = logits.stride()
+    if v > 1 and st[1] != 1:
+        raise ValueError("logits must have dense rows")
+    n = r
+    if row_index is not None:
+        if not isinstance(row_index, torch.Tensor) or row_index.dim() != 1:
+            raise ValueError("row_index must have 1 dim")
+        n = row_index.shape[0]
+    f32, i32, one = torch.float32, torch.int32, (n,)
+    opt = lambda t, name, ty: None if t is None else _arg(t, name, ty, one, dev)  # noqa: E731
+    _invoke(_load().mt_sample_tokens, "mt_sample_tokens", dev, stream, n, v, dt, logits.data_ptr(), r,
+            st[0] if r > 1 else 0, opt(row_index, "row_index", i32), _arg(uniforms, "uniforms", f32, one, dev),
+            opt(temperature, "temperature", f32), opt(top_k, "top_k", i32), opt(top_p, "top_p", f32),
+            opt(min_p, "min_p", f32), _arg(tokens, "tokens", i32, one, dev))
+    return tokens
 
 
 def read_status(workspace: torch.Tensor, stream=None) -> int:

@@ -5,19 +5,7 @@
 #include <cstring>
 #include <vector>
 
-#include <nvtx3/nvToolsExt.h>
-
-#include "../../include/medusa_tree.h"
-#include "kernels.cuh"
-
-// One NVTX range per library call, named after its C entry point, for a
-// timeline tool (nothing is recorded unless such a tool is attached).
-struct mt_call_range {
-  explicit mt_call_range(const char* name) { nvtxRangePushA(name); }
-  ~mt_call_range() { nvtxRangePop(); }
-  mt_call_range(const mt_call_range&) = delete;
-  mt_call_range& operator=(const mt_call_range&) = delete;
-};
+#include "api_common.cuh"
 
 // Bound of the tensor-core kernel's pipeline waits, and the timeout test hook
 // (mt_debug_set_wait); read by every attention call.
@@ -29,23 +17,9 @@ static cudaEvent_t* g_prof_ev = nullptr;  // [cap][2]
 static int g_prof_cap = 0;
 static int g_prof_n = 0;
 
-struct mt_rope {
-  float2* table;  // [max_pos][D/2] (cos, sin)
-  int head_dim;
-  int max_pos;
-  int device;
-};
-
 namespace {
 
 using namespace mt;
-
-constexpr size_t kAlign = 256;
-constexpr int kMaxBatch = 8192;
-
-size_t align_up(size_t x) { return (x + kAlign - 1) / kAlign * kAlign; }
-
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
 
 int elem_bytes(mt_dtype dt) { return dt == MT_F32 ? 4 : 2; }
 
@@ -135,8 +109,6 @@ int check_desc(const mt_attn_desc* d) {
   return MT_OK;
 }
 
-int cuda_status(cudaError_t e) { return e == cudaSuccess ? MT_OK : MT_ERR_CUDA; }
-
 }  // namespace
 
 extern "C" {
@@ -152,6 +124,7 @@ const char* mt_status_string(int s) {
     case MT_ERR_PAGES: return "page id out of range or block table too short";
     case MT_ERR_CUDA: return "CUDA runtime error";
     case MT_ERR_TIMEOUT: return "bounded device wait gave up";
+    case MT_ERR_POSITION: return "position outside the RoPE table";
     default: return "unknown status";
   }
 }

@@ -1,0 +1,627 @@
+// Tree attention over a paged cache of E4M3 codes with one scale for each
+// (page, KV head), fp16/bf16 activations.
+//
+// The T new tokens of a sequence (T = 1: a decoding step) attend to its L
+// cached slots and to their own tree ancestors (the Medusa tree mask, vLLM
+// issue 1171); the cache is only read.  The new keys and values are seen as
+// they will be stored: in blocks of 16 new tokens, each block of a KV head
+// under its own power-of-two scale, so the values do not change when an
+// accepted token is appended (beyond codes that underflow).
+//
+// With few query rows (T * g for g query heads per KV head) the cache's bytes
+// bound the work, so the codes go from memory to the matrix instructions with
+// as few steps as possible: each warp owns a page at a time, brings its 16 keys
+// and values into a ring of its own (cp.async, no barrier between warps), reads
+// them as fragments and converts in registers (one instruction for two codes;
+// every E4M3 value is exact in fp16).  Both products are m16n8k16 fp16 with
+// fp32 accumulators.
+//   S = Q K^T: any order of the D products is the same sum, so a lane takes 16
+//     consecutive bytes of a key row as four k-steps of four, and Q is held in
+//     the same order;
+//   O = P V:   a lane takes 8 or 16 consecutive columns of four value rows
+//     (n-tile t of column group n is column n * (D/8) + t), and a byte permute
+//     pairs two rows' codes before the conversion.
+// Queries are scaled to a power of two per row (exact; a bf16 query keeps all
+// its bits in fp16).  Softmax in base 2 with a lazily moved maximum; P carries
+// 2^3 * v_scale / v_ref, v_ref a running power-of-two reference, so that fp16
+// holds weights from 2^11 down to 2^-24 of it.
+//
+// The batch's 64-slot tiles (four pages, one a warp) are dealt out evenly over
+// persistent CTAs (common.cuh's balanced schedule, its prefix computed by every
+// CTA from the lengths); pieces of a split segment are joined by the combine.
+#include <atomic>
+
+#include "serve.cuh"
+
+namespace mt {
+
+namespace {
+
+constexpr int kWarps = 4;
+constexpr int kThreads = kWarps * 32;
+constexpr int kP = 16;
+constexpr int kMaxDevices = 64;
+
+// MT: 16-row tiles of query rows a CTA holds.
+template <int D, int MT>
+struct Cfg {
+  static constexpr int CTAS = MT == 1 ? 3 : 2;  // per SM, by registers
+  static constexpr int DEPTH = MT == 1 ? 4 : 6;  // pages a warp keeps in flight
+  static constexpr int kPage = 16 * D;           // bytes of a page's K or V
+  static constexpr int kRing = kWarps * DEPTH * 2 * kPage;
+  static constexpr int LDO = D + 4;              // merge rows, in floats
+  static constexpr int kMerge = kWarps * 16 * LDO * 4;
+  static constexpr int kSmem = kRing > kMerge ? kRing : kMerge;
+};
+
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+__device__ __forceinline__ void mma(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ float fast_exp2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+__device__ __forceinline__ uint32_t pack_h2(float a, float b) {
+  const __half2 h = __floats2half2_rn(a, b);
+  uint32_t r;
+  memcpy(&r, &h, 4);
+  return r;
+}
+
+// Byte offset of 16-byte chunk ch of row r in a page's K or V: chunks are
+// permuted within a row so that the fragment reads (eight lanes a phase: K two
+// rows of four chunks, V four even or odd rows of two) hit distinct banks.
+template <int D>
+__device__ __forceinline__ int k_off(int r, int ch) {
+  return r * D + ((D == 128 ? ch ^ ((r & 1) << 2) : ch) << 4);
+}
+template <int D>
+__device__ __forceinline__ int v_off(int r, int ch) {
+  return r * D + ((D == 128 ? ch ^ (((r >> 1) & 3) << 1) : ch ^ ((r >> 1) & 3)) << 4);
+}
+
+// One warp's running result for MT * 16 query rows.
+template <int D, int MT>
+struct State {
+  uint32_t q[MT][D / 16][4];
+  float o[MT][D / 8][4];
+  float m[MT][2], l[MT][2];  // rows gid and gid + 8 of each tile; l is this lane's part
+  float c[MT][2];            // score -> base-2 units, without the page's scale
+  float v_ref;
+
+  __device__ __forceinline__ void clear() {
+#pragma unroll
+    for (int i = 0; i < MT; ++i) {
+#pragma unroll
+      for (int t = 0; t < D / 8; ++t)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[i][t][e] = 0.f;
+      m[i][0] = m[i][1] = -INFINITY;
+      l[i][0] = l[i][1] = 0.f;
+    }
+    v_ref = 0.f;
+  }
+};
+
+// Which of a page's 16 keys a row sees: every one, those before a limit, or
+// those of an ancestor mask.
+enum : int { kSeeAll, kSeeLimit, kSeeMask };
+
+// Folds one page (codes in shared memory) into the running result.
+template <int D, int MT, int SEE>
+__device__ __forceinline__ void page_step(State<D, MT>& st, const uint8_t* kp, const uint8_t* vp, float ks, float vs,
+                                          int limit, const unsigned (&see)[MT][2]) {
+  const int lane = threadIdx.x & 31, gid = lane >> 2, tig = lane & 3;
+  constexpr int CH = D / 64;  // 16-byte chunks of a key row per lane
+  float s[MT][2][4];
+#pragma unroll
+  for (int j = 0; j < 2; ++j) {
+#pragma unroll
+    for (int i = 0; i < MT; ++i)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) s[i][j][e] = 0.f;
+#pragma unroll
+    for (int ch = 0; ch < CH; ++ch) {
+      const uint4 w = *reinterpret_cast<const uint4*>(kp + k_off<D>(j * 8 + gid, ch * 4 + tig));
+      const uint32_t wv[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+      for (int x = 0; x < 4; ++x) {
+        const uint32_t b0 = e4m3x2_to_h2(wv[x] & 0xffffu), b1 = e4m3x2_to_h2(wv[x] >> 16);
+#pragma unroll
+        for (int i = 0; i < MT; ++i) mma(s[i][j], st.q[i][ch * 4 + x], b0, b1);
+      }
+    }
+  }
+  // this page's value scale against the reference, which moves when it is
+  // exceeded 16 times
+  const float vsc = fmaxf(vs, 1e-30f);
+  if (vsc > 16.f * st.v_ref) {
+    const float f = st.v_ref / vsc;
+#pragma unroll
+    for (int i = 0; i < MT; ++i)
+#pragma unroll
+      for (int t = 0; t < D / 8; ++t)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) st.o[i][t][e] *= f;
+    st.v_ref = vsc;
+  }
+  const float pv = 8.f * vs / st.v_ref;
+  uint32_t pa[MT][4];
+#pragma unroll
+  for (int i = 0; i < MT; ++i) {
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {  // rows gid, gid + 8
+      const float c = st.c[i][r] * ks;
+      float x[4] = {s[i][0][2 * r], s[i][0][2 * r + 1], s[i][1][2 * r], s[i][1][2 * r + 1]};
+      if (SEE != kSeeAll) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int key = (e >> 1) * 8 + 2 * tig + (e & 1);
+          const bool ok = SEE == kSeeLimit ? key < limit : ((see[i][r] >> key) & 1u);
+          x[e] = ok ? x[e] * c : -INFINITY;
+        }
+      } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) x[e] *= c;
+      }
+      float mx = fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3]));
+      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+      if (mx > st.m[i][r] + 8.f) {  // O moves only when the maximum grows by more than 2^8
+        const float f = fast_exp2(st.m[i][r] - mx);  // 0 from -inf
+        st.l[i][r] *= f;
+#pragma unroll
+        for (int t = 0; t < D / 8; ++t) {
+          st.o[i][t][2 * r] *= f;
+          st.o[i][t][2 * r + 1] *= f;
+        }
+        st.m[i][r] = mx;
+      }
+      const float nm = st.m[i][r] == -INFINITY ? 0.f : -st.m[i][r];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) x[e] = fast_exp2(x[e] + nm);
+      st.l[i][r] += (x[0] + x[1]) + (x[2] + x[3]);
+      pa[i][r] = pack_h2(x[0] * pv, x[1] * pv);
+      pa[i][2 + r] = pack_h2(x[2] * pv, x[3] * pv);
+    }
+  }
+  // values: rows 2 tig, 2 tig + 1, 2 tig + 8, 2 tig + 9, columns gid * D/8 ...
+  constexpr int NW = D / 32;  // 4-byte words of a row per lane
+  uint32_t v[4][NW];
+#pragma unroll
+  for (int r = 0; r < 4; ++r) {
+    const int row = 2 * tig + (r & 1) + (r >> 1) * 8;
+    if (D == 128) {
+      const uint4 w = *reinterpret_cast<const uint4*>(vp + v_off<D>(row, gid));
+      v[r][0] = w.x;
+      v[r][1] = w.y;
+      v[r][NW - 2] = w.z;
+      v[r][NW - 1] = w.w;
+    } else {
+      const uint2 w = *reinterpret_cast<const uint2*>(vp + v_off<D>(row, gid >> 1) + (gid & 1) * 8);
+      v[r][0] = w.x;
+      v[r][1] = w.y;
+    }
+  }
+#pragma unroll
+  for (int w = 0; w < NW; ++w) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      // bytes 2h and 2h + 1 of both rows, paired by byte
+      const uint32_t sel = h ? 0x7362 : 0x5140;
+      const uint32_t p0 = __byte_perm(v[0][w], v[1][w], sel), p1 = __byte_perm(v[2][w], v[3][w], sel);
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        const uint32_t b0 = e4m3x2_to_h2(k ? p0 >> 16 : p0 & 0xffffu), b1 = e4m3x2_to_h2(k ? p1 >> 16 : p1 & 0xffffu);
+#pragma unroll
+        for (int i = 0; i < MT; ++i) mma(st.o[i][w * 4 + h * 2 + k], pa[i], b0, b1);
+      }
+    }
+  }
+}
+
+// One block of up to 16 new tokens of K or V as codes in shared memory (rows
+// past T are zero); returns the block's scale.
+template <typename T, int D, bool KEYS>
+__device__ __forceinline__ float quantise_new(const T* src, size_t row_stride, int rows, uint8_t* dst) {
+  constexpr int LPR = D / 16, RPS = 32 / LPR, STEPS = 16 / RPS;
+  const int lane = threadIdx.x & 31, sub = lane / LPR, c = lane % LPR;
+  Row8<T> lo[STEPS], hi[STEPS];
+  float amax = 0.f;
+#pragma unroll
+  for (int s = 0; s < STEPS; ++s) {
+    const int r = s * RPS + sub;
+    lo[s].zero();
+    hi[s].zero();
+    if (r < rows) {
+      lo[s].load(src + r * row_stride + 8 * c);
+      hi[s].load(src + r * row_stride + D / 2 + 8 * c);
+    }
+  }
+#pragma unroll
+  for (int s = 0; s < STEPS; ++s) {
+    float x[8];
+    lo[s].to_f(x);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) amax = fmaxf(amax, fabsf(x[e]));
+    hi[s].to_f(x);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) amax = fmaxf(amax, fabsf(x[e]));
+  }
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, off));
+  const float scale = block_scale(amax), inv = 1.f / scale;
+#pragma unroll
+  for (int s = 0; s < STEPS; ++s) {
+    const int r = s * RPS + sub;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int col = h * (D / 2) + 8 * c;
+      float x[8];
+      if (h) hi[s].to_f(x); else lo[s].to_f(x);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) x[e] *= inv;
+      const int off = (KEYS ? k_off<D>(r, col >> 4) : v_off<D>(r, col >> 4)) + (col & 8);
+      *reinterpret_cast<uint2*>(dst + off) = e4m3x8_of(x);
+    }
+  }
+  return scale;
+}
+
+template <typename T, int D, int MT>
+__global__ void __launch_bounds__(kThreads, Cfg<D, MT>::CTAS) attn_block8_kernel(const Block8Params p) {
+  using C = Cfg<D, MT>;
+  constexpr int RG = 16 * MT;
+  extern __shared__ __align__(128) uint8_t smem[];
+  int* s_pfx = reinterpret_cast<int*>(smem + C::kSmem);  // [B + 1]
+  __shared__ int s_warp[kWarps];
+  __shared__ int s_par[kMaxTree];
+  __shared__ unsigned long long s_anc[kMaxTree];
+  __shared__ float s_m[kWarps][RG], s_l[kWarps][RG], s_ref[kWarps];
+  const AttnParams& a = p.a;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, gid = lane >> 2, tig = lane & 3;
+  const int nnew = (a.T + kP - 1) / kP;
+  pdl_wait();
+
+  // ---- every CTA: tiles of each sequence and their prefix ----
+  {
+    int carry = 0;
+    for (int b0 = 0; b0 < a.B; b0 += kThreads) {
+      const int b = b0 + tid;
+      int n = 0;
+      if (b < a.B) {
+        const int L = a.seq_lens[b];
+        if ((long long)L > (long long)a.max_blocks * kP) {
+          if (blockIdx.x == 0) set_status(a.status, kStPages);
+        } else if (L >= 0) {
+          n = ((L + kP - 1) / kP + nnew + 3) / 4;
+        }
+      }
+      int incl = n;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int v = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += v;
+      }
+      if (lane == 31) s_warp[warp] = incl;
+      __syncthreads();
+      int off = carry;
+      for (int w = 0; w < kWarps; ++w) {
+        if (w < warp) off += s_warp[w];
+        carry += s_warp[w];
+      }
+      if (b < a.B) s_pfx[b] = off + incl - n;
+      __syncthreads();
+    }
+    if (tid == 0) s_pfx[a.B] = carry;
+    __syncthreads();
+    if (blockIdx.x == 0)
+      for (int b = tid; b <= a.B; b += kThreads) p.tile_pfx[b] = s_pfx[b];
+  }
+  Sched sc = a.sched;
+  sc.tile_pfx = s_pfx;
+  PieceIter it;
+  it.init(sc, blockIdx.x);
+  Piece pc;
+  uint8_t* ring = smem + warp * (C::DEPTH * 2 * C::kPage);
+  const uint32_t ring_u = static_cast<uint32_t>(__cvta_generic_to_shared(ring));
+  const uint8_t* kc = static_cast<const uint8_t*>(a.k_cache);
+  const uint8_t* vc = static_cast<const uint8_t*>(a.v_cache);
+
+  while (it.next(pc)) {
+    const int b = pc.b, kvh = pc.kvh;
+    const int L = a.seq_lens[b];
+    const int npre = (L + kP - 1) / kP;
+    const int row0 = pc.rg * RG;
+    const bool has_new = pc.tile_end * 4 > npre;
+    if (has_new) {
+      // ancestors of every node, by walking up (a chain without parents)
+      if (tid < a.T) {
+        const int par = p.parents ? p.parents[(size_t)b * a.T + tid] : tid - 1;
+        const bool ok = tid == 0 ? par == -1 : (par >= 0 && par < tid);
+        if (!ok) set_status(a.status, kStTree);
+        s_par[tid] = ok ? par : -1;
+      }
+      __syncthreads();
+      if (tid < a.T) {
+        unsigned long long anc = 0;
+        for (int n = tid; n >= 0; n = s_par[n]) anc |= 1ull << n;  // parents are earlier: at most T steps
+        s_anc[tid] = anc;
+      }
+      __syncthreads();
+    }
+    // this warp's pages: 4 * (tile_begin + i) + warp, the cached ones first
+    const int tiles = pc.tile_end - pc.tile_begin;
+    const int first = 4 * pc.tile_begin + warp;
+    const int npages = min(tiles, max(0, (npre - first + 3) / 4));
+    const int* bt = a.block_tables + (size_t)b * a.max_blocks;
+    // page ids and scales of 32 pages, a lane each; the next 32 ids are fetched
+    // while these are used, their scales half way
+    auto fetch_id = [&](int i) { return i < npages ? bt[first + 4 * i] : -1; };
+    auto fetch_scale = [&](const float* sc_, int id) {
+      return id >= 0 && id < a.num_pages ? __ldg(sc_ + (size_t)id * a.Hkv + kvh) : 0.f;
+    };
+    int id_cur = fetch_id(lane), id_nxt = -1;
+    float ks_cur = fetch_scale(p.k_scales, id_cur), vs_cur = fetch_scale(p.v_scales, id_cur);
+    float ks_nxt = 0.f, vs_nxt = 0.f;
+    int id_iss = id_cur, iss_base = 0;  // the issuing side runs ahead of the computing side
+    bool bad = false;
+    auto issue = [&](int i) {
+      if (i < npages) {
+        if (i - iss_base >= 32) {
+          iss_base += 32;
+          id_iss = id_nxt;
+        }
+        const int id = __shfl_sync(0xffffffffu, id_iss, i - iss_base);
+        if (id >= 0 && id < a.num_pages) {
+          const size_t src = ((size_t)id * a.Hkv + kvh) * C::kPage;
+          const uint32_t dst = ring_u + (i % C::DEPTH) * 2 * C::kPage;
+          constexpr int CPR = D / 16;  // chunks per row
+#pragma unroll
+          for (int x = 0; x < 16 * CPR / 32; ++x) {
+            const int q = x * 32 + lane, r = q / CPR, ch = q % CPR;
+            cp_async16(dst + k_off<D>(r, ch), kc + src + q * 16);
+            cp_async16(dst + C::kPage + v_off<D>(r, ch), vc + src + q * 16);
+          }
+        } else {
+          bad = true;
+        }
+      }
+      cp_commit();
+    };
+#pragma unroll
+    for (int i = 0; i < C::DEPTH - 1; ++i) issue(i);
+
+    // queries: this lane's columns of rows gid and gid + 8, scaled to fp16
+    State<D, MT> st;
+    st.clear();
+#pragma unroll
+    for (int i = 0; i < MT; ++i) {
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        const int row = row0 + i * 16 + r * 8 + gid;
+        Row8<T> raw[D / 32];
+#pragma unroll
+        for (int x = 0; x < D / 32; ++x) raw[x].zero();
+        if (row < a.rows) {
+          const int node = row / a.g, h = kvh * a.g + row % a.g;
+          const T* q = static_cast<const T*>(a.q_rot) + (((size_t)b * a.T + node) * a.Hq + h) * D + tig * 16;
+#pragma unroll
+          for (int x = 0; x < D / 32; ++x) raw[x].load(q + (x / 2) * 64 + (x % 2) * 8);
+        }
+        float amax = 0.f;
+#pragma unroll
+        for (int x = 0; x < D / 32; ++x) {
+          float f[8];
+          raw[x].to_f(f);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) amax = fmaxf(amax, fabsf(f[e]));
+        }
+        amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+        amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+        // 2^8 <= scaled maximum < 2^9: elements down to 2^-33 of it keep their bits
+        const int ex = amax > 0.f ? (int)(__float_as_uint(amax) >> 23) - 127 : 0;
+        const int k = min(max(8 - ex, -120), 120);
+        const float f2 = __uint_as_float((uint32_t)(127 + k) << 23);
+        st.c[i][r] = a.scale_log2 * __uint_as_float((uint32_t)(127 - k) << 23);
+#pragma unroll
+        for (int x = 0; x < D / 32; ++x) {
+          float f[8];
+          raw[x].to_f(f);
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {  // four columns: k-step 2x + e
+            st.q[i][2 * x + e][r] = pack_h2(f[4 * e] * f2, f[4 * e + 1] * f2);
+            st.q[i][2 * x + e][2 + r] = pack_h2(f[4 * e + 2] * f2, f[4 * e + 3] * f2);
+          }
+        }
+      }
+    }
+
+    const unsigned none[MT][2] = {};
+    for (int i = 0; i < npages; ++i) {
+      const int at = i & 31;
+      if (at == 0) {
+        if (i > 0) {
+          id_cur = id_nxt;
+          ks_cur = ks_nxt;
+          vs_cur = vs_nxt;
+        }
+        id_nxt = fetch_id(i + 32 + lane);
+      } else if (at == 16) {
+        ks_nxt = fetch_scale(p.k_scales, id_nxt);
+        vs_nxt = fetch_scale(p.v_scales, id_nxt);
+      }
+      issue(i + C::DEPTH - 1);
+      cp_wait<C::DEPTH - 1>();
+      __syncwarp();
+      uint8_t* kp = ring + (i % C::DEPTH) * 2 * C::kPage;
+      uint8_t* vp = kp + C::kPage;
+      const float ks = __shfl_sync(0xffffffffu, ks_cur, at), vs = __shfl_sync(0xffffffffu, vs_cur, at);
+      const int limit = L - (first + 4 * i) * kP;
+      if (limit >= kP) {
+        page_step<D, MT, kSeeAll>(st, kp, vp, ks, vs, kP, none);
+      } else {
+        // the sequence ends in this page: rows past it may hold anything, NaN
+        // codes too; their weights are 0 and their values are made 0
+        for (int e = lane; e < (kP - limit) * (D / 16); e += 32)
+          *reinterpret_cast<uint4*>(vp + limit * D + e * 16) = make_uint4(0, 0, 0, 0);
+        __syncwarp();
+        page_step<D, MT, kSeeLimit>(st, kp, vp, ks, vs, limit, none);
+      }
+      __syncwarp();  // every lane has read the slot before it is filled again
+    }
+    cp_wait<0>();
+    __syncwarp();
+    if (bad && lane == 0) set_status(a.status, kStPages);
+
+    // the new tokens' block that falls to this warp, if any
+    const int pn = first + 4 * npages - npre;
+    if (npages < tiles && pn >= 0 && pn < nnew) {
+      const size_t rs = (size_t)a.Hkv * D;
+      const size_t src = ((size_t)b * a.T + pn * kP) * rs + (size_t)kvh * D;
+      const int rows = min(kP, a.T - pn * kP);
+      const float ks = quantise_new<T, D, true>(static_cast<const T*>(p.k_new) + src, rs, rows, ring);
+      const float vs = quantise_new<T, D, false>(static_cast<const T*>(p.v_new) + src, rs, rows, ring + C::kPage);
+      __syncwarp();
+      unsigned see[MT][2];
+#pragma unroll
+      for (int i = 0; i < MT; ++i)
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+          const int row = row0 + i * 16 + r * 8 + gid;
+          see[i][r] = row < a.rows ? (unsigned)(s_anc[row / a.g] >> (pn * kP)) & 0xffffu : 0u;
+        }
+      page_step<D, MT, kSeeMask>(st, ring, ring + C::kPage, ks, vs, kP, see);
+    }
+
+    // ---- join the four warps and write the piece ----
+#pragma unroll
+    for (int i = 0; i < MT; ++i)
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        float l = st.l[i][r];
+        l += __shfl_xor_sync(0xffffffffu, l, 1);
+        l += __shfl_xor_sync(0xffffffffu, l, 2);
+        if (tig == 0) {
+          s_m[warp][i * 16 + r * 8 + gid] = st.m[i][r];
+          s_l[warp][i * 16 + r * 8 + gid] = l;
+        }
+      }
+    if (lane == 0) s_ref[warp] = st.v_ref * 0.125f;
+    float* s_o = reinterpret_cast<float*>(smem);  // [warp][16][LDO]
+#pragma unroll
+    for (int i = 0; i < MT; ++i) {
+      __syncthreads();  // rings (or the previous tile's rows) are no longer read
+      constexpr int NT = D / 8;
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        float* o = s_o + (warp * 16 + r * 8 + gid) * C::LDO + tig * 2 * NT;
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+          for (int t = 0; t < NT; t += 4)
+            *reinterpret_cast<float4*>(o + h * NT + t) =
+                make_float4(st.o[i][t][2 * r + h], st.o[i][t + 1][2 * r + h], st.o[i][t + 2][2 * r + h],
+                            st.o[i][t + 3][2 * r + h]);
+      }
+      __syncthreads();
+      const int rr = tid >> 3, rg_row = i * 16 + rr, row = row0 + rg_row;
+      if (row < a.rows) {
+        float M = -INFINITY, f[kWarps], l = 0.f;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) M = fmaxf(M, s_m[w][rg_row]);
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) {
+          const float e = s_m[w][rg_row] == -INFINITY ? 0.f : fast_exp2(s_m[w][rg_row] - M);
+          l += e * s_l[w][rg_row];
+          f[w] = e * s_ref[w];
+        }
+        const float inv = l > 0.f ? 1.f / l : 0.f;
+#pragma unroll
+        for (int e8 = 0; e8 < D / 64; ++e8) {
+          const int c8 = (tid & 7) * (D / 64) + e8;
+          float acc[8] = {};
+#pragma unroll
+          for (int w = 0; w < kWarps; ++w) {
+            const float4* o = reinterpret_cast<const float4*>(s_o + (w * 16 + rr) * C::LDO + c8 * 8);
+            const float4 x = o[0], y = o[1];
+            acc[0] += f[w] * x.x;
+            acc[1] += f[w] * x.y;
+            acc[2] += f[w] * x.z;
+            acc[3] += f[w] * x.w;
+            acc[4] += f[w] * y.x;
+            acc[5] += f[w] * y.y;
+            acc[6] += f[w] * y.z;
+            acc[7] += f[w] * y.w;
+          }
+#pragma unroll
+          for (int e = 0; e < 8; ++e) acc[e] *= inv;
+          Row8<T> v;
+          v.from_f(acc);
+          T* dst;
+          if (pc.slot < 0) {
+            const int node = row / a.g, h = kvh * a.g + row % a.g;
+            dst = static_cast<T*>(a.out) + (((size_t)b * a.T + node) * a.Hq + h) * D + c8 * 8;
+          } else {
+            dst = static_cast<T*>(a.part_o) + (((size_t)pc.slot * (D / 8) + c8) * a.part_rows + rg_row) * 8;
+          }
+          v.store(dst);
+        }
+        if (pc.slot >= 0 && (tid & 7) == 0) a.part_ml[(size_t)pc.slot * a.part_rows + rg_row] = make_float2(M, l);
+      }
+    }
+    __syncthreads();  // the rings are filled again by the next piece
+  }
+}
+
+template <typename T, int D, int MT>
+cudaError_t launch_t(const Block8Params& p, cudaStream_t stream) {
+  using C = Cfg<D, MT>;
+  const size_t smem = (size_t)C::kSmem + sizeof(int) * (size_t)(p.a.B + 1);
+  static std::atomic<bool> opted[kMaxDevices];
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 0 || dev >= kMaxDevices || !opted[dev].load(std::memory_order_acquire)) {
+    // the largest batch's prefix included
+    e = cudaFuncSetAttribute(attn_block8_kernel<T, D, MT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             C::kSmem + 4 * (8192 + 1));
+    if (e != cudaSuccess) return e;
+    if (dev >= 0 && dev < kMaxDevices) opted[dev].store(true, std::memory_order_release);
+  }
+  return launch_pdl(attn_block8_kernel<T, D, MT>, dim3(p.a.sched.G), dim3(kThreads), smem, stream, p);
+}
+
+template <typename T>
+cudaError_t launch_d(const Block8Params& p, cudaStream_t stream) {
+  const bool one = p.a.rows_per_group == 16;
+  if (p.a.D == 64) return one ? launch_t<T, 64, 1>(p, stream) : launch_t<T, 64, 2>(p, stream);
+  return one ? launch_t<T, 128, 1>(p, stream) : launch_t<T, 128, 2>(p, stream);
+}
+
+}  // namespace
+
+Block8Plan block8_plan(int rows) {
+  if (rows <= 16) return Block8Plan{16, Cfg<128, 1>::CTAS, 2};
+  return Block8Plan{32, Cfg<128, 2>::CTAS, 2};
+}
+
+cudaError_t launch_attn_block8(const Block8Params& p, int dtype, cudaStream_t stream) {
+  return dtype == 1 ? launch_d<__half>(p, stream) : launch_d<__nv_bfloat16>(p, stream);
+}
+
+}  // namespace mt

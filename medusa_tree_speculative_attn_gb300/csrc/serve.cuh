@@ -1,0 +1,188 @@
+// Parameter blocks, launchers and device helpers of the serving operators
+// around the verify step (internal to the library): norms with rotation, cache
+// append, block-scaled 8-bit attention, sampling.
+#pragma once
+
+#include "kernels.cuh"
+
+namespace mt {
+
+enum : int { kStPosition = -7 };  // matches MT_ERR_POSITION
+
+// ---------------------------------------------------------------------------
+// 8 consecutive act-dtype elements as 16-byte words.
+// ---------------------------------------------------------------------------
+template <typename T>
+struct Row8 {
+  static constexpr int kWords = 8 * (int)sizeof(T) / 16;
+  uint4 w[kWords];
+  __device__ __forceinline__ void load(const T* p) {
+#pragma unroll
+    for (int k = 0; k < kWords; ++k) w[k] = reinterpret_cast<const uint4*>(p)[k];
+  }
+  __device__ __forceinline__ void load_stream(const T* p) {  // read once
+#pragma unroll
+    for (int k = 0; k < kWords; ++k) w[k] = __ldcs(reinterpret_cast<const uint4*>(p) + k);
+  }
+  __device__ __forceinline__ void store(T* p) const {
+#pragma unroll
+    for (int k = 0; k < kWords; ++k) reinterpret_cast<uint4*>(p)[k] = w[k];
+  }
+  __device__ __forceinline__ void zero() {
+#pragma unroll
+    for (int k = 0; k < kWords; ++k) w[k] = make_uint4(0, 0, 0, 0);
+  }
+  __device__ __forceinline__ void to_f(float (&x)[8]) const {
+    T v[8];
+    memcpy(v, w, sizeof(v));
+#pragma unroll
+    for (int e = 0; e < 8; ++e) x[e] = Act<T>::to_f(v[e]);
+  }
+  __device__ __forceinline__ void from_f(const float (&x)[8]) {
+    T v[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] = Act<T>::from_f(x[e]);
+    memcpy(w, v, sizeof(v));
+  }
+};
+
+// ---------------------------------------------------------------------------
+// E4M3 codes and block scales.
+// ---------------------------------------------------------------------------
+
+// Two values as codes (nearest even, saturated to +-448), a in the low byte.
+__device__ __forceinline__ uint32_t e4m3x2_of(float a, float b) {
+  uint16_t r;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(b), "f"(a));
+  return r;
+}
+
+__device__ __forceinline__ uint2 e4m3x8_of(const float (&x)[8]) {
+  return make_uint2(e4m3x2_of(x[0], x[1]) | e4m3x2_of(x[2], x[3]) << 16,
+                    e4m3x2_of(x[4], x[5]) | e4m3x2_of(x[6], x[7]) << 16);
+}
+
+// Two codes (low 16 bits) as two fp16 values: exact, fp16 holds every E4M3 value.
+__device__ __forceinline__ uint32_t e4m3x2_to_h2(uint32_t pair) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"((uint16_t)pair));
+  return r;
+}
+
+__device__ __forceinline__ void e4m3x8_to_f(uint2 c, float (&x)[8]) {
+  const uint32_t w[4] = {c.x & 0xffffu, c.x >> 16, c.y & 0xffffu, c.y >> 16};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t h = e4m3x2_to_h2(w[i]);
+    __half2 v;
+    memcpy(&v, &h, 4);
+    const float2 f = __half22float2(v);
+    x[2 * i] = f.x;
+    x[2 * i + 1] = f.y;
+  }
+}
+
+// Scale of a block whose largest magnitude is amax: the smallest power of two
+// 2^k, k in [-64, 119], with amax <= 448 * 2^k = 1.75 * 2^(k + 8).  A power of
+// two costs no precision (E4M3's steps are relative, so another scale in the
+// same octave gives steps of the same size), makes code -> value exact in
+// every act dtype, and lets a block's codes move to a larger scale without
+// drift: only codes that fall below the smallest E4M3 step are rounded.  The
+// range keeps the scale, its inverse and 448 times it normal fp32 numbers.
+__device__ __forceinline__ float block_scale(float amax) {
+  const uint32_t bits = __float_as_uint(amax);
+  int k = (int)(bits >> 23) - 127 - ((bits & 0x7fffffu) <= 0x600000u ? 8 : 7);
+  k = min(max(k, -64), 119);
+  return __uint_as_float((uint32_t)(k + 127) << 23);
+}
+
+// ---------------------------------------------------------------------------
+// Per-head norms of queries and keys, with the rotation in the same pass.
+// ---------------------------------------------------------------------------
+struct NormRopeParams {
+  int N, Hq, Hkv, D;
+  const void* q;
+  const void* k;
+  void* q_out;
+  void* k_out;
+  long long q_st[2], k_st[2], qo_st[2], ko_st[2];  // (token, head) strides in elements
+  const int* positions;  // [N] or null
+  const void* q_weight;  // [D] act, or null: no norm
+  const void* k_weight;
+  float eps;
+  const float2* rope;  // null: no rotation
+  int max_pos;
+  int* status;
+};
+cudaError_t launch_norm_rope(const NormRopeParams& a, int dtype, cudaStream_t stream);
+
+// ---------------------------------------------------------------------------
+// Appending keys and values to a paged cache.
+// ---------------------------------------------------------------------------
+enum : int { kCacheAct = 0, kCacheE4m3 = 1, kCacheBlock8 = 2 };
+
+struct AppendParams {
+  int B, N, Hkv, D, max_blocks, num_pages, mode;
+  const void* k;
+  const void* v;
+  long long k_st[2], v_st[2];  // (row, head) strides in elements
+  void* k_cache;
+  void* v_cache;
+  float* k_scales;  // [num_pages][Hkv] (block-scaled caches)
+  float* v_scales;
+  float k_scale, v_scale;  // one scale for the whole cache (kCacheE4m3)
+  const int* block_tables;
+  const int* seq_lens;
+  const int* row_offsets;  // [B + 1], or null: the accepted path's rows
+  const int* accept_path;  // [B][max_depth + 1]
+  const int* accept_len;   // [B]
+  int T, max_depth;
+  const float2* rope;  // null: keys are stored as given
+  int max_pos;
+  int* status;
+};
+cudaError_t launch_append(const AppendParams& a, int dtype, cudaStream_t stream);
+
+// ---------------------------------------------------------------------------
+// Tree attention over a block-scaled 8-bit cache.
+// ---------------------------------------------------------------------------
+struct Block8Params {
+  AttnParams a;           // q_rot: the queries as they attend; part_o, part_ml, sched, out, status, ...
+  const float* k_scales;  // [num_pages][Hkv]
+  const float* v_scales;
+  const void* k_new;      // [B][T][Hkv][D] act, as they attend
+  const void* v_new;
+  const int* parents;     // [B][T], or null: a chain
+  int* tile_pfx;          // [B + 1] out, for the combine
+};
+
+// Row group, CTAs per SM and cost of starting a piece (in 64-slot tiles) of the
+// register-fragment kernel.
+struct Block8Plan {
+  int rows_per_group, ctas_per_sm, seg_cost;
+};
+Block8Plan block8_plan(int rows);
+cudaError_t launch_attn_block8(const Block8Params& p, int dtype, cudaStream_t stream);
+
+// ---------------------------------------------------------------------------
+// Sampling.
+// ---------------------------------------------------------------------------
+// Largest vocab: an eighth of it (a CTA's slice) times 2^16 stays below 2^32,
+// which the histograms' sums of 16-bit halves rely on.
+constexpr int kSampleMaxVocab = 500000;
+
+struct SampleParams {
+  int N, V, rows;  // rows to draw, vocab, rows of logits
+  long long row_stride;
+  const void* logits;
+  const int* row_index;  // [N] or null
+  const float* uniforms;
+  const float* temperature;  // each [N] or null
+  const int* top_k;
+  const float* top_p;
+  const float* min_p;
+  int* tokens;
+};
+cudaError_t launch_sample(const SampleParams& a, int dtype, cudaStream_t stream);
+
+}  // namespace mt

@@ -1,0 +1,662 @@
+"""The serving operators on the GPU against plain implementations in 64 bits (serve_reference).
+
+Tolerances (u = half a step of the output's type relative to the value: bf16 2^-8, fp16 2^-11, fp32 2^-24):
+  norms and rotation  u |y| for the rounding at the end, and 2^-19 of the magnitudes that enter y: a chain of six
+                      rounded 32-bit operations (2^-24 each), the reciprocal square root (2^-22), the sum of D
+                      squares (a tree of depth <= 16: 2^-20) and the table (2^-24);
+  attention           u |out| (output) + u A (a split segment's pieces, rounded once) + 2^-11 A (fp16 weights) +
+                      2 E A, A = sum p |v|, E the error of a score in the exponent: D products and sums in 32 bits,
+                      which tensor cores may truncate, 2 D 2^-24 sum |q k| scale <= 2^-9 for these inputs;
+  codes, scales, values, tokens: equal."""
+import numpy as np
+import pytest
+
+torch = pytest.importorskip("torch")
+
+import medusa_tree_speculative_attn_gb300 as mt
+import serve_reference as ref
+
+pytestmark = pytest.mark.gpu
+
+DT = {"f32": torch.float32, "f16": torch.float16, "bf16": torch.bfloat16}
+P = 16
+BASE = 10000.0
+
+
+def _status():
+    return torch.zeros(256, dtype=torch.uint8, device="cuda")
+
+
+def _rand(rng, *shape, dtype=torch.float32, scale=1.0):
+    return (torch.from_numpy(rng.standard_normal(shape)) * scale).to(dtype)
+
+
+def _i32(x):
+    return torch.as_tensor(np.asarray(x, np.int32))
+
+
+def _codes(t):
+    return t.cpu().view(torch.uint8).numpy()
+
+
+def _table(rng, need, pages):
+    """A block table with need[b] shuffled pages each, -1 behind them."""
+    perm = rng.permutation(pages)
+    out = np.full((len(need), max(1, max(need))), -1, np.int32)
+    at = 0
+    for b, n in enumerate(need):
+        out[b, :n] = perm[at:at + n]
+        at += n
+    return out
+
+
+def _graph(fn):
+    """fn captured on a side stream, then replayed once."""
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.stream(s):
+        fn()
+        s.synchronize()
+        with torch.cuda.graph(g, stream=s):
+            fn()
+    torch.cuda.synchronize()
+    return g
+
+
+# ---- norms and rotation ----------------------------------------------------
+
+@pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("n, hq, hkv, d", [(1, 1, 1, 64), (3, 8, 2, 128), (17, 5, 5, 64), (64, 32, 8, 128), (5, 9, 3, 128)])
+@pytest.mark.parametrize("norm, rope", [(True, True), (True, False), (False, True)])
+def test_norm_rope(dtype, n, hq, hkv, d, norm, rope):
+    rng = np.random.default_rng(n * 100 + hq)
+    dt = DT[dtype]
+    x = _rand(rng, n, hq + 2 * hkv, d, dtype=dt, scale=3.0)
+    if n > 1:
+        x[1] = 0  # a row of zeros
+    w = [(1 + 0.2 * _rand(rng, d)).to(dt) for _ in range(2)] if norm else [None, None]
+    pos = rng.integers(0, 500, n)
+    if n > 2:
+        pos[2] = -1  # no token
+    pos[0] = 499
+    xd = x.cuda()
+    q, k = xd[:, :hq], xd[:, hq:hq + hkv]  # views of a projection's rows
+    qo, ko = torch.full((n, hq, d), 7.0, dtype=dt, device="cuda"), torch.full((n, hkv, d), 7.0, dtype=dt, device="cuda")
+    table = mt.Rope(BASE, d, 500) if rope else None
+    ws = _status()
+    mt.qk_norm_rope(q, k, _i32(pos).cuda(), qo, ko, rope=table, q_weight=w[0].cuda() if norm else None,
+                    k_weight=w[1].cuda() if norm else None, eps=1e-5, status_ws=ws)
+    assert mt.read_status(ws) == 0
+    cos, sin = ref.rope_table(BASE, d, 500)
+    at = np.maximum(pos, 0)
+    c, s = (cos[at][:, None], sin[at][:, None]) if rope else (None, None)
+    for got, src, wt in ((qo, x[:, :hq], w[0]), (ko, x[:, hq:hq + hkv], w[1])):
+        want, mag = ref.norm_rope64(src, wt, 1e-5, c, s)
+        got = got.cpu().double()
+        tol = ref.HALF_STEP[dt] * want.abs() + 2.0 ** -19 * mag + (2.0 ** -25 if dt == torch.float16 else 0)
+        live = torch.from_numpy(pos >= 0)
+        assert bool(((got - want).abs() <= tol)[live].all())
+        assert bool((got[~live] == 7.0).all())
+        if not norm:  # the same bits as the tree attention's own rotation
+            assert torch.equal(got[live], ref.rotate32(src, c, s).to(dt).double()[live])
+
+
+def test_norm_rope_in_place_and_in_a_graph():
+    rng = np.random.default_rng(5)
+    x = _rand(rng, 40, 6, 128, dtype=torch.bfloat16).cuda()
+    want_q, want_k = torch.empty_like(x[:, :4]), torch.empty_like(x[:, 4:])
+    w = torch.ones(128, dtype=torch.bfloat16, device="cuda")
+    pos, rope, ws = torch.arange(40, dtype=torch.int32, device="cuda"), mt.Rope(BASE, 128, 64), _status()
+    mt.qk_norm_rope(x[:, :4], x[:, 4:], pos, want_q, want_k, rope=rope, q_weight=w, k_weight=w, status_ws=ws)
+    y = x.clone()
+    mt.qk_norm_rope(y[:, :4], y[:, 4:], pos, y[:, :4], y[:, 4:], rope=rope, q_weight=w, k_weight=w, status_ws=ws)
+    assert torch.equal(y[:, :4], want_q) and torch.equal(y[:, 4:], want_k)
+    a, b = torch.empty_like(want_q), torch.empty_like(want_k)
+    g = _graph(lambda: mt.qk_norm_rope(x[:, :4], x[:, 4:], pos, a, b, rope=rope, q_weight=w, k_weight=w, status_ws=ws))
+    a.zero_(), b.zero_()
+    g.replay()
+    assert torch.equal(a, want_q) and torch.equal(b, want_k)
+
+
+def test_norm_rope_position_past_the_table():
+    x = torch.ones(2, 2, 64, dtype=torch.float16, device="cuda")
+    out, ws = torch.full_like(x, 3.0), _status()
+    mt.qk_norm_rope(x, x, _i32([10, 3]).cuda(), out, torch.empty_like(x), rope=mt.Rope(BASE, 64, 10), status_ws=ws)
+    assert mt.read_status(ws) == -7
+    assert bool((out[0] == 3.0).all()) and not bool((out[1] == 3.0).any())
+
+
+# ---- appending to the cache ------------------------------------------------
+
+class Cache:
+    """A seeded cache of one kind, on the GPU, and its copy on the host."""
+
+    def __init__(self, rng, kind, pages, hkv, d, dt):
+        self.kind = kind
+        if kind == "act":
+            k, v = (_rand(rng, pages, hkv, P, d, dtype=dt) for _ in range(2))
+        else:  # any code, NaN included, may lie in slots that no sequence holds
+            k, v = (torch.from_numpy(rng.integers(0, 256, (pages, hkv, P, d)).astype(np.uint8)).view(torch.float8_e4m3fn) for _ in range(2))
+        self.host = [k.clone(), v.clone()]
+        self.k, self.v = k.cuda(), v.cuda()
+        self.scales = [None, None]
+        if kind == "block8":
+            self.host_scales = [2.0 ** rng.integers(-8, 3, (pages, hkv)).astype(np.float64) for _ in range(2)]
+            self.scales = [torch.from_numpy(s).float().cuda() for s in self.host_scales]
+
+    def args(self):
+        return dict(k_scales=self.scales[0], v_scales=self.scales[1], k_scale=0.03, v_scale=0.05)
+
+    def append(self, which, x, page, head, r0):
+        """The rows x [m][D] (in the act dtype) into slots r0 .. of a page."""
+        m = x.shape[0]
+        if self.kind == "act":
+            self.host[which][page, head, r0:r0 + m] = x
+            return
+        codes = self.host[which].view(torch.uint8).numpy()[page, head]
+        x = x.double().numpy()
+        if self.kind == "e4m3":
+            scale = np.float32(0.03 if which == 0 else 0.05)
+            codes[r0:r0 + m] = ref.encode((x.astype(np.float32) / scale).astype(np.float64))
+            return
+        finite = np.abs(x[~np.isnan(x)])
+        s = ref.scale_of(finite.max() if finite.size else 0.0)
+        if r0:
+            old = self.host_scales[which][page, head]
+            s = max(s, old)
+            if s > old:
+                codes[:r0] = ref.encode(ref.decode(codes[:r0]) * (old / s))
+        self.host_scales[which][page, head] = s
+        codes[r0:r0 + m] = ref.encode(x / s)
+
+    def check(self):
+        for got, want in ((self.k, self.host[0]), (self.v, self.host[1])):
+            assert torch.equal(got.cpu().view(torch.uint8), want.view(torch.uint8))
+        if self.kind == "block8":
+            for got, want in zip(self.scales, self.host_scales):
+                assert np.array_equal(got.cpu().double().numpy(), want)
+
+
+def _append_on_host(cache, k, v, rows_of, lens, table, rot):
+    """rows_of(b): the new rows of sequence b."""
+    for b in range(len(lens)):
+        rows, n = rows_of(b), int(lens[b])
+        if n < 0:
+            continue
+        i = 0
+        while i < len(rows):
+            slot = n + i
+            r0 = slot % P
+            m = min(P - r0, len(rows) - i)
+            for h in range(k.shape[1]):
+                x = k[rows[i:i + m], h]
+                if rot is not None:
+                    x = ref.rotate32(x, rot[0][slot:slot + m], rot[1][slot:slot + m]).to(k.dtype)
+                cache.append(0, x, table[b, slot // P], h, r0)
+                cache.append(1, v[rows[i:i + m], h], table[b, slot // P], h, r0)
+            i += m
+
+
+APPENDS = [  # past lengths, new rows
+    ([0], [1]), ([0], [16]), ([15], [1]), ([16], [17]), ([5], [60]),
+    ([0, 7, -1, 31, 16], [3, 0, 0, 33, 1]), ([100, 3, 47], [1, 1, 1]), ([12, 0], [50, 2]),
+]
+
+
+@pytest.mark.parametrize("kind", ["act", "e4m3", "block8"])
+@pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("case", range(len(APPENDS)))
+def test_append(kind, dtype, case):
+    past, new = APPENDS[case]
+    rng = np.random.default_rng(case * 10 + len(dtype))
+    dt, hkv, d = DT[dtype], [1, 3, 8][case % 3], [64, 128][case % 2]
+    need = [-(-(max(p, 0) + n) // P) for p, n in zip(past, new)]
+    table = _table(rng, need, sum(need) + 2)
+    cache = Cache(rng, kind, sum(need) + 2, hkv, d, dt)
+    off = np.concatenate([[0], np.cumsum(new)])
+    n = int(off[-1]) + 2  # two rows behind the last sequence's
+    kv = _rand(rng, n, 2, hkv, d, dtype=dt, scale=float(rng.choice([0.01, 1.0, 30.0])))
+    rope = mt.Rope(BASE, d, 256) if case % 4 else None
+    rot = ref.rope_table(BASE, d, 256) if case % 4 else None
+    ws, dev = _status(), kv.cuda()
+    mt.kv_append_paged(dev[:, 0], dev[:, 1], cache.k, cache.v, _i32(table).cuda(), _i32(past).cuda(), _i32(off).cuda(),
+                       status_ws=ws, rope=rope, **cache.args())
+    assert mt.read_status(ws) == 0
+    _append_on_host(cache, kv[:, 0], kv[:, 1], lambda b: list(range(off[b], off[b + 1])), past, table, rot)
+    cache.check()
+
+
+def test_append_again_and_again_to_one_page():
+    # one row at a time, each larger than all before: the scale grows with every row
+    rng = np.random.default_rng(3)
+    cache = Cache(rng, "block8", 2, 2, 64, torch.bfloat16)
+    table, ws = _i32([[1, 0]]).cuda(), _status()
+    for i in range(20):
+        kv = _rand(rng, 1, 2, 2, 64, dtype=torch.bfloat16, scale=2.0 ** (i % 7))
+        d = kv.cuda()
+        mt.kv_append_paged(d[:, 0], d[:, 1], cache.k, cache.v, table, _i32([i]).cuda(), _i32([0, 1]).cuda(), status_ws=ws, **cache.args())
+        _append_on_host(cache, kv[:, 0], kv[:, 1], lambda b: [0], [i], np.array([[1, 0]]), None)
+        cache.check()
+    assert mt.read_status(ws) == 0
+
+
+def test_append_extreme_values():
+    rng = np.random.default_rng(4)
+    cache = Cache(rng, "block8", 3, 1, 64, torch.bfloat16)
+    x = torch.zeros(48, 2, 1, 64, dtype=torch.bfloat16)  # a page of zeros
+    x[16:32] = _rand(rng, 16, 2, 1, 64, dtype=torch.bfloat16)
+    x[17, 0, 0, 5] = float("nan")
+    x[18, 1, 0, 6] = float("inf")
+    x[32:48] = _rand(rng, 16, 2, 1, 64, dtype=torch.bfloat16, scale=1e-25)
+    x[33, 0, 0, 0] = 3e38
+    d, ws, table = x.cuda(), _status(), np.array([[2, 0, 1]])
+    mt.kv_append_paged(d[:, 0], d[:, 1], cache.k, cache.v, _i32(table).cuda(), _i32([0]).cuda(), _i32([0, 48]).cuda(), status_ws=ws, **cache.args())
+    _append_on_host(cache, x[:, 0], x[:, 1], lambda b: list(range(48)), [0], table, None)
+    cache.check()
+
+
+@pytest.mark.parametrize("kind", ["act", "block8"])
+def test_append_accepted(kind):
+    rng = np.random.default_rng(8)
+    b, t, hkv, d, dt = 4, 20, 3, 128, torch.bfloat16
+    past, lens = [14, 0, -1, 33], [3, 0, 2, 4]
+    path = np.full((b, 6), -1)
+    for i, n in enumerate(lens):
+        path[i, :n + 1] = np.sort(rng.choice(np.arange(1, t), n + 1, replace=False))
+        path[i, 0] = 0
+    need = [2, 1, 1, 3]
+    table = _table(rng, need, 8)
+    cache = Cache(rng, kind, 8, hkv, d, dt)
+    k, v = (_rand(rng, b, t, hkv, d, dtype=dt) for _ in range(2))
+    ws = _status()
+    rope = mt.Rope(BASE, d, 64)
+    mt.kv_append_accepted(k.cuda(), v.cuda(), _i32(path).cuda(), _i32(lens).cuda(), cache.k, cache.v, _i32(table).cuda(), _i32(past).cuda(),
+                          status_ws=ws, rope=rope, **cache.args())
+    assert mt.read_status(ws) == 0
+    _append_on_host(cache, k.view(b * t, hkv, d), v.view(b * t, hkv, d), lambda i: [i * t + int(path[i, j]) for j in range(lens[i] + 1)], past,
+                    table, ref.rope_table(BASE, d, 64))
+    cache.check()
+
+
+@pytest.mark.parametrize("bad", ["page", "table", "offsets", "rows", "position", "node"])
+def test_append_reports_and_leaves_the_rest(bad):
+    rng = np.random.default_rng(11)
+    hkv, d, dt = 2, 64, torch.float16
+    past, new = [0, 10, 4], [20, 20, 5]
+    table = _table(rng, [2, 2, 1], 6)
+    off = np.array([0, 20, 40, 45])
+    cache = Cache(rng, "block8", 6, hkv, d, dt)
+    kv = _rand(rng, 45, 2, hkv, d, dtype=dt)
+    dev, ws, want = kv.cuda(), _status(), -4
+    skip = {"page": [(1, 1)], "table": [(1, 0), (1, 1)], "position": [(1, 1)]}.get(bad, [])
+    rope = None
+    if bad == "page":
+        table = table.copy()
+        table[1, 1] = 6
+    elif bad == "table":
+        past[1] = 13
+    elif bad == "position":
+        rope, want = mt.Rope(BASE, d, 29), -7
+    elif bad == "offsets":
+        off = np.array([0, 20, 10, 45])
+    elif bad == "rows":
+        off = np.array([0, 20, 40, 46])
+    if bad == "node":
+        path = np.array([[0, 45], [0, 1], [0, 2]])
+        x = kv.view(3, 15, 2, hkv, d)
+        mt.kv_append_accepted(x[:, :, 0].contiguous().cuda(), x[:, :, 1].contiguous().cuda(), _i32(path).cuda(), _i32([1, 1, 1]).cuda(), cache.k,
+                              cache.v, _i32(table).cuda(), _i32(past).cuda(), status_ws=ws, **cache.args())
+        assert mt.read_status(ws) == -4
+        return
+    mt.kv_append_paged(dev[:, 0], dev[:, 1], cache.k, cache.v, _i32(table).cuda(), _i32(past).cuda(), _i32(off).cuda(), status_ws=ws, rope=rope,
+                       **cache.args())
+    assert mt.read_status(ws) == want
+    if not skip:
+        return
+    rot = ref.rope_table(BASE, d, 64) if rope else None
+    before = [t.clone() for t in cache.host], [s.copy() for s in cache.host_scales]
+    if bad == "page":
+        table[1, 1] = table[1, 0]  # any place: its rows are put back below
+    if bad == "table":
+        past[1] = -1
+    keep = table[1, 1]
+    _append_on_host(cache, kv[:, 0], kv[:, 1], lambda b: list(range(off[b], off[b + 1] - (14 if bad == "page" and b == 1 else 0))), past, table, rot)
+    if bad == "position":
+        for w in range(2):
+            cache.host[w].view(torch.uint8)[keep] = before[0][w].view(torch.uint8)[keep]
+            cache.host_scales[w][keep] = before[1][w][keep]
+    cache.check()
+
+
+# ---- attention over the block-scaled cache ---------------------------------
+
+def _attn_case(rng, b, t, hq, hkv, d, lens, dtype, tree="tree", spread=2.0):
+    dt = DT[dtype]
+    need = [-(-max(n, 0) // P) for n in lens]
+    pages = sum(need) + 2
+    table = _table(rng, need, pages)
+    k, v = (rng.integers(0, 256, (pages, hkv, P, d)).astype(np.uint8) for _ in range(2))  # stale slots hold anything
+    ks, vs = (2.0 ** rng.integers(-3, 2, (pages, hkv)).astype(np.float64) for _ in range(2))
+    for i, n in enumerate(lens):
+        for p in range(max(n, 0)):
+            for c, s in ((k, ks), (v, vs)):
+                pg = table[i, p // P]
+                c[pg, :, p % P] = ref.encode(rng.standard_normal((hkv, d)) / s[pg][:, None])
+    parents = None
+    if tree == "tree":
+        parents = np.full((b, t), -1)
+        for i in range(b):
+            for j in range(1, t):
+                parents[i, j] = rng.integers(max(0, j - 9), j)
+    q, kn, vn = (_rand(rng, b, t, h, d, dtype=dt, scale=s) for h, s in ((hq, spread), (hkv, 1.0), (hkv, 1.0)))
+    return dict(q=q, kn=kn, vn=vn, k=k, v=v, ks=ks, vs=vs, table=table, lens=lens, parents=parents)
+
+
+def _attn_run(c, out=None, ws=None, sm_scale=0.0):
+    f8 = lambda x: torch.from_numpy(x).cuda().view(torch.float8_e4m3fn)  # noqa: E731
+    q, kc, table = c["q"].cuda(), f8(c["k"]), _i32(c["table"]).cuda()
+    out = torch.full_like(q, 5.0) if out is None else out
+    ws = mt.alloc_block8_workspace(q, kc, table) if ws is None else ws
+    args = (q, kc, f8(c["v"]), torch.from_numpy(c["ks"]).float().cuda(), torch.from_numpy(c["vs"]).float().cuda(), table, _i32(c["lens"]).cuda(),
+            None if c["parents"] is None else _i32(c["parents"]).cuda(), out)
+    kw = dict(k_new=c["kn"].cuda(), v_new=c["vn"].cuda(), workspace=ws, sm_scale=sm_scale)
+    mt.tree_attn_paged_block8(*args, **kw)
+    return out, ws, args, kw
+
+
+def _attn_check(c, out, sm_scale=0.0):
+    q = c["q"].double().numpy()
+    d = q.shape[-1]
+    want, mag = ref.attn64(q, c["k"], c["v"], c["ks"], c["vs"], c["table"], c["lens"], c["parents"], c["kn"].double().numpy(),
+                           c["vn"].double().numpy(), sm_scale or d ** -0.5)
+    got = out.cpu().double().numpy()
+    u = ref.HALF_STEP[c["q"].dtype]
+    live = np.array([n >= 0 for n in c["lens"]])
+    tol = u * np.abs(want) + (u + 2.0 ** -11 + 2.0 ** -8) * mag + 1e-7
+    assert np.isfinite(got[live]).all()
+    bad = np.abs(got - want)[live] > tol[live]
+    assert not bad.any(), (np.abs(got - want)[live] / tol[live]).max()
+    assert (got[~live] == 5.0).all()
+
+
+ATTN = [  # T, Hq, Hkv, D, lengths
+    (1, 1, 1, 64, [0]), (1, 1, 1, 64, [1]), (1, 4, 1, 128, [16]), (1, 8, 2, 128, [17, 0, 300]),
+    (1, 7, 1, 128, [63, 64, 65]), (2, 3, 3, 64, [5, 40]), (5, 12, 4, 128, [200, -1, 31]),
+    (16, 2, 2, 128, [100, 3]), (17, 2, 1, 64, [90]), (64, 4, 1, 128, [250, 0]), (64, 8, 8, 64, [33]),
+    (26, 8, 1, 128, [500]), (33, 3, 1, 128, [129, 64]), (64, 32, 4, 128, [100]),
+]
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("tree", ["tree", "chain"])
+@pytest.mark.parametrize("case", range(len(ATTN)))
+def test_block8_attention(dtype, tree, case):
+    t, hq, hkv, d, lens = ATTN[case]
+    rng = np.random.default_rng(case)
+    c = _attn_case(rng, len(lens), t, hq, hkv, d, lens, dtype, tree)
+    out, ws, _, _ = _attn_run(c)
+    assert mt.read_status(ws) == 0
+    _attn_check(c, out)
+
+
+def test_block8_attention_scale_and_empty_batch():
+    c = _attn_case(np.random.default_rng(50), 3, 4, 8, 2, 128, [70, 20, 33], "bf16")
+    out, ws, _, _ = _attn_run(c, sm_scale=0.02)
+    _attn_check(c, out, 0.02)
+    c["lens"] = [-1, -1, -1]
+    out, ws, _, _ = _attn_run(c)
+    assert mt.read_status(ws) == 0 and bool((out == 5.0).all())
+
+
+def test_block8_attention_many_sequences():
+    rng = np.random.default_rng(60)
+    lens = [int(n) for n in rng.integers(-1, 40, 300)]
+    c = _attn_case(rng, 300, 1, 2, 1, 64, lens, "f16", "chain")
+    out, ws, _, _ = _attn_run(c)
+    assert mt.read_status(ws) == 0
+    _attn_check(c, out)
+
+
+def test_block8_attention_of_widely_spread_scales():
+    # pages whose value scales differ by 2^40 and more, a page of zeros, one dominant key
+    rng = np.random.default_rng(70)
+    c = _attn_case(rng, 1, 3, 4, 2, 128, [160], "bf16")
+    for p, k in zip(c["table"][0], (-64, -20, 0, 10, -3, 4, 20, -40, 0, 1)):
+        c["vs"][p] = 2.0 ** k
+    c["v"][c["table"][0][0]] = 0
+    out, ws, _, _ = _attn_run(c)
+    assert mt.read_status(ws) == 0
+    _attn_check(c, out)
+
+
+def test_block8_attention_of_a_dominant_first_key():
+    # the first key takes most of the mass and its value is small: what is left of the output is the others'
+    rng = np.random.default_rng(71)
+    c = _attn_case(rng, 1, 2, 4, 1, 128, [600], "bf16", spread=1.0)
+    q = c["q"].double().numpy()
+    first = c["table"][0][0]
+    c["k"][first, 0, 0] = ref.encode(np.sign(q[0, 0].sum(0)) * 8 / c["ks"][first, 0])
+    c["v"][first, 0, 0] = 0
+    out, ws, _, _ = _attn_run(c)
+    _attn_check(c, out)
+
+
+def test_block8_attention_reports_bad_pages_and_trees():
+    rng = np.random.default_rng(80)
+    c = _attn_case(rng, 2, 4, 4, 2, 64, [50, 20], "f16")
+    good = c["table"].copy()
+    c["table"][0, 2] = 99
+    assert mt.read_status(_attn_run(c)[1]) == -4
+    c["table"] = good
+    c["lens"] = [50, 100]
+    assert mt.read_status(_attn_run(c)[1]) == -4
+    c["lens"] = [50, 20]
+    c["parents"][1, 2] = 3
+    assert mt.read_status(_attn_run(c)[1]) == -3
+
+
+def test_block8_attention_in_a_graph_and_on_another_stream():
+    rng = np.random.default_rng(90)
+    c = _attn_case(rng, 4, 3, 8, 2, 128, [700, 20, 64, 333], "bf16")
+    want, ws, args, kw = _attn_run(c)
+    _attn_check(c, want)
+    out = args[-1]
+    want = out.clone()
+    g = _graph(lambda: mt.tree_attn_paged_block8(*args, **kw))
+    out.fill_(5.0)
+    g.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(out, want)
+    # the lengths are read at replay: a shorter batch with the same graph
+    args[6].copy_(_i32([100, 20, -1, 5]))
+    out.fill_(5.0)
+    g.replay()
+    c["lens"] = [100, 20, -1, 5]
+    _attn_check(c, out)
+
+
+# ---- sampling ---------------------------------------------------------------
+
+def _sample(x, u, t=None, k=None, p=None, m=None, index=None, tokens=None):
+    n = len(u)
+    f = lambda a: None if a is None else torch.as_tensor(np.asarray(a, np.float32)).cuda()  # noqa: E731
+    tokens = torch.full((n,), -7, dtype=torch.int32, device="cuda") if tokens is None else tokens
+    mt.sample_tokens(x, f(u), tokens, temperature=f(t), top_k=None if k is None else _i32(k).cuda(), top_p=f(p), min_p=f(m),
+                     row_index=None if index is None else _i32(index).cuda())
+    return tokens.cpu().numpy()
+
+
+def _sample_check(x, u, t, k, p, m):
+    got = _sample(x, u, t, k, p, m)
+    h = x.cpu().double().numpy()
+    f = lambda a: np.asarray(a, np.float32).astype(np.float64)  # noqa: E731
+    want = [ref.sample64(h[i], f(u)[i], f(t)[i], int(k[i]), f(p)[i], f(m)[i]) for i in range(len(u))]
+    assert got.tolist() == want
+
+
+def _params(rng, n):
+    return (rng.choice([0.0, 0.5, 0.8, 1.0, 1.5], n), rng.choice([0, 1, 2, 17, 50, 1000], n), rng.choice([1.0, 0.9, 0.5, 0.99], n),
+            rng.choice([0.0, 0.0, 0.02, 0.2], n))
+
+
+@pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("n, v", [(1, 1), (4, 2), (33, 7), (16, 1000), (40, 4099), (24, 32000), (3, 32001), (12, 70003), (2, 200000), (1, 499999)])
+def test_sampling(dtype, n, v):
+    rng = np.random.default_rng(v)
+    x = _rand(rng, n, v, scale=2.5)
+    x.view(-1)[torch.from_numpy(rng.integers(0, n * v, 4 * n))] += 5
+    t, k, p, m = _params(rng, n)
+    _sample_check(x.to(DT[dtype]).cuda(), rng.random(n), t, k, p, m)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("kind", ["equal", "two", "whole", "negative", "tiny", "huge", "masked"])
+def test_sampling_ties_and_odd_ranges(dtype, kind):
+    rng = np.random.default_rng(len(kind))
+    n, v = 32, 5003
+    x = {"equal": lambda: np.full((n, v), 0.25), "two": lambda: rng.integers(0, 2, (n, v)) * 1.0, "whole": lambda: np.round(rng.standard_normal((n, v)) * 2),
+         "negative": lambda: -100 - rng.random((n, v)) * 10, "tiny": lambda: rng.standard_normal((n, v)) * 1e-6,
+         "huge": lambda: rng.standard_normal((n, v)) * 1e4, "masked": lambda: np.where(rng.random((n, v)) < 0.9, -np.inf, rng.standard_normal((n, v)))}[kind]()
+    t, k, p, m = _params(rng, n)
+    _sample_check(torch.from_numpy(x).to(DT[dtype]).cuda(), rng.random(n), t, k, p, m)
+
+
+def test_sampling_limits_of_the_parameters():
+    rng = np.random.default_rng(7)
+    v = 3001
+    x = _rand(rng, 1, v, scale=2.0).repeat(20, 1).cuda()
+    u = np.array([0.0, 1 - 2.0 ** -24] * 10, np.float32)
+    t = np.repeat([1e-30, 1e-3, 1.0, 100.0, 1e30, 1.0, 1.0, 1.0, 1.0, 1.0], 2)
+    k = np.repeat([0, 0, v, v + 5, -3, v - 1, 1, 0, 0, 0], 2)
+    p = np.repeat([1.0, 1.0, 2.0, 1.0, 1.0, 1.0, 0.9, 0.0, 1e-9, 0.999999], 2)
+    m = np.repeat([0.0, 0.0, -1.0, 0.0, 0.0, 0.0, 0.0, 0.0, 1.0, 1.5], 2)
+    _sample_check(x, u, t, k, p, m)
+    top = int(x[0].argmax())
+    assert _sample(x[:3], [2.0, -1.0, float("nan")], [1e-3] * 3).tolist() == [top] * 3  # numbers outside [0, 1)
+
+
+def test_sampling_infinities_and_nan():
+    rng = np.random.default_rng(9)
+    v = 777
+    x = _rand(rng, 6, v)
+    x[0, :] = float("-inf")
+    x[1, :] = float("nan")
+    x[2, ::2] = float("nan")
+    x[3, [5, 600]] = float("inf")
+    x[4, :] = float("-inf")
+    x[4, 31] = -3.0
+    u = [0.3, 0.3, 0.4, 0.6, 0.9, 0.2]
+    for k, p, m in ((0, 1.0, 0.0), (3, 0.9, 0.1), (700, 0.99, 0.0)):
+        one = [1.0] * 6
+        _sample_check(x.cuda(), u, one, [k] * 6, [p] * 6, [m] * 6)
+    assert _sample(x.cuda(), u)[:2].tolist() == [-1, -1]
+    assert _sample(x.cuda(), u)[3] == 600 and _sample(x.cuda(), u)[4] == 31
+
+
+def test_sampling_rows_by_index_strides_and_places_without_a_row():
+    rng = np.random.default_rng(12)
+    big = _rand(rng, 10, 3, 1003, dtype=torch.bfloat16).cuda()
+    x = big[:, 1]  # every third row, unaligned
+    u = rng.random(6)
+    index = [3, 0, -1, 9, 10, 3]
+    got = _sample(x, u, index=index)
+    h = x.cpu().double().numpy()
+    want = [ref.sample64(h[r], np.float64(np.float32(v)), 1.0, 0, 1.0, 0.0) if 0 <= r < 10 else (-7 if r < 0 else -1) for r, v in zip(index, u)]
+    assert got.tolist() == want
+
+
+def test_sampling_whole_distribution():
+    # 4096 evenly spread numbers draw each token as often as its probability says, within one
+    v, n = 50, 4096
+    x = _rand(np.random.default_rng(13), 1, v, scale=1.5)
+    got = _sample(x.repeat(n, 1).cuda(), (np.arange(n) + 0.5) / n)
+    w = np.exp(x[0].double().numpy() - float(x.max()))
+    count = np.bincount(got, minlength=v)
+    assert (np.abs(count - w / w.sum() * n) <= 1.0 + 1e-6).all()
+
+
+def test_sampling_in_a_graph():
+    rng = np.random.default_rng(14)
+    x, u = _rand(rng, 5, 9000, scale=2.0).cuda(), torch.rand(5, device="cuda")
+    tokens = torch.zeros(5, dtype=torch.int32, device="cuda")
+    par = dict(temperature=torch.full((5,), 0.9, device="cuda"), top_p=torch.full((5,), 0.9, device="cuda"))
+    g = _graph(lambda: mt.sample_tokens(x, u, tokens, **par))
+    for _ in range(3):
+        x.copy_(_rand(rng, 5, 9000, scale=2.0))
+        u.copy_(torch.rand(5))
+        tokens.zero_()
+        g.replay()
+        got = tokens.cpu().tolist()
+        assert got == mt.sample_tokens(x, u, torch.zeros_like(tokens), **par).cpu().tolist()
+
+
+# ---- together ----------------------------------------------------------------
+
+def test_prompt_step_and_draw_together():
+    """Two layers of one serving pass: prompts into a block-scaled cache, a tree step over it, acceptance, the
+    accepted path appended, a token drawn from the end node's row; each result against the plain implementations."""
+    rng = np.random.default_rng(100)
+    b, t, hq, hkv, d, v, dt = 3, 8, 8, 2, 128, 500, torch.bfloat16
+    prompts = [37, 5, 80]
+    off = np.concatenate([[0], np.cumsum(prompts)])
+    n = int(off[-1])
+    table = _table(rng, [4, 2, 6], 14)
+    rope, rot, ws = mt.Rope(BASE, d, 128), ref.rope_table(BASE, d, 128), _status()
+    lens = torch.zeros(b, dtype=torch.int32, device="cuda")
+    w = (1 + 0.1 * _rand(rng, d)).to(dt)
+    parents = np.array([[-1, 0, 0, 1, 1, 2, 3, 3]] * b)
+    depths = np.array([0, 1, 1, 2, 2, 2, 3, 3])
+    tokens = rng.integers(0, v, (b, t))
+    logits = _rand(rng, b, t, v, scale=2.0)
+    for i, path in enumerate(([0, 1, 3], [0], [0, 2, 5])):  # the accepted paths
+        for a, c in zip(path, path[1:]):
+            logits[i, a, tokens[i, c]] = 30.0
+        logits[i, path[-1], :] += 0  # the end's argmax is none of its children's tokens but by chance
+        for c in range(t):
+            if parents[i, c] == path[-1]:
+                logits[i, path[-1], tokens[i, c]] = -30.0
+    dtab = _i32(table).cuda()
+    states = []
+    for layer in range(2):
+        cache = Cache(rng, "block8", 14, hkv, d, dt)
+        qkv = _rand(rng, n, hq + 2 * hkv, d, dtype=dt).cuda()
+        pos = torch.cat([torch.arange(p) for p in prompts]).int().cuda()
+        q, k = qkv[:, :hq], qkv[:, hq:hq + hkv]
+        mt.qk_norm_rope(q, k, pos, q, k, rope=rope, q_weight=w.cuda(), k_weight=w.cuda(), status_ws=ws)
+        mt.kv_append_paged(k, qkv[:, hq + hkv:], cache.k, cache.v, dtab, lens, _i32(off).cuda(), status_ws=ws, **cache.args())
+        _append_on_host(cache, k.cpu(), qkv[:, hq + hkv:].cpu(), lambda i: list(range(off[i], off[i + 1])), [0] * b, table, None)
+        cache.check()
+        states.append(cache)
+    lens += _i32(prompts).cuda()
+    rows = [_rand(rng, b, t, hq + 2 * hkv, d, dtype=dt) for _ in range(2)]
+    kept = []
+    for cache, x in zip(states, rows):
+        y = x.cuda().view(b * t, -1, d)
+        pos = (lens[:, None] + _i32(depths).cuda()).view(-1).int()
+        q, k = torch.empty(b * t, hq, d, dtype=dt, device="cuda"), torch.empty(b * t, hkv, d, dtype=dt, device="cuda")
+        mt.qk_norm_rope(y[:, :hq], y[:, hq:hq + hkv], pos, q, k, rope=rope, q_weight=w.cuda(), k_weight=w.cuda(), status_ws=ws)
+        q, k, vn = q.view(b, t, hq, d), k.view(b, t, hkv, d), y[:, hq + hkv:].contiguous().view(b, t, hkv, d)
+        out = torch.empty_like(q)
+        aws = mt.alloc_block8_workspace(q, cache.k, dtab)
+        mt.tree_attn_paged_block8(q, cache.k, cache.v, *cache.scales, dtab, lens, _i32(parents).cuda(), out, k_new=k, v_new=vn, workspace=aws)
+        assert mt.read_status(aws) == 0
+        _attn_check(dict(q=q.cpu(), kn=k.cpu(), vn=vn.cpu(), k=_codes(cache.k), v=_codes(cache.v), ks=cache.host_scales[0], vs=cache.host_scales[1],
+                         table=table, lens=prompts, parents=parents), out)
+        kept.append((k, vn))
+    alen, path = torch.zeros(b, dtype=torch.int32, device="cuda"), torch.zeros(b, 4, dtype=torch.int32, device="cuda")
+    mt.tree_accept_greedy(_i32(tokens).cuda(), logits.cuda(), _i32(parents).cuda(), alen, path, argmax_out=torch.zeros(b, t, dtype=torch.int32, device="cuda"),
+                          next_token=torch.zeros(b, dtype=torch.int32, device="cuda"), workspace=mt.alloc_accept_workspace(b, t))
+    assert alen.tolist() == [2, 0, 2]
+    for cache, (k, vn) in zip(states, kept):
+        mt.kv_append_accepted(k, vn, path, alen, cache.k, cache.v, dtab, lens, status_ws=ws, **cache.args())
+        _append_on_host(cache, k.cpu().view(b * t, hkv, d), vn.cpu().view(b * t, hkv, d),
+                        lambda i: [i * t + int(path[i, j]) for j in range(int(alen[i]) + 1)], prompts, table, None)
+        cache.check()
+    lens += alen + 1
+    end = path.gather(1, alen[:, None].long())[:, 0] + torch.arange(b, device="cuda", dtype=torch.int32) * t
+    u = rng.random(b)
+    got = _sample(logits.cuda().view(b * t, v), u, [0.8] * b, [40] * b, [0.95] * b, [0.0] * b, index=end.cpu().numpy())
+    f = lambda a: np.float64(np.float32(a))  # noqa: E731
+    assert got.tolist() == [ref.sample64(logits.view(b * t, v)[int(end[i])].double().numpy(), f(u[i]), f(0.8), 40, f(0.95), 0.0) for i in range(b)]
+    assert mt.read_status(ws) == 0
