@@ -22,6 +22,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 from typing import Optional
 
 import torch
@@ -69,6 +70,14 @@ class AppendDesc(ctypes.Structure):
                 ("v_stride", ctypes.c_longlong * 2)]
 
 
+# The descriptors as the binding passes them: the same bytes, packed in one go
+# (filling a ctypes structure costs several times as much).
+_NORM_ROPE_DESC = struct.Struct("@5if8q")
+_APPEND_DESC = struct.Struct("@9i2f4q")
+_ATTN_DESC = struct.Struct("@10ifi" "i2f")
+assert (_NORM_ROPE_DESC.size == ctypes.sizeof(NormRopeDesc) and _APPEND_DESC.size == ctypes.sizeof(AppendDesc)
+        and _ATTN_DESC.size == ctypes.sizeof(AttnDesc))
+
 _lib = None
 
 
@@ -98,13 +107,12 @@ def _load():
         lib.mt_tree_accept_commit.argtypes = [D, I, I, I] + [P] * 12 + [P, Z, P]
         lib.mt_tree_candidates.argtypes = [I, I, I, I, I] + [P] * 5 + [P]
         L = ctypes.c_longlong
-        lib.mt_qk_norm_rope.argtypes = [ctypes.POINTER(NormRopeDesc)] + [P] * 10
-        A = ctypes.POINTER(AppendDesc)
-        lib.mt_kv_append_paged.argtypes = [A] + [P] * 12
-        lib.mt_kv_append_accepted.argtypes = [A, I, I] + [P] * 13
-        lib.mt_tree_attn_block8_workspace_size.argtypes = [D]
+        lib.mt_qk_norm_rope.argtypes = [P] + [P] * 10
+        lib.mt_kv_append_paged.argtypes = [P] + [P] * 12
+        lib.mt_kv_append_accepted.argtypes = [P, I, I] + [P] * 13
+        lib.mt_tree_attn_block8_workspace_size.argtypes = [P]
         lib.mt_tree_attn_block8_workspace_size.restype = Z
-        lib.mt_tree_attn_paged_block8.argtypes = [D] + [P] * 12 + [Z, P]
+        lib.mt_tree_attn_paged_block8.argtypes = [P] + [P] * 12 + [Z, P]
         lib.mt_sample_tokens.argtypes = [I, I, I, P, I, L] + [P] * 7 + [P]
         lib.mt_read_status.argtypes = [P, P, ctypes.POINTER(I)]
         lib.mt_profile_enable.argtypes = [I]
@@ -466,44 +474,51 @@ def tree_candidates(root_logits, head_logits, tree_parents, tree_tokens, *, stat
 # ---- the serving operators around the step ----------------------------------
 #
 # One check per argument (dtype, shape, device, layout), then the call on the
-# arguments' device: a decoding step makes a dozen of these calls per layer, so
-# the checks are kept short.
+# arguments' device.  A decoding step makes several of these calls per layer, so
+# an argument that fits costs one pass over its attributes; the reason is worked
+# out for one that does not.
 
 _E4M3 = torch.float8_e4m3fn
 
 
-def _arg(t, name, dtype, shape, dev):
-    """A dense CUDA tensor of this dtype, shape and device; its address."""
+def _refuse(t, name, dtype, shape, dev, layout):
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if t.dtype is not dtype:
         raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
     if t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
     if t.device != dev:
         raise ValueError(f"{name} is on {t.device}, the other tensors on {dev}")
-    return t.data_ptr()
+    raise ValueError(f"{name} must {layout}, got strides {t.stride()}")
+
+
+def _arg(t, name, dtype, shape, dev):
+    """A dense CUDA tensor of this dtype, shape and device; its address."""
+    try:
+        if t.dtype is dtype and t.shape == shape and t.device == dev and t.is_contiguous():
+            return t.data_ptr()
+    except AttributeError:
+        pass
+    _refuse(t, name, dtype, shape, dev, "be contiguous")
 
 
 def _rows_arg(t, name, dtype, shape, dev):
     """A CUDA tensor [rows, heads, D] whose head rows are dense and 16-byte
     aligned (a view of a projection's output, say); its address and strides."""
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name} must be a torch.Tensor")
-    if t.dtype is not dtype:
-        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.shape != shape:
-        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
-    if t.device != dev:
-        raise ValueError(f"{name} is on {t.device}, the other tensors on {dev}")
-    st = t.stride()
-    s0, s1 = st[0] if shape[0] > 1 else 0, st[1] if shape[1] > 1 else 0
-    unit = 16 // t.element_size()
-    if st[2] != 1 or s0 % unit or s1 % unit or t.data_ptr() % 16:
-        raise ValueError(f"{name} must have dense, 16-byte aligned head rows, got strides {st}")
-    return t.data_ptr(), (s0, s1)
+    try:
+        if t.dtype is dtype and t.shape == shape and t.device == dev:
+            s0, s1, s2 = t.stride()
+            if shape[0] <= 1:
+                s0 = 0
+            if shape[1] <= 1:
+                s1 = 0
+            p = t.data_ptr()
+            if s2 == 1 and not (p | (s0 | s1) * t.element_size()) & 15:
+                return p, s0, s1
+    except AttributeError:
+        pass
+    _refuse(t, name, dtype, shape, dev, "have dense, 16-byte aligned head rows")
 
 
 def _cuda_device(t, name):
@@ -530,15 +545,15 @@ def _status_arg(t, name, dev, nbytes=256):
 
 def _invoke(fn, what, dev, stream, *args):
     """The call on its tensors' device: on `stream`, or that device's current one."""
+    if stream is None:
+        stream = torch._C._cuda_getCurrentRawStream(dev.index)
+    elif hasattr(stream, "cuda_stream"):
+        stream = stream.cuda_stream
     if torch.cuda.current_device() == dev.index:
-        if stream is None:
-            stream = torch.cuda.current_stream()
-        st = fn(*args, stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream))
+        st = fn(*args, stream)
     else:
         with torch.cuda.device(dev):
-            if stream is None:
-                stream = torch.cuda.current_stream()
-            st = fn(*args, stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream))
+            st = fn(*args, stream)
     if st != MT_OK:
         raise MedusaTreeError(st, what)
 
@@ -555,11 +570,12 @@ def qk_norm_rope(q, k, positions, q_out, k_out, *, rope: Optional[Rope] = None, 
         raise ValueError("q and k must have 3 dims (tokens, heads, head_dim)")
     n, hq, d = q.shape
     hkv = k.shape[1]
-    qp, qs = _rows_arg(q, "q", q.dtype, (n, hq, d), dev)
-    kp, ks = _rows_arg(k, "k", q.dtype, (n, hkv, d), dev)
-    qop, qos = _rows_arg(q_out, "q_out", q.dtype, (n, hq, d), dev)
-    kop, kos = _rows_arg(k_out, "k_out", q.dtype, (n, hkv, d), dev)
-    if (n > 1 and not (qos[0] and kos[0])) or (hq > 1 and not qos[1]) or (hkv > 1 and not kos[1]):
+    ty, qshape, kshape = q.dtype, (n, hq, d), (n, hkv, d)
+    qp, q0, q1 = _rows_arg(q, "q", ty, qshape, dev)
+    kp, k0, k1 = _rows_arg(k, "k", ty, kshape, dev)
+    qop, qo0, qo1 = _rows_arg(q_out, "q_out", ty, qshape, dev)
+    kop, ko0, ko1 = _rows_arg(k_out, "k_out", ty, kshape, dev)
+    if (n > 1 and not (qo0 and ko0)) or (hq > 1 and not qo1) or (hkv > 1 and not ko1):
         raise ValueError("q_out and k_out must not be expanded views")
     pos = None if positions is None else _arg(positions, "positions", torch.int32, (n,), dev)
     if rope is not None and positions is None:
@@ -568,21 +584,21 @@ def qk_norm_rope(q, k, positions, q_out, k_out, *, rope: Optional[Rope] = None, 
         raise ValueError("q_weight and k_weight go together")
     if q_weight is None and rope is None:
         raise ValueError("nothing to do: neither weights nor rope")
-    qw = None if q_weight is None else _arg(q_weight, "q_weight", q.dtype, (d,), dev)
-    kw = None if k_weight is None else _arg(k_weight, "k_weight", q.dtype, (d,), dev)
-    desc = NormRopeDesc(n, hq, hkv, d, dt, eps, qs, ks, qos, kos)
+    qw = None if q_weight is None else _arg(q_weight, "q_weight", ty, (d,), dev)
+    kw = None if k_weight is None else _arg(k_weight, "k_weight", ty, (d,), dev)
+    desc = _NORM_ROPE_DESC.pack(n, hq, hkv, d, dt, eps, q0, q1, k0, k1, qo0, qo1, ko0, ko1)
     _invoke(_load().mt_qk_norm_rope, "mt_qk_norm_rope", dev, stream, desc, qp, kp, pos, qw, kw,
             None if rope is None else rope.handle, qop, kop, _status_arg(status_ws, "status_ws", dev))
     return q_out, k_out
 
 
 def _append_args(k, v, k_cache, v_cache, block_tables, seq_lens, k_scales, v_scales, k_scale, v_scale):
-    """Checks shared by the appends: the descriptor and the addresses."""
+    """Checks shared by the appends: the batch, the descriptor and the addresses."""
     dev = _cuda_device(k, "k")
     dt = _act(k, "k")
     n, hkv, d = k.shape
-    kp, ks = _rows_arg(k, "k", k.dtype, (n, hkv, d), dev)
-    vp, vs = _rows_arg(v, "v", k.dtype, (n, hkv, d), dev)
+    kp, k0, k1 = _rows_arg(k, "k", k.dtype, (n, hkv, d), dev)
+    vp, v0, v1 = _rows_arg(v, "v", k.dtype, (n, hkv, d), dev)
     if not isinstance(k_cache, torch.Tensor) or k_cache.dim() != 4:
         raise ValueError("k_cache must have 4 dims (pages, heads, slots, head_dim)")
     cdt = k_cache.dtype
@@ -604,9 +620,9 @@ def _append_args(k, v, k_cache, v_cache, block_tables, seq_lens, k_scales, v_sca
             raise ValueError(f"block scales need a cache of {_E4M3}")
         ksp = _arg(k_scales, "k_scales", torch.float32, (pages, hkv), dev)
         vsp = _arg(v_scales, "v_scales", torch.float32, (pages, hkv), dev)
-    desc = AppendDesc(b, n, hkv, d, page, blocks, pages, dt, MT_E4M3 if cdt is _E4M3 else 0, k_scale,
-                      v_scale, ks, vs)
-    return dev, desc, (kp, vp), (kcp, vcp, ksp, vsp, btp, slp)
+    desc = _APPEND_DESC.pack(b, n, hkv, d, page, blocks, pages, dt, MT_E4M3 if cdt is _E4M3 else 0,
+                             k_scale, v_scale, k0, k1, v0, v1)
+    return dev, b, desc, (kp, vp), (kcp, vcp, ksp, vsp, btp, slp)
 
 
 def kv_append_paged(k, v, k_cache, v_cache, block_tables, seq_lens, row_offsets, *,
@@ -619,9 +635,9 @@ def kv_append_paged(k, v, k_cache, v_cache, block_tables, seq_lens, row_offsets,
     k_scales / v_scales [pages,Hkv] (updated).  seq_lens is not changed."""
     if not isinstance(k, torch.Tensor) or k.dim() != 3:
         raise ValueError("k must have 3 dims (rows, heads, head_dim)")
-    dev, desc, kv, rest = _append_args(k, v, k_cache, v_cache, block_tables, seq_lens, k_scales,
-                                       v_scales, k_scale, v_scale)
-    off = _arg(row_offsets, "row_offsets", torch.int32, (desc.batch + 1,), dev)
+    dev, b, desc, kv, rest = _append_args(k, v, k_cache, v_cache, block_tables, seq_lens, k_scales,
+                                          v_scales, k_scale, v_scale)
+    off = _arg(row_offsets, "row_offsets", torch.int32, (b + 1,), dev)
     _invoke(_load().mt_kv_append_paged, "mt_kv_append_paged", dev, stream, desc, *kv, off,
             None if rope is None else rope.handle, *rest, _status_arg(status_ws, "status_ws", dev))
 
@@ -640,10 +656,10 @@ def kv_append_accepted(k_new, v_new, accept_path, accept_len, k_cache, v_cache, 
     if not k_new.is_contiguous() or not v_new.is_contiguous():
         raise ValueError("k_new and v_new must be contiguous")
     b, t, hkv, d = k_new.shape
-    dev, desc, kv, rest = _append_args(k_new.view(b * t, hkv, d), v_new.view(b * t, hkv, d), k_cache,
-                                       v_cache, block_tables, seq_lens, k_scales, v_scales, k_scale,
-                                       v_scale)
-    if desc.batch != b:
+    dev, nb, desc, kv, rest = _append_args(k_new.view(b * t, hkv, d), v_new.view(b * t, hkv, d),
+                                           k_cache, v_cache, block_tables, seq_lens, k_scales, v_scales,
+                                           k_scale, v_scale)
+    if nb != b:
         raise ValueError("block_tables must have one row per sequence")
     if not isinstance(accept_path, torch.Tensor) or accept_path.dim() != 2:
         raise ValueError("accept_path must have 2 dims")
@@ -657,8 +673,8 @@ def kv_append_accepted(k_new, v_new, accept_path, accept_len, k_cache, v_cache, 
 def _block8_desc(q, k_cache, block_tables, sm_scale=0.0):
     b, t, hq, d = q.shape
     pages, hkv, page = k_cache.shape[:3]
-    return AttnDesc(b, t, hq, hkv, d, page, block_tables.shape[1], pages, 0, _DTYPES[q.dtype], sm_scale,
-                    0, MT_E4M3, 1.0, 1.0)
+    return _ATTN_DESC.pack(b, t, hq, hkv, d, page, block_tables.shape[1], pages, 0, _DTYPES[q.dtype],
+                           sm_scale, 0, MT_E4M3, 1.0, 1.0)
 
 
 def alloc_block8_workspace(q, k_cache, block_tables) -> torch.Tensor:
@@ -666,7 +682,7 @@ def alloc_block8_workspace(q, k_cache, block_tables) -> torch.Tensor:
     dev = _cuda_device(q, "q")
     _act(q, "q", (torch.float16, torch.bfloat16))
     with torch.cuda.device(dev):
-        n = int(_load().mt_tree_attn_block8_workspace_size(ctypes.byref(_block8_desc(q, k_cache, block_tables))))
+        n = int(_load().mt_tree_attn_block8_workspace_size(_block8_desc(q, k_cache, block_tables)))
     if n == 0:
         raise MedusaTreeError(-1, "mt_tree_attn_block8_workspace_size")
     return torch.zeros(n, dtype=torch.uint8, device=dev)
@@ -692,18 +708,17 @@ def tree_attn_paged_block8(q, k_cache, v_cache, k_scales, v_scales, block_tables
     pages, hkv, page = k_cache.shape[:3]
     if not isinstance(block_tables, torch.Tensor) or block_tables.dim() != 2:
         raise ValueError("block_tables must have 2 dims")
-    cache, scales, new = (pages, hkv, page, d), (pages, hkv), (b, t, hkv, d)
-    desc = _block8_desc(q, k_cache, block_tables, sm_scale)
-    _invoke(_load().mt_tree_attn_paged_block8, "mt_tree_attn_paged_block8", dev, stream, desc,
-            _arg(q, "q", dt, (b, t, hq, d), dev), _arg(k_new, "k_new", dt, new, dev),
-            _arg(v_new, "v_new", dt, new, dev), _arg(k_cache, "k_cache", _E4M3, cache, dev),
-            _arg(v_cache, "v_cache", _E4M3, cache, dev),
-            _arg(k_scales, "k_scales", torch.float32, scales, dev),
-            _arg(v_scales, "v_scales", torch.float32, scales, dev),
-            _arg(block_tables, "block_tables", torch.int32, (b, block_tables.shape[1]), dev),
-            _arg(seq_lens, "seq_lens", torch.int32, (b,), dev),
-            None if tree_parents is None else _arg(tree_parents, "tree_parents", torch.int32, (b, t), dev),
-            _arg(out, "out", dt, (b, t, hq, d), dev), _status_arg(workspace, "workspace", dev),
+    cache, scales, new, rows = (pages, hkv, page, d), (pages, hkv), (b, t, hkv, d), (b, t, hq, d)
+    f32, i32 = torch.float32, torch.int32
+    _invoke(_load().mt_tree_attn_paged_block8, "mt_tree_attn_paged_block8", dev, stream,
+            _block8_desc(q, k_cache, block_tables, sm_scale), _arg(q, "q", dt, rows, dev),
+            _arg(k_new, "k_new", dt, new, dev), _arg(v_new, "v_new", dt, new, dev),
+            _arg(k_cache, "k_cache", _E4M3, cache, dev), _arg(v_cache, "v_cache", _E4M3, cache, dev),
+            _arg(k_scales, "k_scales", f32, scales, dev), _arg(v_scales, "v_scales", f32, scales, dev),
+            _arg(block_tables, "block_tables", i32, (b, block_tables.shape[1]), dev),
+            _arg(seq_lens, "seq_lens", i32, (b,), dev),
+            None if tree_parents is None else _arg(tree_parents, "tree_parents", i32, (b, t), dev),
+            _arg(out, "out", dt, rows, dev), _status_arg(workspace, "workspace", dev),
             workspace.numel() * workspace.element_size())
     return out
 

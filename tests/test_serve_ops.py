@@ -26,7 +26,7 @@ ODD = PTR + 2
 def _norm_desc(**kw):
     base = dict(num_tokens=4, num_q_heads=8, num_kv_heads=2, head_dim=128, dtype=2, eps=1e-6, q_stride=(1024, 128),
                 k_stride=(256, 128), q_out_stride=(1024, 128), k_out_stride=(256, 128))
-    return mt.NormRopeDesc(**{**base, **kw})
+    return ctypes.byref(mt.NormRopeDesc(**{**base, **kw}))
 
 
 @pytest.mark.parametrize("desc, want", [
@@ -52,7 +52,7 @@ def test_norm_rope_pointers(lib, args):
 def _append_desc(**kw):
     base = dict(batch=2, num_rows=10, num_kv_heads=2, head_dim=64, page_size=16, max_blocks_per_seq=4, num_pages=9, dtype=2, cache_dtype=3,
                 k_scale=1.0, v_scale=1.0, k_stride=(128, 64), v_stride=(128, 64))
-    return mt.AppendDesc(**{**base, **kw})
+    return ctypes.byref(mt.AppendDesc(**{**base, **kw}))
 
 
 @pytest.mark.parametrize("desc, want", [
@@ -91,7 +91,7 @@ def test_append_accepted_sizes(lib, t, depth, rows, want):
 def _attn_desc(**kw):
     base = dict(batch=2, tree_size=4, num_q_heads=8, num_kv_heads=2, head_dim=128, page_size=16, max_blocks_per_seq=8, num_pages=32, num_splits=0, dtype=2,
                 sm_scale=0.0, kernel=0, cache_dtype=3, k_scale=1.0, v_scale=1.0)
-    return mt.AttnDesc(**{**base, **kw})
+    return ctypes.byref(mt.AttnDesc(**{**base, **kw}))
 
 
 @pytest.mark.parametrize("desc, want", [
