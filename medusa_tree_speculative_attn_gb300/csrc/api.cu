@@ -111,6 +111,11 @@ int check_desc(const mt_attn_desc* d) {
 
 }  // namespace
 
+void mt::wait_bound(unsigned long long* limit_ns, int* stall) {
+  *limit_ns = g_wait_limit_ns ? g_wait_limit_ns : 2000000000ull;
+  *stall = g_wait_stall;
+}
+
 extern "C" {
 
 int mt_version(void) { return 10000; }
@@ -240,8 +245,7 @@ int mt_tree_attn_paged(const mt_attn_desc* d, const void* q, const void* k_new, 
   ap.part_ml = reinterpret_cast<float2*>(ws + w.ml);
   ap.sched = sched;
   ap.piece_table = pp.piece_table;
-  ap.wait_limit_ns = g_wait_limit_ns ? g_wait_limit_ns : 2000000000ull;
-  ap.test_stall = g_wait_stall;
+  wait_bound(&ap.wait_limit_ns, &ap.test_stall);
   bool prof = g_prof_n < g_prof_cap;
   if (kernel == MT_KERNEL_SIMT) {
     if (prof) cudaEventRecord(g_prof_ev[2 * g_prof_n], stream);

@@ -297,41 +297,10 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, MT>::CTAS) attn_block8_kernel
   const int nnew = (a.T + kP - 1) / kP;
   pdl_wait();
 
-  // ---- every CTA: tiles of each sequence and their prefix ----
-  {
-    int carry = 0;
-    for (int b0 = 0; b0 < a.B; b0 += kThreads) {
-      const int b = b0 + tid;
-      int n = 0;
-      if (b < a.B) {
-        const int L = a.seq_lens[b];
-        if ((long long)L > (long long)a.max_blocks * kP) {
-          if (blockIdx.x == 0) set_status(a.status, kStPages);
-        } else if (L >= 0) {
-          n = ((L + kP - 1) / kP + nnew + 3) / 4;
-        }
-      }
-      int incl = n;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int v = __shfl_up_sync(0xffffffffu, incl, o);
-        if (lane >= o) incl += v;
-      }
-      if (lane == 31) s_warp[warp] = incl;
-      __syncthreads();
-      int off = carry;
-      for (int w = 0; w < kWarps; ++w) {
-        if (w < warp) off += s_warp[w];
-        carry += s_warp[w];
-      }
-      if (b < a.B) s_pfx[b] = off + incl - n;
-      __syncthreads();
-    }
-    if (tid == 0) s_pfx[a.B] = carry;
-    __syncthreads();
-    if (blockIdx.x == 0)
-      for (int b = tid; b <= a.B; b += kThreads) p.tile_pfx[b] = s_pfx[b];
-  }
+  // every CTA: tiles of each sequence and their prefix
+  block8_prefix<kWarps>(a, s_pfx, s_warp, blockIdx.x == 0);
+  if (blockIdx.x == 0)
+    for (int b = tid; b <= a.B; b += kThreads) p.tile_pfx[b] = s_pfx[b];
   Sched sc = a.sched;
   sc.tile_pfx = s_pfx;
   PieceIter it;
@@ -615,9 +584,13 @@ cudaError_t launch_d(const Block8Params& p, cudaStream_t stream) {
 
 }  // namespace
 
-Block8Plan block8_plan(int rows) {
-  if (rows <= 16) return Block8Plan{16, Cfg<128, 1>::CTAS, 2};
-  return Block8Plan{32, Cfg<128, 2>::CTAS, 2};
+Block8Plan block8_plan(int rows, int g, int dtype) {
+  if (rows > 32 && tc_supported(128, g)) {
+    const int parts = dtype == 1 ? 3 : 2;
+    return Block8Plan{true, parts == 2 && rows > 128 ? 256 : 128, 1, 4, parts};
+  }
+  if (rows <= 16) return Block8Plan{false, 16, Cfg<128, 1>::CTAS, 2, 0};
+  return Block8Plan{false, 32, Cfg<128, 2>::CTAS, 2, 0};
 }
 
 cudaError_t launch_attn_block8(const Block8Params& p, int dtype, cudaStream_t stream) {

@@ -1,0 +1,737 @@
+// Tensor-core path of the block-scaled attention (sm_103a: tcgen05 + TMEM +
+// TMA), for calls with more query rows than the register-fragment kernel
+// serves well (attn_block8.cu; the choice is block8_plan's).
+//
+// The structure is the 16-bit kernel's (attn_tc.cu): persistent CTAs, one per
+// SM, walk the balanced schedule; a CTA holds up to MT * 128 query rows of one
+// (sequence, KV head) and streams 64-slot tiles of four pages.  What differs is
+// how 8-bit operands reach the tensor cores:
+//   S = Q K^T  stays in 8 bits (kind::f8f6f4): the cache's key codes go by TMA
+//              straight into the operand tile, and a query row enters as the
+//              sum of two (bf16) or three (fp16) E4M3 parts (block8_prep.cu),
+//              which multiply the same key tile one after the other into the
+//              same accumulator.  An 8-bit step covers 32 of the D products in
+//              the time that a 16-bit step takes for 16, so two parts cost what
+//              a 16-bit product costs, and no key is ever converted;
+//   O = P V    needs softmax weights over a wider range than 8 bits hold, so it
+//              runs in fp16: the producers convert value codes to fp16 (exact,
+//              one instruction for two codes) on the way into the tile.
+// Scales: a page's key scale multiplies its 16 columns of S in the softmax's
+// exponent (no extra operation); its value scale 2^lv joins the exponent, so the
+// running maximum is that of (score + lv), P = 2^(score + lv - max + 3) fits
+// fp16, and the row's sum takes each page's part times 2^-lv.
+//
+// Warps: 4 * MT softmax warps (one thread per query row), one issuing Q K^T, one
+// issuing P V, four producers (one per page of a tile, as in the 16-bit kernel).
+// A ring slot is one tile (keys in 8 bits, values in fp16) or one part of an M
+// tile's queries, copied to TMEM.  Every mbarrier wait is bounded; on a timeout
+// MT_ERR_TIMEOUT is recorded, the other roles stop, the copies and MMAs in
+// flight are waited for and TMEM is freed.
+#include <cudaTypedefs.h>
+
+#include <atomic>
+
+#include "serve.cuh"
+#include "tc_ptx.cuh"
+
+namespace mt {
+
+namespace {
+
+constexpr int kSmemLimit = 232448;  // opt-in dynamic shared memory per CTA
+constexpr int kMaxDevices = 64;
+constexpr int kProducers = kTileKeys / 16;
+
+// What a producer needs to finish a tile whose value codes it has asked for.
+struct Pending {
+  uint32_t pos;  // ring position
+  int krow;      // row of the key page in its map
+  int from_new;  // which map: the cache, or the new tokens' blocks
+  int rows;      // rows of the page that hold keys of the sequence (0: none)
+  float ks, vs;
+};
+
+template <int D, int MT, int NP>
+struct Cfg {
+  static constexpr int NH = D / 64;                   // 64-column halves of an fp16 value row
+  static constexpr int kPTile = 128 * kTileKeys * 2;  // P of one M tile: 128 rows x 128 B
+  static constexpr int kPBytes = MT * kPTile;
+  static constexpr int kKTile = kTileKeys * D;        // key codes, swizzled rows of D bytes
+  static constexpr int kHalf = kTileKeys * 128;       // 64 values of 64 columns
+  static constexpr int kVTile = NH * kHalf;
+  static constexpr int kStage = kKTile + kVTile;      // >= 128 * D: one part of an M tile's queries
+  static constexpr int kDepth = 4;                    // value pages in flight per producer
+  static constexpr int kVPage = 16 * D;
+  static constexpr int kVBytes = kProducers * kDepth * kVPage;
+  static constexpr int kMetaBytes = 4096;  // barriers, pending tiles, scales, piece list
+  static constexpr int kFit = (kSmemLimit - 1024 - kMetaBytes - kPBytes - kVBytes) / kStage;
+  static constexpr int STAGES = kFit > 8 ? 8 : kFit;
+  static constexpr int kSmem = 1024 + kPBytes + STAGES * kStage + kVBytes + kMetaBytes;
+  static constexpr int kSoftmaxWarps = 4 * MT;
+  static constexpr int kQkWarp = kSoftmaxWarps;
+  static constexpr int kPvWarp = kSoftmaxWarps + 1;
+  static constexpr int kProducer0 = kSoftmaxWarps + 2;
+  static constexpr int kThreads = (kSoftmaxWarps + 2 + kProducers) * 32;
+  static constexpr int kQSlots = MT * NP;  // ring slots of a piece's queries
+  // TMEM: O (D fp32 columns per M tile), S (64), Q (D / 4 columns of four codes per part)
+  static constexpr int kTmemUsed = MT * (D + kTileKeys + NP * (D / 4));
+  static constexpr int kTmemCols = kTmemUsed <= 128 ? 128 : kTmemUsed <= 256 ? 256 : 512;
+  static_assert(kTmemUsed <= 512, "TMEM budget");
+  static_assert(STAGES >= 3 && kStage >= 128 * D, "shared memory budget");
+  __device__ static constexpr uint32_t o_col(int m) { return (uint32_t)(m * D); }
+  __device__ static constexpr uint32_t s_col(int m) { return (uint32_t)(MT * D + m * kTileKeys); }
+  __device__ static constexpr uint32_t q_col(int m, int part) {
+    return (uint32_t)(MT * (D + kTileKeys) + (m * NP + part) * (D / 4));
+  }
+};
+
+__device__ __forceinline__ float fast_exp2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+__device__ __forceinline__ uint32_t pack_h2(float a, float b) {
+  const __half2 h = __floats2half2_rn(a, b);
+  uint32_t r;
+  memcpy(&r, &h, 4);
+  return r;
+}
+
+// D[tmem] (+)= A[tmem] * B[smem]: E4M3 both, fp32 accumulator; A is M x 32, one
+// row per lane, four consecutive codes per 32-bit column.
+template <bool ACC>
+__device__ __forceinline__ void mma_f8_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc) {
+  if (ACC) {
+    asm volatile(
+        "{\n.reg .pred p;\nsetp.eq.u32 p, 1, 1;\n"
+        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d_tmem),
+        "r"(a_tmem), "l"(b_desc), "r"(idesc)
+        : "memory");
+  } else {
+    asm volatile(
+        "{\n.reg .pred p;\nsetp.eq.u32 p, 1, 0;\n"
+        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d_tmem),
+        "r"(a_tmem), "l"(b_desc), "r"(idesc)
+        : "memory");
+  }
+}
+
+// Instruction descriptor of kind::f8f6f4 with E4M3 operands (format 0), both
+// K-major, fp32 accumulator (1 at bits 4-5), N >> 3 at bit 17, M >> 4 at bit 24.
+__host__ __device__ constexpr uint32_t idesc_f8(int M, int N) {
+  return (1u << 4) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
+}
+
+// K-major matrix of rows of D bytes, swizzled over 128 (D = 128) or 64 bytes:
+// eight-row groups D * 8 bytes apart; swizzle mode at bits 61-63 (2: 128, 4: 64).
+template <int D>
+__device__ __forceinline__ uint64_t desc_rows8(uint32_t saddr) {
+  uint64_t d = 0;
+  d |= (uint64_t)((saddr >> 4) & 0x3FFFu);
+  d |= (uint64_t)1 << 16;
+  d |= (uint64_t)((8 * D) >> 4) << 32;
+  d |= (uint64_t)1 << 46;
+  d |= (uint64_t)(D == 128 ? 2 : 4) << 61;
+  return d;
+}
+
+// Waits that ignore the abort flag (copies and MMAs in flight at the end).
+__device__ __forceinline__ void drain_wait(uint64_t* bar, uint32_t parity, int* status) {
+  const uint64_t t0 = tc::global_timer_ns();
+  while (!tc::mbar_try_wait(bar, parity)) {
+    if (tc::global_timer_ns() - t0 > tc::kDrainLimitNs) {
+      set_status(status, kStTimeout);
+      return;
+    }
+  }
+}
+
+// Visibility of the 64 columns of tile j: cached slot s < L, or a new token of
+// the row's ancestor mask.  Columns are pages: npre cached ones, then the new
+// tokens' blocks, so new token t sits at column npre * 16 + t.
+__device__ __forceinline__ unsigned long long visible(int L, int npre, int k0, unsigned long long anc) {
+  const int pre = L - k0, base = npre * 16 - k0;
+  unsigned long long see = pre >= 64 ? ~0ull : pre <= 0 ? 0ull : (1ull << pre) - 1ull;
+  if (base < 64) see |= base >= 0 ? anc << base : base > -64 ? anc >> -base : 0ull;
+  return see;
+}
+
+template <typename T, int D, int MT, int NP>
+__global__ void __launch_bounds__(Cfg<D, MT, NP>::kThreads, 1)
+    attn_block8_tc_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v,
+                          const __grid_constant__ CUtensorMap map_kn, const __grid_constant__ CUtensorMap map_vn,
+                          const __grid_constant__ CUtensorMap map_q, const Block8Params p) {
+  using C = Cfg<D, MT, NP>;
+  constexpr int S = C::STAGES;
+  constexpr uint32_t kIdescQK = idesc_f8(128, kTileKeys);
+  constexpr uint32_t kIdescPV = tc::idesc_f16(false, true, 128, D);
+  const AttnParams& a = p.a;
+
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* sP = smem;                       // [m] P tiles, 128-byte swizzled, K-major
+  uint8_t* sKV = sP + C::kPBytes;           // [stage] keys, then values
+  uint8_t* sV8 = sKV + S * C::kStage;       // [producer][kDepth] value codes
+  uint64_t* bars = reinterpret_cast<uint64_t*>(sV8 + C::kVBytes);
+  uint64_t* full = bars;                    // [S] a tile's keys and values, or query rows, are there
+  uint64_t* empty = full + S;               // [S] consumed
+  uint64_t* s_full = empty + S;             // [MT] S computed
+  uint64_t* p_full = s_full + MT;           // [MT] P written (and O rescaled)
+  uint64_t* pv_done = p_full + MT;          // [MT] O += P V done
+  uint64_t* s_free = pv_done + MT;          // [MT] S read out
+  uint64_t* o_free = s_free + MT;           // O of the previous piece read out
+  uint64_t* fin = o_free + 1;               // [2] every MMA of each issuer done
+  uint64_t* never = fin + 2;                // nothing arrives here (timeout test hook)
+  uint64_t* v_full = never + 1;             // [producer][kDepth] value codes landed
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(v_full + kProducers * C::kDepth);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  int* s_npieces = const_cast<int*>(abort_flag + 1);
+  static_assert((2 * 8 + 4 * 2 + 4 + kProducers * C::kDepth) * 8 + 12 <= 1024, "barrier area");
+  Pending* s_pend = reinterpret_cast<Pending*>(reinterpret_cast<uint8_t*>(bars) + 1024);  // [producer][kDepth]
+  float* s_scale = reinterpret_cast<float*>(reinterpret_cast<uint8_t*>(bars) + 1536);     // [S][3][4]: ks, lv, 2^-lv
+  static_assert(kProducers * C::kDepth * sizeof(Pending) <= 512 && 8 * 12 * 4 <= 512, "metadata");
+  PieceRec* s_pieces = reinterpret_cast<PieceRec*>(reinterpret_cast<uint8_t*>(bars) + 2048);
+  static_assert(2048 + kMaxPieceRecs * sizeof(PieceRec) <= C::kMetaBytes, "piece list");
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int nnew = (a.T + 15) / 16;
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < S; ++s) {
+      tc::mbar_init(&full[s], 2 * kProducers);  // a producer's keys, and its values
+      tc::mbar_init(&empty[s], 1);
+    }
+    for (int m = 0; m < MT; ++m) {
+      tc::mbar_init(&s_full[m], 1);
+      tc::mbar_init(&p_full[m], 4);
+      tc::mbar_init(&pv_done[m], 1);
+      tc::mbar_init(&s_free[m], 4);
+    }
+    tc::mbar_init(o_free, C::kSoftmaxWarps);
+    tc::mbar_init(&fin[0], 1);
+    tc::mbar_init(&fin[1], 1);
+    tc::mbar_init(never, 1);
+    for (int k = 0; k < kProducers * C::kDepth; ++k) tc::mbar_init(&v_full[k], 1);
+    *abort_flag = 0;
+    tc::fence_barrier_init();
+  }
+  if (warp == C::kQkWarp) {
+    tc::tmem_alloc(tmem_slot, C::kTmemCols);
+    tc::tmem_relinquish();
+  }
+  if (warp == C::kProducer0 && lane == 0) {
+    tc::prefetch_tmap(&map_k);
+    tc::prefetch_tmap(&map_v);
+    tc::prefetch_tmap(&map_kn);
+    tc::prefetch_tmap(&map_vn);
+    tc::prefetch_tmap(&map_q);
+  }
+  pdl_wait();  // everything above overlaps the preparation's end
+  if (warp == C::kPvWarp) {
+    // this CTA's pieces: the first four records with the count, the rest (rare) after
+    const int* src = p.pieces + piece_rec_offset(a.sched.G) + (size_t)blockIdx.x * kMaxPieceRecs * 8;
+    const int first = src[lane];
+    const int n = p.pieces[blockIdx.x];
+    int* dst = reinterpret_cast<int*>(s_pieces);
+    dst[lane] = first;
+    if (lane == 0) *s_npieces = n;
+    for (int e = 32 + lane; e < (n > 0 ? n : 0) * 8; e += 32) dst[e] = src[e];
+  }
+  tc::tc_fence_before();
+  __syncthreads();
+  tc::tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  const uint32_t sKV_u = tc::smem_u32(sKV), sP_u = tc::smem_u32(sP);
+  bool ok = true;
+  auto wait_all = [&](uint64_t* bar, uint32_t parity) {
+    const bool r = tc::mbar_wait(bar, parity, abort_flag, a.status, a.wait_limit_ns);
+    ok = __all_sync(0xffffffffu, r) && ok;
+  };
+  PieceSrc pi;
+  pi.init(s_pieces, *s_npieces, a.sched, blockIdx.x, a.seq_lens);
+  Piece pc;
+  int L = 0;
+
+  if (warp >= C::kProducer0) {
+    // ----------------------------------------------------------- producers
+    const int pid = warp - C::kProducer0;
+    const uint64_t policy = tc::policy_evict_first();
+    const uint64_t q_policy = tc::policy_evict_last();
+    const int oob_row = a.num_pages * a.Hkv * 16;  // past the cache: TMA fills zeros
+    uint32_t pos = 0;                              // ring position
+    uint32_t issued = 0, done = 0;                 // tiles whose values were asked for, and finished
+    uint32_t landing = 0;                          // positions below this had keys or queries asked for
+    // Finish the oldest tile: its stage, its keys (TMA), then its values
+    // converted: 16-byte chunks of codes, consecutive lanes on consecutive
+    // chunks, become two 8-column chunks of the 128-byte-swizzled fp16 rows.
+    auto finish_oldest = [&]() {
+      const uint32_t f = done % C::kDepth;
+      const Pending pd = s_pend[pid * C::kDepth + f];
+      const uint32_t st = pd.pos % S;
+      if (pd.pos >= (uint32_t)S) {
+        wait_all(&empty[st], ((pd.pos / S) - 1) & 1);
+        if (!ok) return;
+      }
+      uint8_t* stage = sKV + st * C::kStage;
+      if (lane == 0) {
+        tc::mbar_arrive_expect_tx(&full[st], 16 * D);
+        tc::tma_load_2d(stage + pid * 16 * D, pd.from_new ? &map_kn : &map_k, 0, pd.krow, &full[st], policy);
+        float* sc = s_scale + st * 12 + pid;
+        sc[0] = pd.ks;
+        sc[4] = log2f(pd.vs);
+        sc[8] = 1.f / pd.vs;
+      }
+      landing = pd.pos + 1;
+      wait_all(&v_full[pid * C::kDepth + f], (done / C::kDepth) & 1);
+      if (!ok) return;
+      const uint8_t* codes = sV8 + (pid * C::kDepth + f) * C::kVPage;
+      constexpr int CPR = D / 16;
+#pragma unroll
+      for (int i = 0; i < 16 * CPR / 32; ++i) {
+        const int q = i * 32 + lane;
+        const int r = q / CPR, col = (q % CPR) * 16;
+        uint4 c = *reinterpret_cast<const uint4*>(codes + q * 16);
+        // rows that hold no key of the sequence may hold anything (NaN codes
+        // too): their weights are 0 and so are their values
+        if (r >= pd.rows) c = make_uint4(0, 0, 0, 0);
+        const int row = pid * 16 + r, c0 = (col % 64) / 8;
+        uint8_t* dst = stage + C::kKTile + (col / 64) * C::kHalf + row * 128;
+        const uint32_t w[4] = {c.x, c.y, c.z, c.w};
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+          *reinterpret_cast<uint4*>(dst + (((c0 + h) ^ (row & 7)) << 4)) =
+              make_uint4(e4m3x2_to_h2(w[2 * h] & 0xffffu), e4m3x2_to_h2(w[2 * h] >> 16),
+                         e4m3x2_to_h2(w[2 * h + 1] & 0xffffu), e4m3x2_to_h2(w[2 * h + 1] >> 16));
+      }
+      tc::fence_proxy_async_smem();  // read by the tensor core; the codes' slot is refilled by TMA
+      __syncwarp();
+      if (lane == 0) tc::mbar_arrive(&full[st]);
+      ++done;
+    };
+    // finish every tile at ring position <= q - S before a wait on position q's
+    // stage, which can depend on them
+    auto finish_until = [&](uint32_t q) {
+      while (ok && done < issued && q >= (uint32_t)S && s_pend[pid * C::kDepth + done % C::kDepth].pos <= q - S)
+        finish_oldest();
+    };
+    while (ok && pi.next(pc, L)) {
+      // the piece's queries: part `part` of M tile m per ring slot, its 128-row
+      // box loaded by producer (slot % 4); every producer arrives twice
+      for (int s = 0; s < C::kQSlots && ok; ++s, ++pos) {
+        const uint32_t st = pos % S;
+        finish_until(pos);
+        if (ok && pos >= (uint32_t)S) wait_all(&empty[st], ((pos / S) - 1) & 1);
+        if (!ok) break;
+        if (lane == 0) {
+          if (s % kProducers == pid) {
+            const int m = s / NP, part = s % NP;
+            tc::mbar_arrive_expect_tx(&full[st], 128 * D);
+            tc::tma_load_3d(sKV + st * C::kStage, &map_q, 0, pc.kvh * a.g,
+                            (part * a.B + pc.b) * a.T + (pc.rg * a.rows_per_group + m * 128) / a.g, &full[st], q_policy);
+          } else {
+            tc::mbar_arrive(&full[st]);
+          }
+          tc::mbar_arrive(&full[st]);
+        }
+        landing = pos + 1;
+        __syncwarp();
+      }
+      if (!ok) break;
+      // page ids and scales of 32 pages of the table at a time, a lane each; ids
+      // are fetched two windows ahead of use, scales one
+      const int npre = (L + 15) / 16;
+      const int* bt = a.block_tables + (size_t)pc.b * a.max_blocks;
+      const size_t nb0 = ((size_t)pc.b * a.Hkv + pc.kvh) * nnew;  // the new tokens' blocks
+      auto fetch_id = [&](int q) { return q < npre ? __ldg(bt + q) : -1; };
+      auto fetch_scale = [&](const float* sc, int id) {
+        return id >= 0 && id < a.num_pages ? __ldg(sc + (size_t)id * a.Hkv + pc.kvh) : 1.f;
+      };
+      int base = pc.tile_begin * 4;
+      int id0 = fetch_id(base + lane), id1 = fetch_id(base + 32 + lane), id2 = fetch_id(base + 64 + lane);
+      float ks0 = fetch_scale(p.k_scales, id0), vs0 = fetch_scale(p.v_scales, id0);
+      float ks1 = fetch_scale(p.k_scales, id1), vs1 = fetch_scale(p.v_scales, id1);
+      for (int j = pc.tile_begin; j < pc.tile_end; ++j, ++pos) {
+        const int pg = j * 4 + pid;
+        if (j * 4 - base >= 32) {  // the same tile for every lane: windows are whole tiles
+          base += 32;
+          id0 = id1;
+          ks0 = ks1;
+          vs0 = vs1;
+          id1 = id2;
+          ks1 = fetch_scale(p.k_scales, id1);
+          vs1 = fetch_scale(p.v_scales, id1);
+          id2 = fetch_id(base + 64 + lane);
+        }
+        const int id = __shfl_sync(0xffffffffu, id0, pg - base);
+        float ks = __shfl_sync(0xffffffffu, ks0, pg - base), vs = __shfl_sync(0xffffffffu, vs0, pg - base);
+        if (issued - done == (uint32_t)C::kDepth) finish_oldest();
+        if (!ok) break;
+        int row = oob_row, rows = 0, from_new = 0;
+        if (pg < npre) {
+          if (id >= 0 && id < a.num_pages) {
+            row = (id * a.Hkv + pc.kvh) * 16;
+            rows = min(16, L - pg * 16);
+          } else if (lane == 0) {
+            set_status(a.status, kStPages);
+          }
+        } else if (pg - npre < nnew) {
+          from_new = 1;
+          row = (int)((nb0 + pg - npre) * 16);
+          rows = 16;
+          ks = __ldg(p.k_block_scales + nb0 + pg - npre);
+          vs = __ldg(p.v_block_scales + nb0 + pg - npre);
+        }
+        if (lane == 0) {
+          const uint32_t f = issued % C::kDepth;
+          uint64_t* bar = &v_full[pid * C::kDepth + f];
+          // scales are positive; a smaller one (or one that is no number) would
+          // leave the exponent's range
+          s_pend[pid * C::kDepth + f] = Pending{pos, row, from_new, rows, ks, fmaxf(vs, 5.421010862427522e-20f)};
+          tc::mbar_arrive_expect_tx(bar, C::kVPage);
+          tc::tma_load_2d(sV8 + (pid * C::kDepth + f) * C::kVPage, from_new ? &map_vn : &map_v, 0, row, bar, policy);
+        }
+        __syncwarp();
+        ++issued;
+      }
+    }
+    while (ok && done < issued) finish_oldest();
+    // no TMA load may still be writing shared memory when the CTA exits: value
+    // codes never converted (after an abort), keys and queries of the last S slots
+    if (lane == 0) {
+      for (uint32_t u = done; u < issued; ++u)
+        drain_wait(&v_full[pid * C::kDepth + u % C::kDepth], (u / C::kDepth) & 1, a.status);
+      for (uint32_t t = landing > (uint32_t)S ? landing - S : 0; t < landing; ++t)
+        drain_wait(&full[t % S], (t / S) & 1, a.status);
+    }
+    __syncwarp();
+  } else if (warp == C::kQkWarp) {
+    // ---------------------------------------------------------- QK issuer
+    uint32_t it = 0, pos = 0;  // tiles so far; ring position
+    if (a.test_stall) wait_all(never, 0);  // test hook: a wait that can only time out
+    while (ok && pi.next(pc, L)) {
+      for (int s = 0; s < C::kQSlots && ok; ++s) {
+        const uint32_t st = (pos + s) % S;
+        wait_all(&full[st], ((pos + s) / S) & 1);
+        if (!ok) break;
+        tc::tc_fence_after();
+        const uint64_t qd = desc_rows8<D>(sKV_u + st * C::kStage);
+        const uint32_t col = tmem + C::q_col(s / NP, s % NP);
+#pragma unroll
+        for (int kk = 0; kk < D / 32; ++kk)  // 32 codes: 2 descriptor units, 8 columns
+          if (tc::elect_one()) tc::tmem_cp_128x256b(col + kk * 8, qd + (uint64_t)(kk * 2));
+        if (tc::elect_one()) tc::mma_commit(&empty[st]);
+        __syncwarp();
+      }
+      if (!ok) break;
+      pos += C::kQSlots;
+      for (int j = pc.tile_begin; j < pc.tile_end; ++j, ++it, ++pos) {
+        const uint32_t st = pos % S;
+        wait_all(&full[st], (pos / S) & 1);
+        if (!ok) break;
+        const uint64_t kd = desc_rows8<D>(sKV_u + st * C::kStage);
+        for (int m = 0; m < MT; ++m) {
+          if (it >= 1) {
+            wait_all(&s_free[m], (it - 1) & 1);
+            if (!ok) break;
+          }
+          tc::tc_fence_after();
+#pragma unroll
+          for (int part = 0; part < NP; ++part)
+#pragma unroll
+            for (int kk = 0; kk < D / 32; ++kk) {
+              const uint32_t q = tmem + C::q_col(m, part) + kk * 8;
+              if (part == 0 && kk == 0) {
+                if (tc::elect_one()) mma_f8_ts<false>(tmem + C::s_col(m), q, kd, kIdescQK);
+              } else {
+                if (tc::elect_one()) mma_f8_ts<true>(tmem + C::s_col(m), q, kd + (uint64_t)(kk * 2), kIdescQK);
+              }
+            }
+          if (tc::elect_one()) tc::mma_commit(&s_full[m]);
+          __syncwarp();
+        }
+        if (!ok) break;
+      }
+    }
+    if (tc::elect_one()) tc::mma_commit(&fin[0]);
+    __syncwarp();
+    if (lane == 0) drain_wait(&fin[0], 0, a.status);
+    __syncwarp();
+  } else if (warp == C::kPvWarp) {
+    // ---------------------------------------------------------- PV issuer
+    uint32_t it = 0, npieces = 0, pos = 0;
+    while (ok && pi.next(pc, L)) {
+      pos += C::kQSlots;
+      for (int j = pc.tile_begin; j < pc.tile_end; ++j, ++it, ++pos) {
+        const uint32_t st = pos % S;
+        const bool first = j == pc.tile_begin;
+        if (first && npieces > 0) {
+          wait_all(o_free, (npieces - 1) & 1);
+          if (!ok) break;
+        }
+        const uint32_t v_u = sKV_u + st * C::kStage + C::kKTile;
+        const uint64_t vd = tc::smem_desc(v_u, C::kHalf, 1024);
+        for (int m = 0; m < MT; ++m) {
+          wait_all(&p_full[m], it & 1);
+          if (!ok) break;
+          tc::tc_fence_after();
+          const uint32_t d_t = tmem + C::o_col(m);
+          const uint64_t pd = tc::smem_desc(sP_u + m * C::kPTile, 16, 1024);
+          if (first) {
+            if (tc::elect_one()) tc::mma_f16_ss<false>(d_t, pd, vd, kIdescPV);
+          } else {
+            if (tc::elect_one()) tc::mma_f16_ss<true>(d_t, pd, vd, kIdescPV);
+          }
+#pragma unroll
+          for (int kk = 1; kk < kTileKeys / 16; ++kk)  // next 16 keys: P +32 B, V +2048 B
+            if (tc::elect_one()) tc::mma_f16_ss<true>(d_t, pd + (uint64_t)(kk * 2), vd + (uint64_t)(kk * 128), kIdescPV);
+          if (tc::elect_one()) tc::mma_commit(&pv_done[m]);
+          __syncwarp();
+        }
+        if (!ok) break;
+        if (tc::elect_one()) tc::mma_commit(&empty[st]);
+        __syncwarp();
+      }
+      ++npieces;
+    }
+    if (tc::elect_one()) tc::mma_commit(&fin[1]);
+    __syncwarp();
+    if (lane == 0) drain_wait(&fin[1], 0, a.status);
+    __syncwarp();
+  } else {
+    // ------------------------------------------------------------- softmax
+    const int m = warp >> 2;              // M tile of this warpgroup
+    const int quad = warp & 3;            // TMEM lane quadrant
+    const int r = quad * 32 + lane;       // row within the M tile
+    const uint32_t lane_addr = (uint32_t)(quad * 32) << 16;
+    uint32_t it = 0, pos = 0;
+    while (ok && pi.next(pc, L)) {
+      pos += C::kQSlots;
+      const int row = pc.rg * a.rows_per_group + m * 128 + r;
+      const bool row_ok = row < a.rows;
+      const int node = row_ok ? row / a.g : 0, h = pc.kvh * a.g + (row_ok ? row % a.g : 0);
+      const unsigned long long anc = p.anc[(size_t)pc.b * a.T + node];
+      const float qs = p.q_scale[((size_t)pc.b * a.T + node) * a.Hq + h];
+      const int npre = (L + 15) / 16;
+      float m_run = -INFINITY, l_run = 0.f;
+      for (int j = pc.tile_begin; j < pc.tile_end; ++j, ++it, ++pos) {
+        wait_all(&s_full[m], it & 1);
+        if (!ok) break;
+        tc::tc_fence_after();
+        uint32_t sr[64];
+        tc::tmem_ld_x64(tmem + lane_addr + C::s_col(m), sr);
+        const uint32_t st = pos % S;
+        wait_all(&full[st], (pos / S) & 1);  // complete; orders the scales' reads
+        if (!ok) break;
+        const float4 ks = *reinterpret_cast<const float4*>(s_scale + st * 12);
+        const float4 lv = *reinterpret_cast<const float4*>(s_scale + st * 12 + 4);
+        const float4 iv = *reinterpret_cast<const float4*>(s_scale + st * 12 + 8);
+        const float c4[4] = {ks.x * qs, ks.y * qs, ks.z * qs, ks.w * qs};
+        const float l4[4] = {lv.x, lv.y, lv.z, lv.w}, i4[4] = {iv.x, iv.y, iv.z, iv.w};
+        tc::tmem_ld_wait();
+        // the scores are in registers: S may take the next tile's scores
+        tc::tc_fence_before();
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(&s_free[m]);
+        const int k0 = j * kTileKeys;
+        if (k0 + kTileKeys > L) {
+          const unsigned long long see = visible(L, npre, k0, anc);
+#pragma unroll
+          for (int hw = 0; hw < 2; ++hw) {
+            const uint32_t bits = (uint32_t)(see >> (32 * hw));
+            if (bits == 0xffffffffu) continue;
+#pragma unroll
+            for (int c = 0; c < 32; ++c)
+              if (!((bits >> c) & 1u)) sr[32 * hw + c] = 0xff800000u;  // -inf
+          }
+        }
+        // maximum of score + lv: per page of the raw products, then scaled
+        float mx = -INFINITY;
+#pragma unroll
+        for (int g = 0; g < 4; ++g) {
+          float x0 = __uint_as_float(sr[16 * g]), x1 = __uint_as_float(sr[16 * g + 1]);
+#pragma unroll
+          for (int c = 2; c < 16; c += 2) {
+            x0 = fmaxf(x0, __uint_as_float(sr[16 * g + c]));
+            x1 = fmaxf(x1, __uint_as_float(sr[16 * g + c + 1]));
+          }
+          mx = fmaxf(mx, fmaf(fmaxf(x0, x1), c4[g], l4[g]));
+        }
+        // O is rescaled only when the maximum grows by more than 8: P <= 2^11
+        const bool grow = mx > m_run + 8.f;
+        const bool need_o = grow && m_run != -INFINITY;
+        const float m_new = grow ? mx : m_run;
+        const float sc = need_o ? fast_exp2(m_run - m_new) : 1.f;
+        const float off = m_new == -INFINITY ? 0.f : 3.f - m_new;
+        uint32_t pk[32];
+        float sum = 0.f;
+#pragma unroll
+        for (int g = 0; g < 4; ++g) {
+          const float o = off + l4[g];
+          float s0 = 0.f, s1 = 0.f;
+#pragma unroll
+          for (int c = 0; c < 8; ++c) {
+            const float p0 = fast_exp2(fmaf(__uint_as_float(sr[16 * g + 2 * c]), c4[g], o));
+            const float p1 = fast_exp2(fmaf(__uint_as_float(sr[16 * g + 2 * c + 1]), c4[g], o));
+            s0 += p0;
+            s1 += p1;
+            pk[8 * g + c] = pack_h2(p0, p1);
+          }
+          sum = fmaf(s0 + s1, i4[g], sum);
+        }
+        // P once the P.V of the tile before (which read it) is done: row r is
+        // 128 B (64 keys), 16-byte chunk c at c ^ (r % 8)
+        if (it >= 1) {
+          wait_all(&pv_done[m], (it - 1) & 1);
+          if (!ok) break;
+        }
+        uint8_t* prow = sP + m * C::kPTile + (r >> 3) * 1024 + (r & 7) * 128;
+#pragma unroll
+        for (int c = 0; c < 8; ++c)
+          *reinterpret_cast<uint4*>(prow + ((c ^ (r & 7)) << 4)) =
+              make_uint4(pk[4 * c], pk[4 * c + 1], pk[4 * c + 2], pk[4 * c + 3]);
+        tc::fence_proxy_async_smem();
+        if (__any_sync(0xffffffffu, need_o)) {
+          tc::tc_fence_after();
+#pragma unroll 1
+          for (int hh = 0; hh < D / 64; ++hh) {
+            uint32_t o[64];
+            tc::tmem_ld_x64(tmem + lane_addr + C::o_col(m) + 64 * hh, o);
+            tc::tmem_ld_wait();
+#pragma unroll
+            for (int c = 0; c < 64; ++c) o[c] = __float_as_uint(__uint_as_float(o[c]) * sc);
+            tc::tmem_st_x64(tmem + lane_addr + C::o_col(m) + 64 * hh, o);
+          }
+        }
+        tc::tmem_st_wait();
+        l_run = fmaf(l_run, sc, sum);
+        m_run = m_new;
+        tc::tc_fence_before();
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(&p_full[m]);
+      }
+      if (!ok) break;
+      // epilogue, once the piece's last P.V is done: O / l to the output, or the
+      // piece's own O / l with its maximum and sum to a partial slot
+      wait_all(&pv_done[m], (it - 1) & 1);
+      if (!ok) break;
+      tc::tc_fence_after();
+      const int seg_row = m * 128 + r;
+      const float inv = l_run > 0.f ? 1.f / l_run : 0.f;
+#pragma unroll 1
+      for (int hh = 0; hh < D / 64; ++hh) {
+        uint32_t o[64];
+        tc::tmem_ld_x64(tmem + lane_addr + C::o_col(m) + 64 * hh, o);
+        tc::tmem_ld_wait();
+        if (row_ok) {
+          uint4* dst;
+          size_t step;
+          if (pc.slot < 0) {
+            dst = reinterpret_cast<uint4*>(static_cast<T*>(a.out) + (((size_t)pc.b * a.T + node) * a.Hq + h) * D + 64 * hh);
+            step = 1;
+          } else {
+            dst = static_cast<uint4*>(a.part_o) + ((size_t)pc.slot * (D / 8) + 8 * hh) * a.part_rows + seg_row;
+            step = a.part_rows;
+          }
+#pragma unroll
+          for (int c = 0; c < 8; ++c) {
+            T v[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[e] = Act<T>::from_f(__uint_as_float(o[8 * c + e]) * inv);
+            uint4 w;
+            memcpy(&w, v, 16);
+            dst[c * step] = w;
+          }
+        }
+      }
+      if (row_ok && pc.slot >= 0) a.part_ml[(size_t)pc.slot * a.part_rows + seg_row] = make_float2(m_run, l_run);
+      tc::tc_fence_before();
+      __syncwarp();
+      if (lane == 0) tc::mbar_arrive(o_free);
+    }
+  }
+
+  tc::tc_fence_before();
+  __syncthreads();
+  tc::tc_fence_after();
+  if (warp == C::kQkWarp) tc::tmem_dealloc(tmem, C::kTmemCols);
+}
+
+PFN_cuTensorMapEncodeTiled_v12000 get_encode() {
+  static const PFN_cuTensorMapEncodeTiled_v12000 fn = [] {
+    void* f = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &q) != cudaSuccess ||
+        q != cudaDriverEntryPointSuccess)
+      f = nullptr;
+    return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(f);
+  }();
+  return fn;
+}
+
+// Rows of D codes in boxes of 16 rows (one page or block of one KV head), zeros
+// past the end; keys swizzled as the tensor cores read them, values plain.
+bool map_pages(CUtensorMap* map, const void* base, long long rows, int D, bool keys) {
+  auto enc = get_encode();
+  if (!enc) return false;
+  const cuuint64_t dims[2] = {(cuuint64_t)D, (cuuint64_t)rows};
+  const cuuint64_t strides[1] = {(cuuint64_t)D};
+  const cuuint32_t box[2] = {(cuuint32_t)D, 16};
+  const cuuint32_t es[2] = {1, 1};
+  return enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, strides, box, es,
+             CU_TENSOR_MAP_INTERLEAVE_NONE,
+             !keys ? CU_TENSOR_MAP_SWIZZLE_NONE : D == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// Query parts [parts * B * T][Hq][D]: boxes of one 128-row M tile (128 / g nodes
+// x g heads).
+bool map_queries(CUtensorMap* map, const void* base, long long nodes, int Hq, int g, int D) {
+  auto enc = get_encode();
+  if (!enc) return false;
+  const cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)Hq, (cuuint64_t)nodes};
+  const cuuint64_t strides[2] = {(cuuint64_t)D, (cuuint64_t)Hq * D};
+  const cuuint32_t box[3] = {(cuuint32_t)D, (cuuint32_t)g, (cuuint32_t)(128 / g)};
+  const cuuint32_t es[3] = {1, 1, 1};
+  return enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(base), dims, strides, box, es,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, D == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <typename T, int D, int MT, int NP>
+cudaError_t launch_t(const Block8Params& p, cudaStream_t stream) {
+  using C = Cfg<D, MT, NP>;
+  const AttnParams& a = p.a;
+  static std::atomic<bool> opted[kMaxDevices];
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 0 || dev >= kMaxDevices || !opted[dev].load(std::memory_order_acquire)) {
+    e = cudaFuncSetAttribute(attn_block8_tc_kernel<T, D, MT, NP>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             C::kSmem);
+    if (e != cudaSuccess) return e;
+    if (dev >= 0 && dev < kMaxDevices) opted[dev].store(true, std::memory_order_release);
+  }
+  alignas(64) CUtensorMap k, v, kn, vn, q;
+  const long long rows = (long long)a.num_pages * a.Hkv * 16, nrows = (long long)a.B * a.Hkv * ((a.T + 15) / 16) * 16;
+  if (!map_pages(&k, a.k_cache, rows, D, true) || !map_pages(&v, a.v_cache, rows, D, false) ||
+      !map_pages(&kn, p.k_blocks, nrows, D, true) || !map_pages(&vn, p.v_blocks, nrows, D, false) ||
+      !map_queries(&q, p.q8, (long long)NP * a.B * a.T, a.Hq, a.g, D))
+    return cudaErrorInvalidValue;
+  return launch_pdl(attn_block8_tc_kernel<T, D, MT, NP>, dim3(a.sched.G), dim3(C::kThreads), (size_t)C::kSmem, stream,
+                    k, v, kn, vn, q, p);
+}
+
+template <int D>
+cudaError_t launch_d(const Block8Params& p, int dtype, cudaStream_t stream) {
+  if (dtype == 1) return launch_t<__half, D, 1, 3>(p, stream);
+  if (p.a.rows_per_group == 128) return launch_t<__nv_bfloat16, D, 1, 2>(p, stream);
+  return launch_t<__nv_bfloat16, D, 2, 2>(p, stream);
+}
+
+}  // namespace
+
+cudaError_t launch_attn_block8_tc(const Block8Params& p, int dtype, cudaStream_t stream) {
+  return p.a.D == 64 ? launch_d<64>(p, dtype, stream) : launch_d<128>(p, dtype, stream);
+}
+
+}  // namespace mt

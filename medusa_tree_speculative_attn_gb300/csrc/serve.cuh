@@ -154,15 +154,70 @@ struct Block8Params {
   const void* v_new;
   const int* parents;     // [B][T], or null: a chain
   int* tile_pfx;          // [B + 1] out, for the combine
+  // the tensor-core path, written by its preparation:
+  int parts;              // E4M3 parts of a query row: 2 (bf16) or 3 (fp16)
+  uint8_t* q8;            // [parts][B][T][Hq][D]
+  float* q_scale;         // [B][T][Hq] scale of the row's parts times the softmax scale times log2(e)
+  uint8_t* k_blocks;      // [B][Hkv][ceil(T / 16)][16][D] the new tokens' codes
+  uint8_t* v_blocks;
+  float* k_block_scales;  // [B][Hkv][ceil(T / 16)]
+  float* v_block_scales;
+  unsigned long long* anc;  // [B][T]
+  int* pieces;            // piece table (common.cuh)
 };
 
-// Row group, CTAs per SM and cost of starting a piece (in 64-slot tiles) of the
-// register-fragment kernel.
+// Tiles of each sequence (cached pages, then the new tokens' blocks, four to a
+// tile; none for seq_lens < 0) and their exclusive prefix in pfx[0 .. B], by a
+// block of W warps; returns the total.  A length past the block table has no
+// tiles and is recorded by the block that says so.
+template <int W>
+__device__ __forceinline__ int block8_prefix(const AttnParams& a, int* pfx, int* s_warp, bool report) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int nnew = (a.T + 15) / 16;
+  int carry = 0;
+  for (int b0 = 0; b0 < a.B; b0 += W * 32) {
+    const int b = b0 + tid;
+    int n = 0;
+    if (b < a.B) {
+      const int L = a.seq_lens[b];
+      if ((long long)L > (long long)a.max_blocks * 16) {
+        if (report) set_status(a.status, kStPages);
+      } else if (L >= 0) {
+        n = ((L + 15) / 16 + nnew + 3) / 4;
+      }
+    }
+    int incl = n;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int v = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += v;
+    }
+    if (lane == 31) s_warp[warp] = incl;
+    __syncthreads();
+    int off = carry;
+    for (int w = 0; w < W; ++w) {
+      if (w < warp) off += s_warp[w];
+      carry += s_warp[w];
+    }
+    if (b < a.B) pfx[b] = off + incl - n;
+    __syncthreads();
+  }
+  if (tid == 0) pfx[a.B] = carry;
+  __syncthreads();
+  return carry;
+}
+
+// How a call runs: the tensor-core kernel or the register-fragment kernel, its
+// row group, persistent CTAs per SM and cost of starting a piece (in 64-slot
+// tiles).
 struct Block8Plan {
-  int rows_per_group, ctas_per_sm, seg_cost;
+  bool tc;
+  int rows_per_group, ctas_per_sm, seg_cost, parts;
 };
-Block8Plan block8_plan(int rows);
+Block8Plan block8_plan(int rows, int g, int dtype);
 cudaError_t launch_attn_block8(const Block8Params& p, int dtype, cudaStream_t stream);
+cudaError_t launch_block8_prep(const Block8Params& p, int dtype, cudaStream_t stream);
+cudaError_t launch_attn_block8_tc(const Block8Params& p, int dtype, cudaStream_t stream);
 
 // ---------------------------------------------------------------------------
 // Sampling.

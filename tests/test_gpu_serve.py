@@ -660,3 +660,21 @@ def test_prompt_step_and_draw_together():
     f = lambda a: np.float64(np.float32(a))  # noqa: E731
     assert got.tolist() == [ref.sample64(logits.view(b * t, v)[int(end[i])].double().numpy(), f(u[i]), f(0.8), 40, f(0.95), 0.0) for i in range(b)]
     assert mt.read_status(ws) == 0
+
+
+def test_block8_attention_wait_bound():
+    """A pipeline wait that only its bound ends: the status says so, and the next call is right."""
+    rng = np.random.default_rng(95)
+    c = _attn_case(rng, 2, 32, 8, 2, 128, [100, 40], "bf16")
+    out, ws, args, kw = _attn_run(c)
+    _attn_check(c, out)
+    try:
+        mt.debug_set_wait(20_000_000, stall=True)
+        mt.tree_attn_paged_block8(*args, **kw)
+        assert mt.read_status(ws) == -6
+    finally:
+        mt.debug_set_wait()
+    out.fill_(5.0)
+    mt.tree_attn_paged_block8(*args, **kw)
+    assert mt.read_status(ws) == 0
+    _attn_check(c, out)
