@@ -20,10 +20,11 @@
 // good to 6e-8 about one row in a thousand of a flat distribution would draw a
 // neighbour of the token that its definition gives.
 // The cut is found by a histogram of counts (and masses) over 512 bins of
-// (m - x) / temperature, 1/16 of a power of two each, and then by histograms
-// over the keys of the one bin that the cut falls in, 9 bits at a time, until a
-// single value is left.  The CTAs meet in distributed shared memory: each reads
-// all histograms and searches by itself, so a pass costs one cluster barrier.
+// (m - x) / temperature, 1/16 of a power of two each, and then among the tokens
+// of the one bin that the cut falls in: ranked directly if they are at most 512,
+// else by histograms over their keys, 9 bits at a time, until a single value is
+// left.  The CTAs meet in distributed shared memory: each reads all histograms
+// and lists and searches by itself, so a pass costs one cluster barrier.
 #include <cooperative_groups.h>
 
 #include <atomic>
@@ -63,29 +64,40 @@ struct Scale {
 };
 
 // Weight of x: 2^40 exp((x - m) / t), rounded to a whole number.
-// 2^e with e = n/32 + r, |r| <= 1/64:  table[n mod 32] * (1 + r * p(r)) * 2^(n div 32).
+// 2^e with e = n/32 + r, |r| <= 1/64:  table[n mod 32] * (1 + r * p(r)) * 2^(n div 32),
+// n read off the low bits of e * 32 + 1.5 * 2^23, the correction r * p(r) as a
+// 32-bit integer of 2^-37 (the only conversion instruction).
 __device__ __forceinline__ unsigned long long weight(float x, const Scale& s, const unsigned long long* table) {
   const float d = x - s.m;
-  if (x == s.m) return 1ull << kWBits;
   const float p = d * s.hi;
-  if (!(p > -41.f)) return 0ull;  // below half a unit; -inf too
+  // below half a unit (-inf too); d is no number only where x = m = +inf
+  if (!(p > -41.f)) return x == s.m ? 1ull << kWBits : 0ull;
   const float bb = d - x;
   const float err = (x - (d - bb)) + (-s.m - bb);  // x - m = d + err exactly
   const float e = fmaf(d, s.hi, -p) + fmaf(d, s.lo, err * s.hi);
-  const float nf = rintf(p * 32.f);
-  const float r = fmaf(nf, -0.03125f, p) + e;
-  float q = fmaf(r, 9.618129e-3f, 5.5504109e-2f);   // ln2^4/24, ln2^3/6
-  q = fmaf(r, q, 2.4022651e-1f);                    // ln2^2/2
-  q = fmaf(r, q, 6.9314718e-1f) * r;                // ln2
-  const int n = (int)nf;
+  const float z = fmaf(p, 32.f, 12582912.f);
+  const int n = __float_as_int(z) - 0x4B400000;
+  const float r = fmaf(z - 12582912.f, -0.03125f, p) + e;
+  constexpr float k37 = 137438953472.f;
+  float q = fmaf(r, 9.618129e-3f * k37, 5.5504109e-2f * k37);  // ln2^4/24, ln2^3/6
+  q = fmaf(r, q, 2.4022651e-1f * k37);                         // ln2^2/2
+  q = fmaf(r, q, 6.9314718e-1f * k37) * r;                     // ln2
   const unsigned long long t = table[n & 31];
-  const long long w = (long long)t + __float2ll_rn((float)t * q);
+  const unsigned long long w = t + (((long long)(int)(t >> 10) * __float2int_rn(q)) >> 27);
   const int sh = -(n >> 5);
-  return sh > 0 ? ((unsigned long long)w + (1ull << (sh - 1))) >> sh : (unsigned long long)w;
+  return (w + ((1ull << sh) >> 1)) >> sh;
 }
 
 struct Hist {
   unsigned cnt[kBins], lo[kBins], hi[kBins];  // count; low and high 16 bits of the 32-bit weights, summed
+};
+
+constexpr int kList = kThreads;  // tokens of one bin that are ranked directly, a thread each
+
+struct List {
+  unsigned n;
+  uint32_t key[kList];
+  int idx[kList];
 };
 
 struct Found {  // where a search ended
@@ -102,6 +114,13 @@ struct Smem {
   unsigned wc[kWarps];                   // scans
   unsigned long long wm[kWarps];
   Found found;
+  List list[2];                          // this CTA's tokens of a bin, read by the cluster
+  uint32_t mkey[kList];                  // the cluster's
+  int midx[kList];
+  unsigned long long mw[kList];
+  uint32_t cut_key;
+  int cut_idx;
+  unsigned long long cut_mass;
   unsigned long long chunk_mass[kMaxChunks];
   unsigned chunk_ties[kMaxChunks];
   unsigned long long tot_mass;           // this CTA's kept mass (2^40 units), read by the cluster
@@ -143,11 +162,12 @@ struct Slice {
       if ((unsigned)(e0 + e) < (unsigned)V) f(x == x ? x : -INFINITY, e);
     }
   }
-  // f(x) over this thread's elements
+  // f(x, index) over this thread's elements
   template <class F>
   __device__ __forceinline__ void each(F f) const {
 #pragma unroll 1
-    for (int v = beg + (int)threadIdx.x; v < end; v += kThreads) vec(get(v), v, [&](float x, int) { f(x); });
+    for (int v = beg + (int)threadIdx.x; v < end; v += kThreads)
+      vec(get(v), v, [&](float x, int e) { f(x, v * EPV - mis + e); });
   }
   // the first pass: every element as f(x, index), the row into shared memory
   template <class F>
@@ -234,6 +254,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(SampleParams a) {
   const int n = blockIdx.x / C;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   if (tid < 32) sm.table[tid] = (unsigned long long)(exp2(tid * (1.0 / 32)) * (double)(1ull << kWBits) + 0.5);
+  if (tid < 2) sm.list[tid].n = 0;
   for (int b = 0; b < 3; ++b) sm.hist[b].cnt[tid] = sm.hist[b].lo[tid] = sm.hist[b].hi[tid] = 0;
   pdl_wait();
   const int src = a.row_index ? a.row_index[n] : n;
@@ -305,27 +326,97 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(SampleParams a) {
   const bool use_k = want_k > 0 && want_k < a.V, use_p = top_p < 1.f;
   bool cut = false;
   uint32_t cut_key = 0;       // ord >> KS
-  unsigned stay = 0;          // tokens of that value that are kept
+  int cut_idx = -1;           // the last token of that value that is kept,
+  unsigned stay = 0;          // or how many are (where the index is not known)
   if (use_k || use_p) {
     const float width = sc.hi * 16.f;
     auto bin_of = [&](float x) { return x == sc.m ? 0 : min(kBins - 1, __float2int_rz((sc.m - x) * width)); };
+    auto weight_of = [&](float x) {  // 2^32 for the maximum
+      return (weight(x, sc, sm.table) + (1u << (kWBits - 33))) >> (kWBits - 32);
+    };
     auto add = [&](Hist& h, int b, float x) {
-      atomicAdd(&h.cnt[b], 1u);
+      if (use_k) atomicAdd(&h.cnt[b], 1u);
       if (use_p) {
-        // 32 bits below the maximum's 1 (the maximum itself: 2^32 as 2^16 high halves)
-        const unsigned long long w = (weight(x, sc, sm.table) + (1u << (kWBits - 33))) >> (kWBits - 32);
+        const unsigned long long w = weight_of(x);
         const unsigned l = (unsigned)w & 0xffffu, g = (unsigned)(w >> 16);
         if (l) atomicAdd(&h.lo[b], l);
         if (g) atomicAdd(&h.hi[b], g);
       }
     };
-    s.each([&](float x) { add(sm.hist[0], bin_of(x), x); });
+    s.each([&](float x, int) { add(sm.hist[0], bin_of(x), x); });
     cl.sync();
     int buf = 1;  // the next pass's histogram, zero at this point and read by nobody
-    unsigned long long before_mass = 0;
-    // from the bin that a count or mass falls in to its value
+    unsigned long long cut_mass = 0;  // mass up to the cut
+    int which = 0, listed = -1;       // the next list; the bin whose tokens are merged
+    unsigned nlist = 0;
+    auto value_of = [&](uint32_t key) {  // the value of a key
+      const uint32_t o = key << KS;
+      return of_ord((o & 0x80000000u) ? o : o | ((1u << KS) - 1u));
+    };
+    // from the bin that a count or mass falls in to the last token kept
     auto refine = [&](Found f, unsigned want_cnt, unsigned long long want_mass) {
       const int bin = f.bin;
+      // the bin's tokens, ranked directly if they are few (they mostly are)
+      if (bin != listed) {
+        List& mine = sm.list[which];
+        s.each([&](float x, int i) {
+          if (bin_of(x) != bin) return;
+          const unsigned at = atomicAdd(&mine.n, 1u);
+          if (at < kList) {
+            mine.key[at] = ord_of(x) >> KS;
+            mine.idx[at] = i;
+          }
+        });
+        cl.sync();
+        nlist = 0;
+        bool fits = true;
+        int from = -1, at = 0;
+        for (unsigned r = 0; r < C; ++r) {
+          const unsigned c = cl.map_shared_rank(&sm, r)->list[which].n;
+          if (from < 0 && (unsigned)tid < nlist + c) {
+            from = (int)r;
+            at = tid - (int)nlist;
+          }
+          fits = fits && c <= kList;
+          nlist += c;
+        }
+        fits = fits && nlist <= kList;
+        if (fits && tid < (int)nlist) {
+          const List* l = &cl.map_shared_rank(&sm, from)->list[which];
+          sm.mkey[tid] = l->key[at];
+          sm.midx[tid] = l->idx[at];
+          sm.mw[tid] = use_p ? weight_of(value_of(l->key[at])) : 0ull;
+        }
+        __syncthreads();
+        which ^= 1;
+        listed = fits ? bin : -1;
+      }
+      if (listed == bin) {
+        if (tid < (int)nlist) {
+          const uint32_t k = sm.mkey[tid];
+          const int i = sm.midx[tid];
+          const unsigned long long w = sm.mw[tid];
+          unsigned c = f.cnt;
+          unsigned long long m = f.mass;
+          for (unsigned j = 0; j < nlist; ++j)
+            if (sm.mkey[j] > k || (sm.mkey[j] == k && sm.midx[j] < i)) {
+              ++c;
+              m += sm.mw[j];
+            }
+          if (want_cnt ? c + 1 == want_cnt : m < want_mass && want_mass <= m + w) {
+            sm.cut_key = k;
+            sm.cut_idx = i;
+            sm.cut_mass = m + w;
+          }
+        }
+        __syncthreads();
+        cut = true;
+        cut_key = sm.cut_key;
+        cut_idx = sm.cut_idx;
+        cut_mass = sm.cut_mass;
+        __syncthreads();
+        return;
+      }
       // the bin's keys, with room for rounding on both sides
       const float xh = sc.m - (float)bin / width, xl = sc.m - (float)(bin + 1) / width;
       uint32_t hi = ord_of(xh + 1e-5f * (fabsf(sc.m) + fabsf(xh)) + 1e-30f) >> KS;
@@ -338,7 +429,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(SampleParams a) {
         const int bits = 32 - __clz(hi - lo);
         const int shift = max(0, bits - 9);
         Hist& h = sm.hist[buf];
-        s.each([&](float x) {
+        s.each([&](float x, int) {
           const uint32_t k = ord_of(x) >> KS;
           if (k >= lo && k <= hi && bin_of(x) == bin) add(h, (int)((hi - k) >> shift), x);
         });
@@ -355,20 +446,16 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(SampleParams a) {
       }
       cut = true;
       cut_key = hi;
-      stay = want_cnt ? want_cnt - f.cnt : 0;
-      before_mass = f.mass;
-    };
-    auto weight32 = [&](uint32_t key) {
-      // any value of the key: the widened value itself
-      const uint32_t o = key << KS;
-      const float x = of_ord((o & 0x80000000u) ? o : o | ((1u << KS) - 1u));
-      return (weight(x, sc, sm.table) + (1u << (kWBits - 33))) >> (kWBits - 32);
+      cut_idx = -1;
+      const unsigned long long w = use_p ? weight_of(value_of(hi)) : 0ull;
+      stay = want_cnt ? want_cnt - f.cnt : (unsigned)((want_mass - f.mass + w - 1) / w);
+      cut_mass = f.mass + stay * w;
     };
     unsigned long long whole;
     if (use_k) {
       const Found f = search(sm, 0, cl, 0u, 0ull, (unsigned)want_k, 0ull);
       refine(f, (unsigned)want_k, 0ull);
-      whole = before_mass + (use_p ? (unsigned long long)stay * weight32(cut_key) : 0ull);
+      whole = cut_mass;
     } else {
       whole = 0;
       // the mass of every bin: the search below wants a mass, so sum first
@@ -392,8 +479,6 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(SampleParams a) {
       if (want > whole) want = whole;
       const Found f = search(sm, 0, cl, 0u, 0ull, 0u, want);
       refine(f, 0u, want);
-      const unsigned long long w = weight32(cut_key);
-      stay = w ? (unsigned)((want - before_mass + w - 1) / w) : 0xffffffffu;
     }
   }
   // smallest value that min-p keeps: x >= m + t ln(min_p), the next float up
@@ -403,11 +488,12 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(SampleParams a) {
   }
 
   // ---- kept mass of each warp-wide vector, in vocab order ----
-  auto kind = [&](float x) {  // 2: kept, 1: equal to the cut, 0: not kept
+  auto kind = [&](float x, int i) {  // 2: kept, 1: equal to the cut, 0: not kept
     if (x < x_min) return 0;
     if (!cut) return 2;
     const uint32_t k = ord_of(x) >> KS;
-    return k > cut_key ? 2 : k == cut_key ? 1 : 0;
+    if (k != cut_key) return k > cut_key ? 2 : 0;
+    return cut_idx < 0 ? 1 : i <= cut_idx ? 2 : 0;
   };
   const int nch = (s.end - s.beg + 31) / 32;  // chunks of 32 vectors, 32 * EPV elements each
   {
@@ -416,8 +502,8 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(SampleParams a) {
       unsigned long long mass = 0;
       unsigned ties = 0;
       if (v < s.end)
-        s.vec(s.get(v), v, [&](float x, int) {
-          const int k = kind(x);
+        s.vec(s.get(v), v, [&](float x, int e) {
+          const int k = kind(x, v * EPV - s.mis + e);
           if (k == 2) mass += weight(x, sc, sm.table);
           ties += k == 1;
         });
@@ -524,7 +610,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(SampleParams a) {
       }
       if (v < s.end) {
         s.vec(s.get(v), v, [&](float x, int e) {
-          const int k = kind(x);
+          const int k = kind(x, v * EPV - s.mis + e);
           if (k == 2) w[e] = weight(x, sc, sm.table);
           tie[e] = k == 1;
           nt += k == 1;

@@ -46,6 +46,47 @@ struct Row8 {
   }
 };
 
+// Largest magnitude of rows held as packed act-dtype words: 16-bit types stay
+// packed (half the instructions, and no widened copy for the compiler to keep in
+// registers).  A NaN is passed over.
+template <typename T>
+struct AbsMax {
+  typedef __half2 V2;
+  V2 m;
+  __device__ __forceinline__ AbsMax() { m = __float2half2_rn(0.f); }
+  __device__ __forceinline__ void add(const Row8<T>& r) {
+    V2 v[4];
+    memcpy(v, r.w, sizeof(v));
+#pragma unroll
+    for (int e = 0; e < 4; ++e) m = __hmax2(m, __habs2(v[e]));
+  }
+  __device__ __forceinline__ float get() const { return fmaxf(__low2float(m), __high2float(m)); }
+};
+template <>
+struct AbsMax<__nv_bfloat16> {
+  typedef __nv_bfloat162 V2;
+  V2 m;
+  __device__ __forceinline__ AbsMax() { m = __float2bfloat162_rn(0.f); }
+  __device__ __forceinline__ void add(const Row8<__nv_bfloat16>& r) {
+    V2 v[4];
+    memcpy(v, r.w, sizeof(v));
+#pragma unroll
+    for (int e = 0; e < 4; ++e) m = __hmax2(m, __habs2(v[e]));
+  }
+  __device__ __forceinline__ float get() const { return fmaxf(__low2float(m), __high2float(m)); }
+};
+template <>
+struct AbsMax<float> {
+  float m = 0.f;
+  __device__ __forceinline__ void add(const Row8<float>& r) {
+    float v[8];
+    memcpy(v, r.w, sizeof(v));
+#pragma unroll
+    for (int e = 0; e < 8; ++e) m = fmaxf(m, fabsf(v[e]));
+  }
+  __device__ __forceinline__ float get() const { return m; }
+};
+
 // ---------------------------------------------------------------------------
 // E4M3 codes and block scales.
 // ---------------------------------------------------------------------------
