@@ -464,7 +464,7 @@ int mt_tree_attn_paged_block8(const mt_attn_desc* desc, const void* q, const voi
  * -inf; a row without anything above -inf gives -1; entries of +inf share the
  * whole mass.  Sums are exact integers of weights good to 1e-9, so the token is
  * that of the definition unless u lies that close to a border.  Weights below
- * 2^-41 of the largest count as 0.
+ * 2^-44 of the largest count as 0.
  * row_index[i] < 0: no row, tokens[i] is left as it was; >= num_logit_rows: -1.
  * row_stride in elements; rows need no alignment.  vocab <= 500000
  * (MT_ERR_UNSUPPORTED above).  No workspace and no device status. */

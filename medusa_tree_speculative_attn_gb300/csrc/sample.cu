@@ -13,9 +13,9 @@
 // value for min-p.
 //
 // A cluster of CTAs holds a row in registers: the logits are read from memory
-// once.  Weights are integers (2^40 for the maximum), so every sum is exact and
-// the same in any order; each weight is good to about 5e-10 of itself (the
-// exponent as a sum of two floats, a 32-entry table, a short polynomial).  That
+// once.  Weights are integers (2^44 for the maximum), so every sum is exact and
+// the same in any order; each weight is good to about 1e-9 of itself (the
+// exponent as a sum of two floats, a 128-entry table, a short polynomial).  That
 // matters because a draw compares u against up to 10^5 borders: with weights
 // good to 6e-8 about one row in a thousand of a flat distribution would draw a
 // neighbour of the token that its definition gives.
@@ -28,6 +28,8 @@
 #include <cooperative_groups.h>
 
 #include <atomic>
+#include <cmath>
+#include <type_traits>
 
 #include "serve.cuh"
 
@@ -41,8 +43,7 @@ constexpr int kThreads = 512;
 constexpr int kWarps = kThreads / 32;
 constexpr int kBins = kThreads;     // a thread per bin in the search
 constexpr int kMaxCluster = 8;
-constexpr int kMaxChunks = 512;     // warp-wide vectors per CTA: kSampleMaxVocab / kMaxCluster / (32 lanes * 4 fp32)
-constexpr int kWBits = 40;          // weight of the maximum
+constexpr int kWBits = 44;          // weight of the maximum: 2^44 * kSampleMaxVocab < 2^63
 
 // Monotone 32-bit key of a float (-0 as +0).
 __device__ __forceinline__ uint32_t ord_of(float v) {
@@ -58,34 +59,63 @@ template <typename T> struct KeyShift { static constexpr int v = 0; };
 template <> struct KeyShift<__half> { static constexpr int v = 13; };
 template <> struct KeyShift<__nv_bfloat16> { static constexpr int v = 16; };
 
+// The value of a shifted key.
+template <int KS>
+__device__ __forceinline__ float value_of_key(uint32_t key) {
+  const uint32_t o = key << KS;
+  return of_ord((o & 0x80000000u) ? o : o | ((1u << KS) - 1u));
+}
+
 struct Scale {
   float m;         // the row's maximum
   float hi, lo;    // log2(e) / temperature as a sum
 };
 
-// Weight of x: 2^40 exp((x - m) / t), rounded to a whole number.
-// 2^e with e = n/32 + r, |r| <= 1/64:  table[n mod 32] * (1 + r * p(r)) * 2^(n div 32),
-// n read off the low bits of e * 32 + 1.5 * 2^23, the correction r * p(r) as a
-// 32-bit integer of 2^-37 (the only conversion instruction).
-__device__ __forceinline__ unsigned long long weight(float x, const Scale& s, const unsigned long long* table) {
+constexpr int kTable = 128;
+
+struct Table {  // 2^(30 + j/128)
+  int v[kTable];
+};
+
+// floor(2^64 f) for f in [0, 1): exact but for bits below 2^-64.
+__device__ __forceinline__ unsigned long long fraction64(float f) {
+  const uint32_t b = __float_as_uint(f);
+  const int up = (int)(b >> 23) - 127 + 41;  // the 24-bit significand's place
+  const unsigned long long m = (b & 0x7fffffu) | (b >> 23 ? 0x800000u : 0u);
+  return up >= 0 ? m << up : up > -24 ? m >> -up : 0ull;
+}
+
+// Weight of x: 2^44 exp((x - m) / t), cut to a whole number.
+// 2^e with e = n/128 + r, |r| <= 1/256:  table[n mod 128] * (1 + q) * 2^(n div 128),
+// q = 2^r - 1.  n is read off the low bits of e * 128 + 1.5 * 2^23; the product
+// with q is a 32-bit high product of the table's 2^30 .. 2^31 and q * 2^32 (the
+// only conversion), and the power of two a 32-bit shift and a 64-bit product.
+// TWO: the rounding error of x - m by the form for any two floats; 16-bit values
+// need only the form for |x| <= |m|, because elsewhere their difference is exact.
+template <bool TWO>
+__device__ __forceinline__ unsigned long long weight(float x, const Scale& s, const int* table) {
   const float d = x - s.m;
   const float p = d * s.hi;
-  // below half a unit (-inf too); d is no number only where x = m = +inf
-  if (!(p > -41.f)) return x == s.m ? 1ull << kWBits : 0ull;
-  const float bb = d - x;
-  const float err = (x - (d - bb)) + (-s.m - bb);  // x - m = d + err exactly
+  // below one unit (-inf too); d is no number only where x = m = +inf
+  if (!(p > -45.f)) return x == s.m ? 1ull << kWBits : 0ull;
+  float err;
+  if (TWO) {
+    const float bb = d - x;
+    err = (x - (d - bb)) + (-s.m - bb);
+  } else {
+    err = x - (d + s.m);
+  }
   const float e = fmaf(d, s.hi, -p) + fmaf(d, s.lo, err * s.hi);
-  const float z = fmaf(p, 32.f, 12582912.f);
+  const float z = fmaf(p, 128.f, 12582912.f);
   const int n = __float_as_int(z) - 0x4B400000;
-  const float r = fmaf(z - 12582912.f, -0.03125f, p) + e;
-  constexpr float k37 = 137438953472.f;
-  float q = fmaf(r, 9.618129e-3f * k37, 5.5504109e-2f * k37);  // ln2^4/24, ln2^3/6
-  q = fmaf(r, q, 2.4022651e-1f * k37);                         // ln2^2/2
-  q = fmaf(r, q, 6.9314718e-1f * k37) * r;                     // ln2
-  const unsigned long long t = table[n & 31];
-  const unsigned long long w = t + (((long long)(int)(t >> 10) * __float2int_rn(q)) >> 27);
-  const int sh = -(n >> 5);
-  return (w + ((1ull << sh) >> 1)) >> sh;
+  const float r = fmaf(z - 12582912.f, -0.0078125f, p) + e;
+  constexpr float k32 = 4294967296.f;
+  float q = fmaf(r, 5.5504109e-2f * k32, 2.4022651e-1f * k32);  // ln2^3/6, ln2^2/2
+  q = fmaf(r, q, 6.9314718e-1f * k32) * r;                      // ln2
+  const int t = table[n & (kTable - 1)];
+  const unsigned w = (unsigned)(t + __mulhi(t, __float2int_rn(q)));
+  const int up = (kWBits - 30) + (n >> 7);  // n <= 0
+  return (unsigned long long)(w >> max(0, -up)) * (1u << max(0, up));
 }
 
 struct Hist {
@@ -108,11 +138,14 @@ struct Found {  // where a search ended
 
 struct Smem {
   Hist hist[3];  // the bins; two for the bin that is searched further
-  unsigned long long table[32];
+  int table[kTable];
   unsigned long long key[kWarps];        // block reduction of (value, index)
   unsigned long long best;               // this CTA's, read by the cluster
   unsigned wc[kWarps];                   // scans
   unsigned long long wm[kWarps];
+  unsigned long long whole;
+  double ln_min_p;
+  float x_min;
   Found found;
   List list[2];                          // this CTA's tokens of a bin, read by the cluster
   uint32_t mkey[kList];                  // the cluster's
@@ -121,25 +154,84 @@ struct Smem {
   uint32_t cut_key;
   int cut_idx;
   unsigned long long cut_mass;
-  unsigned long long chunk_mass[kMaxChunks];
-  unsigned chunk_ties[kMaxChunks];
-  unsigned long long tot_mass;           // this CTA's kept mass (2^40 units), read by the cluster
-  unsigned tot_ties;
+  unsigned long long run_mass[kWarps];   // each warp's kept mass and tokens equal to the cut
+  unsigned run_ties[kWarps];
 };
 
+// NaN as -inf, in a packed vector.
+template <typename T>
+__device__ __forceinline__ uint4 no_nan(uint4 r) {
+  if constexpr (sizeof(T) == 4) {
+    float v[4];
+    memcpy(v, &r, 16);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) v[e] = fmaxf(v[e], -INFINITY);
+    memcpy(&r, v, 16);
+  } else if constexpr (std::is_same<T, __half>::value) {
+    __half2 v[4];
+    memcpy(v, &r, 16);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) v[e] = __hmax2(v[e], __half2half2(__ushort_as_half(0xfc00)));
+    memcpy(&r, v, 16);
+  } else {
+    __nv_bfloat162 v[4];
+    memcpy(v, &r, 16);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) v[e] = __hmax2(v[e], __bfloat162bfloat162(__ushort_as_bfloat16(0xff80)));
+    memcpy(&r, v, 16);
+  }
+  return r;
+}
+
+// Largest element of a packed vector without NaN.
+template <typename T>
+__device__ __forceinline__ float vec_max(const uint4& r) {
+  if constexpr (sizeof(T) == 4) {
+    return fmaxf(fmaxf(__uint_as_float(r.x), __uint_as_float(r.y)), fmaxf(__uint_as_float(r.z), __uint_as_float(r.w)));
+  } else if constexpr (std::is_same<T, __half>::value) {
+    __half2 v[4];
+    memcpy(v, &r, 16);
+    const __half2 m = __hmax2(__hmax2(v[0], v[1]), __hmax2(v[2], v[3]));
+    return fmaxf(__low2float(m), __high2float(m));
+  } else {
+    __nv_bfloat162 v[4];
+    memcpy(v, &r, 16);
+    const __nv_bfloat162 m = __hmax2(__hmax2(v[0], v[1]), __hmax2(v[2], v[3]));
+    return fmaxf(__low2float(m), __high2float(m));
+  }
+}
+
 // A CTA's part of a row, staged in shared memory by the first pass over it (or,
-// where it does not fit, read again by every pass).
+// where it does not fit, read again by every pass).  Warp w holds a contiguous
+// run of 16-byte vectors, lane l every 32nd of them.  NaN counts as -inf, and so
+// do the places of a ragged first or last vector that lie outside the row (an
+// index outside [0, V) is never drawn: its weight is 0 and it is below every cut
+// but that of a row without enough tokens above -inf, where it adds nothing).
 template <typename T, bool STAGED>
 struct Slice {
   static constexpr int EPV = 16 / (int)sizeof(T);
   const T* row;
   uint4* stage;
-  int V, beg, end, mis;  // this CTA's vectors [beg, end); vector v holds elements v * EPV - mis and on
+  int V, beg, mis;  // this CTA's first vector; vector v holds elements v * EPV - mis and on
+  int wbeg, wend;   // this warp's vectors
 
+  __device__ __forceinline__ void init(const T* row_, int V_, uint4* stage_, unsigned rank, unsigned C) {
+    row = row_;
+    V = V_;
+    stage = stage_;
+    mis = (int)((reinterpret_cast<uintptr_t>(row) & 15) / sizeof(T));
+    const int nvec = (V + mis + EPV - 1) / EPV;
+    const int per = (nvec + (int)C - 1) / (int)C;
+    beg = min(nvec, (int)rank * per);
+    const int end = min(nvec, beg + per);
+    const int run = ((end - beg + kWarps - 1) / kWarps + 31) / 32 * 32;
+    wbeg = min(end, beg + (int)(threadIdx.x >> 5) * run);
+    wend = min(end, wbeg + run);
+  }
   __device__ __forceinline__ uint4 load(int v) const {
     const int e0 = v * EPV - mis;
-    if (e0 >= 0 && e0 + EPV <= V) return __ldg(reinterpret_cast<const uint4*>(row + e0));
-    T t[EPV];  // a row's ragged first or last vector
+    if (e0 >= 0 && e0 + EPV <= V) return no_nan<T>(__ldg(reinterpret_cast<const uint4*>(row + e0)));
+    T t[EPV];
 #pragma unroll
     for (int e = 0; e < EPV; ++e) {
       const int i = e0 + e;
@@ -147,47 +239,54 @@ struct Slice {
     }
     uint4 r;
     memcpy(&r, t, 16);
-    return r;
+    return no_nan<T>(r);
   }
   __device__ __forceinline__ uint4 get(int v) const { return STAGED ? stage[v - beg] : load(v); }
-  // f(x, e) over the elements of vector v that lie in the row; NaN counts as -inf
+  __device__ __forceinline__ int index(int v, int e) const { return v * EPV - mis + e; }
+  // f(x, e) over the elements of a vector
   template <class F>
-  __device__ __forceinline__ void vec(const uint4& r, int v, F f) const {
+  static __device__ __forceinline__ void vec(const uint4& r, F f) {
     T t[EPV];
     memcpy(t, &r, 16);
-    const int e0 = v * EPV - mis;
 #pragma unroll
-    for (int e = 0; e < EPV; ++e) {
-      const float x = Act<T>::to_f(t[e]);
-      if ((unsigned)(e0 + e) < (unsigned)V) f(x == x ? x : -INFINITY, e);
-    }
+    for (int e = 0; e < EPV; ++e) f(Act<T>::to_f(t[e]), e);
   }
-  // f(x, index) over this thread's elements
+  // f(x, v, e) over this thread's elements
   template <class F>
   __device__ __forceinline__ void each(F f) const {
 #pragma unroll 1
-    for (int v = beg + (int)threadIdx.x; v < end; v += kThreads)
-      vec(get(v), v, [&](float x, int e) { f(x, v * EPV - mis + e); });
+    for (int v = wbeg + (int)(threadIdx.x & 31); v < wend; v += 32) vec(get(v), [&](float x, int e) { f(x, v, e); });
   }
-  // the first pass: every element as f(x, index), the row into shared memory
-  template <class F>
-  __device__ __forceinline__ void first(F f) const {
+  // The first pass: the row into shared memory; the largest value and its
+  // lowest index (a thread's indices rise) as a key, 0 where there is nothing
+  // above -inf.
+  __device__ __forceinline__ unsigned long long first() const {
     constexpr int U = 4;  // vectors in flight
+    float best = -INFINITY;
+    int bi = 0;
 #pragma unroll 1
-    for (int v0 = beg + (int)threadIdx.x; v0 < end; v0 += U * kThreads) {
+    for (int v0 = wbeg + (int)(threadIdx.x & 31); v0 < wend; v0 += U * 32) {
       uint4 r[U];
 #pragma unroll
       for (int j = 0; j < U; ++j)
-        if (v0 + j * kThreads < end) r[j] = load(v0 + j * kThreads);
+        if (v0 + j * 32 < wend) r[j] = load(v0 + j * 32);
 #pragma unroll
       for (int j = 0; j < U; ++j) {
-        const int v = v0 + j * kThreads;
-        if (v < end) {
-          if (STAGED) stage[v - beg] = r[j];
-          vec(r[j], v, [&](float x, int e) { f(x, v * EPV - mis + e); });
+        const int v = v0 + j * 32;
+        if (v >= wend) continue;
+        if (STAGED) stage[v - beg] = r[j];
+        const float m = vec_max<T>(r[j]);
+        if (m > best) {  // then search the vector
+          T t[EPV];
+          memcpy(t, &r[j], 16);
+#pragma unroll
+          for (int e = EPV - 1; e >= 0; --e)
+            if (Act<T>::to_f(t[e]) == m) bi = index(v, e);
+          best = m;
         }
       }
     }
+    return best > -INFINITY ? ((unsigned long long)ord_of(best) << 32) | (0xffffffffu - (unsigned)bi) : 0ull;
   }
 };
 
@@ -195,65 +294,73 @@ __device__ __forceinline__ unsigned long long shfl_up64(unsigned long long v, in
   return __shfl_up_sync(0xffffffffu, v, o);
 }
 
-// Sums the cluster's histograms (a thread per bin) and finds the bin at which
-// the running count reaches `want_cnt` or, where that is 0, the running mass
-// reaches want_mass; base_* is what lies before the first bin.  Every CTA finds
-// the same.  *whole: the mass of all bins and what lies before them.
-__device__ Found search(Smem& sm, int buf, cg::cluster_group& cl, unsigned base_cnt, unsigned long long base_mass,
-                        unsigned want_cnt, unsigned long long want_mass) {
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  unsigned c = 0;
-  unsigned long long lo = 0;
-  for (unsigned r = 0; r < cl.num_blocks(); ++r) {
-    const Hist* p = &cl.map_shared_rank(&sm, r)->hist[buf];
-    c += p->cnt[tid];
-    lo += p->lo[tid];
-    lo += (unsigned long long)p->hi[tid] << 16;
-  }
-  unsigned ci = c;
-  unsigned long long mi = lo;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const unsigned cv = __shfl_up_sync(0xffffffffu, ci, o);
-    const unsigned long long mv = shfl_up64(mi, o);
-    if (lane >= o) {
-      ci += cv;
-      mi += mv;
+// A histogram summed over the cluster, a thread per bin: the bin's count and
+// mass, and what lies before it.
+struct Prefix {
+  unsigned cnt, before_cnt;
+  unsigned long long mass, before_mass;
+
+  __device__ void sum(Smem& sm, int buf, cg::cluster_group& cl, unsigned base_cnt, unsigned long long base_mass) {
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    cnt = 0;
+    mass = 0;
+#pragma unroll 4
+    for (unsigned r = 0; r < cl.num_blocks(); ++r) {
+      const Hist* p = &cl.map_shared_rank(&sm, r)->hist[buf];
+      cnt += p->cnt[tid];
+      mass += p->lo[tid] + ((unsigned long long)p->hi[tid] << 16);
     }
+    unsigned ci = cnt;
+    unsigned long long mi = mass;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const unsigned cv = __shfl_up_sync(0xffffffffu, ci, o);
+      const unsigned long long mv = shfl_up64(mi, o);
+      if (lane >= o) {
+        ci += cv;
+        mi += mv;
+      }
+    }
+    if (lane == 31) {
+      sm.wc[warp] = ci;
+      sm.wm[warp] = mi;
+    }
+    __syncthreads();
+    before_cnt = base_cnt + ci - cnt;
+    before_mass = base_mass + mi - mass;
+    for (int w = 0; w < warp; ++w) {
+      before_cnt += sm.wc[w];
+      before_mass += sm.wm[w];
+    }
+    if (tid == kThreads - 1) sm.whole = before_mass + mass;
+    __syncthreads();
   }
-  if (lane == 31) {
-    sm.wc[warp] = ci;
-    sm.wm[warp] = mi;
+  // The bin at which the running count reaches want_cnt or, where that is 0, the
+  // running mass want_mass.  Every CTA finds the same.
+  __device__ Found find(Smem& sm, unsigned want_cnt, unsigned long long want_mass) const {
+    const bool here = want_cnt ? before_cnt < want_cnt && want_cnt <= before_cnt + cnt
+                               : before_mass < want_mass && want_mass <= before_mass + mass;
+    if (here) sm.found = Found{(int)threadIdx.x, before_cnt, before_mass};
+    __syncthreads();
+    const Found f = sm.found;
+    __syncthreads();
+    return f;
   }
-  __syncthreads();
-  unsigned cb = base_cnt;
-  unsigned long long mb = base_mass;
-  for (int w = 0; w < warp; ++w) {
-    cb += sm.wc[w];
-    mb += sm.wm[w];
-  }
-  const unsigned c0 = cb + ci - c;
-  const unsigned long long m0 = mb + mi - lo;
-  const bool here = want_cnt ? c0 < want_cnt && want_cnt <= c0 + c : m0 < want_mass && want_mass <= m0 + lo;
-  if (here) sm.found = Found{tid, c0, m0};
-  __syncthreads();
-  const Found f = sm.found;
-  __syncthreads();
-  return f;
-}
+};
 
 template <typename T, bool STAGED>
-__global__ void __launch_bounds__(kThreads, 2) sample_kernel(SampleParams a) {
+__global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams a, const __grid_constant__ Table table) {
   using S = Slice<T, STAGED>;
   extern __shared__ uint4 stage[];
   constexpr int EPV = S::EPV;
   constexpr int KS = KeyShift<T>::v;
+  constexpr bool TWO = sizeof(T) == 4;
   __shared__ Smem sm;
   cg::cluster_group cl = cg::this_cluster();
   const unsigned C = cl.num_blocks(), rank = cl.block_rank();
   const int n = blockIdx.x / C;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  if (tid < 32) sm.table[tid] = (unsigned long long)(exp2(tid * (1.0 / 32)) * (double)(1ull << kWBits) + 0.5);
+  if (tid < kTable) sm.table[tid] = table.v[tid];
   if (tid < 2) sm.list[tid].n = 0;
   for (int b = 0; b < 3; ++b) sm.hist[b].cnt[tid] = sm.hist[b].lo[tid] = sm.hist[b].hi[tid] = 0;
   pdl_wait();
@@ -268,28 +375,15 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(SampleParams a) {
   float min_p = a.min_p ? a.min_p[n] : 0.f;
   const float u = a.uniforms[n];
   if (min_p > 1.f) want_k = 1;  // no weight reaches it: the first token alone
+  // the one thing that takes 64-bit floats (two results a clock and SM), by one thread
+  if (tid == 0) sm.ln_min_p = min_p > 0.f ? log((double)min_p) : 0.0;
 
   S s;
-  s.row = static_cast<const T*>(a.logits) + src * a.row_stride;
-  s.V = a.V;
-  s.mis = (int)((reinterpret_cast<uintptr_t>(s.row) & 15) / sizeof(T));
-  const int nvec = (a.V + s.mis + EPV - 1) / EPV;
-  const int per = (nvec + (int)C - 1) / (int)C;
-  s.beg = min(nvec, (int)rank * per);
-  s.end = min(nvec, s.beg + per);
-  s.stage = stage;
+  s.init(static_cast<const T*>(a.logits) + src * a.row_stride, a.V, stage, rank, C);
 
   // ---- maximum and its lowest index ----
   {
-    float best = -INFINITY;
-    int bi = 0x7fffffff;
-    s.first([&](float x, int i) {  // a thread's indices rise
-      if (x > best) {
-        best = x;
-        bi = i;
-      }
-    });
-    unsigned long long key = bi == 0x7fffffff ? 0ull : ((unsigned long long)ord_of(best) << 32) | (0xffffffffu - (unsigned)bi);
+    unsigned long long key = s.first();
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) {
       const unsigned long long k = __shfl_xor_sync(0xffffffffu, key, o);
@@ -316,11 +410,18 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(SampleParams a) {
   Scale sc;
   sc.m = of_ord((uint32_t)(best >> 32));
   {
-    double k = 1.4426950408889634074 / (double)temp;
-    k = k > 1e30 ? 1e30 : k;
-    sc.hi = (float)k;
-    sc.lo = (float)(k - (double)sc.hi);
+    // log2(e) / t as the sum of two floats
+    const float h = 1.44269502f, l = 1.92596303e-8f;  // log2(e)
+    sc.hi = h / temp;
+    sc.lo = (fmaf(-sc.hi, temp, h) + l) / temp;
+    if (!(sc.hi < 1e30f)) {
+      sc.hi = 1e30f;
+      sc.lo = 0.f;
+    }
   }
+  // smallest value that min-p keeps: x >= m + t ln(min_p), the next float up
+  if (tid == 0)
+    sm.x_min = min_p > 0.f ? fminf(__double2float_ru((double)sc.m + (double)temp * sm.ln_min_p), sc.m) : -INFINITY;
 
   // ---- the cut ----
   const bool use_k = want_k > 0 && want_k < a.V, use_p = top_p < 1.f;
@@ -332,7 +433,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(SampleParams a) {
     const float width = sc.hi * 16.f;
     auto bin_of = [&](float x) { return x == sc.m ? 0 : min(kBins - 1, __float2int_rz((sc.m - x) * width)); };
     auto weight_of = [&](float x) {  // 2^32 for the maximum
-      return (weight(x, sc, sm.table) + (1u << (kWBits - 33))) >> (kWBits - 32);
+      return (weight<TWO>(x, sc, sm.table) + (1u << (kWBits - 33))) >> (kWBits - 32);
     };
     auto add = [&](Hist& h, int b, float x) {
       if (use_k) atomicAdd(&h.cnt[b], 1u);
@@ -343,24 +444,23 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(SampleParams a) {
         if (g) atomicAdd(&h.hi[b], g);
       }
     };
-    s.each([&](float x, int) { add(sm.hist[0], bin_of(x), x); });
+    s.each([&](float x, int v, int e) {
+      if ((unsigned)s.index(v, e) < (unsigned)a.V) add(sm.hist[0], bin_of(x), x);
+    });
     cl.sync();
     int buf = 1;  // the next pass's histogram, zero at this point and read by nobody
     unsigned long long cut_mass = 0;  // mass up to the cut
     int which = 0, listed = -1;       // the next list; the bin whose tokens are merged
     unsigned nlist = 0;
-    auto value_of = [&](uint32_t key) {  // the value of a key
-      const uint32_t o = key << KS;
-      return of_ord((o & 0x80000000u) ? o : o | ((1u << KS) - 1u));
-    };
     // from the bin that a count or mass falls in to the last token kept
     auto refine = [&](Found f, unsigned want_cnt, unsigned long long want_mass) {
       const int bin = f.bin;
       // the bin's tokens, ranked directly if they are few (they mostly are)
       if (bin != listed) {
         List& mine = sm.list[which];
-        s.each([&](float x, int i) {
-          if (bin_of(x) != bin) return;
+        s.each([&](float x, int v, int e) {
+          const int i = s.index(v, e);
+          if (bin_of(x) != bin || (unsigned)i >= (unsigned)a.V) return;
           const unsigned at = atomicAdd(&mine.n, 1u);
           if (at < kList) {
             mine.key[at] = ord_of(x) >> KS;
@@ -385,7 +485,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(SampleParams a) {
           const List* l = &cl.map_shared_rank(&sm, from)->list[which];
           sm.mkey[tid] = l->key[at];
           sm.midx[tid] = l->idx[at];
-          sm.mw[tid] = use_p ? weight_of(value_of(l->key[at])) : 0ull;
+          sm.mw[tid] = use_p ? weight_of(value_of_key<KS>(l->key[at])) : 0ull;
         }
         __syncthreads();
         which ^= 1;
@@ -429,15 +529,17 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(SampleParams a) {
         const int bits = 32 - __clz(hi - lo);
         const int shift = max(0, bits - 9);
         Hist& h = sm.hist[buf];
-        s.each([&](float x, int) {
+        s.each([&](float x, int v, int e) {
           const uint32_t k = ord_of(x) >> KS;
-          if (k >= lo && k <= hi && bin_of(x) == bin) add(h, (int)((hi - k) >> shift), x);
+          if (k >= lo && k <= hi && bin_of(x) == bin && (unsigned)s.index(v, e) < (unsigned)a.V) add(h, (int)((hi - k) >> shift), x);
         });
         cl.sync();
         // past this barrier nobody reads the other buffer any more
         Hist& o = sm.hist[3 - buf];
         o.cnt[tid] = o.lo[tid] = o.hi[tid] = 0;
-        f = search(sm, buf, cl, f.cnt, f.mass, want_cnt, want_mass);  // ends in a block barrier
+        Prefix sub;
+        sub.sum(sm, buf, cl, f.cnt, f.mass);
+        f = sub.find(sm, want_cnt, want_mass);  // ends in a block barrier
         buf = 3 - buf;
         hi -= (uint32_t)f.bin << shift;
         if (shift == 0) break;
@@ -447,185 +549,129 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(SampleParams a) {
       cut = true;
       cut_key = hi;
       cut_idx = -1;
-      const unsigned long long w = use_p ? weight_of(value_of(hi)) : 0ull;
+      const unsigned long long w = use_p ? weight_of(value_of_key<KS>(hi)) : 0ull;
       stay = want_cnt ? want_cnt - f.cnt : (unsigned)((want_mass - f.mass + w - 1) / w);
       cut_mass = f.mass + stay * w;
     };
-    unsigned long long whole;
+    Prefix bins;
+    bins.sum(sm, 0, cl, 0u, 0ull);
+    unsigned long long whole = sm.whole;
     if (use_k) {
-      const Found f = search(sm, 0, cl, 0u, 0ull, (unsigned)want_k, 0ull);
-      refine(f, (unsigned)want_k, 0ull);
+      refine(bins.find(sm, (unsigned)want_k, 0ull), (unsigned)want_k, 0ull);
       whole = cut_mass;
-    } else {
-      whole = 0;
-      // the mass of every bin: the search below wants a mass, so sum first
-      unsigned long long mine = 0;
-      for (unsigned r = 0; r < C; ++r) {
-        const Hist* p = &cl.map_shared_rank(&sm, r)->hist[0];
-        mine += p->lo[tid] + ((unsigned long long)p->hi[tid] << 16);
-      }
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, o);
-      if (lane == 0) sm.wm[warp] = mine;
-      __syncthreads();
-      for (int w = 0; w < kWarps; ++w) whole += sm.wm[w];
-      __syncthreads();
     }
     if (use_p) {
       // kept: mass before < top_p * whole, a whole number's comparison with the
       // next whole number at or above the product
-      const double pz = ceil((double)top_p * (double)whole);
-      unsigned long long want = pz > 1.0 ? (unsigned long long)pz : 1ull;
+      unsigned long long want = 1;
+      if (top_p > 0.f) {
+        const unsigned long long f = fraction64(top_p);
+        want = max(__umul64hi(whole, f) + (whole * f != 0), 1ull);
+      }
       if (want > whole) want = whole;
-      const Found f = search(sm, 0, cl, 0u, 0ull, 0u, want);
-      refine(f, 0u, want);
+      refine(bins.find(sm, 0u, want), 0u, want);
     }
   }
-  // smallest value that min-p keeps: x >= m + t ln(min_p), the next float up
-  float x_min = -INFINITY;
-  if (min_p > 0.f) {
-    x_min = fminf(__double2float_ru((double)sc.m + (double)temp * log((double)min_p)), sc.m);
-  }
-
-  // ---- kept mass of each warp-wide vector, in vocab order ----
+  __syncthreads();
+  const float x_min = sm.x_min;
   auto kind = [&](float x, int i) {  // 2: kept, 1: equal to the cut, 0: not kept
     if (x < x_min) return 0;
     if (!cut) return 2;
     const uint32_t k = ord_of(x) >> KS;
     if (k != cut_key) return k > cut_key ? 2 : 0;
-    return cut_idx < 0 ? 1 : i <= cut_idx ? 2 : 0;
+    return cut_idx < 0 ? ((unsigned)i < (unsigned)a.V ? 1 : 0) : i <= cut_idx ? 2 : 0;
   };
-  const int nch = (s.end - s.beg + 31) / 32;  // chunks of 32 vectors, 32 * EPV elements each
+
+  // ---- kept mass of each warp's run, in vocab order ----
   {
-#pragma unroll 1
-    for (int v = s.beg + tid; v - lane < s.end; v += kThreads) {
-      unsigned long long mass = 0;
-      unsigned ties = 0;
-      if (v < s.end)
-        s.vec(s.get(v), v, [&](float x, int e) {
-          const int k = kind(x, v * EPV - s.mis + e);
-          if (k == 2) mass += weight(x, sc, sm.table);
-          ties += k == 1;
-        });
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) {
-        mass += __shfl_xor_sync(0xffffffffu, mass, o);
-        ties += __shfl_xor_sync(0xffffffffu, ties, o);
-      }
-      if (lane == 0) {
-        const int c = (v - s.beg) / 32;
-        sm.chunk_mass[c] = mass;
-        sm.chunk_ties[c] = ties;
-      }
-    }
-  }
-  __syncthreads();
-  if (warp == 0) {
     unsigned long long mass = 0;
     unsigned ties = 0;
-    for (int c = lane; c < nch; c += 32) {
-      mass += sm.chunk_mass[c];
-      ties += sm.chunk_ties[c];
-    }
+    s.each([&](float x, int v, int e) {
+      const int k = kind(x, s.index(v, e));
+      if (k == 2) mass += weight<TWO>(x, sc, sm.table);
+      ties += k == 1;
+    });
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) {
       mass += __shfl_xor_sync(0xffffffffu, mass, o);
       ties += __shfl_xor_sync(0xffffffffu, ties, o);
     }
     if (lane == 0) {
-      sm.tot_mass = mass;
-      sm.tot_ties = ties;
+      sm.run_mass[warp] = mass;
+      sm.run_ties[warp] = ties;
     }
   }
   cl.sync();
-  if (warp == 0) {
-    // every CTA's kept mass; the first `stay` ties in vocab order count
-    const uint32_t co = cut_key << KS;
-    const float cx = of_ord((co & 0x80000000u) ? co : co | ((1u << KS) - 1u));
-    const unsigned long long wt = cut ? weight(cx, sc, sm.table) : 0ull;
-    unsigned long long whole = 0, mine0 = 0, mine = 0;
-    unsigned ties = 0, ties0 = 0;
-    for (unsigned r = 0; r < C; ++r) {
-      const Smem* p = cl.map_shared_rank(&sm, r);
-      const unsigned t = p->tot_ties;
-      const unsigned take = ties >= stay ? 0u : min(t, stay - ties);
-      const unsigned long long w = p->tot_mass + take * wt;
-      if (r == rank) {
-        mine0 = whole;
-        mine = w;
-        ties0 = ties;
-      }
-      whole += w;
-      ties += t;
+  // ---- the run that the draw falls in: every warp looks at all of them (a lane
+  // per run, CTA by CTA), and the one that holds it goes on.  Of the tokens equal
+  // to the cut the first `stay` in vocab order count.
+  const unsigned long long wt = cut && cut_idx < 0 ? weight<TWO>(value_of_key<KS>(cut_key), sc, sm.table) : 0ull;
+  const int nruns = (int)C * kWarps;  // at most 128
+  unsigned long long mass[4];
+  unsigned long long whole = 0, mine0 = 0, mine = 0;
+  unsigned tb = 0, ties0 = 0;
+#pragma unroll
+  for (int g = 0; g < 4; ++g) {
+    const int run = g * 32 + lane;
+    mass[g] = 0;
+    unsigned t = 0;
+    if (run < nruns) {
+      const Smem* p = cl.map_shared_rank(&sm, (unsigned)(run / kWarps));
+      mass[g] = p->run_mass[run % kWarps];
+      t = p->run_ties[run % kWarps];
     }
-    // the kept mass must exceed u * whole: a whole number at or below it
-    const double tu = (double)whole * (double)u;
-    unsigned long long target = tu > 0.0 ? (unsigned long long)tu : 0ull;
-    if (target >= whole) target = whole - 1;
-    if (mine0 <= target && target < mine0 + mine) {
-      // the chunk: 32 at a time
-      unsigned long long run = mine0;
-      unsigned trun = ties0;
-      int c0 = 0;
-      unsigned long long m = 0;
-      unsigned t = 0;
-      for (;; c0 += 32) {
-        const int c = c0 + lane;
-        m = c < nch ? sm.chunk_mass[c] : 0ull;
-        t = c < nch ? sm.chunk_ties[c] : 0u;
-        unsigned ti = t;
+    unsigned ti = t;
 #pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-          const unsigned x = __shfl_up_sync(0xffffffffu, ti, o);
-          if (lane >= o) ti += x;
-        }
-        const unsigned tb = trun + ti - t;  // ties before this chunk
-        unsigned long long w = m + (tb >= stay ? 0u : min(t, stay - tb)) * wt;
-        unsigned long long wi = w;
+    for (int o = 1; o < 32; o <<= 1) {
+      const unsigned x = __shfl_up_sync(0xffffffffu, ti, o);
+      if (lane >= o) ti += x;
+    }
+    const unsigned before = tb + ti - t;
+    mass[g] += (before >= stay ? 0u : min(t, stay - before)) * wt;
+    unsigned long long mi = mass[g];
 #pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-          const unsigned long long x = shfl_up64(wi, o);
-          if (lane >= o) wi += x;
-        }
-        const unsigned hit = __ballot_sync(0xffffffffu, run + wi > target);
-        if (hit || c0 + 32 >= nch) {
-          const int l = hit ? __ffs(hit) - 1 : min(31, nch - 1 - c0);
-          run += __shfl_sync(0xffffffffu, wi - w, l);
-          trun = __shfl_sync(0xffffffffu, tb, l);
-          c0 += l;
-          break;
-        }
-        run += __shfl_sync(0xffffffffu, wi, 31);
-        trun += __shfl_sync(0xffffffffu, ti, 31);
-      }
-      // the element: this lane's vector of the chunk
-      const int v = s.beg + c0 * 32 + lane;
+    for (int o = 1; o < 32; o <<= 1) {
+      const unsigned long long x = shfl_up64(mi, o);
+      if (lane >= o) mi += x;
+    }
+    const int me = (int)rank * kWarps + warp;
+    if (me / 32 == g) {
+      ties0 = __shfl_sync(0xffffffffu, before, me % 32);
+      mine = __shfl_sync(0xffffffffu, mass[g], me % 32);
+      mine0 = whole + __shfl_sync(0xffffffffu, mi, me % 32) - mine;
+    }
+    whole += __shfl_sync(0xffffffffu, mi, 31);
+    tb += __shfl_sync(0xffffffffu, ti, 31);
+  }
+  // the kept mass must exceed u * whole: a whole number at or below it
+  const unsigned long long target = u >= 1.f ? whole - 1 : u > 0.f ? __umul64hi(whole, fraction64(u)) : 0ull;
+  if (mine0 <= target && target < mine0 + mine) {
+    unsigned long long run = mine0;
+    unsigned trun = ties0;
+    for (int v0 = s.wbeg; v0 < s.wend; v0 += 32) {  // 32 vectors at a time
+      const int v = v0 + lane;
       unsigned long long w[EPV], sum = 0;
-      unsigned char tie[EPV];
-      unsigned nt = 0;
+      unsigned tie = 0;  // bit e: element e equals the cut
 #pragma unroll
-      for (int e = 0; e < EPV; ++e) {
-        w[e] = 0;
-        tie[e] = 0;
-      }
-      if (v < s.end) {
-        s.vec(s.get(v), v, [&](float x, int e) {
-          const int k = kind(x, v * EPV - s.mis + e);
-          if (k == 2) w[e] = weight(x, sc, sm.table);
-          tie[e] = k == 1;
-          nt += k == 1;
+      for (int e = 0; e < EPV; ++e) w[e] = 0;
+      if (v < s.wend) {
+        S::vec(s.get(v), [&](float x, int e) {
+          const int k = kind(x, s.index(v, e));
+          if (k == 2) w[e] = weight<TWO>(x, sc, sm.table);
+          if (k == 1) tie |= 1u << e;
         });
       }
+      const unsigned nt = __popc(tie);
       unsigned ti = nt;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
         const unsigned x = __shfl_up_sync(0xffffffffu, ti, o);
         if (lane >= o) ti += x;
       }
-      unsigned tb = trun + ti - nt;
+      unsigned t = trun + ti - nt;
 #pragma unroll
       for (int e = 0; e < EPV; ++e) {
-        if (tie[e] && tb++ < stay) w[e] = wt;
+        if (((tie >> e) & 1u) && t++ < stay) w[e] = wt;
         sum += w[e];
       }
       unsigned long long wi = sum;
@@ -634,17 +680,22 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(SampleParams a) {
         const unsigned long long x = shfl_up64(wi, o);
         if (lane >= o) wi += x;
       }
-      unsigned long long at = run + wi - sum;
       const unsigned hit = __ballot_sync(0xffffffffu, run + wi > target);
-      if (hit && lane == __ffs(hit) - 1) {
-        int tok = -1;
+      if (hit) {
+        if (lane == __ffs(hit) - 1) {
+          unsigned long long at = run + wi - sum;
+          int tok = -1;
 #pragma unroll
-        for (int e = 0; e < EPV; ++e) {
-          at += w[e];
-          if (tok < 0 && at > target) tok = v * EPV - s.mis + e;
+          for (int e = 0; e < EPV; ++e) {
+            at += w[e];
+            if (tok < 0 && at > target) tok = s.index(v, e);
+          }
+          a.tokens[n] = tok;
         }
-        a.tokens[n] = tok;
+        break;
       }
+      run += __shfl_sync(0xffffffffu, wi, 31);
+      trun += __shfl_sync(0xffffffffu, ti, 31);
     }
   }
   cl.sync();  // no CTA leaves while others read it
@@ -652,6 +703,12 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(SampleParams a) {
 
 constexpr int kStageMax = 96 * 1024;  // two CTAs per SM
 constexpr int kMaxDevices = 64;
+
+Table make_table() {
+  Table t;
+  for (int j = 0; j < kTable; ++j) t.v[j] = (int)(std::exp2(30.0 + j / (double)kTable) + 0.5);
+  return t;
+}
 
 template <typename T, bool STAGED>
 cudaError_t launch_s(const SampleParams& a, int C, size_t smem, cudaStream_t stream) {
@@ -664,6 +721,7 @@ cudaError_t launch_s(const SampleParams& a, int C, size_t smem, cudaStream_t str
     if (e != cudaSuccess) return e;
     if (dev >= 0 && dev < kMaxDevices) opted[dev].store(true, std::memory_order_release);
   }
+  static const Table table = make_table();
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
@@ -678,7 +736,7 @@ cudaError_t launch_s(const SampleParams& a, int C, size_t smem, cudaStream_t str
   cfg.stream = stream;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, sample_kernel<T, STAGED>, a);
+  return cudaLaunchKernelEx(&cfg, sample_kernel<T, STAGED>, a, table);
 }
 
 // CTAs per row: enough that a slice is at most four vectors a thread, and,

@@ -141,7 +141,7 @@ def sample64(x, u, t, top_k, top_p, min_p):
         return int(np.argmax(x))
     with np.errstate(invalid="ignore", over="ignore"):
         w = np.where(x == m, 1.0, np.exp((x - m) / t))
-    w[w < 2.0 ** -41] = 0  # the definition: such a token is never drawn, not for u = 0 either
+    w[w < 2.0 ** -44] = 0  # the definition: such a token is never drawn, not for u = 0 either
     order = np.lexsort((np.arange(len(x)), -x))
     keep = np.ones(len(x), bool)  # by rank
     if 0 < top_k < len(x):
