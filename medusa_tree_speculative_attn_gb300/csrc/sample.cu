@@ -19,12 +19,18 @@
 // matters because a draw compares u against up to 10^5 borders: with weights
 // good to 6e-8 about one row in a thousand of a flat distribution would draw a
 // neighbour of the token that its definition gives.
-// The cut is found by a histogram of counts (and masses) over 512 bins of
-// (m - x) / temperature, 1/16 of a power of two each, and then among the tokens
-// of the one bin that the cut falls in: ranked directly if they are at most 512,
-// else by histograms over their keys, 9 bits at a time, until a single value is
-// left.  The CTAs meet in distributed shared memory: each reads all histograms
-// and lists and searches by itself, so a pass costs one cluster barrier.
+// The cut is found by a histogram of counts and masses over 64 bins of
+// (m - x) / temperature, half a power of two each, and then among the tokens of
+// the one bin that the cut falls in: by histograms over their keys, 6 bits at a
+// time, until at most 128 are left, which are ranked, or a single value.  A
+// histogram is kept a column per lane, so that 32 lanes never meet in a bank.
+// The CTAs meet in distributed shared memory: each reads all sums and lists and
+// searches by itself, so a pass costs one cluster barrier.
+//
+// What it costs (cycles of one CTA with 16k tokens of bf16): 4k for the load, 4k
+// for a histogram of counts, 13k with masses, 6k for the last pass over the
+// weights, and 1k to 2k for each meeting of the cluster; few rows are bound by the
+// chain of meetings, many by the instructions of the weights.
 #include <cooperative_groups.h>
 
 #include <atomic>
@@ -41,7 +47,8 @@ namespace {
 
 constexpr int kThreads = 512;
 constexpr int kWarps = kThreads / 32;
-constexpr int kBins = kThreads;     // a thread per bin in the search
+constexpr int kBins = 64;           // 6 bits a pass
+constexpr int kList = 128;          // tokens that are ranked directly, four threads each
 constexpr int kMaxCluster = 8;
 constexpr int kWBits = 44;          // weight of the maximum: 2^44 * kSampleMaxVocab < 2^63
 
@@ -94,10 +101,8 @@ __device__ __forceinline__ unsigned long long fraction64(float f) {
 // need only the form for |x| <= |m|, because elsewhere their difference is exact.
 template <bool TWO>
 __device__ __forceinline__ unsigned long long weight(float x, const Scale& s, const int* table) {
-  const float d = x - s.m;
+  const float d = x == s.m ? 0.f : x - s.m;  // 0 for x = m = +inf, too
   const float p = d * s.hi;
-  // below one unit (-inf too); d is no number only where x = m = +inf
-  if (!(p > -45.f)) return x == s.m ? 1ull << kWBits : 0ull;
   float err;
   if (TWO) {
     const float bb = d - x;
@@ -115,47 +120,54 @@ __device__ __forceinline__ unsigned long long weight(float x, const Scale& s, co
   const int t = table[n & (kTable - 1)];
   const unsigned w = (unsigned)(t + __mulhi(t, __float2int_rn(q)));
   const int up = (kWBits - 30) + (n >> 7);  // n <= 0
-  return (unsigned long long)(w >> max(0, -up)) * (1u << max(0, up));
+  const unsigned a = p > -45.f ? w >> max(0, -up) : 0u;  // below one unit (-inf too): nothing
+  return (unsigned long long)a * (1u << (max(0, up) & 31));
 }
 
+// A histogram: counts, and the sums of the low and high 16 bits of the weights
+// (2^32 for the maximum), a column per lane.
 struct Hist {
-  unsigned cnt[kBins], lo[kBins], hi[kBins];  // count; low and high 16 bits of the 32-bit weights, summed
+  unsigned cnt[kBins][32], lo[kBins][32], hi[kBins][32];
 };
 
-constexpr int kList = kThreads;  // tokens of one bin that are ranked directly, a thread each
-
-struct List {
-  unsigned n;
-  uint32_t key[kList];
-  int idx[kList];
+struct Found {  // a bin of a histogram of the whole cluster
+  unsigned in;              // tokens in the bin
+  unsigned cnt;             // tokens before it
+  unsigned long long mass;  // their mass
+  unsigned long long own;   // the bin's
 };
 
-struct Found {  // where a search ended
-  int bin;
-  unsigned cnt;             // tokens before the bin
-  unsigned long long mass;  // their mass (2^32 for the maximum)
+struct Cut {  // the last token that is kept
+  uint32_t key;             // its shifted key
+  int idx;                  // its index, or -1: the first `stay` tokens of that key
+  unsigned stay;
+  unsigned long long mass;  // mass up to it
 };
 
-struct Smem {
-  Hist hist[3];  // the bins; two for the bin that is searched further
+struct __align__(16) Smem {
+  Hist hist;
   int table[kTable];
-  unsigned long long key[kWarps];        // block reduction of (value, index)
-  unsigned long long best;               // this CTA's, read by the cluster
-  unsigned wc[kWarps];                   // scans
-  unsigned long long wm[kWarps];
+  // read by the cluster:
+  unsigned long long best;
+  unsigned bin_cnt[2][kBins];            // this CTA's sums of a histogram, by turns
+  unsigned long long bin_mass[2][kBins];
+  unsigned list_n[2];                    // this CTA's tokens of a range, one list for each cut
+  uint32_t list_key[2][kList];
+  int list_idx[2][kList];
+  unsigned long long tot_mass;           // this CTA's kept mass and tokens equal to the cut
+  unsigned tot_ties;
+  // this CTA's own:
+  unsigned long long key[kWarps];
+  unsigned part_cnt[kMaxCluster][kBins];
+  unsigned long long part_mass[kMaxCluster][kBins];
+  Found bins[kBins];
   unsigned long long whole;
+  unsigned long long rank_key[kList], rank_mass[kList];
+  Cut cut;
+  unsigned long long run_mass[kWarps];
+  unsigned run_ties[kWarps];
   double ln_min_p;
   float x_min;
-  Found found;
-  List list[2];                          // this CTA's tokens of a bin, read by the cluster
-  uint32_t mkey[kList];                  // the cluster's
-  int midx[kList];
-  unsigned long long mw[kList];
-  uint32_t cut_key;
-  int cut_idx;
-  unsigned long long cut_mass;
-  unsigned long long run_mass[kWarps];   // each warp's kept mass and tokens equal to the cut
-  unsigned run_ties[kWarps];
 };
 
 // NaN as -inf, in a packed vector.
@@ -203,17 +215,17 @@ __device__ __forceinline__ float vec_max(const uint4& r) {
 
 // A CTA's part of a row, staged in shared memory by the first pass over it (or,
 // where it does not fit, read again by every pass).  Warp w holds a contiguous
-// run of 16-byte vectors, lane l every 32nd of them.  NaN counts as -inf, and so
-// do the places of a ragged first or last vector that lie outside the row (an
-// index outside [0, V) is never drawn: its weight is 0 and it is below every cut
-// but that of a row without enough tokens above -inf, where it adds nothing).
+// run of 16-byte vectors and lane l a contiguous part of it, so that sums by lane
+// are sums in vocab order.  NaN counts as -inf, and so do the places of a ragged
+// first or last vector that lie outside the row.
 template <typename T, bool STAGED>
 struct Slice {
   static constexpr int EPV = 16 / (int)sizeof(T);
   const T* row;
   uint4* stage;
-  int V, beg, mis;  // this CTA's first vector; vector v holds elements v * EPV - mis and on
-  int wbeg, wend;   // this warp's vectors
+  int V, beg, end, mis;  // this CTA's vectors; vector v holds elements v * EPV - mis and on
+  int per_lane;          // vectors of a lane
+  int lbeg, lend;        // this lane's vectors
 
   __device__ __forceinline__ void init(const T* row_, int V_, uint4* stage_, unsigned rank, unsigned C) {
     row = row_;
@@ -223,10 +235,10 @@ struct Slice {
     const int nvec = (V + mis + EPV - 1) / EPV;
     const int per = (nvec + (int)C - 1) / (int)C;
     beg = min(nvec, (int)rank * per);
-    const int end = min(nvec, beg + per);
-    const int run = ((end - beg + kWarps - 1) / kWarps + 31) / 32 * 32;
-    wbeg = min(end, beg + (int)(threadIdx.x >> 5) * run);
-    wend = min(end, wbeg + run);
+    end = min(nvec, beg + per);
+    per_lane = (end - beg + kThreads - 1) / kThreads;
+    lbeg = min(end, beg + (int)threadIdx.x * per_lane);
+    lend = min(end, lbeg + per_lane);
   }
   __device__ __forceinline__ uint4 load(int v) const {
     const int e0 = v * EPV - mis;
@@ -241,8 +253,12 @@ struct Slice {
     memcpy(&r, t, 16);
     return no_nan<T>(r);
   }
-  __device__ __forceinline__ uint4 get(int v) const { return STAGED ? stage[v - beg] : load(v); }
+  // Where vector beg + i is staged: lanes that read their own parts (four
+  // vectors each, mostly) then hit distinct banks.
+  static __device__ __forceinline__ int place(int i) { return (i & ~3) | ((i & 3) ^ ((i >> 3) & 3)); }
+  __device__ __forceinline__ uint4 get(int v) const { return STAGED ? stage[place(v - beg)] : load(v); }
   __device__ __forceinline__ int index(int v, int e) const { return v * EPV - mis + e; }
+  __device__ __forceinline__ bool in_row(int v, int e) const { return (unsigned)index(v, e) < (unsigned)V; }
   // f(x, e) over the elements of a vector
   template <class F>
   static __device__ __forceinline__ void vec(const uint4& r, F f) {
@@ -251,30 +267,34 @@ struct Slice {
 #pragma unroll
     for (int e = 0; e < EPV; ++e) f(Act<T>::to_f(t[e]), e);
   }
-  // f(x, v, e) over this thread's elements
+  // f(x, v, e) over this lane's elements; vectors whose elements are all below
+  // `least` may be left out
   template <class F>
-  __device__ __forceinline__ void each(F f) const {
+  __device__ __forceinline__ void each(float least, F f) const {
 #pragma unroll 1
-    for (int v = wbeg + (int)(threadIdx.x & 31); v < wend; v += 32) vec(get(v), [&](float x, int e) { f(x, v, e); });
+    for (int v = lbeg; v < lend; ++v) {
+      const uint4 r = get(v);
+      if (!(vec_max<T>(r) < least)) vec(r, [&](float x, int e) { f(x, v, e); });
+    }
   }
-  // The first pass: the row into shared memory; the largest value and its
-  // lowest index (a thread's indices rise) as a key, 0 where there is nothing
-  // above -inf.
+  // The first pass, in whole lines: the row into shared memory; the largest value
+  // and its lowest index (a thread's indices rise) as a key, 0 where there is
+  // nothing above -inf.
   __device__ __forceinline__ unsigned long long first() const {
     constexpr int U = 4;  // vectors in flight
     float best = -INFINITY;
     int bi = 0;
 #pragma unroll 1
-    for (int v0 = wbeg + (int)(threadIdx.x & 31); v0 < wend; v0 += U * 32) {
+    for (int v0 = beg + (int)threadIdx.x; v0 < end; v0 += U * kThreads) {
       uint4 r[U];
 #pragma unroll
       for (int j = 0; j < U; ++j)
-        if (v0 + j * 32 < wend) r[j] = load(v0 + j * 32);
+        if (v0 + j * kThreads < end) r[j] = load(v0 + j * kThreads);
 #pragma unroll
       for (int j = 0; j < U; ++j) {
-        const int v = v0 + j * 32;
-        if (v >= wend) continue;
-        if (STAGED) stage[v - beg] = r[j];
+        const int v = v0 + j * kThreads;
+        if (v >= end) continue;
+        if (STAGED) stage[place(v - beg)] = r[j];
         const float m = vec_max<T>(r[j]);
         if (m > best) {  // then search the vector
           T t[EPV];
@@ -294,75 +314,103 @@ __device__ __forceinline__ unsigned long long shfl_up64(unsigned long long v, in
   return __shfl_up_sync(0xffffffffu, v, o);
 }
 
-// A histogram summed over the cluster, a thread per bin: the bin's count and
-// mass, and what lies before it.
-struct Prefix {
-  unsigned cnt, before_cnt;
-  unsigned long long mass, before_mass;
+__device__ __forceinline__ void clear(Hist& h) {
+  uint4* p = reinterpret_cast<uint4*>(&h);
+  for (int i = threadIdx.x; i < (int)(sizeof(Hist) / 16); i += kThreads) p[i] = make_uint4(0, 0, 0, 0);
+}
 
-  __device__ void sum(Smem& sm, int buf, cg::cluster_group& cl, unsigned base_cnt, unsigned long long base_mass) {
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    cnt = 0;
-    mass = 0;
-#pragma unroll 4
-    for (unsigned r = 0; r < cl.num_blocks(); ++r) {
-      const Hist* p = &cl.map_shared_rank(&sm, r)->hist[buf];
-      cnt += p->cnt[tid];
-      mass += p->lo[tid] + ((unsigned long long)p->hi[tid] << 16);
+// The cluster's histogram in sm.bins, each bin with what lies before it (base_cnt
+// and base_mass included).  The histogram is left zero; turn: which of the two
+// places the sums pass through.
+__device__ __noinline__ void meet(Smem& sm, int turn, unsigned base_cnt, unsigned long long base_mass) {
+  cg::cluster_group cl = cg::this_cluster();
+  const int tid = threadIdx.x, lane = tid & 31, C = (int)cl.num_blocks();
+  __syncthreads();
+  {  // eight threads a bin, four columns each
+    const int b = tid >> 3, c = tid & 7;
+    unsigned n = 0;
+    unsigned long long m = 0;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      n += sm.hist.cnt[b][c + 8 * j];
+      m += sm.hist.lo[b][c + 8 * j] + ((unsigned long long)sm.hist.hi[b][c + 8 * j] << 16);
+      sm.hist.cnt[b][c + 8 * j] = sm.hist.lo[b][c + 8 * j] = sm.hist.hi[b][c + 8 * j] = 0;
     }
-    unsigned ci = cnt;
-    unsigned long long mi = mass;
+#pragma unroll
+    for (int o = 4; o > 0; o >>= 1) {
+      n += __shfl_xor_sync(0xffffffffu, n, o);
+      m += __shfl_xor_sync(0xffffffffu, m, o);
+    }
+    if (c == 0) {
+      sm.bin_cnt[turn][b] = n;
+      sm.bin_mass[turn][b] = m;
+    }
+  }
+  cl.sync();
+  const int r = tid / kBins, b = tid % kBins;  // a thread per CTA and bin
+  if (r < C) {
+    const Smem* p = cl.map_shared_rank(&sm, r);
+    sm.part_cnt[r][b] = p->bin_cnt[turn][b];
+    sm.part_mass[r][b] = p->bin_mass[turn][b];
+  }
+  __syncthreads();
+  if (tid < 32) {  // two bins a lane
+    unsigned n[2] = {0, 0};
+    unsigned long long m[2] = {0, 0};
+    for (int q = 0; q < C; ++q)
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        n[j] += sm.part_cnt[q][2 * lane + j];
+        m[j] += sm.part_mass[q][2 * lane + j];
+      }
+    unsigned ni = n[0] + n[1];
+    unsigned long long mi = m[0] + m[1];
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-      const unsigned cv = __shfl_up_sync(0xffffffffu, ci, o);
-      const unsigned long long mv = shfl_up64(mi, o);
+      const unsigned x = __shfl_up_sync(0xffffffffu, ni, o);
+      const unsigned long long y = shfl_up64(mi, o);
       if (lane >= o) {
-        ci += cv;
-        mi += mv;
+        ni += x;
+        mi += y;
       }
     }
-    if (lane == 31) {
-      sm.wc[warp] = ci;
-      sm.wm[warp] = mi;
-    }
-    __syncthreads();
-    before_cnt = base_cnt + ci - cnt;
-    before_mass = base_mass + mi - mass;
-    for (int w = 0; w < warp; ++w) {
-      before_cnt += sm.wc[w];
-      before_mass += sm.wm[w];
-    }
-    if (tid == kThreads - 1) sm.whole = before_mass + mass;
-    __syncthreads();
+    ni += base_cnt;
+    mi += base_mass;
+    sm.bins[2 * lane] = Found{n[0], ni - n[0] - n[1], mi - m[0] - m[1], m[0]};
+    sm.bins[2 * lane + 1] = Found{n[1], ni - n[1], mi - m[1], m[1]};
+    if (lane == 31) sm.whole = mi;
   }
-  // The bin at which the running count reaches want_cnt or, where that is 0, the
-  // running mass want_mass.  Every CTA finds the same.
-  __device__ Found find(Smem& sm, unsigned want_cnt, unsigned long long want_mass) const {
-    const bool here = want_cnt ? before_cnt < want_cnt && want_cnt <= before_cnt + cnt
-                               : before_mass < want_mass && want_mass <= before_mass + mass;
-    if (here) sm.found = Found{(int)threadIdx.x, before_cnt, before_mass};
-    __syncthreads();
-    const Found f = sm.found;
-    __syncthreads();
-    return f;
+  __syncthreads();
+}
+
+// The bin of sm.bins at which the running count reaches want_cnt or, where that is
+// 0, the running mass want_mass; every warp for itself.
+__device__ __forceinline__ int find(const Smem& sm, unsigned want_cnt, unsigned long long want_mass) {
+  int at = 0;
+#pragma unroll
+  for (int j = 0; j < 2; ++j) {
+    const Found f = sm.bins[32 * j + (threadIdx.x & 31)];
+    at += __popc(__ballot_sync(0xffffffffu, want_cnt ? f.cnt + f.in < want_cnt : f.mass + f.own < want_mass));
   }
-};
+  return min(at, kBins - 1);
+}
 
 template <typename T, bool STAGED>
 __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams a, const __grid_constant__ Table table) {
   using S = Slice<T, STAGED>;
-  extern __shared__ uint4 stage[];
   constexpr int EPV = S::EPV;
   constexpr int KS = KeyShift<T>::v;
   constexpr bool TWO = sizeof(T) == 4;
-  __shared__ Smem sm;
+  extern __shared__ uint4 dyn[];  // Smem, then the staged slice
+  static_assert(sizeof(Smem) % 16 == 0, "the slice is aligned");
+  Smem& sm = *reinterpret_cast<Smem*>(dyn);
   cg::cluster_group cl = cg::this_cluster();
-  const unsigned C = cl.num_blocks(), rank = cl.block_rank();
+  const int C = (int)cl.num_blocks(), rank = (int)cl.block_rank();
   const int n = blockIdx.x / C;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   if (tid < kTable) sm.table[tid] = table.v[tid];
-  if (tid < 2) sm.list[tid].n = 0;
-  for (int b = 0; b < 3; ++b) sm.hist[b].cnt[tid] = sm.hist[b].lo[tid] = sm.hist[b].hi[tid] = 0;
+  if (tid < 2) sm.list_n[tid] = 0;
+  clear(sm.hist);
   pdl_wait();
   const int src = a.row_index ? a.row_index[n] : n;
   if (src < 0 || src >= a.rows) {  // the same for the whole cluster
@@ -372,14 +420,14 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
   const float temp = a.temperature ? a.temperature[n] : 1.f;
   int want_k = a.top_k ? a.top_k[n] : 0;
   const float top_p = a.top_p ? a.top_p[n] : 1.f;
-  float min_p = a.min_p ? a.min_p[n] : 0.f;
+  const float min_p = a.min_p ? a.min_p[n] : 0.f;
   const float u = a.uniforms[n];
   if (min_p > 1.f) want_k = 1;  // no weight reaches it: the first token alone
   // the one thing that takes 64-bit floats (two results a clock and SM), by one thread
   if (tid == 0) sm.ln_min_p = min_p > 0.f ? log((double)min_p) : 0.0;
 
   S s;
-  s.init(static_cast<const T*>(a.logits) + src * a.row_stride, a.V, stage, rank, C);
+  s.init(static_cast<const T*>(a.logits) + src * a.row_stride, a.V, dyn + sizeof(Smem) / 16, (unsigned)rank, (unsigned)C);
 
   // ---- maximum and its lowest index ----
   {
@@ -391,17 +439,24 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
     }
     if (lane == 0) sm.key[warp] = key;
     __syncthreads();
-    if (tid == 0) {
-      for (int w = 1; w < kWarps; ++w) key = sm.key[w] > key ? sm.key[w] : key;
-      sm.best = key;
+    if (warp == 0) {
+      key = lane < kWarps ? sm.key[lane] : 0ull;
+#pragma unroll
+      for (int o = kWarps / 2; o > 0; o >>= 1) {
+        const unsigned long long k = __shfl_xor_sync(0xffffffffu, key, o);
+        key = k > key ? k : key;
+      }
+      if (lane == 0) sm.best = key;
     }
   }
-  cl.sync();  // (histograms are zero, too)
-  unsigned long long best = 0;
-  for (unsigned r = 0; r < C; ++r) {
-    const unsigned long long k = cl.map_shared_rank(&sm, r)->best;
+  cl.sync();
+  unsigned long long best = lane < C ? cl.map_shared_rank(&sm, lane)->best : 0ull;
+#pragma unroll
+  for (int o = kMaxCluster / 2; o > 0; o >>= 1) {
+    const unsigned long long k = __shfl_xor_sync(0xffffffffu, best, o);
     best = k > best ? k : best;
   }
+  best = __shfl_sync(0xffffffffu, best, 0);
   if (!(temp > 0.f) || best == 0ull) {  // greedy, or a row of nothing but -inf
     if (rank == 0 && tid == 0) a.tokens[n] = best == 0ull ? -1 : (int)(0xffffffffu - (unsigned)best);
     cl.sync();  // no CTA leaves while others read it
@@ -425,140 +480,132 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
 
   // ---- the cut ----
   const bool use_k = want_k > 0 && want_k < a.V, use_p = top_p < 1.f;
-  bool cut = false;
-  uint32_t cut_key = 0;       // ord >> KS
-  int cut_idx = -1;           // the last token of that value that is kept,
-  unsigned stay = 0;          // or how many are (where the index is not known)
+  Cut cut{0u, -1, 0u, 0ull};
   if (use_k || use_p) {
-    const float width = sc.hi * 16.f;
-    auto bin_of = [&](float x) { return x == sc.m ? 0 : min(kBins - 1, __float2int_rz((sc.m - x) * width)); };
+    const float width = sc.hi * 2.f;
+    auto bin_of = [&](float x) {  // rounded, so that no conversion is needed; it never falls as x falls
+      const float z = fminf((sc.m - x) * width, (float)(kBins - 1)) + 12582912.f;
+      return x == sc.m ? 0 : __float_as_int(z) - 0x4B400000;
+    };
     auto weight_of = [&](float x) {  // 2^32 for the maximum
       return (weight<TWO>(x, sc, sm.table) + (1u << (kWBits - 33))) >> (kWBits - 32);
     };
-    auto add = [&](Hist& h, int b, float x) {
-      if (use_k) atomicAdd(&h.cnt[b], 1u);
+    auto add = [&](int b, float x) {
+      atomicAdd(&sm.hist.cnt[b][lane], 1u);
       if (use_p) {
         const unsigned long long w = weight_of(x);
         const unsigned l = (unsigned)w & 0xffffu, g = (unsigned)(w >> 16);
-        if (l) atomicAdd(&h.lo[b], l);
-        if (g) atomicAdd(&h.hi[b], g);
+        if (l) atomicAdd(&sm.hist.lo[b][lane], l);
+        if (g) atomicAdd(&sm.hist.hi[b][lane], g);
       }
     };
-    s.each([&](float x, int v, int e) {
-      if ((unsigned)s.index(v, e) < (unsigned)a.V) add(sm.hist[0], bin_of(x), x);
+    s.each(-INFINITY, [&](float x, int v, int e) {
+      if (s.in_row(v, e)) add(bin_of(x), x);
     });
-    cl.sync();
-    int buf = 1;  // the next pass's histogram, zero at this point and read by nobody
-    unsigned long long cut_mass = 0;  // mass up to the cut
-    int which = 0, listed = -1;       // the next list; the bin whose tokens are merged
-    unsigned nlist = 0;
+    int turn = 0;
+    meet(sm, turn, 0u, 0ull);
+    unsigned long long whole = sm.whole;
+    const int bin_k = use_k ? find(sm, (unsigned)want_k, 0ull) : 0;
+    Found in_k = sm.bins[bin_k];
+    // sm.bins is written again by the first cut's passes: what the second may need
+    // of it is kept by each warp, two bins a lane
+    const Found mine0 = sm.bins[lane], mine1 = sm.bins[32 + lane];
+    __syncthreads();
+
     // from the bin that a count or mass falls in to the last token kept
-    auto refine = [&](Found f, unsigned want_cnt, unsigned long long want_mass) {
-      const int bin = f.bin;
-      // the bin's tokens, ranked directly if they are few (they mostly are)
-      if (bin != listed) {
-        List& mine = sm.list[which];
-        s.each([&](float x, int v, int e) {
-          const int i = s.index(v, e);
-          if (bin_of(x) != bin || (unsigned)i >= (unsigned)a.V) return;
-          const unsigned at = atomicAdd(&mine.n, 1u);
-          if (at < kList) {
-            mine.key[at] = ord_of(x) >> KS;
-            mine.idx[at] = i;
-          }
-        });
-        cl.sync();
-        nlist = 0;
-        bool fits = true;
-        int from = -1, at = 0;
-        for (unsigned r = 0; r < C; ++r) {
-          const unsigned c = cl.map_shared_rank(&sm, r)->list[which].n;
-          if (from < 0 && (unsigned)tid < nlist + c) {
-            from = (int)r;
-            at = tid - (int)nlist;
-          }
-          fits = fits && c <= kList;
-          nlist += c;
-        }
-        fits = fits && nlist <= kList;
-        if (fits && tid < (int)nlist) {
-          const List* l = &cl.map_shared_rank(&sm, from)->list[which];
-          sm.mkey[tid] = l->key[at];
-          sm.midx[tid] = l->idx[at];
-          sm.mw[tid] = use_p ? weight_of(value_of_key<KS>(l->key[at])) : 0ull;
-        }
-        __syncthreads();
-        which ^= 1;
-        listed = fits ? bin : -1;
-      }
-      if (listed == bin) {
-        if (tid < (int)nlist) {
-          const uint32_t k = sm.mkey[tid];
-          const int i = sm.midx[tid];
-          const unsigned long long w = sm.mw[tid];
-          unsigned c = f.cnt;
-          unsigned long long m = f.mass;
-          for (unsigned j = 0; j < nlist; ++j)
-            if (sm.mkey[j] > k || (sm.mkey[j] == k && sm.midx[j] < i)) {
-              ++c;
-              m += sm.mw[j];
-            }
-          if (want_cnt ? c + 1 == want_cnt : m < want_mass && want_mass <= m + w) {
-            sm.cut_key = k;
-            sm.cut_idx = i;
-            sm.cut_mass = m + w;
-          }
-        }
-        __syncthreads();
-        cut = true;
-        cut_key = sm.cut_key;
-        cut_idx = sm.cut_idx;
-        cut_mass = sm.cut_mass;
-        __syncthreads();
-        return;
-      }
+    auto refine = [&](int bin, Found f, int which, unsigned want_cnt, unsigned long long want_mass) {
       // the bin's keys, with room for rounding on both sides
-      const float xh = sc.m - (float)bin / width, xl = sc.m - (float)(bin + 1) / width;
-      uint32_t hi = ord_of(xh + 1e-5f * (fabsf(sc.m) + fabsf(xh)) + 1e-30f) >> KS;
+      const float xh = sc.m - ((float)bin - 0.5f) / width, xl = sc.m - ((float)bin + 0.5f) / width;
+      uint32_t hi = bin == 0 ? 0xffffffffu >> KS : ord_of(xh + 1e-5f * (fabsf(sc.m) + fabsf(xh)) + 1e-30f) >> KS;
       uint32_t lo = bin == kBins - 1 ? 0u : ord_of(xl - 1e-5f * (fabsf(sc.m) + fabsf(xl)) - 1e-30f) >> KS;
       if (!(fabsf(sc.m) < INFINITY)) {
         hi = 0xffffffffu >> KS;
         lo = 0;
       }
-      while (true) {
-        const int bits = 32 - __clz(hi - lo);
-        const int shift = max(0, bits - 9);
-        Hist& h = sm.hist[buf];
-        s.each([&](float x, int v, int e) {
+      hi = min(hi, (uint32_t)(best >> 32) >> KS);
+      for (int pass = 0; pass < 7; ++pass) {  // 6 of at most 32 bits each, then one value or a list
+        // whole vectors below the range are passed over (keys below -inf's are no numbers)
+        const float least = lo <= ord_of(-INFINITY) >> KS ? -INFINITY : value_of_key<KS>(lo);
+        if (f.in <= kList) {
+          // few tokens: listed, and ranked by (key, lower index) by four threads each
+          s.each(least, [&](float x, int v, int e) {
+            const uint32_t k = ord_of(x) >> KS;
+            if (k < lo || k > hi || bin_of(x) != bin || !s.in_row(v, e)) return;
+            const unsigned at = atomicAdd(&sm.list_n[which], 1u);
+            if (at < kList) {  // f.in says so
+              sm.list_key[which][at] = k;
+              sm.list_idx[which][at] = s.index(v, e);
+            }
+          });
+          cl.sync();
+          const int c = lane < C ? (int)cl.map_shared_rank(&sm, lane)->list_n[which] : 0;
+          int ci = c;
+#pragma unroll
+          for (int o = 1; o < kMaxCluster; o <<= 1) {
+            const int x = __shfl_up_sync(0xffffffffu, ci, o);
+            if (lane >= o) ci += x;
+          }
+          const int total = min(__shfl_sync(0xffffffffu, ci, kMaxCluster - 1), kList);
+          int from = 0;
+#pragma unroll
+          for (int r = 0; r < kMaxCluster - 1; ++r) from += tid >= __shfl_sync(0xffffffffu, ci, r);
+          const int before = __shfl_sync(0xffffffffu, ci - c, from);  // (from < 8: lists before this thread's)
+          if (tid < total) {
+            const Smem* p = cl.map_shared_rank(&sm, from);
+            const uint32_t k = p->list_key[which][tid - before];
+            sm.rank_key[tid] = ((unsigned long long)k << 32) | (0xffffffffu - (unsigned)p->list_idx[which][tid - before]);
+            sm.rank_mass[tid] = use_p ? weight_of(value_of_key<KS>(k)) : 0ull;
+          }
+          __syncthreads();
+          const int t = tid >> 2;
+          const unsigned long long k = t < total ? sm.rank_key[t] : ~0ull;
+          unsigned cnt = 0;
+          unsigned long long m = 0;
+#pragma unroll 4
+          for (int j = tid & 3; j < total; j += 4) {
+            const bool before = sm.rank_key[j] > k;
+            cnt += before;
+            m += before ? sm.rank_mass[j] : 0ull;
+          }
+          cnt += __shfl_xor_sync(0xffffffffu, cnt, 1);
+          m += __shfl_xor_sync(0xffffffffu, m, 1);
+          cnt += __shfl_xor_sync(0xffffffffu, cnt, 2);
+          m += __shfl_xor_sync(0xffffffffu, m, 2);
+          cnt += f.cnt;
+          m += f.mass;
+          if (t < total && (tid & 3) == 0) {
+            const unsigned long long w = sm.rank_mass[t];
+            if (want_cnt ? cnt + 1 == want_cnt : m < want_mass && want_mass <= m + w)
+              sm.cut = Cut{(uint32_t)(k >> 32), (int)(0xffffffffu - (unsigned)k), 0u, m + w};
+          }
+          __syncthreads();
+          cut = sm.cut;
+          __syncthreads();
+          return;
+        }
+        if (hi == lo) break;
+        const int shift = max(0, 32 - __clz(hi - lo) - 6);
+        s.each(least, [&](float x, int v, int e) {
           const uint32_t k = ord_of(x) >> KS;
-          if (k >= lo && k <= hi && bin_of(x) == bin && (unsigned)s.index(v, e) < (unsigned)a.V) add(h, (int)((hi - k) >> shift), x);
+          if (k >= lo && k <= hi && bin_of(x) == bin && s.in_row(v, e)) add((int)((hi - k) >> shift), x);
         });
-        cl.sync();
-        // past this barrier nobody reads the other buffer any more
-        Hist& o = sm.hist[3 - buf];
-        o.cnt[tid] = o.lo[tid] = o.hi[tid] = 0;
-        Prefix sub;
-        sub.sum(sm, buf, cl, f.cnt, f.mass);
-        f = sub.find(sm, want_cnt, want_mass);  // ends in a block barrier
-        buf = 3 - buf;
-        hi -= (uint32_t)f.bin << shift;
-        if (shift == 0) break;
+        turn ^= 1;
+        meet(sm, turn, f.cnt, f.mass);
+        const int b = find(sm, want_cnt, want_mass);
+        f = sm.bins[b];
+        __syncthreads();
+        hi -= (uint32_t)b << shift;
         const uint32_t span = (1u << shift) - 1u;
         lo = max(lo, hi > span ? hi - span : 0u);
       }
-      cut = true;
-      cut_key = hi;
-      cut_idx = -1;
+      // one value, of many tokens: the first `stay` of them
       const unsigned long long w = use_p ? weight_of(value_of_key<KS>(hi)) : 0ull;
-      stay = want_cnt ? want_cnt - f.cnt : (unsigned)((want_mass - f.mass + w - 1) / w);
-      cut_mass = f.mass + stay * w;
+      const unsigned stay = want_cnt ? want_cnt - f.cnt : w ? (unsigned)((want_mass - f.mass + w - 1) / w) : f.in;
+      cut = Cut{hi, -1, stay, f.mass + stay * w};
     };
-    Prefix bins;
-    bins.sum(sm, 0, cl, 0u, 0ull);
-    unsigned long long whole = sm.whole;
     if (use_k) {
-      refine(bins.find(sm, (unsigned)want_k, 0ull), (unsigned)want_k, 0ull);
-      whole = cut_mass;
+      refine(bin_k, in_k, 0, (unsigned)want_k, 0ull);
+      whole = cut.mass;
     }
     if (use_p) {
       // kept: mass before < top_p * whole, a whole number's comparison with the
@@ -569,133 +616,142 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
         want = max(__umul64hi(whole, f) + (whole * f != 0), 1ull);
       }
       if (want > whole) want = whole;
-      refine(bins.find(sm, 0u, want), 0u, want);
+      const int b = min(__popc(__ballot_sync(0xffffffffu, mine0.mass + mine0.own < want)) +
+                            __popc(__ballot_sync(0xffffffffu, mine1.mass + mine1.own < want)),
+                        kBins - 1);
+      Found f;
+      f.in = __shfl_sync(0xffffffffu, b < 32 ? mine0.in : mine1.in, b & 31);
+      f.cnt = __shfl_sync(0xffffffffu, b < 32 ? mine0.cnt : mine1.cnt, b & 31);
+      f.mass = __shfl_sync(0xffffffffu, b < 32 ? mine0.mass : mine1.mass, b & 31);
+      f.own = __shfl_sync(0xffffffffu, b < 32 ? mine0.own : mine1.own, b & 31);
+      refine(b, f, 1, 0u, want);
     }
   }
+  const bool cuts = use_k || use_p;
   __syncthreads();
   const float x_min = sm.x_min;
-  auto kind = [&](float x, int i) {  // 2: kept, 1: equal to the cut, 0: not kept
+  auto kind = [&](float x, int v, int e) {  // 2: kept, 1: equal to the cut, 0: not kept
     if (x < x_min) return 0;
-    if (!cut) return 2;
+    if (!cuts) return 2;
     const uint32_t k = ord_of(x) >> KS;
-    if (k != cut_key) return k > cut_key ? 2 : 0;
-    return cut_idx < 0 ? ((unsigned)i < (unsigned)a.V ? 1 : 0) : i <= cut_idx ? 2 : 0;
+    if (k != cut.key) return k > cut.key ? 2 : 0;
+    return cut.idx >= 0 ? (s.index(v, e) <= cut.idx ? 2 : 0) : s.in_row(v, e) ? 1 : 0;
   };
 
-  // ---- kept mass of each warp's run, in vocab order ----
-  {
-    unsigned long long mass = 0;
-    unsigned ties = 0;
-    s.each([&](float x, int v, int e) {
-      const int k = kind(x, s.index(v, e));
-      if (k == 2) mass += weight<TWO>(x, sc, sm.table);
-      ties += k == 1;
+  // ---- kept mass of each lane's part, in vocab order; of the tokens equal to the
+  // cut the first `stay` count ----
+  const float least = cuts ? fmaxf(x_min, value_of_key<KS>(cut.key)) : x_min;
+  unsigned long long lane_mass = 0;
+  unsigned lane_ties = 0;
+  if (!cuts && x_min == -INFINITY) {
+    s.each(-INFINITY, [&](float x, int, int) { lane_mass += weight<TWO>(x, sc, sm.table); });
+  } else {
+    s.each(least, [&](float x, int v, int e) {
+      const int k = kind(x, v, e);
+      if (k == 2) lane_mass += weight<TWO>(x, sc, sm.table);
+      lane_ties += k == 1;
     });
+  }
+  {
+    unsigned long long m = lane_mass;
+    unsigned t = lane_ties;
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) {
-      mass += __shfl_xor_sync(0xffffffffu, mass, o);
-      ties += __shfl_xor_sync(0xffffffffu, ties, o);
+      m += __shfl_xor_sync(0xffffffffu, m, o);
+      t += __shfl_xor_sync(0xffffffffu, t, o);
     }
     if (lane == 0) {
-      sm.run_mass[warp] = mass;
-      sm.run_ties[warp] = ties;
+      sm.run_mass[warp] = m;
+      sm.run_ties[warp] = t;
+    }
+    __syncthreads();
+    if (warp == 0) {
+      m = lane < kWarps ? sm.run_mass[lane] : 0ull;
+      t = lane < kWarps ? sm.run_ties[lane] : 0u;
+#pragma unroll
+      for (int o = kWarps / 2; o > 0; o >>= 1) {
+        m += __shfl_xor_sync(0xffffffffu, m, o);
+        t += __shfl_xor_sync(0xffffffffu, t, o);
+      }
+      if (lane == 0) {
+        sm.tot_mass = m;
+        sm.tot_ties = t;
+      }
     }
   }
   cl.sync();
-  // ---- the run that the draw falls in: every warp looks at all of them (a lane
-  // per run, CTA by CTA), and the one that holds it goes on.  Of the tokens equal
-  // to the cut the first `stay` in vocab order count.
-  const unsigned long long wt = cut && cut_idx < 0 ? weight<TWO>(value_of_key<KS>(cut_key), sc, sm.table) : 0ull;
-  const int nruns = (int)C * kWarps;  // at most 128
-  unsigned long long mass[4];
-  unsigned long long whole = 0, mine0 = 0, mine = 0;
-  unsigned tb = 0, ties0 = 0;
-#pragma unroll
-  for (int g = 0; g < 4; ++g) {
-    const int run = g * 32 + lane;
-    mass[g] = 0;
-    unsigned t = 0;
-    if (run < nruns) {
-      const Smem* p = cl.map_shared_rank(&sm, (unsigned)(run / kWarps));
-      mass[g] = p->run_mass[run % kWarps];
-      t = p->run_ties[run % kWarps];
-    }
+  // ---- the CTA, the warp, the lane and the token that the draw falls in ----
+  const unsigned long long wt = cuts && cut.idx < 0 ? weight<TWO>(value_of_key<KS>(cut.key), sc, sm.table) : 0ull;
+  // From each lane's (mass, ties) to running values: `run` and `ties` become what
+  // lies before the lane (added to base_*), and the lane's mass with its share of
+  // the ties is returned.
+  auto running = [&](unsigned long long m, unsigned t, unsigned long long base_mass, unsigned base_ties,
+                     unsigned long long& run, unsigned& ties) {
     unsigned ti = t;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const unsigned x = __shfl_up_sync(0xffffffffu, ti, o);
       if (lane >= o) ti += x;
     }
-    const unsigned before = tb + ti - t;
-    mass[g] += (before >= stay ? 0u : min(t, stay - before)) * wt;
-    unsigned long long mi = mass[g];
+    ties = base_ties + ti - t;
+    m += (ties >= cut.stay ? 0u : min(t, cut.stay - ties)) * wt;
+    unsigned long long mi = m;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const unsigned long long x = shfl_up64(mi, o);
       if (lane >= o) mi += x;
     }
-    const int me = (int)rank * kWarps + warp;
-    if (me / 32 == g) {
-      ties0 = __shfl_sync(0xffffffffu, before, me % 32);
-      mine = __shfl_sync(0xffffffffu, mass[g], me % 32);
-      mine0 = whole + __shfl_sync(0xffffffffu, mi, me % 32) - mine;
-    }
-    whole += __shfl_sync(0xffffffffu, mi, 31);
-    tb += __shfl_sync(0xffffffffu, ti, 31);
-  }
+    run = base_mass + mi - m;
+    return m;
+  };
+  unsigned long long run, m;
+  unsigned ties;
+  m = running(lane < C ? cl.map_shared_rank(&sm, lane)->tot_mass : 0ull,
+              lane < C ? cl.map_shared_rank(&sm, lane)->tot_ties : 0u, 0ull, 0u, run, ties);
+  const unsigned long long whole = __shfl_sync(0xffffffffu, run + m, 31);
   // the kept mass must exceed u * whole: a whole number at or below it
   const unsigned long long target = u >= 1.f ? whole - 1 : u > 0.f ? __umul64hi(whole, fraction64(u)) : 0ull;
-  if (mine0 <= target && target < mine0 + mine) {
-    unsigned long long run = mine0;
-    unsigned trun = ties0;
-    for (int v0 = s.wbeg; v0 < s.wend; v0 += 32) {  // 32 vectors at a time
-      const int v = v0 + lane;
-      unsigned long long w[EPV], sum = 0;
-      unsigned tie = 0;  // bit e: element e equals the cut
-#pragma unroll
-      for (int e = 0; e < EPV; ++e) w[e] = 0;
-      if (v < s.wend) {
-        S::vec(s.get(v), [&](float x, int e) {
-          const int k = kind(x, s.index(v, e));
-          if (k == 2) w[e] = weight<TWO>(x, sc, sm.table);
-          if (k == 1) tie |= 1u << e;
-        });
-      }
-      const unsigned nt = __popc(tie);
-      unsigned ti = nt;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const unsigned x = __shfl_up_sync(0xffffffffu, ti, o);
-        if (lane >= o) ti += x;
-      }
-      unsigned t = trun + ti - nt;
-#pragma unroll
-      for (int e = 0; e < EPV; ++e) {
-        if (((tie >> e) & 1u) && t++ < stay) w[e] = wt;
-        sum += w[e];
-      }
-      unsigned long long wi = sum;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const unsigned long long x = shfl_up64(wi, o);
-        if (lane >= o) wi += x;
-      }
-      const unsigned hit = __ballot_sync(0xffffffffu, run + wi > target);
+  unsigned hit = __ballot_sync(0xffffffffu, run <= target && target < run + m);
+  if (hit && __ffs(hit) - 1 == rank) {
+    const unsigned long long cta_run = __shfl_sync(0xffffffffu, run, rank);
+    const unsigned cta_ties = __shfl_sync(0xffffffffu, ties, rank);
+    m = running(lane < kWarps ? sm.run_mass[lane] : 0ull, lane < kWarps ? sm.run_ties[lane] : 0u, cta_run, cta_ties, run, ties);
+    hit = __ballot_sync(0xffffffffu, run <= target && target < run + m);
+    if (hit && __ffs(hit) - 1 == warp) {
+      const unsigned long long warp_run = __shfl_sync(0xffffffffu, run, warp);
+      const unsigned warp_ties = __shfl_sync(0xffffffffu, ties, warp);
+      m = running(lane_mass, lane_ties, warp_run, warp_ties, run, ties);
+      hit = __ballot_sync(0xffffffffu, run <= target && target < run + m);
       if (hit) {
-        if (lane == __ffs(hit) - 1) {
-          unsigned long long at = run + wi - sum;
-          int tok = -1;
-#pragma unroll
-          for (int e = 0; e < EPV; ++e) {
-            at += w[e];
-            if (tok < 0 && at > target) tok = s.index(v, e);
+        // that lane's elements, 32 at a time
+        const int l = __ffs(hit) - 1;
+        unsigned long long r = __shfl_sync(0xffffffffu, run, l);
+        unsigned t = __shfl_sync(0xffffffffu, ties, l);
+        const int v0 = __shfl_sync(0xffffffffu, s.lbeg, l), v1 = __shfl_sync(0xffffffffu, s.lend, l);
+        for (int v = v0; v < v1; v += 32 / EPV) {
+          const int vv = v + lane / EPV, e = lane % EPV;
+          unsigned long long w = 0;
+          unsigned tie = 0;
+          if (vv < v1) {
+            const uint4 raw = s.get(vv);
+            float x = 0.f;
+            S::vec(raw, [&](float y, int j) {
+              if (j == e) x = y;
+            });
+            const int k = kind(x, vv, e);
+            if (k == 2) w = weight<TWO>(x, sc, sm.table);
+            tie = k == 1;
           }
-          a.tokens[n] = tok;
+          m = running(w, tie, r, t, run, ties);
+          hit = __ballot_sync(0xffffffffu, run <= target && target < run + m);
+          if (hit) {
+            if (lane == __ffs(hit) - 1) a.tokens[n] = s.index(vv, e);
+            break;
+          }
+          r = __shfl_sync(0xffffffffu, run + m, 31);
+          t = __shfl_sync(0xffffffffu, ties + tie, 31);
         }
-        break;
       }
-      run += __shfl_sync(0xffffffffu, wi, 31);
-      trun += __shfl_sync(0xffffffffu, ti, 31);
     }
   }
   cl.sync();  // no CTA leaves while others read it
@@ -717,7 +773,8 @@ cudaError_t launch_s(const SampleParams& a, int C, size_t smem, cudaStream_t str
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if (dev < 0 || dev >= kMaxDevices || !opted[dev].load(std::memory_order_acquire)) {
-    e = cudaFuncSetAttribute(sample_kernel<T, STAGED>, cudaFuncAttributeMaxDynamicSharedMemorySize, kStageMax);
+    e = cudaFuncSetAttribute(sample_kernel<T, STAGED>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             (int)sizeof(Smem) + kStageMax);
     if (e != cudaSuccess) return e;
     if (dev >= 0 && dev < kMaxDevices) opted[dev].store(true, std::memory_order_release);
   }
@@ -732,7 +789,7 @@ cudaError_t launch_s(const SampleParams& a, int C, size_t smem, cudaStream_t str
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)((long long)a.N * C));
   cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = smem;
+  cfg.dynamicSmemBytes = sizeof(Smem) + smem;
   cfg.stream = stream;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
@@ -750,7 +807,7 @@ cudaError_t launch_t(const SampleParams& a, cudaStream_t stream) {
   const int nvec = (a.V + EPV - 1) / EPV + 1;
   int C = 1;
   while (C < kMaxCluster && (nvec / C > 4 * kThreads || ((long long)a.N * C < 2 * sms && nvec / C > kThreads))) C *= 2;
-  const size_t bytes = 16 * (size_t)((nvec + C - 1) / C);
+  const size_t bytes = 16 * (size_t)(((nvec + C - 1) / C + 3) / 4 * 4);  // Slice::place permutes within four
   if (bytes <= (size_t)kStageMax) return launch_s<T, true>(a, C, bytes, stream);
   return launch_s<T, false>(a, C, 0, stream);
 }
