@@ -796,9 +796,12 @@ cudaError_t launch_s(const SampleParams& a, int C, size_t smem, cudaStream_t str
   return cudaLaunchKernelEx(&cfg, sample_kernel<T, STAGED>, a, table);
 }
 
-// CTAs per row: enough that a slice is at most four vectors a thread, and,
-// when rows are few, until the grid fills the GPU twice or a thread has less
-// than one vector.
+// CTAs per row: enough that a lane has at most eight vectors of a slice, and, when
+// rows are few, until the grid is about one resident wave (two CTAs per SM) or a
+// lane has less than one vector.  One wave, because a row's chain of meetings is
+// what a second wave would repeat: 64 rows of 128k bf16, top-p, take 73 us with 4
+// CTAs a row and 90 with 8; 256 rows of 32k fp16, unfiltered, 20 with 1 and 26
+// with 2.
 template <typename T>
 cudaError_t launch_t(const SampleParams& a, cudaStream_t stream) {
   constexpr int EPV = 16 / (int)sizeof(T);
@@ -806,7 +809,7 @@ cudaError_t launch_t(const SampleParams& a, cudaStream_t stream) {
   if (cudaGetDevice(&dev) == cudaSuccess) cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
   const int nvec = (a.V + EPV - 1) / EPV + 1;
   int C = 1;
-  while (C < kMaxCluster && (nvec / C > 4 * kThreads || ((long long)a.N * C < 2 * sms && nvec / C > kThreads))) C *= 2;
+  while (C < kMaxCluster && (nvec / C > 8 * kThreads || (2LL * a.N * C < 3 * sms && nvec / C > kThreads))) C *= 2;
   const size_t bytes = 16 * (size_t)(((nvec + C - 1) / C + 3) / 4 * 4);  // Slice::place permutes within four
   if (bytes <= (size_t)kStageMax) return launch_s<T, true>(a, C, bytes, stream);
   return launch_s<T, false>(a, C, 0, stream);
