@@ -13,18 +13,22 @@
 // as few steps as possible: each warp owns a page at a time, brings its 16 keys
 // and values into a ring of its own (cp.async, no barrier between warps), reads
 // them as fragments and converts in registers (one instruction for two codes;
-// every E4M3 value is exact in fp16).  Both products are m16n8k16 fp16 with
-// fp32 accumulators.
-//   S = Q K^T: any order of the D products is the same sum, so a lane takes 16
+// every E4M3 value is exact in fp16).  Both products are m16n8k16 fp16 with fp32
+// accumulators, with the cache on the 16-row side and the query rows on the
+// 8-column side, so that eight rows (a decoding step of eight heads a KV head)
+// waste nothing:
+//   S^T = K Q^T: any order of the D products is the same sum, so a lane takes 16
 //     consecutive bytes of a key row as four k-steps of four, and Q is held in
 //     the same order;
-//   O = P V:   a lane takes 8 or 16 consecutive columns of four value rows
-//     (n-tile t of column group n is column n * (D/8) + t), and a byte permute
-//     pairs two rows' codes before the conversion.
+//   O^T = V^T P^T: a lane takes 8 or 16 consecutive columns of four value rows
+//     (row i of tile t is column i * (D/8) + 2t, row i + 8 the one after), a byte
+//     permute pairs two rows' codes before the conversion, and P^T is S^T's
+//     fragment after an 8x8 transposition.
 // Queries are scaled to a power of two per row (exact; a bf16 query keeps all
-// its bits in fp16).  Softmax in base 2 with a lazily moved maximum; P carries
-// 2^3 * v_scale / v_ref, v_ref a running power-of-two reference, so that fp16
-// holds weights from 2^11 down to 2^-24 of it.
+// its bits in fp16).  Softmax in base 2; the maximum of a row moves only when a
+// score exceeds it by more than 8, which one vote per page finds, so the common
+// page has no reduction.  P carries 2^3 * v_scale / v_ref, v_ref a running
+// reference, so that fp16 holds weights from 2^11 down to 2^-24 of it.
 //
 // The batch's 64-slot tiles (four pages, one a warp) are dealt out evenly over
 // persistent CTAs (common.cuh's balanced schedule, its prefix computed by every
@@ -42,15 +46,16 @@ constexpr int kThreads = kWarps * 32;
 constexpr int kP = 16;
 constexpr int kMaxDevices = 64;
 
-// MT: 16-row tiles of query rows a CTA holds.
-template <int D, int MT>
+// NT: 8-row tiles of query rows a CTA holds.
+template <int D, int NT>
 struct Cfg {
-  static constexpr int CTAS = MT == 1 ? 3 : 2;  // per SM, by registers
-  static constexpr int DEPTH = MT == 1 ? 4 : 6;  // pages a warp keeps in flight
-  static constexpr int kPage = 16 * D;           // bytes of a page's K or V
+  static constexpr int ROWS = 8 * NT;
+  static constexpr int CTAS = NT == 1 ? 4 : NT == 2 ? 3 : 2;   // per SM, by registers
+  static constexpr int DEPTH = NT == 1 ? 3 : NT == 2 ? 4 : 6;  // pages a warp keeps in flight
+  static constexpr int kPage = 16 * D;                         // bytes of a page's K or V
   static constexpr int kRing = kWarps * DEPTH * 2 * kPage;
-  static constexpr int LDO = D + 4;              // merge rows, in floats
-  static constexpr int kMerge = kWarps * 16 * LDO * 4;
+  static constexpr int LDO = D + 4;                            // merge rows, in floats
+  static constexpr int kMerge = kWarps * 8 * LDO * 4;
   static constexpr int kSmem = kRing > kMerge ? kRing : kMerge;
 };
 
@@ -67,6 +72,13 @@ __device__ __forceinline__ void mma(float (&c)[4], const uint32_t (&a)[4], uint3
   asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// The 8x8 transposition of 16-bit values held two a lane, row i in lanes 4i .. 4i + 3.
+__device__ __forceinline__ uint32_t transpose8(uint32_t x) {
+  uint32_t r;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
+  return r;
 }
 
 __device__ __forceinline__ float fast_exp2(float x) {
@@ -94,26 +106,27 @@ __device__ __forceinline__ int v_off(int r, int ch) {
   return r * D + ((D == 128 ? ch ^ (((r >> 1) & 3) << 1) : ch ^ ((r >> 1) & 3)) << 4);
 }
 
-// One warp's running result for MT * 16 query rows.
-template <int D, int MT>
+// One warp's running result for NT * 8 query rows.  Lane (gid, tig) holds query
+// row gid of each tile as an operand, and rows 2 tig and 2 tig + 1 of the results.
+template <int D, int NT>
 struct State {
-  uint32_t q[MT][D / 16][4];
-  float o[MT][D / 8][4];
-  float m[MT][2], l[MT][2];  // rows gid and gid + 8 of each tile; l is this lane's part
-  float c[MT][2];            // score -> base-2 units, without the page's scale
-  float v_ref;
+  uint32_t q[NT][D / 16][2];
+  float o[NT][D / 16][4];
+  float m[NT][2], l[NT][2];  // l is this lane's part
+  float c[NT][2];            // score -> base-2 units, without the page's scale
+  float v_ref, inv_ref;
 
   __device__ __forceinline__ void clear() {
 #pragma unroll
-    for (int i = 0; i < MT; ++i) {
+    for (int i = 0; i < NT; ++i) {
 #pragma unroll
-      for (int t = 0; t < D / 8; ++t)
+      for (int t = 0; t < D / 16; ++t)
 #pragma unroll
         for (int e = 0; e < 4; ++e) o[i][t][e] = 0.f;
       m[i][0] = m[i][1] = -INFINITY;
       l[i][0] = l[i][1] = 0.f;
     }
-    v_ref = 0.f;
+    v_ref = inv_ref = 0.f;
   }
 };
 
@@ -122,82 +135,87 @@ struct State {
 enum : int { kSeeAll, kSeeLimit, kSeeMask };
 
 // Folds one page (codes in shared memory) into the running result.
-template <int D, int MT, int SEE>
-__device__ __forceinline__ void page_step(State<D, MT>& st, const uint8_t* kp, const uint8_t* vp, float ks, float vs,
-                                          int limit, const unsigned (&see)[MT][2]) {
+template <int D, int NT, int SEE>
+__device__ __forceinline__ void page_step(State<D, NT>& st, const uint8_t* kp, const uint8_t* vp, float ks, float vs,
+                                          int limit, const unsigned (&see)[NT][2]) {
   const int lane = threadIdx.x & 31, gid = lane >> 2, tig = lane & 3;
-  constexpr int CH = D / 64;  // 16-byte chunks of a key row per lane
-  float s[MT][2][4];
+  float s[NT][4];
 #pragma unroll
-  for (int j = 0; j < 2; ++j) {
+  for (int i = 0; i < NT; ++i)
 #pragma unroll
-    for (int i = 0; i < MT; ++i)
+    for (int e = 0; e < 4; ++e) s[i][e] = 0.f;
 #pragma unroll
-      for (int e = 0; e < 4; ++e) s[i][j][e] = 0.f;
+  for (int ch = 0; ch < D / 64; ++ch) {  // 16-byte chunks of a key row per lane
+    const uint4 w0 = *reinterpret_cast<const uint4*>(kp + k_off<D>(gid, ch * 4 + tig));
+    const uint4 w1 = *reinterpret_cast<const uint4*>(kp + k_off<D>(gid + 8, ch * 4 + tig));
+    const uint32_t x0[4] = {w0.x, w0.y, w0.z, w0.w}, x1[4] = {w1.x, w1.y, w1.z, w1.w};
 #pragma unroll
-    for (int ch = 0; ch < CH; ++ch) {
-      const uint4 w = *reinterpret_cast<const uint4*>(kp + k_off<D>(j * 8 + gid, ch * 4 + tig));
-      const uint32_t wv[4] = {w.x, w.y, w.z, w.w};
+    for (int x = 0; x < 4; ++x) {
+      const uint32_t a[4] = {e4m3x2_to_h2(x0[x] & 0xffffu), e4m3x2_to_h2(x1[x] & 0xffffu), e4m3x2_to_h2(x0[x] >> 16),
+                             e4m3x2_to_h2(x1[x] >> 16)};
 #pragma unroll
-      for (int x = 0; x < 4; ++x) {
-        const uint32_t b0 = e4m3x2_to_h2(wv[x] & 0xffffu), b1 = e4m3x2_to_h2(wv[x] >> 16);
-#pragma unroll
-        for (int i = 0; i < MT; ++i) mma(s[i][j], st.q[i][ch * 4 + x], b0, b1);
-      }
+      for (int i = 0; i < NT; ++i) mma(s[i], a, st.q[i][ch * 4 + x][0], st.q[i][ch * 4 + x][1]);
     }
   }
-  // this page's value scale against the reference, which moves when it is
-  // exceeded 16 times
-  const float vsc = fmaxf(vs, 1e-30f);
-  if (vsc > 16.f * st.v_ref) {
-    const float f = st.v_ref / vsc;
+  // scores in base-2 units; element e: row 2 tig + (e & 1), key gid + 8 (e >> 1)
+  bool over = false;
 #pragma unroll
-    for (int i = 0; i < MT; ++i)
+  for (int i = 0; i < NT; ++i) {
 #pragma unroll
-      for (int t = 0; t < D / 8; ++t)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) st.o[i][t][e] *= f;
-    st.v_ref = vsc;
-  }
-  const float pv = 8.f * vs / st.v_ref;
-  uint32_t pa[MT][4];
-#pragma unroll
-  for (int i = 0; i < MT; ++i) {
-#pragma unroll
-    for (int r = 0; r < 2; ++r) {  // rows gid, gid + 8
-      const float c = st.c[i][r] * ks;
-      float x[4] = {s[i][0][2 * r], s[i][0][2 * r + 1], s[i][1][2 * r], s[i][1][2 * r + 1]};
+    for (int e = 0; e < 4; ++e) {
+      s[i][e] *= st.c[i][e & 1] * ks;
       if (SEE != kSeeAll) {
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int key = (e >> 1) * 8 + 2 * tig + (e & 1);
-          const bool ok = SEE == kSeeLimit ? key < limit : ((see[i][r] >> key) & 1u);
-          x[e] = ok ? x[e] * c : -INFINITY;
-        }
-      } else {
-#pragma unroll
-        for (int e = 0; e < 4; ++e) x[e] *= c;
+        const int key = gid + 8 * (e >> 1);
+        if (!(SEE == kSeeLimit ? key < limit : ((see[i][e & 1] >> key) & 1u))) s[i][e] = -INFINITY;
       }
-      float mx = fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3]));
-      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-      if (mx > st.m[i][r] + 8.f) {  // O moves only when the maximum grows by more than 2^8
-        const float f = fast_exp2(st.m[i][r] - mx);  // 0 from -inf
-        st.l[i][r] *= f;
-#pragma unroll
-        for (int t = 0; t < D / 8; ++t) {
-          st.o[i][t][2 * r] *= f;
-          st.o[i][t][2 * r + 1] *= f;
-        }
-        st.m[i][r] = mx;
-      }
-      const float nm = st.m[i][r] == -INFINITY ? 0.f : -st.m[i][r];
-#pragma unroll
-      for (int e = 0; e < 4; ++e) x[e] = fast_exp2(x[e] + nm);
-      st.l[i][r] += (x[0] + x[1]) + (x[2] + x[3]);
-      pa[i][r] = pack_h2(x[0] * pv, x[1] * pv);
-      pa[i][2 + r] = pack_h2(x[2] * pv, x[3] * pv);
+      over = over || s[i][e] > st.m[i][e & 1] + 8.f;
     }
+  }
+  const float vsc = fmaxf(vs, 1e-30f);
+  if (__any_sync(0xffffffffu, over || vsc > 16.f * st.v_ref)) {
+    // a maximum grows by more than 2^8, or the page's value scale exceeds the
+    // reference 16 times: O moves
+    float fv = 1.f;
+    if (vsc > 16.f * st.v_ref) {
+      fv = st.v_ref / vsc;
+      st.v_ref = vsc;
+      st.inv_ref = 1.f / vsc;
+    }
+#pragma unroll
+    for (int i = 0; i < NT; ++i) {
+      float f[2];
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        float mx = fmaxf(s[i][r], s[i][2 + r]);
+#pragma unroll
+        for (int o = 4; o < 32; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+        f[r] = 1.f;
+        if (mx > st.m[i][r] + 8.f) {
+          f[r] = fast_exp2(st.m[i][r] - mx);  // 0 from -inf
+          st.l[i][r] *= f[r];
+          st.m[i][r] = mx;
+        }
+        f[r] *= fv;
+      }
+#pragma unroll
+      for (int t = 0; t < D / 16; ++t)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) st.o[i][t][e] *= f[e & 1];
+    }
+  }
+  const float pv = 8.f * vs * st.inv_ref;
+  uint32_t pb[NT][2];
+#pragma unroll
+  for (int i = 0; i < NT; ++i) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const float m = st.m[i][e & 1];
+      s[i][e] = fast_exp2(s[i][e] - (m == -INFINITY ? 0.f : m));
+    }
+    st.l[i][0] += s[i][0] + s[i][2];
+    st.l[i][1] += s[i][1] + s[i][3];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) pb[i][h] = transpose8(pack_h2(s[i][2 * h] * pv, s[i][2 * h + 1] * pv));
   }
   // values: rows 2 tig, 2 tig + 1, 2 tig + 8, 2 tig + 9, columns gid * D/8 ...
   constexpr int NW = D / 32;  // 4-byte words of a row per lane
@@ -224,12 +242,10 @@ __device__ __forceinline__ void page_step(State<D, MT>& st, const uint8_t* kp, c
       // bytes 2h and 2h + 1 of both rows, paired by byte
       const uint32_t sel = h ? 0x7362 : 0x5140;
       const uint32_t p0 = __byte_perm(v[0][w], v[1][w], sel), p1 = __byte_perm(v[2][w], v[3][w], sel);
+      const uint32_t a[4] = {e4m3x2_to_h2(p0 & 0xffffu), e4m3x2_to_h2(p0 >> 16), e4m3x2_to_h2(p1 & 0xffffu),
+                             e4m3x2_to_h2(p1 >> 16)};
 #pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        const uint32_t b0 = e4m3x2_to_h2(k ? p0 >> 16 : p0 & 0xffffu), b1 = e4m3x2_to_h2(k ? p1 >> 16 : p1 & 0xffffu);
-#pragma unroll
-        for (int i = 0; i < MT; ++i) mma(st.o[i][w * 4 + h * 2 + k], pa[i], b0, b1);
-      }
+      for (int i = 0; i < NT; ++i) mma(st.o[i][2 * w + h], a, pb[i][0], pb[i][1]);
     }
   }
 }
@@ -282,10 +298,10 @@ __device__ __forceinline__ float quantise_new(const T* src, size_t row_stride, i
   return scale;
 }
 
-template <typename T, int D, int MT>
-__global__ void __launch_bounds__(kThreads, Cfg<D, MT>::CTAS) attn_block8_kernel(const Block8Params p) {
-  using C = Cfg<D, MT>;
-  constexpr int RG = 16 * MT;
+template <typename T, int D, int NT>
+__global__ void __launch_bounds__(kThreads, Cfg<D, NT>::CTAS) attn_block8_kernel(const Block8Params p) {
+  using C = Cfg<D, NT>;
+  constexpr int RG = C::ROWS;
   extern __shared__ __align__(128) uint8_t smem[];
   int* s_pfx = reinterpret_cast<int*>(smem + C::kSmem);  // [B + 1]
   __shared__ int s_warp[kWarps];
@@ -375,52 +391,47 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, MT>::CTAS) attn_block8_kernel
 #pragma unroll
     for (int i = 0; i < C::DEPTH - 1; ++i) issue(i);
 
-    // queries: this lane's columns of rows gid and gid + 8, scaled to fp16
-    State<D, MT> st;
+    // queries: this lane's columns of row gid of each tile, scaled to fp16
+    State<D, NT> st;
     st.clear();
 #pragma unroll
-    for (int i = 0; i < MT; ++i) {
+    for (int i = 0; i < NT; ++i) {
+      const int row = row0 + i * 8 + gid;
+      Row8<T> raw[D / 32];
 #pragma unroll
-      for (int r = 0; r < 2; ++r) {
-        const int row = row0 + i * 16 + r * 8 + gid;
-        Row8<T> raw[D / 32];
+      for (int x = 0; x < D / 32; ++x) raw[x].zero();
+      if (row < a.rows) {
+        const int node = row / a.g, h = kvh * a.g + row % a.g;
+        const T* q = static_cast<const T*>(a.q_rot) + (((size_t)b * a.T + node) * a.Hq + h) * D + tig * 16;
 #pragma unroll
-        for (int x = 0; x < D / 32; ++x) raw[x].zero();
-        if (row < a.rows) {
-          const int node = row / a.g, h = kvh * a.g + row % a.g;
-          const T* q = static_cast<const T*>(a.q_rot) + (((size_t)b * a.T + node) * a.Hq + h) * D + tig * 16;
+        for (int x = 0; x < D / 32; ++x) raw[x].load(q + (x / 2) * 64 + (x % 2) * 8);
+      }
+      AbsMax<T> top;
 #pragma unroll
-          for (int x = 0; x < D / 32; ++x) raw[x].load(q + (x / 2) * 64 + (x % 2) * 8);
-        }
-        float amax = 0.f;
+      for (int x = 0; x < D / 32; ++x) top.add(raw[x]);
+      float amax = top.get();
+      amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+      amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+      // 2^8 <= scaled maximum < 2^9: elements down to 2^-33 of it keep their bits
+      const int ex = amax > 0.f ? (int)(__float_as_uint(amax) >> 23) - 127 : 0;
+      const int k = min(max(8 - ex, -120), 120);
+      const float f2 = __uint_as_float((uint32_t)(127 + k) << 23);
+      const float c = a.scale_log2 * __uint_as_float((uint32_t)(127 - k) << 23);
+      st.c[i][0] = __shfl_sync(0xffffffffu, c, 8 * tig);  // rows 2 tig and 2 tig + 1
+      st.c[i][1] = __shfl_sync(0xffffffffu, c, 8 * tig + 4);
 #pragma unroll
-        for (int x = 0; x < D / 32; ++x) {
-          float f[8];
-          raw[x].to_f(f);
+      for (int x = 0; x < D / 32; ++x) {
+        float f[8];
+        raw[x].to_f(f);
 #pragma unroll
-          for (int e = 0; e < 8; ++e) amax = fmaxf(amax, fabsf(f[e]));
-        }
-        amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
-        amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
-        // 2^8 <= scaled maximum < 2^9: elements down to 2^-33 of it keep their bits
-        const int ex = amax > 0.f ? (int)(__float_as_uint(amax) >> 23) - 127 : 0;
-        const int k = min(max(8 - ex, -120), 120);
-        const float f2 = __uint_as_float((uint32_t)(127 + k) << 23);
-        st.c[i][r] = a.scale_log2 * __uint_as_float((uint32_t)(127 - k) << 23);
-#pragma unroll
-        for (int x = 0; x < D / 32; ++x) {
-          float f[8];
-          raw[x].to_f(f);
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {  // four columns: k-step 2x + e
-            st.q[i][2 * x + e][r] = pack_h2(f[4 * e] * f2, f[4 * e + 1] * f2);
-            st.q[i][2 * x + e][2 + r] = pack_h2(f[4 * e + 2] * f2, f[4 * e + 3] * f2);
-          }
+        for (int e = 0; e < 2; ++e) {  // four columns: k-step 2x + e
+          st.q[i][2 * x + e][0] = pack_h2(f[4 * e] * f2, f[4 * e + 1] * f2);
+          st.q[i][2 * x + e][1] = pack_h2(f[4 * e + 2] * f2, f[4 * e + 3] * f2);
         }
       }
     }
 
-    const unsigned none[MT][2] = {};
+    const unsigned none[NT][2] = {};
     for (int i = 0; i < npages; ++i) {
       const int at = i & 31;
       if (at == 0) {
@@ -442,14 +453,14 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, MT>::CTAS) attn_block8_kernel
       const float ks = __shfl_sync(0xffffffffu, ks_cur, at), vs = __shfl_sync(0xffffffffu, vs_cur, at);
       const int limit = L - (first + 4 * i) * kP;
       if (limit >= kP) {
-        page_step<D, MT, kSeeAll>(st, kp, vp, ks, vs, kP, none);
+        page_step<D, NT, kSeeAll>(st, kp, vp, ks, vs, kP, none);
       } else {
         // the sequence ends in this page: rows past it may hold anything, NaN
         // codes too; their weights are 0 and their values are made 0
         for (int e = lane; e < (kP - limit) * (D / 16); e += 32)
           *reinterpret_cast<uint4*>(vp + limit * D + e * 16) = make_uint4(0, 0, 0, 0);
         __syncwarp();
-        page_step<D, MT, kSeeLimit>(st, kp, vp, ks, vs, limit, none);
+        page_step<D, NT, kSeeLimit>(st, kp, vp, ks, vs, limit, none);
       }
       __syncwarp();  // every lane has read the slot before it is filled again
     }
@@ -466,50 +477,46 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, MT>::CTAS) attn_block8_kernel
       const float ks = quantise_new<T, D, true>(static_cast<const T*>(p.k_new) + src, rs, rows, ring);
       const float vs = quantise_new<T, D, false>(static_cast<const T*>(p.v_new) + src, rs, rows, ring + C::kPage);
       __syncwarp();
-      unsigned see[MT][2];
+      unsigned see[NT][2];
 #pragma unroll
-      for (int i = 0; i < MT; ++i)
+      for (int i = 0; i < NT; ++i)
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
-          const int row = row0 + i * 16 + r * 8 + gid;
+          const int row = row0 + i * 8 + 2 * tig + r;
           see[i][r] = row < a.rows ? (unsigned)(s_anc[row / a.g] >> (pn * kP)) & 0xffffu : 0u;
         }
-      page_step<D, MT, kSeeMask>(st, ring, ring + C::kPage, ks, vs, kP, see);
+      page_step<D, NT, kSeeMask>(st, ring, ring + C::kPage, ks, vs, kP, see);
     }
 
     // ---- join the four warps and write the piece ----
 #pragma unroll
-    for (int i = 0; i < MT; ++i)
+    for (int i = 0; i < NT; ++i)
 #pragma unroll
       for (int r = 0; r < 2; ++r) {
         float l = st.l[i][r];
-        l += __shfl_xor_sync(0xffffffffu, l, 1);
-        l += __shfl_xor_sync(0xffffffffu, l, 2);
-        if (tig == 0) {
-          s_m[warp][i * 16 + r * 8 + gid] = st.m[i][r];
-          s_l[warp][i * 16 + r * 8 + gid] = l;
+#pragma unroll
+        for (int o = 4; o < 32; o <<= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+        if (gid == 0) {
+          s_m[warp][i * 8 + 2 * tig + r] = st.m[i][r];
+          s_l[warp][i * 8 + 2 * tig + r] = l;
         }
       }
     if (lane == 0) s_ref[warp] = st.v_ref * 0.125f;
-    float* s_o = reinterpret_cast<float*>(smem);  // [warp][16][LDO]
+    float* s_o = reinterpret_cast<float*>(smem);  // [warp][8][LDO]
 #pragma unroll
-    for (int i = 0; i < MT; ++i) {
+    for (int i = 0; i < NT; ++i) {
       __syncthreads();  // rings (or the previous tile's rows) are no longer read
-      constexpr int NT = D / 8;
 #pragma unroll
       for (int r = 0; r < 2; ++r) {
-        float* o = s_o + (warp * 16 + r * 8 + gid) * C::LDO + tig * 2 * NT;
+        float* o = s_o + (warp * 8 + 2 * tig + r) * C::LDO + gid * (D / 8);
 #pragma unroll
-        for (int h = 0; h < 2; ++h)
-#pragma unroll
-          for (int t = 0; t < NT; t += 4)
-            *reinterpret_cast<float4*>(o + h * NT + t) =
-                make_float4(st.o[i][t][2 * r + h], st.o[i][t + 1][2 * r + h], st.o[i][t + 2][2 * r + h],
-                            st.o[i][t + 3][2 * r + h]);
+        for (int t = 0; t < D / 16; t += 2)
+          *reinterpret_cast<float4*>(o + 2 * t) =
+              make_float4(st.o[i][t][r], st.o[i][t][2 + r], st.o[i][t + 1][r], st.o[i][t + 1][2 + r]);
       }
       __syncthreads();
-      const int rr = tid >> 3, rg_row = i * 16 + rr, row = row0 + rg_row;
-      if (row < a.rows) {
+      const int rr = tid >> 4, rg_row = i * 8 + rr, row = row0 + rg_row;  // 16 threads a row
+      if (row < a.rows && (tid & 15) < D / 8) {
         float M = -INFINITY, f[kWarps], l = 0.f;
 #pragma unroll
         for (int w = 0; w < kWarps; ++w) M = fmaxf(M, s_m[w][rg_row]);
@@ -520,46 +527,43 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, MT>::CTAS) attn_block8_kernel
           f[w] = e * s_ref[w];
         }
         const float inv = l > 0.f ? 1.f / l : 0.f;
+        const int c8 = tid & 15;
+        float acc[8] = {};
 #pragma unroll
-        for (int e8 = 0; e8 < D / 64; ++e8) {
-          const int c8 = (tid & 7) * (D / 64) + e8;
-          float acc[8] = {};
-#pragma unroll
-          for (int w = 0; w < kWarps; ++w) {
-            const float4* o = reinterpret_cast<const float4*>(s_o + (w * 16 + rr) * C::LDO + c8 * 8);
-            const float4 x = o[0], y = o[1];
-            acc[0] += f[w] * x.x;
-            acc[1] += f[w] * x.y;
-            acc[2] += f[w] * x.z;
-            acc[3] += f[w] * x.w;
-            acc[4] += f[w] * y.x;
-            acc[5] += f[w] * y.y;
-            acc[6] += f[w] * y.z;
-            acc[7] += f[w] * y.w;
-          }
-#pragma unroll
-          for (int e = 0; e < 8; ++e) acc[e] *= inv;
-          Row8<T> v;
-          v.from_f(acc);
-          T* dst;
-          if (pc.slot < 0) {
-            const int node = row / a.g, h = kvh * a.g + row % a.g;
-            dst = static_cast<T*>(a.out) + (((size_t)b * a.T + node) * a.Hq + h) * D + c8 * 8;
-          } else {
-            dst = static_cast<T*>(a.part_o) + (((size_t)pc.slot * (D / 8) + c8) * a.part_rows + rg_row) * 8;
-          }
-          v.store(dst);
+        for (int w = 0; w < kWarps; ++w) {
+          const float4* o = reinterpret_cast<const float4*>(s_o + (w * 8 + rr) * C::LDO + c8 * 8);
+          const float4 x = o[0], y = o[1];
+          acc[0] += f[w] * x.x;
+          acc[1] += f[w] * x.y;
+          acc[2] += f[w] * x.z;
+          acc[3] += f[w] * x.w;
+          acc[4] += f[w] * y.x;
+          acc[5] += f[w] * y.y;
+          acc[6] += f[w] * y.z;
+          acc[7] += f[w] * y.w;
         }
-        if (pc.slot >= 0 && (tid & 7) == 0) a.part_ml[(size_t)pc.slot * a.part_rows + rg_row] = make_float2(M, l);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) acc[e] *= inv;
+        Row8<T> v;
+        v.from_f(acc);
+        T* dst;
+        if (pc.slot < 0) {
+          const int node = row / a.g, h = kvh * a.g + row % a.g;
+          dst = static_cast<T*>(a.out) + (((size_t)b * a.T + node) * a.Hq + h) * D + c8 * 8;
+        } else {
+          dst = static_cast<T*>(a.part_o) + (((size_t)pc.slot * (D / 8) + c8) * a.part_rows + rg_row) * 8;
+        }
+        v.store(dst);
+        if (pc.slot >= 0 && c8 == 0) a.part_ml[(size_t)pc.slot * a.part_rows + rg_row] = make_float2(M, l);
       }
     }
     __syncthreads();  // the rings are filled again by the next piece
   }
 }
 
-template <typename T, int D, int MT>
+template <typename T, int D, int NT>
 cudaError_t launch_t(const Block8Params& p, cudaStream_t stream) {
-  using C = Cfg<D, MT>;
+  using C = Cfg<D, NT>;
   const size_t smem = (size_t)C::kSmem + sizeof(int) * (size_t)(p.a.B + 1);
   static std::atomic<bool> opted[kMaxDevices];
   int dev = 0;
@@ -567,19 +571,26 @@ cudaError_t launch_t(const Block8Params& p, cudaStream_t stream) {
   if (e != cudaSuccess) return e;
   if (dev < 0 || dev >= kMaxDevices || !opted[dev].load(std::memory_order_acquire)) {
     // the largest batch's prefix included
-    e = cudaFuncSetAttribute(attn_block8_kernel<T, D, MT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    e = cudaFuncSetAttribute(attn_block8_kernel<T, D, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              C::kSmem + 4 * (8192 + 1));
     if (e != cudaSuccess) return e;
     if (dev >= 0 && dev < kMaxDevices) opted[dev].store(true, std::memory_order_release);
   }
-  return launch_pdl(attn_block8_kernel<T, D, MT>, dim3(p.a.sched.G), dim3(kThreads), smem, stream, p);
+  return launch_pdl(attn_block8_kernel<T, D, NT>, dim3(p.a.sched.G), dim3(kThreads), smem, stream, p);
+}
+
+template <typename T, int D>
+cudaError_t launch_n(const Block8Params& p, cudaStream_t stream) {
+  switch (p.a.rows_per_group) {
+    case 8: return launch_t<T, D, 1>(p, stream);
+    case 16: return launch_t<T, D, 2>(p, stream);
+    default: return launch_t<T, D, 4>(p, stream);
+  }
 }
 
 template <typename T>
 cudaError_t launch_d(const Block8Params& p, cudaStream_t stream) {
-  const bool one = p.a.rows_per_group == 16;
-  if (p.a.D == 64) return one ? launch_t<T, 64, 1>(p, stream) : launch_t<T, 64, 2>(p, stream);
-  return one ? launch_t<T, 128, 1>(p, stream) : launch_t<T, 128, 2>(p, stream);
+  return p.a.D == 64 ? launch_n<T, 64>(p, stream) : launch_n<T, 128>(p, stream);
 }
 
 }  // namespace
@@ -589,8 +600,9 @@ Block8Plan block8_plan(int rows, int g, int dtype) {
     const int parts = dtype == 1 ? 3 : 2;
     return Block8Plan{true, parts == 2 && rows > 128 ? 256 : 128, 1, 4, parts};
   }
-  if (rows <= 16) return Block8Plan{false, 16, Cfg<128, 1>::CTAS, 2, 0};
-  return Block8Plan{false, 32, Cfg<128, 2>::CTAS, 2, 0};
+  if (rows <= 8) return Block8Plan{false, 8, Cfg<128, 1>::CTAS, 2, 0};
+  if (rows <= 16) return Block8Plan{false, 16, Cfg<128, 2>::CTAS, 2, 0};
+  return Block8Plan{false, 32, Cfg<128, 4>::CTAS, 2, 0};
 }
 
 cudaError_t launch_attn_block8(const Block8Params& p, int dtype, cudaStream_t stream) {
