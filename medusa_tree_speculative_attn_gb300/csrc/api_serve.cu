@@ -44,7 +44,7 @@ int check_block8(const mt_attn_desc* d) {
 }
 
 struct Block8Ws {
-  size_t pfx, ml, o, anc, pieces, q8, q_scale, k_blocks, v_blocks, block_scales, total;
+  size_t ml, o, counters, pfx, anc, pieces, q8, q_scale, k_blocks, v_blocks, block_scales, total;
   int rows, nrg, part_rows, G;
   Block8Plan plan;
 };
@@ -57,26 +57,33 @@ int block8_ws(const mt_attn_desc* d, Block8Ws* w) {
   const long long rows = (long long)d->tree_size * (d->num_q_heads / d->num_kv_heads);
   if (rows > (1 << 20)) return MT_ERR_UNSUPPORTED;
   w->rows = (int)rows;
-  w->plan = block8_plan(w->rows, d->num_q_heads / d->num_kv_heads, d->dtype);
-  w->nrg = (w->rows + w->plan.rows_per_group - 1) / w->plan.rows_per_group;
+  w->plan = block8_plan(d->batch, d->num_kv_heads, w->rows, d->num_q_heads / d->num_kv_heads, d->max_blocks_per_seq,
+                        d->tree_size, d->dtype, sms);
+  w->nrg = w->plan.nrg;
   w->part_rows = w->rows < w->plan.rows_per_group ? w->rows : w->plan.rows_per_group;
-  w->G = sms * w->plan.ctas_per_sm;
+  w->G = w->plan.ctas;
+  if (!w->plan.tc && w->G > kMaxFragCtas) return MT_ERR_UNSUPPORTED;
   const long long nslots = (long long)d->batch * d->num_kv_heads * w->nrg + w->G;
   if (nslots > (1ll << 30)) return MT_ERR_INVALID_ARG;
-  w->pfx = kAlign;
-  w->ml = align_up(w->pfx + sizeof(int) * (size_t)(d->batch + 1));
-  w->o = align_up(w->ml + sizeof(float2) * (size_t)nslots * w->part_rows);
-  w->total = align_up(w->o + (size_t)2 * nslots * w->part_rows * d->head_dim);
-  if (w->plan.tc) {
+  size_t off = kAlign;  // status word and padding
+  auto take = [&](size_t bytes) {
+    const size_t at = off;
+    off = align_up(off + bytes);
+    return at;
+  };
+  // the one part that has to be zero between calls comes first, at the same place
+  // for every descriptor, so that a workspace serves any that it is large enough for
+  w->counters = take(kMaxFragCtas * sizeof(unsigned));
+  const size_t part = (size_t)nslots * w->part_rows;
+  w->ml = take(part * sizeof(float2));
+  if (!w->plan.tc) {
+    w->o = take(part * d->head_dim * sizeof(float));
+  } else {
     const size_t nodes = (size_t)d->batch * d->tree_size, qrows = nodes * d->num_q_heads;
     const size_t blocks = (size_t)d->batch * d->num_kv_heads * ((d->tree_size + 15) / 16);
     if ((long long)blocks * 16 >= (1ll << 31)) return MT_ERR_UNSUPPORTED;
-    size_t off = w->total;
-    auto take = [&](size_t bytes) {
-      const size_t at = off;
-      off = align_up(off + bytes);
-      return at;
-    };
+    w->o = take(part * d->head_dim * 2);
+    w->pfx = take(sizeof(int) * (size_t)(d->batch + 1));
     w->anc = take(nodes * sizeof(unsigned long long));
     w->pieces = take(sizeof(int) * (size_t)piece_rec_offset(w->G) + sizeof(PieceRec) * kMaxPieceRecs * (size_t)w->G);
     w->q8 = take(qrows * d->head_dim * w->plan.parts);
@@ -84,8 +91,8 @@ int block8_ws(const mt_attn_desc* d, Block8Ws* w) {
     w->k_blocks = take(blocks * 16 * d->head_dim);
     w->v_blocks = take(blocks * 16 * d->head_dim);
     w->block_scales = take(2 * blocks * sizeof(float));
-    w->total = off;
   }
+  w->total = off;
   return MT_OK;
 }
 
@@ -236,30 +243,31 @@ int mt_tree_attn_paged_block8(const mt_attn_desc* d, const void* q, const void* 
   a.q_rot = q; a.k_cache = k_cache; a.v_cache = v_cache;
   a.block_tables = block_tables; a.seq_lens = seq_lens;
   a.out = out; a.status = reinterpret_cast<int*>(ws);
-  a.part_o = ws + w.o;
   a.part_ml = reinterpret_cast<float2*>(ws + w.ml);
   a.sched.B = d->batch; a.sched.T = d->tree_size; a.sched.Hkv = d->num_kv_heads;
   a.sched.nrg = w.nrg; a.sched.G = w.G; a.sched.splits = 0; a.sched.seg_cost = w.plan.seg_cost;
-  p.tile_pfx = reinterpret_cast<int*>(ws + w.pfx);
-  a.sched.tile_pfx = p.tile_pfx;
   p.k_scales = k_scales; p.v_scales = v_scales;
   p.k_new = k_new; p.v_new = v_new; p.parents = tree_parents;
-  if (w.plan.tc) {
-    p.parts = w.plan.parts;
-    p.q8 = reinterpret_cast<uint8_t*>(ws + w.q8);
-    p.q_scale = reinterpret_cast<float*>(ws + w.q_scale);
-    p.k_blocks = reinterpret_cast<uint8_t*>(ws + w.k_blocks);
-    p.v_blocks = reinterpret_cast<uint8_t*>(ws + w.v_blocks);
-    p.k_block_scales = reinterpret_cast<float*>(ws + w.block_scales);
-    p.v_block_scales = p.k_block_scales + (size_t)d->batch * d->num_kv_heads * ((d->tree_size + 15) / 16);
-    p.anc = reinterpret_cast<unsigned long long*>(ws + w.anc);
-    p.pieces = reinterpret_cast<int*>(ws + w.pieces);
-    wait_bound(&a.wait_limit_ns, &a.test_stall);
-    st = cuda_status(launch_block8_prep(p, d->dtype, stream));
-    if (st == MT_OK) st = cuda_status(launch_attn_block8_tc(p, d->dtype, stream));
-  } else {
-    st = cuda_status(launch_attn_block8(p, d->dtype, stream));
+  if (!w.plan.tc) {
+    p.frag_o = reinterpret_cast<float*>(ws + w.o);
+    p.frag_tiles = reinterpret_cast<unsigned*>(ws + w.counters);
+    return cuda_status(launch_attn_block8(p, d->dtype, stream));
   }
+  a.part_o = ws + w.o;
+  p.tile_pfx = reinterpret_cast<int*>(ws + w.pfx);
+  a.sched.tile_pfx = p.tile_pfx;
+  p.parts = w.plan.parts;
+  p.q8 = reinterpret_cast<uint8_t*>(ws + w.q8);
+  p.q_scale = reinterpret_cast<float*>(ws + w.q_scale);
+  p.k_blocks = reinterpret_cast<uint8_t*>(ws + w.k_blocks);
+  p.v_blocks = reinterpret_cast<uint8_t*>(ws + w.v_blocks);
+  p.k_block_scales = reinterpret_cast<float*>(ws + w.block_scales);
+  p.v_block_scales = p.k_block_scales + (size_t)d->batch * d->num_kv_heads * ((d->tree_size + 15) / 16);
+  p.anc = reinterpret_cast<unsigned long long*>(ws + w.anc);
+  p.pieces = reinterpret_cast<int*>(ws + w.pieces);
+  wait_bound(&a.wait_limit_ns, &a.test_stall);
+  st = cuda_status(launch_block8_prep(p, d->dtype, stream));
+  if (st == MT_OK) st = cuda_status(launch_attn_block8_tc(p, d->dtype, stream));
   if (st != MT_OK) return st;
   return cuda_status(launch_combine(a, d->dtype, stream));
 }

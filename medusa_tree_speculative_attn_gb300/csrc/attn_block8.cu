@@ -32,8 +32,11 @@
 //
 // The batch's 64-slot tiles (four pages, one a warp) are dealt out evenly over
 // persistent CTAs (common.cuh's balanced schedule, its prefix computed by every
-// CTA from the lengths); pieces of a split segment are joined by the combine.
+// CTA from the lengths).  A split segment's pieces leave O / l in fp32 with their
+// maximum and sum; the one that completes the segment's tile count merges them, so
+// a call is one launch.
 #include <atomic>
+#include <cmath>
 
 #include "serve.cuh"
 
@@ -92,6 +95,14 @@ __device__ __forceinline__ uint32_t pack_h2(float a, float b) {
   uint32_t r;
   memcpy(&r, &h, 4);
   return r;
+}
+
+// Adds to a segment's tile count and returns the count before: acquire-release at
+// GPU scope, so that the piece that completes it sees what the others wrote.
+__device__ __forceinline__ unsigned count_tiles(unsigned* counter, unsigned n) {
+  unsigned old;
+  asm volatile("atom.acq_rel.gpu.global.add.u32 %0, [%1], %2;" : "=r"(old) : "l"(counter), "r"(n) : "memory");
+  return old;
 }
 
 // Byte offset of 16-byte chunk ch of row r in a page's K or V: chunks are
@@ -308,6 +319,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::CTAS) attn_block8_kernel
   __shared__ int s_par[kMaxTree];
   __shared__ unsigned long long s_anc[kMaxTree];
   __shared__ float s_m[kWarps][RG], s_l[kWarps][RG], s_ref[kWarps];
+  __shared__ int s_last;
   const AttnParams& a = p.a;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, gid = lane >> 2, tig = lane & 3;
   const int nnew = (a.T + kP - 1) / kP;
@@ -315,19 +327,26 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::CTAS) attn_block8_kernel
 
   // every CTA: tiles of each sequence and their prefix
   block8_prefix<kWarps>(a, s_pfx, s_warp, blockIdx.x == 0);
-  if (blockIdx.x == 0)
-    for (int b = tid; b <= a.B; b += kThreads) p.tile_pfx[b] = s_pfx[b];
-  Sched sc = a.sched;
-  sc.tile_pfx = s_pfx;
-  PieceIter it;
-  it.init(sc, blockIdx.x);
-  Piece pc;
+  // one thread walks the pieces: its cursor and the schedule's 64-bit arithmetic
+  // stay out of everybody's registers
+  __shared__ PieceIter s_it;
+  __shared__ Piece s_piece;
+  __shared__ int s_more;
+  if (tid == 0) {
+    Sched sc = a.sched;
+    sc.tile_pfx = s_pfx;
+    s_it.init(sc, blockIdx.x);
+  }
   uint8_t* ring = smem + warp * (C::DEPTH * 2 * C::kPage);
   const uint32_t ring_u = static_cast<uint32_t>(__cvta_generic_to_shared(ring));
   const uint8_t* kc = static_cast<const uint8_t*>(a.k_cache);
   const uint8_t* vc = static_cast<const uint8_t*>(a.v_cache);
 
-  while (it.next(pc)) {
+  while (true) {
+    if (tid == 0) s_more = s_it.next(s_piece);
+    __syncthreads();
+    if (!s_more) break;
+    const Piece pc = s_piece;
     const int b = pc.b, kvh = pc.kvh;
     const int L = a.seq_lens[b];
     const int npre = (L + kP - 1) / kP;
@@ -503,6 +522,44 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::CTAS) attn_block8_kernel
       }
     if (lane == 0) s_ref[warp] = st.v_ref * 0.125f;
     float* s_o = reinterpret_cast<float*>(smem);  // [warp][8][LDO]
+    // Rows 8i .. 8i + 7 from the four warps' parts in s_m, s_l, s_o and s_ref: to
+    // the output, or to the piece's slot.
+    auto join = [&](int i, int slot) {
+      const int rr = tid >> 4, rg_row = i * 8 + rr, row = row0 + rg_row, c8 = tid & 15;  // 16 threads a row
+      if (row >= a.rows || c8 >= D / 8) return;
+      float M = -INFINITY, f[kWarps], l = 0.f;
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) M = fmaxf(M, s_m[w][rg_row]);
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) {
+        const float e = s_m[w][rg_row] == -INFINITY ? 0.f : fast_exp2(s_m[w][rg_row] - M);
+        l += e * s_l[w][rg_row];
+        f[w] = e * s_ref[w];
+      }
+      const float inv = l > 0.f ? 1.f / l : 0.f;
+      float acc[8] = {};
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) {
+        const float4* o = reinterpret_cast<const float4*>(s_o + (w * 8 + rr) * C::LDO + c8 * 8);
+        const float4 x = o[0], y = o[1];
+        const float v[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
+#pragma unroll
+        for (int e = 0; e < 8; ++e) acc[e] = fmaf(f[w], v[e], acc[e]);
+      }
+#pragma unroll
+      for (int e = 0; e < 8; ++e) acc[e] *= inv;
+      if (slot < 0) {
+        Row8<T> v;
+        v.from_f(acc);
+        const int node = row / a.g, h = kvh * a.g + row % a.g;
+        v.store(static_cast<T*>(a.out) + (((size_t)b * a.T + node) * a.Hq + h) * D + c8 * 8);
+      } else {
+        float4* d = reinterpret_cast<float4*>(p.frag_o + ((size_t)slot * a.part_rows + rg_row) * D + c8 * 8);
+        d[0] = make_float4(acc[0], acc[1], acc[2], acc[3]);
+        d[1] = make_float4(acc[4], acc[5], acc[6], acc[7]);
+        if (c8 == 0) a.part_ml[(size_t)slot * a.part_rows + rg_row] = make_float2(M, l);
+      }
+    };
 #pragma unroll
     for (int i = 0; i < NT; ++i) {
       __syncthreads();  // rings (or the previous tile's rows) are no longer read
@@ -515,46 +572,89 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::CTAS) attn_block8_kernel
               make_float4(st.o[i][t][r], st.o[i][t][2 + r], st.o[i][t + 1][r], st.o[i][t + 1][2 + r]);
       }
       __syncthreads();
-      const int rr = tid >> 4, rg_row = i * 8 + rr, row = row0 + rg_row;  // 16 threads a row
-      if (row < a.rows && (tid & 15) < D / 8) {
-        float M = -INFINITY, f[kWarps], l = 0.f;
+      join(i, pc.slot);
+    }
+    if (pc.slot >= 0) {
+      // the piece that brings the segment's tiles to their number merges it: the
+      // others' results are visible to it through the counter, which is that of
+      // the segment's first CTA (a CTA's run crosses into at most one segment that
+      // another CTA goes on with)
+      Sched sc = a.sched;
+      sc.tile_pfx = s_pfx;
+      const int nt = s_pfx[b + 1] - s_pfx[b];
+      const int HR = sc.Hkv * sc.nrg;
+      const long long X = sched_total_cost(sc);
+      const long long t0 = (long long)s_pfx[b] * HR + (long long)(pc.seg - b * HR) * nt;
+      const int c0 = sched_cta_of(sched_tile_cost(sc, t0, pc.seg), X, sc.G);
+      __threadfence();
+      __syncthreads();
+      if (tid == 0) {
+        unsigned* counter = p.frag_tiles + c0;
+        s_last = count_tiles(counter, (unsigned)tiles) + (unsigned)tiles == (unsigned)nt;
+        if (s_last) *counter = 0;  // left at zero for the next call
+      }
+      __syncthreads();
+      if (s_last) {
+        const int c1 = sched_cta_of(sched_tile_cost(sc, t0 + nt - 1, pc.seg), X, sc.G);
+        // warp w takes every fourth of the segment's CTAs; those between the first
+        // and the last that hold no tile (their cost range is empty) are left out
+        constexpr int J = 4;  // 16-byte units of a lane: 32 J of a row's D / 4 at a time
+        constexpr int R = 32 * J / (D / 4);
+#pragma unroll 1
+        for (int g = 0; g < RG / R; ++g) {
+          const int i = g * R / 8;
+          float4 acc[J];
+          float M[J], l[J];
 #pragma unroll
-        for (int w = 0; w < kWarps; ++w) M = fmaxf(M, s_m[w][rg_row]);
+          for (int j = 0; j < J; ++j) {
+            acc[j] = make_float4(0.f, 0.f, 0.f, 0.f);
+            M[j] = -INFINITY;
+            l[j] = 0.f;
+          }
+#pragma unroll 1
+          for (int cta = c0 + warp; cta <= c1; cta += kWarps) {
+            if (cta != c0 && cta != c1 && X * (cta + 1) / sc.G == X * cta / sc.G) continue;
+            const size_t r0 = (size_t)(pc.seg + cta) * a.part_rows;
+            float2 ml[J];
+            float4 v[J];
 #pragma unroll
-        for (int w = 0; w < kWarps; ++w) {
-          const float e = s_m[w][rg_row] == -INFINITY ? 0.f : fast_exp2(s_m[w][rg_row] - M);
-          l += e * s_l[w][rg_row];
-          f[w] = e * s_ref[w];
+            for (int j = 0; j < J; ++j) {
+              const int u = j * 32 + lane, rg_row = g * R + u / (D / 4);
+              ml[j] = make_float2(-INFINITY, 0.f);
+              if (rg_row < a.part_rows && row0 + rg_row < a.rows) {
+                ml[j] = __ldcg(a.part_ml + r0 + rg_row);
+                v[j] = __ldcg(reinterpret_cast<const float4*>(p.frag_o + (r0 + rg_row) * D) + u % (D / 4));
+              }
+            }
+#pragma unroll
+            for (int j = 0; j < J; ++j) {
+              if (ml[j].x == -INFINITY) continue;  // the piece saw no key of the row
+              const float m = fmaxf(M[j], ml[j].x);
+              const float fo = fast_exp2(M[j] - m), fn = fast_exp2(ml[j].x - m) * ml[j].y;
+              acc[j].x = acc[j].x * fo + v[j].x * fn;
+              acc[j].y = acc[j].y * fo + v[j].y * fn;
+              acc[j].z = acc[j].z * fo + v[j].z * fn;
+              acc[j].w = acc[j].w * fo + v[j].w * fn;
+              l[j] = l[j] * fo + fn;
+              M[j] = m;
+            }
+          }
+          if (g * R % 8 == 0) __syncthreads();  // the rows joined before are no longer read
+#pragma unroll
+          for (int j = 0; j < J; ++j) {
+            const int u = j * 32 + lane, rr = (g * R + u / (D / 4)) % 8, c4 = u % (D / 4);
+            *reinterpret_cast<float4*>(s_o + (warp * 8 + rr) * C::LDO + c4 * 4) = acc[j];
+            if (c4 == 0) {
+              s_m[warp][i * 8 + rr] = M[j];
+              s_l[warp][i * 8 + rr] = l[j];
+            }
+          }
+          if (lane == 0) s_ref[warp] = 1.f;
+          if ((g + 1) * R % 8 == 0) {
+            __syncthreads();
+            join(i, -1);
+          }
         }
-        const float inv = l > 0.f ? 1.f / l : 0.f;
-        const int c8 = tid & 15;
-        float acc[8] = {};
-#pragma unroll
-        for (int w = 0; w < kWarps; ++w) {
-          const float4* o = reinterpret_cast<const float4*>(s_o + (w * 8 + rr) * C::LDO + c8 * 8);
-          const float4 x = o[0], y = o[1];
-          acc[0] += f[w] * x.x;
-          acc[1] += f[w] * x.y;
-          acc[2] += f[w] * x.z;
-          acc[3] += f[w] * x.w;
-          acc[4] += f[w] * y.x;
-          acc[5] += f[w] * y.y;
-          acc[6] += f[w] * y.z;
-          acc[7] += f[w] * y.w;
-        }
-#pragma unroll
-        for (int e = 0; e < 8; ++e) acc[e] *= inv;
-        Row8<T> v;
-        v.from_f(acc);
-        T* dst;
-        if (pc.slot < 0) {
-          const int node = row / a.g, h = kvh * a.g + row % a.g;
-          dst = static_cast<T*>(a.out) + (((size_t)b * a.T + node) * a.Hq + h) * D + c8 * 8;
-        } else {
-          dst = static_cast<T*>(a.part_o) + (((size_t)pc.slot * (D / 8) + c8) * a.part_rows + rg_row) * 8;
-        }
-        v.store(dst);
-        if (pc.slot >= 0 && c8 == 0) a.part_ml[(size_t)pc.slot * a.part_rows + rg_row] = make_float2(M, l);
       }
     }
     __syncthreads();  // the rings are filled again by the next piece
@@ -595,14 +695,29 @@ cudaError_t launch_d(const Block8Params& p, cudaStream_t stream) {
 
 }  // namespace
 
-Block8Plan block8_plan(int rows, int g, int dtype) {
+Block8Plan block8_plan(int batch, int kv_heads, int rows, int g, int max_blocks, int tree_size, int dtype, int sms) {
+  Block8Plan p{};
   if (rows > 32 && tc_supported(128, g)) {
-    const int parts = dtype == 1 ? 3 : 2;
-    return Block8Plan{true, parts == 2 && rows > 128 ? 256 : 128, 1, 4, parts};
+    p.tc = true;
+    p.parts = dtype == 1 ? 3 : 2;
+    p.rows_per_group = p.parts == 2 && rows > 128 ? 256 : 128;
+    p.ctas = sms;
+    p.seg_cost = 8;
+  } else {
+    p.rows_per_group = rows <= 8 ? 8 : rows <= 16 ? 16 : 32;
+    p.ctas = sms * (rows <= 8 ? Cfg<128, 1>::CTAS : rows <= 16 ? Cfg<128, 2>::CTAS : Cfg<128, 4>::CTAS);
+    p.seg_cost = 2;
   }
-  if (rows <= 8) return Block8Plan{false, 8, Cfg<128, 1>::CTAS, 2, 0};
-  if (rows <= 16) return Block8Plan{false, 16, Cfg<128, 2>::CTAS, 2, 0};
-  return Block8Plan{false, 32, Cfg<128, 4>::CTAS, 2, 0};
+  p.nrg = (rows + p.rows_per_group - 1) / p.rows_per_group;
+  if (!p.tc) {
+    // Few segments: a piece of t tiles takes about t / 2 us and the merge about
+    // 0.1 us a piece, so a segment of n tiles is best cut into about sqrt(5 n)
+    // pieces (n from the block table's width, which is all the host knows).
+    const double n = max_blocks / 4.0 + (tree_size + 63) / 64;
+    const double most = (double)batch * kv_heads * p.nrg * std::ceil(std::sqrt(5.0 * n));
+    if (most < p.ctas) p.ctas = (int)most;
+  }
+  return p;
 }
 
 cudaError_t launch_attn_block8(const Block8Params& p, int dtype, cudaStream_t stream) {

@@ -14,19 +14,22 @@
 //              the time that a 16-bit step takes for 16, so two parts cost what
 //              a 16-bit product costs, and no key is ever converted;
 //   O = P V    needs softmax weights over a wider range than 8 bits hold, so it
-//              runs in fp16: the producers convert value codes to fp16 (exact,
-//              one instruction for two codes) on the way into the tile.
+//              runs in fp16: four warps convert value codes to fp16 (exact, one
+//              instruction for two codes) on the way into the tile.
 // Scales: a page's key scale multiplies its 16 columns of S in the softmax's
 // exponent (no extra operation); its value scale 2^lv joins the exponent, so the
 // running maximum is that of (score + lv), P = 2^(score + lv - max + 3) fits
 // fp16, and the row's sum takes each page's part times 2^-lv.
 //
 // Warps: 4 * MT softmax warps (one thread per query row), one issuing Q K^T, one
-// issuing P V, four producers (one per page of a tile, as in the 16-bit kernel).
-// A ring slot is one tile (keys in 8 bits, values in fp16) or one part of an M
-// tile's queries, copied to TMEM.  Every mbarrier wait is bounded; on a timeout
-// MT_ERR_TIMEOUT is recorded, the other roles stop, the copies and MMAs in
-// flight are waited for and TMEM is freed.
+// issuing P V, one issuing the copies (a lane per page of a tile) and four
+// converting (a page each).  Issuing and converting are apart because each is a
+// chain of short steps that one warp cannot overlap: in one warp they took 2250
+// cycles a tile, more than the softmax (stamps in a copy of the kernel).  A ring
+// slot is one tile (keys in 8 bits, value codes, values in fp16) or one part of an
+// M tile's queries, copied to TMEM.  Every mbarrier wait is bounded; on a timeout
+// MT_ERR_TIMEOUT is recorded, the other roles stop, the copies and MMAs in flight
+// are waited for and TMEM is freed.
 #include <cudaTypedefs.h>
 
 #include <atomic>
@@ -40,16 +43,7 @@ namespace {
 
 constexpr int kSmemLimit = 232448;  // opt-in dynamic shared memory per CTA
 constexpr int kMaxDevices = 64;
-constexpr int kProducers = kTileKeys / 16;
-
-// What a producer needs to finish a tile whose value codes it has asked for.
-struct Pending {
-  uint32_t pos;  // ring position
-  int krow;      // row of the key page in its map
-  int from_new;  // which map: the cache, or the new tokens' blocks
-  int rows;      // rows of the page that hold keys of the sequence (0: none)
-  float ks, vs;
-};
+constexpr int kPages = kTileKeys / 16;  // of a tile
 
 template <int D, int MT, int NP>
 struct Cfg {
@@ -59,19 +53,18 @@ struct Cfg {
   static constexpr int kKTile = kTileKeys * D;        // key codes, swizzled rows of D bytes
   static constexpr int kHalf = kTileKeys * 128;       // 64 values of 64 columns
   static constexpr int kVTile = NH * kHalf;
-  static constexpr int kStage = kKTile + kVTile;      // >= 128 * D: one part of an M tile's queries
-  static constexpr int kDepth = 4;                    // value pages in flight per producer
-  static constexpr int kVPage = 16 * D;
-  static constexpr int kVBytes = kProducers * kDepth * kVPage;
-  static constexpr int kMetaBytes = 4096;  // barriers, pending tiles, scales, piece list
-  static constexpr int kFit = (kSmemLimit - 1024 - kMetaBytes - kPBytes - kVBytes) / kStage;
+  static constexpr int kV8 = kKTile;                  // value codes, plain rows
+  static constexpr int kStage = kKTile + kVTile + kV8;  // >= 128 * D: one part of an M tile's queries
+  static constexpr int kMetaBytes = 4096;  // barriers, scales, piece list
+  static constexpr int kFit = (kSmemLimit - 1024 - kMetaBytes - kPBytes) / kStage;
   static constexpr int STAGES = kFit > 8 ? 8 : kFit;
-  static constexpr int kSmem = 1024 + kPBytes + STAGES * kStage + kVBytes + kMetaBytes;
+  static constexpr int kSmem = 1024 + kPBytes + STAGES * kStage + kMetaBytes;
   static constexpr int kSoftmaxWarps = 4 * MT;
   static constexpr int kQkWarp = kSoftmaxWarps;
   static constexpr int kPvWarp = kSoftmaxWarps + 1;
-  static constexpr int kProducer0 = kSoftmaxWarps + 2;
-  static constexpr int kThreads = (kSoftmaxWarps + 2 + kProducers) * 32;
+  static constexpr int kCopyWarp = kSoftmaxWarps + 2;
+  static constexpr int kConvert0 = kSoftmaxWarps + 3;
+  static constexpr int kThreads = (kSoftmaxWarps + 3 + kPages) * 32;
   static constexpr int kQSlots = MT * NP;  // ring slots of a piece's queries
   // TMEM: O (D fp32 columns per M tile), S (64), Q (D / 4 columns of four codes per part)
   static constexpr int kTmemUsed = MT * (D + kTileKeys + NP * (D / 4));
@@ -171,10 +164,10 @@ __global__ void __launch_bounds__(Cfg<D, MT, NP>::kThreads, 1)
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* sP = smem;                       // [m] P tiles, 128-byte swizzled, K-major
-  uint8_t* sKV = sP + C::kPBytes;           // [stage] keys, then values
-  uint8_t* sV8 = sKV + S * C::kStage;       // [producer][kDepth] value codes
-  uint64_t* bars = reinterpret_cast<uint64_t*>(sV8 + C::kVBytes);
-  uint64_t* full = bars;                    // [S] a tile's keys and values, or query rows, are there
+  uint8_t* sKV = sP + C::kPBytes;           // [stage] keys, values, value codes
+  uint64_t* bars = reinterpret_cast<uint64_t*>(sKV + S * C::kStage);
+  uint64_t* land = bars;                    // [S] a tile's codes, or query rows, have landed
+  uint64_t* full = land + S;                // [S] a tile's values are converted (tiles only)
   uint64_t* empty = full + S;               // [S] consumed
   uint64_t* s_full = empty + S;             // [MT] S computed
   uint64_t* p_full = s_full + MT;           // [MT] P written (and O rescaled)
@@ -183,14 +176,14 @@ __global__ void __launch_bounds__(Cfg<D, MT, NP>::kThreads, 1)
   uint64_t* o_free = s_free + MT;           // O of the previous piece read out
   uint64_t* fin = o_free + 1;               // [2] every MMA of each issuer done
   uint64_t* never = fin + 2;                // nothing arrives here (timeout test hook)
-  uint64_t* v_full = never + 1;             // [producer][kDepth] value codes landed
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(v_full + kProducers * C::kDepth);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(never + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   int* s_npieces = const_cast<int*>(abort_flag + 1);
-  static_assert((2 * 8 + 4 * 2 + 4 + kProducers * C::kDepth) * 8 + 12 <= 1024, "barrier area");
-  Pending* s_pend = reinterpret_cast<Pending*>(reinterpret_cast<uint8_t*>(bars) + 1024);  // [producer][kDepth]
-  float* s_scale = reinterpret_cast<float*>(reinterpret_cast<uint8_t*>(bars) + 1536);     // [S][3][4]: ks, lv, 2^-lv
-  static_assert(kProducers * C::kDepth * sizeof(Pending) <= 512 && 8 * 12 * 4 <= 512, "metadata");
+  static_assert((3 * 8 + 4 * 2 + 4) * 8 + 12 <= 1024, "barrier area");
+  // per stage: key scales, log2 and inverse of the value scales, and how many rows
+  // of each page hold keys of the sequence
+  float* s_scale = reinterpret_cast<float*>(reinterpret_cast<uint8_t*>(bars) + 1024);  // [S][4][4]
+  static_assert(8 * 16 * 4 <= 1024, "metadata");
   PieceRec* s_pieces = reinterpret_cast<PieceRec*>(reinterpret_cast<uint8_t*>(bars) + 2048);
   static_assert(2048 + kMaxPieceRecs * sizeof(PieceRec) <= C::kMetaBytes, "piece list");
 
@@ -198,7 +191,8 @@ __global__ void __launch_bounds__(Cfg<D, MT, NP>::kThreads, 1)
   const int nnew = (a.T + 15) / 16;
   if (threadIdx.x == 0) {
     for (int s = 0; s < S; ++s) {
-      tc::mbar_init(&full[s], 2 * kProducers);  // a producer's keys, and its values
+      tc::mbar_init(&land[s], 1);
+      tc::mbar_init(&full[s], kPages);
       tc::mbar_init(&empty[s], 1);
     }
     for (int m = 0; m < MT; ++m) {
@@ -211,7 +205,6 @@ __global__ void __launch_bounds__(Cfg<D, MT, NP>::kThreads, 1)
     tc::mbar_init(&fin[0], 1);
     tc::mbar_init(&fin[1], 1);
     tc::mbar_init(never, 1);
-    for (int k = 0; k < kProducers * C::kDepth; ++k) tc::mbar_init(&v_full[k], 1);
     *abort_flag = 0;
     tc::fence_barrier_init();
   }
@@ -219,7 +212,7 @@ __global__ void __launch_bounds__(Cfg<D, MT, NP>::kThreads, 1)
     tc::tmem_alloc(tmem_slot, C::kTmemCols);
     tc::tmem_relinquish();
   }
-  if (warp == C::kProducer0 && lane == 0) {
+  if (warp == C::kCopyWarp && lane == 0) {
     tc::prefetch_tmap(&map_k);
     tc::prefetch_tmap(&map_v);
     tc::prefetch_tmap(&map_kn);
@@ -252,88 +245,24 @@ __global__ void __launch_bounds__(Cfg<D, MT, NP>::kThreads, 1)
   Piece pc;
   int L = 0;
 
-  if (warp >= C::kProducer0) {
-    // ----------------------------------------------------------- producers
-    const int pid = warp - C::kProducer0;
+  if (warp == C::kCopyWarp) {
+    // -------------------------------------------------------------- copies
     const uint64_t policy = tc::policy_evict_first();
     const uint64_t q_policy = tc::policy_evict_last();
     const int oob_row = a.num_pages * a.Hkv * 16;  // past the cache: TMA fills zeros
     uint32_t pos = 0;                              // ring position
-    uint32_t issued = 0, done = 0;                 // tiles whose values were asked for, and finished
-    uint32_t landing = 0;                          // positions below this had keys or queries asked for
-    // Finish the oldest tile: its stage, its keys (TMA), then its values
-    // converted: 16-byte chunks of codes, consecutive lanes on consecutive
-    // chunks, become two 8-column chunks of the 128-byte-swizzled fp16 rows.
-    auto finish_oldest = [&]() {
-      const uint32_t f = done % C::kDepth;
-      const Pending pd = s_pend[pid * C::kDepth + f];
-      const uint32_t st = pd.pos % S;
-      if (pd.pos >= (uint32_t)S) {
-        wait_all(&empty[st], ((pd.pos / S) - 1) & 1);
-        if (!ok) return;
-      }
-      uint8_t* stage = sKV + st * C::kStage;
-      if (lane == 0) {
-        tc::mbar_arrive_expect_tx(&full[st], 16 * D);
-        tc::tma_load_2d(stage + pid * 16 * D, pd.from_new ? &map_kn : &map_k, 0, pd.krow, &full[st], policy);
-        float* sc = s_scale + st * 12 + pid;
-        sc[0] = pd.ks;
-        sc[4] = log2f(pd.vs);
-        sc[8] = 1.f / pd.vs;
-      }
-      landing = pd.pos + 1;
-      wait_all(&v_full[pid * C::kDepth + f], (done / C::kDepth) & 1);
-      if (!ok) return;
-      const uint8_t* codes = sV8 + (pid * C::kDepth + f) * C::kVPage;
-      constexpr int CPR = D / 16;
-#pragma unroll
-      for (int i = 0; i < 16 * CPR / 32; ++i) {
-        const int q = i * 32 + lane;
-        const int r = q / CPR, col = (q % CPR) * 16;
-        uint4 c = *reinterpret_cast<const uint4*>(codes + q * 16);
-        // rows that hold no key of the sequence may hold anything (NaN codes
-        // too): their weights are 0 and so are their values
-        if (r >= pd.rows) c = make_uint4(0, 0, 0, 0);
-        const int row = pid * 16 + r, c0 = (col % 64) / 8;
-        uint8_t* dst = stage + C::kKTile + (col / 64) * C::kHalf + row * 128;
-        const uint32_t w[4] = {c.x, c.y, c.z, c.w};
-#pragma unroll
-        for (int h = 0; h < 2; ++h)
-          *reinterpret_cast<uint4*>(dst + (((c0 + h) ^ (row & 7)) << 4)) =
-              make_uint4(e4m3x2_to_h2(w[2 * h] & 0xffffu), e4m3x2_to_h2(w[2 * h] >> 16),
-                         e4m3x2_to_h2(w[2 * h + 1] & 0xffffu), e4m3x2_to_h2(w[2 * h + 1] >> 16));
-      }
-      tc::fence_proxy_async_smem();  // read by the tensor core; the codes' slot is refilled by TMA
-      __syncwarp();
-      if (lane == 0) tc::mbar_arrive(&full[st]);
-      ++done;
-    };
-    // finish every tile at ring position <= q - S before a wait on position q's
-    // stage, which can depend on them
-    auto finish_until = [&](uint32_t q) {
-      while (ok && done < issued && q >= (uint32_t)S && s_pend[pid * C::kDepth + done % C::kDepth].pos <= q - S)
-        finish_oldest();
-    };
     while (ok && pi.next(pc, L)) {
-      // the piece's queries: part `part` of M tile m per ring slot, its 128-row
-      // box loaded by producer (slot % 4); every producer arrives twice
+      // the piece's queries: part `part` of M tile m per ring slot
       for (int s = 0; s < C::kQSlots && ok; ++s, ++pos) {
         const uint32_t st = pos % S;
-        finish_until(pos);
-        if (ok && pos >= (uint32_t)S) wait_all(&empty[st], ((pos / S) - 1) & 1);
+        if (pos >= (uint32_t)S) wait_all(&empty[st], ((pos / S) - 1) & 1);
         if (!ok) break;
         if (lane == 0) {
-          if (s % kProducers == pid) {
-            const int m = s / NP, part = s % NP;
-            tc::mbar_arrive_expect_tx(&full[st], 128 * D);
-            tc::tma_load_3d(sKV + st * C::kStage, &map_q, 0, pc.kvh * a.g,
-                            (part * a.B + pc.b) * a.T + (pc.rg * a.rows_per_group + m * 128) / a.g, &full[st], q_policy);
-          } else {
-            tc::mbar_arrive(&full[st]);
-          }
-          tc::mbar_arrive(&full[st]);
+          const int m = s / NP, part = s % NP;
+          tc::mbar_arrive_expect_tx(&land[st], 128 * D);
+          tc::tma_load_3d(sKV + st * C::kStage, &map_q, 0, pc.kvh * a.g,
+                          (part * a.B + pc.b) * a.T + (pc.rg * a.rows_per_group + m * 128) / a.g, &land[st], q_policy);
         }
-        landing = pos + 1;
         __syncwarp();
       }
       if (!ok) break;
@@ -346,72 +275,123 @@ __global__ void __launch_bounds__(Cfg<D, MT, NP>::kThreads, 1)
       auto fetch_scale = [&](const float* sc, int id) {
         return id >= 0 && id < a.num_pages ? __ldg(sc + (size_t)id * a.Hkv + pc.kvh) : 1.f;
       };
+      // value scales are positive; a smaller one (or one that is no number) would
+      // leave the exponent's range
+      auto clamp = [](float v) { return fmaxf(v, 5.421010862427522e-20f); };
       int base = pc.tile_begin * 4;
       int id0 = fetch_id(base + lane), id1 = fetch_id(base + 32 + lane), id2 = fetch_id(base + 64 + lane);
-      float ks0 = fetch_scale(p.k_scales, id0), vs0 = fetch_scale(p.v_scales, id0);
+      float ks0 = fetch_scale(p.k_scales, id0), vs0 = clamp(fetch_scale(p.v_scales, id0));
       float ks1 = fetch_scale(p.k_scales, id1), vs1 = fetch_scale(p.v_scales, id1);
+      float lv0 = log2f(vs0), iv0 = 1.f / vs0;
       for (int j = pc.tile_begin; j < pc.tile_end; ++j, ++pos) {
-        const int pg = j * 4 + pid;
-        if (j * 4 - base >= 32) {  // the same tile for every lane: windows are whole tiles
+        const uint32_t st = pos % S;
+        if (j * 4 - base >= 32) {  // windows are whole tiles
           base += 32;
           id0 = id1;
           ks0 = ks1;
-          vs0 = vs1;
+          vs0 = clamp(vs1);
+          lv0 = log2f(vs0);
+          iv0 = 1.f / vs0;
           id1 = id2;
           ks1 = fetch_scale(p.k_scales, id1);
           vs1 = fetch_scale(p.v_scales, id1);
           id2 = fetch_id(base + 64 + lane);
         }
+        // lane l < 4 has page l of the tile
+        const int pg = j * 4 + (lane & 3);
         const int id = __shfl_sync(0xffffffffu, id0, pg - base);
-        float ks = __shfl_sync(0xffffffffu, ks0, pg - base), vs = __shfl_sync(0xffffffffu, vs0, pg - base);
-        if (issued - done == (uint32_t)C::kDepth) finish_oldest();
-        if (!ok) break;
-        int row = oob_row, rows = 0, from_new = 0;
+        float ks = __shfl_sync(0xffffffffu, ks0, pg - base), lv = __shfl_sync(0xffffffffu, lv0, pg - base);
+        float iv = __shfl_sync(0xffffffffu, iv0, pg - base);
+        int row = oob_row, rows = 0;
+        const bool from_new = pg >= npre && pg - npre < nnew;
         if (pg < npre) {
           if (id >= 0 && id < a.num_pages) {
             row = (id * a.Hkv + pc.kvh) * 16;
             rows = min(16, L - pg * 16);
-          } else if (lane == 0) {
+          } else if (lane < kPages) {
             set_status(a.status, kStPages);
           }
-        } else if (pg - npre < nnew) {
-          from_new = 1;
+        } else if (from_new) {
           row = (int)((nb0 + pg - npre) * 16);
           rows = 16;
           ks = __ldg(p.k_block_scales + nb0 + pg - npre);
-          vs = __ldg(p.v_block_scales + nb0 + pg - npre);
+          const float vs = clamp(__ldg(p.v_block_scales + nb0 + pg - npre));
+          lv = log2f(vs);
+          iv = 1.f / vs;
         }
-        if (lane == 0) {
-          const uint32_t f = issued % C::kDepth;
-          uint64_t* bar = &v_full[pid * C::kDepth + f];
-          // scales are positive; a smaller one (or one that is no number) would
-          // leave the exponent's range
-          s_pend[pid * C::kDepth + f] = Pending{pos, row, from_new, rows, ks, fmaxf(vs, 5.421010862427522e-20f)};
-          tc::mbar_arrive_expect_tx(bar, C::kVPage);
-          tc::tma_load_2d(sV8 + (pid * C::kDepth + f) * C::kVPage, from_new ? &map_vn : &map_v, 0, row, bar, policy);
+        if (pos >= (uint32_t)S) wait_all(&empty[st], ((pos / S) - 1) & 1);
+        if (!ok) break;
+        if (lane < kPages) {
+          float* sc = s_scale + st * 16 + lane;
+          sc[0] = ks;
+          sc[4] = lv;
+          sc[8] = iv;
+          sc[12] = __int_as_float(rows);
         }
         __syncwarp();
-        ++issued;
+        if (lane == 0) tc::mbar_arrive_expect_tx(&land[st], 2 * C::kKTile);
+        __syncwarp();
+        if (lane < kPages) {
+          uint8_t* stage = sKV + st * C::kStage + lane * 16 * D;
+          tc::tma_load_2d(stage, from_new ? &map_kn : &map_k, 0, row, &land[st], policy);
+          tc::tma_load_2d(stage + C::kKTile + C::kVTile, from_new ? &map_vn : &map_v, 0, row, &land[st], policy);
+        }
+        __syncwarp();
       }
     }
-    while (ok && done < issued) finish_oldest();
-    // no TMA load may still be writing shared memory when the CTA exits: value
-    // codes never converted (after an abort), keys and queries of the last S slots
-    if (lane == 0) {
-      for (uint32_t u = done; u < issued; ++u)
-        drain_wait(&v_full[pid * C::kDepth + u % C::kDepth], (u / C::kDepth) & 1, a.status);
-      for (uint32_t t = landing > (uint32_t)S ? landing - S : 0; t < landing; ++t)
-        drain_wait(&full[t % S], (t / S) & 1, a.status);
-    }
+    // no TMA load may still be writing shared memory when the CTA exits
+    if (lane == 0)
+      for (uint32_t t = pos > (uint32_t)S ? pos - S : 0; t < pos; ++t) drain_wait(&land[t % S], (t / S) & 1, a.status);
     __syncwarp();
+  } else if (warp >= C::kConvert0) {
+    // ---------------------------------------------------------- conversion
+    // Warp pid turns page pid's value codes into fp16: 16-byte chunks of codes,
+    // consecutive lanes on consecutive chunks, become two 8-column chunks of the
+    // 128-byte-swizzled rows.  The slot is the warp's once the codes have landed
+    // (they were asked for after its last use).
+    const int pid = warp - C::kConvert0;
+    uint32_t pos = 0;
+    while (ok && pi.next(pc, L)) {
+      pos += C::kQSlots;
+      for (int j = pc.tile_begin; j < pc.tile_end; ++j, ++pos) {
+        const uint32_t st = pos % S;
+        wait_all(&land[st], (pos / S) & 1);
+        if (!ok) break;
+        uint8_t* stage = sKV + st * C::kStage;
+        const uint8_t* codes = stage + C::kKTile + C::kVTile + pid * 16 * D;
+        const int rows = __float_as_int(s_scale[st * 16 + 12 + pid]);
+        constexpr int CPR = D / 16;
+#pragma unroll
+        for (int i = 0; i < 16 * CPR / 32; ++i) {
+          const int q = i * 32 + lane;
+          const int r = q / CPR, col = (q % CPR) * 16;
+          uint4 c = *reinterpret_cast<const uint4*>(codes + q * 16);
+          // rows that hold no key of the sequence may hold anything (NaN codes
+          // too): their weights are 0 and so are their values
+          if (r >= rows) c = make_uint4(0, 0, 0, 0);
+          const int row = pid * 16 + r, c0 = (col % 64) / 8;
+          uint8_t* dst = stage + C::kKTile + (col / 64) * C::kHalf + row * 128;
+          const uint32_t w[4] = {c.x, c.y, c.z, c.w};
+#pragma unroll
+          for (int h = 0; h < 2; ++h)
+            *reinterpret_cast<uint4*>(dst + (((c0 + h) ^ (row & 7)) << 4)) =
+                make_uint4(e4m3x2_to_h2(w[2 * h] & 0xffffu), e4m3x2_to_h2(w[2 * h] >> 16),
+                           e4m3x2_to_h2(w[2 * h + 1] & 0xffffu), e4m3x2_to_h2(w[2 * h + 1] >> 16));
+        }
+        tc::fence_proxy_async_smem();  // read by the tensor core; the codes' place is refilled by TMA
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(&full[st]);
+      }
+    }
   } else if (warp == C::kQkWarp) {
     // ---------------------------------------------------------- QK issuer
     uint32_t it = 0, pos = 0;  // tiles so far; ring position
+    uint32_t phase = 0;        // bit s: parity of slot s's next tile (queries leave `full` alone)
     if (a.test_stall) wait_all(never, 0);  // test hook: a wait that can only time out
     while (ok && pi.next(pc, L)) {
       for (int s = 0; s < C::kQSlots && ok; ++s) {
         const uint32_t st = (pos + s) % S;
-        wait_all(&full[st], ((pos + s) / S) & 1);
+        wait_all(&land[st], ((pos + s) / S) & 1);
         if (!ok) break;
         tc::tc_fence_after();
         const uint64_t qd = desc_rows8<D>(sKV_u + st * C::kStage);
@@ -426,7 +406,8 @@ __global__ void __launch_bounds__(Cfg<D, MT, NP>::kThreads, 1)
       pos += C::kQSlots;
       for (int j = pc.tile_begin; j < pc.tile_end; ++j, ++it, ++pos) {
         const uint32_t st = pos % S;
-        wait_all(&full[st], (pos / S) & 1);
+        wait_all(&full[st], (phase >> st) & 1);
+        phase ^= 1u << st;
         if (!ok) break;
         const uint64_t kd = desc_rows8<D>(sKV_u + st * C::kStage);
         for (int m = 0; m < MT; ++m) {
@@ -520,11 +501,11 @@ __global__ void __launch_bounds__(Cfg<D, MT, NP>::kThreads, 1)
         uint32_t sr[64];
         tc::tmem_ld_x64(tmem + lane_addr + C::s_col(m), sr);
         const uint32_t st = pos % S;
-        wait_all(&full[st], (pos / S) & 1);  // complete; orders the scales' reads
+        wait_all(&land[st], (pos / S) & 1);  // complete; orders the scales' reads
         if (!ok) break;
-        const float4 ks = *reinterpret_cast<const float4*>(s_scale + st * 12);
-        const float4 lv = *reinterpret_cast<const float4*>(s_scale + st * 12 + 4);
-        const float4 iv = *reinterpret_cast<const float4*>(s_scale + st * 12 + 8);
+        const float4 ks = *reinterpret_cast<const float4*>(s_scale + st * 16);
+        const float4 lv = *reinterpret_cast<const float4*>(s_scale + st * 16 + 4);
+        const float4 iv = *reinterpret_cast<const float4*>(s_scale + st * 16 + 8);
         const float c4[4] = {ks.x * qs, ks.y * qs, ks.z * qs, ks.w * qs};
         const float l4[4] = {lv.x, lv.y, lv.z, lv.w}, i4[4] = {iv.x, iv.y, iv.z, iv.w};
         tc::tmem_ld_wait();

@@ -187,6 +187,8 @@ cudaError_t launch_append(const AppendParams& a, int dtype, cudaStream_t stream)
 // ---------------------------------------------------------------------------
 // Tree attention over a block-scaled 8-bit cache.
 // ---------------------------------------------------------------------------
+constexpr int kMaxFragCtas = 4096;
+
 struct Block8Params {
   AttnParams a;           // q_rot: the queries as they attend; part_o, part_ml, sched, out, status, ...
   const float* k_scales;  // [num_pages][Hkv]
@@ -194,8 +196,11 @@ struct Block8Params {
   const void* k_new;      // [B][T][Hkv][D] act, as they attend
   const void* v_new;
   const int* parents;     // [B][T], or null: a chain
-  int* tile_pfx;          // [B + 1] out, for the combine
+  // the register-fragment kernel's split segments, merged by their last piece:
+  float* frag_o;          // [slots][rows per slot][D] each piece's O / l
+  unsigned* frag_tiles;   // [kMaxFragCtas] tiles done of the segment that a CTA starts and another ends
   // the tensor-core path, written by its preparation:
+  int* tile_pfx;          // [B + 1], for the combine
   int parts;              // E4M3 parts of a query row: 2 (bf16) or 3 (fp16)
   uint8_t* q8;            // [parts][B][T][Hq][D]
   float* q_scale;         // [B][T][Hq] scale of the row's parts times the softmax scale times log2(e)
@@ -249,13 +254,13 @@ __device__ __forceinline__ int block8_prefix(const AttnParams& a, int* pfx, int*
 }
 
 // How a call runs: the tensor-core kernel or the register-fragment kernel, its
-// row group, persistent CTAs per SM and cost of starting a piece (in 64-slot
-// tiles).
+// row group, row groups per KV head, persistent CTAs, and the cost of starting a
+// piece (in 64-slot tiles).
 struct Block8Plan {
   bool tc;
-  int rows_per_group, ctas_per_sm, seg_cost, parts;
+  int rows_per_group, nrg, ctas, seg_cost, parts;
 };
-Block8Plan block8_plan(int rows, int g, int dtype);
+Block8Plan block8_plan(int batch, int kv_heads, int rows, int g, int max_blocks, int tree_size, int dtype, int sms);
 cudaError_t launch_attn_block8(const Block8Params& p, int dtype, cudaStream_t stream);
 cudaError_t launch_block8_prep(const Block8Params& p, int dtype, cudaStream_t stream);
 cudaError_t launch_attn_block8_tc(const Block8Params& p, int dtype, cudaStream_t stream);
