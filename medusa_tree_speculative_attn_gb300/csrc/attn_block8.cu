@@ -697,12 +697,12 @@ cudaError_t launch_d(const Block8Params& p, cudaStream_t stream) {
 
 Block8Plan block8_plan(int batch, int kv_heads, int rows, int g, int max_blocks, int tree_size, int dtype, int sms) {
   Block8Plan p{};
-  if (rows > 32 && tc_supported(128, g)) {
+  if (rows > 16 && tc_supported(128, g)) {
     p.tc = true;
     p.parts = dtype == 1 ? 3 : 2;
     p.rows_per_group = p.parts == 2 && rows > 128 ? 256 : 128;
     p.ctas = sms;
-    p.seg_cost = 8;
+    p.seg_cost = 5;
   } else {
     p.rows_per_group = rows <= 8 ? 8 : rows <= 16 ? 16 : 32;
     p.ctas = sms * (rows <= 8 ? Cfg<128, 1>::CTAS : rows <= 16 ? Cfg<128, 2>::CTAS : Cfg<128, 4>::CTAS);
