@@ -35,6 +35,11 @@
 // CTA from the lengths).  A split segment's pieces leave O / l in fp32 with their
 // maximum and sum; the one that completes the segment's tile count merges them, so
 // a call is one launch.
+//
+// Bound by the cache's bytes: 64 sequences of 256 to 8192 tokens, 32 query and 8 KV
+// heads of 128 columns, one query each: 94 us for 549 MB, 5.8 TB/s (86 % of a copy).
+// A call for one sequence of 2048 tokens takes 12.7 us, all of it latency: the
+// prefix, the first page ids, the first pages, one merge.
 #include <atomic>
 #include <cmath>
 
@@ -53,9 +58,11 @@ constexpr int kMaxDevices = 64;
 template <int D, int NT>
 struct Cfg {
   static constexpr int ROWS = 8 * NT;
-  static constexpr int CTAS = NT == 1 ? 4 : NT == 2 ? 3 : 2;   // per SM, by registers
-  static constexpr int DEPTH = NT == 1 ? 3 : NT == 2 ? 4 : 6;  // pages a warp keeps in flight
-  static constexpr int kPage = 16 * D;                         // bytes of a page's K or V
+  // per SM, by registers.  NT = 1: four CTAs of 128 registers and three pages a warp
+  // were slower, 100 us against 97 at the size named above, and spilled.
+  static constexpr int CTAS = NT <= 2 ? 3 : 2;
+  static constexpr int DEPTH = NT <= 2 ? 4 : 6;  // pages a warp keeps in flight
+  static constexpr int kPage = 16 * D;           // bytes of a page's K or V
   static constexpr int kRing = kWarps * DEPTH * 2 * kPage;
   static constexpr int LDO = D + 4;                            // merge rows, in floats
   static constexpr int kMerge = kWarps * 8 * LDO * 4;
@@ -263,8 +270,8 @@ __device__ __forceinline__ void page_step(State<D, NT>& st, const uint8_t* kp, c
 
 // One block of up to 16 new tokens of K or V as codes in shared memory (rows
 // past T are zero); returns the block's scale.
-template <typename T, int D, bool KEYS>
-__device__ __forceinline__ float quantise_new(const T* src, size_t row_stride, int rows, uint8_t* dst) {
+template <typename T, int D>
+__device__ __forceinline__ float quantise_new(const T* src, size_t row_stride, int rows, uint8_t* dst, bool keys) {
   constexpr int LPR = D / 16, RPS = 32 / LPR, STEPS = 16 / RPS;
   const int lane = threadIdx.x & 31, sub = lane / LPR, c = lane % LPR;
   Row8<T> lo[STEPS], hi[STEPS];
@@ -302,11 +309,80 @@ __device__ __forceinline__ float quantise_new(const T* src, size_t row_stride, i
       if (h) hi[s].to_f(x); else lo[s].to_f(x);
 #pragma unroll
       for (int e = 0; e < 8; ++e) x[e] *= inv;
-      const int off = (KEYS ? k_off<D>(r, col >> 4) : v_off<D>(r, col >> 4)) + (col & 8);
+      const int off = (keys ? k_off<D>(r, col >> 4) : v_off<D>(r, col >> 4)) + (col & 8);
       *reinterpret_cast<uint2*>(dst + off) = e4m3x8_of(x);
     }
   }
   return scale;
+}
+
+// Merges the pieces that CTAs c0 .. c1 left of a segment, by the block of the last
+// one: 16 threads a row, eight columns each.  Each thread brings its own part of up
+// to 4 * DEPTH pieces into the idle rings at once, so that a round costs one trip to
+// L2 (0.33 us a piece one after the other).  X: the schedule's total cost.
+template <typename T, int D, int NT>
+__device__ __forceinline__ void merge_pieces(const Block8Params& p, const Piece& done, int c0, int c1, long long X,
+                                             uint8_t* ring) {
+  constexpr int U = 4 * Cfg<D, NT>::DEPTH;  // pieces of eight rows that the rings hold
+  __shared__ float2 s_ml[U][8];
+  const AttnParams& a = p.a;
+  const int tid = threadIdx.x, rr = tid >> 4, c8 = tid & 15, G = a.sched.G;
+  const uint32_t mine = static_cast<uint32_t>(__cvta_generic_to_shared(ring)) + (rr * (D / 8) + c8) * 16;
+#pragma unroll 1
+  for (int i = 0; i < NT; ++i) {
+    const int row = done.rg * (8 * NT) + i * 8 + rr;
+    const bool live = row < a.rows && c8 < D / 8;
+    float M = -INFINITY, l = 0.f, acc[8] = {};
+#pragma unroll 1
+    for (int k0 = c0; k0 <= c1; k0 += U) {
+      const int n = min(U, c1 - k0 + 1);
+      for (int x = tid; x < n * 8; x += kThreads) {
+        const int cta = k0 + (x >> 3), r = i * 8 + (x & 7);
+        float2 v = make_float2(-INFINITY, 0.f);
+        // a CTA between the first and the last may hold no tile, and has written
+        // nothing then
+        if (done.rg * (8 * NT) + r < a.rows && (cta == c0 || cta == c1 || X * (cta + 1) / G != X * cta / G))
+          v = __ldcg(a.part_ml + (size_t)(done.seg + cta) * a.part_rows + r);
+        s_ml[x >> 3][x & 7] = v;
+      }
+      if (live) {
+#pragma unroll 4
+        for (int k = 0; k < n; ++k) {
+          const float* o = p.frag_o + ((size_t)(done.seg + k0 + k) * a.part_rows + i * 8 + rr) * D + c8 * 8;
+          cp_async16(mine + k * 32 * D, o);
+          cp_async16(mine + k * 32 * D + 16 * D, o + 4);
+        }
+      }
+      cp_commit();
+      cp_wait<0>();
+      __syncthreads();
+      if (live) {
+#pragma unroll 4
+        for (int k = 0; k < n; ++k) {
+          const float2 ml = s_ml[k][rr];
+          if (ml.x == -INFINITY) continue;  // no piece, or one that saw no key of the row
+          const float4* o = reinterpret_cast<const float4*>(ring + k * 32 * D) + rr * (D / 8) + c8;
+          const float4 x = o[0], y = o[D];
+          const float m = fmaxf(M, ml.x);
+          const float fo = fast_exp2(M - m), fn = fast_exp2(ml.x - m) * ml.y;
+          const float v[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
+#pragma unroll
+          for (int e = 0; e < 8; ++e) acc[e] = fmaf(v[e], fn, acc[e] * fo);
+          l = fmaf(l, fo, fn);
+          M = m;
+        }
+      }
+      __syncthreads();  // the rings and s_ml are filled again
+    }
+    if (!live) continue;
+    const float inv = l > 0.f ? 1.f / l : 0.f;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) acc[e] *= inv;
+    const int node = row / a.g, h = done.kvh * a.g + row % a.g;
+    Row8<T> v;
+    v.from_f(acc);
+    v.store(static_cast<T*>(a.out) + (((size_t)done.b * a.T + node) * a.Hq + h) * D + c8 * 8);
+  }
 }
 
 template <typename T, int D, int NT>
@@ -451,6 +527,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::CTAS) attn_block8_kernel
     }
 
     const unsigned none[NT][2] = {};
+#pragma unroll 1
     for (int i = 0; i < npages; ++i) {
       const int at = i & 31;
       if (at == 0) {
@@ -493,8 +570,12 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::CTAS) attn_block8_kernel
       const size_t rs = (size_t)a.Hkv * D;
       const size_t src = ((size_t)b * a.T + pn * kP) * rs + (size_t)kvh * D;
       const int rows = min(kP, a.T - pn * kP);
-      const float ks = quantise_new<T, D, true>(static_cast<const T*>(p.k_new) + src, rs, rows, ring);
-      const float vs = quantise_new<T, D, false>(static_cast<const T*>(p.v_new) + src, rs, rows, ring + C::kPage);
+      float ks = 0.f, vs = 0.f;
+#pragma unroll 1  // one after the other: both at once take more registers than there are
+      for (int x = 0; x < 2; ++x) {
+        ks = vs;
+        vs = quantise_new<T, D>(static_cast<const T*>(x ? p.v_new : p.k_new) + src, rs, rows, ring + x * C::kPage, x == 0);
+      }
       __syncwarp();
       unsigned see[NT][2];
 #pragma unroll
@@ -586,7 +667,6 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::CTAS) attn_block8_kernel
       const long long X = sched_total_cost(sc);
       const long long t0 = (long long)s_pfx[b] * HR + (long long)(pc.seg - b * HR) * nt;
       const int c0 = sched_cta_of(sched_tile_cost(sc, t0, pc.seg), X, sc.G);
-      __threadfence();
       __syncthreads();
       if (tid == 0) {
         unsigned* counter = p.frag_tiles + c0;
@@ -596,65 +676,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::CTAS) attn_block8_kernel
       __syncthreads();
       if (s_last) {
         const int c1 = sched_cta_of(sched_tile_cost(sc, t0 + nt - 1, pc.seg), X, sc.G);
-        // warp w takes every fourth of the segment's CTAs; those between the first
-        // and the last that hold no tile (their cost range is empty) are left out
-        constexpr int J = 4;  // 16-byte units of a lane: 32 J of a row's D / 4 at a time
-        constexpr int R = 32 * J / (D / 4);
-#pragma unroll 1
-        for (int g = 0; g < RG / R; ++g) {
-          const int i = g * R / 8;
-          float4 acc[J];
-          float M[J], l[J];
-#pragma unroll
-          for (int j = 0; j < J; ++j) {
-            acc[j] = make_float4(0.f, 0.f, 0.f, 0.f);
-            M[j] = -INFINITY;
-            l[j] = 0.f;
-          }
-#pragma unroll 1
-          for (int cta = c0 + warp; cta <= c1; cta += kWarps) {
-            if (cta != c0 && cta != c1 && X * (cta + 1) / sc.G == X * cta / sc.G) continue;
-            const size_t r0 = (size_t)(pc.seg + cta) * a.part_rows;
-            float2 ml[J];
-            float4 v[J];
-#pragma unroll
-            for (int j = 0; j < J; ++j) {
-              const int u = j * 32 + lane, rg_row = g * R + u / (D / 4);
-              ml[j] = make_float2(-INFINITY, 0.f);
-              if (rg_row < a.part_rows && row0 + rg_row < a.rows) {
-                ml[j] = __ldcg(a.part_ml + r0 + rg_row);
-                v[j] = __ldcg(reinterpret_cast<const float4*>(p.frag_o + (r0 + rg_row) * D) + u % (D / 4));
-              }
-            }
-#pragma unroll
-            for (int j = 0; j < J; ++j) {
-              if (ml[j].x == -INFINITY) continue;  // the piece saw no key of the row
-              const float m = fmaxf(M[j], ml[j].x);
-              const float fo = fast_exp2(M[j] - m), fn = fast_exp2(ml[j].x - m) * ml[j].y;
-              acc[j].x = acc[j].x * fo + v[j].x * fn;
-              acc[j].y = acc[j].y * fo + v[j].y * fn;
-              acc[j].z = acc[j].z * fo + v[j].z * fn;
-              acc[j].w = acc[j].w * fo + v[j].w * fn;
-              l[j] = l[j] * fo + fn;
-              M[j] = m;
-            }
-          }
-          if (g * R % 8 == 0) __syncthreads();  // the rows joined before are no longer read
-#pragma unroll
-          for (int j = 0; j < J; ++j) {
-            const int u = j * 32 + lane, rr = (g * R + u / (D / 4)) % 8, c4 = u % (D / 4);
-            *reinterpret_cast<float4*>(s_o + (warp * 8 + rr) * C::LDO + c4 * 4) = acc[j];
-            if (c4 == 0) {
-              s_m[warp][i * 8 + rr] = M[j];
-              s_l[warp][i * 8 + rr] = l[j];
-            }
-          }
-          if (lane == 0) s_ref[warp] = 1.f;
-          if ((g + 1) * R % 8 == 0) {
-            __syncthreads();
-            join(i, -1);
-          }
-        }
+        merge_pieces<T, D, NT>(p, pc, c0, c1, X, smem);
       }
     }
     __syncthreads();  // the rings are filled again by the next piece
@@ -697,16 +719,24 @@ cudaError_t launch_d(const Block8Params& p, cudaStream_t stream) {
 
 Block8Plan block8_plan(int batch, int kv_heads, int rows, int g, int max_blocks, int tree_size, int dtype, int sms) {
   Block8Plan p{};
+  // Up to 16 rows the register-fragment kernel, which wastes no rows; from 17 on the
+  // tensor-core kernel, whose tile has 128 (256) rows.  64 sequences of 256 to 8192
+  // tokens, 8 KV heads: 16 rows 115 us against 195, 32 rows 337 against 201.  The
+  // latter keeps a token's g rows in one tile, so where g does not divide 128 the
+  // former takes every count.  fp16 queries fill three operand parts, and with those
+  // two tiles do not fit in shared memory.
   if (rows > 16 && tc_supported(128, g)) {
     p.tc = true;
     p.parts = dtype == 1 ? 3 : 2;
     p.rows_per_group = p.parts == 2 && rows > 128 ? 256 : 128;
     p.ctas = sms;
-    p.seg_cost = 5;
+    p.seg_cost = 5;  // 8 and 12 were slower for 16 sequences of 64 nodes
   } else {
     p.rows_per_group = rows <= 8 ? 8 : rows <= 16 ? 16 : 32;
     p.ctas = sms * (rows <= 8 ? Cfg<128, 1>::CTAS : rows <= 16 ? Cfg<128, 2>::CTAS : Cfg<128, 4>::CTAS);
-    p.seg_cost = 2;
+    // starting and leaving a piece costs as much as eight tiles (2: 107 us, 4: 102,
+    // 8: 100, 12: 100 for 64 sequences of one query)
+    p.seg_cost = 8;
   }
   p.nrg = (rows + p.rows_per_group - 1) / p.rows_per_group;
   if (!p.tc) {
