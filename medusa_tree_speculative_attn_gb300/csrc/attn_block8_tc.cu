@@ -22,7 +22,7 @@
 // fp16, and the row's sum takes each page's part times 2^-lv.
 //
 // Warps: 4 * MT softmax warps (one thread per query row), one issuing Q K^T, one
-// issuing P V, one issuing the copies (a lane per page of a tile) and four
+// issuing P V, two issuing the copies (a lane per page of a tile) and four
 // converting (a page each).  Issuing and converting are apart because each is a
 // chain of short steps that one warp cannot overlap: in one warp they took 2250
 // cycles a tile, more than the softmax (stamps in a copy of the kernel).  A ring
@@ -30,6 +30,13 @@
 // M tile's queries, copied to TMEM.  Every mbarrier wait is bounded; on a timeout
 // MT_ERR_TIMEOUT is recorded, the other roles stop, the copies and MMAs in flight
 // are waited for and TMEM is freed.
+//
+// Bound by the roles' chains of steps, not by a unit: with 256 rows a tile takes
+// about 2050 cycles, of which the tensor cores work 1070 and the schedulers issue
+// half.  8 sequences of 32768 keys, 26 nodes, 64 query and 8 KV heads: 238 us, half
+// of the products' floor; 16 sequences of 512 to 8192 keys, 64 nodes, 32 query and 8
+// KV heads: 98 us; 64 sequences of 256 to 8192 keys, 32 rows a head: 184 us, 45 % of
+// a copy of the cache.
 #include <cudaTypedefs.h>
 
 #include <atomic>
@@ -63,8 +70,11 @@ struct Cfg {
   static constexpr int kQkWarp = kSoftmaxWarps;
   static constexpr int kPvWarp = kSoftmaxWarps + 1;
   static constexpr int kCopyWarp = kSoftmaxWarps + 2;
-  static constexpr int kConvert0 = kSoftmaxWarps + 3;
-  static constexpr int kThreads = (kSoftmaxWarps + 3 + kPages) * 32;
+  // One copy warp was busy for 1700 cycles a tile: 64 sequences of 32 rows took 199 us
+  // (fp16 204) against 184 (187) with two, 8 of 208 rows 241 against 238.
+  static constexpr int kCopyWarps = 2;
+  static constexpr int kConvert0 = kCopyWarp + kCopyWarps;
+  static constexpr int kThreads = (kConvert0 + kPages) * 32;
   static constexpr int kQSlots = MT * NP;  // ring slots of a piece's queries
   // TMEM: O (D fp32 columns per M tile), S (64), Q (D / 4 columns of four codes per part)
   static constexpr int kTmemUsed = MT * (D + kTileKeys + NP * (D / 4));
@@ -88,6 +98,26 @@ __device__ __forceinline__ uint32_t pack_h2(float a, float b) {
   const __half2 h = __floats2half2_rn(a, b);
   uint32_t r;
   memcpy(&r, &h, 4);
+  return r;
+}
+
+// Two fp32 in one register pair, for the instructions that take both at once.
+using F2 = unsigned long long;
+__device__ __forceinline__ F2 f2_of(float a, float b) {
+  F2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ float f2_lo(F2 x) { return __uint_as_float((uint32_t)x); }
+__device__ __forceinline__ float f2_hi(F2 x) { return __uint_as_float((uint32_t)(x >> 32)); }
+__device__ __forceinline__ F2 f2_fma(F2 a, F2 b, F2 c) {
+  F2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ F2 f2_add(F2 a, F2 b) {
+  F2 r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
   return r;
 }
 
@@ -168,7 +198,7 @@ __global__ void __launch_bounds__(Cfg<D, MT, NP>::kThreads, 1)
   uint64_t* bars = reinterpret_cast<uint64_t*>(sKV + S * C::kStage);
   uint64_t* land = bars;                    // [S] a tile's codes, or query rows, have landed
   uint64_t* full = land + S;                // [S] a tile's values are converted (tiles only)
-  uint64_t* empty = full + S;               // [S] consumed
+  uint64_t* empty = full + S;               // [S] consumed by the MMAs (or copied to TMEM) and by the four converters
   uint64_t* s_full = empty + S;             // [MT] S computed
   uint64_t* p_full = s_full + MT;           // [MT] P written (and O rescaled)
   uint64_t* pv_done = p_full + MT;          // [MT] O += P V done
@@ -193,7 +223,7 @@ __global__ void __launch_bounds__(Cfg<D, MT, NP>::kThreads, 1)
     for (int s = 0; s < S; ++s) {
       tc::mbar_init(&land[s], 1);
       tc::mbar_init(&full[s], kPages);
-      tc::mbar_init(&empty[s], 1);
+      tc::mbar_init(&empty[s], 1 + kPages);
     }
     for (int m = 0; m < MT; ++m) {
       tc::mbar_init(&s_full[m], 2);  // the MMAs, and the issuer itself (below)
@@ -245,8 +275,14 @@ __global__ void __launch_bounds__(Cfg<D, MT, NP>::kThreads, 1)
   Piece pc;
   int L = 0;
 
-  if (warp == C::kCopyWarp) {
+  if (warp >= C::kCopyWarp && warp < C::kCopyWarp + C::kCopyWarps) {
     // -------------------------------------------------------------- copies
+    // The two warps share the ring by slots, odd and even: a slot's every `empty`
+    // phase is then waited for by one warp, in order.  (By positions, a warp could
+    // come to a slot whose last phase but one is still open, and a wait by parity
+    // would take that for the last: the other warp's position is two phases back,
+    // and queries are consumed ahead of the tiles before them.)
+    const uint32_t turn = warp - C::kCopyWarp;
     const uint64_t policy = tc::policy_evict_first();
     const uint64_t q_policy = tc::policy_evict_last();
     const int oob_row = a.num_pages * a.Hkv * 16;  // past the cache: TMA fills zeros
@@ -255,6 +291,7 @@ __global__ void __launch_bounds__(Cfg<D, MT, NP>::kThreads, 1)
       // the piece's queries: part `part` of M tile m per ring slot
       for (int s = 0; s < C::kQSlots && ok; ++s, ++pos) {
         const uint32_t st = pos % S;
+        if (st % C::kCopyWarps != turn) continue;
         if (pos >= (uint32_t)S) wait_all(&empty[st], ((pos / S) - 1) & 1);
         if (!ok) break;
         if (lane == 0) {
@@ -284,7 +321,6 @@ __global__ void __launch_bounds__(Cfg<D, MT, NP>::kThreads, 1)
       float ks1 = fetch_scale(p.k_scales, id1), vs1 = fetch_scale(p.v_scales, id1);
       float lv0 = log2f(vs0), iv0 = 1.f / vs0;
       for (int j = pc.tile_begin; j < pc.tile_end; ++j, ++pos) {
-        const uint32_t st = pos % S;
         if (j * 4 - base >= 32) {  // windows are whole tiles
           base += 32;
           id0 = id1;
@@ -297,6 +333,8 @@ __global__ void __launch_bounds__(Cfg<D, MT, NP>::kThreads, 1)
           vs1 = fetch_scale(p.v_scales, id1);
           id2 = fetch_id(base + 64 + lane);
         }
+        const uint32_t st = pos % S;
+        if (st % C::kCopyWarps != turn) continue;
         // lane l < 4 has page l of the tile
         const int pg = j * 4 + (lane & 3);
         const int id = __shfl_sync(0xffffffffu, id0, pg - base);
@@ -339,9 +377,10 @@ __global__ void __launch_bounds__(Cfg<D, MT, NP>::kThreads, 1)
         __syncwarp();
       }
     }
-    // no TMA load may still be writing shared memory when the CTA exits
+    // no TMA load of this warp's may still be writing shared memory when the CTA exits
     if (lane == 0)
-      for (uint32_t t = pos > (uint32_t)S ? pos - S : 0; t < pos; ++t) drain_wait(&land[t % S], (t / S) & 1, a.status);
+      for (uint32_t t = pos > (uint32_t)S ? pos - S : 0; t < pos; ++t)
+        if (t % S % C::kCopyWarps == turn) drain_wait(&land[t % S], (t / S) & 1, a.status);
     __syncwarp();
   } else if (warp >= C::kConvert0) {
     // ---------------------------------------------------------- conversion
@@ -352,7 +391,14 @@ __global__ void __launch_bounds__(Cfg<D, MT, NP>::kThreads, 1)
     const int pid = warp - C::kConvert0;
     uint32_t pos = 0;
     while (ok && pi.next(pc, L)) {
-      pos += C::kQSlots;
+      // The queries' slots too are waited for and given back: a wait by parity must
+      // neither skip a phase nor come two late.
+      for (int s = 0; s < C::kQSlots && ok; ++s, ++pos) {
+        wait_all(&land[pos % S], (pos / S) & 1);
+        if (lane == 0) tc::mbar_arrive(&empty[pos % S]);
+        __syncwarp();
+      }
+      if (!ok) break;
       for (int j = pc.tile_begin; j < pc.tile_end; ++j, ++pos) {
         const uint32_t st = pos % S;
         wait_all(&land[st], (pos / S) & 1);
@@ -380,7 +426,11 @@ __global__ void __launch_bounds__(Cfg<D, MT, NP>::kThreads, 1)
         }
         tc::fence_proxy_async_smem();  // read by the tensor core; the codes' place is refilled by TMA
         __syncwarp();
-        if (lane == 0) tc::mbar_arrive(&full[st]);
+        if (lane == 0) {
+          tc::mbar_arrive(&full[st]);
+          tc::mbar_arrive(&empty[st]);
+        }
+        __syncwarp();
       }
     }
   } else if (warp == C::kQkWarp) {
@@ -530,12 +580,14 @@ __global__ void __launch_bounds__(Cfg<D, MT, NP>::kThreads, 1)
         float mx = -INFINITY;
 #pragma unroll
         for (int g = 0; g < 4; ++g) {
+          // three inputs an instruction, two chains
           float x0 = __uint_as_float(sr[16 * g]), x1 = __uint_as_float(sr[16 * g + 1]);
 #pragma unroll
-          for (int c = 2; c < 16; c += 2) {
-            x0 = fmaxf(x0, __uint_as_float(sr[16 * g + c]));
-            x1 = fmaxf(x1, __uint_as_float(sr[16 * g + c + 1]));
+          for (int c = 2; c < 14; c += 4) {
+            x0 = fmaxf(fmaxf(x0, __uint_as_float(sr[16 * g + c])), __uint_as_float(sr[16 * g + c + 1]));
+            x1 = fmaxf(fmaxf(x1, __uint_as_float(sr[16 * g + c + 2])), __uint_as_float(sr[16 * g + c + 3]));
           }
+          x0 = fmaxf(fmaxf(x0, __uint_as_float(sr[16 * g + 14])), __uint_as_float(sr[16 * g + 15]));
           mx = fmaxf(mx, fmaf(fmaxf(x0, x1), c4[g], l4[g]));
         }
         // O is rescaled only when the maximum grows by more than 8: P <= 2^11
@@ -549,16 +601,16 @@ __global__ void __launch_bounds__(Cfg<D, MT, NP>::kThreads, 1)
 #pragma unroll
         for (int g = 0; g < 4; ++g) {
           const float o = off + l4[g];
-          float s0 = 0.f, s1 = 0.f;
+          const F2 c2 = f2_of(c4[g], c4[g]), o2 = f2_of(o, o);
+          F2 s2 = f2_of(0.f, 0.f);
 #pragma unroll
           for (int c = 0; c < 8; ++c) {
-            const float p0 = fast_exp2(fmaf(__uint_as_float(sr[16 * g + 2 * c]), c4[g], o));
-            const float p1 = fast_exp2(fmaf(__uint_as_float(sr[16 * g + 2 * c + 1]), c4[g], o));
-            s0 += p0;
-            s1 += p1;
+            const F2 x = f2_fma(f2_of(__uint_as_float(sr[16 * g + 2 * c]), __uint_as_float(sr[16 * g + 2 * c + 1])), c2, o2);
+            const float p0 = fast_exp2(f2_lo(x)), p1 = fast_exp2(f2_hi(x));
+            s2 = f2_add(s2, f2_of(p0, p1));
             pk[8 * g + c] = pack_h2(p0, p1);
           }
-          sum = fmaf(s0 + s1, i4[g], sum);
+          sum = fmaf(f2_lo(s2) + f2_hi(s2), i4[g], sum);
         }
         // P once the P.V of the tile before (which read it) is done: row r is
         // 128 B (64 keys), 16-byte chunk c at c ^ (r % 8)

@@ -418,6 +418,18 @@ def test_block8_attention_many_sequences():
     _attn_check(c, out)
 
 
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("batch, t, d, longest", [(500, 8, 128, 50), (300, 8, 64, 330), (200, 40, 128, 100), (150, 40, 64, 400)])
+def test_block8_attention_many_pieces(dtype, batch, t, d, longest):
+    # 32 or 160 rows a head: a CTA walks several pieces, of one tile and of more
+    rng = np.random.default_rng(batch)
+    lens = [int(n) for n in rng.integers(-1, longest, batch)]
+    c = _attn_case(rng, batch, t, 8, 2, d, lens, dtype, "tree")
+    out, ws, _, _ = _attn_run(c)
+    assert mt.read_status(ws) == 0
+    _attn_check(c, out)
+
+
 def test_block8_attention_of_widely_spread_scales():
     # pages whose value scales differ by 2^40 and more, a page of zeros, one dominant key
     rng = np.random.default_rng(70)
