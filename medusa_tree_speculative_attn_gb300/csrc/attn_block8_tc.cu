@@ -439,6 +439,9 @@ __global__ void __launch_bounds__(Cfg<D, MT, NP>::kThreads, 1)
     uint32_t phase = 0;        // bit s: parity of slot s's next tile (queries leave `full` alone)
     if (a.test_stall) wait_all(never, 0);  // test hook: a wait that can only time out
     while (ok && pi.next(pc, L)) {
+      // the queries in TMEM give way once the products that read them are done
+      if (it >= 1)
+        for (int m = 0; m < MT; ++m) wait_all(&s_full[m], (it - 1) & 1);
       for (int s = 0; s < C::kQSlots && ok; ++s) {
         const uint32_t st = (pos + s) % S;
         wait_all(&land[st], ((pos + s) / S) & 1);
