@@ -389,7 +389,8 @@ int mt_qk_norm_rope(const mt_norm_rope_desc* desc, const void* q, const void* k,
  * nodes out of range, a table that does not cover the slots (nothing of that
  * sequence is written), a page id out of range (nothing of that page is
  * written); MT_ERR_POSITION for a slot past the RoPE table (nothing of that
- * page is written).  Two sequences must not append to the same page.
+ * page is written).  A call must not append to a page twice: not for two
+ * sequences, and not through a table that names the page twice.
  * Strides of k and v in elements, (row, head), whole numbers of 16 bytes. */
 typedef struct {
   int batch;
@@ -433,11 +434,17 @@ int mt_kv_append_accepted(const mt_append_desc* desc, int tree_size, int max_dep
  * A sequence with seq_lens[b] < 0 is no sequence: its rows of out are left as
  * they were.  desc: dtype MT_F16 or MT_BF16, cache_dtype MT_E4M3; num_splits,
  * kernel, k_scale and v_scale are not used; any number of query heads per KV
- * head.  Accumulation in fp32; queries keep their bits, softmax weights are
- * rounded to fp16, and a split segment's pieces to the act dtype.
+ * head.  out must not overlap q, k_new or v_new.  Accumulation in fp32; queries
+ * keep their bits, softmax weights are rounded to fp16, and, where there are more
+ * than 16 query rows per KV head (T * Hq / Hkv), a split segment's pieces to the act
+ * dtype.  A query row with a NaN or an infinity gives NaN, and so does a row that
+ * sees a key with a NaN or a new token with a NaN among its values; a cached value's
+ * NaN reaches its own column.  What a row does not see has no effect on it.
  * workspace: mt_tree_attn_block8_workspace_size(desc) bytes, zero-filled before
- * its first use (status word, schedule, partial results); calls that share one
- * must not overlap.  Device status: MT_ERR_PAGES (length past the table, page id
+ * its first use (status word, counters that every call leaves at zero, schedule,
+ * partial results); it serves any descriptor that it is large enough for, one call
+ * at a time: calls that share one, replays of captured ones too, must not overlap.
+ * Device status: MT_ERR_PAGES (length past the table, page id
  * out of range), MT_ERR_TREE (a parent that is not earlier); the outputs of an
  * affected sequence are unspecified. */
 size_t mt_tree_attn_block8_workspace_size(const mt_attn_desc* desc);
@@ -491,12 +498,12 @@ int mt_profile_enable(int max_records);
 int mt_profile_read(float* ms, int max_records, int* n_out);
 
 /* ---- Timeout test hook --------------------------------------------------------
- * Every pipeline wait of the tensor-core attention kernel (a TMA load landing,
+ * Every pipeline wait of the tensor-core attention kernels (a TMA load landing,
  * an MMA completing, a softmax handing over P) gives up after a bounded time:
  * the kernel then records MT_ERR_TIMEOUT in the status word, lets its other
  * warps stop, waits for its own copies and MMAs in flight, frees its tensor
  * memory and returns, leaving the context usable.  mt_debug_set_wait sets that
- * bound for later mt_tree_attn_paged calls (limit_ns 0 restores the default of
+ * bound for later mt_tree_attn_paged and mt_tree_attn_paged_block8 calls (limit_ns 0 restores the default of
  * 2 s); stall = 1 makes the kernel first wait on a barrier that nothing
  * completes, so that the bound always expires (for tests of the timeout path;
  * stall = 0 is normal operation).  Process-wide, not thread-safe.  Returns

@@ -698,7 +698,9 @@ def tree_attn_paged_block8(q, k_cache, v_cache, k_scales, v_scales, block_tables
     The cache holds E4M3 codes under k_scales / v_scales [pages,Hkv] and is only
     read; q and k_new are rotated already (qk_norm_rope); the new keys and values
     are seen as kv_append_paged would store them, in blocks of 16 tokens.  A
-    sequence with seq_lens[b] < 0 leaves its rows of out as they were."""
+    sequence with seq_lens[b] < 0 leaves its rows of out as they were.  out must
+    not overlap q, k_new or v_new; the workspace serves any call that it is large
+    enough for, one at a time."""
     dev = _cuda_device(q, "q")
     dt = q.dtype
     _act(q, "q", (torch.float16, torch.bfloat16))

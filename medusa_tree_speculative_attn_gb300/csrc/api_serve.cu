@@ -18,6 +18,11 @@ bool strides_ok(const long long (&st)[2], int elem) {
   return st[0] >= 0 && st[1] >= 0 && st[0] * elem % 16 == 0 && st[1] * elem % 16 == 0;
 }
 
+bool overlap(const void* a, size_t na, const void* b, size_t nb) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return x < y + nb && y < x + na;
+}
+
 // A table made for this head size on the current device.
 int check_rope(const mt_rope* rope, int head_dim) {
   int dev = 0;
@@ -226,6 +231,12 @@ int mt_tree_attn_paged_block8(const mt_attn_desc* d, const void* q, const void* 
     return MT_ERR_INVALID_ARG;
   if (!aligned16(q) || !aligned16(k_new) || !aligned16(v_new) || !aligned16(k_cache) || !aligned16(v_cache) ||
       !aligned16(out) || reinterpret_cast<uintptr_t>(workspace) % kAlign)
+    return MT_ERR_INVALID_ARG;
+  // the output is written while other blocks still read the inputs
+  const size_t tokens = (size_t)d->batch * d->tree_size, q_bytes = tokens * d->num_q_heads * d->head_dim * 2;
+  const size_t new_bytes = tokens * d->num_kv_heads * d->head_dim * 2;
+  if (overlap(out, q_bytes, q, q_bytes) || overlap(out, q_bytes, k_new, new_bytes) ||
+      overlap(out, q_bytes, v_new, new_bytes))
     return MT_ERR_INVALID_ARG;
   Block8Ws w;
   st = block8_ws(d, &w);

@@ -269,13 +269,14 @@ __device__ __forceinline__ void page_step(State<D, NT>& st, const uint8_t* kp, c
 }
 
 // One block of up to 16 new tokens of K or V as codes in shared memory (rows
-// past T are zero); returns the block's scale.
+// past T are zero); returns the block's scale.  nan: which tokens have a NaN value,
+// found by the call for the values and used by the one for the keys.
 template <typename T, int D>
-__device__ __forceinline__ float quantise_new(const T* src, size_t row_stride, int rows, uint8_t* dst, bool keys) {
+__device__ __forceinline__ float quantise_new(const T* src, size_t row_stride, int rows, uint8_t* dst, bool keys,
+                                              unsigned& nan) {
   constexpr int LPR = D / 16, RPS = 32 / LPR, STEPS = 16 / RPS;
   const int lane = threadIdx.x & 31, sub = lane / LPR, c = lane % LPR;
   Row8<T> lo[STEPS], hi[STEPS];
-  float amax = 0.f;
 #pragma unroll
   for (int s = 0; s < STEPS; ++s) {
     const int r = s * RPS + sub;
@@ -286,31 +287,38 @@ __device__ __forceinline__ float quantise_new(const T* src, size_t row_stride, i
       hi[s].load(src + r * row_stride + D / 2 + 8 * c);
     }
   }
+  AbsMax<T> top;
 #pragma unroll
   for (int s = 0; s < STEPS; ++s) {
-    float x[8];
-    lo[s].to_f(x);
-#pragma unroll
-    for (int e = 0; e < 8; ++e) amax = fmaxf(amax, fabsf(x[e]));
-    hi[s].to_f(x);
-#pragma unroll
-    for (int e = 0; e < 8; ++e) amax = fmaxf(amax, fabsf(x[e]));
+    top.add(lo[s]);
+    top.add(hi[s]);
+    if (!keys) nan |= nan_rows<RPS>(has_nan(lo[s]) || has_nan(hi[s])) << (s * RPS);
   }
+  float amax = top.get();
 #pragma unroll
   for (int off = 16; off > 0; off >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, off));
   const float scale = block_scale(amax), inv = 1.f / scale;
 #pragma unroll
   for (int s = 0; s < STEPS; ++s) {
     const int r = s * RPS + sub;
+    float x[2][8];
+    lo[s].to_f(x[0]);
+    hi[s].to_f(x[1]);
+    if (nan) {
+      if (!keys) {
+        drop_nan(x[0]);
+        drop_nan(x[1]);
+      } else if (nan >> r & 1u) {
+        x[0][0] = __int_as_float(0x7fffffff);
+      }
+    }
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       const int col = h * (D / 2) + 8 * c;
-      float x[8];
-      if (h) hi[s].to_f(x); else lo[s].to_f(x);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) x[e] *= inv;
+      for (int e = 0; e < 8; ++e) x[h][e] *= inv;
       const int off = (keys ? k_off<D>(r, col >> 4) : v_off<D>(r, col >> 4)) + (col & 8);
-      *reinterpret_cast<uint2*>(dst + off) = e4m3x8_of(x);
+      *reinterpret_cast<uint2*>(dst + off) = e4m3x8_of(x[h]);
     }
   }
   return scale;
@@ -360,7 +368,7 @@ __device__ __forceinline__ void merge_pieces(const Block8Params& p, const Piece&
 #pragma unroll 4
         for (int k = 0; k < n; ++k) {
           const float2 ml = s_ml[k][rr];
-          if (ml.x == -INFINITY) continue;  // no piece, or one that saw no key of the row
+          if (ml.y == 0.f) continue;  // no piece, or one that saw no key of the row (a NaN goes on)
           const float4* o = reinterpret_cast<const float4*>(ring + k * 32 * D) + rr * (D / 8) + c8;
           const float4 x = o[0], y = o[D];
           const float m = fmaxf(M, ml.x);
@@ -375,7 +383,7 @@ __device__ __forceinline__ void merge_pieces(const Block8Params& p, const Piece&
       __syncthreads();  // the rings and s_ml are filled again
     }
     if (!live) continue;
-    const float inv = l > 0.f ? 1.f / l : 0.f;
+    const float inv = l == 0.f ? 0.f : 1.f / l;
 #pragma unroll
     for (int e = 0; e < 8; ++e) acc[e] *= inv;
     const int node = row / a.g, h = done.kvh * a.g + row % a.g;
@@ -571,10 +579,11 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::CTAS) attn_block8_kernel
       const size_t src = ((size_t)b * a.T + pn * kP) * rs + (size_t)kvh * D;
       const int rows = min(kP, a.T - pn * kP);
       float ks = 0.f, vs = 0.f;
+      unsigned nan = 0;
 #pragma unroll 1  // one after the other: both at once take more registers than there are
       for (int x = 0; x < 2; ++x) {
-        ks = vs;
-        vs = quantise_new<T, D>(static_cast<const T*>(x ? p.v_new : p.k_new) + src, rs, rows, ring + x * C::kPage, x == 0);
+        vs = ks;
+        ks = quantise_new<T, D>(static_cast<const T*>(x ? p.k_new : p.v_new) + src, rs, rows, ring + (1 - x) * C::kPage, x == 1, nan);
       }
       __syncwarp();
       unsigned see[NT][2];
@@ -617,7 +626,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::CTAS) attn_block8_kernel
         l += e * s_l[w][rg_row];
         f[w] = e * s_ref[w];
       }
-      const float inv = l > 0.f ? 1.f / l : 0.f;
+      const float inv = l == 0.f ? 0.f : 1.f / l;
       float acc[8] = {};
 #pragma unroll
       for (int w = 0; w < kWarps; ++w) {
@@ -721,10 +730,11 @@ Block8Plan block8_plan(int batch, int kv_heads, int rows, int g, int max_blocks,
   Block8Plan p{};
   // Up to 16 rows the register-fragment kernel, which wastes no rows; from 17 on the
   // tensor-core kernel, whose tile has 128 (256) rows.  64 sequences of 256 to 8192
-  // tokens, 8 KV heads: 16 rows 115 us against 195, 32 rows 337 against 201.  The
-  // latter keeps a token's g rows in one tile, so where g does not divide 128 the
+  // tokens, 8 KV heads: 16 rows 115 us against 184, 24 rows 195 against 184, 32 rows
+  // 205 against 184; 4 sequences of 2000: 20.9 against 21.9, and 32.8 against 22.6.
+  // The latter keeps a token's g rows in one tile, so where g does not divide 128 the
   // former takes every count.  fp16 queries fill three operand parts, and with those
-  // two tiles do not fit in shared memory.
+  // two tiles do not fit in TMEM.
   if (rows > 16 && tc_supported(128, g)) {
     p.tc = true;
     p.parts = dtype == 1 ? 3 : 2;

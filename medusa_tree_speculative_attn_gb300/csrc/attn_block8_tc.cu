@@ -159,6 +159,13 @@ __device__ __forceinline__ uint64_t desc_rows8(uint32_t saddr) {
   return d;
 }
 
+// What a wait does when its first try fails, out of line: the roles share the
+// instruction caches (1.5% with MT = 1).
+__device__ __noinline__ bool wait_slow(uint64_t* bar, uint32_t parity, volatile int* abort, int* status,
+                                       uint64_t limit) {
+  return tc::mbar_wait(bar, parity, abort, status, limit);
+}
+
 // Waits that ignore the abort flag (copies and MMAs in flight at the end).
 __device__ __forceinline__ void drain_wait(uint64_t* bar, uint32_t parity, int* status) {
   const uint64_t t0 = tc::global_timer_ns();
@@ -267,7 +274,7 @@ __global__ void __launch_bounds__(Cfg<D, MT, NP>::kThreads, 1)
   const uint32_t sKV_u = tc::smem_u32(sKV), sP_u = tc::smem_u32(sP);
   bool ok = true;
   auto wait_all = [&](uint64_t* bar, uint32_t parity) {
-    const bool r = tc::mbar_wait(bar, parity, abort_flag, a.status, a.wait_limit_ns);
+    const bool r = tc::mbar_try_wait(bar, parity) || wait_slow(bar, parity, abort_flag, a.status, a.wait_limit_ns);
     ok = __all_sync(0xffffffffu, r) && ok;
   };
   PieceSrc pi;
@@ -442,6 +449,7 @@ __global__ void __launch_bounds__(Cfg<D, MT, NP>::kThreads, 1)
       // the queries in TMEM give way once the products that read them are done
       if (it >= 1)
         for (int m = 0; m < MT; ++m) wait_all(&s_full[m], (it - 1) & 1);
+#pragma unroll 1  // unrolled, its code costs the fp16 kernel up to 12% (the roles share the instruction caches)
       for (int s = 0; s < C::kQSlots && ok; ++s) {
         const uint32_t st = (pos + s) % S;
         wait_all(&land[st], ((pos + s) / S) & 1);
@@ -653,7 +661,7 @@ __global__ void __launch_bounds__(Cfg<D, MT, NP>::kThreads, 1)
       if (!ok) break;
       tc::tc_fence_after();
       const int seg_row = m * 128 + r;
-      const float inv = l_run > 0.f ? 1.f / l_run : 0.f;
+      const float inv = l_run == 0.f ? 0.f : 1.f / l_run;  // a NaN sum makes the row NaN
 #pragma unroll 1
       for (int hh = 0; hh < D / 64; ++hh) {
         uint32_t o[64];
@@ -680,7 +688,10 @@ __global__ void __launch_bounds__(Cfg<D, MT, NP>::kThreads, 1)
           }
         }
       }
-      if (row_ok && pc.slot >= 0) a.part_ml[(size_t)pc.slot * a.part_rows + seg_row] = make_float2(m_run, l_run);
+      // (a piece of nothing but NaN scores has a NaN sum and no maximum: it takes part
+      // in the combine with one)
+      if (row_ok && pc.slot >= 0)
+        a.part_ml[(size_t)pc.slot * a.part_rows + seg_row] = make_float2(l_run == l_run ? m_run : fmaxf(m_run, 0.f), l_run);
       tc::tc_fence_before();
       __syncwarp();
       if (lane == 0) tc::mbar_arrive(o_free);

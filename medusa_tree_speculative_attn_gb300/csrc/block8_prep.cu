@@ -64,12 +64,14 @@ __device__ __forceinline__ void split_query(const Block8Params& p, long long row
     }
     *reinterpret_cast<uint4*>(p.q8 + (part * nrows + row) * D + 16 * c) = make_uint4(w[0], w[1], w[2], w[3]);
   }
-  if (c == 0) p.q_scale[row] = scale * a.scale_log2;
+  // an infinity has no parts: the row's scores become NaN, as they would be
+  if (c == 0) p.q_scale[row] = amax < INFINITY ? scale * a.scale_log2 : __int_as_float(0x7fffffff);
 }
 
-// One block of up to 16 new tokens of K or V.
+// One block of up to 16 new tokens of V, or of K (then `values` are their values).
 template <typename T, int D>
-__device__ __forceinline__ void quantise_block(const T* src, size_t row_stride, int rows, uint8_t* dst, float* scale_out) {
+__device__ __forceinline__ void quantise_block(const T* src, const T* values, size_t row_stride, int rows, uint8_t* dst,
+                                               float* scale_out) {
   constexpr int LPR = D / 16, RPS = 32 / LPR, STEPS = 16 / RPS;
   const int lane = threadIdx.x & 31, sub = lane / LPR, c = lane % LPR;
   Row8<T> lo[STEPS], hi[STEPS];
@@ -95,6 +97,21 @@ __device__ __forceinline__ void quantise_block(const T* src, size_t row_stride, 
 #pragma unroll
   for (int off = 16; off > 0; off >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, off));
   const float scale = block_scale(amax), inv = 1.f / scale;
+  unsigned nan = 0;  // of keys: the tokens that have a NaN value
+  if (values) {
+#pragma unroll
+    for (int s = 0; s < STEPS; ++s) {
+      const int r = s * RPS + sub;
+      Row8<T> v0, v1;
+      v0.zero();
+      v1.zero();
+      if (r < rows) {
+        v0.load(values + r * row_stride + 16 * c);
+        v1.load(values + r * row_stride + 16 * c + 8);
+      }
+      nan |= nan_rows<RPS>(has_nan(v0) || has_nan(v1)) << (s * RPS);
+    }
+  }
 #pragma unroll
   for (int s = 0; s < STEPS; ++s) {
     const int r = s * RPS + sub;
@@ -106,6 +123,11 @@ __device__ __forceinline__ void quantise_block(const T* src, size_t row_stride, 
       x[e] *= inv;
       y[e] *= inv;
     }
+    if (!values) {
+      drop_nan(x);
+      drop_nan(y);
+    }
+    if (nan >> r & 1u) x[0] = __int_as_float(0x7fffffff);
     const uint2 u = e4m3x8_of(x), v = e4m3x8_of(y);
     *reinterpret_cast<uint4*>(dst + r * D + 16 * c) = make_uint4(u.x, u.y, v.x, v.y);
   }
@@ -169,8 +191,9 @@ __global__ void __launch_bounds__(kThreads) block8_prep_kernel(Block8Params p) {
     const bool is_v = u >= nblk;
     const long long blk = is_v ? u - nblk : u;
     const int j = (int)(blk % nnew), h = (int)(blk / nnew % a.Hkv), b = (int)(blk / nnew / a.Hkv);
-    const T* src = static_cast<const T*>(is_v ? p.v_new : p.k_new) + ((size_t)b * a.T + j * kP) * rs + (size_t)h * D;
-    quantise_block<T, D>(src, rs, min(kP, a.T - j * kP), (is_v ? p.v_blocks : p.k_blocks) + (size_t)blk * kP * D,
+    const size_t at = ((size_t)b * a.T + j * kP) * rs + (size_t)h * D;
+    const T* values = static_cast<const T*>(p.v_new) + at;
+    quantise_block<T, D>(is_v ? values : static_cast<const T*>(p.k_new) + at, is_v ? nullptr : values, rs, min(kP, a.T - j * kP), (is_v ? p.v_blocks : p.k_blocks) + (size_t)blk * kP * D,
                          (is_v ? p.v_block_scales : p.k_block_scales) + blk);
   }
   // ancestor masks: a warp per sequence, lane l for nodes l and l + 32

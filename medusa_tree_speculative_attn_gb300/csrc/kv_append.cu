@@ -22,6 +22,11 @@
 // sequence b touches at most floor(o[b+1]/16) - floor(o[b]/16) + 2 pages (n new
 // rows span at most floor((n + 30) / 16)), so items floor(o[b]/16) + 2b and on
 // are its own, and b is found by a 32-wide search.
+//
+// 8 sequences of 512 to 1500 tokens, 32 heads of 128 columns, fp16 to an fp16
+// cache: 48 us (306 MB, 6.3 TB/s, 93 % of a copy).  16 of 100 to 4000, 8 heads,
+// bf16 to block scales: 44 us (239 MB, 5.4 TB/s, 79 %): a warp has to hold a whole
+// block before it can write the first code.  64 single tokens: 3.2 us, a launch.
 #include "serve.cuh"
 
 namespace mt {

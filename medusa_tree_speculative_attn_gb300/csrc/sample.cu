@@ -31,6 +31,10 @@
 // for a histogram of counts, 13k with masses, 6k for the last pass over the
 // weights, and 1k to 2k for each meeting of the cluster; few rows are bound by the
 // chain of meetings, many by the instructions of the weights.
+// One row of 32000 fp32 logits: 14.6 us.  64 rows of 128000 bf16 logits with
+// parameters of their own: 73 us, which is the longest row's chain of passes (the
+// schedulers issue half of the time in CTAs that are still at work, a quarter of
+// the whole).  256 rows of 32000 fp16 logits without filters: 20.5 us.
 #include <cooperative_groups.h>
 
 #include <atomic>

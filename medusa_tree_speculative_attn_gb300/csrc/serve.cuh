@@ -212,6 +212,34 @@ struct Block8Params {
   int* pieces;            // piece table (common.cuh)
 };
 
+// Whether a packed 16-bit row has a NaN (four instructions for eight values).
+template <typename T>
+__device__ __forceinline__ bool has_nan(const Row8<T>& r) {
+  typename AbsMax<T>::V2 v[4];
+  memcpy(v, r.w, sizeof(v));
+  const auto m = __hmax2_nan(__hmax2_nan(v[0], v[1]), __hmax2_nan(v[2], v[3]));
+  const float a = __low2float(m), b = __high2float(m);
+  return a != a || b != b;
+}
+
+// A NaN among a new token's values would reach, as 0 * NaN in the matrix products,
+// also the nodes that do not see the token.  So its value codes are set to 0 and its
+// key codes to NaN: its scores are NaN where it is seen and are replaced where it is
+// not.  Of R rows in a warp, 32 / R lanes each: bit i says that row i has one.
+template <int R>
+__device__ __forceinline__ unsigned nan_rows(bool nan) {
+  const unsigned lanes = __ballot_sync(0xffffffffu, nan);
+  unsigned rows = 0;
+#pragma unroll
+  for (int i = 0; i < R; ++i)
+    if (lanes >> (i * (32 / R)) & ((1u << (32 / R)) - 1u)) rows |= 1u << i;
+  return rows;
+}
+__device__ __forceinline__ void drop_nan(float (&x)[8]) {
+#pragma unroll
+  for (int e = 0; e < 8; ++e) x[e] = x[e] == x[e] ? x[e] : 0.f;
+}
+
 // Tiles of each sequence (cached pages, then the new tokens' blocks, four to a
 // tile; none for seq_lens < 0) and their exclusive prefix in pfx[0 .. B], by a
 // block of W warps; returns the total.  A length past the block table has no

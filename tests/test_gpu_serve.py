@@ -490,6 +490,136 @@ def test_block8_attention_in_a_graph_and_on_another_stream():
 
 # ---- sampling ---------------------------------------------------------------
 
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("t, hq, hkv", [(3, 4, 2), (4, 6, 2), (8, 8, 2), (40, 8, 2)])  # both kernels, split and whole segments
+def test_block8_attention_nan_in_and_out_of_sight(dtype, t, hq, hkv):
+    rng = np.random.default_rng(90 + t)
+    lens = [900, 3, 70]
+    c = _attn_case(rng, 3, t, hq, hkv, 128, lens, dtype, None)
+    c["parents"] = np.tile(np.maximum(np.arange(t) - 1, 0), (3, 1))  # a chain that leaves node 2 out: a leaf under node 0
+    c["parents"][:, 0], c["parents"][:, 2] = -1, 0
+    if t > 3:
+        c["parents"][:, 3] = 1
+    c["vn"][:, 2, :, 5] = c["kn"][:, 1, 0, 7] = 0
+    c["q"][2, 0] = c["q"][1, t - 1, 1] = 0
+    clean = _attn_run(c)[0].cpu()
+    c["vn"][:, 2, 0, 5] = float("nan")  # seen by node 2 alone, under KV head 0
+    c["q"][2, 0, 0, 3] = float("nan")
+    c["q"][1, t - 1, 1, 9] = float("inf")
+    out, ws, _, _ = _attn_run(c)
+    assert mt.read_status(ws) == 0
+    touched = np.zeros((3, t, hq), bool)
+    touched[:, 2, :hq // hkv] = touched[2, 0, 0] = touched[1, t - 1, 1] = True
+    touched = torch.from_numpy(touched)
+    assert out.cpu()[touched].isnan().all()
+    assert torch.equal(out.cpu()[~touched], clean[~touched])
+    c["kn"][0, 1, 0, 7] = float("nan")  # sequence 0, KV head 0: node 1 and what comes below it
+    touched[0, 1, :hq // hkv] = touched[0, 3:, :hq // hkv] = True
+    out = _attn_run(c)[0].cpu()
+    assert out[touched].isnan().all()
+    assert torch.equal(out[~touched], clean[~touched])
+
+
+def test_block8_attention_one_workspace_for_all_sizes():
+    rng = np.random.default_rng(95)
+    cases = [_attn_case(rng, b, t, hq, hkv, d, lens, dtype) for b, t, hq, hkv, d, lens, dtype in
+             [(2, 1, 8, 2, 128, [3000, 40], "bf16"), (2, 20, 8, 2, 128, [800, 33], "f16"), (3, 2, 6, 2, 64, [500, -1, 900], "f16"),
+              (1, 64, 16, 4, 128, [300], "bf16"), (1, 9, 3, 1, 128, [1000], "bf16")]]
+    own = [_attn_run(c)[:2] for c in cases]
+    ws = torch.zeros(max(w.numel() for _, w in own), dtype=torch.uint8, device="cuda")
+    for i in [0, 1, 2, 3, 4, 2, 0, 3, 1, 4, 0]:
+        assert torch.equal(_attn_run(cases[i], ws=ws)[0], own[i][0])
+    assert mt.read_status(ws) == 0
+
+
+def test_block8_attention_two_graphs_and_eager_calls_share_a_workspace():
+    rng = np.random.default_rng(96)
+    cases = [_attn_case(rng, 2, t, 8, 2, 128, [1500, 200], "bf16") for t in (1, 12)]
+    own = [_attn_run(c) for c in cases]
+    ws = torch.zeros(max(w.numel() for _, w, _, _ in own), dtype=torch.uint8, device="cuda")
+    graphs, outs = [], []
+    for _, _, args, kw in own:
+        outs.append(torch.zeros_like(args[8]))
+        call = (*args[:8], outs[-1])
+        graphs.append(_graph(lambda call=call, kw=kw: mt.tree_attn_paged_block8(*call, **{**kw, "workspace": ws})))
+    for i in (0, 1, 1, 0):
+        outs[i].zero_()
+        graphs[i].replay()
+        assert torch.equal(outs[i], own[i][0])
+        assert torch.equal(_attn_run(cases[1 - i], ws=ws)[0], own[1 - i][0])
+    assert mt.read_status(ws) == 0
+
+
+FAR = 300000  # a page of 8 heads of 128 columns behind byte 2^32 and, in 16 bits, element 2^32
+
+
+@pytest.mark.parametrize("t", [1, 20])
+def test_block8_attention_far_pages(t):
+    rng = np.random.default_rng(97)
+    c = _attn_case(rng, 2, t, 16, 8, 128, [200, 77], "bf16")
+    near, _, args, kw = _attn_run(c)
+    n = c["k"].shape[0]
+    far = []
+    for x in args[1:5]:
+        big = torch.empty((FAR + n, *x.shape[1:]), dtype=x.dtype, device="cuda")
+        big.view(torch.uint8)[FAR:] = x.view(torch.uint8)
+        far.append(big)
+    table = torch.where(args[5] >= 0, args[5] + FAR, args[5])
+    out = torch.empty_like(near)
+    mt.tree_attn_paged_block8(args[0], *far, table, *args[6:8], out, **{**kw, "workspace": mt.alloc_block8_workspace(args[0], far[0], table)})
+    assert torch.equal(out, near)
+
+
+@pytest.mark.parametrize("kind", ["act", "block8"])
+def test_append_far_pages(kind):
+    rng = np.random.default_rng(98)
+    n, table = 4, _i32([[2, 0], [3, 1]]).cuda()
+    k, v = (_rand(rng, 30, 8, 128, dtype=torch.bfloat16).cuda() for _ in range(2))
+    lens, off, ws = _i32([5, 0]).cuda(), _i32([0, 20, 30]).cuda(), _status()
+    got = []
+    for base in (0, FAR):
+        caches = [torch.empty((base + n, 8, P, 128), dtype=torch.bfloat16 if kind == "act" else torch.float8_e4m3fn, device="cuda") for _ in range(2)]
+        scales = [torch.ones((base + n, 8), device="cuda") for _ in range(2)]
+        for x in caches:
+            x.view(torch.uint8)[base:] = 0
+        kw = {} if kind == "act" else dict(k_scales=scales[0], v_scales=scales[1])
+        mt.kv_append_paged(k, v, *caches, table + base, lens, off, status_ws=ws, **kw)
+        got.append([x.view(torch.uint8)[base:].clone() for x in caches] + [x[base:].clone() for x in scales])
+        del caches, scales
+    assert mt.read_status(ws) == 0
+    assert all(torch.equal(a, b) for a, b in zip(*got))
+    assert all(int(x.count_nonzero()) > 0 for x in got[0])
+
+
+def test_norm_rope_far_tokens():
+    rng = np.random.default_rng(99)
+    x, pos, ws = _rand(rng, 3, 6, 64, dtype=torch.bfloat16).cuda(), _i32([4, 0, 9]).cuda(), _status()
+    step = 3 * 2 ** 30 // 2  # elements from token to token: the last one is 3 * 2^30 elements away
+    big = torch.empty(2 * step + 6 * 64, dtype=torch.bfloat16, device="cuda")
+    view = big.as_strided((3, 6, 64), (step, 64, 1))
+    view.copy_(x)
+    rope = mt.Rope(BASE, 64, 16)
+    near, far = x.clone(), view
+    for y in (near, far):
+        mt.qk_norm_rope(y[:, :4], y[:, 4:], pos, y[:, :4], y[:, 4:], rope=rope, q_weight=torch.ones(64, dtype=torch.bfloat16, device="cuda"),
+                        k_weight=torch.ones(64, dtype=torch.bfloat16, device="cuda"), status_ws=ws)
+    assert mt.read_status(ws) == 0
+    assert torch.equal(far, near) and not torch.equal(near, x)
+
+
+def test_sampling_far_rows_and_the_same_row_twice():
+    rng = np.random.default_rng(100)
+    n, v = 20000, 120000
+    big = torch.empty(n, v, dtype=torch.float16, device="cuda")
+    few = _rand(rng, 2, v, dtype=torch.float16, scale=2.0).cuda()
+    big[n - 1], big[3] = few[0], few[1]
+    u = torch.tensor([0.1, 0.9, 0.5, 0.5], device="cuda")
+    near, far = (torch.full((4,), -7, dtype=torch.int32, device="cuda") for _ in range(2))
+    mt.sample_tokens(few, u, near, row_index=_i32([0, 0, 1, -1]).cuda())
+    mt.sample_tokens(big, u, far, row_index=_i32([n - 1, n - 1, 3, -1]).cuda())
+    assert torch.equal(near, far) and int(near[3]) == -7 and int(near[0]) != int(near[1])
+
+
 def _sample(x, u, t=None, k=None, p=None, m=None, index=None, tokens=None):
     n = len(u)
     f = lambda a: None if a is None else torch.as_tensor(np.asarray(a, np.float32)).cuda()  # noqa: E731

@@ -118,6 +118,17 @@ def test_attention_pointers(lib):
     assert lib.mt_tree_attn_paged_block8(None, *[PTR] * 12, 1 << 40, None) == INVALID
 
 
+def test_attention_output_over_its_inputs(lib):
+    at = [(i + 1) << 32 for i in range(12)]  # q, k_new, v_new, ... far apart
+    d = _attn_desc()
+    size = 2 * 2 * 4 * 8 * 128
+    for i in (0, 1, 2):
+        for shift in (0, 16, 16 - size):  # the same, just behind, just before
+            args = list(at)
+            args[10] = args[i] + shift
+            assert lib.mt_tree_attn_paged_block8(d, *args, 1 << 40, None) == INVALID, (i, shift)
+
+
 @pytest.mark.parametrize("n, v, dt, rows, index, stride, want", [
     (-1, 10, 2, 4, PTR, 10, INVALID), (4, 0, 2, 4, PTR, 10, INVALID), (4, 500001, 2, 4, PTR, 10, UNSUPPORTED), (4, 10, 3, 4, PTR, 10, UNSUPPORTED),
     (4, 10, 2, 5, None, 10, INVALID), (4, 10, 2, -1, PTR, 10, INVALID), (4, 10, 2, 4, None, -10, INVALID), (0, 10, 2, 0, None, 10, OK), (0, 10, 2, 7, PTR, 10, OK),
