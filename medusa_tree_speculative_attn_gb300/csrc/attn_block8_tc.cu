@@ -32,10 +32,10 @@
 // are waited for and TMEM is freed.
 //
 // Bound by the roles' chains of steps, not by a unit: with 256 rows a tile takes
-// about 2050 cycles, of which the tensor cores work 1070 and the schedulers issue
-// half.  8 sequences of 32768 keys, 26 nodes, 64 query and 8 KV heads: 238 us, half
-// of the products' floor; 16 sequences of 512 to 8192 keys, 64 nodes, 32 query and 8
-// KV heads: 98 us; 64 sequences of 256 to 8192 keys, 32 rows a head: 184 us, 45 % of
+// about 1950 cycles, of which the tensor cores work 1070 and the schedulers issue
+// half.  8 sequences of 32768 keys, 26 nodes, 64 query and 8 KV heads: 229 us, 52 % of
+// the products' floor; 16 sequences of 512 to 8192 keys, 64 nodes, 32 query and 8
+// KV heads: 95 us; 64 sequences of 256 to 8192 keys, 32 rows a head: 181 us, 45 % of
 // a copy of the cache.
 #include <cudaTypedefs.h>
 
@@ -56,7 +56,11 @@ template <int D, int MT, int NP>
 struct Cfg {
   static constexpr int NH = D / 64;                   // 64-column halves of an fp16 value row
   static constexpr int kPTile = 128 * kTileKeys * 2;  // P of one M tile: 128 rows x 128 B
-  static constexpr int kPBytes = MT * kPTile;
+  // P tiles of an M tile, by turns: with two, P does not wait for the P V of the tile
+  // before.  8 sequences of 208 rows and 32768 keys 240 -> 229 us; with MT = 1 the ring
+  // slot that it takes costs more (64 sequences of 32 rows 181 -> 186, fp16 184 -> 198).
+  static constexpr int PB = MT == 2 ? 2 : 1;
+  static constexpr int kPBytes = MT * PB * kPTile;
   static constexpr int kKTile = kTileKeys * D;        // key codes, swizzled rows of D bytes
   static constexpr int kHalf = kTileKeys * 128;       // 64 values of 64 columns
   static constexpr int kVTile = NH * kHalf;
@@ -193,7 +197,7 @@ __global__ void __launch_bounds__(Cfg<D, MT, NP>::kThreads, 1)
                           const __grid_constant__ CUtensorMap map_kn, const __grid_constant__ CUtensorMap map_vn,
                           const __grid_constant__ CUtensorMap map_q, const Block8Params p) {
   using C = Cfg<D, MT, NP>;
-  constexpr int S = C::STAGES;
+  constexpr int S = C::STAGES, PB = C::PB;
   constexpr uint32_t kIdescQK = idesc_f8(128, kTileKeys);
   constexpr uint32_t kIdescPV = tc::idesc_f16(false, true, 128, D);
   const AttnParams& a = p.a;
@@ -207,16 +211,16 @@ __global__ void __launch_bounds__(Cfg<D, MT, NP>::kThreads, 1)
   uint64_t* full = land + S;                // [S] a tile's values are converted (tiles only)
   uint64_t* empty = full + S;               // [S] consumed by the MMAs (or copied to TMEM) and by the four converters
   uint64_t* s_full = empty + S;             // [MT] S computed
-  uint64_t* p_full = s_full + MT;           // [MT] P written (and O rescaled)
-  uint64_t* pv_done = p_full + MT;          // [MT] O += P V done
-  uint64_t* s_free = pv_done + MT;          // [MT] S read out
+  uint64_t* p_full = s_full + MT;           // [MT][PB] P written (and O rescaled)
+  uint64_t* pv_done = p_full + MT * C::PB;  // [MT][PB] O += P V done
+  uint64_t* s_free = pv_done + MT * C::PB;  // [MT] S read out
   uint64_t* o_free = s_free + MT;           // O of the previous piece read out
   uint64_t* fin = o_free + 1;               // [2] every MMA of each issuer done
   uint64_t* never = fin + 2;                // nothing arrives here (timeout test hook)
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(never + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   int* s_npieces = const_cast<int*>(abort_flag + 1);
-  static_assert((3 * 8 + 4 * 2 + 4) * 8 + 12 <= 1024, "barrier area");
+  static_assert((3 * 8 + 8 * 2 + 4) * 8 + 12 <= 1024, "barrier area");
   // per stage: key scales, log2 and inverse of the value scales, and how many rows
   // of each page hold keys of the sequence
   float* s_scale = reinterpret_cast<float*>(reinterpret_cast<uint8_t*>(bars) + 1024);  // [S][4][4]
@@ -234,8 +238,10 @@ __global__ void __launch_bounds__(Cfg<D, MT, NP>::kThreads, 1)
     }
     for (int m = 0; m < MT; ++m) {
       tc::mbar_init(&s_full[m], 2);  // the MMAs, and the issuer itself (below)
-      tc::mbar_init(&p_full[m], 4);
-      tc::mbar_init(&pv_done[m], 1);
+      for (int i = 0; i < C::PB; ++i) {
+        tc::mbar_init(&p_full[m * C::PB + i], 4);
+        tc::mbar_init(&pv_done[m * C::PB + i], 1);
+      }
       tc::mbar_init(&s_free[m], 4);
     }
     tc::mbar_init(o_free, C::kSoftmaxWarps);
@@ -516,11 +522,11 @@ __global__ void __launch_bounds__(Cfg<D, MT, NP>::kThreads, 1)
         const uint32_t v_u = sKV_u + st * C::kStage + C::kKTile;
         const uint64_t vd = tc::smem_desc(v_u, C::kHalf, 1024);
         for (int m = 0; m < MT; ++m) {
-          wait_all(&p_full[m], it & 1);
+          wait_all(&p_full[m * PB + it % PB], (it / PB) & 1);
           if (!ok) break;
           tc::tc_fence_after();
           const uint32_t d_t = tmem + C::o_col(m);
-          const uint64_t pd = tc::smem_desc(sP_u + m * C::kPTile, 16, 1024);
+          const uint64_t pd = tc::smem_desc(sP_u + (m * PB + it % PB) * C::kPTile, 16, 1024);
           if (first) {
             if (tc::elect_one()) tc::mma_f16_ss<false>(d_t, pd, vd, kIdescPV);
           } else {
@@ -529,7 +535,7 @@ __global__ void __launch_bounds__(Cfg<D, MT, NP>::kThreads, 1)
 #pragma unroll
           for (int kk = 1; kk < kTileKeys / 16; ++kk)  // next 16 keys: P +32 B, V +2048 B
             if (tc::elect_one()) tc::mma_f16_ss<true>(d_t, pd + (uint64_t)(kk * 2), vd + (uint64_t)(kk * 128), kIdescPV);
-          if (tc::elect_one()) tc::mma_commit(&pv_done[m]);
+          if (tc::elect_one()) tc::mma_commit(&pv_done[m * PB + it % PB]);
           __syncwarp();
         }
         if (!ok) break;
@@ -623,19 +629,23 @@ __global__ void __launch_bounds__(Cfg<D, MT, NP>::kThreads, 1)
           }
           sum = fmaf(f2_lo(s2) + f2_hi(s2), i4[g], sum);
         }
-        // P once the P.V of the tile before (which read it) is done: row r is
+        // P once the P.V that read its place last is done: row r is
         // 128 B (64 keys), 16-byte chunk c at c ^ (r % 8)
-        if (it >= 1) {
-          wait_all(&pv_done[m], (it - 1) & 1);
+        if (it >= (uint32_t)PB) {
+          wait_all(&pv_done[m * PB + it % PB], (it / PB - 1) & 1);
           if (!ok) break;
         }
-        uint8_t* prow = sP + m * C::kPTile + (r >> 3) * 1024 + (r & 7) * 128;
+        uint8_t* prow = sP + (m * PB + it % PB) * C::kPTile + (r >> 3) * 1024 + (r & 7) * 128;
 #pragma unroll
         for (int c = 0; c < 8; ++c)
           *reinterpret_cast<uint4*>(prow + ((c ^ (r & 7)) << 4)) =
               make_uint4(pk[4 * c], pk[4 * c + 1], pk[4 * c + 2], pk[4 * c + 3]);
         tc::fence_proxy_async_smem();
         if (__any_sync(0xffffffffu, need_o)) {
+          if (PB > 1 && it >= 1) {  // O of the tile before
+            wait_all(&pv_done[m * PB + (it - 1) % PB], ((it - 1) / PB) & 1);
+            if (!ok) break;
+          }
           tc::tc_fence_after();
 #pragma unroll 1
           for (int hh = 0; hh < D / 64; ++hh) {
@@ -652,12 +662,12 @@ __global__ void __launch_bounds__(Cfg<D, MT, NP>::kThreads, 1)
         m_run = m_new;
         tc::tc_fence_before();
         __syncwarp();
-        if (lane == 0) tc::mbar_arrive(&p_full[m]);
+        if (lane == 0) tc::mbar_arrive(&p_full[m * PB + it % PB]);
       }
       if (!ok) break;
       // epilogue, once the piece's last P.V is done: O / l to the output, or the
       // piece's own O / l with its maximum and sum to a partial slot
-      wait_all(&pv_done[m], (it - 1) & 1);
+      wait_all(&pv_done[m * PB + (it - 1) % PB], ((it - 1) / PB) & 1);
       if (!ok) break;
       tc::tc_fence_after();
       const int seg_row = m * 128 + r;
