@@ -27,14 +27,15 @@
 // The CTAs meet in distributed shared memory: each reads all sums and lists and
 // searches by itself, so a pass costs one cluster barrier.
 //
-// What it costs (cycles of one CTA with 16k tokens of bf16): 4k for the load, 4k
-// for a histogram of counts, 13k with masses, 6k for the last pass over the
-// weights, and 1k to 2k for each meeting of the cluster; few rows are bound by the
-// chain of meetings, many by the instructions of the weights.
-// One row of 32000 fp32 logits: 14.6 us.  64 rows of 128000 bf16 logits with
-// parameters of their own: 73 us, which is the longest row's chain of passes (the
-// schedulers issue half of the time in CTAs that are still at work, a quarter of
-// the whole).  256 rows of 32000 fp16 logits without filters: 20.5 us.
+// What it costs (cycles of one of two CTAs of an SM with 32k tokens of bf16): 9k for
+// the load, 5k for a histogram of counts, 17k with masses, 7k to 16k for a pass over
+// the tokens of a bin, 5k for a meeting of the cluster with its search, 12k to 16k
+// for the last pass over the weights, 8k for the walk to the token; few rows are
+// bound by the chain of meetings, many by the instructions.  The weights are worked
+// out two at a time, in instructions for pairs.
+// One row of 32000 fp32 logits: 14.2 us.  64 rows of 128000 bf16 logits with
+// parameters of their own: 56 us, which is the longest row's chain of passes.  256
+// rows of 32000 fp16 logits without filters: 19.4 us.
 #include <cooperative_groups.h>
 
 #include <atomic>
@@ -82,9 +83,9 @@ struct Scale {
   float hi, lo;    // log2(e) / temperature as a sum
 };
 
-constexpr int kTable = 128;
+constexpr unsigned kTable = 128;
 
-struct Table {  // 2^(30 + j/128)
+struct Table {  // entry k: 2^(30 + (127 - k)/128)
   int v[kTable];
 };
 
@@ -96,36 +97,73 @@ __device__ __forceinline__ unsigned long long fraction64(float f) {
   return up >= 0 ? m << up : up > -24 ? m >> -up : 0ull;
 }
 
-// Weight of x: 2^44 exp((x - m) / t), cut to a whole number.
-// 2^e with e = n/128 + r, |r| <= 1/256:  table[n mod 128] * (1 + q) * 2^(n div 128),
-// q = 2^r - 1.  n is read off the low bits of e * 128 + 1.5 * 2^23; the product
-// with q is a 32-bit high product of the table's 2^30 .. 2^31 and q * 2^32 (the
-// only conversion), and the power of two a 32-bit shift and a 64-bit product.
+// Two fp32 in one register pair, for the instructions that take both at once.
+using F2 = unsigned long long;
+__device__ __forceinline__ F2 f2_of(float a, float b) {
+  F2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ F2 f2_of(float a) { return f2_of(a, a); }
+__device__ __forceinline__ float f2_get(F2 x, int i) { return __uint_as_float((uint32_t)(i ? x >> 32 : x)); }
+__device__ __forceinline__ F2 f2_fma(F2 a, F2 b, F2 c) {
+  F2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ F2 f2_mul(F2 a, F2 b) {
+  F2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ F2 f2_add(F2 a, F2 b) {
+  F2 r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ F2 f2_sub(F2 a, F2 b) { return f2_fma(b, f2_of(-1.f), a); }
+
+// Weights of two values: 2^44 exp((x - m) / t), cut to a whole number.
+// 2^e with e = n/128 + r, |r| <= 1/256:  2^(30 + (n mod 128)/128) * (1 + q) *
+// 2^(n div 128 - 30), q = 2^r - 1.  -n (>= 0) is read off the low bits of
+// -e * 128 + 1.5 * 2^23; with 127 added, its low 7 bits are the table's index and the
+// others the shift.  The product with q is a 32-bit high product of the table's
+// 2^30 .. 2^31 and q * 2^32 (the only conversion).  -inf shifts everything out.
 // TWO: the rounding error of x - m by the form for any two floats; 16-bit values
 // need only the form for |x| <= |m|, because elsewhere their difference is exact.
 template <bool TWO>
-__device__ __forceinline__ unsigned long long weight(float x, const Scale& s, const int* table) {
-  const float d = x == s.m ? 0.f : x - s.m;  // 0 for x = m = +inf, too
-  const float p = d * s.hi;
-  float err;
+__device__ __forceinline__ void weights(float x0, float x1, const Scale& s, const int* table, unsigned long long (&w)[2]) {
+  const F2 x = f2_of(x0, x1), m = f2_of(s.m), hi = f2_of(s.hi);
+  F2 d = f2_sub(x, m);
+  d = f2_of(fminf(f2_get(d, 0), 0.f), fminf(f2_get(d, 1), 0.f));  // 0 for x = m = +inf, too
+  const F2 minus_p = f2_mul(d, f2_of(-s.hi));
+  F2 err;
   if (TWO) {
-    const float bb = d - x;
-    err = (x - (d - bb)) + (-s.m - bb);
+    const F2 bb = f2_sub(d, x);
+    err = f2_add(f2_sub(x, f2_sub(d, bb)), f2_sub(f2_of(-s.m), bb));
   } else {
-    err = x - (d + s.m);
+    err = f2_sub(x, f2_add(d, m));
   }
-  const float e = fmaf(d, s.hi, -p) + fmaf(d, s.lo, err * s.hi);
-  const float z = fmaf(p, 128.f, 12582912.f);
-  const int n = __float_as_int(z) - 0x4B400000;
-  const float r = fmaf(z - 12582912.f, -0.0078125f, p) + e;
+  const F2 e = f2_add(f2_fma(d, hi, minus_p), f2_fma(d, f2_of(s.lo), f2_mul(err, hi)));
+  const F2 z = f2_fma(minus_p, f2_of(128.f), f2_of(12582912.f));
+  const F2 minus_r = f2_fma(f2_add(z, f2_of(-12582912.f)), f2_of(-0.0078125f), minus_p);
+  const F2 r = f2_sub(e, minus_r);
   constexpr float k32 = 4294967296.f;
-  float q = fmaf(r, 5.5504109e-2f * k32, 2.4022651e-1f * k32);  // ln2^3/6, ln2^2/2
-  q = fmaf(r, q, 6.9314718e-1f * k32) * r;                      // ln2
-  const int t = table[n & (kTable - 1)];
-  const unsigned w = (unsigned)(t + __mulhi(t, __float2int_rn(q)));
-  const int up = (kWBits - 30) + (n >> 7);  // n <= 0
-  const unsigned a = p > -45.f ? w >> max(0, -up) : 0u;  // below one unit (-inf too): nothing
-  return (unsigned long long)a * (1u << (max(0, up) & 31));
+  F2 q = f2_fma(r, f2_of(5.5504109e-2f * k32), f2_of(2.4022651e-1f * k32));  // ln2^3/6, ln2^2/2
+  q = f2_mul(f2_fma(r, q, f2_of(6.9314718e-1f * k32)), r);                   // ln2
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const unsigned n = __float_as_uint(f2_get(z, i)) - (0x4B400000u - (kTable - 1));
+    const int t = table[n & (kTable - 1)];
+    const unsigned v = (unsigned)(t + __mulhi(t, __float2int_rn(f2_get(q, i))));
+    w[i] = ((unsigned long long)v << (kWBits - 30)) >> min(n / kTable, 63u);
+  }
+}
+template <bool TWO>
+__device__ __forceinline__ unsigned long long weight(float x, const Scale& s, const int* table) {
+  unsigned long long w[2];
+  weights<TWO>(x, x, s, table, w);
+  return w[0];
 }
 
 // A histogram: counts, and the sums of the low and high 16 bits of the weights
@@ -165,6 +203,7 @@ struct __align__(16) Smem {
   unsigned part_cnt[kMaxCluster][kBins];
   unsigned long long part_mass[kMaxCluster][kBins];
   Found bins[kBins];
+  unsigned long long unit[kBins];        // a token's mass, where a bin is one value
   unsigned long long whole;
   unsigned long long rank_key[kList], rank_mass[kList];
   Cut cut;
@@ -271,6 +310,28 @@ struct Slice {
 #pragma unroll
     for (int e = 0; e < EPV; ++e) f(Act<T>::to_f(t[e]), e);
   }
+  // f(x0, x1, v, e) over the pairs of elements (e and e + 1) of this lane's vectors;
+  // vectors whose elements are all below `least` may be left out.  Those that reach
+  // out of the row go to g(x, v, e) instead, element by element, without what lies
+  // outside.
+  template <class F, class G>
+  __device__ __forceinline__ void pairs(float least, F f, G g) const {
+#pragma unroll 1
+    for (int v = lbeg; v < lend; ++v) {
+      const uint4 r = get(v);
+      if (vec_max<T>(r) < least) continue;
+      if (index(v, 0) >= 0 && index(v, EPV) <= V) {
+        T t[EPV];
+        memcpy(t, &r, 16);
+#pragma unroll
+        for (int e = 0; e < EPV; e += 2) f(Act<T>::to_f(t[e]), Act<T>::to_f(t[e + 1]), v, e);
+      } else {
+#pragma unroll 1
+        for (int e = 0; e < EPV; ++e)
+          if (in_row(v, e)) g(fmaxf(Act<T>::to_f(row[index(v, e)]), -INFINITY), v, e);
+      }
+    }
+  }
   // f(x, v, e) over this lane's elements; vectors whose elements are all below
   // `least` may be left out
   template <class F>
@@ -325,8 +386,8 @@ __device__ __forceinline__ void clear(Hist& h) {
 
 // The cluster's histogram in sm.bins, each bin with what lies before it (base_cnt
 // and base_mass included).  The histogram is left zero; turn: which of the two
-// places the sums pass through.
-__device__ __noinline__ void meet(Smem& sm, int turn, unsigned base_cnt, unsigned long long base_mass) {
+// places the sums pass through; units: the masses are counts times sm.unit.
+__device__ __noinline__ void meet(Smem& sm, int turn, unsigned base_cnt, unsigned long long base_mass, bool units) {
   cg::cluster_group cl = cg::this_cluster();
   const int tid = threadIdx.x, lane = tid & 31, C = (int)cl.num_blocks();
   __syncthreads();
@@ -347,7 +408,7 @@ __device__ __noinline__ void meet(Smem& sm, int turn, unsigned base_cnt, unsigne
     }
     if (c == 0) {
       sm.bin_cnt[turn][b] = n;
-      sm.bin_mass[turn][b] = m;
+      sm.bin_mass[turn][b] = units ? n * sm.unit[b] : m;
     }
   }
   cl.sync();
@@ -412,7 +473,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
   const int C = (int)cl.num_blocks(), rank = (int)cl.block_rank();
   const int n = blockIdx.x / C;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  if (tid < kTable) sm.table[tid] = table.v[tid];
+  if (tid < (int)kTable) sm.table[tid] = table.v[tid];
   if (tid < 2) sm.list_n[tid] = 0;
   clear(sm.hist);
   pdl_wait();
@@ -494,20 +555,34 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
     auto weight_of = [&](float x) {  // 2^32 for the maximum
       return (weight<TWO>(x, sc, sm.table) + (1u << (kWBits - 33))) >> (kWBits - 32);
     };
+    auto rounded = [](unsigned long long w) { return (w + (1u << (kWBits - 33))) >> (kWBits - 32); };
+    auto add_mass = [&](int b, unsigned long long w) {
+      atomicAdd(&sm.hist.lo[b][lane], (unsigned)w & 0xffffu);
+      atomicAdd(&sm.hist.hi[b][lane], (unsigned)(w >> 16));
+    };
     auto add = [&](int b, float x) {
       atomicAdd(&sm.hist.cnt[b][lane], 1u);
-      if (use_p) {
-        const unsigned long long w = weight_of(x);
-        const unsigned l = (unsigned)w & 0xffffu, g = (unsigned)(w >> 16);
-        if (l) atomicAdd(&sm.hist.lo[b][lane], l);
-        if (g) atomicAdd(&sm.hist.hi[b][lane], g);
-      }
+      if (use_p) add_mass(b, weight_of(x));
     };
-    s.each(-INFINITY, [&](float x, int v, int e) {
-      if (s.in_row(v, e)) add(bin_of(x), x);
-    });
+    auto add_one = [&](float x, int, int) { add(bin_of(x), x); };
+    if (use_p) {
+      s.pairs(-INFINITY, [&](float x0, float x1, int, int) {
+        const int b0 = bin_of(x0), b1 = bin_of(x1);
+        unsigned long long w[2];
+        weights<TWO>(x0, x1, sc, sm.table, w);
+        atomicAdd(&sm.hist.cnt[b0][lane], 1u);
+        add_mass(b0, rounded(w[0]));
+        atomicAdd(&sm.hist.cnt[b1][lane], 1u);
+        add_mass(b1, rounded(w[1]));
+      }, add_one);
+    } else {
+      s.pairs(-INFINITY, [&](float x0, float x1, int, int) {
+        atomicAdd(&sm.hist.cnt[bin_of(x0)][lane], 1u);
+        atomicAdd(&sm.hist.cnt[bin_of(x1)][lane], 1u);
+      }, add_one);
+    }
     int turn = 0;
-    meet(sm, turn, 0u, 0ull);
+    meet(sm, turn, 0u, 0ull, false);
     unsigned long long whole = sm.whole;
     const int bin_k = use_k ? find(sm, (unsigned)want_k, 0ull) : 0;
     Found in_k = sm.bins[bin_k];
@@ -529,12 +604,12 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
       hi = min(hi, (uint32_t)(best >> 32) >> KS);
       for (int pass = 0; pass < 7; ++pass) {  // 6 of at most 32 bits each, then one value or a list
         // whole vectors below the range are passed over (keys below -inf's are no numbers)
-        const float least = lo <= ord_of(-INFINITY) >> KS ? -INFINITY : value_of_key<KS>(lo);
+        const float least = lo <= ord_of(-INFINITY) >> KS ? -INFINITY : value_of_key<KS>(lo), most = value_of_key<KS>(hi);
         if (f.in <= kList) {
           // few tokens: listed, and ranked by (key, lower index) by four threads each
           s.each(least, [&](float x, int v, int e) {
+            if (x < least || x > most || bin_of(x) != bin || !s.in_row(v, e)) return;
             const uint32_t k = ord_of(x) >> KS;
-            if (k < lo || k > hi || bin_of(x) != bin || !s.in_row(v, e)) return;
             const unsigned at = atomicAdd(&sm.list_n[which], 1u);
             if (at < kList) {  // f.in says so
               sm.list_key[which][at] = k;
@@ -590,11 +665,16 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
         if (hi == lo) break;
         const int shift = max(0, 32 - __clz(hi - lo) - 6);
         s.each(least, [&](float x, int v, int e) {
+          if (x < least || x > most || bin_of(x) != bin || !s.in_row(v, e)) return;
           const uint32_t k = ord_of(x) >> KS;
-          if (k >= lo && k <= hi && bin_of(x) == bin && s.in_row(v, e)) add((int)((hi - k) >> shift), x);
+          if (shift) add((int)((hi - k) >> shift), x);
+          else atomicAdd(&sm.hist.cnt[hi - k][lane], 1u);
         });
+        // a bin of one value needs no masses: the rare lanes in the range would hold up
+        // every warp for them (64 rows of 128k bf16, top-p 0.9: 69 -> 63 us)
+        if (shift == 0 && use_p && tid < kBins) sm.unit[tid] = hi >= (unsigned)tid ? weight_of(value_of_key<KS>(hi - tid)) : 0ull;
         turn ^= 1;
-        meet(sm, turn, f.cnt, f.mass);
+        meet(sm, turn, f.cnt, f.mass, shift == 0 && use_p);
         const int b = find(sm, want_cnt, want_mass);
         f = sm.bins[b];
         __syncthreads();
@@ -634,23 +714,41 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
   const bool cuts = use_k || use_p;
   __syncthreads();
   const float x_min = sm.x_min;
+  // the smallest value that is kept, and whether of its tokens only some are
+  const float cut_x = cuts ? value_of_key<KS>(cut.key) : -INFINITY;
+  const float least = fmaxf(x_min, cut_x);
+  const bool some = cuts && cut_x >= x_min;
   auto kind = [&](float x, int v, int e) {  // 2: kept, 1: equal to the cut, 0: not kept
-    if (x < x_min) return 0;
-    if (!cuts) return 2;
-    const uint32_t k = ord_of(x) >> KS;
-    if (k != cut.key) return k > cut.key ? 2 : 0;
+    if (x < least) return 0;
+    if (x > least || !some) return 2;
     return cut.idx >= 0 ? (s.index(v, e) <= cut.idx ? 2 : 0) : s.in_row(v, e) ? 1 : 0;
   };
 
   // ---- kept mass of each lane's part, in vocab order; of the tokens equal to the
   // cut the first `stay` count ----
-  const float least = cuts ? fmaxf(x_min, value_of_key<KS>(cut.key)) : x_min;
   unsigned long long lane_mass = 0;
   unsigned lane_ties = 0;
   if (!cuts && x_min == -INFINITY) {
-    s.each(-INFINITY, [&](float x, int, int) { lane_mass += weight<TWO>(x, sc, sm.table); });
+    s.pairs(-INFINITY, [&](float x0, float x1, int, int) {
+      unsigned long long w[2];
+      weights<TWO>(x0, x1, sc, sm.table, w);
+      lane_mass += w[0] + w[1];
+    }, [&](float x, int, int) { lane_mass += weight<TWO>(x, sc, sm.table); });
   } else {
-    s.each(least, [&](float x, int v, int e) {
+    s.pairs(least, [&](float x0, float x1, int v, int e) {
+      bool in0 = x0 > least, in1 = x1 > least;
+      if (x0 == least || x1 == least) {
+        const int k0 = kind(x0, v, e), k1 = kind(x1, v, e + 1);
+        in0 = k0 == 2;
+        in1 = k1 == 2;
+        lane_ties += (k0 == 1) + (k1 == 1);
+      }
+      if (in0 || in1) {
+        unsigned long long w[2];
+        weights<TWO>(x0, x1, sc, sm.table, w);
+        lane_mass += (in0 ? w[0] : 0ull) + (in1 ? w[1] : 0ull);
+      }
+    }, [&](float x, int v, int e) {
       const int k = kind(x, v, e);
       if (k == 2) lane_mass += weight<TWO>(x, sc, sm.table);
       lane_ties += k == 1;
@@ -766,7 +864,7 @@ constexpr int kMaxDevices = 64;
 
 Table make_table() {
   Table t;
-  for (int j = 0; j < kTable; ++j) t.v[j] = (int)(std::exp2(30.0 + j / (double)kTable) + 0.5);
+  for (int j = 0; j < (int)kTable; ++j) t.v[kTable - 1 - j] = (int)(std::exp2(30.0 + j / 128.0) + 0.5);
   return t;
 }
 
@@ -803,9 +901,9 @@ cudaError_t launch_s(const SampleParams& a, int C, size_t smem, cudaStream_t str
 // CTAs per row: enough that a lane has at most eight vectors of a slice, and, when
 // rows are few, until the grid is about one resident wave (two CTAs per SM) or a
 // lane has less than one vector.  One wave, because a row's chain of meetings is
-// what a second wave would repeat: 64 rows of 128k bf16, top-p, take 73 us with 4
-// CTAs a row and 90 with 8; 256 rows of 32k fp16, unfiltered, 20 with 1 and 26
-// with 2.
+// what a second wave would repeat: before the weights went in pairs, 64 rows of 128k
+// bf16, top-p, took 73 us with 4 CTAs a row and 90 with 8; 256 rows of 32k fp16,
+// unfiltered, 20 with 1 and 26 with 2.
 template <typename T>
 cudaError_t launch_t(const SampleParams& a, cudaStream_t stream) {
   constexpr int EPV = 16 / (int)sizeof(T);
