@@ -435,9 +435,7 @@ int mt_kv_append_accepted(const mt_append_desc* desc, int tree_size, int max_dep
  * they were.  desc: dtype MT_F16 or MT_BF16, cache_dtype MT_E4M3; num_splits,
  * kernel, k_scale and v_scale are not used; any number of query heads per KV
  * head.  out must not overlap q, k_new or v_new.  Accumulation in fp32; queries
- * keep their bits, softmax weights are rounded to fp16, and, where there are more
- * than 16 query rows per KV head (T * Hq / Hkv), a split segment's pieces to the act
- * dtype.  A query row with a NaN or an infinity gives NaN, and so does a row that
+ * keep their bits, softmax weights are rounded to fp16.  A query row with a NaN or an infinity gives NaN, and so does a row that
  * sees a key with a NaN or a new token with a NaN among its values; a cached value's
  * NaN reaches its own column.  What a row does not see has no effect on it.
  * workspace: mt_tree_attn_block8_workspace_size(desc) bytes, zero-filled before

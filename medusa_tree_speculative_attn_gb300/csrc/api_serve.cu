@@ -81,13 +81,11 @@ int block8_ws(const mt_attn_desc* d, Block8Ws* w) {
   w->counters = take(kMaxFragCtas * sizeof(unsigned));
   const size_t part = (size_t)nslots * w->part_rows;
   w->ml = take(part * sizeof(float2));
-  if (!w->plan.tc) {
-    w->o = take(part * d->head_dim * sizeof(float));
-  } else {
+  w->o = take(part * d->head_dim * sizeof(float));
+  if (w->plan.tc) {
     const size_t nodes = (size_t)d->batch * d->tree_size, qrows = nodes * d->num_q_heads;
     const size_t blocks = (size_t)d->batch * d->num_kv_heads * ((d->tree_size + 15) / 16);
     if ((long long)blocks * 16 >= (1ll << 31)) return MT_ERR_UNSUPPORTED;
-    w->o = take(part * d->head_dim * 2);
     w->pfx = take(sizeof(int) * (size_t)(d->batch + 1));
     w->anc = take(nodes * sizeof(unsigned long long));
     w->pieces = take(sizeof(int) * (size_t)piece_rec_offset(w->G) + sizeof(PieceRec) * kMaxPieceRecs * (size_t)w->G);
@@ -280,7 +278,7 @@ int mt_tree_attn_paged_block8(const mt_attn_desc* d, const void* q, const void* 
   st = cuda_status(launch_block8_prep(p, d->dtype, stream));
   if (st == MT_OK) st = cuda_status(launch_attn_block8_tc(p, d->dtype, stream));
   if (st != MT_OK) return st;
-  return cuda_status(launch_combine(a, d->dtype, stream));
+  return cuda_status(launch_block8_combine(p, d->dtype, stream));
 }
 
 int mt_sample_tokens(int num_rows, int vocab, mt_dtype logits_dtype, const void* logits, int num_logit_rows,

@@ -730,8 +730,8 @@ Block8Plan block8_plan(int batch, int kv_heads, int rows, int g, int max_blocks,
   Block8Plan p{};
   // Up to 16 rows the register-fragment kernel, which wastes no rows; from 17 on the
   // tensor-core kernel, whose tile has 128 (256) rows.  64 sequences of 256 to 8192
-  // tokens, 8 KV heads: 16 rows 115 us against 184, 24 rows 195 against 184, 32 rows
-  // 205 against 184; 4 sequences of 2000: 20.9 against 21.9, and 32.8 against 22.6.
+  // tokens, 8 KV heads: 16 rows 115 us against 177, 24 rows 195 against 177, 32 rows
+  // 205 against 177; 4 sequences of 2000: 20.9 against 21.9, and 32.8 against 22.6.
   // The latter keeps a token's g rows in one tile, so where g does not divide 128 the
   // former takes every count.  fp16 queries fill three operand parts, and with those
   // two tiles do not fit in TMEM.

@@ -33,9 +33,9 @@
 //
 // Bound by the roles' chains of steps, not by a unit: with 256 rows a tile takes
 // about 1950 cycles, of which the tensor cores work 1070 and the schedulers issue
-// half.  8 sequences of 32768 keys, 26 nodes, 64 query and 8 KV heads: 229 us, 52 % of
+// half.  8 sequences of 32768 keys, 26 nodes, 64 query and 8 KV heads: 231 us, 52 % of
 // the products' floor; 16 sequences of 512 to 8192 keys, 64 nodes, 32 query and 8
-// KV heads: 95 us; 64 sequences of 256 to 8192 keys, 32 rows a head: 181 us, 45 % of
+// KV heads: 96 us; 64 sequences of 256 to 8192 keys, 32 rows a head: 177 us, 46 % of
 // a copy of the cache.
 #include <cudaTypedefs.h>
 
@@ -103,6 +103,30 @@ __device__ __forceinline__ uint32_t pack_h2(float a, float b) {
   uint32_t r;
   memcpy(&r, &h, 4);
   return r;
+}
+
+// 32 lanes x 32 bits, 32 consecutive columns per thread; and the wait, through which
+// the registers pass so that no use of them can move ahead of it.
+__device__ __forceinline__ void tmem_ld_x32(uint32_t taddr, uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
+        "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+        "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(taddr));
+}
+__device__ __forceinline__ void tmem_ld_wait(uint32_t (&r)[32]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+                 "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]),
+                 "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]),
+                 "+r"(r[23]), "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29])
+               :
+               : "memory");
+  asm volatile("" : "+r"(r[30]), "+r"(r[31]));
 }
 
 // Two fp32 in one register pair, for the instructions that take both at once.
@@ -672,36 +696,31 @@ __global__ void __launch_bounds__(Cfg<D, MT, NP>::kThreads, 1)
       tc::tc_fence_after();
       const int seg_row = m * 128 + r;
       const float inv = l_run == 0.f ? 0.f : 1.f / l_run;  // a NaN sum makes the row NaN
-#pragma unroll 1
-      for (int hh = 0; hh < D / 64; ++hh) {
-        uint32_t o[64];
-        tc::tmem_ld_x64(tmem + lane_addr + C::o_col(m) + 64 * hh, o);
-        tc::tmem_ld_wait();
-        if (row_ok) {
-          uint4* dst;
-          size_t step;
-          if (pc.slot < 0) {
-            dst = reinterpret_cast<uint4*>(static_cast<T*>(a.out) + (((size_t)pc.b * a.T + node) * a.Hq + h) * D + 64 * hh);
-            step = 1;
-          } else {
-            dst = static_cast<uint4*>(a.part_o) + ((size_t)pc.slot * (D / 8) + 8 * hh) * a.part_rows + seg_row;
-            step = a.part_rows;
-          }
+#pragma unroll 1  // 32 columns at a time: with 64 the code is long enough to slow the other roles (fp16 12%)
+      for (int col = 0; col < D; col += 32) {
+        uint32_t o[32];
+        tmem_ld_x32(tmem + lane_addr + C::o_col(m) + col, o);
+        tmem_ld_wait(o);
 #pragma unroll
-          for (int c = 0; c < 8; ++c) {
+        for (int c = 0; c < 32; ++c) o[c] = __float_as_uint(__uint_as_float(o[c]) * inv);
+        if (row_ok && pc.slot < 0) {
+          uint4* dst = reinterpret_cast<uint4*>(static_cast<T*>(a.out) + (((size_t)pc.b * a.T + node) * a.Hq + h) * D + col);
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
             T v[8];
 #pragma unroll
-            for (int e = 0; e < 8; ++e) v[e] = Act<T>::from_f(__uint_as_float(o[8 * c + e]) * inv);
+            for (int e = 0; e < 8; ++e) v[e] = Act<T>::from_f(__uint_as_float(o[8 * c + e]));
             uint4 w;
             memcpy(&w, v, 16);
-            dst[c * step] = w;
+            dst[c] = w;
           }
+        } else if (row_ok) {
+          uint4* dst = reinterpret_cast<uint4*>(a.part_o) + ((size_t)pc.slot * (D / 4) + col / 4) * a.part_rows + seg_row;
+#pragma unroll
+          for (int c = 0; c < 8; ++c) dst[(size_t)c * a.part_rows] = make_uint4(o[4 * c], o[4 * c + 1], o[4 * c + 2], o[4 * c + 3]);
         }
       }
-      // (a piece of nothing but NaN scores has a NaN sum and no maximum: it takes part
-      // in the combine with one)
-      if (row_ok && pc.slot >= 0)
-        a.part_ml[(size_t)pc.slot * a.part_rows + seg_row] = make_float2(l_run == l_run ? m_run : fmaxf(m_run, 0.f), l_run);
+      if (row_ok && pc.slot >= 0) a.part_ml[(size_t)pc.slot * a.part_rows + seg_row] = make_float2(m_run, l_run);
       tc::tc_fence_before();
       __syncwarp();
       if (lane == 0) tc::mbar_arrive(o_free);
@@ -712,6 +731,89 @@ __global__ void __launch_bounds__(Cfg<D, MT, NP>::kThreads, 1)
   __syncthreads();
   tc::tc_fence_after();
   if (warp == C::kQkWarp) tc::tmem_dealloc(tmem, C::kTmemCols);
+}
+
+// Merges a split segment's pieces, each left as O / l in fp32 with its maximum and
+// sum: a block per 32 rows of a segment, a lane per row, a warp per eight columns of
+// every 64, four pieces in flight.  (In the act dtype the pieces cost a second
+// rounding, 1.4 times the whole error.)
+constexpr int kCombineWarps = 8;
+
+template <typename T, int D>
+__global__ void __launch_bounds__(kCombineWarps * 32) block8_combine_kernel(const AttnParams a) {
+  constexpr int U = 4, N = D / 64;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const Sched& s = a.sched;
+  const int HR = s.Hkv * s.nrg, blocks = (a.part_rows + 31) / 32;
+  const int seg = blockIdx.x / blocks, r = blockIdx.x % blocks * 32 + lane;
+  const int b = seg / HR, kvh = seg % HR / s.nrg, rg = seg % s.nrg;
+  pdl_wait();
+  const int nt = s.tile_pfx[b + 1] - s.tile_pfx[b];
+  if (nt == 0) return;
+  const long long X = sched_total_cost(s), t0 = (long long)s.tile_pfx[b] * HR + (long long)(seg - b * HR) * nt;
+  const int c0 = sched_cta_of(sched_tile_cost(s, t0, seg), X, s.G);
+  const int c1 = sched_cta_of(sched_tile_cost(s, t0 + nt - 1, seg), X, s.G);
+  const int row = rg * a.rows_per_group + r;
+  if (c0 == c1 || r >= a.part_rows || row >= a.rows) return;  // one piece has written the output
+  float M = -INFINITY, l = 0.f, acc[N][8] = {};
+  const float4* part = reinterpret_cast<const float4*>(a.part_o);
+#pragma unroll 1
+  for (int k0 = c0; k0 <= c1; k0 += U) {
+    float2 ml[U];
+    float4 v[U][N][2];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      // a CTA between the first and the last may hold no tile, and has written
+      // nothing then
+      const int cta = k0 + u;
+      ml[u] = make_float2(-INFINITY, 0.f);
+      if (cta > c1 || !(cta == c0 || cta == c1 || X * (cta + 1) / s.G != X * cta / s.G)) continue;
+      const size_t slot = (size_t)seg + cta;
+      ml[u] = a.part_ml[slot * a.part_rows + r];
+#pragma unroll
+      for (int n = 0; n < N; ++n)
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+          v[u][n][h] = part[(slot * (D / 4) + 16 * n + 2 * warp + h) * a.part_rows + r];
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      if (ml[u].y == 0.f) continue;  // no piece, or one that saw no key of the row (a NaN goes on)
+      const float m = fmaxf(M, ml[u].x);
+      const float fo = fast_exp2(M - m), fn = fast_exp2(ml[u].x - m) * ml[u].y;
+      l = fmaf(l, fo, fn);
+      M = m;
+#pragma unroll
+      for (int n = 0; n < N; ++n)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          float* o = acc[n] + 4 * h;
+          const float4 x = v[u][n][h];
+          o[0] = fmaf(x.x, fn, o[0] * fo);
+          o[1] = fmaf(x.y, fn, o[1] * fo);
+          o[2] = fmaf(x.z, fn, o[2] * fo);
+          o[3] = fmaf(x.w, fn, o[3] * fo);
+        }
+    }
+  }
+  const float inv = l == 0.f ? 0.f : 1.f / l;
+  const int node = row / a.g, h = kvh * a.g + row % a.g;
+  T* out = static_cast<T*>(a.out) + (((size_t)b * a.T + node) * a.Hq + h) * D + 8 * warp;
+#pragma unroll
+  for (int n = 0; n < N; ++n) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) acc[n][e] *= inv;
+    Row8<T> w;
+    w.from_f(acc[n]);
+    w.store(out + 64 * n);
+  }
+}
+
+template <typename T, int D>
+cudaError_t launch_combine_t(const AttnParams& a, cudaStream_t stream) {
+  const long long blocks = (long long)a.B * a.sched.Hkv * a.sched.nrg * ((a.part_rows + 31) / 32);
+  if (blocks >= (1ll << 31)) return cudaErrorInvalidValue;
+  return launch_pdl(block8_combine_kernel<T, D>, dim3((unsigned)blocks), dim3(kCombineWarps * 32), 0, stream, a);
 }
 
 PFN_cuTensorMapEncodeTiled_v12000 get_encode() {
@@ -790,6 +892,12 @@ cudaError_t launch_d(const Block8Params& p, int dtype, cudaStream_t stream) {
 
 cudaError_t launch_attn_block8_tc(const Block8Params& p, int dtype, cudaStream_t stream) {
   return p.a.D == 64 ? launch_d<64>(p, dtype, stream) : launch_d<128>(p, dtype, stream);
+}
+
+cudaError_t launch_block8_combine(const Block8Params& p, int dtype, cudaStream_t stream) {
+  if (p.a.D == 64)
+    return dtype == 1 ? launch_combine_t<__half, 64>(p.a, stream) : launch_combine_t<__nv_bfloat16, 64>(p.a, stream);
+  return dtype == 1 ? launch_combine_t<__half, 128>(p.a, stream) : launch_combine_t<__nv_bfloat16, 128>(p.a, stream);
 }
 
 }  // namespace mt

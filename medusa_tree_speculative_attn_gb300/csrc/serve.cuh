@@ -291,6 +291,7 @@ struct Block8Plan {
 Block8Plan block8_plan(int batch, int kv_heads, int rows, int g, int max_blocks, int tree_size, int dtype, int sms);
 cudaError_t launch_attn_block8(const Block8Params& p, int dtype, cudaStream_t stream);
 cudaError_t launch_block8_prep(const Block8Params& p, int dtype, cudaStream_t stream);
+cudaError_t launch_block8_combine(const Block8Params& p, int dtype, cudaStream_t stream);
 cudaError_t launch_attn_block8_tc(const Block8Params& p, int dtype, cudaStream_t stream);
 
 // ---------------------------------------------------------------------------
