@@ -33,9 +33,9 @@
 //
 // Bound by the roles' chains of steps, not by a unit: with 256 rows a tile takes
 // about 1950 cycles, of which the tensor cores work 1070 and the schedulers issue
-// half.  8 sequences of 32768 keys, 26 nodes, 64 query and 8 KV heads: 231 us, 52 % of
+// half.  8 sequences of 32768 keys, 26 nodes, 64 query and 8 KV heads: 227 us, 53 % of
 // the products' floor; 16 sequences of 512 to 8192 keys, 64 nodes, 32 query and 8
-// KV heads: 96 us; 64 sequences of 256 to 8192 keys, 32 rows a head: 177 us, 46 % of
+// KV heads: 94 us; 64 sequences of 256 to 8192 keys, 32 rows a head: 176 us, 47 % of
 // a copy of the cache.
 #include <cudaTypedefs.h>
 
@@ -501,24 +501,25 @@ __global__ void __launch_bounds__(Cfg<D, MT, NP>::kThreads, 1)
         phase ^= 1u << st;
         if (!ok) break;
         const uint64_t kd = desc_rows8<D>(sKV_u + st * C::kStage);
+#pragma unroll 1  // (short code: 2% with MT = 2)
         for (int m = 0; m < MT; ++m) {
           if (it >= 1) {
             wait_all(&s_free[m], (it - 1) & 1);
             if (!ok) break;
           }
           tc::tc_fence_after();
+          if (tc::elect_one()) {
 #pragma unroll
-          for (int part = 0; part < NP; ++part)
+            for (int part = 0; part < NP; ++part)
 #pragma unroll
-            for (int kk = 0; kk < D / 32; ++kk) {
-              const uint32_t q = tmem + C::q_col(m, part) + kk * 8;
-              if (part == 0 && kk == 0) {
-                if (tc::elect_one()) mma_f8_ts<false>(tmem + C::s_col(m), q, kd, kIdescQK);
-              } else {
-                if (tc::elect_one()) mma_f8_ts<true>(tmem + C::s_col(m), q, kd + (uint64_t)(kk * 2), kIdescQK);
+              for (int kk = 0; kk < D / 32; ++kk) {
+                const uint32_t q = tmem + C::q_col(m, part) + kk * 8;
+                if (part == 0 && kk == 0) mma_f8_ts<false>(tmem + C::s_col(m), q, kd, kIdescQK);
+                else mma_f8_ts<true>(tmem + C::s_col(m), q, kd + (uint64_t)(kk * 2), kIdescQK);
               }
-            }
-          if (tc::elect_one()) tc::mma_commit(&s_full[m]);
+            tc::mma_commit(&s_full[m]);
+          }
+          __syncwarp();
           // passes on what this warp acquired with the tile: the softmax reads the
           // page scales without a wait of its own on `land` (4% of the 32k workload)
           if (lane == 0) tc::mbar_arrive(&s_full[m]);
@@ -545,6 +546,7 @@ __global__ void __launch_bounds__(Cfg<D, MT, NP>::kThreads, 1)
         }
         const uint32_t v_u = sKV_u + st * C::kStage + C::kKTile;
         const uint64_t vd = tc::smem_desc(v_u, C::kHalf, 1024);
+#pragma unroll 1
         for (int m = 0; m < MT; ++m) {
           wait_all(&p_full[m * PB + it % PB], (it / PB) & 1);
           if (!ok) break;
