@@ -730,7 +730,7 @@ Block8Plan block8_plan(int batch, int kv_heads, int rows, int g, int max_blocks,
   Block8Plan p{};
   // Up to 16 rows the register-fragment kernel, which wastes no rows; from 17 on the
   // tensor-core kernel, whose tile has 128 (256) rows.  64 sequences of 256 to 8192
-  // tokens, 8 KV heads: 16 rows 115 us against 177, 24 rows 195 against 177, 32 rows
+  // tokens, 8 KV heads: 16 rows 106 us against 177, 24 rows 195 against 177, 32 rows
   // 205 against 177; 4 sequences of 2000: 20.9 against 21.9, and 32.8 against 22.6.
   // The latter keeps a token's g rows in one tile, so where g does not divide 128 the
   // former takes every count.  fp16 queries fill three operand parts, and with those
@@ -740,13 +740,15 @@ Block8Plan block8_plan(int batch, int kv_heads, int rows, int g, int max_blocks,
     p.parts = dtype == 1 ? 3 : 2;
     p.rows_per_group = p.parts == 2 && rows > 128 ? 256 : 128;
     p.ctas = sms;
-    p.seg_cost = 5;  // 8 and 12 were slower for 16 sequences of 64 nodes
+    p.seg_cost = 5;  // 16 sequences of 64 nodes: 3 98 us, 5 95, 8 97, 12 100
   } else {
     p.rows_per_group = rows <= 8 ? 8 : rows <= 16 ? 16 : 32;
     p.ctas = sms * (rows <= 8 ? Cfg<128, 1>::CTAS : rows <= 16 ? Cfg<128, 2>::CTAS : Cfg<128, 4>::CTAS);
-    // starting and leaving a piece costs as much as eight tiles (2: 107 us, 4: 102,
-    // 8: 100, 12: 100 for 64 sequences of one query)
-    p.seg_cost = 8;
+    // starting and leaving a piece costs as much as twelve tiles: 64 sequences of one
+    // query and of 16 rows, and 16 of 16 rows, take 95, 107 and 51 us with 8, 95, 106
+    // and 50 with 12, 96, 113 and 53 with 24 (with 2, an earlier kernel took 107 us
+    // for the first against 100 with 8)
+    p.seg_cost = 12;
   }
   p.nrg = (rows + p.rows_per_group - 1) / p.rows_per_group;
   if (!p.tc) {
