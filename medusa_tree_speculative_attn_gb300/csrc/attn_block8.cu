@@ -37,8 +37,8 @@
 // a call is one launch.
 //
 // Bound by the cache's bytes: 64 sequences of 256 to 8192 tokens, 32 query and 8 KV
-// heads of 128 columns, one query each: 94 us for 549 MB, 5.8 TB/s (86 % of a copy).
-// A call for one sequence of 2048 tokens takes 12.7 us, all of it latency: the
+// heads of 128 columns, one query each: 95 us for 549 MB, 5.8 TB/s (85 % of a copy).
+// A call for one sequence of 2048 tokens takes 13.1 us, all of it latency: the
 // prefix, the first page ids, the first pages, one merge.
 #include <atomic>
 #include <cmath>
