@@ -519,7 +519,10 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::CTAS) attn_block8_kernel
       const int ex = amax > 0.f ? (int)(__float_as_uint(amax) >> 23) - 127 : 0;
       const int k = min(max(8 - ex, -120), 120);
       const float f2 = __uint_as_float((uint32_t)(127 + k) << 23);
-      const float c = a.scale_log2 * __uint_as_float((uint32_t)(127 - k) << 23);
+      // an infinity makes every score NaN (of its products alone, keys of one sign would
+      // give -inf throughout, and with that a sum of 0)
+      const float c = amax < INFINITY ? a.scale_log2 * __uint_as_float((uint32_t)(127 - k) << 23)
+                                      : __int_as_float(0x7fffffff);
       st.c[i][0] = __shfl_sync(0xffffffffu, c, 8 * tig);  // rows 2 tig and 2 tig + 1
       st.c[i][1] = __shfl_sync(0xffffffffu, c, 8 * tig + 4);
 #pragma unroll

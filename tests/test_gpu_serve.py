@@ -820,3 +820,23 @@ def test_block8_attention_wait_bound():
     mt.tree_attn_paged_block8(*args, **kw)
     assert mt.read_status(ws) == 0
     _attn_check(c, out)
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("t, hq, hkv, lens", [(1, 1, 1, [0, 1, 40]), (1, 8, 2, [5, 900, 0]), (4, 8, 2, [900, 3, 70]), (4, 18, 2, [33, 0, 200]), (9, 8, 2, [900, 3, 70])])
+@pytest.mark.parametrize("sign", [1.0, -1.0])
+def test_block8_attention_infinite_query_among_keys_of_one_sign(dtype, t, hq, hkv, lens, sign):
+    # every product with the infinity has the same sign: all scores +inf, or all -inf
+    c = _attn_case(np.random.default_rng(110), 3, t, hq, hkv, 128, lens, dtype, "chain")
+    c["k"][:, :, :, 9] = ref.encode(1.0)
+    c["kn"][..., 9] = 1.0
+    c["q"][..., 9] = 0.5
+    clean = _attn_run(c)[0].cpu()
+    c["q"][1, 0, 0, 9] = c["q"][:, t - 1, hq - 1, 9] = sign * float("inf")
+    touched = torch.zeros(3, t, hq, dtype=torch.bool)
+    touched[1, 0, 0] = touched[:, t - 1, hq - 1] = True
+    out, ws, _, _ = _attn_run(c)
+    assert mt.read_status(ws) == 0
+    out = out.cpu()
+    assert out[touched].isnan().all()
+    assert torch.equal(out[~touched], clean[~touched])
