@@ -411,15 +411,20 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::CTAS) attn_block8_kernel
 
   // every CTA: tiles of each sequence and their prefix
   block8_prefix<kWarps>(a, s_pfx, s_warp, blockIdx.x == 0);
-  // one thread walks the pieces: its cursor and the schedule's 64-bit arithmetic
-  // stay out of everybody's registers
+  // One warp walks the pieces: the cursor and the schedule's 64-bit arithmetic stay out
+  // of everybody's registers.  Its lanes do so together, with the same values: where one
+  // thread did, its loops and divisions left it apart from its warp in an instance that
+  // fills its registers, and the warp then came to each barrier twice.
   __shared__ PieceIter s_it;
   __shared__ Piece s_piece;
   __shared__ int s_more;
-  if (tid == 0) {
+  if (warp == 0) {
     Sched sc = a.sched;
     sc.tile_pfx = s_pfx;
-    s_it.init(sc, blockIdx.x);
+    PieceIter it;
+    it.init(sc, blockIdx.x);
+    s_it = it;
+    __syncwarp();
   }
   uint8_t* ring = smem + warp * (C::DEPTH * 2 * C::kPage);
   const uint32_t ring_u = static_cast<uint32_t>(__cvta_generic_to_shared(ring));
@@ -427,7 +432,16 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::CTAS) attn_block8_kernel
   const uint8_t* vc = static_cast<const uint8_t*>(a.v_cache);
 
   while (true) {
-    if (tid == 0) s_more = s_it.next(s_piece);
+    if (warp == 0) {
+      PieceIter it = s_it;
+      Piece next;
+      const bool more = it.next(next);
+      __syncwarp();  // every lane has read the cursor
+      s_it = it;
+      s_piece = next;
+      s_more = more;
+      __syncwarp();
+    }
     __syncthreads();
     if (!s_more) break;
     const Piece pc = s_piece;
