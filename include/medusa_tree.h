@@ -430,12 +430,18 @@ int mt_kv_append_accepted(const mt_append_desc* desc, int tree_size, int max_dep
  * chain, each node the child of the one before it.
  *   q [B][T][Hq][D], k_new, v_new [B][T][Hkv][D], out [B][T][Hq][D]  act (fp16 or bf16)
  *   k_cache, v_cache [num_pages][Hkv][16][D] codes; k_scales, v_scales fp32
- *   [num_pages][Hkv], finite and positive
+ *   [num_pages][Hkv], of the range that the appends write, 2^-64 to 2^119 (powers
+ *   of two or not); a value scale below it counts as 2^-64
  * A sequence with seq_lens[b] < 0 is no sequence: its rows of out are left as
  * they were.  desc: dtype MT_F16 or MT_BF16, cache_dtype MT_E4M3; num_splits,
  * kernel, k_scale and v_scale are not used; any number of query heads per KV
- * head.  out must not overlap q, k_new or v_new.  Accumulation in fp32; queries
- * keep their bits, softmax weights are rounded to fp16.  A query row with a NaN or an infinity gives NaN, and so does a row that
+ * head.  out must not overlap q, k_new or v_new.  Accumulation in fp32.  A query's
+ * elements keep their bits down to 2^-17 of the row's largest.  A key's softmax
+ * weight times its block's value scale is rounded to fp16, relative to the largest
+ * such product that the row sees: to 2^-11 of itself or, where it is small, to 2^-28
+ * of the largest.  (Value scales some 2^100 apart in one sequence can cost the
+ * smaller ones' keys their share of the sum of weights, too.)
+ * A query row with a NaN or an infinity gives NaN, and so does a row that
  * sees a key with a NaN or a new token with a NaN among its values; a cached value's
  * NaN reaches its own column.  What a row does not see has no effect on it.
  * workspace: mt_tree_attn_block8_workspace_size(desc) bytes, zero-filled before

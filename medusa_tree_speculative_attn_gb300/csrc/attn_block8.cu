@@ -27,8 +27,12 @@
 // Queries are scaled to a power of two per row (exact; a bf16 query keeps all
 // its bits in fp16).  Softmax in base 2; the maximum of a row moves only when a
 // score exceeds it by more than 8, which one vote per page finds, so the common
-// page has no reduction.  P carries 2^3 * v_scale / v_ref, v_ref a running
-// reference, so that fp16 holds weights from 2^11 down to 2^-24 of it.
+// page has no reduction.  A page's value scale 2^lv joins the exponent: the
+// maximum is that of score + lv, P = 2^(score + lv - max + 3) is what a value's
+// code is multiplied with, and the row's sum takes P * 2^-lv.  So the fp16 of P is
+// spent on what a key adds to the output, 2^11 down to 2^-24, whatever the scales
+// and the weights of the pages before it (scaled by the largest value scale so far,
+// a page of a large scale and next to no weight left the others no bits).
 //
 // The batch's 64-slot tiles (four pages, one a warp) are dealt out evenly over
 // persistent CTAs (common.cuh's balanced schedule, its prefix computed by every
@@ -97,6 +101,14 @@ __device__ __forceinline__ float fast_exp2(float x) {
   return y;
 }
 
+// log2 and inverse of a page's value scale.  One below 2^-64 (or one that is no number)
+// would leave the exponent's range: it counts as 2^-64.
+__device__ __forceinline__ void log2_scale(float vs, float& lv, float& iv) {
+  vs = fmaxf(vs, 5.421010862427522e-20f);
+  lv = log2f(vs);
+  iv = 1.f / vs;
+}
+
 __device__ __forceinline__ uint32_t pack_h2(float a, float b) {
   const __half2 h = __floats2half2_rn(a, b);
   uint32_t r;
@@ -132,7 +144,6 @@ struct State {
   float o[NT][D / 16][4];
   float m[NT][2], l[NT][2];  // l is this lane's part
   float c[NT][2];            // score -> base-2 units, without the page's scale
-  float v_ref, inv_ref;
 
   __device__ __forceinline__ void clear() {
 #pragma unroll
@@ -144,7 +155,6 @@ struct State {
       m[i][0] = m[i][1] = -INFINITY;
       l[i][0] = l[i][1] = 0.f;
     }
-    v_ref = inv_ref = 0.f;
   }
 };
 
@@ -152,10 +162,11 @@ struct State {
 // those of an ancestor mask.
 enum : int { kSeeAll, kSeeLimit, kSeeMask };
 
-// Folds one page (codes in shared memory) into the running result.
+// Folds one page (codes in shared memory) into the running result; lv, iv: log2 and
+// inverse of its value scale.
 template <int D, int NT, int SEE>
-__device__ __forceinline__ void page_step(State<D, NT>& st, const uint8_t* kp, const uint8_t* vp, float ks, float vs,
-                                          int limit, const unsigned (&see)[NT][2]) {
+__device__ __forceinline__ void page_step(State<D, NT>& st, const uint8_t* kp, const uint8_t* vp, float ks, float lv,
+                                          float iv, int limit, const unsigned (&see)[NT][2]) {
   const int lane = threadIdx.x & 31, gid = lane >> 2, tig = lane & 3;
   float s[NT][4];
 #pragma unroll
@@ -175,13 +186,13 @@ __device__ __forceinline__ void page_step(State<D, NT>& st, const uint8_t* kp, c
       for (int i = 0; i < NT; ++i) mma(s[i], a, st.q[i][ch * 4 + x][0], st.q[i][ch * 4 + x][1]);
     }
   }
-  // scores in base-2 units; element e: row 2 tig + (e & 1), key gid + 8 (e >> 1)
+  // scores in base-2 units + lv; element e: row 2 tig + (e & 1), key gid + 8 (e >> 1)
   bool over = false;
 #pragma unroll
   for (int i = 0; i < NT; ++i) {
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-      s[i][e] *= st.c[i][e & 1] * ks;
+      s[i][e] = fmaf(s[i][e], st.c[i][e & 1] * ks, lv);
       if (SEE != kSeeAll) {
         const int key = gid + 8 * (e >> 1);
         if (!(SEE == kSeeLimit ? key < limit : ((see[i][e & 1] >> key) & 1u))) s[i][e] = -INFINITY;
@@ -189,16 +200,7 @@ __device__ __forceinline__ void page_step(State<D, NT>& st, const uint8_t* kp, c
       over = over || s[i][e] > st.m[i][e & 1] + 8.f;
     }
   }
-  const float vsc = fmaxf(vs, 1e-30f);
-  if (__any_sync(0xffffffffu, over || vsc > 16.f * st.v_ref)) {
-    // a maximum grows by more than 2^8, or the page's value scale exceeds the
-    // reference 16 times: O moves
-    float fv = 1.f;
-    if (vsc > 16.f * st.v_ref) {
-      fv = st.v_ref / vsc;
-      st.v_ref = vsc;
-      st.inv_ref = 1.f / vsc;
-    }
+  if (__any_sync(0xffffffffu, over)) {  // a maximum grows by more than 2^8: O moves
 #pragma unroll
     for (int i = 0; i < NT; ++i) {
       float f[2];
@@ -213,7 +215,6 @@ __device__ __forceinline__ void page_step(State<D, NT>& st, const uint8_t* kp, c
           st.l[i][r] *= f[r];
           st.m[i][r] = mx;
         }
-        f[r] *= fv;
       }
 #pragma unroll
       for (int t = 0; t < D / 16; ++t)
@@ -221,19 +222,18 @@ __device__ __forceinline__ void page_step(State<D, NT>& st, const uint8_t* kp, c
         for (int e = 0; e < 4; ++e) st.o[i][t][e] *= f[e & 1];
     }
   }
-  const float pv = 8.f * vs * st.inv_ref;
   uint32_t pb[NT][2];
 #pragma unroll
   for (int i = 0; i < NT; ++i) {
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
       const float m = st.m[i][e & 1];
-      s[i][e] = fast_exp2(s[i][e] - (m == -INFINITY ? 0.f : m));
+      s[i][e] = fast_exp2(s[i][e] + (m == -INFINITY ? 0.f : 3.f - m));
     }
-    st.l[i][0] += s[i][0] + s[i][2];
-    st.l[i][1] += s[i][1] + s[i][3];
 #pragma unroll
-    for (int h = 0; h < 2; ++h) pb[i][h] = transpose8(pack_h2(s[i][2 * h] * pv, s[i][2 * h + 1] * pv));
+    for (int r = 0; r < 2; ++r) st.l[i][r] = fmaf(s[i][r] + s[i][2 + r], iv, st.l[i][r]);
+#pragma unroll
+    for (int h = 0; h < 2; ++h) pb[i][h] = transpose8(pack_h2(s[i][2 * h], s[i][2 * h + 1]));
   }
   // values: rows 2 tig, 2 tig + 1, 2 tig + 8, 2 tig + 9, columns gid * D/8 ...
   constexpr int NW = D / 32;  // 4-byte words of a row per lane
@@ -402,7 +402,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::CTAS) attn_block8_kernel
   __shared__ int s_warp[kWarps];
   __shared__ int s_par[kMaxTree];
   __shared__ unsigned long long s_anc[kMaxTree];
-  __shared__ float s_m[kWarps][RG], s_l[kWarps][RG], s_ref[kWarps];
+  __shared__ float s_m[kWarps][RG], s_l[kWarps][RG];
   __shared__ int s_last;
   const AttnParams& a = p.a;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, gid = lane >> 2, tig = lane & 3;
@@ -478,8 +478,9 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::CTAS) attn_block8_kernel
       return id >= 0 && id < a.num_pages ? __ldg(sc_ + (size_t)id * a.Hkv + kvh) : 0.f;
     };
     int id_cur = fetch_id(lane), id_nxt = -1;
-    float ks_cur = fetch_scale(p.k_scales, id_cur), vs_cur = fetch_scale(p.v_scales, id_cur);
-    float ks_nxt = 0.f, vs_nxt = 0.f;
+    float ks_cur = fetch_scale(p.k_scales, id_cur), vs_nxt = fetch_scale(p.v_scales, id_cur);
+    float ks_nxt = 0.f, lv_cur, iv_cur;
+    log2_scale(vs_nxt, lv_cur, iv_cur);
     int id_iss = id_cur, iss_base = 0;  // the issuing side runs ahead of the computing side
     bool bad = false;
     auto issue = [&](int i) {
@@ -529,7 +530,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::CTAS) attn_block8_kernel
       float amax = top.get();
       amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
       amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
-      // 2^8 <= scaled maximum < 2^9: elements down to 2^-33 of it keep their bits
+      // 2^8 <= scaled maximum < 2^9: a bf16 keeps its bits down to 2^-26 of it, an fp16 all
       const int ex = amax > 0.f ? (int)(__float_as_uint(amax) >> 23) - 127 : 0;
       const int k = min(max(8 - ex, -120), 120);
       const float f2 = __uint_as_float((uint32_t)(127 + k) << 23);
@@ -559,7 +560,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::CTAS) attn_block8_kernel
         if (i > 0) {
           id_cur = id_nxt;
           ks_cur = ks_nxt;
-          vs_cur = vs_nxt;
+          log2_scale(vs_nxt, lv_cur, iv_cur);
         }
         id_nxt = fetch_id(i + 32 + lane);
       } else if (at == 16) {
@@ -571,17 +572,18 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::CTAS) attn_block8_kernel
       __syncwarp();
       uint8_t* kp = ring + (i % C::DEPTH) * 2 * C::kPage;
       uint8_t* vp = kp + C::kPage;
-      const float ks = __shfl_sync(0xffffffffu, ks_cur, at), vs = __shfl_sync(0xffffffffu, vs_cur, at);
+      const float ks = __shfl_sync(0xffffffffu, ks_cur, at), lv = __shfl_sync(0xffffffffu, lv_cur, at);
+      const float iv = __shfl_sync(0xffffffffu, iv_cur, at);
       const int limit = L - (first + 4 * i) * kP;
       if (limit >= kP) {
-        page_step<D, NT, kSeeAll>(st, kp, vp, ks, vs, kP, none);
+        page_step<D, NT, kSeeAll>(st, kp, vp, ks, lv, iv, kP, none);
       } else {
         // the sequence ends in this page: rows past it may hold anything, NaN
         // codes too; their weights are 0 and their values are made 0
         for (int e = lane; e < (kP - limit) * (D / 16); e += 32)
           *reinterpret_cast<uint4*>(vp + limit * D + e * 16) = make_uint4(0, 0, 0, 0);
         __syncwarp();
-        page_step<D, NT, kSeeLimit>(st, kp, vp, ks, vs, limit, none);
+        page_step<D, NT, kSeeLimit>(st, kp, vp, ks, lv, iv, limit, none);
       }
       __syncwarp();  // every lane has read the slot before it is filled again
     }
@@ -611,7 +613,9 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::CTAS) attn_block8_kernel
           const int row = row0 + i * 8 + 2 * tig + r;
           see[i][r] = row < a.rows ? (unsigned)(s_anc[row / a.g] >> (pn * kP)) & 0xffffu : 0u;
         }
-      page_step<D, NT, kSeeMask>(st, ring, ring + C::kPage, ks, vs, kP, see);
+      float lv, iv;
+      log2_scale(vs, lv, iv);
+      page_step<D, NT, kSeeMask>(st, ring, ring + C::kPage, ks, lv, iv, kP, see);
     }
 
     // ---- join the four warps and write the piece ----
@@ -627,10 +631,9 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::CTAS) attn_block8_kernel
           s_l[warp][i * 8 + 2 * tig + r] = l;
         }
       }
-    if (lane == 0) s_ref[warp] = st.v_ref * 0.125f;
     float* s_o = reinterpret_cast<float*>(smem);  // [warp][8][LDO]
-    // Rows 8i .. 8i + 7 from the four warps' parts in s_m, s_l, s_o and s_ref: to
-    // the output, or to the piece's slot.
+    // Rows 8i .. 8i + 7 from the four warps' parts in s_m, s_l and s_o: to the output,
+    // or to the piece's slot.
     auto join = [&](int i, int slot) {
       const int rr = tid >> 4, rg_row = i * 8 + rr, row = row0 + rg_row, c8 = tid & 15;  // 16 threads a row
       if (row >= a.rows || c8 >= D / 8) return;
@@ -639,9 +642,8 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::CTAS) attn_block8_kernel
       for (int w = 0; w < kWarps; ++w) M = fmaxf(M, s_m[w][rg_row]);
 #pragma unroll
       for (int w = 0; w < kWarps; ++w) {
-        const float e = s_m[w][rg_row] == -INFINITY ? 0.f : fast_exp2(s_m[w][rg_row] - M);
-        l += e * s_l[w][rg_row];
-        f[w] = e * s_ref[w];
+        f[w] = s_m[w][rg_row] == -INFINITY ? 0.f : fast_exp2(s_m[w][rg_row] - M);
+        l += f[w] * s_l[w][rg_row];
       }
       const float inv = l == 0.f ? 0.f : 1.f / l;
       float acc[8] = {};

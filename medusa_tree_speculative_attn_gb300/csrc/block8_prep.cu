@@ -4,7 +4,7 @@
 //     largest magnitude is at most 448, then x = hi + lo (+ lo2 for fp16), each
 //     part the code nearest to what is left.  A part takes 4 significant bits,
 //     so two hold a bf16's 8 and three an fp16's 11; what falls below the last
-//     part's smallest step is under 2^-18 of the row's maximum;
+//     part's smallest step is under 2^-17 of the row's maximum;
 //   - the new tokens' keys and values as blocks of codes with their scales, in
 //     the page layout [b][KV head][block][16][D];
 //   - each node's ancestor mask (the Medusa tree mask, vLLM issue 1171);

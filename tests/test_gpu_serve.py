@@ -840,3 +840,96 @@ def test_block8_attention_infinite_query_among_keys_of_one_sign(dtype, t, hq, hk
     out = out.cpu()
     assert out[touched].isnan().all()
     assert torch.equal(out[~touched], clean[~touched])
+
+
+def _leaf_2(parents):
+    """Every node the child of the one before it, but node 2, a leaf under node 0, and node 3, under node 1."""
+    t = parents.shape[1]
+    parents[:] = np.arange(t) - 1
+    parents[:, 2:3], parents[:, 3:4] = 0, 1
+
+
+def _attn_check_nodes(c, out, nodes=slice(None)):
+    """As _attn_check, of some of the nodes, with two more terms.  A weight below 2^-14 is a subnormal fp16, off by up
+    to 2^-25 where the row's largest weight times value scale stands for 2^3: together sum |code| 2^-28 max(p scale),
+    which counts where the scales in sight differ by much.  And what is past the output type's largest value is
+    infinite (or, within the tolerance, is not yet)."""
+    q, kn, vn = (c[n].double().numpy() for n in ("q", "kn", "vn"))
+    b, t, hq, d = q.shape
+    hkv = kn.shape[2]
+    got, top = out.cpu().double().numpy(), torch.finfo(c["q"].dtype).max
+    for i in range(b):
+        n = c["lens"][i]
+        tree = ref.ancestors(None if c["parents"] is None else c["parents"][i], t)
+        sees = np.concatenate([np.ones((t, n), bool), tree], 1)
+        at = [(c["table"][i][s // P], s % P) for s in range(n)]
+        for h in range(hkv):
+            both = []
+            for cache, scales, new in ((c["k"], c["ks"], kn), (c["v"], c["vs"], vn)):
+                code, scale = [ref.decode(cache[pg, h, s]) for pg, s in at], [float(scales[pg, h]) for pg, s in at]
+                for j in range(0, t, P):
+                    block, s = ref.block_codes(new[i, j:j + P, h])
+                    code.extend(ref.decode(block))
+                    scale.extend([s] * len(block))
+                both.append((np.array(code), np.array(scale)[:, None]))
+            (k, ks), (v, vs) = both
+            for j in range(h * (hq // hkv), (h + 1) * (hq // hkv)):
+                z = np.where(sees, q[i, :, j] @ (k * ks).T * d ** -0.5, -np.inf)
+                w = np.exp(z - z.max(1, keepdims=True))
+                w /= w.sum(1, keepdims=True)
+                want, mag = w @ (v * vs), w @ np.abs(v * vs)
+                tol = ref.HALF_STEP[c["q"].dtype] * np.abs(want) + (2.0 ** -11 + 2.0 ** -8) * mag + 1e-7
+                tol += 2.0 ** -28 * (w * vs.T).max(1, keepdims=True) * (sees @ np.abs(v))
+                with np.errstate(invalid="ignore"):
+                    fine = np.abs(got[i, :, j] - want) <= tol
+                    fine |= (np.abs(want) + tol >= top) & (got[i, :, j] == np.sign(want) * np.inf)
+                assert fine[nodes].all(), (i, j, np.argwhere(~fine)[:3])
+
+
+ROWS = [(1, 1, 1), (1, 8, 1), (4, 8, 2), (4, 18, 2), (6, 16, 4), (40, 8, 2), (64, 4, 1)]  # T, Hq, Hkv: 1 to 256 rows a KV head, both kernels
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("t, hq, hkv", ROWS)
+@pytest.mark.parametrize("at, power", [(0, 24), (0, 40), (3, 28), (18, 60)])
+def test_block8_attention_large_values_of_no_weight(dtype, t, hq, hkv, at, power):
+    # a page whose value scale is 2^power times the others' and whose scores are 120 lower, in powers of two: what
+    # is left of it is below 2^-50, and the other pages' weights keep their bits
+    c = _attn_case(np.random.default_rng(120 + at), 1, t, hq, hkv, 128, [333], dtype, spread=1.0)
+    c["q"][..., 9], c["kn"][..., 9], c["k"][:, :, :, 9] = 120.0, 0, 0
+    page = c["table"][0][at]
+    c["ks"][page] = 1.0
+    c["k"][page, :, :, 9] = ref.encode(-9.0)
+    c["vs"][page] = 2.0 ** power
+    c["v"][page] = ref.encode(np.random.default_rng(1).standard_normal((hkv, P, 128)))
+    out, ws, _, _ = _attn_run(c)
+    assert mt.read_status(ws) == 0
+    _attn_check(c, out)
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("t, hq, hkv", [r for r in ROWS if r[0] > 1])
+def test_block8_attention_large_values_out_of_sight(dtype, t, hq, hkv):
+    # they raise the scale of their block of new tokens, and so cost its other rows precision; nothing else
+    c = _attn_case(np.random.default_rng(130), 2, t, hq, hkv, 128, [100, 0], dtype)
+    _leaf_2(c["parents"])
+    c["vn"][:, 2, 0, 5], c["kn"][0, 2, hkv - 1, 7] = 30000.0, -30000.0
+    out, ws, _, _ = _attn_run(c)
+    assert mt.read_status(ws) == 0
+    _attn_check_nodes(c, out, np.arange(t) != 2)
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("t, hq, hkv", ROWS)
+def test_block8_attention_of_spread_scales_in_every_kernel(dtype, t, hq, hkv):
+    # as the tests of widely spread scales and of a dominant key, for every number of rows
+    c = _attn_case(np.random.default_rng(140), 1, t, hq, hkv, 128, [160], dtype, spread=1.0)
+    for p, k in zip(c["table"][0], (-64, -20, 0, 10, -3, 4, 20, -40, 0, 1)):
+        c["vs"][p] = 2.0 ** k
+    c["v"][c["table"][0][0]] = 0
+    _attn_check_nodes(c, _attn_run(c)[0])
+    c = _attn_case(np.random.default_rng(141), 1, t, hq, hkv, 128, [600], dtype, spread=1.0)
+    first = c["table"][0][0]
+    c["q"][..., 9], c["kn"][..., 9], c["k"][:, :, :, 9] = 8.0, 0, 0
+    c["k"][first, 0, 0, 9], c["v"][first, 0, 0] = ref.encode(16 / c["ks"][first, 0]), 0
+    _attn_check_nodes(c, _attn_run(c)[0])
