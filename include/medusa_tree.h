@@ -441,9 +441,13 @@ int mt_kv_append_accepted(const mt_append_desc* desc, int tree_size, int max_dep
  * such product that the row sees: to 2^-11 of itself or, where it is small, to 2^-28
  * of the largest.  (Value scales some 2^100 apart in one sequence can cost the
  * smaller ones' keys their share of the sum of weights, too.)
- * A query row with a NaN or an infinity gives NaN, and so does a row that
- * sees a key with a NaN or a new token with a NaN among its values; a cached value's
- * NaN reaches its own column.  What a row does not see has no effect on it.
+ * A query row with a NaN or an infinity gives NaN, and so does a row that sees a
+ * cached key with a NaN, or a new token with a NaN or an infinity in its key or
+ * value; a cached value's NaN reaches its own column.  (A cached infinity is the
+ * saturated code under the scale 2^119.)  NaN and infinities that a row does not see
+ * have no effect on it: those of new tokens do not enter a block's scale.  A large
+ * finite value that it does not see has one: it raises the scale of its block of 16
+ * new tokens, so that the others' codes there are coarser.
  * workspace: mt_tree_attn_block8_workspace_size(desc) bytes, zero-filled before
  * its first use (status word, counters that every call leaves at zero, schedule,
  * partial results); it serves any descriptor that it is large enough for, one call

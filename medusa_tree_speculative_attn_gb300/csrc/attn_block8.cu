@@ -269,11 +269,11 @@ __device__ __forceinline__ void page_step(State<D, NT>& st, const uint8_t* kp, c
 }
 
 // One block of up to 16 new tokens of K or V as codes in shared memory (rows
-// past T are zero); returns the block's scale.  nan: which tokens have a NaN value,
-// found by the call for the values and used by the one for the keys.
+// past T are zero); returns the block's scale.  odd: which tokens have a value that is
+// not finite, found by the call for the values and used by the one for the keys.
 template <typename T, int D>
 __device__ __forceinline__ float quantise_new(const T* src, size_t row_stride, int rows, uint8_t* dst, bool keys,
-                                              unsigned& nan) {
+                                              unsigned& odd) {
   constexpr int LPR = D / 16, RPS = 32 / LPR, STEPS = 16 / RPS;
   const int lane = threadIdx.x & 31, sub = lane / LPR, c = lane % LPR;
   Row8<T> lo[STEPS], hi[STEPS];
@@ -287,12 +287,22 @@ __device__ __forceinline__ float quantise_new(const T* src, size_t row_stride, i
       hi[s].load(src + r * row_stride + D / 2 + 8 * c);
     }
   }
+  unsigned found = 0;
+#pragma unroll
+  for (int s = 0; s < STEPS; ++s) found |= odd_rows<RPS>(not_finite(lo[s]) || not_finite(hi[s])) << (s * RPS);
+  if (found) {
+#pragma unroll
+    for (int s = 0; s < STEPS; ++s) {
+      replace_odd(lo[s], keys ? __int_as_float(0x7fffffff) : 0.f);
+      replace_odd(hi[s], keys ? __int_as_float(0x7fffffff) : 0.f);
+    }
+  }
+  if (!keys) odd = found;
   AbsMax<T> top;
 #pragma unroll
   for (int s = 0; s < STEPS; ++s) {
     top.add(lo[s]);
     top.add(hi[s]);
-    if (!keys) nan |= nan_rows<RPS>(has_nan(lo[s]) || has_nan(hi[s])) << (s * RPS);
   }
   float amax = top.get();
 #pragma unroll
@@ -304,14 +314,7 @@ __device__ __forceinline__ float quantise_new(const T* src, size_t row_stride, i
     float x[2][8];
     lo[s].to_f(x[0]);
     hi[s].to_f(x[1]);
-    if (nan) {
-      if (!keys) {
-        drop_nan(x[0]);
-        drop_nan(x[1]);
-      } else if (nan >> r & 1u) {
-        x[0][0] = __int_as_float(0x7fffffff);
-      }
-    }
+    if (keys && (odd >> r & 1u)) x[0][0] = __int_as_float(0x7fffffff);
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       const int col = h * (D / 2) + 8 * c;
@@ -530,7 +533,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::CTAS) attn_block8_kernel
       float amax = top.get();
       amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
       amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
-      // 2^8 <= scaled maximum < 2^9: a bf16 keeps its bits down to 2^-26 of it, an fp16 all
+      // 2^8 <= scaled maximum < 2^9: a bf16 keeps its bits down to 2^-25 of it, an fp16 to 2^-22
       const int ex = amax > 0.f ? (int)(__float_as_uint(amax) >> 23) - 127 : 0;
       const int k = min(max(8 - ex, -120), 120);
       const float f2 = __uint_as_float((uint32_t)(127 + k) << 23);
@@ -598,11 +601,11 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::CTAS) attn_block8_kernel
       const size_t src = ((size_t)b * a.T + pn * kP) * rs + (size_t)kvh * D;
       const int rows = min(kP, a.T - pn * kP);
       float ks = 0.f, vs = 0.f;
-      unsigned nan = 0;
+      unsigned odd = 0;
 #pragma unroll 1  // one after the other: both at once take more registers than there are
       for (int x = 0; x < 2; ++x) {
         vs = ks;
-        ks = quantise_new<T, D>(static_cast<const T*>(x ? p.k_new : p.v_new) + src, rs, rows, ring + (1 - x) * C::kPage, x == 1, nan);
+        ks = quantise_new<T, D>(static_cast<const T*>(x ? p.k_new : p.v_new) + src, rs, rows, ring + (1 - x) * C::kPage, x == 1, odd);
       }
       __syncwarp();
       unsigned see[NT][2];

@@ -85,6 +85,16 @@ __device__ __forceinline__ void quantise_block(const T* src, const T* values, si
       hi[s].load(src + r * row_stride + 16 * c + 8);
     }
   }
+  unsigned found = 0;
+#pragma unroll
+  for (int s = 0; s < STEPS; ++s) found |= odd_rows<RPS>(not_finite(lo[s]) || not_finite(hi[s])) << (s * RPS);
+  if (found) {
+#pragma unroll
+    for (int s = 0; s < STEPS; ++s) {
+      replace_odd(lo[s], values ? __int_as_float(0x7fffffff) : 0.f);
+      replace_odd(hi[s], values ? __int_as_float(0x7fffffff) : 0.f);
+    }
+  }
   float amax = 0.f;
 #pragma unroll
   for (int s = 0; s < STEPS; ++s) {
@@ -97,7 +107,7 @@ __device__ __forceinline__ void quantise_block(const T* src, const T* values, si
 #pragma unroll
   for (int off = 16; off > 0; off >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, off));
   const float scale = block_scale(amax), inv = 1.f / scale;
-  unsigned nan = 0;  // of keys: the tokens that have a NaN value
+  unsigned odd = 0;  // of keys: the tokens that have a value that is not finite
   if (values) {
 #pragma unroll
     for (int s = 0; s < STEPS; ++s) {
@@ -109,7 +119,7 @@ __device__ __forceinline__ void quantise_block(const T* src, const T* values, si
         v0.load(values + r * row_stride + 16 * c);
         v1.load(values + r * row_stride + 16 * c + 8);
       }
-      nan |= nan_rows<RPS>(has_nan(v0) || has_nan(v1)) << (s * RPS);
+      odd |= odd_rows<RPS>(not_finite(v0) || not_finite(v1)) << (s * RPS);
     }
   }
 #pragma unroll
@@ -123,11 +133,7 @@ __device__ __forceinline__ void quantise_block(const T* src, const T* values, si
       x[e] *= inv;
       y[e] *= inv;
     }
-    if (!values) {
-      drop_nan(x);
-      drop_nan(y);
-    }
-    if (nan >> r & 1u) x[0] = __int_as_float(0x7fffffff);
+    if (odd >> r & 1u) x[0] = __int_as_float(0x7fffffff);
     const uint2 u = e4m3x8_of(x), v = e4m3x8_of(y);
     *reinterpret_cast<uint4*>(dst + r * D + 16 * c) = make_uint4(u.x, u.y, v.x, v.y);
   }

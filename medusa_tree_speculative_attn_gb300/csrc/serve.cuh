@@ -212,32 +212,40 @@ struct Block8Params {
   int* pieces;            // piece table (common.cuh)
 };
 
-// Whether a packed 16-bit row has a NaN (four instructions for eight values).
+// Whether a packed 16-bit row has a NaN or an infinity.
 template <typename T>
-__device__ __forceinline__ bool has_nan(const Row8<T>& r) {
+__device__ __forceinline__ bool not_finite(const Row8<T>& r) {
   typename AbsMax<T>::V2 v[4];
   memcpy(v, r.w, sizeof(v));
+#pragma unroll
+  for (int e = 0; e < 4; ++e) v[e] = __habs2(v[e]);
   const auto m = __hmax2_nan(__hmax2_nan(v[0], v[1]), __hmax2_nan(v[2], v[3]));
-  const float a = __low2float(m), b = __high2float(m);
-  return a != a || b != b;
+  return !(__low2float(m) < INFINITY && __high2float(m) < INFINITY);
 }
 
-// A NaN among a new token's values would reach, as 0 * NaN in the matrix products,
-// also the nodes that do not see the token.  So its value codes are set to 0 and its
-// key codes to NaN: its scores are NaN where it is seen and are replaced where it is
-// not.  Of R rows in a warp, 32 / R lanes each: bit i says that row i has one.
+// A new token that holds a NaN or an infinity makes NaN of the nodes that see it and must
+// leave the others alone.  But a NaN value would reach those too, as 0 * NaN in the matrix
+// products, and an infinity by way of its block's scale, under which every other code of
+// the block is 0.  So neither enters a scale, in a value it becomes a code of 0, in a key
+// NaN, and of a token with such a value a key code is NaN, too: its scores are NaN where it
+// is seen and are replaced where it is not.  Of R rows in a warp, 32 / R lanes each: bit i
+// says that row i has one.
 template <int R>
-__device__ __forceinline__ unsigned nan_rows(bool nan) {
-  const unsigned lanes = __ballot_sync(0xffffffffu, nan);
+__device__ __forceinline__ unsigned odd_rows(bool odd) {
+  const unsigned lanes = __ballot_sync(0xffffffffu, odd);
   unsigned rows = 0;
 #pragma unroll
   for (int i = 0; i < R; ++i)
     if (lanes >> (i * (32 / R)) & ((1u << (32 / R)) - 1u)) rows |= 1u << i;
   return rows;
 }
-__device__ __forceinline__ void drop_nan(float (&x)[8]) {
+template <typename T>
+__device__ __forceinline__ void replace_odd(Row8<T>& r, float by) {
+  float x[8];
+  r.to_f(x);
 #pragma unroll
-  for (int e = 0; e < 8; ++e) x[e] = x[e] == x[e] ? x[e] : 0.f;
+  for (int e = 0; e < 8; ++e) x[e] = fabsf(x[e]) < INFINITY ? x[e] : by;
+  r.from_f(x);
 }
 
 // Tiles of each sequence (cached pages, then the new tokens' blocks, four to a

@@ -933,3 +933,26 @@ def test_block8_attention_of_spread_scales_in_every_kernel(dtype, t, hq, hkv):
     c["q"][..., 9], c["kn"][..., 9], c["k"][:, :, :, 9] = 8.0, 0, 0
     c["k"][first, 0, 0, 9], c["v"][first, 0, 0] = ref.encode(16 / c["ks"][first, 0]), 0
     _attn_check_nodes(c, _attn_run(c)[0])
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("t, hq, hkv", [r for r in ROWS if r[0] > 1])
+@pytest.mark.parametrize("where", ["value", "key", "both"])
+def test_block8_attention_infinity_in_and_out_of_sight(dtype, t, hq, hkv, where):
+    # as a NaN: the nodes that see it are NaN, the others as if it were 0
+    c = _attn_case(np.random.default_rng(150), 2, t, hq, hkv, 128, [100, 0], dtype)
+    _leaf_2(c["parents"])
+    places = ([(c["vn"], 2, 0, 5)] if where != "key" else []) + ([(c["kn"], 2, hkv - 1, 7), (c["kn"], 1, hkv - 1, 100)] if where != "value" else [])
+    for x, node, h, col in places:
+        x[:, node, h, col] = 0
+    clean = _attn_run(c)[0].cpu()
+    _attn_check_nodes(c, clean)
+    touched = torch.zeros(2, t, hq, dtype=torch.bool)
+    for i, (x, node, h, col) in enumerate(places):
+        x[:, node, h, col] = (-1) ** i * float("inf")
+        sees = torch.from_numpy(ref.ancestors(c["parents"][0], t)[:, node])
+        touched[:, sees, h * (hq // hkv):(h + 1) * (hq // hkv)] = True
+    out, ws, _, _ = _attn_run(c)
+    assert mt.read_status(ws) == 0
+    assert out.cpu()[touched].isnan().all()
+    assert torch.equal(out.cpu()[~touched], clean[~touched])
