@@ -477,9 +477,11 @@ int mt_tree_attn_paged_block8(const mt_attn_desc* desc, const void* q, const voi
  * top_p >= 1, min_p <= 0: off.  A null parameter array: temperature 1, filters
  * off.  uniforms: numbers of [0, 1), others are clamped.  A NaN logit counts as
  * -inf; a row without anything above -inf gives -1; entries of +inf share the
- * whole mass.  Sums are exact integers of weights good to 1e-9, so the token is
- * that of the definition unless u lies that close to a border.  Weights below
- * 2^-44 of the largest count as 0.
+ * whole mass.  Weights are cut to whole multiples of 2^-44 of the largest and are
+ * good to 1e-9 of themselves besides; their sums are exact (2^-38 for the cut by
+ * top_p).  So the token is that of the definition unless u or top_p times its mass
+ * lies next to a border: by 1e-9 of the mass and vocab * 2^-44 of the largest weight
+ * (3e-8 for 500000 tokens).
  * row_index[i] < 0: no row, tokens[i] is left as it was; >= num_logit_rows: -1.
  * row_stride in elements; rows need no alignment.  vocab <= 500000
  * (MT_ERR_UNSUPPORTED above).  No workspace and no device status. */

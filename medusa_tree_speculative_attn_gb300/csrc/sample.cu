@@ -12,13 +12,15 @@
 // value, how many tokens equal to it stay (the lowest indices), and a smallest
 // value for min-p.
 //
-// A cluster of CTAs holds a row in registers: the logits are read from memory
-// once.  Weights are integers (2^44 for the maximum), so every sum is exact and
-// the same in any order; each weight is good to about 1e-9 of itself (the
-// exponent as a sum of two floats, a 128-entry table, a short polynomial).  That
-// matters because a draw compares u against up to 10^5 borders: with weights
-// good to 6e-8 about one row in a thousand of a flat distribution would draw a
-// neighbour of the token that its definition gives.
+// A cluster of CTAs holds a row in shared memory: the logits are read from memory
+// once (by every pass, where a slice does not fit).  Weights are integers (2^44 for
+// the maximum), so every sum is the same in any order; each is good to about 1e-9 of
+// itself (the exponent as a sum of two floats, a 128-entry table, a short polynomial)
+// before it is cut to a whole number, which costs up to 2^-44 of the maximum.  That
+// matters because a draw compares u against up to 10^5 borders: with weights good to
+// 6e-8 about one row in a thousand of a flat distribution would draw a neighbour of
+// the token that its definition gives; and with 32 bits a cut by top_p near 1 missed
+// a long flat tail altogether.
 // The cut is found by a histogram of counts and masses over 64 bins of
 // (m - x) / temperature, half a power of two each, and then among the tokens of
 // the one bin that the cut falls in: by histograms over their keys, 6 bits at a
@@ -166,8 +168,12 @@ __device__ __forceinline__ unsigned long long weight(float x, const Scale& s, co
   return w[0];
 }
 
-// A histogram: counts, and the sums of the low and high 16 bits of the weights
-// (2^32 for the maximum), a column per lane.
+// A histogram: counts, and the sums of the low 21 bits of the weights and of what is
+// above them, a column per lane.  A column has at most 2^11 tokens, so neither sum
+// overflows where a weight is below 2^42; the larger ones, of the first kCoarse bins of
+// (m - x) / temperature, are added in units of 8, 2^-38 of themselves.  (Sums of 64 bits
+// took 59 us for 60 of 128k bf16 tokens with top-p 0.9 where these take 56.)
+constexpr int kCoarse = 5;
 struct Hist {
   unsigned cnt[kBins][32], lo[kBins][32], hi[kBins][32];
 };
@@ -386,8 +392,9 @@ __device__ __forceinline__ void clear(Hist& h) {
 
 // The cluster's histogram in sm.bins, each bin with what lies before it (base_cnt
 // and base_mass included).  The histogram is left zero; turn: which of the two
-// places the sums pass through; units: the masses are counts times sm.unit.
-__device__ __noinline__ void meet(Smem& sm, int turn, unsigned base_cnt, unsigned long long base_mass, bool units) {
+// places the sums pass through; coarse: how many bins' masses are in units of 8; units:
+// the masses are counts times sm.unit.
+__device__ __noinline__ void meet(Smem& sm, int turn, unsigned base_cnt, unsigned long long base_mass, int coarse, bool units) {
   cg::cluster_group cl = cg::this_cluster();
   const int tid = threadIdx.x, lane = tid & 31, C = (int)cl.num_blocks();
   __syncthreads();
@@ -398,7 +405,7 @@ __device__ __noinline__ void meet(Smem& sm, int turn, unsigned base_cnt, unsigne
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       n += sm.hist.cnt[b][c + 8 * j];
-      m += sm.hist.lo[b][c + 8 * j] + ((unsigned long long)sm.hist.hi[b][c + 8 * j] << 16);
+      m += sm.hist.lo[b][c + 8 * j] + ((unsigned long long)sm.hist.hi[b][c + 8 * j] << 21);
       sm.hist.cnt[b][c + 8 * j] = sm.hist.lo[b][c + 8 * j] = sm.hist.hi[b][c + 8 * j] = 0;
     }
 #pragma unroll
@@ -408,7 +415,7 @@ __device__ __noinline__ void meet(Smem& sm, int turn, unsigned base_cnt, unsigne
     }
     if (c == 0) {
       sm.bin_cnt[turn][b] = n;
-      sm.bin_mass[turn][b] = units ? n * sm.unit[b] : m;
+      sm.bin_mass[turn][b] = units ? n * sm.unit[b] : b < coarse ? m << 3 : m;
     }
   }
   cl.sync();
@@ -552,28 +559,33 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
       const float z = fminf((sc.m - x) * width, (float)(kBins - 1)) + 12582912.f;
       return x == sc.m ? 0 : __float_as_int(z) - 0x4B400000;
     };
-    auto weight_of = [&](float x) {  // 2^32 for the maximum
-      return (weight<TWO>(x, sc, sm.table) + (1u << (kWBits - 33))) >> (kWBits - 32);
+    // a weight as the histograms hold it; coarse: its token's bin is one of the first
+    auto weight_of = [&](float x, bool coarse) {
+      const unsigned long long w = weight<TWO>(x, sc, sm.table);
+      return coarse ? w & ~7ull : w;
     };
-    auto rounded = [](unsigned long long w) { return (w + (1u << (kWBits - 33))) >> (kWBits - 32); };
-    auto add_mass = [&](int b, unsigned long long w) {
-      atomicAdd(&sm.hist.lo[b][lane], (unsigned)w & 0xffffu);
-      atomicAdd(&sm.hist.hi[b][lane], (unsigned)(w >> 16));
+    auto add_mass = [&](int b, unsigned long long w, bool coarse) {
+      w >>= coarse ? 3 : 0;
+      atomicAdd(&sm.hist.lo[b][lane], (unsigned)w & 0x1fffffu);
+      atomicAdd(&sm.hist.hi[b][lane], (unsigned)(w >> 21));
     };
-    auto add = [&](int b, float x) {
+    auto add = [&](int b, float x, bool coarse) {
       atomicAdd(&sm.hist.cnt[b][lane], 1u);
-      if (use_p) add_mass(b, weight_of(x));
+      if (use_p) add_mass(b, weight<TWO>(x, sc, sm.table), coarse);
     };
-    auto add_one = [&](float x, int, int) { add(bin_of(x), x); };
+    auto add_one = [&](float x, int, int) {
+      const int b = bin_of(x);
+      add(b, x, b < kCoarse);
+    };
     if (use_p) {
       s.pairs(-INFINITY, [&](float x0, float x1, int, int) {
         const int b0 = bin_of(x0), b1 = bin_of(x1);
         unsigned long long w[2];
         weights<TWO>(x0, x1, sc, sm.table, w);
         atomicAdd(&sm.hist.cnt[b0][lane], 1u);
-        add_mass(b0, rounded(w[0]));
+        add_mass(b0, w[0], b0 < kCoarse);
         atomicAdd(&sm.hist.cnt[b1][lane], 1u);
-        add_mass(b1, rounded(w[1]));
+        add_mass(b1, w[1], b1 < kCoarse);
       }, add_one);
     } else {
       s.pairs(-INFINITY, [&](float x0, float x1, int, int) {
@@ -582,7 +594,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
       }, add_one);
     }
     int turn = 0;
-    meet(sm, turn, 0u, 0ull, false);
+    meet(sm, turn, 0u, 0ull, kCoarse, false);
     unsigned long long whole = sm.whole;
     const int bin_k = use_k ? find(sm, (unsigned)want_k, 0ull) : 0;
     Found in_k = sm.bins[bin_k];
@@ -593,6 +605,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
 
     // from the bin that a count or mass falls in to the last token kept
     auto refine = [&](int bin, Found f, int which, unsigned want_cnt, unsigned long long want_mass) {
+      const bool coarse = bin < kCoarse;
       // the bin's keys, with room for rounding on both sides
       const float xh = sc.m - ((float)bin - 0.5f) / width, xl = sc.m - ((float)bin + 0.5f) / width;
       uint32_t hi = bin == 0 ? 0xffffffffu >> KS : ord_of(xh + 1e-5f * (fabsf(sc.m) + fabsf(xh)) + 1e-30f) >> KS;
@@ -633,7 +646,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
             const Smem* p = cl.map_shared_rank(&sm, from);
             const uint32_t k = p->list_key[which][tid - before];
             sm.rank_key[tid] = ((unsigned long long)k << 32) | (0xffffffffu - (unsigned)p->list_idx[which][tid - before]);
-            sm.rank_mass[tid] = use_p ? weight_of(value_of_key<KS>(k)) : 0ull;
+            sm.rank_mass[tid] = use_p ? weight_of(value_of_key<KS>(k), coarse) : 0ull;
           }
           __syncthreads();
           const int t = tid >> 2;
@@ -667,14 +680,14 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
         s.each(least, [&](float x, int v, int e) {
           if (x < least || x > most || bin_of(x) != bin || !s.in_row(v, e)) return;
           const uint32_t k = ord_of(x) >> KS;
-          if (shift) add((int)((hi - k) >> shift), x);
+          if (shift) add((int)((hi - k) >> shift), x, coarse);
           else atomicAdd(&sm.hist.cnt[hi - k][lane], 1u);
         });
         // a bin of one value needs no masses: the rare lanes in the range would hold up
         // every warp for them (64 rows of 128k bf16, top-p 0.9: 69 -> 63 us)
-        if (shift == 0 && use_p && tid < kBins) sm.unit[tid] = hi >= (unsigned)tid ? weight_of(value_of_key<KS>(hi - tid)) : 0ull;
+        if (shift == 0 && use_p && tid < kBins) sm.unit[tid] = hi >= (unsigned)tid ? weight_of(value_of_key<KS>(hi - tid), coarse) : 0ull;
         turn ^= 1;
-        meet(sm, turn, f.cnt, f.mass, shift == 0 && use_p);
+        meet(sm, turn, f.cnt, f.mass, coarse ? kBins : 0, shift == 0 && use_p);
         const int b = find(sm, want_cnt, want_mass);
         f = sm.bins[b];
         __syncthreads();
@@ -683,7 +696,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
         lo = max(lo, hi > span ? hi - span : 0u);
       }
       // one value, of many tokens: the first `stay` of them
-      const unsigned long long w = use_p ? weight_of(value_of_key<KS>(hi)) : 0ull;
+      const unsigned long long w = use_p ? weight_of(value_of_key<KS>(hi), coarse) : 0ull;
       const unsigned stay = want_cnt ? want_cnt - f.cnt : w ? (unsigned)((want_mass - f.mass + w - 1) / w) : f.in;
       cut = Cut{hi, -1, stay, f.mass + stay * w};
     };
@@ -859,7 +872,9 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
   cl.sync();  // no CTA leaves while others read it
 }
 
-constexpr int kStageMax = 96 * 1024;  // two CTAs per SM
+// Largest staged slice.  Up to about 74 KB of it two CTAs fit an SM beside their Smem of
+// 39 KB; above (fp32 rows of 151k to 196k tokens) one.
+constexpr int kStageMax = 96 * 1024;
 constexpr int kMaxDevices = 64;
 
 Table make_table() {

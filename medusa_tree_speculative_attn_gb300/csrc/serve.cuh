@@ -305,8 +305,9 @@ cudaError_t launch_attn_block8_tc(const Block8Params& p, int dtype, cudaStream_t
 // ---------------------------------------------------------------------------
 // Sampling.
 // ---------------------------------------------------------------------------
-// Largest vocab: an eighth of it (a CTA's slice) times 2^16 stays below 2^32,
-// which the histograms' sums of 16-bit halves rely on.
+// Largest vocab: that many weights of 2^44 (the maximum's) stay below 2^63, and an
+// eighth of it (a CTA's slice) leaves a lane at most 2^11 tokens of 16 warps, which the
+// histograms' columns rely on.
 constexpr int kSampleMaxVocab = 500000;
 
 struct SampleParams {

@@ -956,3 +956,22 @@ def test_block8_attention_infinity_in_and_out_of_sight(dtype, t, hq, hkv, where)
     assert mt.read_status(ws) == 0
     assert out.cpu()[touched].isnan().all()
     assert torch.equal(out.cpu()[~touched], clean[~touched])
+
+
+@pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("v, gap, t", [(400000, 23.0, 1.0), (200000, 22.0, 1.0), (300000, 11.5, 0.5), (70000, 20.0, 1.0), (400000, 15.0, 1.0)])
+def test_sampling_top_p_of_a_long_flat_tail(dtype, v, gap, t):
+    # one token of weight 1 and v - 1 of e^(-gap / t), far below it but together worth a cut.  A weight is good to 1e-9
+    # of itself and 2^-44: all together to E, which is E / w tail tokens; the cut and the draw each compare such a sum
+    # with a multiple of another
+    p = np.float32([0.99999, 0.999995, 0.999999, 0.9, 0.99999, 0.99999])
+    u = np.float32([0.99999, 0.999998, 1 - 2.0 ** -24, 0.99999, 0.5, 0.999999])
+    x = torch.full((1, v), -gap)
+    x[0, 0] = 0
+    got = _sample(x.to(DT[dtype]).cuda().expand(len(u), v), u, [t] * len(u), p=p)
+    w = np.exp(-gap / t)
+    slack = 2 + 4 * (v * (2.0 ** -44 + 1e-9 * w) + 1e-9) / w
+    for a, b, token in zip(p.astype(np.float64), u.astype(np.float64), got):
+        kept = min(max(np.ceil((a * (1 + (v - 1) * w) - 1) / w), 0), v - 1)
+        want = (b * (1 + kept * w) - 1) / w + 1
+        assert abs(token - max(want, 0)) <= slack, (a, b, token, want, slack)
