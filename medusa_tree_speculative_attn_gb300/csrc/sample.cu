@@ -82,8 +82,20 @@ __device__ __forceinline__ float value_of_key(uint32_t key) {
 
 struct Scale {
   float m;         // the row's maximum
+  float ref;       // what the weights refer to: m, or a little more (reference below)
   float hi, lo;    // log2(e) / temperature as a sum
 };
+
+// For 16-bit values: their maximum m, unless it is so much smaller than the values that
+// matter (|x| up to |m| + 31 t: weights above 2^-44) that 24 bits do not hold every x - m,
+// as with log-probabilities of a nearly certain token.  Then 0, or for m > 0 a power of
+// two of at least m and at most 0.016 t: within 2^13 of all of those, so that a difference
+// is exact where |x| is the larger, as it is with m otherwise.
+__device__ __forceinline__ float reference(float m, float t) {
+  const float r = t * (31.f / 4095.f);
+  if (!(fabsf(m) < r) || !(r < 1e30f)) return m;
+  return m > 0.f ? __uint_as_float((__float_as_uint(r) + 0x7fffffu) & 0xff800000u) : 0.f;
+}
 
 constexpr unsigned kTable = 128;
 
@@ -125,24 +137,24 @@ __device__ __forceinline__ F2 f2_add(F2 a, F2 b) {
 }
 __device__ __forceinline__ F2 f2_sub(F2 a, F2 b) { return f2_fma(b, f2_of(-1.f), a); }
 
-// Weights of two values: 2^44 exp((x - m) / t), cut to a whole number.
+// Weights of two values: 2^44 exp((x - ref) / t), cut to a whole number.
 // 2^e with e = n/128 + r, |r| <= 1/256:  2^(30 + (n mod 128)/128) * (1 + q) *
 // 2^(n div 128 - 30), q = 2^r - 1.  -n (>= 0) is read off the low bits of
 // -e * 128 + 1.5 * 2^23; with 127 added, its low 7 bits are the table's index and the
 // others the shift.  The product with q is a 32-bit high product of the table's
 // 2^30 .. 2^31 and q * 2^32 (the only conversion).  -inf shifts everything out.
-// TWO: the rounding error of x - m by the form for any two floats; 16-bit values
-// need only the form for |x| <= |m|, because elsewhere their difference is exact.
+// TWO: the rounding error of x - ref by the form for any two floats; 16-bit values
+// need only the form for |x| <= |ref|, because elsewhere their difference is exact.
 template <bool TWO>
 __device__ __forceinline__ void weights(float x0, float x1, const Scale& s, const int* table, unsigned long long (&w)[2]) {
-  const F2 x = f2_of(x0, x1), m = f2_of(s.m), hi = f2_of(s.hi);
+  const F2 x = f2_of(x0, x1), m = f2_of(s.ref), hi = f2_of(s.hi);
   F2 d = f2_sub(x, m);
   d = f2_of(fminf(f2_get(d, 0), 0.f), fminf(f2_get(d, 1), 0.f));  // 0 for x = m = +inf, too
   const F2 minus_p = f2_mul(d, f2_of(-s.hi));
   F2 err;
   if (TWO) {
     const F2 bb = f2_sub(d, x);
-    err = f2_add(f2_sub(x, f2_sub(d, bb)), f2_sub(f2_of(-s.m), bb));
+    err = f2_add(f2_sub(x, f2_sub(d, bb)), f2_sub(f2_of(-s.ref), bb));
   } else {
     err = f2_sub(x, f2_add(d, m));
   }
@@ -536,6 +548,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
   }
   Scale sc;
   sc.m = of_ord((uint32_t)(best >> 32));
+  sc.ref = TWO ? sc.m : reference(sc.m, temp);
   {
     // log2(e) / t as the sum of two floats
     const float h = 1.44269502f, l = 1.92596303e-8f;  // log2(e)

@@ -975,3 +975,23 @@ def test_sampling_top_p_of_a_long_flat_tail(dtype, v, gap, t):
         kept = min(max(np.ceil((a * (1 + (v - 1) * w) - 1) / w), 0), v - 1)
         want = (b * (1 + kept * w) - 1) / w + 1
         assert abs(token - max(want, 0)) <= slack, (a, b, token, want, slack)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("m, low, t", [(7 * 2.0 ** -24, -8.0, 1.0), (-7 * 2.0 ** -24, -8.0, 1.0), (7 * 2.0 ** -24, -4.0, 0.5), (-2.0 ** -23, -2.0, 0.25),
+                                       (0.0, -8.0, 1.0), (2.0 ** -11, -8.0, 1.0), (-2.0 ** -10, -16.0, 2.0), (0.0625, -8.0, 1.0)])
+def test_sampling_next_to_a_border_of_a_nearly_certain_token(dtype, m, low, t):
+    # e^8 tokens of weight about e^-8, then the maximum, next to 0: differences that 24 bits do not hold.  The draw is
+    # the maximum from the border on, which lies where all weights are good to 1e-9 and 2^-44
+    n = 2981
+    x = torch.full((1, n + 1), low)
+    x[0, n] = m
+    x = x.to(DT[dtype])
+    h = x.double().numpy()[0]
+    w = np.exp((h[0] - h[n]) / t)
+    border, slack = n * w / (1 + n * w), 1e-9 + n * 2.0 ** -44
+    u = np.float32(border) + np.arange(-40, 41, dtype=np.float32) * np.float32(2.0 ** -24)
+    got = _sample(x.cuda().expand(len(u), n + 1), u, [t] * len(u))
+    want = np.where(u.astype(np.float64) >= border, n, n - 1)
+    sure = np.abs(u.astype(np.float64) - border) > slack
+    assert sure.sum() >= 79 and np.array_equal(got[sure], want[sure])
