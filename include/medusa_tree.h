@@ -385,9 +385,10 @@ int mt_qk_norm_rope(const mt_norm_rope_desc* desc, const void* q, const void* k,
  * A NaN is stored as the NaN code and does not enter the scale; an infinity
  * makes the scale 2^119 and saturates.
  * A sequence with seq_lens[b] < 0 is no sequence: nothing is written for it.
- * Device status (status_ws, at least 256 bytes): MT_ERR_PAGES for offsets or
- * nodes out of range, a table that does not cover the slots (nothing of that
- * sequence is written), a page id out of range (nothing of that page is
+ * Device status (status_ws, at least 256 bytes): MT_ERR_PAGES for offsets out of
+ * range or falling, an accepted length or node out of range, a table that does not
+ * cover the slots (nothing of that sequence is written; after falling offsets, of
+ * later sequences perhaps not all), a page id out of range (nothing of that page is
  * written); MT_ERR_POSITION for a slot past the RoPE table (nothing of that
  * page is written).  A call must not append to a page twice: not for two
  * sequences, and not through a table that names the page twice.

@@ -181,7 +181,12 @@ __global__ void __launch_bounds__(kWarps * 32, sizeof(T) == 4 ? 5 : 7) append_ke
     pg = (int)(item - (long long)b * per);
     n = a.accept_len[b] + 1;
     len = a.seq_lens[b];
-    if (n < 1 || n > a.max_depth + 1) {
+    // a node outside the tree anywhere on the path (of 64 at most), and nothing is written
+    const int* path = a.accept_path + (size_t)b * (a.max_depth + 1);
+    const unsigned n0 = lane < n && lane <= a.max_depth ? (unsigned)path[lane] : 0u;
+    const unsigned n1 = lane + 32 < n && lane + 32 <= a.max_depth ? (unsigned)path[lane + 32] : 0u;
+    const bool stray = max(n0, n1) >= (unsigned)a.T;
+    if (n < 1 || n > a.max_depth + 1 || __any_sync(0xffffffffu, stray)) {
       if (lane == 0 && len >= 0) set_status(a.status, kStPages);
       return;
     }
@@ -200,22 +205,15 @@ __global__ void __launch_bounds__(kWarps * 32, sizeof(T) == 4 ? 5 : 7) append_ke
   const T* src = static_cast<const T*>(is_v ? a.v : a.k);
   const long long st0 = is_v ? a.v_st[0] : a.k_st[0], st1 = is_v ? a.v_st[1] : a.k_st[1];
   Row8<T> lo[STEPS], hi[STEPS];
-  bool bad = false;
 #pragma unroll
   for (int s = 0; s < STEPS; ++s) {
     const int r = s * RPS + sub;
-    bool live = r >= r0 && r < r1;
+    const bool live = r >= r0 && r < r1;
     long long row = 0;
     if (live) {
       const int i = pg * kP + r - len;
-      if (a.row_offsets) {
-        row = first_row + i;
-      } else {
-        const int node = a.accept_path[(size_t)b * (a.max_depth + 1) + i];
-        live = node >= 0 && node < a.T;
-        bad = bad || !live;
-        row = (long long)b * a.T + node;
-      }
+      if (a.row_offsets) row = first_row + i;
+      else row = (long long)b * a.T + a.accept_path[(size_t)b * (a.max_depth + 1) + i];
     }
     if (live) {
       const T* p = src + row * st0 + head * st1 + 8 * c;
@@ -226,7 +224,7 @@ __global__ void __launch_bounds__(kWarps * 32, sizeof(T) == 4 ? 5 : 7) append_ke
       hi[s].zero();
     }
   }
-  if (page < 0 || page >= a.num_pages || __any_sync(0xffffffffu, bad)) {  // or a node outside the tree
+  if (page < 0 || page >= a.num_pages) {
     if (lane == 0) set_status(a.status, kStPages);
     return;
   }

@@ -995,3 +995,25 @@ def test_sampling_next_to_a_border_of_a_nearly_certain_token(dtype, m, low, t):
     want = np.where(u.astype(np.float64) >= border, n, n - 1)
     sure = np.abs(u.astype(np.float64) - border) > slack
     assert sure.sum() >= 79 and np.array_equal(got[sure], want[sure])
+
+
+@pytest.mark.parametrize("kind", ["act", "e4m3", "block8"])
+def test_append_accepted_writes_nothing_of_a_path_with_a_stray_node(kind):
+    # the path spans two pages or more, and the node outside the tree falls in one of them
+    rng = np.random.default_rng(160)
+    b, t, hkv, d, dt = 5, 40, 2, 64, torch.float16
+    past, lens = [14, 3, 14, 0, 30], [3, 35, 3, 39, 2]
+    path = np.full((b, 40), -1)
+    for i, n in enumerate(lens):
+        path[i, :n + 1] = rng.permutation(t)[:n + 1]
+    path[0, 3], path[1, 1], path[3, 39] = t, -1, 1 << 30
+    table = _table(rng, [2, 3, 2, 3, 3], 14)
+    cache = Cache(rng, kind, 14, hkv, d, dt)
+    k, v = (_rand(rng, b, t, hkv, d, dtype=dt) for _ in range(2))
+    ws = _status()
+    mt.kv_append_accepted(k.cuda(), v.cuda(), _i32(path).cuda(), _i32(lens).cuda(), cache.k, cache.v, _i32(table).cuda(), _i32(past).cuda(),
+                          status_ws=ws, **cache.args())
+    assert mt.read_status(ws) == -4
+    good = [p if i in (2, 4) else -1 for i, p in enumerate(past)]
+    _append_on_host(cache, k.view(b * t, hkv, d), v.view(b * t, hkv, d), lambda i: [i * t + int(path[i, j]) for j in range(lens[i] + 1)], good, table, None)
+    cache.check()
