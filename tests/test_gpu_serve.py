@@ -1017,3 +1017,116 @@ def test_append_accepted_writes_nothing_of_a_path_with_a_stray_node(kind):
     good = [p if i in (2, 4) else -1 for i, p in enumerate(past)]
     _append_on_host(cache, k.view(b * t, hkv, d), v.view(b * t, hkv, d), lambda i: [i * t + int(path[i, j]) for j in range(lens[i] + 1)], good, table, None)
     cache.check()
+
+
+@pytest.mark.parametrize("bad", ["offsets", "rows", "node", "length"])
+def test_append_of_a_bad_sequence_leaves_its_pages(bad):
+    # what test_append_reports_and_leaves_the_rest reads the status of: the first sequence is written, the bad one is not
+    rng = np.random.default_rng(170)
+    hkv, d, dt = 2, 64, torch.float16
+    past, table = [0, 10, 4], _table(rng, [2, 2, 1], 7)
+    cache, ws = Cache(rng, "block8", 7, hkv, d, dt), _status()
+    kv = _rand(rng, 45, 2, hkv, d, dtype=dt)
+    dev, live = kv.cuda(), [0, -1, -1]
+    if bad in ("offsets", "rows"):
+        # offsets that fall, and after them 35 rows, more than the last sequence's table covers; or a row too many
+        off = [0, 20, 10, 45] if bad == "offsets" else [0, 20, 40, 46]
+        mt.kv_append_paged(dev[:, 0], dev[:, 1], cache.k, cache.v, _i32(table).cuda(), _i32(past).cuda(), _i32(off).cuda(), status_ws=ws, **cache.args())
+        live = [0, -1, -1] if bad == "offsets" else [0, 10, -1]
+        rows = lambda b: list(range(off[b], off[b + 1]))  # noqa: E731
+    else:
+        path, lens = np.array([[0, 1], [0, 3], [0, 2]]), [1, 1, 1]
+        if bad == "node":
+            path[1, 1] = 15
+        else:
+            lens[1] = 2
+        x, live = kv.view(3, 15, 2, hkv, d), [0, -1, 4]
+        mt.kv_append_accepted(x[:, :, 0].contiguous().cuda(), x[:, :, 1].contiguous().cuda(), _i32(path).cuda(), _i32(lens).cuda(), cache.k, cache.v,
+                              _i32(table).cuda(), _i32(past).cuda(), status_ws=ws, **cache.args())
+        rows = lambda b: [15 * b + int(n) for n in path[b]]  # noqa: E731
+    assert mt.read_status(ws) == -4
+    _append_on_host(cache, kv[:, 0], kv[:, 1], rows, live, table, None)
+    cache.check()
+
+
+@pytest.mark.parametrize("batch", [32, 33, 1024, 1025, 2000])
+@pytest.mark.parametrize("kind", ["act", "block8"])
+def test_append_of_large_batches(batch, kind):
+    # an item's sequence is found in one, two or three rounds of 32; some sequences are empty, some absent
+    rng = np.random.default_rng(batch)
+    past = rng.integers(-3, 40, batch)
+    new = rng.integers(-6, 12, batch).clip(0)
+    new[rng.integers(0, batch, 3)] = 50
+    if batch > 1000:
+        new[200:260] = 0
+    past = np.where(past < 0, -1, past)
+    off = np.concatenate([[0], np.cumsum(new)]) + 5  # rows before the first sequence's, too
+    need = [-(-(max(int(p), 0) + int(n)) // P) for p, n in zip(past, new)]
+    table = _table(rng, need, sum(need) + 1)
+    cache = Cache(rng, kind, sum(need) + 1, 1, 64, torch.bfloat16)
+    kv = _rand(rng, int(off[-1]) + 3, 2, 1, 64, dtype=torch.bfloat16)
+    dev, ws = kv.cuda(), _status()
+    mt.kv_append_paged(dev[:, 0], dev[:, 1], cache.k, cache.v, _i32(table).cuda(), _i32(past).cuda(), _i32(off).cuda(), status_ws=ws, **cache.args())
+    assert mt.read_status(ws) == 0
+    _append_on_host(cache, kv[:, 0], kv[:, 1], lambda b: list(range(off[b], off[b + 1])), past, table, None)
+    cache.check()
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("batch, t, hq, hkv, longest", [(330, 20, 32, 32, 16), (300, 17, 64, 64, 60)])
+def test_block8_attention_more_pieces_than_a_list_holds(dtype, batch, t, hq, hkv, longest):
+    # tens of whole segments for every CTA of the tensor-core kernel: each role walks the schedule by itself
+    rng = np.random.default_rng(180)
+    lens = [int(n) for n in rng.integers(-1, longest + 1, batch)]
+    c = _attn_case(rng, batch, t, hq, hkv, 64, [0] * batch, dtype)
+    need = [-(-max(n, 0) // P) for n in lens]
+    c["lens"], pages = lens, 40  # sequences share the pages, which nothing writes
+    c["k"], c["v"] = (ref.encode(rng.standard_normal((pages, hkv, P, 64))) for _ in range(2))
+    c["ks"], c["vs"] = (2.0 ** rng.integers(-2, 2, (pages, hkv)).astype(np.float64) for _ in range(2))
+    c["table"] = np.where(np.arange(max(need))[None] < np.array(need)[:, None], rng.integers(0, pages, (batch, max(need))), -1)
+    top = max(float(c["vn"].abs().max()), float((np.abs(ref.decode(c["v"])) * c["vs"][:, :, None, None]).max()))
+    out, ws, args, kw = _attn_run(c)
+    assert mt.read_status(ws) == 0
+    got = out.clone()
+    # some sequences against the definition, and all of them against calls of a few at a time (each within its tolerance)
+    few = rng.choice(batch, 4, replace=False)
+    part = {n: c[n][few] for n in ("q", "kn", "vn", "table", "parents")}
+    _attn_check({**c, **part, "lens": [lens[i] for i in few]}, got[torch.from_numpy(few).cuda()])
+    for b0 in range(0, batch, 30):
+        sub = [args[0][b0:b0 + 30], *args[1:5], *(x[b0:b0 + 30].contiguous() for x in args[5:8]), torch.full_like(args[0][b0:b0 + 30], 5.0)]
+        new = {n: kw[n][b0:b0 + 30] for n in ("k_new", "v_new")}
+        mt.tree_attn_paged_block8(*sub, **new, workspace=mt.alloc_block8_workspace(sub[0], sub[1], sub[5]))
+        a, b = sub[8].double(), got[b0:b0 + 30].double()
+        assert bool(((a - b).abs() <= 2 * (ref.HALF_STEP[out.dtype] * b.abs() + (2.0 ** -11 + 2.0 ** -8) * top)).all())
+
+
+@pytest.mark.parametrize("t, hq, hkv", ROWS)
+def test_block8_attention_under_a_wide_block_table(t, hq, hkv):
+    # a serving loop's tables have the model's whole length, whatever the sequences have
+    c = _attn_case(np.random.default_rng(190), 2, t, hq, hkv, 128, [700, 37], "bf16")
+    near = _attn_run(c)[0]
+    wide = np.full((2, 131072 // P), -1)
+    wide[:, :c["table"].shape[1]] = c["table"]
+    c["table"] = wide
+    out, ws, _, _ = _attn_run(c)
+    assert mt.read_status(ws) == 0
+    _attn_check(c, out)
+    _attn_check(c, near)
+
+
+@pytest.mark.parametrize("t, hq, hkv", ROWS)
+def test_block8_attention_keeps_eleven_bits_of_a_weight(t, hq, hkv):
+    # as _attn_check, with queries so small that scores are good to 2^-13 (2 D 2^-24 sum |q k| scale < 2^-14 with a sum
+    # <= 3; elements to 2^-17.8 of a largest of 1.1, times sum |k| scale <= 9: < 2^-14): what is left is the rounding of
+    # the weights and of the output
+    c = _attn_case(np.random.default_rng(200), 2, t, hq, hkv, 128, [300, 20], "f16", spread=0.25)
+    q = c["q"].double().numpy()
+    want, mag = ref.attn64(q, c["k"], c["v"], c["ks"], c["vs"], c["table"], c["lens"], c["parents"], c["kn"].double().numpy(), c["vn"].double().numpy(), 128 ** -0.5)
+    out, ws, args, kw = _attn_run(c)
+    tol = ref.HALF_STEP[torch.float16] * np.abs(want) + (2.0 ** -11 + 2 * 2.0 ** -13) * mag + 1e-7
+    assert (np.abs(out.cpu().double().numpy() - want) <= tol).all()
+    again = out.clone()
+    for _ in range(3):  # and the same bits every time
+        out.zero_()
+        mt.tree_attn_paged_block8(*args, **kw)
+        assert torch.equal(out, again)
