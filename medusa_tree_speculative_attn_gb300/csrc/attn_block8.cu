@@ -269,8 +269,8 @@ __device__ __forceinline__ void page_step(State<D, NT>& st, const uint8_t* kp, c
 }
 
 // One block of up to 16 new tokens of K or V as codes in shared memory (rows
-// past T are zero); returns the block's scale.  odd: which tokens have a value that is
-// not finite, found by the call for the values and used by the one for the keys.
+// past T are zero); returns the block's scale.  odd: which tokens have an element that is
+// not finite, added to by the call for the values and then the one for the keys.
 template <typename T, int D>
 __device__ __forceinline__ float quantise_new(const T* src, size_t row_stride, int rows, uint8_t* dst, bool keys,
                                               unsigned& odd) {
@@ -287,26 +287,16 @@ __device__ __forceinline__ float quantise_new(const T* src, size_t row_stride, i
       hi[s].load(src + r * row_stride + D / 2 + 8 * c);
     }
   }
-  unsigned found = 0;
-#pragma unroll
-  for (int s = 0; s < STEPS; ++s) found |= odd_rows<RPS>(not_finite(lo[s]) || not_finite(hi[s])) << (s * RPS);
-  if (found) {
+  float amax = largest_bits<T, STEPS>(lo, hi);
+  if (!(amax < INFINITY)) {
 #pragma unroll
     for (int s = 0; s < STEPS; ++s) {
-      replace_odd(lo[s], keys ? __int_as_float(0x7fffffff) : 0.f);
-      replace_odd(hi[s], keys ? __int_as_float(0x7fffffff) : 0.f);
+      odd |= odd_rows<RPS>(not_finite(lo[s]) || not_finite(hi[s])) << (s * RPS);
+      drop_odd(lo[s]);
+      drop_odd(hi[s]);
     }
+    amax = largest_bits<T, STEPS>(lo, hi);
   }
-  if (!keys) odd = found;
-  AbsMax<T> top;
-#pragma unroll
-  for (int s = 0; s < STEPS; ++s) {
-    top.add(lo[s]);
-    top.add(hi[s]);
-  }
-  float amax = top.get();
-#pragma unroll
-  for (int off = 16; off > 0; off >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, off));
   const float scale = block_scale(amax), inv = 1.f / scale;
 #pragma unroll
   for (int s = 0; s < STEPS; ++s) {

@@ -74,54 +74,39 @@ __device__ __forceinline__ void quantise_block(const T* src, const T* values, si
                                                float* scale_out) {
   constexpr int LPR = D / 16, RPS = 32 / LPR, STEPS = 16 / RPS;
   const int lane = threadIdx.x & 31, sub = lane / LPR, c = lane % LPR;
-  Row8<T> lo[STEPS], hi[STEPS];
+  Row8<T> lo[STEPS], hi[STEPS], vlo[STEPS], vhi[STEPS];
 #pragma unroll
   for (int s = 0; s < STEPS; ++s) {
     const int r = s * RPS + sub;
     lo[s].zero();
     hi[s].zero();
+    vlo[s].zero();
+    vhi[s].zero();
     if (r < rows) {
       lo[s].load(src + r * row_stride + 16 * c);
       hi[s].load(src + r * row_stride + 16 * c + 8);
-    }
-  }
-  unsigned found = 0;
-#pragma unroll
-  for (int s = 0; s < STEPS; ++s) found |= odd_rows<RPS>(not_finite(lo[s]) || not_finite(hi[s])) << (s * RPS);
-  if (found) {
-#pragma unroll
-    for (int s = 0; s < STEPS; ++s) {
-      replace_odd(lo[s], values ? __int_as_float(0x7fffffff) : 0.f);
-      replace_odd(hi[s], values ? __int_as_float(0x7fffffff) : 0.f);
-    }
-  }
-  float amax = 0.f;
-#pragma unroll
-  for (int s = 0; s < STEPS; ++s) {
-    float x[8], y[8];
-    lo[s].to_f(x);
-    hi[s].to_f(y);
-#pragma unroll
-    for (int e = 0; e < 8; ++e) amax = fmaxf(amax, fmaxf(fabsf(x[e]), fabsf(y[e])));
-  }
-#pragma unroll
-  for (int off = 16; off > 0; off >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, off));
-  const float scale = block_scale(amax), inv = 1.f / scale;
-  unsigned odd = 0;  // of keys: the tokens that have a value that is not finite
-  if (values) {
-#pragma unroll
-    for (int s = 0; s < STEPS; ++s) {
-      const int r = s * RPS + sub;
-      Row8<T> v0, v1;
-      v0.zero();
-      v1.zero();
-      if (r < rows) {
-        v0.load(values + r * row_stride + 16 * c);
-        v1.load(values + r * row_stride + 16 * c + 8);
+      if (values) {  // asked for with the rest
+        vlo[s].load(values + r * row_stride + 16 * c);
+        vhi[s].load(values + r * row_stride + 16 * c + 8);
       }
-      odd |= odd_rows<RPS>(not_finite(v0) || not_finite(v1)) << (s * RPS);
     }
   }
+  unsigned odd = 0;  // the tokens that have an element that is not finite
+  if (values && !(largest_bits<T, STEPS>(vlo, vhi) < INFINITY)) {
+#pragma unroll
+    for (int s = 0; s < STEPS; ++s) odd |= odd_rows<RPS>(not_finite(vlo[s]) || not_finite(vhi[s])) << (s * RPS);
+  }
+  float amax = largest_bits<T, STEPS>(lo, hi);
+  if (!(amax < INFINITY)) {
+#pragma unroll
+    for (int s = 0; s < STEPS; ++s) {
+      odd |= odd_rows<RPS>(not_finite(lo[s]) || not_finite(hi[s])) << (s * RPS);
+      drop_odd(lo[s]);
+      drop_odd(hi[s]);
+    }
+    amax = largest_bits<T, STEPS>(lo, hi);
+  }
+  const float scale = block_scale(amax), inv = 1.f / scale;
 #pragma unroll
   for (int s = 0; s < STEPS; ++s) {
     const int r = s * RPS + sub;
@@ -133,7 +118,7 @@ __device__ __forceinline__ void quantise_block(const T* src, const T* values, si
       x[e] *= inv;
       y[e] *= inv;
     }
-    if (odd >> r & 1u) x[0] = __int_as_float(0x7fffffff);
+    if (values && (odd >> r & 1u)) x[0] = __int_as_float(0x7fffffff);
     const uint2 u = e4m3x8_of(x), v = e4m3x8_of(y);
     *reinterpret_cast<uint4*>(dst + r * D + 16 * c) = make_uint4(u.x, u.y, v.x, v.y);
   }

@@ -212,6 +212,24 @@ struct Block8Params {
   int* pieces;            // piece table (common.cuh)
 };
 
+// Largest magnitude of a warp's rows of 16-bit values, by their bits, so that an infinity
+// or a NaN is larger than any number.
+template <typename T, int STEPS>
+__device__ __forceinline__ float largest_bits(const Row8<T> (&lo)[STEPS], const Row8<T> (&hi)[STEPS]) {
+  unsigned top = 0;
+#pragma unroll
+  for (int s = 0; s < STEPS; ++s) {
+    const uint4 a = lo[s].w[0], b = hi[s].w[0];
+    const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+#pragma unroll
+    for (int e = 0; e < 8; ++e) top = __vmaxu2(top, w[e] & 0x7fff7fffu);
+  }
+  const uint16_t bits = (uint16_t)__reduce_max_sync(0xffffffffu, max(top >> 16, top & 0xffffu));
+  T v;
+  memcpy(&v, &bits, 2);
+  return Act<T>::to_f(v);
+}
+
 // Whether a packed 16-bit row has a NaN or an infinity.
 template <typename T>
 __device__ __forceinline__ bool not_finite(const Row8<T>& r) {
@@ -226,10 +244,9 @@ __device__ __forceinline__ bool not_finite(const Row8<T>& r) {
 // A new token that holds a NaN or an infinity makes NaN of the nodes that see it and must
 // leave the others alone.  But a NaN value would reach those too, as 0 * NaN in the matrix
 // products, and an infinity by way of its block's scale, under which every other code of
-// the block is 0.  So neither enters a scale, in a value it becomes a code of 0, in a key
-// NaN, and of a token with such a value a key code is NaN, too: its scores are NaN where it
-// is seen and are replaced where it is not.  Of R rows in a warp, 32 / R lanes each: bit i
-// says that row i has one.
+// the block is 0.  So neither enters a scale, both get codes of 0, and a code of the
+// token's key is NaN: its scores are NaN where it is seen and are replaced where it is not.
+// Of R rows in a warp, 32 / R lanes each: bit i says that row i has one.
 template <int R>
 __device__ __forceinline__ unsigned odd_rows(bool odd) {
   const unsigned lanes = __ballot_sync(0xffffffffu, odd);
@@ -240,11 +257,11 @@ __device__ __forceinline__ unsigned odd_rows(bool odd) {
   return rows;
 }
 template <typename T>
-__device__ __forceinline__ void replace_odd(Row8<T>& r, float by) {
+__device__ __forceinline__ void drop_odd(Row8<T>& r) {
   float x[8];
   r.to_f(x);
 #pragma unroll
-  for (int e = 0; e < 8; ++e) x[e] = fabsf(x[e]) < INFINITY ? x[e] : by;
+  for (int e = 0; e < 8; ++e) x[e] = fabsf(x[e]) < INFINITY ? x[e] : 0.f;
   r.from_f(x);
 }
 
