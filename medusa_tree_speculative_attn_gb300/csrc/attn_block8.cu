@@ -408,15 +408,18 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::CTAS) attn_block8_kernel
   // of everybody's registers.  Its lanes do so together, with the same values: where one
   // thread did, its loops and divisions left it apart from its warp in an instance that
   // fills its registers, and the warp then came to each barrier twice.
-  __shared__ PieceIter s_it;
+  __shared__ long long s_cur, s_end;
   __shared__ Piece s_piece;
-  __shared__ int s_more;
+  __shared__ int s_bcur, s_more;
+  Sched sc = a.sched;
+  sc.tile_pfx = s_pfx;
+  sc.splits = 0;
   if (warp == 0) {
-    Sched sc = a.sched;
-    sc.tile_pfx = s_pfx;
     PieceIter it;
     it.init(sc, blockIdx.x);
-    s_it = it;
+    s_cur = it.cur;
+    s_end = it.end;
+    s_bcur = it.bcur;
     __syncwarp();
   }
   uint8_t* ring = smem + warp * (C::DEPTH * 2 * C::kPage);
@@ -426,11 +429,17 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::CTAS) attn_block8_kernel
 
   while (true) {
     if (warp == 0) {
-      PieceIter it = s_it;
+      PieceIter it;
+      it.s = sc;
+      it.cta = blockIdx.x;
+      it.cur = s_cur;
+      it.end = s_end;
+      it.bcur = s_bcur;
       Piece next;
       const bool more = it.next(next);
       __syncwarp();  // every lane has read the cursor
-      s_it = it;
+      s_cur = it.cur;
+      s_bcur = it.bcur;
       s_piece = next;
       s_more = more;
       __syncwarp();
@@ -681,8 +690,6 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::CTAS) attn_block8_kernel
       // others' results are visible to it through the counter, which is that of
       // the segment's first CTA (a CTA's run crosses into at most one segment that
       // another CTA goes on with)
-      Sched sc = a.sched;
-      sc.tile_pfx = s_pfx;
       const int nt = s_pfx[b + 1] - s_pfx[b];
       const int HR = sc.Hkv * sc.nrg;
       const long long X = sched_total_cost(sc);

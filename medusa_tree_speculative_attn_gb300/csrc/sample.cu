@@ -886,7 +886,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
 }
 
 // Largest staged slice.  Up to about 74 KB of it two CTAs fit an SM beside their Smem of
-// 39 KB; above (fp32 rows of 151k to 196k tokens) one.
+// 39 KB; above (fp32 rows of 153k to 196k tokens, 16-bit ones of twice that) one.
 constexpr int kStageMax = 96 * 1024;
 constexpr int kMaxDevices = 64;
 
