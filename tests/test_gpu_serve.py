@@ -1130,3 +1130,13 @@ def test_block8_attention_keeps_eleven_bits_of_a_weight(t, hq, hkv):
         out.zero_()
         mt.tree_attn_paged_block8(*args, **kw)
         assert torch.equal(out, again)
+
+
+@pytest.mark.parametrize("t, hq, hkv", ROWS)
+def test_block8_attention_of_value_scales_below_the_range(t, hq, hkv):
+    # the documented floor, in either kernel
+    c = _attn_case(np.random.default_rng(210), 1, t, hq, hkv, 128, [90], "bf16")
+    low, floor = {**c, "vs": c["vs"].copy()}, {**c, "vs": c["vs"].copy()}
+    for page, value in zip(c["table"][0], (2.0 ** -90, 1e-30, 2.0 ** -126)):
+        low["vs"][page], floor["vs"][page] = value, 2.0 ** -64
+    assert torch.equal(_attn_run(low)[0], _attn_run(floor)[0])
