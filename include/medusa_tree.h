@@ -424,9 +424,11 @@ int mt_kv_append_accepted(const mt_append_desc* desc, int tree_size, int max_dep
  *     mt_kv_append_paged writes them, and is only read: no scratch slots, and the
  *     table need cover slots 0 .. seq_lens[b] - 1 only;
  *   - q and k_new are rows as they attend (rotated by mt_qk_norm_rope);
- *   - the tree's own keys and values are seen as they will be stored, as E4M3
- *     codes in blocks of 16 nodes (nodes 16j .. 16j + 15 of one KV head) with the
- *     block scale above.
+ *   - the tree's own keys and values are seen as the append would encode them in
+ *     blocks of 16 nodes (nodes 16j .. 16j + 15 of one KV head), as E4M3 codes with
+ *     the block scale above.  (An accepted node's page has other rows and so perhaps
+ *     another scale: its stored values differ where a code underflows under one of
+ *     the two, here by way of large siblings that were rejected.)
  * T = 1 is a decoding step (tree_parents null, or -1); tree_parents null is a
  * chain, each node the child of the one before it.
  *   q [B][T][Hq][D], k_new, v_new [B][T][Hkv][D], out [B][T][Hq][D]  act (fp16 or bf16)

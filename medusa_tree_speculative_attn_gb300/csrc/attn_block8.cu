@@ -3,10 +3,10 @@
 //
 // The T new tokens of a sequence (T = 1: a decoding step) attend to its L
 // cached slots and to their own tree ancestors (the Medusa tree mask, vLLM
-// issue 1171); the cache is only read.  The new keys and values are seen as
-// they will be stored: in blocks of 16 new tokens, each block of a KV head
-// under its own power-of-two scale, so the values do not change when an
-// accepted token is appended (beyond codes that underflow).
+// issue 1171); the cache is only read.  The new keys and values are seen as the
+// append encodes them, in blocks of 16 new tokens, each block of a KV head under
+// its own power-of-two scale.  Stored, an accepted token shares its page's scale
+// with other rows: a power of two changes no code's value but by underflow.
 //
 // With few query rows (T * g for g query heads per KV head) the cache's bytes
 // bound the work, so the codes go from memory to the matrix instructions with
@@ -41,8 +41,8 @@
 // a call is one launch.
 //
 // Bound by the cache's bytes: 64 sequences of 256 to 8192 tokens, 32 query and 8 KV
-// heads of 128 columns, one query each: 95 us for 549 MB, 5.8 TB/s (85 % of a copy).
-// A call for one sequence of 2048 tokens takes 13.1 us, all of it latency: the
+// heads of 128 columns, one query each: 95 to 97 us for 549 MB, 5.7 TB/s (84 % of a copy).
+// A call for one sequence of 2048 tokens takes 12.4 us, all of it latency: the
 // prefix, the first page ids, the first pages, one merge.
 #include <atomic>
 #include <cmath>
@@ -749,11 +749,14 @@ Block8Plan block8_plan(int batch, int kv_heads, int rows, int g, int max_blocks,
   Block8Plan p{};
   // Up to 16 rows the register-fragment kernel, which wastes no rows; from 17 on the
   // tensor-core kernel, whose tile has 128 (256) rows.  64 sequences of 256 to 8192
-  // tokens, 8 KV heads: 16 rows 106 us against 177, 24 rows 195 against 177, 32 rows
+  // tokens, 8 KV heads: 16 rows 107 us against 177, 24 rows 195 against 177, 32 rows
   // 205 against 177; 4 sequences of 2000: 20.9 against 21.9, and 32.8 against 22.6.
-  // The latter keeps a token's g rows in one tile, so where g does not divide 128 the
-  // former takes every count.  fp16 queries fill three operand parts, and with those
-  // two tiles do not fit in TMEM.
+  // The latter's tiles are built for g that divides 128; for any other g the former
+  // takes every count, and streams a KV head's cache once per 32 rows: 16 sequences of
+  // 512 to 8192 tokens, 64 nodes, 24, 28 and 40 query heads for 8, 4 and 8 KV heads 321,
+  // 348 and 518 us, where 32 for 8 take 95.  (A tile of 128 / g * g rows would hold whole
+  // tokens of any g.)  fp16 queries fill three operand parts, and with those two tiles
+  // do not fit in TMEM: the same trees 119 us.
   if (rows > 16 && tc_supported(128, g)) {
     p.tc = true;
     p.parts = dtype == 1 ? 3 : 2;
@@ -766,14 +769,17 @@ Block8Plan block8_plan(int batch, int kv_heads, int rows, int g, int max_blocks,
     // starting and leaving a piece costs as much as twelve tiles: 64 sequences of one
     // query and of 16 rows, and 16 of 16 rows, take 95, 107 and 51 us with 8, 95, 106
     // and 50 with 12, 96, 113 and 53 with 24 (with 2, an earlier kernel took 107 us
-    // for the first against 100 with 8)
+    // for the first against 100 with 8).  Not measured with few sequences, whose pieces
+    // are few
     p.seg_cost = 12;
   }
   p.nrg = (rows + p.rows_per_group - 1) / p.rows_per_group;
   if (!p.tc) {
     // Few segments: a piece of t tiles takes about t / 2 us and the merge about
     // 0.1 us a piece, so a segment of n tiles is best cut into about sqrt(5 n)
-    // pieces (n from the block table's width, which is all the host knows).
+    // pieces (n from the block table's width, which is all the host knows: under a
+    // table of 131072 slots one sequence of 2048 tokens, 32/8 heads, takes 16.2 us
+    // against 12.2 under one of 2048; with 32 KV heads 12.9 and 12.8).
     const double n = max_blocks / 4.0 + (tree_size + 63) / 64;
     const double most = (double)batch * kv_heads * p.nrg * std::ceil(std::sqrt(5.0 * n));
     if (most < p.ctas) p.ctas = (int)most;

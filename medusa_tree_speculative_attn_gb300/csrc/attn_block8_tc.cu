@@ -33,10 +33,10 @@
 //
 // Bound by the roles' chains of steps, not by a unit: with 256 rows a tile takes
 // about 1950 cycles, of which the tensor cores work 1070 and the schedulers issue
-// half.  8 sequences of 32768 keys, 26 nodes, 64 query and 8 KV heads: 227 us, 53 % of
-// the products' floor; 16 sequences of 512 to 8192 keys, 64 nodes, 32 query and 8
-// KV heads: 94 us; 64 sequences of 256 to 8192 keys, 32 rows a head: 176 us, 47 % of
-// a copy of the cache.
+// half.  8 sequences of 32768 keys, 26 nodes, 64 query and 8 KV heads: 228 us, 53 % of
+// the products' floor (238 called with other inputs each time); 16 sequences of 512 to
+// 8192 keys, 64 nodes, 32 query and 8 KV heads: 95 us; 64 sequences of 256 to 8192 keys,
+// 32 rows a head: 176 us, 47 % of a copy of the cache.
 #include <cudaTypedefs.h>
 
 #include <atomic>
