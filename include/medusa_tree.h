@@ -466,6 +466,29 @@ int mt_tree_attn_paged_block8(const mt_attn_desc* desc, const void* q, const voi
                               const int32_t* tree_parents, void* out, void* workspace,
                               size_t ws_bytes, cudaStream_t stream);
 
+/* ---- A sliding window and sinks; log-sum-exp of the rows -----------------------
+ * mt_tree_attn_paged_block8 with a window over a long sequence whose first tokens stay
+ * visible, and with the softmax's denominator as an output.  Cached slot s has position
+ * s; new token i, at depth d of the tree (the chain), has position seq_lens[b] + d.  It
+ * sees a cached slot, or an ancestor, of position p when
+ *   p < sinks  or  p > seq_lens[b] + d - window
+ * (itself always: window >= 1 counts it; window 0: everything, whatever `sinks`).
+ *   lse fp32 [B][T][Hq], or null: ln of the sum of exp(score) over what the row sees
+ *   (scores times sm_scale, natural units).
+ * Pages that no new token of the sequence sees are not read, nor their entries of the
+ * block table: those pages may serve other sequences, and the entries may hold anything.
+ * The bytes read, and the time, go by the window and not by the length.  seq_lens[b] is
+ * still bounded by the table's width.
+ * All else as for mt_tree_attn_paged_block8: its rounding, its workspace (its size is
+ * enough), its device status.  lse must not overlap q, k_new, v_new or out.  NaN and
+ * infinities in places that a row does not see have no effect on it. */
+int mt_tree_attn_paged_block8_window(const mt_attn_desc* desc, int window, int sinks, const void* q,
+                                     const void* k_new, const void* v_new, const void* k_cache,
+                                     const void* v_cache, const float* k_scales, const float* v_scales,
+                                     const int32_t* block_tables, const int32_t* seq_lens,
+                                     const int32_t* tree_parents, void* out, float* lse,
+                                     void* workspace, size_t ws_bytes, cudaStream_t stream);
+
 /* ---- Sampling --------------------------------------------------------------------
  * A drawn token beside the argmax that greedy and typical acceptance return (the
  * bonus token of an accepted path's last row, or a decoding step's).  For each i,

@@ -15,7 +15,8 @@ Calls (same names as the C ABI without the ``mt_`` prefix):
   qk_norm_rope       norms of query and key heads, with the rotation in the same pass
   kv_append_paged    new keys and values into the paged cache (prompts, decoding steps)
   kv_append_accepted an accepted path's keys and values into the paged cache
-  tree_attn_paged_block8  tree attention over an 8-bit cache with a scale per page and head
+  tree_attn_paged_block8  tree attention over an 8-bit cache with a scale per page and head,
+                     of the whole cache or under a sliding window with sinks
   sample_tokens      temperature, top-k, top-p and min-p from given uniform numbers
 """
 from __future__ import annotations
@@ -113,6 +114,7 @@ def _load():
         lib.mt_tree_attn_block8_workspace_size.argtypes = [P]
         lib.mt_tree_attn_block8_workspace_size.restype = Z
         lib.mt_tree_attn_paged_block8.argtypes = [P] + [P] * 12 + [Z, P]
+        lib.mt_tree_attn_paged_block8_window.argtypes = [P, I, I] + [P] * 13 + [Z, P]
         lib.mt_sample_tokens.argtypes = [I, I, I, P, I, L] + [P] * 7 + [P]
         lib.mt_read_status.argtypes = [P, P, ctypes.POINTER(I)]
         lib.mt_profile_enable.argtypes = [I]
@@ -535,6 +537,13 @@ def _act(t, name, kinds=_DTYPES):
     return _DTYPES[t.dtype]
 
 
+def _int32(x, name):
+    """A count: a whole number of 0 .. 2^31 - 1 (ctypes would cut a larger one)."""
+    if not 0 <= x < 2 ** 31:
+        raise ValueError(f"{name} must be in [0, 2^31), got {x}")
+    return int(x)
+
+
 def _status_arg(t, name, dev, nbytes=256):
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
@@ -690,7 +699,7 @@ def alloc_block8_workspace(q, k_cache, block_tables) -> torch.Tensor:
 
 def tree_attn_paged_block8(q, k_cache, v_cache, k_scales, v_scales, block_tables, seq_lens,
                            tree_parents, out, *, k_new, v_new, workspace: torch.Tensor,
-                           sm_scale: float = 0.0, stream=None):
+                           sm_scale: float = 0.0, window: int = 0, sinks: int = 0, lse=None, stream=None):
     """out[b,i,h] = attention of new token i (head h) over the cached slots
     0 .. seq_lens[b]-1 and its tree ancestors, itself included (tree_parents
     None: the tokens are a chain; T = 1: a decoding step).
@@ -700,7 +709,13 @@ def tree_attn_paged_block8(q, k_cache, v_cache, k_scales, v_scales, block_tables
     are seen as kv_append_paged would store them, in blocks of 16 tokens.  A
     sequence with seq_lens[b] < 0 leaves its rows of out as they were.  out must
     not overlap q, k_new or v_new; the workspace serves any call that it is large
-    enough for, one at a time."""
+    enough for, one at a time.
+
+    With window > 0 a new token at position p (seq_lens[b] + its depth) sees the
+    positions behind p - window and the first `sinks` ones alone; the cost goes by
+    the window, and pages that no new token sees are not touched (their table
+    entries may be -1).  lse [B,T,Hq] (float32, or None) receives ln of each row's
+    sum of exp(score)."""
     dev = _cuda_device(q, "q")
     dt = q.dtype
     _act(q, "q", (torch.float16, torch.bfloat16))
@@ -712,16 +727,21 @@ def tree_attn_paged_block8(q, k_cache, v_cache, k_scales, v_scales, block_tables
         raise ValueError("block_tables must have 2 dims")
     cache, scales, new, rows = (pages, hkv, page, d), (pages, hkv), (b, t, hkv, d), (b, t, hq, d)
     f32, i32 = torch.float32, torch.int32
-    _invoke(_load().mt_tree_attn_paged_block8, "mt_tree_attn_paged_block8", dev, stream,
-            _block8_desc(q, k_cache, block_tables, sm_scale), _arg(q, "q", dt, rows, dev),
-            _arg(k_new, "k_new", dt, new, dev), _arg(v_new, "v_new", dt, new, dev),
+    args = (_arg(q, "q", dt, rows, dev), _arg(k_new, "k_new", dt, new, dev), _arg(v_new, "v_new", dt, new, dev),
             _arg(k_cache, "k_cache", _E4M3, cache, dev), _arg(v_cache, "v_cache", _E4M3, cache, dev),
             _arg(k_scales, "k_scales", f32, scales, dev), _arg(v_scales, "v_scales", f32, scales, dev),
             _arg(block_tables, "block_tables", i32, (b, block_tables.shape[1]), dev),
             _arg(seq_lens, "seq_lens", i32, (b,), dev),
             None if tree_parents is None else _arg(tree_parents, "tree_parents", i32, (b, t), dev),
-            _arg(out, "out", dt, rows, dev), _status_arg(workspace, "workspace", dev),
-            workspace.numel() * workspace.element_size())
+            _arg(out, "out", dt, rows, dev))
+    desc = _block8_desc(q, k_cache, block_tables, sm_scale)
+    ws = _status_arg(workspace, "workspace", dev), workspace.numel() * workspace.element_size()
+    if window == 0 and lse is None:
+        _invoke(_load().mt_tree_attn_paged_block8, "mt_tree_attn_paged_block8", dev, stream, desc, *args, *ws)
+    else:
+        _invoke(_load().mt_tree_attn_paged_block8_window, "mt_tree_attn_paged_block8_window", dev, stream, desc,
+                _int32(window, "window"), _int32(sinks, "sinks"), *args,
+                None if lse is None else _arg(lse, "lse", f32, (b, t, hq), dev), *ws)
     return out
 
 

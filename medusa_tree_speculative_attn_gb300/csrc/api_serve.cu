@@ -1,5 +1,6 @@
 // C ABI of the serving operators around the verify step: host-side validation,
 // workspace layout and launches.
+#include <climits>
 #include <cmath>
 
 #include "api_common.cuh"
@@ -49,12 +50,13 @@ int check_block8(const mt_attn_desc* d) {
 }
 
 struct Block8Ws {
-  size_t ml, o, counters, pfx, anc, pieces, q8, q_scale, k_blocks, v_blocks, block_scales, total;
+  size_t ml, o, counters, pfx, anc, pieces, q8, q_scale, k_blocks, v_blocks, block_scales, depth, total;
   int rows, nrg, part_rows, G;
   Block8Plan plan;
 };
 
-int block8_ws(const mt_attn_desc* d, Block8Ws* w) {
+// visible_blocks: the most pages that a sequence's new tokens see
+int block8_ws(const mt_attn_desc* d, int visible_blocks, Block8Ws* w) {
   int dev = 0, sms = 0;
   if (cudaGetDevice(&dev) != cudaSuccess ||
       cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
@@ -62,8 +64,8 @@ int block8_ws(const mt_attn_desc* d, Block8Ws* w) {
   const long long rows = (long long)d->tree_size * (d->num_q_heads / d->num_kv_heads);
   if (rows > (1 << 20)) return MT_ERR_UNSUPPORTED;
   w->rows = (int)rows;
-  w->plan = block8_plan(d->batch, d->num_kv_heads, w->rows, d->num_q_heads / d->num_kv_heads, d->max_blocks_per_seq,
-                        d->tree_size, d->dtype, sms);
+  w->plan = block8_plan(d->batch, d->num_kv_heads, w->rows, d->num_q_heads / d->num_kv_heads, visible_blocks, d->tree_size,
+                        d->dtype, sms);
   w->nrg = w->plan.nrg;
   w->part_rows = w->rows < w->plan.rows_per_group ? w->rows : w->plan.rows_per_group;
   w->G = w->plan.ctas;
@@ -94,9 +96,87 @@ int block8_ws(const mt_attn_desc* d, Block8Ws* w) {
     w->k_blocks = take(blocks * 16 * d->head_dim);
     w->v_blocks = take(blocks * 16 * d->head_dim);
     w->block_scales = take(2 * blocks * sizeof(float));
+    w->depth = take(nodes * sizeof(int));
   }
   w->total = off;
   return MT_OK;
+}
+
+// window 0: the whole cache is visible and there is no lse (the kernels without either)
+int attn_block8(const mt_attn_desc* d, int window, int sinks, const void* q, const void* k_new, const void* v_new,
+                const void* k_cache, const void* v_cache, const float* k_scales, const float* v_scales,
+                const int32_t* block_tables, const int32_t* seq_lens, const int32_t* tree_parents, void* out,
+                float* lse, void* workspace, size_t ws_bytes, cudaStream_t stream) {
+  int st = check_block8(d);
+  if (st != MT_OK) return st;
+  if (!q || !k_new || !v_new || !k_cache || !v_cache || !k_scales || !v_scales || !block_tables || !seq_lens || !out ||
+      !workspace)
+    return MT_ERR_INVALID_ARG;
+  if (!aligned16(q) || !aligned16(k_new) || !aligned16(v_new) || !aligned16(k_cache) || !aligned16(v_cache) ||
+      !aligned16(out) || reinterpret_cast<uintptr_t>(workspace) % kAlign)
+    return MT_ERR_INVALID_ARG;
+  // the output is written while other blocks still read the inputs
+  const size_t tokens = (size_t)d->batch * d->tree_size, q_bytes = tokens * d->num_q_heads * d->head_dim * 2;
+  const size_t new_bytes = tokens * d->num_kv_heads * d->head_dim * 2;
+  if (overlap(out, q_bytes, q, q_bytes) || overlap(out, q_bytes, k_new, new_bytes) ||
+      overlap(out, q_bytes, v_new, new_bytes))
+    return MT_ERR_INVALID_ARG;
+  if (lse) {
+    const size_t lse_bytes = tokens * d->num_q_heads * 4;
+    if (reinterpret_cast<uintptr_t>(lse) % 4 || overlap(lse, lse_bytes, q, q_bytes) ||
+        overlap(lse, lse_bytes, k_new, new_bytes) || overlap(lse, lse_bytes, v_new, new_bytes) ||
+        overlap(lse, lse_bytes, out, q_bytes))
+      return MT_ERR_INVALID_ARG;
+  }
+  // sinks in whole pages, and a window that starts and ends inside two
+  long long blocks = d->max_blocks_per_seq;
+  if (window > 0 && ((long long)sinks + 15) / 16 + ((long long)window + 15) / 16 + 1 < blocks)
+    blocks = ((long long)sinks + 15) / 16 + ((long long)window + 15) / 16 + 1;
+  Block8Ws w;
+  st = block8_ws(d, (int)blocks, &w);
+  if (st != MT_OK) return st;
+  if (ws_bytes < w.total) return MT_ERR_INVALID_ARG;
+  char* ws = static_cast<char*>(workspace);
+  Block8Params p{};
+  AttnParams& a = p.a;
+  a.B = d->batch; a.T = d->tree_size; a.Hq = d->num_q_heads; a.Hkv = d->num_kv_heads;
+  a.D = d->head_dim; a.P = d->page_size; a.max_blocks = d->max_blocks_per_seq; a.num_pages = d->num_pages;
+  a.g = d->num_q_heads / d->num_kv_heads;
+  a.rows = w.rows; a.rows_per_group = w.plan.rows_per_group; a.part_rows = w.part_rows;
+  const float scale = d->sm_scale > 0.f ? d->sm_scale : (float)(1.0 / std::sqrt((double)d->head_dim));
+  a.scale_log2 = scale * 1.4426950408889634f;
+  a.q_rot = q; a.k_cache = k_cache; a.v_cache = v_cache;
+  a.block_tables = block_tables; a.seq_lens = seq_lens;
+  a.out = out; a.status = reinterpret_cast<int*>(ws);
+  a.part_ml = reinterpret_cast<float2*>(ws + w.ml);
+  a.sched.B = d->batch; a.sched.T = d->tree_size; a.sched.Hkv = d->num_kv_heads;
+  a.sched.nrg = w.nrg; a.sched.G = w.G; a.sched.splits = 0; a.sched.seg_cost = w.plan.seg_cost;
+  p.k_scales = k_scales; p.v_scales = v_scales;
+  p.k_new = k_new; p.v_new = v_new; p.parents = tree_parents;
+  p.window = window; p.sinks = sinks; p.lse = lse;
+  if (!w.plan.tc) {
+    p.frag_o = reinterpret_cast<float*>(ws + w.o);
+    p.frag_tiles = reinterpret_cast<unsigned*>(ws + w.counters);
+    return cuda_status(launch_attn_block8(p, d->dtype, stream));
+  }
+  a.part_o = ws + w.o;
+  p.tile_pfx = reinterpret_cast<int*>(ws + w.pfx);
+  a.sched.tile_pfx = p.tile_pfx;
+  p.parts = w.plan.parts;
+  p.q8 = reinterpret_cast<uint8_t*>(ws + w.q8);
+  p.q_scale = reinterpret_cast<float*>(ws + w.q_scale);
+  p.k_blocks = reinterpret_cast<uint8_t*>(ws + w.k_blocks);
+  p.v_blocks = reinterpret_cast<uint8_t*>(ws + w.v_blocks);
+  p.k_block_scales = reinterpret_cast<float*>(ws + w.block_scales);
+  p.v_block_scales = p.k_block_scales + (size_t)d->batch * d->num_kv_heads * ((d->tree_size + 15) / 16);
+  p.anc = reinterpret_cast<unsigned long long*>(ws + w.anc);
+  p.depth = reinterpret_cast<int*>(ws + w.depth);
+  p.pieces = reinterpret_cast<int*>(ws + w.pieces);
+  wait_bound(&a.wait_limit_ns, &a.test_stall);
+  st = cuda_status(launch_block8_prep(p, d->dtype, stream));
+  if (st == MT_OK) st = cuda_status(launch_attn_block8_tc(p, d->dtype, stream));
+  if (st != MT_OK) return st;
+  return cuda_status(launch_block8_combine(p, d->dtype, stream));
 }
 
 int append(const mt_append_desc* d, AppendParams& a, const void* k, const void* v, const mt_rope* rope, void* k_cache,
@@ -213,7 +293,7 @@ int mt_kv_append_accepted(const mt_append_desc* d, int tree_size, int max_depth,
 
 size_t mt_tree_attn_block8_workspace_size(const mt_attn_desc* d) {
   Block8Ws w;
-  if (check_block8(d) != MT_OK || block8_ws(d, &w) != MT_OK) return 0;
+  if (check_block8(d) != MT_OK || block8_ws(d, d->max_blocks_per_seq, &w) != MT_OK) return 0;
   return w.total;
 }
 
@@ -222,63 +302,19 @@ int mt_tree_attn_paged_block8(const mt_attn_desc* d, const void* q, const void* 
                               const int32_t* block_tables, const int32_t* seq_lens, const int32_t* tree_parents,
                               void* out, void* workspace, size_t ws_bytes, cudaStream_t stream) {
   const mt_call_range range("mt_tree_attn_paged_block8");
-  int st = check_block8(d);
-  if (st != MT_OK) return st;
-  if (!q || !k_new || !v_new || !k_cache || !v_cache || !k_scales || !v_scales || !block_tables || !seq_lens || !out ||
-      !workspace)
-    return MT_ERR_INVALID_ARG;
-  if (!aligned16(q) || !aligned16(k_new) || !aligned16(v_new) || !aligned16(k_cache) || !aligned16(v_cache) ||
-      !aligned16(out) || reinterpret_cast<uintptr_t>(workspace) % kAlign)
-    return MT_ERR_INVALID_ARG;
-  // the output is written while other blocks still read the inputs
-  const size_t tokens = (size_t)d->batch * d->tree_size, q_bytes = tokens * d->num_q_heads * d->head_dim * 2;
-  const size_t new_bytes = tokens * d->num_kv_heads * d->head_dim * 2;
-  if (overlap(out, q_bytes, q, q_bytes) || overlap(out, q_bytes, k_new, new_bytes) ||
-      overlap(out, q_bytes, v_new, new_bytes))
-    return MT_ERR_INVALID_ARG;
-  Block8Ws w;
-  st = block8_ws(d, &w);
-  if (st != MT_OK) return st;
-  if (ws_bytes < w.total) return MT_ERR_INVALID_ARG;
-  char* ws = static_cast<char*>(workspace);
-  Block8Params p{};
-  AttnParams& a = p.a;
-  a.B = d->batch; a.T = d->tree_size; a.Hq = d->num_q_heads; a.Hkv = d->num_kv_heads;
-  a.D = d->head_dim; a.P = d->page_size; a.max_blocks = d->max_blocks_per_seq; a.num_pages = d->num_pages;
-  a.g = d->num_q_heads / d->num_kv_heads;
-  a.rows = w.rows; a.rows_per_group = w.plan.rows_per_group; a.part_rows = w.part_rows;
-  const float scale = d->sm_scale > 0.f ? d->sm_scale : (float)(1.0 / std::sqrt((double)d->head_dim));
-  a.scale_log2 = scale * 1.4426950408889634f;
-  a.q_rot = q; a.k_cache = k_cache; a.v_cache = v_cache;
-  a.block_tables = block_tables; a.seq_lens = seq_lens;
-  a.out = out; a.status = reinterpret_cast<int*>(ws);
-  a.part_ml = reinterpret_cast<float2*>(ws + w.ml);
-  a.sched.B = d->batch; a.sched.T = d->tree_size; a.sched.Hkv = d->num_kv_heads;
-  a.sched.nrg = w.nrg; a.sched.G = w.G; a.sched.splits = 0; a.sched.seg_cost = w.plan.seg_cost;
-  p.k_scales = k_scales; p.v_scales = v_scales;
-  p.k_new = k_new; p.v_new = v_new; p.parents = tree_parents;
-  if (!w.plan.tc) {
-    p.frag_o = reinterpret_cast<float*>(ws + w.o);
-    p.frag_tiles = reinterpret_cast<unsigned*>(ws + w.counters);
-    return cuda_status(launch_attn_block8(p, d->dtype, stream));
-  }
-  a.part_o = ws + w.o;
-  p.tile_pfx = reinterpret_cast<int*>(ws + w.pfx);
-  a.sched.tile_pfx = p.tile_pfx;
-  p.parts = w.plan.parts;
-  p.q8 = reinterpret_cast<uint8_t*>(ws + w.q8);
-  p.q_scale = reinterpret_cast<float*>(ws + w.q_scale);
-  p.k_blocks = reinterpret_cast<uint8_t*>(ws + w.k_blocks);
-  p.v_blocks = reinterpret_cast<uint8_t*>(ws + w.v_blocks);
-  p.k_block_scales = reinterpret_cast<float*>(ws + w.block_scales);
-  p.v_block_scales = p.k_block_scales + (size_t)d->batch * d->num_kv_heads * ((d->tree_size + 15) / 16);
-  p.anc = reinterpret_cast<unsigned long long*>(ws + w.anc);
-  p.pieces = reinterpret_cast<int*>(ws + w.pieces);
-  wait_bound(&a.wait_limit_ns, &a.test_stall);
-  st = cuda_status(launch_block8_prep(p, d->dtype, stream));
-  if (st == MT_OK) st = cuda_status(launch_attn_block8_tc(p, d->dtype, stream));
-  if (st != MT_OK) return st;
-  return cuda_status(launch_block8_combine(p, d->dtype, stream));
+  return attn_block8(d, 0, 0, q, k_new, v_new, k_cache, v_cache, k_scales, v_scales, block_tables, seq_lens,
+                     tree_parents, out, nullptr, workspace, ws_bytes, stream);
+}
+
+int mt_tree_attn_paged_block8_window(const mt_attn_desc* d, int window, int sinks, const void* q, const void* k_new,
+                                     const void* v_new, const void* k_cache, const void* v_cache,
+                                     const float* k_scales, const float* v_scales, const int32_t* block_tables,
+                                     const int32_t* seq_lens, const int32_t* tree_parents, void* out, float* lse,
+                                     void* workspace, size_t ws_bytes, cudaStream_t stream) {
+  const mt_call_range range("mt_tree_attn_paged_block8_window");
+  if (window < 0 || sinks < 0) return MT_ERR_INVALID_ARG;
+  return attn_block8(d, window ? window : INT_MAX, sinks, q, k_new, v_new, k_cache, v_cache, k_scales, v_scales,
+                     block_tables, seq_lens, tree_parents, out, lse, workspace, ws_bytes, stream);
 }
 
 int mt_sample_tokens(int num_rows, int vocab, mt_dtype logits_dtype, const void* logits, int num_logit_rows,

@@ -40,6 +40,7 @@
 #include <cudaTypedefs.h>
 
 #include <atomic>
+#include <climits>
 
 #include "serve.cuh"
 #include "tc_ptx.cuh"
@@ -215,7 +216,30 @@ __device__ __forceinline__ unsigned long long visible(int L, int npre, int k0, u
   return see;
 }
 
-template <typename T, int D, int MT, int NP>
+// Whether 16 codes hold a NaN; those that do become 0.
+__device__ __forceinline__ bool drop_nan(uint4& c) {
+  uint32_t w[4] = {c.x, c.y, c.z, c.w};
+  bool nan = false;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t m = __vcmpeq4(w[i] & 0x7f7f7f7fu, 0x7f7f7f7fu);
+    nan = nan || m != 0u;
+    w[i] &= ~m;
+  }
+  c = make_uint4(w[0], w[1], w[2], w[3]);
+  return nan;
+}
+
+// REACH: with a window and sinks, and the rows' log-sum-exp.  Only the visible pages are
+// streamed.  A value row of the window's edge, which not every node sees, must not bring a
+// NaN to those that do not: its NaN codes are 0 in the products, and each row that sees it
+// looks for them itself at its end (a CTA that has met one).  16 sequences of 512 to 32768
+// keys under a window of 4096, 64 nodes, 32 query and 8 KV heads: 88 us, 40 % of the
+// products' rate, as without a window.
+// Columns of tile j (from k0) that are cached pages'.
+__device__ __forceinline__ unsigned long long cached(int npre, int k0) { return Reach::below64(npre * 16 - k0); }
+
+template <typename T, int D, int MT, int NP, bool REACH>
 __global__ void __launch_bounds__(Cfg<D, MT, NP>::kThreads, 1)
     attn_block8_tc_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v,
                           const __grid_constant__ CUtensorMap map_kn, const __grid_constant__ CUtensorMap map_vn,
@@ -244,7 +268,8 @@ __global__ void __launch_bounds__(Cfg<D, MT, NP>::kThreads, 1)
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(never + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   int* s_npieces = const_cast<int*>(abort_flag + 1);
-  static_assert((3 * 8 + 8 * 2 + 4) * 8 + 12 <= 1024, "barrier area");
+  volatile int* s_nan = s_npieces + 1;  // REACH: a value row of the window's edge had a NaN
+  static_assert((3 * 8 + 8 * 2 + 4) * 8 + 16 <= 1024, "barrier area");
   // per stage: key scales, log2 and inverse of the value scales, and how many rows
   // of each page hold keys of the sequence
   float* s_scale = reinterpret_cast<float*>(reinterpret_cast<uint8_t*>(bars) + 1024);  // [S][4][4]
@@ -273,6 +298,7 @@ __global__ void __launch_bounds__(Cfg<D, MT, NP>::kThreads, 1)
     tc::mbar_init(&fin[1], 1);
     tc::mbar_init(never, 1);
     *abort_flag = 0;
+    *s_nan = 0;
     tc::fence_barrier_init();
   }
   if (warp == C::kQkWarp) {
@@ -342,10 +368,11 @@ __global__ void __launch_bounds__(Cfg<D, MT, NP>::kThreads, 1)
       if (!ok) break;
       // page ids and scales of 32 pages of the table at a time, a lane each; ids
       // are fetched two windows ahead of use, scales one
-      const int npre = (L + 15) / 16;
+      const Reach reach(L, REACH ? p.window : INT_MAX, REACH ? p.sinks : 0);
+      const int npre = REACH ? reach.npre : (L + 15) / 16;
       const int* bt = a.block_tables + (size_t)pc.b * a.max_blocks;
       const size_t nb0 = ((size_t)pc.b * a.Hkv + pc.kvh) * nnew;  // the new tokens' blocks
-      auto fetch_id = [&](int q) { return q < npre ? __ldg(bt + q) : -1; };
+      auto fetch_id = [&](int q) { return q < npre ? __ldg(bt + (REACH ? reach.page(q) : q)) : -1; };
       auto fetch_scale = [&](const float* sc, int id) {
         return id >= 0 && id < a.num_pages ? __ldg(sc + (size_t)id * a.Hkv + pc.kvh) : 1.f;
       };
@@ -382,13 +409,19 @@ __global__ void __launch_bounds__(Cfg<D, MT, NP>::kThreads, 1)
         if (pg < npre) {
           if (id >= 0 && id < a.num_pages) {
             row = (id * a.Hkv + pc.kvh) * 16;
-            rows = min(16, L - pg * 16);
+            // REACH: the rows that some node sees, and those that not every node sees
+            if (REACH) {
+              rows = (int)reach.see16(pg * 16, 0);
+              rows |= (rows & ~(int)reach.see16(pg * 16, a.T - 1)) << 16;
+            } else {
+              rows = min(16, L - pg * 16);
+            }
           } else if (lane < kPages) {
             set_status(a.status, kStPages);
           }
         } else if (from_new) {
           row = (int)((nb0 + pg - npre) * 16);
-          rows = 16;
+          rows = REACH ? 0xffff : 16;
           ks = __ldg(p.k_block_scales + nb0 + pg - npre);
           const float vs = clamp(__ldg(p.v_block_scales + nb0 + pg - npre));
           lv = log2f(vs);
@@ -451,7 +484,8 @@ __global__ void __launch_bounds__(Cfg<D, MT, NP>::kThreads, 1)
           uint4 c = *reinterpret_cast<const uint4*>(codes + q * 16);
           // rows that hold no key of the sequence may hold anything (NaN codes
           // too): their weights are 0 and so are their values
-          if (r >= rows) c = make_uint4(0, 0, 0, 0);
+          if (REACH ? !(rows >> r & 1) : r >= rows) c = make_uint4(0, 0, 0, 0);
+          if (REACH && (rows >> (16 + r) & 1) && drop_nan(c)) *s_nan = 1;
           const int row = pid * 16 + r, c0 = (col % 64) / 8;
           uint8_t* dst = stage + C::kKTile + (col / 64) * C::kHalf + row * 128;
           const uint32_t w[4] = {c.x, c.y, c.z, c.w};
@@ -588,7 +622,9 @@ __global__ void __launch_bounds__(Cfg<D, MT, NP>::kThreads, 1)
       const int node = row_ok ? row / a.g : 0, h = pc.kvh * a.g + (row_ok ? row % a.g : 0);
       const unsigned long long anc = p.anc[(size_t)pc.b * a.T + node];
       const float qs = p.q_scale[((size_t)pc.b * a.T + node) * a.Hq + h];
-      const int npre = (L + 15) / 16;
+      const Reach reach(L, REACH ? p.window : INT_MAX, REACH ? p.sinks : 0);
+      const int npre = REACH ? reach.npre : (L + 15) / 16;
+      const int depth = REACH ? p.depth[(size_t)pc.b * a.T + node] : 0;
       float m_run = -INFINITY, l_run = 0.f;
       for (int j = pc.tile_begin; j < pc.tile_end; ++j, ++it, ++pos) {
         wait_all(&s_full[m], it & 1);
@@ -608,8 +644,9 @@ __global__ void __launch_bounds__(Cfg<D, MT, NP>::kThreads, 1)
         __syncwarp();
         if (lane == 0) tc::mbar_arrive(&s_free[m]);
         const int k0 = j * kTileKeys;
-        if (k0 + kTileKeys > L) {
-          const unsigned long long see = visible(L, npre, k0, anc);
+        if (REACH ? reach.partial(k0, kTileKeys, a.T - 1) : k0 + kTileKeys > L) {
+          const unsigned long long see = REACH ? (visible(reach.Lv, npre, k0, anc) & ~cached(npre, k0)) | reach.see64(k0, depth)
+                                               : visible(L, npre, k0, anc);
 #pragma unroll
           for (int hw = 0; hw < 2; ++hw) {
             const uint32_t bits = (uint32_t)(see >> (32 * hw));
@@ -697,6 +734,19 @@ __global__ void __launch_bounds__(Cfg<D, MT, NP>::kThreads, 1)
       if (!ok) break;
       tc::tc_fence_after();
       const int seg_row = m * 128 + r;
+      // NaN values at the window's edge, for the columns col .. col + 31 of a row that sees them
+      auto edge_nan = [&](uint32_t (&o)[32], int col) {
+        const int last = min(reach.edge + a.T - 1, min(reach.Lv, pc.tile_end * kTileKeys));
+        for (int c = max(max(reach.edge, 0), pc.tile_begin * kTileKeys); c < last; ++c) {
+          if (!(reach.see16(c & ~15, depth) >> (c & 15) & 1u)) continue;
+          const int id = a.block_tables[(size_t)pc.b * a.max_blocks + reach.page(c >> 4)];
+          if (id < 0 || id >= a.num_pages) continue;
+          const uint8_t* v = static_cast<const uint8_t*>(a.v_cache) + (((size_t)id * a.Hkv + pc.kvh) * 16 + (c & 15)) * D + col;
+#pragma unroll
+          for (int i = 0; i < 32; ++i)
+            if ((v[i] & 0x7f) == 0x7f) o[i] = 0x7fffffffu;
+        }
+      };
       const float inv = l_run == 0.f ? 0.f : 1.f / l_run;  // a NaN sum makes the row NaN
 #pragma unroll 1  // 32 columns at a time: with 64 the code is long enough to slow the other roles (fp16 12%)
       for (int col = 0; col < D; col += 32) {
@@ -705,6 +755,7 @@ __global__ void __launch_bounds__(Cfg<D, MT, NP>::kThreads, 1)
         tmem_ld_wait(o);
 #pragma unroll
         for (int c = 0; c < 32; ++c) o[c] = __float_as_uint(__uint_as_float(o[c]) * inv);
+        if (REACH && row_ok && *s_nan) edge_nan(o, col);
         if (row_ok && pc.slot < 0) {
           uint4* dst = reinterpret_cast<uint4*>(static_cast<T*>(a.out) + (((size_t)pc.b * a.T + node) * a.Hq + h) * D + col);
 #pragma unroll
@@ -723,6 +774,8 @@ __global__ void __launch_bounds__(Cfg<D, MT, NP>::kThreads, 1)
         }
       }
       if (row_ok && pc.slot >= 0) a.part_ml[(size_t)pc.slot * a.part_rows + seg_row] = make_float2(m_run, l_run);
+      if (REACH && row_ok && pc.slot < 0 && p.lse)
+        p.lse[((size_t)pc.b * a.T + node) * a.Hq + h] = row_lse(m_run, l_run);
       tc::tc_fence_before();
       __syncwarp();
       if (lane == 0) tc::mbar_arrive(o_free);
@@ -742,7 +795,7 @@ __global__ void __launch_bounds__(Cfg<D, MT, NP>::kThreads, 1)
 constexpr int kCombineWarps = 8;
 
 template <typename T, int D>
-__global__ void __launch_bounds__(kCombineWarps * 32) block8_combine_kernel(const AttnParams a) {
+__global__ void __launch_bounds__(kCombineWarps * 32) block8_combine_kernel(const AttnParams a, float* lse) {
   constexpr int U = 4, N = D / 64;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const Sched& s = a.sched;
@@ -800,7 +853,9 @@ __global__ void __launch_bounds__(kCombineWarps * 32) block8_combine_kernel(cons
   }
   const float inv = l == 0.f ? 0.f : 1.f / l;
   const int node = row / a.g, h = kvh * a.g + row % a.g;
-  T* out = static_cast<T*>(a.out) + (((size_t)b * a.T + node) * a.Hq + h) * D + 8 * warp;
+  const size_t at = ((size_t)b * a.T + node) * a.Hq + h;
+  if (lse && warp == 0) lse[at] = row_lse(M, l);
+  T* out = static_cast<T*>(a.out) + at * D + 8 * warp;
 #pragma unroll
   for (int n = 0; n < N; ++n) {
 #pragma unroll
@@ -812,10 +867,10 @@ __global__ void __launch_bounds__(kCombineWarps * 32) block8_combine_kernel(cons
 }
 
 template <typename T, int D>
-cudaError_t launch_combine_t(const AttnParams& a, cudaStream_t stream) {
+cudaError_t launch_combine_t(const AttnParams& a, float* lse, cudaStream_t stream) {
   const long long blocks = (long long)a.B * a.sched.Hkv * a.sched.nrg * ((a.part_rows + 31) / 32);
   if (blocks >= (1ll << 31)) return cudaErrorInvalidValue;
-  return launch_pdl(block8_combine_kernel<T, D>, dim3((unsigned)blocks), dim3(kCombineWarps * 32), 0, stream, a);
+  return launch_pdl(block8_combine_kernel<T, D>, dim3((unsigned)blocks), dim3(kCombineWarps * 32), 0, stream, a, lse);
 }
 
 PFN_cuTensorMapEncodeTiled_v12000 get_encode() {
@@ -859,8 +914,8 @@ bool map_queries(CUtensorMap* map, const void* base, long long nodes, int Hq, in
              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <typename T, int D, int MT, int NP>
-cudaError_t launch_t(const Block8Params& p, cudaStream_t stream) {
+template <typename T, int D, int MT, int NP, bool REACH>
+cudaError_t launch_r(const Block8Params& p, cudaStream_t stream) {
   using C = Cfg<D, MT, NP>;
   const AttnParams& a = p.a;
   static std::atomic<bool> opted[kMaxDevices];
@@ -868,7 +923,7 @@ cudaError_t launch_t(const Block8Params& p, cudaStream_t stream) {
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if (dev < 0 || dev >= kMaxDevices || !opted[dev].load(std::memory_order_acquire)) {
-    e = cudaFuncSetAttribute(attn_block8_tc_kernel<T, D, MT, NP>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    e = cudaFuncSetAttribute(attn_block8_tc_kernel<T, D, MT, NP, REACH>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              C::kSmem);
     if (e != cudaSuccess) return e;
     if (dev >= 0 && dev < kMaxDevices) opted[dev].store(true, std::memory_order_release);
@@ -879,8 +934,13 @@ cudaError_t launch_t(const Block8Params& p, cudaStream_t stream) {
       !map_pages(&kn, p.k_blocks, nrows, D, true) || !map_pages(&vn, p.v_blocks, nrows, D, false) ||
       !map_queries(&q, p.q8, (long long)NP * a.B * a.T, a.Hq, a.g, D))
     return cudaErrorInvalidValue;
-  return launch_pdl(attn_block8_tc_kernel<T, D, MT, NP>, dim3(a.sched.G), dim3(C::kThreads), (size_t)C::kSmem, stream,
-                    k, v, kn, vn, q, p);
+  return launch_pdl(attn_block8_tc_kernel<T, D, MT, NP, REACH>, dim3(a.sched.G), dim3(C::kThreads), (size_t)C::kSmem,
+                    stream, k, v, kn, vn, q, p);
+}
+
+template <typename T, int D, int MT, int NP>
+cudaError_t launch_t(const Block8Params& p, cudaStream_t stream) {
+  return p.window > 0 ? launch_r<T, D, MT, NP, true>(p, stream) : launch_r<T, D, MT, NP, false>(p, stream);
 }
 
 template <int D>
@@ -898,8 +958,8 @@ cudaError_t launch_attn_block8_tc(const Block8Params& p, int dtype, cudaStream_t
 
 cudaError_t launch_block8_combine(const Block8Params& p, int dtype, cudaStream_t stream) {
   if (p.a.D == 64)
-    return dtype == 1 ? launch_combine_t<__half, 64>(p.a, stream) : launch_combine_t<__nv_bfloat16, 64>(p.a, stream);
-  return dtype == 1 ? launch_combine_t<__half, 128>(p.a, stream) : launch_combine_t<__nv_bfloat16, 128>(p.a, stream);
+    return dtype == 1 ? launch_combine_t<__half, 64>(p.a, p.lse, stream) : launch_combine_t<__nv_bfloat16, 64>(p.a, p.lse, stream);
+  return dtype == 1 ? launch_combine_t<__half, 128>(p.a, p.lse, stream) : launch_combine_t<__nv_bfloat16, 128>(p.a, p.lse, stream);
 }
 
 }  // namespace mt

@@ -7,7 +7,8 @@
 //     part's smallest step is under 2^-17 of the row's maximum;
 //   - the new tokens' keys and values as blocks of codes with their scales, in
 //     the page layout [b][KV head][block][16][D];
-//   - each node's ancestor mask (the Medusa tree mask, vLLM issue 1171);
+//   - each node's ancestor mask (the Medusa tree mask, vLLM issue 1171), under a window
+//     (REACH) without the ancestors that it leaves out, and with the node's depth;
 //   - the schedule: tiles per sequence, their prefix, every CTA's pieces.
 // Latency matters more than bytes here: the rows are a few MB at most.
 #include "serve.cuh"
@@ -156,7 +157,7 @@ __device__ void list_pieces(const Block8Params& p, const Sched& sc) {
   }
 }
 
-template <typename T, int D>
+template <typename T, int D, bool REACH>
 __global__ void __launch_bounds__(kThreads) block8_prep_kernel(Block8Params p) {
   const AttnParams& a = p.a;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -165,7 +166,7 @@ __global__ void __launch_bounds__(kThreads) block8_prep_kernel(Block8Params p) {
   if (blockIdx.x == 0) {
     extern __shared__ int s_pfx[];  // [B + 1]
     __shared__ int s_warp[kWarps];
-    const int total = block8_prefix<kWarps>(a, s_pfx, s_warp, true);
+    const int total = block8_prefix<kWarps, REACH>(a, s_pfx, s_warp, true, p.window, p.sinks);
     for (int b = tid; b <= a.B; b += kThreads) p.tile_pfx[b] = s_pfx[b];
     Sched sc = a.sched;
     sc.tile_pfx = s_pfx;
@@ -202,6 +203,11 @@ __global__ void __launch_bounds__(kThreads) block8_prep_kernel(Block8Params p) {
     for (int i = lane; i < a.T; i += 32) {
       unsigned long long anc = 0;
       for (int n = i; n >= 0; n = s_par[warp][n]) anc |= 1ull << n;  // parents are earlier: at most T steps
+      if (REACH) {
+        int depth;
+        anc = seen_ancestors(anc, i, s_par[warp], max(a.seq_lens[b], 0), p.window, p.sinks, depth);
+        p.depth[(size_t)b * a.T + i] = depth;
+      }
       p.anc[(size_t)b * a.T + i] = anc;
     }
     __syncwarp();
@@ -228,8 +234,9 @@ cudaError_t launch_t(const Block8Params& p, cudaStream_t stream) {
   const long long wave = 4LL * sms;
   if (blocks > wave) blocks = wave;
   if (blocks < 2) blocks = 2;
-  return launch_pdl(block8_prep_kernel<T, D>, dim3((unsigned)blocks), dim3(kThreads), sizeof(int) * (size_t)(a.B + 1),
-                    stream, p);
+  const size_t smem = sizeof(int) * (size_t)(a.B + 1);
+  if (p.window > 0) return launch_pdl(block8_prep_kernel<T, D, true>, dim3((unsigned)blocks), dim3(kThreads), smem, stream, p);
+  return launch_pdl(block8_prep_kernel<T, D, false>, dim3((unsigned)blocks), dim3(kThreads), smem, stream, p);
 }
 
 template <typename T>

@@ -210,7 +210,70 @@ struct Block8Params {
   float* v_block_scales;
   unsigned long long* anc;  // [B][T]
   int* pieces;            // piece table (common.cuh)
+  // a window and sinks (the kernels' REACH instances; window INT_MAX: every slot)
+  int window, sinks;
+  int* depth;             // [B][T] written by the tensor-core path's preparation
+  float* lse;             // [B][T][Hq] log-sum-exp of each row's scores, or null
 };
+
+// What the window and the sinks leave of a sequence's L cached slots.  A node at depth d
+// has position L + d and sees slot s when s < sinks or s > L + d - window.  Pages that no
+// node sees are left out: the visible ones are numbered 0, 1, ... (the sinks' pages, then
+// from the first page of the root's window on), so a slot behind the gap has the column
+// slot - 16 * skip, and the columns of a row are [0, sv) and [rv(d), Lv).
+struct Reach {
+  int Lv;          // columns: L less the pages left out
+  int npre;        // pages
+  int sink_pages, skip;
+  int sv;          // columns of the sinks
+  int edge;        // the root's first column of the window: rv(d) = edge + d, as far as Lv
+  __device__ __forceinline__ Reach(int L, int window, int sinks) {
+    sv = min(sinks, L);
+    sink_pages = (sv + 15) / 16;
+    const int w0 = L - (window - 1);  // the root's first slot, perhaps below 0
+    // a window of the token alone has no page, not even the one that L lies in
+    skip = max(sink_pages, w0 < L ? max(w0, 0) / 16 : (L + 15) / 16) - sink_pages;
+    Lv = w0 < L ? L - 16 * skip : sv;
+    npre = (Lv + 15) / 16;
+    edge = max(w0 - 16 * skip, -kMaxTree);  // further back, no row misses a slot of the window
+  }
+  // table entry of visible page q
+  __device__ __forceinline__ int page(int q) const { return q < sink_pages ? q : q + skip; }
+  // whether some row of depth <= deepest misses some of the n columns from c0 on
+  __device__ __forceinline__ bool partial(int c0, int n, int deepest) const {
+    return c0 + n > Lv || (c0 + n > sv && c0 < edge + deepest);
+  }
+  // columns c0 .. c0 + 15 that a row of this depth sees
+  __device__ __forceinline__ unsigned see16(int c0, int depth) const {
+    const unsigned end = below(Lv - c0), sink = below(sv - c0), far = below(edge + depth - c0);
+    return end & (sink | ~far);
+  }
+  // the same of 64 columns
+  __device__ __forceinline__ unsigned long long see64(int c0, int depth) const {
+    const unsigned long long end = below64(Lv - c0), sink = below64(sv - c0), far = below64(edge + depth - c0);
+    return end & (sink | ~far);
+  }
+  static __device__ __forceinline__ unsigned below(int n) { return n <= 0 ? 0u : n >= 16 ? 0xffffu : (1u << n) - 1u; }
+  static __device__ __forceinline__ unsigned long long below64(int n) {
+    return n <= 0 ? 0ull : n >= 64 ? ~0ull : (1ull << n) - 1ull;
+  }
+};
+
+// ln of a row's sum of exp(score), from its maximum and sum in the attention kernels, whose
+// weights are 2^(score + 3 - max).
+__device__ __forceinline__ float row_lse(float m, float l) { return (m - 3.f + log2f(l)) * 0.6931471805599453f; }
+
+// A node's ancestors (itself included) that it sees, of those in `all`: the node k steps up
+// is in the window when k < window, and a sink when its position is below sinks.
+__device__ __forceinline__ unsigned long long seen_ancestors(unsigned long long all, int node, const int* parents, int L,
+                                                             int window, int sinks, int& depth) {
+  depth = __popcll(all) - 1;
+  if (window > depth) return all;
+  unsigned long long anc = 0;
+  for (int n = node, k = 0; n >= 0; n = parents[n], ++k)
+    if (k < window || L + depth - k < sinks) anc |= 1ull << n;
+  return anc;
+}
 
 // Largest magnitude of a warp's rows of 16-bit values, by their bits, so that an infinity
 // or a NaN is larger than any number.
@@ -269,8 +332,9 @@ __device__ __forceinline__ void drop_odd(Row8<T>& r) {
 // tile; none for seq_lens < 0) and their exclusive prefix in pfx[0 .. B], by a
 // block of W warps; returns the total.  A length past the block table has no
 // tiles and is recorded by the block that says so.
-template <int W>
-__device__ __forceinline__ int block8_prefix(const AttnParams& a, int* pfx, int* s_warp, bool report) {
+template <int W, bool REACH = false>
+__device__ __forceinline__ int block8_prefix(const AttnParams& a, int* pfx, int* s_warp, bool report, int window = 0,
+                                             int sinks = 0) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int nnew = (a.T + 15) / 16;
   int carry = 0;
@@ -282,7 +346,7 @@ __device__ __forceinline__ int block8_prefix(const AttnParams& a, int* pfx, int*
       if ((long long)L > (long long)a.max_blocks * 16) {
         if (report) set_status(a.status, kStPages);
       } else if (L >= 0) {
-        n = ((L + 15) / 16 + nnew + 3) / 4;
+        n = ((REACH ? Reach(L, window, sinks).npre : (L + 15) / 16) + nnew + 3) / 4;
       }
     }
     int incl = n;

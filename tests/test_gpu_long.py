@@ -1,0 +1,204 @@
+"""The operators for long sequences on the GPU against plain implementations in 64 bits (long_reference).
+
+Tolerances (u = half a step of the output's type relative to the value: bf16 2^-8, fp16 2^-11, fp32 2^-24):
+  window attention    as the attention without one (test_gpu_serve): u |out| + 2^-11 A + 2 E A, A = sum p |v|, E = 2^-9 the
+                      error of a score in the exponent (D products and sums in 32 bits, 2 D 2^-24 sum |q k| scale, and
+                      what falls below a query's parts);
+  log-sum-exp         E for the scores, and 2^-20 (1 + |lse|) for the sum's 32 bits, its logarithm and the units."""
+import numpy as np
+import pytest
+
+torch = pytest.importorskip("torch")
+
+import long_reference as lref
+import medusa_tree_speculative_attn_gb300 as mt
+import serve_reference as ref
+from test_gpu_serve import DT, P, _attn_case, _codes, _graph, _i32, _rand, _status, _table
+
+pytestmark = pytest.mark.gpu
+
+
+# ---- attention under a window ------------------------------------------------
+
+def _f8(x):
+    return torch.from_numpy(np.ascontiguousarray(x)).cuda().view(torch.float8_e4m3fn)
+
+
+def _hide(c, window, sinks):
+    """Table entries that no new token needs become nonsense."""
+    t = c["q"].shape[1]
+    for i, n in enumerate(c["lens"]):
+        if n > 0:
+            some = lref.sees(n, t, None if c["parents"] is None else c["parents"][i], window, sinks).any(0)
+            for p in range(c["table"].shape[1]):
+                if not some[p * P:min(n, (p + 1) * P)].any():
+                    c["table"][i, p] = 2 ** 30 if (i + p) % 2 else -1
+
+
+def _window_run(c, window, sinks, sm_scale=0.0, lse=True, ws=None):
+    q, kc, table = c["q"].cuda(), _f8(c["k"]), _i32(c["table"]).cuda()
+    out = torch.full_like(q, 5.0)
+    lse = torch.full(q.shape[:3], 5.0, device="cuda") if lse else None
+    ws = mt.alloc_block8_workspace(q, kc, table) if ws is None else ws
+    args = (q, kc, _f8(c["v"]), torch.from_numpy(c["ks"]).float().cuda(), torch.from_numpy(c["vs"]).float().cuda(), table, _i32(c["lens"]).cuda(),
+            None if c["parents"] is None else _i32(c["parents"]).cuda(), out)
+    kw = dict(k_new=c["kn"].cuda(), v_new=c["vn"].cuda(), workspace=ws, sm_scale=sm_scale, window=window, sinks=sinks, lse=lse)
+    mt.tree_attn_paged_block8(*args, **kw)
+    return out, lse, ws, args, kw
+
+
+def _window_check(c, out, lse, window, sinks, sm_scale=0.0):
+    d = c["q"].shape[-1]
+    want, mag, wlse = lref.window_attn64(c, window, sinks, sm_scale or d ** -0.5)
+    live = np.array([n >= 0 for n in c["lens"]])
+    got = out.cpu().double().numpy()
+    tol = ref.HALF_STEP[c["q"].dtype] * np.abs(want) + (2.0 ** -11 + 2.0 ** -8) * mag + 1e-7
+    assert np.array_equal(np.isnan(got[live]), np.isnan(want[live]))
+    bad = np.abs(got - want)[live] > tol[live]
+    assert not bad.any(), np.argwhere(bad)[:4]
+    assert (got[~live] == 5.0).all()
+    if lse is not None:
+        got = lse.cpu().double().numpy()
+        bad = np.abs(got - wlse)[live] > (2.0 ** -9 + 2.0 ** -20 * (1 + np.abs(wlse)))[live]
+        assert np.isfinite(got[live]).all() and not bad.any(), np.argwhere(bad)[:4]
+        assert (got[~live] == 5.0).all()
+
+
+WINDOWS = [  # T, Hq, Hkv, D, lengths
+    (1, 1, 1, 64, [0, 1, 40]), (1, 8, 2, 128, [17, -1, 300]), (2, 3, 3, 64, [5, 140]), (5, 12, 4, 128, [200, -1, 31]), (16, 2, 2, 128, [100, 3]),
+    (17, 2, 1, 64, [90, 16]), (64, 4, 1, 128, [250, 0]), (64, 8, 8, 64, [133]), (26, 8, 1, 128, [500]), (33, 3, 1, 128, [129, 64]), (40, 8, 2, 128, [70, 300]),
+]
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("tree", ["tree", "chain"])
+@pytest.mark.parametrize("window, sinks", [(1, 0), (3, 20), (16, 0), (33, 4), (64, 16), (100, 1), (1000, 5), (2 ** 31 - 1, 2 ** 31 - 1), (0, 7)])
+@pytest.mark.parametrize("case", range(len(WINDOWS)))
+def test_window_attention(dtype, tree, window, sinks, case):
+    t, hq, hkv, d, lens = WINDOWS[case]
+    c = _attn_case(np.random.default_rng(1000 + case), len(lens), t, hq, hkv, d, lens, dtype, tree)
+    _hide(c, window, sinks)
+    out, lse, ws, _, _ = _window_run(c, window, sinks)
+    assert mt.read_status(ws) == 0
+    _window_check(c, out, lse, window, sinks)
+
+
+@pytest.mark.parametrize("t, hq, hkv", [(1, 8, 2), (4, 8, 2), (24, 8, 2), (64, 4, 1), (4, 18, 2)])
+@pytest.mark.parametrize("window, sinks", [(0, 0), (900, 4)])
+def test_window_attention_long_sequences_in_pieces(t, hq, hkv, window, sinks):
+    lens = [3000, 40, 1100, 2047]
+    c = _attn_case(np.random.default_rng(20 + t), 4, t, hq, hkv, 128, lens, "bf16", "tree")
+    _hide(c, window, sinks)
+    out, lse, ws, _, _ = _window_run(c, window, sinks)
+    assert mt.read_status(ws) == 0
+    _window_check(c, out, lse, window, sinks)
+
+
+@pytest.mark.parametrize("t, hq, hkv", [(3, 8, 2), (24, 8, 2)])
+def test_window_zero_is_the_call_without_one(t, hq, hkv):
+    c = _attn_case(np.random.default_rng(31), 3, t, hq, hkv, 128, [700, 20, 64], "bf16")
+    out, _, _, args, kw = _window_run(c, 0, 9)
+    plain = torch.full_like(out, 5.0)
+    mt.tree_attn_paged_block8(*args[:8], plain, **{k: kw[k] for k in ("k_new", "v_new", "workspace")})
+    assert torch.equal(out, plain)
+
+
+def test_window_attention_scale_many_sequences_and_no_lse():
+    rng = np.random.default_rng(32)
+    lens = [int(n) for n in rng.integers(-1, 150, 300)]
+    for t, dtype in ((1, "f16"), (20, "bf16")):
+        c = _attn_case(rng, 300, t, 2, 1, 64, lens, dtype, "chain")
+        _hide(c, 37, 3)
+        out, _, ws, _, _ = _window_run(c, 37, 3, sm_scale=0.05, lse=False)
+        assert mt.read_status(ws) == 0
+        _window_check(c, out, None, 37, 3, sm_scale=0.05)
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("t, hq, hkv", [(6, 4, 2), (8, 8, 4), (6, 18, 2), (40, 8, 2), (64, 16, 4)])  # both kernels
+@pytest.mark.parametrize("lens", [[90], [300, 2000]])  # whole segments, and ones in pieces
+def test_window_attention_nan_in_and_out_of_sight(dtype, t, hq, hkv, lens):
+    # NaN codes in the keys and values of slots that nobody sees, and values' at the window's edge, which the deeper
+    # nodes do not see; the sinks' page has both kinds too
+    window, sinks = 40, 5
+    c = _attn_case(np.random.default_rng(33), len(lens), t, hq, hkv, 128, lens, dtype, "chain")
+    for i, n in enumerate(lens):
+        far = n - window + 1
+        for s in (sinks, 15, far - 1, far - 2):
+            c["k"][c["table"][i, s // P], :, s % P, 3] = c["v"][c["table"][i, s // P], :, s % P, 70] = 0x7F
+        for s, col in ((far, 9), (far + 2, 127), (far + 3, 0)):  # seen by nodes 0, 0 .. 2, 0 .. 3
+            c["v"][c["table"][i, s // P], 0, s % P, col] = 0xFF
+    _hide(c, window, sinks)
+    out, lse, ws, _, _ = _window_run(c, window, sinks)
+    assert mt.read_status(ws) == 0
+    _window_check(c, out, lse, window, sinks)
+    assert out.isnan().any() and not out[:, 4:].isnan().any()
+
+
+def test_window_attention_reports_bad_pages_in_sight_alone():
+    c = _attn_case(np.random.default_rng(34), 2, 4, 4, 2, 64, [150, 20], "f16")
+    c["table"][0, 3] = 99  # out of sight
+    assert mt.read_status(_window_run(c, 30, 4)[2]) == 0
+    c["table"][0, 8] = 99
+    assert mt.read_status(_window_run(c, 30, 4)[2]) == -4
+    c["table"][0, 8] = 0
+    c["lens"] = [161, 20]  # past the table, whatever the window
+    assert mt.read_status(_window_run(c, 30, 4)[2]) == -4
+    c["lens"] = [150, 20]
+    c["parents"][1, 2] = 3
+    assert mt.read_status(_window_run(c, 30, 4)[2]) == -3
+
+
+@pytest.mark.parametrize("t", [1, 20])
+def test_window_attention_in_a_graph_with_other_lengths(t):
+    c = _attn_case(np.random.default_rng(35), 4, t, 8, 2, 128, [700, 20, 64, 333], "bf16")
+    out, lse, ws, args, kw = _window_run(c, 100, 4)
+    _window_check(c, out, lse, 100, 4)
+    g = _graph(lambda: mt.tree_attn_paged_block8(*args, **kw))
+    args[6].copy_(_i32([101, 20, -1, 5]))
+    out.fill_(5.0)
+    lse.fill_(5.0)
+    g.replay()
+    c["lens"] = [101, 20, -1, 5]
+    _window_check(c, out, lse, 100, 4)
+    assert mt.read_status(ws) == 0
+
+
+def test_window_attention_shares_a_workspace_with_any_call():
+    rng = np.random.default_rng(36)
+    cases = [_attn_case(rng, 2, t, 8, 2, 128, [1500, 200], dt) for t, dt in ((1, "bf16"), (12, "f16"), (40, "bf16"))]
+    sizes = [(0, 0), (64, 4), (700, 0)]
+    own = [[_window_run(c, w, s) for w, s in sizes] for c in cases]
+    ws = torch.zeros(max(x[2].numel() for o in own for x in o), dtype=torch.uint8, device="cuda")
+    for i, j in ((0, 1), (1, 1), (2, 2), (0, 0), (2, 1), (1, 2), (0, 2), (2, 0), (1, 0), (0, 1)):
+        out, lse, _, _, _ = _window_run(cases[i], *sizes[j], ws=ws)
+        assert torch.equal(out, own[i][j][0]) and torch.equal(lse, own[i][j][1])
+    assert mt.read_status(ws) == 0
+
+
+@pytest.mark.parametrize("t", [1, 20])
+def test_window_attention_of_a_very_long_sequence(t):
+    # positions near 2^31 behind a table of as many entries; only the pages in sight exist
+    n, window, sinks, d = 2 ** 31 - 4096 - 200, 50, 20, 64
+    rng = np.random.default_rng(37)
+    blocks = (n + 63) // P
+    table = torch.full((1, blocks), -1, dtype=torch.int32, device="cuda")
+    first = (n - window + 1) // P
+    seen = [0, 1] + list(range(first, -(-n // P)))
+    table[0, torch.tensor(seen, device="cuda")] = torch.arange(len(seen), dtype=torch.int32, device="cuda")
+    short = _attn_case(rng, 1, t, 8, 2, d, [len(seen) * P], "bf16", "chain")
+    short["table"] = np.arange(len(seen), dtype=np.int32)[None]
+    short["k"], short["v"], short["ks"], short["vs"] = (short[x][:len(seen)] for x in ("k", "v", "ks", "vs"))
+    short["k"] &= 0x77  # (no NaN)
+    short["v"] &= 0x77
+    # the same under a short numbering: 32 slots of sinks' pages, then the window
+    short["lens"] = [n - 16 * (first - 2)]
+    want, _, _, _, _ = _window_run(short, window, sinks)
+    _window_check(short, want, None, window, sinks)
+    q = short["q"].cuda()
+    out, ws = torch.empty_like(q), mt.alloc_block8_workspace(q, _f8(short["k"]), table)
+    mt.tree_attn_paged_block8(q, _f8(short["k"]), _f8(short["v"]), torch.from_numpy(short["ks"]).float().cuda(), torch.from_numpy(short["vs"]).float().cuda(),
+                              table, _i32([n]).cuda(), None, out, k_new=short["kn"].cuda(), v_new=short["vn"].cuda(), workspace=ws, window=window, sinks=sinks)
+    assert mt.read_status(ws) == 0
+    tol = 2.0 ** -7 * want.abs().float() + 2.0 ** -7  # another split of the sum
+    assert bool(((out.float() - want.float()).abs() <= tol).all())

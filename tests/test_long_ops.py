@@ -1,0 +1,56 @@
+"""Host-side checks of the operators for long sequences and shaped answers, without a GPU: the C ABI refuses bad
+descriptors and pointers before it touches the device, and the binding refuses arguments that do not fit."""
+import ctypes
+
+import pytest
+
+torch = pytest.importorskip("torch")
+
+import medusa_tree_speculative_attn_gb300 as mt
+from test_serve_ops import INVALID, ODD, OK, PTR, UNSUPPORTED, _attn_desc, lib  # noqa: F401 (lib: the fixture)
+
+
+# ---- attention under a window ----
+
+@pytest.mark.parametrize("window, sinks, desc, want", [
+    (-1, 0, {}, INVALID), (8, -1, {}, INVALID), (8, 4, dict(tree_size=65), UNSUPPORTED), (8, 4, dict(dtype=0), UNSUPPORTED), (0, 0, dict(batch=0), INVALID),
+])
+def test_window_sizes(lib, window, sinks, desc, want):  # noqa: F811
+    assert lib.mt_tree_attn_paged_block8_window(_attn_desc(**desc), window, sinks, *[PTR] * 13, 1 << 40, None) == want
+
+
+def test_window_pointers(lib):  # noqa: F811
+    at = [(i + 1) << 32 for i in range(13)]  # q, k_new, v_new, ... far apart; tree_parents 9, out 10, lse 11, workspace 12
+    for i in (0, 1, 2, 3, 4, 5, 6, 7, 8, 10, 12):
+        args = list(at)
+        args[i] = None
+        assert lib.mt_tree_attn_paged_block8_window(_attn_desc(), 8, 4, *args, 1 << 40, None) == INVALID, i
+    for i in (0, 1, 2, 3, 4, 10, 11, 12):
+        args = list(at)
+        args[i] += 2
+        assert lib.mt_tree_attn_paged_block8_window(_attn_desc(), 8, 4, *args, 1 << 40, None) == INVALID, i
+    size = 4 * 2 * 4 * 8  # lse, just before and just behind what it must not overlap
+    for i, n in ((0, 2 * 2 * 4 * 8 * 128), (1, 2 * 2 * 4 * 2 * 128), (2, 2 * 2 * 4 * 2 * 128), (10, 2 * 2 * 4 * 8 * 128)):
+        for shift in (0, 4 - size, n - 4):
+            args = list(at)
+            args[11] = args[i] + shift
+            assert lib.mt_tree_attn_paged_block8_window(_attn_desc(), 8, 4, *args, 1 << 40, None) == INVALID, (i, shift)
+    assert lib.mt_tree_attn_paged_block8_window(None, 8, 4, *at, 1 << 40, None) == INVALID
+
+
+@pytest.mark.gpu
+def test_the_binding_refuses_windows_that_do_not_fit():
+    cu = lambda *s, dtype=torch.bfloat16: torch.zeros(*s, dtype=dtype, device="cuda")  # noqa: E731
+    q, n, cache, table = cu(3, 4, 8, 128), cu(3, 4, 2, 128), cu(6, 2, 16, 128, dtype=torch.float8_e4m3fn), cu(3, 2, dtype=torch.int32)
+    scales, ws, lse = cu(6, 2, dtype=torch.float32) + 1, mt.alloc_block8_workspace(q, cache, table), cu(3, 4, 8, dtype=torch.float32)
+    call = lambda **kw: mt.tree_attn_paged_block8(**{**dict(q=q, k_cache=cache, v_cache=cache, k_scales=scales, v_scales=scales, block_tables=table,  # noqa: E731
+                                                            seq_lens=cu(3, dtype=torch.int32), tree_parents=None, out=torch.empty_like(q), k_new=n, v_new=n, workspace=ws,
+                                                            window=5, sinks=2, lse=lse), **kw})
+    call()
+    for kw in (dict(window=-1), dict(sinks=-1), dict(window=2 ** 31), dict(sinks=2 ** 32 + 1), dict(lse=lse[:2]), dict(lse=lse.half()), dict(lse=lse.cpu()),
+               dict(lse=lse.transpose(0, 1)), dict(window=0, sinks=-1)):
+        with pytest.raises((ValueError, TypeError)):
+            call(**kw)
+    with pytest.raises(mt.MedusaTreeError):
+        call(workspace=ws[:512])
+    torch.cuda.synchronize()
