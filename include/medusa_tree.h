@@ -489,6 +489,34 @@ int mt_tree_attn_paged_block8_window(const mt_attn_desc* desc, int window, int s
                                      const int32_t* tree_parents, void* out, float* lse,
                                      void* workspace, size_t ws_bytes, cudaStream_t stream);
 
+/* ---- Attention weights of cached slots -------------------------------------------
+ * What a cache of bounded size can go by: how much attention each slot has received.
+ * For every cached slot s < seq_lens[b] of sequence b and KV head h, with the query rows
+ * r of the call under that head and lse_r as mt_tree_attn_paged_block8_window returned it
+ * (window 0: a slot's weight is its share of the softmax over the whole cache):
+ *   out[slot] = decay * (s < prev_lens[b] ? weights[slot] : 0)
+ *               + sum_r exp(q_r . k_s * sm_scale - lse_r)
+ * in fp32; a slot's sum has one order, so results are the same in every run.
+ * Rows: all tree_size nodes (a decoding step, a chunk of a prompt), or with accept_path
+ * and accept_len the nodes accept_path[b][0 .. accept_len[b]], as the acceptance calls
+ * give them; accept_path int32 [B][max_depth + 1].
+ *   q [B][T][Hq][D] as it attended; lse fp32 [B][T][Hq]
+ *   k_cache, k_scales as for the attention, which are only read
+ *   weights, out fp32 [num_pages][Hkv][16], in place or apart; slots that are not the
+ *   sequences' cached ones are left as they were in `out`
+ *   prev_lens int32 [B] or null (seq_lens): slots from prev_lens[b] on are new and start
+ *   from 0.  A page must not be listed by two sequences of the call.
+ * desc as for mt_tree_attn_paged_block8 (num_splits, kernel, k_scale, v_scale unused);
+ * decay >= 0, finite.  A sequence with seq_lens[b] < 0 is no sequence.  Device status
+ * (status_ws, at least 256 bytes): MT_ERR_PAGES for a length past the table, an accepted
+ * length or node out of range (nothing of that sequence is written), a page id out of
+ * range (nothing of that page). */
+int mt_kv_attn_weights(const mt_attn_desc* desc, int max_depth, float decay, const void* q, const float* lse,
+                       const void* k_cache, const float* k_scales, const int32_t* block_tables,
+                       const int32_t* seq_lens, const int32_t* prev_lens, const int32_t* accept_path,
+                       const int32_t* accept_len, const float* weights, float* out, void* status_ws,
+                       cudaStream_t stream);
+
 /* ---- Sampling --------------------------------------------------------------------
  * A drawn token beside the argmax that greedy and typical acceptance return (the
  * bonus token of an accepted path's last row, or a decoding step's).  For each i,

@@ -17,6 +17,7 @@ Calls (same names as the C ABI without the ``mt_`` prefix):
   kv_append_accepted an accepted path's keys and values into the paged cache
   tree_attn_paged_block8  tree attention over an 8-bit cache with a scale per page and head,
                      of the whole cache or under a sliding window with sinks
+  kv_attn_weights    the attention weight that each cached slot has received
   sample_tokens      temperature, top-k, top-p and min-p from given uniform numbers
 """
 from __future__ import annotations
@@ -115,6 +116,7 @@ def _load():
         lib.mt_tree_attn_block8_workspace_size.restype = Z
         lib.mt_tree_attn_paged_block8.argtypes = [P] + [P] * 12 + [Z, P]
         lib.mt_tree_attn_paged_block8_window.argtypes = [P, I, I] + [P] * 13 + [Z, P]
+        lib.mt_kv_attn_weights.argtypes = [P, I, ctypes.c_float] + [P] * 13
         lib.mt_sample_tokens.argtypes = [I, I, I, P, I, L] + [P] * 7 + [P]
         lib.mt_read_status.argtypes = [P, P, ctypes.POINTER(I)]
         lib.mt_profile_enable.argtypes = [I]
@@ -743,6 +745,43 @@ def tree_attn_paged_block8(q, k_cache, v_cache, k_scales, v_scales, block_tables
                 _int32(window, "window"), _int32(sinks, "sinks"), *args,
                 None if lse is None else _arg(lse, "lse", f32, (b, t, hq), dev), *ws)
     return out
+
+
+def kv_attn_weights(q, k_cache, k_scales, block_tables, seq_lens, lse, weights, *, status_ws: torch.Tensor,
+                    out=None, prev_lens=None, accept_path=None, accept_len=None, decay: float = 1.0,
+                    sm_scale: float = 0.0, stream=None):
+    """Adds to weights [pages,Hkv,16] (float32; or writes the sums to `out`, of that
+    shape) what the rows of q [B,T,Hq,D] give to each cached slot: exp(score - lse),
+    with lse [B,T,Hq] from tree_attn_paged_block8 over the whole cache.  The rows are
+    all T nodes', or the accepted path's.  What a slot had before counts `decay`
+    times; slots from prev_lens[b] on (None: none) are new and had nothing."""
+    dev = _cuda_device(q, "q")
+    dt = q.dtype
+    _act(q, "q", (torch.float16, torch.bfloat16))
+    if q.dim() != 4 or not isinstance(k_cache, torch.Tensor) or k_cache.dim() != 4:
+        raise ValueError("q and k_cache must have 4 dims")
+    b, t, hq, d = q.shape
+    pages, hkv, page = k_cache.shape[:3]
+    if not isinstance(block_tables, torch.Tensor) or block_tables.dim() != 2:
+        raise ValueError("block_tables must have 2 dims")
+    if (accept_path is None) != (accept_len is None):
+        raise ValueError("accept_path and accept_len go together")
+    depth, path, length = 0, None, None
+    f32, i32 = torch.float32, torch.int32
+    if accept_path is not None:
+        if not isinstance(accept_path, torch.Tensor) or accept_path.dim() != 2:
+            raise ValueError("accept_path must have 2 dims")
+        depth = accept_path.shape[1] - 1
+        path, length = _arg(accept_path, "accept_path", i32, (b, depth + 1), dev), _arg(accept_len, "accept_len", i32, (b,), dev)
+    slots = (pages, hkv, page)
+    wp = _arg(weights, "weights", f32, slots, dev)
+    _invoke(_load().mt_kv_attn_weights, "mt_kv_attn_weights", dev, stream, _block8_desc(q, k_cache, block_tables, sm_scale),
+            depth, decay, _arg(q, "q", dt, (b, t, hq, d), dev), _arg(lse, "lse", f32, (b, t, hq), dev),
+            _arg(k_cache, "k_cache", _E4M3, (pages, hkv, page, d), dev), _arg(k_scales, "k_scales", f32, (pages, hkv), dev),
+            _arg(block_tables, "block_tables", i32, (b, block_tables.shape[1]), dev), _arg(seq_lens, "seq_lens", i32, (b,), dev),
+            None if prev_lens is None else _arg(prev_lens, "prev_lens", i32, (b,), dev), path, length, wp,
+            wp if out is None else _arg(out, "out", f32, slots, dev), _status_arg(status_ws, "status_ws", dev))
+    return weights if out is None else out
 
 
 def sample_tokens(logits, uniforms, tokens, *, temperature=None, top_k=None, top_p=None, min_p=None,

@@ -317,6 +317,41 @@ int mt_tree_attn_paged_block8_window(const mt_attn_desc* d, int window, int sink
                      block_tables, seq_lens, tree_parents, out, lse, workspace, ws_bytes, stream);
 }
 
+int mt_kv_attn_weights(const mt_attn_desc* d, int max_depth, float decay, const void* q, const float* lse,
+                       const void* k_cache, const float* k_scales, const int32_t* block_tables,
+                       const int32_t* seq_lens, const int32_t* prev_lens, const int32_t* accept_path,
+                       const int32_t* accept_len, const float* weights, float* out, void* status_ws,
+                       cudaStream_t stream) {
+  const mt_call_range range("mt_kv_attn_weights");
+  const int st = check_block8(d);
+  if (st != MT_OK) return st;
+  if (!q || !lse || !k_cache || !k_scales || !block_tables || !seq_lens || !weights || !out || !status_ws)
+    return MT_ERR_INVALID_ARG;
+  if (!aligned16(q) || !aligned16(k_cache) || !aligned16(weights) || !aligned16(out) || !aligned16(status_ws))
+    return MT_ERR_INVALID_ARG;
+  if ((accept_path == nullptr) != (accept_len == nullptr)) return MT_ERR_INVALID_ARG;
+  if (accept_path && (max_depth < 0 || max_depth >= kMaxTree)) return MT_ERR_INVALID_ARG;
+  if (!(decay >= 0.f) || std::isinf(decay)) return MT_ERR_INVALID_ARG;
+  const size_t bytes = (size_t)d->num_pages * d->num_kv_heads * 16 * sizeof(float);
+  if (out != weights && overlap(out, bytes, weights, bytes)) return MT_ERR_INVALID_ARG;
+  WeightsParams p{};
+  p.B = d->batch; p.T = d->tree_size; p.Hq = d->num_q_heads; p.Hkv = d->num_kv_heads; p.D = d->head_dim;
+  p.max_blocks = d->max_blocks_per_seq; p.num_pages = d->num_pages;
+  p.g = d->num_q_heads / d->num_kv_heads;
+  const long long rows = (long long)(accept_path ? max_depth + 1 : d->tree_size) * p.g;
+  if (rows > (1 << 20)) return MT_ERR_UNSUPPORTED;
+  p.rows = (int)rows;
+  p.q = q; p.lse = lse; p.k_cache = k_cache; p.k_scales = k_scales;
+  p.block_tables = block_tables; p.seq_lens = seq_lens; p.prev_lens = prev_lens;
+  p.accept_path = accept_path; p.accept_len = accept_len; p.max_depth = max_depth;
+  const float scale = d->sm_scale > 0.f ? d->sm_scale : (float)(1.0 / std::sqrt((double)d->head_dim));
+  p.scale_log2 = scale * 1.4426950408889634f;
+  p.decay = decay;
+  p.weights = weights; p.out = out;
+  p.status = static_cast<int*>(status_ws);
+  return cuda_status(launch_kv_weights(p, d->dtype, stream));
+}
+
 int mt_sample_tokens(int num_rows, int vocab, mt_dtype logits_dtype, const void* logits, int num_logit_rows,
                      long long row_stride, const int32_t* row_index, const float* uniforms, const float* temperature,
                      const int32_t* top_k, const float* top_p, const float* min_p, int32_t* tokens,

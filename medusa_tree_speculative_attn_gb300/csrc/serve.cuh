@@ -384,6 +384,29 @@ cudaError_t launch_block8_combine(const Block8Params& p, int dtype, cudaStream_t
 cudaError_t launch_attn_block8_tc(const Block8Params& p, int dtype, cudaStream_t stream);
 
 // ---------------------------------------------------------------------------
+// Weights of cached slots.
+// ---------------------------------------------------------------------------
+struct WeightsParams {
+  int B, T, Hq, Hkv, D, max_blocks, num_pages, g;
+  int rows;             // most query rows of a KV head: nodes of the call (of a path) * g
+  const void* q;        // [B][T][Hq][D] act
+  const float* lse;     // [B][T][Hq]
+  const void* k_cache;  // codes
+  const float* k_scales;
+  const int* block_tables;
+  const int* seq_lens;
+  const int* prev_lens;    // [B] or null: slots from there on start from 0
+  const int* accept_path;  // [B][max_depth + 1] or null: every node
+  const int* accept_len;
+  int max_depth;
+  float scale_log2, decay;
+  const float* weights;  // [num_pages][Hkv][16]
+  float* out;
+  int* status;
+};
+cudaError_t launch_kv_weights(const WeightsParams& p, int dtype, cudaStream_t stream);
+
+// ---------------------------------------------------------------------------
 // Sampling.
 // ---------------------------------------------------------------------------
 // Largest vocab: that many weights of 2^44 (the maximum's) stay below 2^63, and an

@@ -74,3 +74,33 @@ def window_attn64(c, window, sinks, scale):
                 if odd.any():
                     out[i, :, j][(m.astype(float) @ odd) > 0] = np.nan
     return out, mag, lse
+
+
+def weights64(c, weights, lse, lens, prev, nodes_of, decay, scale):
+    """(weights after the call, their tolerance), [pages][Hkv][16] in 64 bits.  nodes_of(b): the nodes whose rows count.
+    Tolerance, by term: a score in 32 bits is off by 2 D 2^-24 sum |q k| scale (D products and sums, which tensor cores
+    may truncate), score - lse by 2^-22 (|score| + |lse|) more (the units, the constants, one subtraction), the
+    exponential by 2^-21 of itself, each sum and product of weights by 2^-20 of what it adds up."""
+    q = c["q"].double().numpy()
+    b, t, hq, d = q.shape
+    hkv = c["k"].shape[1]
+    g = hq // hkv
+    out, tol = weights.astype(np.float64).copy(), np.zeros(weights.shape)
+    for i in range(b):
+        n = int(lens[i])
+        if n < 1:
+            continue
+        slots = np.arange(n)
+        page, at = c["table"][i][slots // P], slots % P
+        for h in range(hkv):
+            k = ref.decode(c["k"][page, h, at]) * c["ks"][page, h][:, None].astype(np.float64)
+            had = np.where(slots < prev[i], out[page, h, at], 0.0) * decay
+            got, off = had.copy(), 2.0 ** -20 * np.abs(had)
+            for a in nodes_of(i):
+                for j in range(h * g, (h + 1) * g):
+                    z = k @ q[i, a, j] * scale
+                    p = np.exp(z - lse[i, a, j])
+                    got += p
+                    off += p * (2 * d * 2.0 ** -24 * scale * (np.abs(k) @ np.abs(q[i, a, j])) + 2.0 ** -22 * (np.abs(z) + abs(lse[i, a, j])) + 2.0 ** -19)
+            out[page, h, at], tol[page, h, at] = got, off
+    return out, tol

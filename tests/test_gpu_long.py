@@ -202,3 +202,151 @@ def test_window_attention_of_a_very_long_sequence(t):
     assert mt.read_status(ws) == 0
     tol = 2.0 ** -7 * want.abs().float() + 2.0 ** -7  # another split of the sum
     assert bool(((out.float() - want.float()).abs() <= tol).all())
+
+
+# ---- weights of cached slots ---------------------------------------------------
+
+def _lse_of(c, nodes=None):
+    """The attention's log-sum-exp over the whole cache, from the call that returns it."""
+    return _window_run(c, 0, 0)[1]
+
+
+def _weights_check(c, prev, path, decay, in_place, seed=0, lse=None, sm_scale=0.0):
+    """One call against the plain implementation; returns what it wrote."""
+    rng = np.random.default_rng(seed)
+    b, t, hq, d = c["q"].shape
+    pages, hkv = c["k"].shape[:2]
+    lse = _lse_of(c) if lse is None else lse
+    old = rng.random((pages, hkv, P)).astype(np.float32) * 3
+    w, ws = torch.from_numpy(old).cuda(), _status()
+    out = w if in_place else torch.full_like(w, -7.0)
+    kw = dict(prev_lens=None if prev is None else _i32(prev).cuda(), decay=decay, status_ws=ws, sm_scale=sm_scale)
+    if path is not None:
+        kw |= dict(accept_path=_i32(path[0]).cuda(), accept_len=_i32(path[1]).cuda())
+    got = mt.kv_attn_weights(c["q"].cuda(), _f8(c["k"]), torch.from_numpy(c["ks"]).float().cuda(), _i32(c["table"]).cuda(), _i32(c["lens"]).cuda(), lse, w,
+                             out=None if in_place else out, **kw)
+    assert got is out and mt.read_status(ws) == 0
+    nodes = (lambda i: range(t)) if path is None else (lambda i: path[0][i][:path[1][i] + 1])
+    want, tol = lref.weights64(c, old, lse.cpu().double().numpy(), c["lens"], c["lens"] if prev is None else prev, nodes, decay, sm_scale or d ** -0.5)
+    got = got.cpu().double().numpy()
+    live = np.zeros(old.shape, bool)
+    for i, n in enumerate(c["lens"]):
+        for s in range(max(n, 0)):
+            live[c["table"][i][s // P], :, s % P] = True
+    bad = np.abs(got - want) > tol
+    assert not bad[live].any(), np.argwhere(bad & live)[:4]
+    assert (got[~live] == (old.astype(np.float64)[~live] if in_place else -7.0)).all()
+    return got
+
+
+WEIGHTS = [  # T, Hq, Hkv, D, lengths
+    (1, 1, 1, 64, [0, 1, 40]), (1, 8, 2, 128, [17, -1, 300]), (2, 3, 3, 64, [5, 140]), (5, 12, 4, 128, [200, -1, 31]), (1, 7, 1, 128, [15, 16, 33]),
+    (17, 2, 1, 64, [90, 16]), (64, 4, 1, 128, [250, 0]), (64, 9, 1, 128, [70, 40]), (64, 8, 8, 64, [133]), (33, 3, 1, 128, [129, 64]),
+]
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("which", ["all", "path", "decayed"])
+@pytest.mark.parametrize("case", range(len(WEIGHTS)))
+def test_slot_weights(dtype, which, case):
+    t, hq, hkv, d, lens = WEIGHTS[case]
+    rng = np.random.default_rng(2000 + case)
+    c = _attn_case(rng, len(lens), t, hq, hkv, d, lens, dtype, "tree")
+    path = None
+    if which == "path":
+        depth = min(t, 6)
+        rows = np.stack([np.concatenate([np.sort(rng.permutation(t)[:depth]), [-1]]) for _ in lens])  # one place more than the longest
+        path = rows, rng.integers(0, depth, len(lens))
+    prev = [max(n - 20, 0) for n in lens] if which == "decayed" else None
+    _weights_check(c, prev, path, 0.9 if which == "decayed" else 1.0, in_place=case % 2 == 0, seed=case)
+
+
+def test_slot_weights_long_batch_scale_and_sum():
+    c = _attn_case(np.random.default_rng(41), 3, 1, 8, 2, 128, [3000, 40, 2047], "bf16", "chain")
+    _weights_check(c, [0, 40, 5000], None, 0.5, True)
+    lse = torch.randn(3, 1, 8, device="cuda")
+    _weights_check(c, None, None, 1.0, False, lse=lse, sm_scale=0.03)
+    # the weights of a step's rows, and of their own new token, are shares of 1
+    got = _weights_check(c, [0, 0, 0], None, 1.0, True)
+    for i, n in enumerate(c["lens"]):
+        pages = c["table"][i][np.arange(n) // P]
+        total = got[pages, :, np.arange(n) % P].sum(0)  # per KV head: 4 rows
+        assert (total < 4.001).all() and (total > 3.0 * n / (n + 20)).all()
+
+
+def test_slot_weights_of_many_rows_a_head():
+    c = _attn_case(np.random.default_rng(42), 1, 64, 40, 2, 64, [100], "f16", "chain")  # 1280 rows: five passes
+    _weights_check(c, [33], None, 0.7, True)
+    _weights_check(c, [33], None, 0.7, False)
+
+
+def test_slot_weights_status_and_what_errors_leave():
+    c = _attn_case(np.random.default_rng(43), 2, 4, 4, 2, 64, [50, 20], "f16")
+    lse = torch.zeros(2, 4, 4, device="cuda")
+    run = lambda **kw: mt.kv_attn_weights(c["q"].cuda(), _f8(c["k"]), torch.from_numpy(c["ks"]).float().cuda(), _i32(c["table"]).cuda(), _i32(c["lens"]).cuda(), lse,  # noqa: E731
+                                          **{**dict(weights=w, status_ws=ws), **kw})
+    for bad in ("page", "length", "path", "node"):
+        w, ws, kw = torch.ones(c["k"].shape[0], 2, P, device="cuda"), _status(), {}
+        table, lens, touched = c["table"].copy(), list(c["lens"]), set(c["table"][1][:2])
+        if bad == "page":
+            touched |= {c["table"][0][p] for p in (0, 1, 3)}
+            c["table"][0, 2] = c["k"].shape[0]
+        elif bad == "length":
+            c["lens"][0] = 65
+        else:
+            kw = dict(accept_path=_i32([[0, 1], [0, 1]]).cuda(), accept_len=_i32([1, 1]).cuda())
+            kw["accept_path" if bad == "node" else "accept_len"][0] = 4 if bad == "node" else 2
+        run(**kw)
+        assert mt.read_status(ws) == -4, bad
+        left = torch.tensor([p not in touched for p in range(len(w))])
+        assert bool((w.cpu()[left] == 1).all()) and not bool((w.cpu()[~left][:, :, 0] == 1).any()), bad
+        c["table"], c["lens"] = table, lens
+
+
+def test_slot_weights_infinities_and_nan():
+    c = _attn_case(np.random.default_rng(44), 2, 3, 4, 2, 64, [50, 20], "bf16", "chain")
+    c["k"][c["table"][0][1], 1, 4, 9] = 0x7F  # a cached key of one head
+    c["q"][1, 2, 0, 5] = float("inf")
+    lse = torch.zeros(2, 3, 4, device="cuda")
+    lse[0, 1, 0] = float("inf")  # a row that gives nothing
+    w, ws = torch.zeros(c["k"].shape[0], 2, P, device="cuda"), _status()
+    mt.kv_attn_weights(c["q"].cuda(), _f8(c["k"]), torch.from_numpy(c["ks"]).float().cuda(), _i32(c["table"]).cuda(), _i32(c["lens"]).cuda(), lse, w, status_ws=ws)
+    want = np.zeros(w.shape, bool)
+    want[c["table"][0][1], 1, 4] = True
+    want[c["table"][1][0], 0, :] = want[c["table"][1][1], 0, :4] = True
+    assert np.array_equal(w.isnan().cpu().numpy(), want)
+
+
+def test_slot_weights_in_a_graph_on_another_stream_and_the_same_twice():
+    c = _attn_case(np.random.default_rng(45), 4, 2, 8, 2, 128, [700, 20, 64, 333], "bf16", "chain")
+    lse = _lse_of(c)
+    w, ws, out = torch.rand(c["k"].shape[0], 2, P, device="cuda"), _status(), None
+    out = torch.zeros_like(w)
+    args = (c["q"].cuda(), _f8(c["k"]), torch.from_numpy(c["ks"]).float().cuda(), _i32(c["table"]).cuda(), _i32(c["lens"]).cuda(), lse, w)
+    mt.kv_attn_weights(*args, out=out, status_ws=ws)
+    want = out.clone()
+    g = _graph(lambda: mt.kv_attn_weights(*args, out=out, status_ws=ws))
+    out.zero_()
+    g.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(out, want)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    other = torch.zeros_like(w)
+    s.wait_stream(torch.cuda.current_stream())
+    mt.kv_attn_weights(*args, out=other, status_ws=ws, stream=s)
+    s.synchronize()
+    assert torch.equal(other, want)
+
+
+def test_slot_weights_far_pages():
+    c = _attn_case(np.random.default_rng(46), 2, 1, 16, 8, 128, [200, 77], "bf16", "chain")
+    lse, far, n = _lse_of(c), 300000, c["k"].shape[0]  # a page behind byte 2^32
+    table, ws = _i32(c["table"]).cuda(), _status()
+    k, ks = torch.empty((far + n, 8, P, 128), dtype=torch.uint8, device="cuda"), torch.empty((far + n, 8), device="cuda")
+    k[far:], ks[far:] = torch.from_numpy(c["k"]).cuda(), torch.from_numpy(c["ks"]).float().cuda()
+    w, v = torch.zeros(far + n, 8, P, device="cuda"), torch.zeros(n, 8, P, device="cuda")
+    args = (c["q"].cuda(), _i32(c["lens"]).cuda(), lse)
+    mt.kv_attn_weights(args[0], k.view(torch.float8_e4m3fn), ks, torch.where(table >= 0, table + far, table), *args[1:], w, status_ws=ws)
+    mt.kv_attn_weights(args[0], _f8(c["k"]), ks[far:].contiguous(), table, *args[1:], v, status_ws=ws)
+    assert torch.equal(w[far:], v) and not bool(w[:far].any()) and mt.read_status(ws) == 0

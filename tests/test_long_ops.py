@@ -54,3 +54,50 @@ def test_the_binding_refuses_windows_that_do_not_fit():
     with pytest.raises(mt.MedusaTreeError):
         call(workspace=ws[:512])
     torch.cuda.synchronize()
+
+
+# ---- weights of cached slots ----
+
+@pytest.mark.parametrize("depth, decay, desc, want", [
+    (-1, 1.0, {}, INVALID), (64, 1.0, {}, INVALID), (3, -0.5, {}, INVALID), (3, float("inf"), {}, INVALID), (3, float("nan"), {}, INVALID),
+    (3, 1.0, dict(head_dim=96), UNSUPPORTED), (3, 1.0, dict(dtype=0), UNSUPPORTED), (3, 1.0, dict(cache_dtype=0), UNSUPPORTED), (3, 1.0, dict(batch=0), INVALID),
+    (3, 1.0, dict(num_q_heads=7), INVALID), (3, 1.0, dict(sm_scale=-1.0), INVALID),
+])
+def test_weights_sizes(lib, depth, decay, desc, want):  # noqa: F811
+    assert lib.mt_kv_attn_weights(_attn_desc(**desc), depth, decay, *[PTR] * 12, None) == want
+
+
+def test_weights_pointers(lib):  # noqa: F811
+    # q, lse, k_cache, k_scales, tables, lens, prev (may be null), path, path lengths (both or none), weights, out, status
+    for i in (0, 1, 2, 3, 4, 5, 7, 8, 9, 10, 11):
+        args = [PTR] * 12
+        args[i] = None
+        assert lib.mt_kv_attn_weights(_attn_desc(), 3, 1.0, *args, None) == INVALID, i
+    for i in (0, 2, 9, 10, 11):
+        args = [PTR] * 12
+        args[i] = ODD
+        assert lib.mt_kv_attn_weights(_attn_desc(), 3, 1.0, *args, None) == INVALID, i
+    args = [PTR] * 12
+    args[10] = PTR + 16  # out over a part of weights
+    assert lib.mt_kv_attn_weights(_attn_desc(), 3, 1.0, *args, None) == INVALID
+    assert lib.mt_kv_attn_weights(None, 3, 1.0, *[PTR] * 12, None) == INVALID
+
+
+@pytest.mark.gpu
+def test_the_binding_refuses_weights_that_do_not_fit():
+    cu = lambda *s, dtype=torch.float32: torch.zeros(*s, dtype=dtype, device="cuda")  # noqa: E731
+    q, cache, table = cu(3, 4, 8, 128, dtype=torch.bfloat16), cu(6, 2, 16, 128, dtype=torch.float8_e4m3fn), cu(3, 2, dtype=torch.int32)
+    i32 = lambda *s: cu(*s, dtype=torch.int32)  # noqa: E731
+    call = lambda **kw: mt.kv_attn_weights(**{**dict(q=q, k_cache=cache, k_scales=cu(6, 2), block_tables=table, seq_lens=i32(3), lse=cu(3, 4, 8), weights=cu(6, 2, 16),  # noqa: E731
+                                                     status_ws=cu(64)), **kw})
+    call()
+    call(accept_path=i32(3, 2), accept_len=i32(3), prev_lens=i32(3), out=cu(6, 2, 16))
+    for kw in (dict(q=q.float()), dict(q=q[0]), dict(q=q.cpu()), dict(k_cache=q), dict(k_scales=cu(6, 3)), dict(block_tables=i32(3)), dict(seq_lens=i32(2)), dict(lse=cu(3, 4, 7)),
+               dict(weights=cu(6, 2, 8)), dict(weights=cu(6, 16, 2).transpose(1, 2)), dict(out=cu(5, 2, 16)), dict(prev_lens=i32(4)), dict(accept_path=i32(3, 2)),
+               dict(accept_path=i32(2, 2), accept_len=i32(3)), dict(accept_path=i32(3), accept_len=i32(3)), dict(status_ws=cu(8)), dict(weights=None)):
+        with pytest.raises((ValueError, TypeError)):
+            call(**kw)
+    for kw in (dict(decay=-1.0), dict(sm_scale=-1.0), dict(accept_path=i32(3, 65), accept_len=i32(3))):
+        with pytest.raises(mt.MedusaTreeError):
+            call(**kw)
+    torch.cuda.synchronize()
