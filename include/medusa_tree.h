@@ -517,6 +517,38 @@ int mt_kv_attn_weights(const mt_attn_desc* desc, int max_depth, float decay, con
                        const int32_t* accept_len, const float* weights, float* out, void* status_ws,
                        cudaStream_t stream);
 
+/* ---- Eviction ---------------------------------------------------------------------
+ * Keeps a sequence's cache within a budget of slots.  For each sequence b and KV head h,
+ * with L = seq_lens[b] and n = min(L, budget): all slots when L <= budget; else the first
+ * `sinks`, the last `recent`, and of those between the budget - sinks - recent of largest
+ * weight (a NaN is lowest, below -inf; of equal ones the lower slots).  Each head chooses
+ * for itself.  The kept slots in ascending order become slots 0 .. n-1 of the pages
+ * new_tables[b][0 ..]: their keys, values and weights are copied there.
+ *   kept int32 [B][Hkv][budget] out: the old slot of each new one, -1 from n on
+ *   weights fp32 [num_pages][Hkv][16], as mt_kv_attn_weights writes them
+ *   new_tables int32 [B][new_blocks_per_seq], new_blocks_per_seq * 16 >= budget: pages
+ *   that no sequence of the call is read from, each listed once; entries behind the
+ *   ceil(n / 16)-th are not used
+ * The old pages, tables and lengths are left as they were (a prompt's pages may be shared):
+ * a model's layers evict with the same tables, then the caller takes new_tables and lengths
+ * min(L, budget).  Slots from n on of the last new page are left as they were.  Keys stay
+ * rotated at the positions they had: a slot's number is no longer its position, and the new
+ * tokens' positions have to be counted apart (mt_qk_norm_rope takes any).
+ * The cache holds dtype's elements (cache_dtype 0) or E4M3 codes (MT_E4M3), copied as they
+ * are; with k_scales and v_scales (fp32 [num_pages][Hkv], positive) a new page's scale is
+ * the largest of its rows' pages', and a row from a page of a smaller scale has the codes of
+ * (its value / the new scale), rounded to nearest even; a NaN stays one.
+ * desc: batch, num_kv_heads, head_dim, page_size, max_blocks_per_seq (of block_tables),
+ * num_pages, dtype, cache_dtype; the rest is not used.  budget >= 1, sinks + recent <=
+ * budget.  A sequence with seq_lens[b] < 0 is no sequence: nothing is written for it.
+ * Device status (status_ws, at least 256 bytes): MT_ERR_PAGES for a length past the table
+ * (nothing of that sequence is written), a page id out of range (a new page that would
+ * take a row from it, or that has none itself, is not written; its slots count as lowest). */
+int mt_kv_evict(const mt_attn_desc* desc, int new_blocks_per_seq, int budget, int sinks, int recent,
+                void* k_cache, void* v_cache, float* k_scales, float* v_scales, float* weights,
+                const int32_t* block_tables, const int32_t* seq_lens, const int32_t* new_tables,
+                int32_t* kept, void* status_ws, cudaStream_t stream);
+
 /* ---- Sampling --------------------------------------------------------------------
  * A drawn token beside the argmax that greedy and typical acceptance return (the
  * bonus token of an accepted path's last row, or a decoding step's).  For each i,

@@ -18,6 +18,7 @@ Calls (same names as the C ABI without the ``mt_`` prefix):
   tree_attn_paged_block8  tree attention over an 8-bit cache with a scale per page and head,
                      of the whole cache or under a sliding window with sinks
   kv_attn_weights    the attention weight that each cached slot has received
+  kv_evict           the slots worth keeping, by weight, into new pages
   sample_tokens      temperature, top-k, top-p and min-p from given uniform numbers
 """
 from __future__ import annotations
@@ -117,6 +118,7 @@ def _load():
         lib.mt_tree_attn_paged_block8.argtypes = [P] + [P] * 12 + [Z, P]
         lib.mt_tree_attn_paged_block8_window.argtypes = [P, I, I] + [P] * 13 + [Z, P]
         lib.mt_kv_attn_weights.argtypes = [P, I, ctypes.c_float] + [P] * 13
+        lib.mt_kv_evict.argtypes = [P, I, I, I, I] + [P] * 11
         lib.mt_sample_tokens.argtypes = [I, I, I, P, I, L] + [P] * 7 + [P]
         lib.mt_read_status.argtypes = [P, P, ctypes.POINTER(I)]
         lib.mt_profile_enable.argtypes = [I]
@@ -782,6 +784,49 @@ def kv_attn_weights(q, k_cache, k_scales, block_tables, seq_lens, lse, weights, 
             None if prev_lens is None else _arg(prev_lens, "prev_lens", i32, (b,), dev), path, length, wp,
             wp if out is None else _arg(out, "out", f32, slots, dev), _status_arg(status_ws, "status_ws", dev))
     return weights if out is None else out
+
+
+def kv_evict(k_cache, v_cache, weights, block_tables, seq_lens, new_tables, kept, *, status_ws: torch.Tensor,
+             sinks: int = 0, recent: int = 0, k_scales=None, v_scales=None, stream=None):
+    """Copies the slots worth keeping of each sequence and KV head to the pages of
+    new_tables [B,blocks], in their order: all of them up to the budget, which is
+    kept.shape[2]; else the first `sinks`, the last `recent` and the heaviest between,
+    by weights [pages,Hkv,16].  kept [B,Hkv,budget] (int32) receives their old slots,
+    -1 behind the last.  The old pages, block_tables and seq_lens stay as they are;
+    once every layer has evicted, the tables are new_tables and the lengths
+    min(seq_lens, budget)."""
+    dev = _cuda_device(k_cache, "k_cache")
+    cdt = k_cache.dtype
+    if cdt is not _E4M3:
+        _act(k_cache, "k_cache")
+    if k_cache.dim() != 4:
+        raise ValueError("k_cache must have 4 dims (pages, heads, slots, head_dim)")
+    pages, hkv, page, d = k_cache.shape
+    for t, name in ((block_tables, "block_tables"), (new_tables, "new_tables")):
+        if not isinstance(t, torch.Tensor) or t.dim() != 2:
+            raise ValueError(f"{name} must have 2 dims")
+    if not isinstance(kept, torch.Tensor) or kept.dim() != 3:
+        raise ValueError("kept must have 3 dims (batch, heads, budget)")
+    if (k_scales is None) != (v_scales is None):
+        raise ValueError("k_scales and v_scales go together")
+    f32, i32 = torch.float32, torch.int32
+    ksp = vsp = None
+    if k_scales is not None:
+        if cdt is not _E4M3:
+            raise ValueError(f"block scales need a cache of {_E4M3}")
+        ksp = _arg(k_scales, "k_scales", f32, (pages, hkv), dev)
+        vsp = _arg(v_scales, "v_scales", f32, (pages, hkv), dev)
+    b, blocks = block_tables.shape
+    budget = kept.shape[2]
+    desc = _ATTN_DESC.pack(b, 1, hkv, hkv, d, page, blocks, pages, 0, _DTYPES.get(cdt, 2), 0.0, 0,
+                           MT_E4M3 if cdt is _E4M3 else 0, 1.0, 1.0)
+    _invoke(_load().mt_kv_evict, "mt_kv_evict", dev, stream, desc, new_tables.shape[1], budget, _int32(sinks, "sinks"),
+            _int32(recent, "recent"), _arg(k_cache, "k_cache", cdt, k_cache.shape, dev),
+            _arg(v_cache, "v_cache", cdt, k_cache.shape, dev), ksp, vsp, _arg(weights, "weights", f32, (pages, hkv, page), dev),
+            _arg(block_tables, "block_tables", i32, (b, blocks), dev), _arg(seq_lens, "seq_lens", i32, (b,), dev),
+            _arg(new_tables, "new_tables", i32, (b, new_tables.shape[1]), dev), _arg(kept, "kept", i32, (b, hkv, budget), dev),
+            _status_arg(status_ws, "status_ws", dev))
+    return kept
 
 
 def sample_tokens(logits, uniforms, tokens, *, temperature=None, top_k=None, top_p=None, min_p=None,

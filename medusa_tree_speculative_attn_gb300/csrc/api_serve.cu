@@ -352,6 +352,40 @@ int mt_kv_attn_weights(const mt_attn_desc* d, int max_depth, float decay, const 
   return cuda_status(launch_kv_weights(p, d->dtype, stream));
 }
 
+int mt_kv_evict(const mt_attn_desc* d, int new_blocks_per_seq, int budget, int sinks, int recent, void* k_cache,
+                void* v_cache, float* k_scales, float* v_scales, float* weights, const int32_t* block_tables,
+                const int32_t* seq_lens, const int32_t* new_tables, int32_t* kept, void* status_ws,
+                cudaStream_t stream) {
+  const mt_call_range range("mt_kv_evict");
+  if (!d || d->batch < 1 || d->batch > kMaxBatch || d->num_kv_heads < 1 || d->max_blocks_per_seq < 1 || d->num_pages < 1)
+    return MT_ERR_INVALID_ARG;
+  if (!act_dtype(d->dtype) || (d->cache_dtype != 0 && d->cache_dtype != MT_E4M3)) return MT_ERR_UNSUPPORTED;
+  if (d->head_dim != 64 && d->head_dim != 128) return MT_ERR_UNSUPPORTED;
+  if (d->page_size != 16) return MT_ERR_UNSUPPORTED;
+  if ((long long)d->num_pages * d->num_kv_heads * d->page_size >= (1ll << 31) ||
+      (long long)d->max_blocks_per_seq * d->page_size >= (1ll << 31) - 4096)
+    return MT_ERR_UNSUPPORTED;
+  if (budget < 1 || sinks < 0 || recent < 0 || (long long)sinks + recent > budget || new_blocks_per_seq < 1 ||
+      (long long)new_blocks_per_seq * 16 < budget)
+    return MT_ERR_INVALID_ARG;
+  if ((k_scales == nullptr) != (v_scales == nullptr) || (k_scales && d->cache_dtype != MT_E4M3))
+    return MT_ERR_INVALID_ARG;
+  if (!k_cache || !v_cache || !weights || !block_tables || !seq_lens || !new_tables || !kept || !status_ws)
+    return MT_ERR_INVALID_ARG;
+  if (!aligned16(k_cache) || !aligned16(v_cache) || !aligned16(weights) || !aligned16(status_ws))
+    return MT_ERR_INVALID_ARG;
+  EvictParams p{};
+  p.B = d->batch; p.Hkv = d->num_kv_heads; p.max_blocks = d->max_blocks_per_seq; p.new_blocks = new_blocks_per_seq;
+  p.num_pages = d->num_pages;
+  p.row_bytes = d->head_dim * (d->cache_dtype == MT_E4M3 ? 1 : act_bytes(d->dtype));
+  p.budget = budget; p.sinks = sinks; p.recent = recent;
+  p.k_cache = k_cache; p.v_cache = v_cache; p.k_scales = k_scales; p.v_scales = v_scales; p.weights = weights;
+  p.block_tables = block_tables; p.seq_lens = seq_lens; p.new_tables = new_tables;
+  p.kept = kept;
+  p.status = static_cast<int*>(status_ws);
+  return cuda_status(launch_kv_evict(p, stream));
+}
+
 int mt_sample_tokens(int num_rows, int vocab, mt_dtype logits_dtype, const void* logits, int num_logit_rows,
                      long long row_stride, const int32_t* row_index, const float* uniforms, const float* temperature,
                      const int32_t* top_k, const float* top_p, const float* min_p, int32_t* tokens,

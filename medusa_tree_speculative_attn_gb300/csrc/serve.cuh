@@ -407,6 +407,26 @@ struct WeightsParams {
 cudaError_t launch_kv_weights(const WeightsParams& p, int dtype, cudaStream_t stream);
 
 // ---------------------------------------------------------------------------
+// Eviction.
+// ---------------------------------------------------------------------------
+struct EvictParams {
+  int B, Hkv, max_blocks, new_blocks, num_pages;
+  int row_bytes;  // of a key or value: 64, 128, 256 or 512
+  int budget, sinks, recent;
+  void* k_cache;
+  void* v_cache;
+  float* k_scales;  // [num_pages][Hkv], or null
+  float* v_scales;
+  float* weights;   // [num_pages][Hkv][16]
+  const int* block_tables;
+  const int* seq_lens;
+  const int* new_tables;  // [B][new_blocks]
+  int* kept;              // [B][Hkv][budget]
+  int* status;
+};
+cudaError_t launch_kv_evict(const EvictParams& p, cudaStream_t stream);
+
+// ---------------------------------------------------------------------------
 // Sampling.
 // ---------------------------------------------------------------------------
 // Largest vocab: that many weights of 2^44 (the maximum's) stay below 2^63, and an

@@ -104,3 +104,45 @@ def weights64(c, weights, lse, lens, prev, nodes_of, decay, scale):
                     off += p * (2 * d * 2.0 ** -24 * scale * (np.abs(k) @ np.abs(q[i, a, j])) + 2.0 ** -22 * (np.abs(z) + abs(lse[i, a, j])) + 2.0 ** -19)
             out[page, h, at], tol[page, h, at] = got, off
     return out, tol
+
+
+def kept_slots(weights, budget, sinks, recent):
+    """The slots that stay of one head's weights [L], ascending."""
+    n = len(weights)
+    if n <= budget:
+        return np.arange(n)
+    middle = np.arange(sinks, n - recent)
+    w = weights[middle].astype(np.float64)
+    w = np.where(np.isnan(w), -np.inf, w)
+    order = np.lexsort((middle, ~np.isnan(weights[middle]) * -1, -w))  # heavier; a number before a NaN; lower slot
+    best = middle[order[:budget - sinks - recent]]
+    return np.sort(np.concatenate([np.arange(sinks), best, np.arange(n - recent, n)]))
+
+
+def evict(kind, caches, scales, weights, table, lens, new_tables, budget, sinks, recent):
+    """Changes the host arrays as kv_evict does; returns kept.  caches: [k, v] as raw arrays [pages][Hkv][16][..]; scales:
+    [k, v] in 64 bits for `block8`."""
+    hkv = weights.shape[1]
+    kept = np.full((len(lens), hkv, budget), -1, np.int64)
+    for b, n in enumerate(lens):
+        if n < 1:
+            continue
+        page, at = table[b][np.arange(n) // P], np.arange(n) % P
+        for h in range(hkv):
+            stay = kept_slots(weights[page, h, at], budget, sinks, recent)
+            kept[b, h, :len(stay)] = stay
+            rows = [c[page[stay], h, at[stay]].copy() for c in caches]
+            w = weights[page[stay], h, at[stay]].copy()
+            old = [s[page[stay], h].copy() for s in scales] if kind == "block8" else None
+            for j in range(0, len(stay), P):
+                m, to = min(P, len(stay) - j), new_tables[b][j // P]
+                weights[to, h, :m] = w[j:j + m]
+                for x in range(2):
+                    block = rows[x][j:j + m]
+                    if kind == "block8":
+                        top = old[x][j:j + m].max()
+                        f = (old[x][j:j + m] / top)[:, None]
+                        block = np.where(f == 1, block, ref.encode(ref.decode(block) * f))
+                        scales[x][to, h] = top
+                    caches[x][to, h, :m] = block
+    return kept

@@ -13,7 +13,7 @@ torch = pytest.importorskip("torch")
 import long_reference as lref
 import medusa_tree_speculative_attn_gb300 as mt
 import serve_reference as ref
-from test_gpu_serve import DT, P, _attn_case, _codes, _graph, _i32, _rand, _status, _table
+from test_gpu_serve import DT, P, Cache, _attn_case, _codes, _graph, _i32, _rand, _status, _table
 
 pytestmark = pytest.mark.gpu
 
@@ -350,3 +350,186 @@ def test_slot_weights_far_pages():
     mt.kv_attn_weights(args[0], k.view(torch.float8_e4m3fn), ks, torch.where(table >= 0, table + far, table), *args[1:], w, status_ws=ws)
     mt.kv_attn_weights(args[0], _f8(c["k"]), ks[far:].contiguous(), table, *args[1:], v, status_ws=ws)
     assert torch.equal(w[far:], v) and not bool(w[:far].any()) and mt.read_status(ws) == 0
+
+
+# ---- eviction -------------------------------------------------------------------
+
+class Evict:
+    """A cache of one kind with weights, tables and new pages, on both sides."""
+
+    def __init__(self, rng, kind, dt, hkv, d, lens, budget, spread=2.0):
+        self.cache, self.lens, self.budget, self.kind = None, lens, budget, kind
+        need, after = [-(-max(n, 0) // P) for n in lens], [-(-min(max(n, 0), budget) // P) for n in lens]
+        self.pages = sum(need) + sum(after) + 3
+        perm, at = rng.permutation(self.pages), 0
+        self.table, self.new = np.full((len(lens), max(1, *need)), -1, np.int32), np.full((len(lens), -(-budget // P) + 1), -1, np.int32)
+        for b in range(len(lens)):
+            for t, n in ((self.table, need[b]), (self.new, after[b])):
+                t[b, :n] = perm[at:at + n]
+                at += n
+        self.cache = Cache(rng, kind, self.pages, hkv, d, dt)
+        self.weights = np.exp(spread * rng.standard_normal((self.pages, hkv, P))).astype(np.float32)
+        self.weights[rng.random(self.weights.shape) < 0.2] = 0  # ties
+
+    def run(self, sinks, recent, status=0, **kw):
+        self.w, self.ws = torch.from_numpy(self.weights).cuda(), _status()
+        self.kept = torch.full((len(self.lens), self.weights.shape[1], self.budget), 77, dtype=torch.int32, device="cuda")
+        c = self.cache
+        self.args = (c.k, c.v, self.w, _i32(self.table).cuda(), _i32(self.lens).cuda(), _i32(self.new).cuda(), self.kept)
+        self.kw = dict(sinks=sinks, recent=recent, k_scales=c.scales[0], v_scales=c.scales[1], status_ws=self.ws, **kw)
+        assert mt.kv_evict(*self.args, **self.kw) is self.kept
+        assert mt.read_status(self.ws) == status
+
+    def check(self, sinks, recent):
+        raw = [c.view(torch.uint8).numpy() for c in self.cache.host]  # the same memory; rows of bytes
+        kept = lref.evict(self.kind, raw, getattr(self.cache, "host_scales", None), self.weights, self.table, self.lens, self.new, self.budget, sinks, recent)
+        live = np.array([n >= 0 for n in self.lens])
+        got = self.kept.cpu().numpy()
+        assert np.array_equal(got[live], kept[live]) and (got[~live] == 77).all()
+        self.cache.check()
+        assert np.array_equal(self.w.cpu().numpy(), self.weights, equal_nan=True)
+
+
+EVICTS = [  # heads, D, lengths, budget, sinks, recent
+    (1, 64, [1], 1, 0, 0), (1, 64, [2], 1, 0, 1), (2, 128, [40, 0, 17], 16, 2, 5), (3, 64, [100, -1, 99, 33], 33, 33, 0), (2, 128, [500, 31, 32], 31, 0, 31),
+    (2, 64, [70], 100, 10, 20), (8, 128, [300, 290, 1], 256, 4, 64), (1, 128, [1000], 999, 0, 0), (5, 128, [129], 64, 0, 0), (2, 64, [3000, 64], 65, 1, 1),
+]
+
+
+@pytest.mark.parametrize("kind, dtype", [("act", "f32"), ("act", "f16"), ("act", "bf16"), ("e4m3", "bf16"), ("block8", "bf16")])
+@pytest.mark.parametrize("case", range(len(EVICTS)))
+def test_evict(kind, dtype, case):
+    hkv, d, lens, budget, sinks, recent = EVICTS[case]
+    e = Evict(np.random.default_rng(3000 + case), kind, DT[dtype], hkv, d, lens, budget)
+    if kind == "block8":  # no NaN codes: a re-encoded one keeps no sign
+        for c, h in zip((e.cache.k, e.cache.v), e.cache.host):
+            h.view(torch.uint8).numpy()[...] &= 0xF7
+            c.view(torch.uint8).copy_(h.view(torch.uint8).cuda())
+    e.run(sinks, recent)
+    e.check(sinks, recent)
+
+
+@pytest.mark.parametrize("what", ["equal", "zero", "negative", "odd", "close", "two"])
+@pytest.mark.parametrize("longest", [700, 44000])  # keys in shared memory, and more of them
+def test_evict_ties_and_odd_weights(what, longest):
+    rng = np.random.default_rng(50)
+    e = Evict(rng, "e4m3", torch.bfloat16, 2, 64, [longest, 600], 500)
+    w = e.weights
+    if what == "equal":
+        w[...] = 0.7
+    elif what == "zero":
+        w[...] = np.where(rng.random(w.shape) < 0.5, 0.0, -0.0)
+    elif what == "negative":
+        w[...] = -w
+    elif what == "odd":
+        w[...] = rng.choice(np.array([np.nan, np.inf, -np.inf, 0, 1, -1e-42, 1e-42, 3e38], np.float32), w.shape)
+    elif what == "close":
+        w[...] = (np.float32(1).view(np.int32) + rng.integers(0, 40, w.shape).astype(np.int32)).view(np.float32)
+    else:
+        w[...] = np.where(rng.random(w.shape) < 0.05, 2.0, 1.0)
+    e.run(4, 100)
+    e.check(4, 100)
+
+
+def test_evict_scales_far_apart():
+    rng = np.random.default_rng(51)
+    e = Evict(rng, "block8", torch.bfloat16, 2, 128, [400], 100)
+    for x in range(2):
+        e.cache.host[x].view(torch.uint8).numpy()[...] &= 0xF7
+        (e.cache.k, e.cache.v)[x].view(torch.uint8).copy_(e.cache.host[x].view(torch.uint8).cuda())
+        e.cache.host_scales[x][...] = 2.0 ** rng.integers(-64, 120, e.cache.host_scales[x].shape)
+        e.cache.scales[x].copy_(torch.from_numpy(e.cache.host_scales[x]).float())
+    e.run(3, 10)
+    e.check(3, 10)
+
+
+def test_evict_keeps_nan_codes():
+    rng = np.random.default_rng(52)
+    e = Evict(rng, "block8", torch.bfloat16, 1, 64, [200], 64)
+    e.run(0, 0)
+    kept = e.kept.cpu().numpy()[0, 0]
+    src = e.cache.host[0].view(torch.uint8).numpy()[e.table[0][kept // P], 0, kept % P]
+    got = _codes(e.cache.k)[e.new[0][np.arange(64) // P], 0, np.arange(64) % P]
+    assert np.array_equal(np.isnan(ref.decode(got)), np.isnan(ref.decode(src))) and np.isnan(ref.decode(src)).any()
+
+
+def test_evict_pages_of_a_prefix_that_two_sequences_share():
+    rng = np.random.default_rng(53)
+    e = Evict(rng, "act", torch.float16, 2, 64, [100, 140], 60)
+    e.table[1, :4] = e.table[0, :4]
+    e.run(2, 20)
+    e.check(2, 20)  # the shared pages are where they were
+
+
+@pytest.mark.parametrize("bad", ["length", "page", "new"])
+def test_evict_status_and_what_errors_leave(bad):
+    rng = np.random.default_rng(54)
+    e = Evict(rng, "act", torch.bfloat16, 2, 64, [70, 60], 40)
+    before, table, new, lens = [c.clone() for c in e.cache.host], e.table.copy(), e.new.copy(), list(e.lens)
+    untouched = set(range(e.pages)) - set(new[1][:3])
+    if bad == "length":
+        e.lens[0] = 81
+    elif bad == "page":  # the recent rows' page: slots 64 .. 69 are new slots 34 .. 39, of the third new page
+        e.table[0, 4] = e.pages
+        untouched -= set(new[0][:2])
+    else:
+        e.new[0, 1] = -1
+        untouched -= {new[0][0], new[0][2]}
+    e.run(0, 6, status=-4)
+    for c, h in zip((e.cache.k, e.cache.v), before):
+        for p in untouched:
+            assert torch.equal(c[p].cpu(), h[p]), (bad, p)
+    # the other sequence is as it should be
+    e.table, e.new, e.lens = table, new, lens
+    kept = lref.evict("act", [h.view(torch.uint8).numpy() for h in e.cache.host], None, e.weights, table, [-1, 60], new, 40, 0, 6)
+    assert np.array_equal(e.kept.cpu().numpy()[1], kept[1])
+    for p in new[1][:2]:
+        assert torch.equal(e.cache.k[p].cpu(), e.cache.host[0][p])
+
+
+def test_evict_in_a_graph_with_other_lengths_and_twice_the_same():
+    rng = np.random.default_rng(55)
+    e = Evict(rng, "block8", torch.bfloat16, 2, 64, [200, 170, 64], 64)
+    for c, h in zip((e.cache.k, e.cache.v), e.cache.host):
+        h.view(torch.uint8).numpy()[...] &= 0xF7
+        c.view(torch.uint8).copy_(h.view(torch.uint8).cuda())
+    e.run(4, 16)
+    first = e.kept.clone()
+    mt.kv_evict(*e.args, **e.kw)  # the old pages are still there
+    assert torch.equal(e.kept, first)
+    e.check(4, 16)
+    g = _graph(lambda: mt.kv_evict(*e.args, **e.kw))
+    e.lens = [100, 30, -1]
+    e.args[4].copy_(_i32(e.lens))
+    e.kept.fill_(77)
+    g.replay()
+    torch.cuda.synchronize()
+    e.check(4, 16)
+    assert mt.read_status(e.ws) == 0
+
+
+@pytest.mark.parametrize("kind", ["act", "block8"])
+def test_evict_far_pages(kind):
+    rng = np.random.default_rng(56)
+    hkv, d, far = 8, 128, 300000  # a page behind byte 2^32 and, in 16 bits, element 2^32
+    e = Evict(rng, kind, torch.bfloat16, hkv, d, [100, 37], 48)
+    e.run(2, 8)
+    n, c = e.pages, e.cache
+    big = [torch.empty((far + n, *x.shape[1:]), dtype=x.dtype, device="cuda") for x in (c.k, c.v, e.w)]
+    for x, y in zip(big, (c.k, c.v, e.w)):
+        x.view(torch.uint8)[far:] = y.view(torch.uint8)
+        x.view(torch.uint8)[torch.from_numpy(far + e.new[e.new >= 0]).cuda()] = 0
+    scales = [None, None]
+    if kind == "block8":
+        scales = [torch.ones(far + n, hkv, device="cuda") for _ in range(2)]
+        for x, y in zip(scales, c.scales):
+            x[far:] = y
+    move = lambda t: torch.where(t >= 0, t + far, t)  # noqa: E731
+    kept = torch.zeros_like(e.kept)
+    mt.kv_evict(*big, move(e.args[3]), e.args[4], move(e.args[5]), kept, sinks=2, recent=8, k_scales=scales[0], v_scales=scales[1], status_ws=e.ws)
+    assert mt.read_status(e.ws) == 0 and torch.equal(kept, e.kept)
+    for b, m in enumerate([48, 37]):
+        for j in range(0, m, P):
+            p, rows = int(e.new[b, j // P]), min(P, m - j)
+            for x, y in zip(big, (c.k, c.v, e.w)):
+                assert torch.equal(x[far + p, :, :rows].view(torch.uint8), y[p, :, :rows].view(torch.uint8))

@@ -101,3 +101,52 @@ def test_the_binding_refuses_weights_that_do_not_fit():
         with pytest.raises(mt.MedusaTreeError):
             call(**kw)
     torch.cuda.synchronize()
+
+
+# ---- eviction ----
+
+def _evict(lib, args, blocks=2, budget=20, sinks=2, recent=4, **desc):  # noqa: F811
+    return lib.mt_kv_evict(_attn_desc(**desc), blocks, budget, sinks, recent, *args, None)
+
+
+@pytest.mark.parametrize("kw, want", [
+    (dict(budget=0), INVALID), (dict(sinks=-1), INVALID), (dict(recent=-1), INVALID), (dict(sinks=10, recent=11), INVALID), (dict(sinks=2 ** 31 - 1, recent=2 ** 31 - 1), INVALID),
+    (dict(blocks=1), INVALID), (dict(blocks=0), INVALID), (dict(batch=0), INVALID), (dict(batch=8193), INVALID), (dict(num_kv_heads=0), INVALID), (dict(head_dim=96), UNSUPPORTED),
+    (dict(page_size=32), UNSUPPORTED), (dict(max_blocks_per_seq=0), INVALID), (dict(num_pages=0), INVALID), (dict(num_pages=1 << 27), UNSUPPORTED), (dict(dtype=3), UNSUPPORTED),
+    (dict(cache_dtype=2), UNSUPPORTED), (dict(cache_dtype=0), INVALID), (dict(max_blocks_per_seq=1 << 27), UNSUPPORTED),
+])
+def test_evict_sizes(lib, kw, want):  # noqa: F811
+    assert _evict(lib, [PTR] * 10, **kw) == want
+
+
+def test_evict_pointers(lib):  # noqa: F811
+    # k_cache, v_cache, k_scales, v_scales (both or none), weights, tables, lens, new tables, kept, status
+    for i in range(10):
+        args = [PTR] * 10
+        args[i] = None
+        assert _evict(lib, args) == INVALID, i
+    for i in (0, 1, 4, 9):
+        args = [PTR] * 10
+        args[i] = ODD
+        assert _evict(lib, args) == INVALID, i
+    assert lib.mt_kv_evict(None, 2, 20, 2, 4, *[PTR] * 10, None) == INVALID
+
+
+@pytest.mark.gpu
+def test_the_binding_refuses_evictions_that_do_not_fit():
+    cu = lambda *s, dtype=torch.float32: torch.zeros(*s, dtype=dtype, device="cuda")  # noqa: E731
+    i32 = lambda *s: cu(*s, dtype=torch.int32)  # noqa: E731
+    f8 = lambda *s: cu(*s, dtype=torch.float8_e4m3fn)  # noqa: E731
+    call = lambda **kw: mt.kv_evict(**{**dict(k_cache=f8(6, 2, 16, 64), v_cache=f8(6, 2, 16, 64), weights=cu(6, 2, 16), block_tables=i32(3, 2), seq_lens=i32(3) - 1,  # noqa: E731
+                                              new_tables=i32(3, 2), kept=i32(3, 2, 20), sinks=2, recent=4, k_scales=cu(6, 2), v_scales=cu(6, 2), status_ws=cu(64)), **kw})
+    call()
+    call(k_scales=None, v_scales=None)
+    for kw in (dict(k_scales=None), dict(k_cache=cu(6, 2, 16, 64), v_cache=cu(6, 2, 16, 64)), dict(v_cache=f8(6, 2, 16, 128)), dict(weights=cu(6, 2, 17)), dict(weights=cu(6, 2, 16).half()),
+               dict(block_tables=i32(2, 2)), dict(new_tables=i32(6)), dict(seq_lens=i32(3, 1)), dict(kept=i32(3, 3, 20)), dict(kept=i32(3, 2, 20).long()), dict(sinks=-1), dict(recent=2 ** 31),
+               dict(k_cache=torch.zeros(6, 2, 16, 64)), dict(status_ws=cu(8)), dict(k_cache=f8(6, 16, 2, 64).transpose(1, 2))):
+        with pytest.raises((ValueError, TypeError)):
+            call(**kw)
+    for kw in (dict(sinks=17), dict(kept=i32(3, 2, 33)), dict(kept=i32(3, 2, 0))):
+        with pytest.raises(mt.MedusaTreeError):
+            call(**kw)
+    torch.cuda.synchronize()
