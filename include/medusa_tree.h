@@ -549,6 +549,54 @@ int mt_kv_evict(const mt_attn_desc* desc, int new_blocks_per_seq, int budget, in
                 const int32_t* block_tables, const int32_t* seq_lens, const int32_t* new_tables,
                 int32_t* kept, void* status_ws, cudaStream_t stream);
 
+/* ---- Penalties, biases and grammar masks on logits ---------------------------------
+ * What is done to logits before a token is drawn (mt_sample_tokens) or a tree accepted.
+ * For row t of sequence b (a node of its tree; tree_size 1: a decoding step), with seen_v:
+ * token v is in the history or on the node's path, and c_v: how often it is in the history
+ * from output_starts[b] on and on the path; in fp32, each operation rounded on its own, one
+ * rounding to the logits' dtype:
+ *   x = x > 0 ? x / repetition[b] : x * repetition[b]     where seen_v
+ *   x = x - frequency[b] * c_v - presence[b]               where c_v > 0
+ *   x = x + value of the bias                              where one names v
+ *   x = -inf                                               where the row's mask has a 0
+ * Entries that none of these concerns keep their bits.
+ *   history int32 [B][history_width] and history_lens int32 [B] (or both null: no
+ *   history): the first history_lens[b] tokens (at most history_width); a length < 0: no
+ *   sequence, its rows of `out` are left as they were.  output_starts int32 [B] or null
+ *   (0): a prompt's tokens come before.  repetition, presence, frequency fp32 [B], each or
+ *   null (1, 0, 0).
+ *   bias_tokens int32, bias_values fp32 [B][num_bias], or both null; of entries that name a
+ *   token twice the last counts.
+ *   mask int32 [num_masks][ceil(vocab / 32)] or null, bit v % 32 of word v / 32 for token
+ *   v, 1: allowed; mask_index int32 [B][T] the mask of each row, < 0: none, >= num_masks:
+ *   nothing is allowed; null: mask b * T + t (num_masks >= B * T).
+ *   tree_tokens int32 [B][T], or null: no paths (tree_size may then be any number);
+ *   tree_parents int32 [B][T] (as in mt_tree_attn_paged), or null: a chain.  A node's path
+ *   is its ancestors and itself: its row scores what comes after its own token.
+ * Token ids outside the vocabulary (of history, bias, tree) are passed over.
+ * Strides are in elements, (sequence, row), a row's entries dense; rows need no alignment.
+ * `out` may be the logits themselves (same pointer and strides); it must not overlap them
+ * otherwise, nor its own rows one another.  vocab <= 2^30, tree_size <= 64 with
+ * tree_tokens.  Device status (status_ws, at least 256 bytes): MT_ERR_TREE for a malformed
+ * tree (a node with such a parent counts as a root). */
+typedef struct {
+  int batch;
+  int tree_size;
+  int vocab;
+  mt_dtype dtype;
+  int history_width;
+  int num_bias;
+  int num_masks;
+  long long stride[2];
+  long long out_stride[2];
+} mt_logits_desc;
+int mt_process_logits(const mt_logits_desc* desc, const void* logits, void* out, const int32_t* history,
+                      const int32_t* history_lens, const int32_t* output_starts, const float* repetition,
+                      const float* presence, const float* frequency, const int32_t* bias_tokens,
+                      const float* bias_values, const int32_t* mask, const int32_t* mask_index,
+                      const int32_t* tree_tokens, const int32_t* tree_parents, void* status_ws,
+                      cudaStream_t stream);
+
 /* ---- Sampling --------------------------------------------------------------------
  * A drawn token beside the argmax that greedy and typical acceptance return (the
  * bonus token of an accepted path's last row, or a decoding step's).  For each i,

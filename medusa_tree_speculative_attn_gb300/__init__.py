@@ -19,6 +19,7 @@ Calls (same names as the C ABI without the ``mt_`` prefix):
                      of the whole cache or under a sliding window with sinks
   kv_attn_weights    the attention weight that each cached slot has received
   kv_evict           the slots worth keeping, by weight, into new pages
+  process_logits     penalties for repeated tokens, biases and grammar masks on logits
   sample_tokens      temperature, top-k, top-p and min-p from given uniform numbers
 """
 from __future__ import annotations
@@ -73,12 +74,20 @@ class AppendDesc(ctypes.Structure):
                 ("v_stride", ctypes.c_longlong * 2)]
 
 
+class LogitsDesc(ctypes.Structure):
+    _fields_ = [("batch", ctypes.c_int), ("tree_size", ctypes.c_int), ("vocab", ctypes.c_int),
+                ("dtype", ctypes.c_int), ("history_width", ctypes.c_int), ("num_bias", ctypes.c_int),
+                ("num_masks", ctypes.c_int), ("stride", ctypes.c_longlong * 2),
+                ("out_stride", ctypes.c_longlong * 2)]
+
+
 # The descriptors as the binding passes them: the same bytes, packed in one go
 # (filling a ctypes structure costs several times as much).
 _NORM_ROPE_DESC = struct.Struct("@5if8q")
 _APPEND_DESC = struct.Struct("@9i2f4q")
 _ATTN_DESC = struct.Struct("@10ifi" "i2f")
-assert (_NORM_ROPE_DESC.size == ctypes.sizeof(NormRopeDesc) and _APPEND_DESC.size == ctypes.sizeof(AppendDesc)
+_LOGITS_DESC = struct.Struct("@7i4x4q")
+assert (_LOGITS_DESC.size == ctypes.sizeof(LogitsDesc) and _NORM_ROPE_DESC.size == ctypes.sizeof(NormRopeDesc) and _APPEND_DESC.size == ctypes.sizeof(AppendDesc)
         and _ATTN_DESC.size == ctypes.sizeof(AttnDesc))
 
 _lib = None
@@ -119,6 +128,7 @@ def _load():
         lib.mt_tree_attn_paged_block8_window.argtypes = [P, I, I] + [P] * 13 + [Z, P]
         lib.mt_kv_attn_weights.argtypes = [P, I, ctypes.c_float] + [P] * 13
         lib.mt_kv_evict.argtypes = [P, I, I, I, I] + [P] * 11
+        lib.mt_process_logits.argtypes = [P] + [P] * 16
         lib.mt_sample_tokens.argtypes = [I, I, I, P, I, L] + [P] * 7 + [P]
         lib.mt_read_status.argtypes = [P, P, ctypes.POINTER(I)]
         lib.mt_profile_enable.argtypes = [I]
@@ -827,6 +837,63 @@ def kv_evict(k_cache, v_cache, weights, block_tables, seq_lens, new_tables, kept
             _arg(new_tables, "new_tables", i32, (b, new_tables.shape[1]), dev), _arg(kept, "kept", i32, (b, hkv, budget), dev),
             _status_arg(status_ws, "status_ws", dev))
     return kept
+
+
+def process_logits(logits, out, *, status_ws: torch.Tensor, history=None, history_lens=None, output_starts=None,
+                   repetition=None, presence=None, frequency=None, bias_tokens=None, bias_values=None, mask=None,
+                   mask_index=None, tree_tokens=None, tree_parents=None, stream=None):
+    """Penalises repeated tokens, adds biases and masks tokens of logits [B,T,V] or
+    [B,V], into out (which may be logits).
+
+    history [B,H] (int32) with history_lens [B]: the sequences' tokens, generated ones
+    from output_starts [B] on.  For trees, tree_tokens and tree_parents [B,T] (None: a
+    chain) add each node's path.  repetition, presence and frequency are tensors [B]
+    (float32) or None.  bias_tokens, bias_values [B,K]: a negative token is no entry, the
+    last of a token's entries counts.  mask [M,ceil(V/32)] (int32, bit set: allowed) with
+    mask_index [B,T] or [B] (negative: no mask; None: a mask per row)."""
+    dev = _cuda_device(logits, "logits")
+    dt = _act(logits, "logits")
+    if logits.dim() not in (2, 3):
+        raise ValueError("logits must have 2 or 3 dims")
+    shape, two = logits.shape, logits.dim() == 2
+    b, v = shape[0], shape[-1]
+    t = 1 if two else shape[1]
+    if not isinstance(out, torch.Tensor):
+        raise TypeError("out must be a torch.Tensor")
+    if out.dtype is not logits.dtype or out.shape != shape or out.device != dev:
+        _refuse(out, "out", logits.dtype, shape, dev, "fit")
+    strides = []
+    for x, name in ((logits, "logits"), (out, "out")):
+        st = x.stride()
+        if v > 1 and st[-1] != 1:
+            raise ValueError(f"{name} must have dense rows")
+        strides += [st[0] if b > 1 else 0, 0 if two or t <= 1 else st[1]]
+    f32, i32, rows = torch.float32, torch.int32, (b,) if two else (b, t)
+    opt = lambda x, name, ty, shp: None if x is None else _arg(x, name, ty, shp, dev)  # noqa: E731
+    width = lambda x, name: x.shape[1] if isinstance(x, torch.Tensor) and x.dim() == 2 else _two_dims(x, name)  # noqa: E731
+    h, k, m = width(history, "history"), width(bias_tokens, "bias_tokens"), 0
+    for x, y, names in ((history, history_lens, "history and history_lens"), (bias_tokens, bias_values, "bias_tokens and bias_values")):
+        if (x is None) != (y is None):
+            raise ValueError(f"{names} go together")
+    if mask is not None:
+        width(mask, "mask")
+        m = mask.shape[0]
+    desc = _LOGITS_DESC.pack(b, t, v, dt, h, k, m, *strides)
+    _invoke(_load().mt_process_logits, "mt_process_logits", dev, stream, desc, logits.data_ptr(), out.data_ptr(),
+            opt(history, "history", i32, (b, h)), opt(history_lens, "history_lens", i32, (b,)),
+            opt(output_starts, "output_starts", i32, (b,)), opt(repetition, "repetition", f32, (b,)),
+            opt(presence, "presence", f32, (b,)), opt(frequency, "frequency", f32, (b,)),
+            opt(bias_tokens, "bias_tokens", i32, (b, k)), opt(bias_values, "bias_values", f32, (b, k)),
+            opt(mask, "mask", i32, (m, (v + 31) // 32)), opt(mask_index, "mask_index", i32, rows),
+            opt(tree_tokens, "tree_tokens", i32, rows), opt(tree_parents, "tree_parents", i32, rows),
+            _status_arg(status_ws, "status_ws", dev))
+    return out
+
+
+def _two_dims(x, name):
+    if x is not None:
+        raise ValueError(f"{name} must be a tensor of 2 dims")
+    return 0
 
 
 def sample_tokens(logits, uniforms, tokens, *, temperature=None, top_k=None, top_p=None, min_p=None,

@@ -386,6 +386,58 @@ int mt_kv_evict(const mt_attn_desc* d, int new_blocks_per_seq, int budget, int s
   return cuda_status(launch_kv_evict(p, stream));
 }
 
+int mt_process_logits(const mt_logits_desc* d, const void* logits, void* out, const int32_t* history,
+                      const int32_t* history_lens, const int32_t* output_starts, const float* repetition,
+                      const float* presence, const float* frequency, const int32_t* bias_tokens,
+                      const float* bias_values, const int32_t* mask, const int32_t* mask_index,
+                      const int32_t* tree_tokens, const int32_t* tree_parents, void* status_ws, cudaStream_t stream) {
+  const mt_call_range range("mt_process_logits");
+  if (!d || d->batch < 0 || d->tree_size < 0 || d->vocab < 1 || d->history_width < 0 || d->num_bias < 0 ||
+      d->num_masks < 0 || d->history_width >= (1 << 30))
+    return MT_ERR_INVALID_ARG;
+  if (!act_dtype(d->dtype) || d->vocab > (1 << 30)) return MT_ERR_UNSUPPORTED;
+  const long long rows = (long long)d->batch * d->tree_size;
+  if (rows > (1 << 24)) return MT_ERR_INVALID_ARG;
+  for (const long long s : {d->stride[0], d->stride[1], d->out_stride[0], d->out_stride[1]})
+    if (s < 0) return MT_ERR_INVALID_ARG;
+  if ((history && !history_lens) || (history_lens && !history && d->history_width > 0) || (output_starts && !history_lens))
+    return MT_ERR_INVALID_ARG;
+  if ((bias_tokens == nullptr) != (bias_values == nullptr) || (mask_index && !mask) || (tree_parents && !tree_tokens))
+    return MT_ERR_INVALID_ARG;
+  if (mask && !mask_index && d->num_masks < rows) return MT_ERR_INVALID_ARG;
+  if (tree_tokens && d->tree_size > kMaxTree) return MT_ERR_UNSUPPORTED;
+  if (rows == 0) return MT_OK;
+  const size_t eb = (size_t)act_bytes(d->dtype);
+  if (!logits || !out || !status_ws || reinterpret_cast<uintptr_t>(logits) % eb ||
+      reinterpret_cast<uintptr_t>(out) % eb || !aligned16(status_ws))
+    return MT_ERR_INVALID_ARG;
+  // rows of `out` apart from one another, and `out` the logits themselves or apart from them
+  const long long b1 = d->batch - 1, t1 = d->tree_size - 1, v = d->vocab;
+  const long long* st = d->out_stride;
+  if ((t1 && st[1] < v) || (b1 && st[0] < v) ||
+      (t1 && b1 && st[0] < t1 * st[1] + v && st[1] < b1 * st[0] + v))
+    return MT_ERR_INVALID_ARG;
+  const size_t in_bytes = (size_t)(b1 * d->stride[0] + t1 * d->stride[1] + v) * eb;
+  const size_t out_bytes = (size_t)(b1 * st[0] + t1 * st[1] + v) * eb;
+  const bool same = logits == out && (!b1 || d->stride[0] == st[0]) && (!t1 || d->stride[1] == st[1]);
+  if (!same && overlap(logits, in_bytes, out, out_bytes)) return MT_ERR_INVALID_ARG;
+  LogitsParams p{};
+  p.B = d->batch; p.T = d->tree_size; p.V = d->vocab;
+  p.logits = logits; p.out = out;
+  for (int i = 0; i < 2; ++i) {
+    p.stride[i] = d->stride[i];
+    p.out_stride[i] = d->out_stride[i];
+  }
+  p.history = history; p.history_lens = history_lens; p.history_width = history ? d->history_width : 0;
+  p.output_starts = output_starts;
+  p.repetition = repetition; p.presence = presence; p.frequency = frequency;
+  p.bias_tokens = bias_tokens; p.bias_values = bias_values; p.num_bias = bias_tokens ? d->num_bias : 0;
+  p.mask = mask; p.num_masks = mask ? d->num_masks : 0; p.mask_index = mask_index;
+  p.tree_tokens = tree_tokens; p.tree_parents = tree_parents;
+  p.status = static_cast<int*>(status_ws);
+  return cuda_status(launch_logits(p, d->dtype, stream));
+}
+
 int mt_sample_tokens(int num_rows, int vocab, mt_dtype logits_dtype, const void* logits, int num_logit_rows,
                      long long row_stride, const int32_t* row_index, const float* uniforms, const float* temperature,
                      const int32_t* top_k, const float* top_p, const float* min_p, int32_t* tokens,

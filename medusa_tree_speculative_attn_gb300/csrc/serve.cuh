@@ -427,6 +427,33 @@ struct EvictParams {
 cudaError_t launch_kv_evict(const EvictParams& p, cudaStream_t stream);
 
 // ---------------------------------------------------------------------------
+// Penalties, biases and masks on logits.
+// ---------------------------------------------------------------------------
+struct LogitsParams {
+  int B, T, V;
+  const void* logits;
+  void* out;
+  long long stride[2], out_stride[2];  // (sequence, row) in elements
+  const int* history;  // [B][history_width]
+  int history_width;
+  const int* history_lens;   // [B], or null: no history
+  const int* output_starts;  // [B] or null
+  const float* repetition;   // [B] or null, each
+  const float* presence;
+  const float* frequency;
+  const int* bias_tokens;  // [B][num_bias]
+  const float* bias_values;
+  int num_bias;
+  const int* mask;  // [num_masks][ceil(V / 32)] or null
+  int num_masks;
+  const int* mask_index;    // [B][T], or null: a mask for each row
+  const int* tree_tokens;   // [B][T] or null
+  const int* tree_parents;  // [B][T], or null: a chain
+  int* status;
+};
+cudaError_t launch_logits(const LogitsParams& p, int dtype, cudaStream_t stream);
+
+// ---------------------------------------------------------------------------
 // Sampling.
 // ---------------------------------------------------------------------------
 // Largest vocab: that many weights of 2^44 (the maximum's) stay below 2^63, and an

@@ -146,3 +146,47 @@ def evict(kind, caches, scales, weights, table, lens, new_tables, budget, sinks,
                         scales[x][to, h] = top
                     caches[x][to, h, :m] = block
     return kept
+
+
+def logits64(x, history, lens, starts, rep, pres, freq, bias, mask, mask_index, tokens, parents):
+    """(logits [B][T][V] in 64 bits after the call, magnitudes that entered each, which were touched).  history [B][H] or
+    None; bias: (tokens, values) or None; mask: truth values [M][V] or None; a sequence of negative length is left."""
+    out = np.array(x, np.float64)
+    b, t, v = out.shape
+    mag, touched = np.abs(out), np.zeros(out.shape, bool)
+    for i in range(b):
+        n = 0 if lens is None else int(lens[i])
+        if n < 0:
+            continue
+        words = [] if history is None else [int(w) for w in history[i][:min(n, len(history[i]))]]
+        start = 0 if starts is None else int(starts[i])
+        for a in range(t):
+            path = [] if tokens is None else [int(tokens[i][j]) for j in _chain(None if parents is None else parents[i], a)]
+            count = {}
+            for w in words[max(start, 0):] + path:
+                count[w] = count.get(w, 0) + 1
+            for w in set(words) | set(path):
+                if not 0 <= w < v:
+                    continue
+                y = out[i, a, w]
+                if rep is not None:
+                    y = y / float(rep[i]) if y > 0 else y * float(rep[i])
+                m = max(abs(out[i, a, w]), abs(y))
+                c = count.get(w, 0)
+                if c and freq is not None:
+                    y, m = y - float(freq[i]) * c, m + abs(float(freq[i])) * c
+                if c and pres is not None:
+                    y, m = y - float(pres[i]), m + abs(float(pres[i]))
+                out[i, a, w], mag[i, a, w], touched[i, a, w] = y, m, True
+            if bias is not None:
+                for w, y in {int(w): float(y) for w, y in zip(bias[0][i], bias[1][i])}.items():
+                    if 0 <= w < v:
+                        out[i, a, w] += y
+                        mag[i, a, w] += abs(y)
+                        touched[i, a, w] = True
+            if mask is not None:
+                m = i * t + a if mask_index is None else int(mask_index[i][a])
+                if m >= 0:
+                    no = ~mask[m] if m < len(mask) else np.ones(v, bool)
+                    out[i, a, no], mag[i, a, no], touched[i, a, no] = -np.inf, 0.0, True
+    return out, mag, touched

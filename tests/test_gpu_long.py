@@ -533,3 +533,199 @@ def test_evict_far_pages(kind):
             p, rows = int(e.new[b, j // P]), min(P, m - j)
             for x, y in zip(big, (c.k, c.v, e.w)):
                 assert torch.equal(x[far + p, :, :rows].view(torch.uint8), y[p, :, :rows].view(torch.uint8))
+
+
+# ---- logits ----------------------------------------------------------------------
+
+def _logits_case(rng, b, t, v, dtype, history=0, bias=0, masks=0, tree="tree", per_row=False):
+    """Inputs on the host; every kind of token id out of the vocabulary among them."""
+    c = dict(x=_rand(rng, b, t, v, dtype=DT[dtype], scale=4.0), history=None, lens=None, starts=None, rep=None, pres=None, freq=None, bias=None, mask=None,
+             index=None, tokens=None, parents=None)
+    few = lambda *shape: np.minimum((v ** rng.random(shape)).astype(np.int64), v - 1)  # noqa: E731
+    if history:
+        c["history"] = np.where(rng.random((b, history)) < 0.05, rng.choice([-1, v, -2 ** 31, 2 ** 31 - 1], (b, history)), few(b, history))
+        c["lens"], c["starts"] = rng.integers(0, history + 5, b), rng.integers(-2, history, b)
+        c["rep"], c["pres"], c["freq"] = (rng.choice(a, b).astype(np.float32) for a in ([1.0, 1.3, 0.8], [0.0, 0.7, -0.4], [0.0, 0.31, -0.2]))
+    if bias:
+        c["bias"] = np.where(rng.random((b, bias)) < 0.2, rng.choice([-1, v], (b, bias)), few(b, bias)), (3 * rng.standard_normal((b, bias))).astype(np.float32)
+    if masks:
+        n = b * t if per_row else masks
+        c["mask"] = rng.random((n, v)) < rng.choice([0.0, 0.01, 0.5, 0.99, 1.0], (n, 1))
+        c["index"] = None if per_row else rng.integers(-1, masks + 1, (b, t))
+    if tree:
+        c["tokens"] = np.where(rng.random((b, t)) < 0.1, rng.choice([-1, v], (b, t)), few(b, t))
+        c["parents"] = None if tree == "chain" else np.array([[-1] + [int(rng.integers(max(0, j - 9), j)) for j in range(1, t)] for _ in range(b)])
+    return c
+
+
+def _bits(mask):
+    pad = np.pad(mask, ((0, 0), (0, -mask.shape[1] % 32)))
+    return torch.from_numpy(np.packbits(pad, axis=1, bitorder="little").view(np.int32).copy()).cuda()
+
+
+def _logits_kw(c, ws, two=False):
+    i32 = lambda x: None if x is None else _i32(x).cuda()  # noqa: E731
+    f32 = lambda x: None if x is None else torch.from_numpy(x).cuda()  # noqa: E731
+    flat = lambda x: x if x is None or not two else x[:, 0]  # noqa: E731
+    return dict(history=i32(c["history"]), history_lens=i32(c["lens"]), output_starts=i32(c["starts"]), repetition=f32(c["rep"]), presence=f32(c["pres"]), frequency=f32(c["freq"]),
+                bias_tokens=i32(c["bias"] and c["bias"][0]), bias_values=f32(c["bias"] and c["bias"][1]), mask=None if c["mask"] is None else _bits(c["mask"]),
+                mask_index=flat(i32(c["index"])), tree_tokens=flat(i32(c["tokens"])), tree_parents=flat(i32(c["parents"])), status_ws=ws)
+
+
+def _logits_check(c, got, left=None):
+    """`left`: what rows without a sequence hold."""
+    x = c["x"]
+    want, mag, touched = lref.logits64(x.double().numpy(), c["history"], c["lens"], c["starts"], c["rep"], c["pres"], c["freq"], c["bias"], c["mask"], c["index"], c["tokens"],
+                                       c["parents"])
+    got = got.cpu()
+    live = torch.from_numpy(np.array([c["lens"] is None or n >= 0 for n in (c["lens"] if c["lens"] is not None else [0] * len(x))]))
+    same = torch.from_numpy(~touched) & live[:, None, None]
+    raw = {4: torch.int32, 2: torch.int16}[x.element_size()]
+    assert torch.equal(got.view(raw)[same], x.view(raw)[same])  # untouched entries keep their bits
+    y, lost = got.double().numpy(), np.isneginf(want)
+    assert np.array_equal(np.isneginf(y)[live.numpy()], lost[live.numpy()])
+    fine = touched & ~lost & live.numpy()[:, None, None]
+    # the rounding at the end and four in 32 bits before it
+    tol = ref.HALF_STEP[x.dtype] * np.abs(want) + 4 * 2.0 ** -24 * mag + (2.0 ** -25 if x.dtype == torch.float16 else 0)
+    bad = np.abs(y - np.where(lost, 0, want)) > tol
+    assert not bad[fine].any(), np.argwhere(bad & fine)[:4]
+    if left is not None:
+        assert torch.equal(got[~live], left.cpu()[~live])
+
+
+LOGITS = [  # B, T, V, history, bias, masks, tree
+    (1, 1, 1, 3, 0, 0, None), (1, 1, 33, 10, 5, 2, None), (3, 1, 1000, 100, 0, 0, None), (2, 5, 4097, 700, 30, 3, "tree"), (1, 64, 1003, 50, 9, 0, "tree"),
+    (2, 64, 32000, 2000, 0, 9, "tree"), (4, 3, 8192, 0, 0, 4, "chain"), (5, 1, 32001, 3000, 50, 0, "chain"), (2, 100, 500, 20, 4, 3, None), (1, 1, 200000, 5000, 300, 1, None),
+    (300, 1, 70, 9, 3, 8, None), (2, 7, 12345, 40, 0, 2, "chain"),
+]
+
+
+@pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("in_place", [False, True])
+@pytest.mark.parametrize("case", range(len(LOGITS)))
+def test_logits(dtype, in_place, case):
+    b, t, v, history, bias, masks, tree = LOGITS[case]
+    c = _logits_case(np.random.default_rng(4000 + case), b, t, v, dtype, history, bias, masks, tree)
+    x, ws = c["x"].cuda(), _status()
+    out = x if in_place else torch.full_like(x, 7.0)
+    assert mt.process_logits(x, out, **_logits_kw(c, ws)) is out and mt.read_status(ws) == 0
+    _logits_check(c, out)
+    if not in_place:
+        assert torch.equal(x.cpu(), c["x"])
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_logits_each_part_alone_and_nothing(dtype):
+    rng = np.random.default_rng(60)
+    full = _logits_case(rng, 3, 4, 999, dtype, 60, 10, 3, "tree")
+    keep = {"x": full["x"]}
+    for names in ((), ("rep", "history", "lens"), ("pres", "history", "lens"), ("freq", "history", "lens", "starts"), ("bias",), ("mask", "index"), ("tokens", "parents", "freq"),
+                  ("tokens", "rep"), ("history", "lens")):
+        c = {k: None for k in full} | keep | {n: full[n] for n in names}
+        for in_place in (False, True):
+            x, ws = c["x"].cuda(), _status()
+            out = x if in_place else torch.full_like(x, 7.0)
+            mt.process_logits(x, out, **_logits_kw(c, ws))
+            assert mt.read_status(ws) == 0
+            _logits_check(c, out)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "f16"])
+@pytest.mark.parametrize("shift, out_shift", [(0, 0), (1, 1), (3, 0), (0, 5), (2, 3)])
+def test_logits_strides_and_alignment(dtype, shift, out_shift):
+    rng = np.random.default_rng(61)
+    c = _logits_case(rng, 3, 2, 501, dtype, 60, 10, 3, "chain", per_row=True)
+    wide, to = torch.full((3, 5, 600), 9.0, dtype=DT[dtype], device="cuda"), torch.full((3, 3, 611), 9.0, dtype=DT[dtype], device="cuda")
+    x, out = wide[:, 1::2, shift:shift + 501], to[:, :2, out_shift:out_shift + 501]
+    x.copy_(c["x"])
+    ws, kw = _status(), None
+    kw = _logits_kw(c, ws)
+    mt.process_logits(x, out, **kw)
+    _logits_check(c, out)
+    rest = to.clone()
+    rest[:, :2, out_shift:out_shift + 501] = 9.0
+    assert bool((rest == 9.0).all())  # nothing beside the rows
+    mt.process_logits(x, x, **kw)
+    _logits_check(c, x)
+    both = torch.empty(2, 3, 501, dtype=DT[dtype], device="cuda").transpose(0, 1)  # rows of a sequence far apart
+    mt.process_logits(both.copy_(c["x"]), both, **kw)
+    _logits_check(c, both)
+    one = torch.empty(3, 2, 501, dtype=DT[dtype], device="cuda")
+    mt.process_logits(c["x"][:1, :1].cuda().expand(3, 2, 501), one, status_ws=ws)  # one row read by all
+    assert torch.equal(one.cpu(), c["x"][:1, :1].expand(3, 2, 501)) and mt.read_status(ws) == 0
+
+
+def test_logits_two_dims_and_places_without_a_sequence():
+    rng = np.random.default_rng(62)
+    c = _logits_case(rng, 5, 1, 777, "bf16", 40, 4, 3, None)
+    c["lens"] = np.array([30, -1, 0, 45, -7])
+    x, ws = c["x"].cuda(), _status()
+    out = torch.full((5, 777), 7.0, dtype=torch.bfloat16, device="cuda")
+    mt.process_logits(x[:, 0], out, **_logits_kw(c, ws, two=True))
+    _logits_check(c, out[:, None], left=torch.full_like(x, 7.0))
+    y = x.clone()
+    mt.process_logits(y, y, **_logits_kw(c, ws))
+    _logits_check(c, y, left=x)
+    assert mt.read_status(ws) == 0
+
+
+@pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
+def test_logits_infinities_and_nan(dtype):
+    x = torch.tensor([[float("nan"), float("inf"), float("-inf"), 0.0, -0.0, 65504.0 if dtype == "f16" else 3e38, 1.0, -1.0] * 2], dtype=DT[dtype])
+    history, ws = _i32([[0, 1, 2, 3, 4, 5, 6, 7]]).cuda(), _status()
+    f = lambda a: torch.tensor([a], device="cuda")  # noqa: E731
+    out = torch.empty_like(x).cuda()
+    mt.process_logits(x.cuda(), out, history=history, history_lens=_i32([8]).cuda(), repetition=f(2.0), presence=f(0.5), frequency=f(0.25), status_ws=ws)
+    y = x.float()[0, :8]
+    want = torch.where(y > 0, y / 2, y * 2) - 0.25 - 0.5
+    assert torch.equal(out[0, :8].cpu().isnan(), want.isnan()) and torch.equal(out[0, 1:8].cpu(), want[1:].to(x.dtype))
+    assert torch.equal(out[0, 8:].cpu().nan_to_num(9), x[0, 8:].nan_to_num(9))
+    none = torch.zeros(1, 1, dtype=torch.int32, device="cuda")
+    mt.process_logits(x.cuda(), out, mask=none, mask_index=_i32([0]).cuda(), status_ws=ws)  # a NaN is masked like the rest
+    assert bool((out == float("-inf")).all())
+    mt.process_logits(x.cuda(), out, history=torch.empty(1, 0, dtype=torch.int32, device="cuda"), history_lens=_i32([3]).cuda(), status_ws=ws)
+    assert torch.equal(out.cpu().nan_to_num(9), x.nan_to_num(9)) and mt.read_status(ws) == 0
+
+
+def test_logits_of_a_bad_tree():
+    c = _logits_case(np.random.default_rng(63), 2, 4, 300, "f32", 10, 0, 0, "tree")
+    c["parents"][1] = [-1, 0, 2, 9]
+    x, ws = c["x"].cuda(), _status()
+    out = torch.empty_like(x)
+    mt.process_logits(x, out, **_logits_kw(c, ws))
+    assert mt.read_status(ws) == -3
+    c["parents"][1] = [-1, 0, -1, -1]
+    _logits_check(c, out)
+
+
+def test_logits_in_a_graph_on_another_stream_and_the_same_twice():
+    c = _logits_case(np.random.default_rng(64), 2, 6, 32000, "bf16", 500, 20, 3, "tree")
+    x, ws = c["x"].cuda(), _status()
+    kw, out = _logits_kw(c, ws), torch.empty_like(x)
+    mt.process_logits(x, out, **kw)
+    want = out.clone()
+    g = _graph(lambda: mt.process_logits(x, out, **kw))
+    out.zero_()
+    g.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(out, want)
+    other, s = torch.empty_like(x), torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    mt.process_logits(x, other, stream=s, **kw)
+    s.synchronize()
+    assert torch.equal(other, want)
+
+
+def test_logits_far_rows():
+    v, rows = 500000, 4500  # elements past 2^31
+    x = torch.empty(rows, v, dtype=torch.float16, device="cuda")
+    x[-1] = torch.arange(v, device="cuda") % 1000
+    lens, ws = torch.full((rows,), -1, dtype=torch.int32, device="cuda"), _status()
+    lens[-1] = 2
+    history = torch.zeros(rows, 2, dtype=torch.int32, device="cuda")
+    history[-1] = _i32([499999, 5]).cuda()
+    before = x[-1].clone()
+    mt.process_logits(x, x, history=history, history_lens=lens, presence=torch.ones(rows, device="cuda"), status_ws=ws)
+    before[499999] -= 1
+    before[5] -= 1
+    assert torch.equal(x[-1], before) and mt.read_status(ws) == 0

@@ -150,3 +150,54 @@ def test_the_binding_refuses_evictions_that_do_not_fit():
         with pytest.raises(mt.MedusaTreeError):
             call(**kw)
     torch.cuda.synchronize()
+
+
+# ---- logits ----
+
+def _logits_desc(**kw):
+    base = dict(batch=2, tree_size=4, vocab=100, dtype=2, history_width=8, num_bias=3, num_masks=2, stride=(400, 100), out_stride=(400, 100))
+    return ctypes.byref(mt.LogitsDesc(**{**base, **kw}))
+
+
+@pytest.mark.parametrize("desc, want", [
+    (dict(batch=-1), INVALID), (dict(tree_size=-1), INVALID), (dict(vocab=0), INVALID), (dict(vocab=(1 << 30) + 1), UNSUPPORTED), (dict(dtype=3), UNSUPPORTED),
+    (dict(history_width=-1), INVALID), (dict(history_width=1 << 30), INVALID), (dict(num_bias=-1), INVALID), (dict(num_masks=-1), INVALID), (dict(stride=(-400, 100)), INVALID),
+    (dict(out_stride=(400, 99)), INVALID), (dict(out_stride=(399, 100)), INVALID), (dict(out_stride=(0, 100)), INVALID), (dict(out_stride=(150, 200)), INVALID),
+    (dict(tree_size=65, stride=(6500, 100), out_stride=(6500, 100)), UNSUPPORTED), (dict(batch=1 << 24), INVALID), (dict(batch=0), OK), (dict(tree_size=0), OK),
+    (dict(stride=(800, 100)), INVALID),  # the same place under other strides
+])
+def test_logits_sizes(lib, desc, want):  # noqa: F811
+    assert lib.mt_process_logits(_logits_desc(**desc), *[PTR] * 15, None) == want
+
+
+def test_logits_pointers(lib):  # noqa: F811
+    names = "logits out history lens starts rep pres freq bias_tokens bias_values mask index tokens parents status".split()
+    at = {n: (i + 1) << 32 for i, n in enumerate(names)}
+    call = lambda **kw: lib.mt_process_logits(_logits_desc(), *{**at, **kw}.values(), None)  # noqa: E731
+    for kw in (dict(logits=None), dict(out=None), dict(status=None), dict(logits=PTR + 1), dict(out=PTR + 1), dict(status=ODD), dict(history=None), dict(lens=None, starts=None),
+               dict(history=None, lens=None), dict(bias_tokens=None), dict(bias_values=None), dict(mask=None), dict(index=None), dict(tokens=None)):
+        assert call(**kw) == INVALID, kw
+    for shift in (2, 1598, -2, -1598):  # out over a part of the logits
+        assert call(out=at["logits"] + shift) == INVALID
+    assert lib.mt_process_logits(None, *at.values(), None) == INVALID
+
+
+@pytest.mark.gpu
+def test_the_binding_refuses_logits_that_do_not_fit():
+    cu = lambda *s, dtype=torch.float32: torch.zeros(*s, dtype=dtype, device="cuda")  # noqa: E731
+    i32 = lambda *s: cu(*s, dtype=torch.int32)  # noqa: E731
+    x = cu(2, 3, 50)
+    call = lambda **kw: mt.process_logits(**{**dict(logits=x, out=cu(2, 3, 50), history=i32(2, 9), history_lens=i32(2), output_starts=i32(2), repetition=cu(2) + 1,  # noqa: E731
+                                                    presence=cu(2), frequency=cu(2), bias_tokens=i32(2, 4), bias_values=cu(2, 4), mask=i32(5, 2), mask_index=i32(2, 3),
+                                                    tree_tokens=i32(2, 3), tree_parents=i32(2, 3) - 1, status_ws=cu(64)), **kw})
+    call()
+    for kw in (dict(logits=x.double()), dict(logits=x[0, 0]), dict(logits=x.cpu()), dict(out=x[:1]), dict(out=x.half()), dict(out=None), dict(out=cu(2, 50, 3).transpose(1, 2)),
+               dict(history=i32(2)), dict(history=None), dict(history_lens=None), dict(history_lens=i32(3)), dict(output_starts=cu(2)), dict(repetition=cu(3)), dict(presence=cu(2).double()),
+               dict(frequency=[0.0, 0.0]), dict(bias_tokens=i32(2, 3)), dict(bias_values=None), dict(mask=i32(5, 1)), dict(mask=i32(10)), dict(mask_index=i32(6)), dict(tree_tokens=i32(2, 4)),
+               dict(tree_parents=i32(2, 2)), dict(status_ws=cu(8))):
+        with pytest.raises((ValueError, TypeError)):
+            call(**kw)
+    for kw in (dict(out=cu(1, 3, 50).expand(2, 3, 50)), dict(mask=None), dict(mask_index=None), dict(tree_tokens=None), dict(history=None, history_lens=None)):
+        with pytest.raises(mt.MedusaTreeError):
+            call(**kw)
+    torch.cuda.synchronize()
