@@ -10,8 +10,10 @@
 // As in attn_block8.cu the keys are the 16-row side of m16n8k16 products in fp16 (every E4M3
 // code is exact there, and a query scaled to a power of two keeps its bits), converted in
 // registers; a lane takes 16 consecutive bytes of a key row as four k-steps, and the queries
-// lie in shared memory in that order, one 16-byte read for two k-steps.  A warp takes pages
-// of its own, four in flight, and a slot's sum over rows is two shuffles at the end.
+// lie in shared memory in that order, one 16-byte read for two k-steps.  Persistent CTAs walk
+// the balanced schedule of 64-slot tiles; a warp takes a page of each and brings the pages,
+// with their old weights, into a ring of its own.  A slot's sum over rows is two shuffles.
+#include <atomic>
 #include <cmath>
 
 #include "serve.cuh"
@@ -23,8 +25,26 @@ namespace {
 constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
 constexpr int kP = 16;
-constexpr int kFlight = 4;     // pages a warp keeps in flight
 constexpr int kMaxRows = 256;  // query rows in shared memory at a time
+constexpr int kMaxDevices = 64;
+
+template <int D>
+struct Cfg {
+  static constexpr int CTAS = 4;   // per SM
+  static constexpr int DEPTH = 6;  // pages a warp keeps in flight
+  static constexpr int kKeys = kP * D;
+  static constexpr int kSlot = kKeys + kP * 4;  // a page's keys and old weights
+  static constexpr int kRing = kWarps * DEPTH * kSlot;
+};
+
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
 
 __device__ __forceinline__ void mma(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
   asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
@@ -45,141 +65,167 @@ __device__ __forceinline__ uint32_t pack_h2(float a, float b) {
   return r;
 }
 
-// A page as one lane holds it: 16-byte chunks ch * 4 + tig of rows gid and gid + 8, and (of
-// the lanes with tig 0) those slots' weights before the call.
+// Byte offset of 16-byte chunk ch of key row r in a slot: permuted so that the fragment
+// reads (eight lanes a phase: two rows of four chunks) hit distinct banks.
 template <int D>
-struct Page {
-  uint4 k[D / 64][2];
-  float old[2];
-};
+__device__ __forceinline__ int k_off(int r, int ch) {
+  return r * D + ((D == 128 ? ch ^ ((r & 1) << 2) : ch) << 4);
+}
 
 template <typename T, int D>
-__global__ void __launch_bounds__(kThreads) kv_weights_kernel(const WeightsParams p, int chunks, int per_warp) {
-  constexpr int NC = D / 64;
-  extern __shared__ __align__(16) uint8_t smem[];
-  uint4* s_q = reinterpret_cast<uint4*>(smem);  // [tile of 8 rows][chunk][half][lane]
+__global__ void __launch_bounds__(kThreads, Cfg<D>::CTAS) kv_weights_kernel(const WeightsParams p, const Sched sched) {
+  using C = Cfg<D>;
+  constexpr int NC = D / 64, DEPTH = C::DEPTH;
+  extern __shared__ __align__(128) uint8_t smem[];
   const int most = min(kMaxRows, (p.rows + 7) & ~7);
-  float2* s_row = reinterpret_cast<float2*>(smem + (size_t)most * D * 2);  // score -> base 2, lse in base 2
+  uint4* s_q = reinterpret_cast<uint4*>(smem + C::kRing);                   // [tile of 8 rows][chunk][half][lane]
+  float2* s_row = reinterpret_cast<float2*>(smem + C::kRing + most * D * 2);  // score -> base 2, lse in base 2
+  int* s_pfx = reinterpret_cast<int*>(s_row + most);                        // [B + 1]
+  __shared__ int s_warp[kWarps];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, gid = lane >> 2, tig = lane & 3;
-  const int h = blockIdx.x % p.Hkv, chunk = blockIdx.x / p.Hkv % chunks, b = blockIdx.x / p.Hkv / chunks;
   pdl_wait();
-  const int L = p.seq_lens[b];
-  if ((long long)L > (long long)p.max_blocks * kP) {
-    if (chunk == 0 && threadIdx.x == 0) set_status(p.status, kStPages);
-    return;
-  }
-  const int npages = (max(L, 0) + kP - 1) / kP;
-  const int first = chunk * per_warp * kWarps + warp;  // this warp's pages: first, first + 4, ...
-  if (chunk * per_warp * kWarps >= npages) return;
-  int nodes = p.T;
-  const int* path = nullptr;
-  if (p.accept_path) {
-    path = p.accept_path + (size_t)b * (p.max_depth + 1);
-    nodes = p.accept_len[b] + 1;
-    bool stray = nodes < 1 || nodes > p.max_depth + 1;
-    if (!stray)
-      for (int i = lane; i < nodes; i += 32) stray = stray || (unsigned)path[i] >= (unsigned)p.T;
-    if (__any_sync(0xffffffffu, stray)) {  // the same in every warp
-      if (threadIdx.x == 0) set_status(p.status, kStPages);
-      return;
+  AttnParams a{};  // the tiles of the cached slots alone
+  a.B = p.B;
+  a.T = 0;
+  a.max_blocks = p.max_blocks;
+  a.seq_lens = p.seq_lens;
+  a.status = p.status;
+  block8_prefix<kWarps>(a, s_pfx, s_warp, blockIdx.x == 0);
+  Sched sc = sched;
+  sc.tile_pfx = s_pfx;
+  PieceIter it;
+  it.init(sc, blockIdx.x);
+  uint8_t* ring = smem + warp * (DEPTH * C::kSlot);
+  const uint32_t ring_u = static_cast<uint32_t>(__cvta_generic_to_shared(ring));
+  Piece pc;
+  while (it.next(pc)) {  // every thread walks with the same values
+    const int b = pc.b, h = pc.kvh;
+    const int L = p.seq_lens[b], npages = (L + kP - 1) / kP;
+    int nodes = p.T;
+    const int* path = nullptr;
+    if (p.accept_path) {
+      path = p.accept_path + (size_t)b * (p.max_depth + 1);
+      nodes = p.accept_len[b] + 1;
+      bool stray = nodes < 1 || nodes > p.max_depth + 1;
+      if (!stray)
+        for (int i = lane; i < nodes; i += 32) stray = stray || (unsigned)path[i] >= (unsigned)p.T;
+      if (__any_sync(0xffffffffu, stray)) {  // the same in every warp
+        if (threadIdx.x == 0) set_status(p.status, kStPages);
+        continue;
+      }
     }
-  }
-  const int rows = nodes * p.g;
-  const int mine = min(per_warp, (npages - first + kWarps - 1) / kWarps);  // perhaps below 1
-  const int* bt = p.block_tables + (size_t)b * p.max_blocks;
-  const int prev = p.prev_lens ? p.prev_lens[b] : L;
-
-  for (int r0 = 0; r0 < rows; r0 += kMaxRows) {
-    const int n = min(kMaxRows, rows - r0), tiles = (n + 7) / 8;
-    const float* before = r0 == 0 ? p.weights : p.out;  // later rows add to what the earlier ones left
-    const float decay = r0 == 0 ? p.decay : 1.f;
-    // ids and key scales of 32 pages, a lane each (per_warp <= 32)
-    const int id = lane < mine ? bt[first + lane * kWarps] : -1;
-    const bool good = id >= 0 && id < p.num_pages;
-    const float ks = good ? __ldg(p.k_scales + (size_t)id * p.Hkv + h) : 0.f;
-    if (lane < mine && !good) set_status(p.status, kStPages);
-    auto load = [&](Page<D>& x, int i) {
-      const int pg = __shfl_sync(0xffffffffu, good ? id : -1, i & 31);
-      if (i >= mine || pg < 0) return;
-      const size_t at = (size_t)pg * p.Hkv + h;
-      const uint8_t* k = static_cast<const uint8_t*>(p.k_cache) + at * kP * D;
+    const int rows = nodes * p.g, prev = p.prev_lens ? p.prev_lens[b] : L;
+    // this warp's pages: first + 4 i
+    const int first = 4 * pc.tile_begin + warp;
+    const int mine = min(pc.tile_end - pc.tile_begin, max(0, (npages - first + kWarps - 1) / kWarps));
+    const int* bt = p.block_tables + (size_t)b * p.max_blocks;
+    for (int r0 = 0; r0 < rows; r0 += kMaxRows) {
+      const int n = min(kMaxRows, rows - r0), tiles = (n + 7) / 8;
+      const float* before = r0 == 0 ? p.weights : p.out;  // later rows add to what the earlier ones left
+      const int had = r0 == 0 ? prev : L;
+      const float decay = r0 == 0 ? p.decay : 1.f;
+      // page ids and scales of 32 pages, a lane each; the next 32 ids are fetched while
+      // these are used, their scales half way
+      auto fetch_id = [&](int i) { return i < mine ? bt[first + 4 * i] : -1; };
+      auto fetch_scale = [&](int id) {
+        return id >= 0 && id < p.num_pages ? __ldg(p.k_scales + (size_t)id * p.Hkv + h) : 0.f;
+      };
+      int id_cur = fetch_id(lane), id_nxt = -1, id_iss = id_cur, iss_base = 0;
+      float ks_cur = fetch_scale(id_cur), ks_nxt = 0.f;
+      auto issue = [&](int i) {
+        if (i < mine) {
+          if (i - iss_base >= 32) {
+            iss_base += 32;
+            id_iss = id_nxt;
+          }
+          const int id = __shfl_sync(0xffffffffu, id_iss, i - iss_base);
+          if (id >= 0 && id < p.num_pages) {
+            const size_t page = (size_t)id * p.Hkv + h;
+            const uint8_t* src = static_cast<const uint8_t*>(p.k_cache) + page * C::kKeys;
+            const uint32_t dst = ring_u + (i % DEPTH) * C::kSlot;
+            constexpr int CPR = D / 16;  // chunks per row
 #pragma unroll
-      for (int c = 0; c < NC; ++c)
+            for (int x = 0; x < kP * CPR / 32; ++x) {
+              const int q = x * 32 + lane;
+              cp_async16(dst + k_off<D>(q / CPR, q % CPR), src + q * 16);
+            }
+            if (lane < 4 && (first + 4 * i) * kP < had) cp_async16(dst + C::kKeys + lane * 16, before + page * kP + lane * 4);
+          }
+        }
+        cp_commit();
+      };
 #pragma unroll
-        for (int r = 0; r < 2; ++r)
-          x.k[c][r] = __ldg(reinterpret_cast<const uint4*>(k + (gid + 8 * r) * D + (c * 4 + tig) * 16));
-      if (tig == 0) {
+      for (int i = 0; i < DEPTH - 1; ++i) issue(i);
+      // the queries: a warp eight rows, lanes as they multiply
+      __syncthreads();  // those of the piece before are no longer read
+      for (int t = warp; t < tiles; t += kWarps) {
+        const int row = t * 8 + gid;
+        Row8<T> raw[2 * NC];
 #pragma unroll
-        for (int r = 0; r < 2; ++r) {
-          const int slot = (first + i * kWarps) * kP + gid + 8 * r;
-          x.old[r] = slot < (r0 == 0 ? prev : L) ? before[at * kP + gid + 8 * r] * decay : 0.f;
+        for (int x = 0; x < 2 * NC; ++x) raw[x].zero();
+        float l2 = INFINITY;
+        if (row < n) {
+          const int at = (r0 + row) / p.g, node = path ? path[at] : at, head = h * p.g + (r0 + row) % p.g;
+          const size_t q = ((size_t)b * p.T + node) * p.Hq + head;
+#pragma unroll
+          for (int x = 0; x < 2 * NC; ++x)
+            raw[x].load(static_cast<const T*>(p.q) + q * D + (x / 2) * 64 + tig * 16 + (x % 2) * 8);
+          l2 = p.lse[q] * 1.4426950408889634f;
+        }
+        AbsMax<T> top;
+#pragma unroll
+        for (int x = 0; x < 2 * NC; ++x) top.add(raw[x]);
+        float amax = top.get();
+        amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+        amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+        // 2^8 <= scaled maximum < 2^9: a bf16 keeps its bits down to 2^-25 of it, an fp16 to 2^-22
+        const int ex = amax > 0.f ? (int)(__float_as_uint(amax) >> 23) - 127 : 0;
+        const int k = min(max(8 - ex, -120), 120);
+        const float f2 = __uint_as_float((uint32_t)(127 + k) << 23);
+        const float c = amax < INFINITY ? p.scale_log2 * __uint_as_float((uint32_t)(127 - k) << 23)
+                                        : __int_as_float(0x7fffffff);
+        if (tig == 0) s_row[row] = make_float2(row < n ? c : 0.f, l2);
+#pragma unroll
+        for (int x = 0; x < 2 * NC; ++x) {  // 8 columns: two k-steps of four
+          float f[8];
+          raw[x].to_f(f);
+          s_q[(t * 2 * NC + x) * 32 + lane] = make_uint4(pack_h2(f[0] * f2, f[1] * f2), pack_h2(f[2] * f2, f[3] * f2),
+                                                         pack_h2(f[4] * f2, f[5] * f2), pack_h2(f[6] * f2, f[7] * f2));
         }
       }
-    };
-    Page<D> ring[kFlight];
-#pragma unroll
-    for (int u = 0; u < kFlight; ++u) load(ring[u], u);
-    // the queries: a warp a row of 8, lanes as they multiply
-    if (r0 > 0) __syncthreads();
-    for (int t = warp; t < tiles; t += kWarps) {
-      const int row = t * 8 + gid;
-      Row8<T> raw[2 * NC];
-#pragma unroll
-      for (int x = 0; x < 2 * NC; ++x) raw[x].zero();
-      float l2 = INFINITY;
-      if (row < n) {
-        const int at = (r0 + row) / p.g, node = path ? path[at] : at, head = h * p.g + (r0 + row) % p.g;
-        const size_t q = ((size_t)b * p.T + node) * p.Hq + head;
-#pragma unroll
-        for (int x = 0; x < 2 * NC; ++x)
-          raw[x].load(static_cast<const T*>(p.q) + q * D + (x / 2) * 64 + tig * 16 + (x % 2) * 8);
-        l2 = p.lse[q] * 1.4426950408889634f;
-      }
-      AbsMax<T> top;
-#pragma unroll
-      for (int x = 0; x < 2 * NC; ++x) top.add(raw[x]);
-      float amax = top.get();
-      amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
-      amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
-      // 2^8 <= scaled maximum < 2^9: a bf16 keeps its bits down to 2^-25 of it, an fp16 to 2^-22
-      const int ex = amax > 0.f ? (int)(__float_as_uint(amax) >> 23) - 127 : 0;
-      const int k = min(max(8 - ex, -120), 120);
-      const float f2 = __uint_as_float((uint32_t)(127 + k) << 23);
-      const float c = amax < INFINITY ? p.scale_log2 * __uint_as_float((uint32_t)(127 - k) << 23)
-                                      : __int_as_float(0x7fffffff);
-      if (tig == 0) s_row[row] = make_float2(row < n ? c : 0.f, l2);
-#pragma unroll
-      for (int x = 0; x < 2 * NC; ++x) {  // 8 columns: two k-steps of four
-        float f[8];
-        raw[x].to_f(f);
-        s_q[(t * 2 * NC + x) * 32 + lane] = make_uint4(pack_h2(f[0] * f2, f[1] * f2), pack_h2(f[2] * f2, f[3] * f2),
-                                                       pack_h2(f[4] * f2, f[5] * f2), pack_h2(f[6] * f2, f[7] * f2));
-      }
-    }
-    __syncthreads();
+      __syncthreads();
 #pragma unroll 1
-    for (int i0 = 0; i0 < mine; i0 += kFlight) {
-#pragma unroll
-      for (int u = 0; u < kFlight; ++u) {
-        const int i = i0 + u;
-        if (i >= mine) break;
-        const int pg = __shfl_sync(0xffffffffu, good ? id : -1, i);
-        const float scale = __shfl_sync(0xffffffffu, ks, i);
-        uint32_t a[NC][4][4];
+      for (int i = 0; i < mine; ++i) {
+        const int at = i & 31;
+        if (at == 0) {
+          if (i > 0) {
+            id_cur = id_nxt;
+            ks_cur = ks_nxt;
+          }
+          id_nxt = fetch_id(i + 32 + lane);
+        } else if (at == 16) {
+          ks_nxt = fetch_scale(id_nxt);
+        }
+        issue(i + DEPTH - 1);
+        cp_wait<DEPTH - 1>();
+        __syncwarp();
+        const uint8_t* kp = ring + (i % DEPTH) * C::kSlot;
+        const int pg = __shfl_sync(0xffffffffu, id_cur, at);
+        const float scale = __shfl_sync(0xffffffffu, ks_cur, at);
+        uint32_t k[NC][4][4];
 #pragma unroll
         for (int c = 0; c < NC; ++c) {
-          const uint4 w0 = ring[u].k[c][0], w1 = ring[u].k[c][1];
+          const uint4 w0 = *reinterpret_cast<const uint4*>(kp + k_off<D>(gid, c * 4 + tig));
+          const uint4 w1 = *reinterpret_cast<const uint4*>(kp + k_off<D>(gid + 8, c * 4 + tig));
           const uint32_t x0[4] = {w0.x, w0.y, w0.z, w0.w}, x1[4] = {w1.x, w1.y, w1.z, w1.w};
 #pragma unroll
           for (int x = 0; x < 4; ++x) {
-            a[c][x][0] = e4m3x2_to_h2(x0[x] & 0xffffu);
-            a[c][x][1] = e4m3x2_to_h2(x1[x] & 0xffffu);
-            a[c][x][2] = e4m3x2_to_h2(x0[x] >> 16);
-            a[c][x][3] = e4m3x2_to_h2(x1[x] >> 16);
+            k[c][x][0] = e4m3x2_to_h2(x0[x] & 0xffffu);
+            k[c][x][1] = e4m3x2_to_h2(x1[x] & 0xffffu);
+            k[c][x][2] = e4m3x2_to_h2(x0[x] >> 16);
+            k[c][x][3] = e4m3x2_to_h2(x1[x] >> 16);
           }
         }
-        const float old[2] = {ring[u].old[0], ring[u].old[1]};
-        load(ring[u], i + kFlight);
         float sum[2] = {0.f, 0.f};
 #pragma unroll 2
         for (int t = 0; t < tiles; ++t) {
@@ -188,8 +234,8 @@ __global__ void __launch_bounds__(kThreads) kv_weights_kernel(const WeightsParam
 #pragma unroll
           for (int x = 0; x < 2 * NC; ++x) {
             const uint4 q = s_q[(t * 2 * NC + x) * 32 + lane];
-            mma(s, a[x / 2][2 * (x % 2)], q.x, q.y);
-            mma(s, a[x / 2][2 * (x % 2) + 1], q.z, q.w);
+            mma(s, k[x / 2][2 * (x % 2)], q.x, q.y);
+            mma(s, k[x / 2][2 * (x % 2) + 1], q.z, q.w);
           }
           // element e: row 2 tig + (e & 1), key gid + 8 (e >> 1)
           const float c0 = rc.x * scale, c1 = rc.z * scale;
@@ -200,32 +246,57 @@ __global__ void __launch_bounds__(kThreads) kv_weights_kernel(const WeightsParam
         for (int r = 0; r < 2; ++r) {
           sum[r] += __shfl_xor_sync(0xffffffffu, sum[r], 1);
           sum[r] += __shfl_xor_sync(0xffffffffu, sum[r], 2);
-          const int slot = (first + i * kWarps) * kP + gid + 8 * r;
-          if (tig == 0 && pg >= 0 && slot < L) p.out[((size_t)pg * p.Hkv + h) * kP + gid + 8 * r] = old[r] + sum[r];
         }
+        // lanes 0 .. 15: a slot each
+        const float lo = __shfl_sync(0xffffffffu, sum[0], 4 * (lane & 7)), hi = __shfl_sync(0xffffffffu, sum[1], 4 * (lane & 7));
+        const int slot = (first + 4 * i) * kP + lane;
+        if (lane < kP && slot < L) {
+          if (pg >= 0 && pg < p.num_pages) {
+            const float old = slot < had ? reinterpret_cast<const float*>(kp + C::kKeys)[lane] * decay : 0.f;
+            p.out[((size_t)pg * p.Hkv + h) * kP + lane] = old + (lane < 8 ? lo : hi);
+          } else {
+            set_status(p.status, kStPages);
+          }
+        }
+        __syncwarp();  // every lane has read the slot before it is filled again
       }
+      cp_wait<0>();
+      __syncwarp();
     }
   }
 }
 
 template <typename T, int D>
 cudaError_t launch_t(const WeightsParams& p, cudaStream_t stream) {
-  int dev = 0, sms = 0;
+  using C = Cfg<D>;
+  static std::atomic<int> sms_of[kMaxDevices];
+  int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
-  e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-  if (e != cudaSuccess) return e;
-  int per_warp = 32;
-  auto chunks = [&] { return (p.max_blocks + per_warp * kWarps - 1) / (per_warp * kWarps); };
-  while (per_warp > 1 && (long long)p.B * p.Hkv * chunks() < 16LL * sms) per_warp /= 2;
-  const long long blocks = (long long)p.B * p.Hkv * chunks();
-  if (blocks >= (1ll << 31)) return cudaErrorInvalidValue;
+  int sms = dev >= 0 && dev < kMaxDevices ? sms_of[dev].load(std::memory_order_acquire) : 0;
+  if (!sms) {
+    e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    if (e != cudaSuccess) return e;
+    e = cudaFuncSetAttribute(kv_weights_kernel<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             C::kRing + kMaxRows * (D * 2 + (int)sizeof(float2)) + 4 * (8192 + 1));
+    if (e != cudaSuccess) return e;
+    if (dev >= 0 && dev < kMaxDevices) sms_of[dev].store(sms, std::memory_order_release);
+  }
   const int most = p.rows < kMaxRows ? (p.rows + 7) & ~7 : kMaxRows;
-  const size_t smem = (size_t)most * (D * 2 + sizeof(float2));
-  e = cudaFuncSetAttribute(kv_weights_kernel<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                           kMaxRows * (D * 2 + (int)sizeof(float2)));
-  if (e != cudaSuccess) return e;
-  return launch_pdl(kv_weights_kernel<T, D>, dim3((unsigned)blocks), dim3(kThreads), smem, stream, p, chunks(), per_warp);
+  const size_t smem = C::kRing + (size_t)most * (D * 2 + sizeof(float2)) + 4 * ((size_t)p.B + 1);
+  int per_sm = (int)(232448 / (smem + 1024));
+  per_sm = per_sm < 1 ? 1 : per_sm < C::CTAS ? per_sm : C::CTAS;
+  // no more CTAs than tiles that the tables can hold
+  const long long tiles = (long long)p.B * p.Hkv * ((p.max_blocks + 3) / 4);
+  Sched s{};
+  s.B = p.B;
+  s.T = 0;
+  s.Hkv = p.Hkv;
+  s.nrg = 1;
+  s.G = (int)(tiles < (long long)per_sm * sms ? tiles : (long long)per_sm * sms);
+  s.splits = 0;
+  s.seg_cost = 4;
+  return launch_pdl(kv_weights_kernel<T, D>, dim3(s.G), dim3(kThreads), smem, stream, p, s);
 }
 
 }  // namespace
