@@ -349,6 +349,7 @@ int mt_kv_attn_weights(const mt_attn_desc* d, int max_depth, float decay, const 
   p.decay = decay;
   p.weights = weights; p.out = out;
   p.status = static_cast<int*>(status_ws);
+  wait_bound(&p.wait_limit_ns, &p.test_stall);
   return cuda_status(launch_kv_weights(p, d->dtype, stream));
 }
 

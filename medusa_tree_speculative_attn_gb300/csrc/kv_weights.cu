@@ -31,7 +31,7 @@ constexpr int kMaxDevices = 64;
 template <int D>
 struct Cfg {
   static constexpr int CTAS = 4;   // per SM
-  static constexpr int DEPTH = 6;  // pages a warp keeps in flight
+  static constexpr int DEPTH = 4;  // pages a warp keeps in flight
   static constexpr int kKeys = kP * D;
   static constexpr int kSlot = kKeys + kP * 4;  // a page's keys and old weights
   static constexpr int kRing = kWarps * DEPTH * kSlot;
@@ -302,6 +302,7 @@ cudaError_t launch_t(const WeightsParams& p, cudaStream_t stream) {
 }  // namespace
 
 cudaError_t launch_kv_weights(const WeightsParams& p, int dtype, cudaStream_t stream) {
+  if (p.rows > 48) return launch_kv_weights_tc(p, dtype, stream);
   if (p.D == 64)
     return dtype == 1 ? launch_t<__half, 64>(p, stream) : launch_t<__nv_bfloat16, 64>(p, stream);
   return dtype == 1 ? launch_t<__half, 128>(p, stream) : launch_t<__nv_bfloat16, 128>(p, stream);

@@ -328,11 +328,11 @@ __device__ __forceinline__ void drop_odd(Row8<T>& r) {
   r.from_f(x);
 }
 
-// Tiles of each sequence (cached pages, then the new tokens' blocks, four to a
+// Tiles of each sequence (cached pages, then the new tokens' blocks, PAGES to a
 // tile; none for seq_lens < 0) and their exclusive prefix in pfx[0 .. B], by a
 // block of W warps; returns the total.  A length past the block table has no
 // tiles and is recorded by the block that says so.
-template <int W, bool REACH = false>
+template <int W, bool REACH = false, int PAGES = 4>
 __device__ __forceinline__ int block8_prefix(const AttnParams& a, int* pfx, int* s_warp, bool report, int window = 0,
                                              int sinks = 0) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -346,7 +346,7 @@ __device__ __forceinline__ int block8_prefix(const AttnParams& a, int* pfx, int*
       if ((long long)L > (long long)a.max_blocks * 16) {
         if (report) set_status(a.status, kStPages);
       } else if (L >= 0) {
-        n = ((REACH ? Reach(L, window, sinks).npre : (L + 15) / 16) + nnew + 3) / 4;
+        n = ((REACH ? Reach(L, window, sinks).npre : (L + 15) / 16) + nnew + PAGES - 1) / PAGES;
       }
     }
     int incl = n;
@@ -403,7 +403,10 @@ struct WeightsParams {
   const float* weights;  // [num_pages][Hkv][16]
   float* out;
   int* status;
+  unsigned long long wait_limit_ns;  // as in AttnParams
+  int test_stall;
 };
+cudaError_t launch_kv_weights_tc(const WeightsParams& p, int dtype, cudaStream_t stream);
 cudaError_t launch_kv_weights(const WeightsParams& p, int dtype, cudaStream_t stream);
 
 // ---------------------------------------------------------------------------

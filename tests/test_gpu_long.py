@@ -729,3 +729,73 @@ def test_logits_far_rows():
     before[499999] -= 1
     before[5] -= 1
     assert torch.equal(x[-1], before) and mt.read_status(ws) == 0
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("t, hq, hkv, d, lens", [(64, 8, 2, 128, [3000, 1, 700, -1, 130]), (25, 2, 1, 64, [1027]), (64, 12, 2, 128, [260, 900]), (49, 4, 4, 64, [128, 127, 129]),
+                                                  (64, 40, 4, 128, [500, 77])])
+@pytest.mark.parametrize("which", ["all", "path"])
+def test_slot_weights_of_chunks(dtype, t, hq, hkv, d, lens, which):
+    # more rows a head than a few tiles of eight: the tensor-core path, in one pass and in more
+    rng = np.random.default_rng(47)
+    c = _attn_case(rng, len(lens), t, hq, hkv, d, lens, dtype, "tree")
+    path = None
+    if which == "path":
+        rows = np.stack([np.sort(rng.permutation(t)) for _ in lens])
+        path = rows, rng.integers(t - 25, t, len(lens))
+        path[1][0] = 0  # one row
+    prev = [max(n - 150, 0) for n in lens]
+    _weights_check(c, prev, path, 0.9, in_place=True, seed=t)
+
+
+def test_slot_weights_of_many_sequences_in_chunks():
+    rng = np.random.default_rng(48)
+    lens = [int(n) for n in rng.integers(-1, 300, 200)]
+    c = _attn_case(rng, 200, 20, 8, 2, 64, lens, "bf16", "chain")
+    _weights_check(c, None, None, 1.0, False)
+
+
+def test_slot_weights_of_chunks_bad_paths_and_pages():
+    rng = np.random.default_rng(49)
+    c = _attn_case(rng, 3, 64, 4, 2, 64, [300, 200, 40], "bf16", "chain")
+    lse, ws = torch.zeros(3, 64, 4, device="cuda"), _status()
+    w = torch.ones(c["k"].shape[0], 2, P, device="cuda")
+    path = np.tile(np.arange(64), (3, 1))
+    path[1, 5] = 64
+    c["table"][0, 3] = -5
+    mt.kv_attn_weights(c["q"].cuda(), _f8(c["k"]), torch.from_numpy(c["ks"]).float().cuda(), _i32(c["table"]).cuda(), _i32(c["lens"]).cuda(), lse, w,
+                       accept_path=_i32(path).cuda(), accept_len=_i32([40, 40, 40]).cuda(), status_ws=ws)
+    assert mt.read_status(ws) == -4
+    touched = {p for p in c["table"][0][:19] if p >= 0} | set(c["table"][2][:3])
+    left = torch.tensor([p not in touched for p in range(len(w))])
+    assert bool((w.cpu()[left] == 1).all()) and not bool((w.cpu()[~left][:, :, 0] == 1).any())
+
+
+def test_slot_weights_nan_among_chunks():
+    c = _attn_case(np.random.default_rng(57), 2, 40, 8, 2, 128, [250, 130], "bf16", "chain")
+    c["k"][c["table"][0][1], 1, 4, 9] = 0x7F
+    c["k"][c["table"][1][8], 0, 5, 9] = 0x7F  # behind the second sequence's end
+    c["q"][1, 2, 0, 5] = float("inf")
+    lse = torch.zeros(2, 40, 8, device="cuda")
+    w, ws = torch.zeros(c["k"].shape[0], 2, P, device="cuda"), _status()
+    mt.kv_attn_weights(c["q"].cuda(), _f8(c["k"]), torch.from_numpy(c["ks"]).float().cuda(), _i32(c["table"]).cuda(), _i32(c["lens"]).cuda(), lse, w, status_ws=ws)
+    want = np.zeros(w.shape, bool)
+    want[c["table"][0][1], 1, 4] = True
+    for s in range(130):
+        want[c["table"][1][s // P], 0, s % P] = True
+    assert np.array_equal(w.isnan().cpu().numpy(), want)
+
+
+def test_slot_weights_wait_bound():
+    """A pipeline wait that only its bound ends: the status says so, and the next call is right."""
+    c = _attn_case(np.random.default_rng(58), 2, 32, 8, 2, 128, [100, 400], "bf16", "chain")
+    lse = _lse_of(c)
+    w, ws = torch.zeros(c["k"].shape[0], 2, P, device="cuda"), _status()
+    args = (c["q"].cuda(), _f8(c["k"]), torch.from_numpy(c["ks"]).float().cuda(), _i32(c["table"]).cuda(), _i32(c["lens"]).cuda(), lse, w)
+    try:
+        mt.debug_set_wait(20_000_000, stall=True)
+        mt.kv_attn_weights(*args, status_ws=ws)
+        assert mt.read_status(ws) == -6
+    finally:
+        mt.debug_set_wait()
+    _weights_check(c, None, None, 1.0, True)
