@@ -13,6 +13,12 @@
 // lie in shared memory in that order, one 16-byte read for two k-steps.  Persistent CTAs walk
 // the balanced schedule of 64-slot tiles; a warp takes a page of each and brings the pages,
 // with their old weights, into a ring of its own.  A slot's sum over rows is two shuffles.
+// Up to 48 rows a KV head: beyond, the tensor-core path (kv_weights_tc.cu).
+//
+// Bound by the keys' bytes: 64 sequences of 256 to 8192 tokens, one query each, 32 query and 8
+// KV heads: 54 us for 291 MB, 5.4 TB/s (79 % of a copy; six pages in flight instead of four 57,
+// with fewer CTAs 62); accepted paths of 1 to 5 nodes, 16 sequences: 25 us; one sequence of
+// 4096: 5.5 us.
 #include <atomic>
 #include <cmath>
 
@@ -31,7 +37,7 @@ constexpr int kMaxDevices = 64;
 template <int D>
 struct Cfg {
   static constexpr int CTAS = 4;   // per SM
-  static constexpr int DEPTH = 4;  // pages a warp keeps in flight
+  static constexpr int DEPTH = 4;  // pages a warp has in its ring
   static constexpr int kKeys = kP * D;
   static constexpr int kSlot = kKeys + kP * 4;  // a page's keys and old weights
   static constexpr int kRing = kWarps * DEPTH * kSlot;

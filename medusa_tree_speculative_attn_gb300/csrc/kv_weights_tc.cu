@@ -10,13 +10,23 @@
 //
 // Operands stay in 8 bits (kind::f8f6f4): key codes go by TMA straight into the tile, and a
 // query row enters as the sum of two (bf16) or three (fp16) E4M3 parts, as in block8_prep.cu,
-// worked out by the CTA when it takes up a segment and kept for all of its tiles.  Roles: a
-// warp issues the copies (a lane per page), one the products, eight add up, four of them the
-// even tiles and four the odd ones, each set with a 256-column accumulator of its own.  Every
-// mbarrier wait is bounded (as in attn_block8_tc.cu), and the sums' warps meet by mbarriers
-// too, so that a timeout leaves nobody waiting.
+// worked out by the CTA when it takes up a segment and kept for all of its tiles.
+//
+// Roles: a warp issues the copies (a lane per page), one the products, sixteen add up.  A
+// constant from shared memory costs a 16-byte read for every two columns and warp, so a thread
+// takes a key of two tiles at once: a unit is two tiles by 128 columns, two units fill TMEM,
+// and each has a group of eight warps, 64 columns a warp.  The sums of a pair of tiles meet in
+// shared memory.  Every mbarrier wait is bounded (as in attn_block8_tc.cu), and the sums'
+// warps meet by mbarriers too, so that a timeout leaves nobody waiting.
 //
 // More than 256 query rows of a KV head are taken in passes over the segment's tiles.
+//
+// Bound by a unit's chain, products (16 of 100 cycles) then sums (2800 cycles with both groups
+// at work, of which the exponentials' unit is busy 2050), one accumulator a group.  Chunks of
+// 64 tokens for 8 sequences of 4096 to 16384, 32 query and 8 KV heads, bf16: 69 us, 39 % of the
+// products' rate; 4.0 of 5.2 thousand cycles a pair of tiles for the chain, 8000 cycles to
+// begin and 7000 to change a segment.  A tile at a time with eight warps took 80 us, with
+// sixteen 75; four groups of 64 columns 81 (a product of 64 columns takes 80 cycles).
 #include <cudaTypedefs.h>
 
 #include <atomic>
@@ -33,16 +43,22 @@ constexpr int kP = 16;
 constexpr int kPages = 8;  // of a tile
 constexpr int kTile = kPages * kP;
 constexpr int kCols = 256;  // query rows at a time
+constexpr int kInfo = 32;  // tiles whose pages' numbers and scales are kept: more than the roles are ever apart
 constexpr int kSmemLimit = 232448;
 constexpr int kMaxDevices = 64;
-constexpr int kSumWarps = 8, kCopyWarp = 8, kMmaWarp = 9, kThreads = 10 * 32;
+constexpr int kNone = INT_MIN;  // no page
+constexpr int kUnit = 128;  // query rows of a unit: an accumulator has them for two tiles
+constexpr int kAcc = 2;     // accumulators, each of a group of eight warps
+constexpr int kSumWarps = 16, kCopyWarp = 16, kMmaWarp = 17, kThreads = 18 * 32;
 
 template <int D, int NP>
 struct Cfg {
   static constexpr int kQPart = kCols * D;
   static constexpr int kQ = NP * kQPart;
   static constexpr int kStage = kTile * D;
-  static constexpr int kMeta = 1024 + kCols * 8;  // barriers, columns
+  static constexpr int kPart = kAcc * 4 * 2 * kTile * 4;
+  static constexpr int kMeta = 1024 + kCols * 8 + kPart + kInfo * kPages * 8 +
+                               kMaxPieceRecs * (int)sizeof(PieceRec);  // barriers, columns, parts of sums, pages, pieces
   static constexpr int kFit = (kSmemLimit - 1024 - kMeta - kQ - 4 * (8192 + 4)) / kStage;
   static constexpr int STAGES = kFit > 6 ? 6 : kFit;
   static constexpr int kSmem = 1024 + kQ + STAGES * kStage + kMeta;  // and the prefix
@@ -55,28 +71,19 @@ __device__ __forceinline__ float fast_exp2(float x) {
   return y;
 }
 
-// 32 lanes x 32 bits, 32 consecutive columns per thread; and the wait, through which the
-// registers pass so that no use of them can move ahead of it.
-__device__ __forceinline__ void tmem_ld_x32(uint32_t taddr, uint32_t (&r)[32]) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
-      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
-      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
-        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
-        "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
-        "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
-      : "r"(taddr));
+// 32 lanes x 32 bits, eight consecutive columns per thread of two accumulators; and the
+// wait, through which the registers pass so that no use of them can move ahead of it.
+__device__ __forceinline__ void tmem_ld_x8(uint32_t taddr, uint32_t (&r)[8]) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+               : "r"(taddr));
 }
-__device__ __forceinline__ void tmem_ld_wait(uint32_t (&r)[32]) {
+__device__ __forceinline__ void tmem_ld_wait(uint32_t (&r)[8], uint32_t (&s)[8]) {
   asm volatile("tcgen05.wait::ld.sync.aligned;"
                : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
-                 "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]),
-                 "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]),
-                 "+r"(r[23]), "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29])
+                 "+r"(s[0]), "+r"(s[1]), "+r"(s[2]), "+r"(s[3]), "+r"(s[4]), "+r"(s[5]), "+r"(s[6]), "+r"(s[7])
                :
                : "memory");
-  asm volatile("" : "+r"(r[30]), "+r"(r[31]));
 }
 
 // Two fp32 in one register pair, for the instructions that take both at once.
@@ -163,56 +170,82 @@ __device__ __forceinline__ void drain_wait(uint64_t* bar, uint32_t parity, int* 
   }
 }
 
-// Eight lanes (D / 16) a row: 16 columns c of query row `row` of this pass as E4M3 parts in
-// their places; returns the row's scale (scores of the parts -> base 2).
-template <typename T, int D, int NP>
-__device__ __forceinline__ float place_query(const T* src, float scale_log2, uint8_t* sq, int row, int c) {
+// A query row's 16 columns of one lane (D / 16 lanes a row).
+template <typename T>
+struct QueryPart {
   Row8<T> r0, r1;
-  r0.zero();
-  r1.zero();
-  if (src) {
-    r0.load(src + 16 * c);
-    r1.load(src + 16 * c + 8);
+  __device__ __forceinline__ void load(const T* src) {
+    r0.zero();
+    r1.zero();
+    if (src) {
+      r0.load(src);
+      r1.load(src + 8);
+    }
   }
-  float x[16];
-  {
-    float t[8];
-    r0.to_f(t);
-#pragma unroll
-    for (int e = 0; e < 8; ++e) x[e] = t[e];
-    r1.to_f(t);
-#pragma unroll
-    for (int e = 0; e < 8; ++e) x[8 + e] = t[e];
-  }
-  float amax = 0.f;
-#pragma unroll
-  for (int e = 0; e < 16; ++e) amax = fmaxf(amax, fabsf(x[e]));
+};
+
+// Columns 16 c .. 16 c + 15 of query row `row` of this pass as E4M3 parts in their places;
+// returns the row's scale (scores of the parts -> base 2).  Scaled to 448 at most, an fp16
+// holds all of a query's bits above 2^-24, far below the last part's smallest step (2^-9).
+template <typename T, int D, int NP>
+__device__ __forceinline__ float place_query(const QueryPart<T>& q, float scale_log2, uint8_t* sq, int row, int c) {
+  AbsMax<T> top;
+  top.add(q.r0);
+  top.add(q.r1);
+  float amax = top.get();
 #pragma unroll
   for (int off = 1; off < D / 16; off <<= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, off));
   const float scale = block_scale(amax), inv = 1.f / scale;
+  __half2 x[8];
+  {
+    float t[8];
+    q.r0.to_f(t);
 #pragma unroll
-  for (int e = 0; e < 16; ++e) x[e] *= inv;
+    for (int e = 0; e < 4; ++e) x[e] = __floats2half2_rn(t[2 * e] * inv, t[2 * e + 1] * inv);
+    q.r1.to_f(t);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) x[4 + e] = __floats2half2_rn(t[2 * e] * inv, t[2 * e + 1] * inv);
+  }
 #pragma unroll
   for (int part = 0; part < NP; ++part) {
     uint32_t w[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const uint32_t lo = e4m3x2_of(x[4 * i], x[4 * i + 1]), hi = e4m3x2_of(x[4 * i + 2], x[4 * i + 3]);
-      w[i] = lo | hi << 16;
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {  // what the part leaves, exactly
-        const uint32_t h2 = e4m3x2_to_h2(h ? hi : lo);
+    for (int e = 0; e < 8; ++e) {
+      uint32_t bits;
+      memcpy(&bits, &x[e], 4);
+      uint16_t code;
+      asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(code) : "r"(bits));
+      if (e & 1) w[e / 2] |= (uint32_t)code << 16; else w[e / 2] = code;
+      if (part + 1 < NP) {  // what the part leaves, exactly
+        const uint32_t h = e4m3x2_to_h2(code);
         __half2 v;
-        memcpy(&v, &h2, 4);
-        const float2 f = __half22float2(v);
-        x[4 * i + 2 * h] -= f.x;
-        x[4 * i + 2 * h + 1] -= f.y;
+        memcpy(&v, &h, 4);
+        x[e] = __hsub2(x[e], v);
       }
     }
     *reinterpret_cast<uint4*>(sq + part * (kCols * D) + row_off<D>(row, c)) = make_uint4(w[0], w[1], w[2], w[3]);
   }
   // an infinity has no parts: the row's weights become NaN, as they would be
   return amax < INFINITY ? scale * scale_log2 : __int_as_float(0x7fffffff);
+}
+
+// The pieces of this CTA, by a whole warp with the same values in every lane; their number,
+// -1 for more than a list holds.
+template <typename I>
+__device__ __forceinline__ int list_pieces(const Sched& sc, PieceRec* recs, const int* seq_lens) {
+  PieceIterT<I> it;
+  it.init(sc, blockIdx.x);
+  Piece pc;
+  int n = 0;
+  while (it.next(pc)) {
+    if (n == kMaxPieceRecs) return -1;
+    PieceRec r;
+    r.b = pc.b; r.kvh = pc.kvh; r.rg = pc.rg; r.seg = pc.seg;
+    r.tile_begin = pc.tile_begin; r.tile_end = pc.tile_end; r.slot = pc.slot;
+    r.L = seq_lens[pc.b];
+    recs[n++] = r;
+  }
+  return n;
 }
 
 template <typename T, int D, int NP>
@@ -225,19 +258,24 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint8_t* sQ = smem;             // [part][256 rows] swizzled
   uint8_t* sK = sQ + C::kQ;       // [stage][128 rows] swizzled
   float4* s_col = reinterpret_cast<float4*>(sK + S * C::kStage);  // of two columns: their scales, minus their lse
-  uint64_t* bars = reinterpret_cast<uint64_t*>(s_col + kCols / 2);
+  float* s_part = reinterpret_cast<float*>(s_col + kCols / 2);  // [pair's turn][half unit][tile][key]
+  int2* s_page = reinterpret_cast<int2*>(s_part + C::kPart / 4);  // [kInfo][8] a tile's pages: number, scale
+  uint64_t* bars = reinterpret_cast<uint64_t*>(s_page + kInfo * kPages);
   uint64_t* full = bars;           // [S] a tile's codes have landed
   uint64_t* empty = full + S;      // [S] and are multiplied
-  uint64_t* acc_full = empty + S;  // [2] a tile's scores are there
-  uint64_t* acc_empty = acc_full + 2;  // [2] and read out
-  uint64_t* idle = acc_empty + 2;      // the sums' warps have left the pass before
+  uint64_t* acc_full = empty + S;         // [kAcc] a unit's scores are there
+  uint64_t* acc_empty = acc_full + kAcc;  // [kAcc] and read out
+  uint64_t* parts = acc_empty + kAcc;     // [kAcc] the units' sums of a pair are there
+  uint64_t* parts_read = parts + kAcc;    // [kAcc] and read
+  uint64_t* idle = parts_read + kAcc;     // the sums' warps have left the pass before
   uint64_t* q_full = idle + 1;         // the pass's queries are in place
   uint64_t* fin = q_full + 1;          // every product done
   uint64_t* never = fin + 1;           // nothing arrives here (timeout test hook)
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(never + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
-  static_assert((2 * 6 + 8) * 8 + 8 <= 1024, "barrier area");
-  int* s_pfx = reinterpret_cast<int*>(reinterpret_cast<uint8_t*>(bars) + 1024);  // [B + 1]
+  static_assert((2 * 6 + 4 * kAcc + 4) * 8 + 8 <= 1024, "barrier area");
+  PieceRec* s_pieces = reinterpret_cast<PieceRec*>(reinterpret_cast<uint8_t*>(bars) + 1024);
+  int* s_pfx = reinterpret_cast<int*>(s_pieces + kMaxPieceRecs);  // [B + 1]
   __shared__ int s_warp[kThreads / 32];
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -246,9 +284,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc::mbar_init(&full[s], 1);
       tc::mbar_init(&empty[s], 1);
     }
-    for (int s = 0; s < 2; ++s) {
-      tc::mbar_init(&acc_full[s], 1);
-      tc::mbar_init(&acc_empty[s], 4);
+    for (int s = 0; s < kAcc; ++s) {
+      tc::mbar_init(&acc_full[s], 2);  // the products, and their issuer itself (below)
+      tc::mbar_init(&acc_empty[s], kSumWarps / kAcc);
+      tc::mbar_init(&parts[s], kSumWarps);
+      tc::mbar_init(&parts_read[s], kSumWarps);
     }
     tc::mbar_init(idle, kSumWarps);
     tc::mbar_init(q_full, kSumWarps);
@@ -270,14 +310,24 @@ __global__ void __launch_bounds__(kThreads, 1)
   a.seq_lens = p.seq_lens;
   a.status = p.status;
   tc::tc_fence_before();
-  block8_prefix<kThreads / 32, false, kPages>(a, s_pfx, s_warp, blockIdx.x == 0);  // (ends in a barrier)
-  tc::tc_fence_after();
-  const uint32_t tmem = *tmem_slot;
+  const int total = block8_prefix<kThreads / 32, false, kPages>(a, s_pfx, s_warp, blockIdx.x == 0);
   Sched sc = sched;
   sc.tile_pfx = s_pfx;
-  PieceIter it;
-  it.init(sc, blockIdx.x);
+  // this CTA's pieces, listed once by a warp (the walk's divisions are slow in 64 bits)
+  __shared__ int s_npieces;
+  if (warp == kCopyWarp) {
+    const long long nseg = (long long)sc.B * sc.Hkv;
+    const bool small = ((long long)total * sc.Hkv + sc.seg_cost * nseg) * (sc.G + 1) < (1LL << 31);
+    const int n = small ? list_pieces<int>(sc, s_pieces, p.seq_lens) : list_pieces<long long>(sc, s_pieces, p.seq_lens);
+    if (lane == 0) s_npieces = n;
+  }
+  __syncthreads();
+  tc::tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  PieceSrc it;
+  it.init(s_pieces, s_npieces, sc, blockIdx.x, p.seq_lens);
   Piece pc;
+  int L = 0;
   bool ok = true;
   auto wait_all = [&](uint64_t* bar, uint32_t parity) {
     const bool r = tc::mbar_try_wait(bar, parity) || wait_slow(bar, parity, abort_flag, p.status, p.wait_limit_ns);
@@ -303,24 +353,37 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint64_t policy = tc::policy_evict_first();
     const int oob_row = p.num_pages * p.Hkv * kP;  // past the cache: TMA fills zeros
     uint32_t pos = 0;
-    while (ok && it.next(pc)) {
-      const int rows = rows_of(pc.b), npages = (p.seq_lens[pc.b] + kP - 1) / kP;
+    while (ok && it.next(pc, L)) {
+      const int rows = rows_of(pc.b), npages = (L + kP - 1) / kP;
       const int* bt = p.block_tables + (size_t)pc.b * p.max_blocks;
       for (int r0 = 0; ok && r0 < rows; r0 += kCols) {
-        // page ids of 32 pages (four tiles) at a time, a lane each, the next 32 in flight
-        auto fetch = [&](int q) { return q < npages ? __ldg(bt + q) : -1; };
+        // page ids of 32 pages (four tiles) at a time, a lane each, the next 64 in flight
+        // (their scales with them): kNone behind the last
+        auto fetch = [&](int q) { return q < npages ? max(__ldg(bt + q), -1) : kNone; };
+        auto fetch_scale = [&](int id) {
+          return id >= 0 && id < p.num_pages ? __ldg(p.k_scales + (size_t)id * p.Hkv + pc.kvh) : 0.f;
+        };
         int base = pc.tile_begin * kPages;
-        int id0 = fetch(base + lane), id1 = fetch(base + 32 + lane);
+        int id0 = fetch(base + lane), id1 = fetch(base + 32 + lane), id2 = fetch(base + 64 + lane);
+        float ks0 = fetch_scale(id0), ks1 = fetch_scale(id1);
         for (int j = pc.tile_begin; j < pc.tile_end; ++j, ++pos) {
           if (j * kPages - base >= 32) {
             base += 32;
             id0 = id1;
-            id1 = fetch(base + 32 + lane);
+            ks0 = ks1;
+            id1 = id2;
+            ks1 = fetch_scale(id1);
+            id2 = fetch(base + 64 + lane);
           }
           const uint32_t st = pos % S;
           const int id = __shfl_sync(0xffffffffu, id0, (j * kPages - base) + (lane & 7));
+          const float ks = __shfl_sync(0xffffffffu, ks0, (j * kPages - base) + (lane & 7));
           if (pos >= (uint32_t)S) wait_all(&empty[st], ((pos / S) - 1) & 1);
           if (!ok) break;
+          // (the place is free: the products of the tile S before are done, so every group has
+          // left the pair eight before that tile's, which holds tiles after the one kInfo back)
+          if (lane < kPages) s_page[pos % kInfo * kPages + lane] = make_int2(id, __float_as_int(ks));
+          __syncwarp();
           if (lane == 0) tc::mbar_arrive_expect_tx(&full[st], C::kStage);
           __syncwarp();
           if (lane < kPages)
@@ -337,35 +400,46 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else if (warp == kMmaWarp) {
     // ------------------------------------------------------------ products
     const uint32_t sQ_u = tc::smem_u32(sQ), sK_u = tc::smem_u32(sK);
-    uint32_t pos = 0, pass = 0;
+    uint32_t pos = 0, unit = 0, pass = 0;
     if (p.test_stall) wait_all(never, 0);  // test hook: a wait that can only time out
-    while (ok && it.next(pc)) {
+    while (ok && it.next(pc, L)) {
       const int rows = rows_of(pc.b);
       for (int r0 = 0; ok && r0 < rows; r0 += kCols, ++pass) {
-        const int n = (min(kCols, rows - r0) + 31) / 32 * 32;
-        const uint32_t idesc = idesc_f8(kTile, n);
+        const int cols = (min(kCols, rows - r0) + 31) / 32 * 32;
         wait_all(q_full, pass & 1);
-        for (int j = pc.tile_begin; ok && j < pc.tile_end; ++j, ++pos) {
-          const uint32_t st = pos % S, buf = pos & 1;
-          wait_all(&full[st], (pos / S) & 1);
-          if (pos >= 2) wait_all(&acc_empty[buf], ((pos / 2) - 1) & 1);
-          if (!ok) break;
-          tc::tc_fence_after();
-          const uint64_t kd = desc_rows8<D>(sK_u + st * C::kStage);
-          if (tc::elect_one()) {
+        for (int j = pc.tile_begin; ok && j < pc.tile_end; j += 2) {
+          const int two = min(2, pc.tile_end - j);
+          for (int x = 0; x < two; ++x) wait_all(&full[(pos + x) % S], ((pos + x) / S) & 1);
+          for (int c0 = 0; ok && c0 < cols; c0 += kUnit, ++unit) {
+            const uint32_t buf = unit % kAcc;
+            if (unit >= kAcc) wait_all(&acc_empty[buf], ((unit / kAcc) - 1) & 1);
+            if (!ok) break;
+            tc::tc_fence_after();
+            const uint32_t idesc = idesc_f8(kTile, min(kUnit, cols - c0));
+#pragma unroll 1
+            for (int x = 0; x < two; ++x) {
+              const uint64_t kd = desc_rows8<D>(sK_u + (pos + x) % S * C::kStage);
+              const uint32_t d = tmem + buf * (2 * kUnit) + x * kUnit;
+              if (tc::elect_one()) {
 #pragma unroll
-            for (int part = 0; part < NP; ++part) {
-              const uint64_t qd = desc_rows8<D>(sQ_u + part * C::kQPart);
+                for (int part = 0; part < NP; ++part) {
+                  const uint64_t qd = desc_rows8<D>(sQ_u + part * C::kQPart + c0 * D);
 #pragma unroll
-              for (int kk = 0; kk < D / 32; ++kk) {  // 32 codes: 2 descriptor units
-                if (part == 0 && kk == 0) mma_f8_ss<false>(tmem + buf * kCols, kd, qd, idesc);
-                else mma_f8_ss<true>(tmem + buf * kCols, kd + (uint64_t)(kk * 2), qd + (uint64_t)(kk * 2), idesc);
+                  for (int kk = 0; kk < D / 32; ++kk) {  // 32 codes: 2 descriptor units
+                    if (part == 0 && kk == 0) mma_f8_ss<false>(d, kd, qd, idesc);
+                    else mma_f8_ss<true>(d, kd + (uint64_t)(kk * 2), qd + (uint64_t)(kk * 2), idesc);
+                  }
+                }
+                if (c0 + kUnit >= cols) tc::mma_commit(&empty[(pos + x) % S]);
+                if (x == two - 1) tc::mma_commit(&acc_full[buf]);
               }
+              __syncwarp();
             }
-            tc::mma_commit(&empty[st]);
-            tc::mma_commit(&acc_full[buf]);
+            // passes on what this warp acquired with the tiles: their pages
+            if (lane == 0) tc::mbar_arrive(&acc_full[buf]);
+            __syncwarp();
           }
-          __syncwarp();
+          pos += (uint32_t)two;
         }
       }
     }
@@ -375,112 +449,150 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncwarp();
   } else {
     // ---------------------------------------------------------------- sums
-    const int set = warp >> 2, quad = warp & 3;  // tiles of this parity; TMEM lanes 32 quad ...
-    const int key = quad * 32 + lane;            // of the tile
-    const uint32_t addr = tmem + ((uint32_t)(quad * 32) << 16) + (uint32_t)(set * kCols);
-    uint32_t pos = 0, pass = 0;
-    while (ok && it.next(pc)) {
+    const int quad = warp & 3, half = warp >> 2 & 1;  // TMEM lanes 32 quad ..; 64 columns of a unit
+    const uint32_t group = warp >> 3;                 // units of this number modulo kAcc
+    const int key = quad * 32 + lane;                 // of a tile
+    const uint32_t addr = tmem + ((uint32_t)(quad * 32) << 16) + group * (2 * kUnit) + (uint32_t)(half * 64);
+    const float inv_g = 1.f / (float)p.g;
+    uint32_t unit = 0, pair = 0, pos = 0, pass = 0;
+    while (ok && it.next(pc, L)) {
       const int b = pc.b, h = pc.kvh, rows = rows_of(b);
       if (rows == 0 && threadIdx.x == 0) set_status(p.status, kStPages);
-      const int L = p.seq_lens[b], prev = p.prev_lens ? p.prev_lens[b] : L;
+      const int prev = p.prev_lens ? p.prev_lens[b] : L;
       const int* path = p.accept_path ? p.accept_path + (size_t)b * (p.max_depth + 1) : nullptr;
-      const int* bt = p.block_tables + (size_t)b * p.max_blocks;
       const int tiles = pc.tile_end - pc.tile_begin;
-      for (int r0 = 0; ok && r0 < rows; r0 += kCols, ++pass, pos += (uint32_t)tiles) {
-        // the queries and the columns' constants, once nobody uses the pass before's
+      for (int r0 = 0; ok && r0 < rows; r0 += kCols, ++pass) {
+        // the queries and the columns' constants, asked for together, and put in their places
+        // once nobody uses the pass before's
+        const int n = min(kCols, rows - r0), cols = (n + 31) / 32 * 32;
+        constexpr int LPR = D / 16, RPW = 32 / LPR, IT = kCols / (kSumWarps * RPW);
+        QueryPart<T> raw[IT];
+        float l2[IT];
+#pragma unroll
+        for (int i = 0; i < IT; ++i) {
+          const int row = (i * kSumWarps + warp) * RPW + lane / LPR;
+          l2[i] = INFINITY;  // a column past the rows gives 2^-inf
+          const T* src = nullptr;
+          if (row < n) {
+            // (exact: rows are below 2^20)
+            const int at = (int)(((float)(r0 + row) + 0.5f) * inv_g), node = path ? path[at] : at;
+            const int head = h * p.g + (r0 + row) - at * p.g;
+            const size_t q = ((size_t)b * p.T + node) * p.Hq + head;
+            src = static_cast<const T*>(p.q) + q * D + 16 * (lane % LPR);
+            l2[i] = p.lse[q];
+          }
+          raw[i].load(src);
+        }
         __syncwarp();
         if (lane == 0) tc::mbar_arrive(idle);
         wait_all(idle, pass & 1);
         if (!ok) break;
-        const int n = min(kCols, rows - r0), cols = (n + 31) / 32 * 32;
-        constexpr int LPR = D / 16, RPW = 32 / LPR;
-        for (int q0 = warp * RPW; q0 < cols; q0 += kSumWarps * RPW) {
-          const int row = q0 + lane / LPR;
-          const T* src = nullptr;
-          float l2 = INFINITY;  // a column past the rows gives 2^-inf
-          if (row < n) {
-            const int at = (r0 + row) / p.g, node = path ? path[at] : at, head = h * p.g + (r0 + row) % p.g;
-            const size_t q = ((size_t)b * p.T + node) * p.Hq + head;
-            src = static_cast<const T*>(p.q) + q * D;
-            l2 = p.lse[q] * 1.4426950408889634f;
-          }
-          const float c = place_query<T, D, NP>(src, p.scale_log2, sQ, row, lane % LPR);
+#pragma unroll
+        for (int i = 0; i < IT; ++i) {
+          const int row = (i * kSumWarps + warp) * RPW + lane / LPR;
+          if ((i * kSumWarps + warp) * RPW >= cols) break;  // the same for the warp
+          const float c = place_query<T, D, NP>(raw[i], p.scale_log2, sQ, row, lane % LPR);
           if (lane % LPR == 0) {
             float* col = reinterpret_cast<float*>(s_col + row / 2) + (row & 1);
             col[0] = row < n ? c : 0.f;
-            col[2] = -l2;
+            col[2] = -l2[i] * 1.4426950408889634f;
           }
         }
         tc::fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) tc::mbar_arrive(q_full);
-        // this thread's keys: page id two of its tiles ahead, scale and old weight one
-        const float* before = r0 == 0 ? p.weights : p.out;
+        const float* before = r0 == 0 ? p.weights : p.out;  // later rows add to what the earlier ones left
         const int had = r0 == 0 ? prev : L;
         const float decay = r0 == 0 ? p.decay : 1.f;
-        auto fetch_id = [&](int j) {
-          const int slot = (pc.tile_begin + j) * kTile + key;
-          return j < tiles && slot < L ? bt[slot / kP] : INT_MIN;
-        };
-        auto fetch = [&](int j, int id, float& ks, float& old) {
-          ks = old = 0.f;
-          if (id < 0 || id >= p.num_pages) return;
-          const size_t page = (size_t)id * p.Hkv + h;
-          ks = __ldg(p.k_scales + page);
-          if ((pc.tile_begin + j) * kTile + key < had) old = before[page * kP + key % kP];
-        };
-        int j = (int)((set ^ pos) & 1);  // this set's first tile
-        int id = fetch_id(j), id_next = fetch_id(j + 2);
-        float ks, old;
-        fetch(j, id, ks, old);
         wait_all(q_full, pass & 1);
-        for (; ok && j < tiles; j += 2) {
-          float ks_next, old_next;
-          fetch(j + 2, id_next, ks_next, old_next);
-          const int id_after = fetch_id(j + 4);
-          const uint32_t at = (pos + (uint32_t)j) / 2;
-          wait_all(&acc_full[set], at & 1);
-          if (!ok) break;
-          tc::tc_fence_after();
-          const F2 k2 = f2_of(ks, ks);
-          F2 sum0 = f2_of(0.f, 0.f), sum1 = sum0;
-          uint32_t s0[32], s1[32];
-          auto add = [&](uint32_t (&s)[32], int col) {
+        // A pair's sums: a unit's group leaves its own, and when all are there each warp writes
+        // one page's (a half-warp adds a unit's), a pair later, so that nobody waits.
+        const int units = (cols + kUnit - 1) / kUnit;
+        size_t at = 0;
+        bool writes = false;
+        float old = 0.f;
+        auto finish = [&](uint32_t pr) {
+          const uint32_t side = pr % kAcc;
+          wait_all(&parts[side], (pr / kAcc) & 1);
+          if (!ok) return;
+          const float* part = s_part + (size_t)((side * 4 + (lane >> 4) * 2) * 2 + (warp >> 3)) * kTile + (warp & 7) * kP + (lane & 15);
+          const int first = (lane >> 4) * 2;
+          float all = first < 2 * units ? part[0] + part[2 * kTile] : 0.f;
+          all += __shfl_xor_sync(0xffffffffu, all, 16);
+          if (lane == 0) tc::mbar_arrive(&parts_read[side]);
+          if (writes) p.out[at] = fmaf(old, decay, all);
+        };
+        for (int j = 0; ok && j < tiles; j += 2, ++pair, unit += (uint32_t)units) {
+          const uint32_t side = pair % kAcc;
+          const int u = (int)((group - unit) % kAcc);  // the pair's unit that is this group's, if there is one
+          if (u < units) {
+            F2 k[2], sum[2][2];
+            wait_all(&acc_full[group], ((unit + (uint32_t)u) / kAcc) & 1);
+            if (!ok) break;
+            tc::tc_fence_after();
 #pragma unroll
-            for (int i = 0; i < 32; i += 4) {
-              const float4 u = s_col[(col + i) / 2], v = s_col[(col + i) / 2 + 1];
-              const F2 x = f2_fma(f2_mul(f2_of(__uint_as_float(s[i]), __uint_as_float(s[i + 1])), k2), f2_of(u.x, u.y),
-                                  f2_of(u.z, u.w));
-              const F2 y = f2_fma(f2_mul(f2_of(__uint_as_float(s[i + 2]), __uint_as_float(s[i + 3])), k2),
-                                  f2_of(v.x, v.y), f2_of(v.z, v.w));
-              sum0 = f2_add(sum0, f2_of(fast_exp2(f2_lo(x)), fast_exp2(f2_hi(x))));
-              sum1 = f2_add(sum1, f2_of(fast_exp2(f2_lo(y)), fast_exp2(f2_hi(y))));
+            for (int x = 0; x < 2; ++x) {
+              const float ks = __int_as_float(s_page[(pos + x) % kInfo * kPages + key / kP].y);
+              k[x] = f2_of(ks, ks);
+              sum[x][0] = sum[x][1] = f2_of(0.f, 0.f);
             }
-          };
-          tmem_ld_x32(addr, s0);
-          tmem_ld_wait(s0);
+            const int c0 = u * kUnit + half * 64, steps = max(0, min(8, (cols - c0) / 8));  // whole fours: cols are
+            const float4* col = s_col + c0 / 2;
+            uint32_t s[2][2][8];  // [turn][tile]: eight columns are added while eight are on their way
+            auto load = [&](int y, int turn) {  // (no second tile: what is left over there, and not used)
+              tmem_ld_x8(addr + y * 8, s[turn][0]);
+              tmem_ld_x8(addr + kUnit + y * 8, s[turn][1]);
+            };
+            auto add = [&](int y, int turn) {
+#pragma unroll
+              for (int i = 0; i < 8; i += 2) {
+                const float4 c = col[y * 4 + i / 2];
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {
+                  const uint32_t* v = s[turn][x] + i;
+                  const F2 z = f2_fma(f2_mul(f2_of(__uint_as_float(v[0]), __uint_as_float(v[1])), k[x]), f2_of(c.x, c.y),
+                                      f2_of(c.z, c.w));
+                  sum[x][i / 2 & 1] = f2_add(sum[x][i / 2 & 1], f2_of(fast_exp2(f2_lo(z)), fast_exp2(f2_hi(z))));
+                }
+              }
+            };
+            if (steps > 0) load(0, 0);
 #pragma unroll 1
-          for (int col = 0; col < cols; col += 64) {  // 32 columns in flight while 32 are added
-            if (col + 32 < cols) tmem_ld_x32(addr + col + 32, s1);
-            add(s0, col);
-            if (col + 32 < cols) {
-              tmem_ld_wait(s1);
-              if (col + 64 < cols) tmem_ld_x32(addr + col + 64, s0);
-              add(s1, col + 32);
-              if (col + 64 < cols) tmem_ld_wait(s0);
+            for (int y = 0; y < steps; y += 2) {
+              tmem_ld_wait(s[0][0], s[0][1]);
+              load(y + 1, 1);
+              add(y, 0);
+              tmem_ld_wait(s[1][0], s[1][1]);
+              if (y + 2 < steps) load(y + 2, 0);
+              add(y + 1, 1);
             }
+            tc::tc_fence_before();
+            __syncwarp();
+            if (lane == 0) tc::mbar_arrive(&acc_empty[group]);
+            if (pair >= kAcc) wait_all(&parts_read[side], ((pair / kAcc) - 1) & 1);
+            if (!ok) break;
+#pragma unroll
+            for (int x = 0; x < 2; ++x)
+              s_part[((side * 4 + u * 2 + half) * 2 + x) * kTile + key] =
+                  (f2_lo(sum[x][0]) + f2_hi(sum[x][0])) + (f2_lo(sum[x][1]) + f2_hi(sum[x][1]));
+          } else if (pair >= kAcc) {
+            wait_all(&parts_read[side], ((pair / kAcc) - 1) & 1);
+            if (!ok) break;
           }
-          tc::tc_fence_before();
           __syncwarp();
-          if (lane == 0) tc::mbar_arrive(&acc_empty[set]);
-          const float sum = (f2_lo(sum0) + f2_hi(sum0)) + (f2_lo(sum1) + f2_hi(sum1));
-          if (id >= 0 && id < p.num_pages) p.out[((size_t)id * p.Hkv + h) * kP + key % kP] = fmaf(old, decay, sum);
-          else if (id != INT_MIN) set_status(p.status, kStPages);
-          id = id_next;
-          id_next = id_after;
-          ks = ks_next;
-          old = old_next;
+          if (lane == 0) tc::mbar_arrive(&parts[side]);
+          if (j > 0) finish(pair - 1);
+          // what this warp will write, and the old weight
+          const int x = warp >> 3, id = j + x < tiles ? s_page[(pos + x) % kInfo * kPages + (warp & 7)].x : kNone;
+          const int slot = (pc.tile_begin + j + x) * kTile + (warp & 7) * kP + (lane & 15);
+          const bool good = id >= 0 && id < p.num_pages;
+          writes = good && lane < kP && slot < L;
+          at = ((size_t)(good ? id : 0) * p.Hkv + h) * kP + (lane & 15);
+          old = writes && slot < had ? before[at] : 0.f;
+          if (id != kNone && !good && lane == 0) set_status(p.status, kStPages);
+          pos += (uint32_t)min(2, tiles - j);
         }
+        if (ok) finish(pair - 1);
       }
     }
   }
