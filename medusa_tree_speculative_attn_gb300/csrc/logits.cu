@@ -16,6 +16,7 @@
 //   - changes the listed tokens of every row, a warp a row.
 // A node's path is a bit mask of its ancestors, and a tree token has the bit mask of the
 // nodes that hold it, so its count in a row is a population count.
+#include <atomic>
 #include <cmath>
 
 #include "serve.cuh"
@@ -27,9 +28,14 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kMaxSlice = 4096;
+constexpr int kMaxDevices = 64;
+constexpr int kCtas = 4;      // per SM, by registers
+constexpr int kMaxRows = 64;  // of a CTA
 constexpr unsigned kSeen = 0x80000000u;    // in a slice's count word: in the history
 constexpr unsigned kInTree = 0x40000000u;  // a tree token: listed apart
 constexpr unsigned kCount = 0x3fffffffu;
+constexpr int kPartBytes = 2048;           // of a row, that a warp takes at a time: four 16-byte vectors a lane
+constexpr int kPlace = kPartBytes + 16;    // its place in shared memory
 
 template <typename T> struct Lowest;
 template <> struct Lowest<float> { static constexpr uint32_t word = 0xff800000u, one = 0xff800000u; };
@@ -53,19 +59,31 @@ __device__ __forceinline__ unsigned mask_bits(const int* mask, int v) {
   return bits & ((1u << N) - 1u);
 }
 
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
 template <typename T>
-__global__ void __launch_bounds__(kThreads) logits_kernel(const LogitsParams p, int slice, int slices, int groups, int group_rows) {
-  constexpr int N = 16 / (int)sizeof(T);  // of a vector
-  extern __shared__ unsigned s_count[];                                     // [slice]
-  unsigned* s_entry = s_count + slice;                                      // [slice] bias entry + 1 (with biases)
+__global__ void __launch_bounds__(kThreads, kCtas) logits_kernel(const LogitsParams p, int slice, int slices, int groups, int group_rows) {
+  constexpr int N = 16 / (int)sizeof(T), kPart = kPartBytes / (int)sizeof(T);  // tokens of a vector, of a part
+  constexpr unsigned kAll = (1u << N) - 1u;
+  extern __shared__ __align__(16) uint8_t smem[];  // the warps' parts
+  unsigned* s_count = reinterpret_cast<unsigned*>(smem + kWarps * 2 * kPlace);  // [slice]
+  unsigned* s_entry = s_count + slice;                                          // [slice] bias entry + 1 (with biases)
   uint16_t* s_list = reinterpret_cast<uint16_t*>(s_count + (p.num_bias ? 2 : 1) * slice);  // [slice]
   __shared__ int s_listed, s_trees;
+  __shared__ int s_which[kMaxRows];
   __shared__ int s_tok[kMaxTree], s_par[kMaxTree], s_at[kMaxTree];
   __shared__ unsigned long long s_anc[kMaxTree], s_nodes[kMaxTree];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int v0 = blockIdx.x % slices * slice, group = blockIdx.x / slices % groups, b = blockIdx.x / slices / groups;
   const int n = min(slice, p.V - v0);
-  const int t0 = group * group_rows, t1 = min(t0 + group_rows, p.T);
+  const int t0 = group * group_rows, rows = min(group_rows, p.T - t0);
   pdl_wait();
   int len = 0, start = 0;
   if (p.history_lens) {
@@ -73,7 +91,18 @@ __global__ void __launch_bounds__(kThreads) logits_kernel(const LogitsParams p, 
     if (len < 0) return;  // no sequence
     start = p.output_starts ? p.output_starts[b] : 0;
   }
-  for (int i = tid; i < (p.num_bias ? 2 : 1) * slice; i += kThreads) s_count[i] = 0;
+  const T* in = static_cast<const T*>(p.logits) + (size_t)b * p.stride[0] + (size_t)t0 * p.stride[1] + v0;
+  T* out = static_cast<T*>(p.out) + (size_t)b * p.out_stride[0] + (size_t)t0 * p.out_stride[1] + v0;
+  const bool in_place = p.logits == p.out;
+  const int words = (p.V + 31) / 32;
+
+  // ---- the slice's tokens that matter ----
+  for (int i = tid; i < (p.num_bias ? 2 : 1) * slice / 4; i += kThreads)
+    reinterpret_cast<uint4*>(s_count)[i] = make_uint4(0, 0, 0, 0);
+  if (tid < rows) {  // each row's mask: -1 for none, num_masks for one past the last, which allows nothing
+    const int row = b * p.T + t0 + tid;
+    s_which[tid] = !p.mask ? -1 : p.mask_index ? min(max(p.mask_index[row], -1), p.num_masks) : row;
+  }
   if (tid == 0) s_listed = s_trees = 0;
   if (p.tree_tokens && tid < p.T) {
     s_tok[tid] = p.tree_tokens[(size_t)b * p.T + tid];
@@ -82,26 +111,40 @@ __global__ void __launch_bounds__(kThreads) logits_kernel(const LogitsParams p, 
     if (!ok) set_status(p.status, kStTree);
     s_par[tid] = ok ? par : -1;
   }
-  __syncthreads();
   const int* history = p.history + (size_t)b * p.history_width;
-#pragma unroll 4
-  for (int i = tid; i < len; i += kThreads) {
-    const unsigned at = (unsigned)(history[i] - v0);
-    if (at < (unsigned)n) {
-      if (i >= start) atomicAdd(&s_count[at], 1u);
-      else atomicOr(&s_count[at], kSeen);
+  int tok[16];
+  auto fetch = [&](int i0) {
+#pragma unroll
+    for (int e = 0; e < 16; ++e) {
+      const int i = i0 + e * kThreads + tid;
+      tok[e] = i < len ? history[i] : -1;
+    }
+  };
+  fetch(0);
+  __syncthreads();
+#pragma unroll 1
+  for (int i0 = 0; i0 < len; i0 += 16 * kThreads) {
+    if (i0) fetch(i0);
+#pragma unroll
+    for (int e = 0; e < 16; ++e) {
+      const unsigned at = (unsigned)tok[e] - (unsigned)v0;
+      if (tok[e] >= 0 && at < (unsigned)n) {
+        if (i0 + e * kThreads + tid >= start) atomicAdd(&s_count[at], 1u);
+        else atomicOr(&s_count[at], kSeen);
+      }
     }
   }
   for (int i = tid; i < p.num_bias; i += kThreads) {
-    const unsigned at = (unsigned)(p.bias_tokens[(size_t)b * p.num_bias + i] - v0);
-    if (at < (unsigned)n) atomicMax(&s_entry[at], (unsigned)i + 1u);
+    const int token = p.bias_tokens[(size_t)b * p.num_bias + i];
+    const unsigned at = (unsigned)token - (unsigned)v0;
+    if (token >= 0 && at < (unsigned)n) atomicMax(&s_entry[at], (unsigned)i + 1u);
   }
   if (p.tree_tokens && tid < p.T) {
     unsigned long long anc = 0, nodes = 0;
     for (int a = tid; a >= 0; a = s_par[a]) anc |= 1ull << a;  // parents are earlier: at most T steps
     s_anc[tid] = anc;
-    const unsigned at = (unsigned)(s_tok[tid] - v0);
-    if (at < (unsigned)n) {
+    const unsigned at = (unsigned)s_tok[tid] - (unsigned)v0;
+    if (s_tok[tid] >= 0 && at < (unsigned)n) {
       for (int a = 0; a < p.T; ++a)
         if (s_tok[a] == s_tok[tid]) nodes |= 1ull << a;
       if (__ffsll((long long)nodes) - 1 == tid) {  // the first of the nodes that hold it
@@ -117,111 +160,158 @@ __global__ void __launch_bounds__(kThreads) logits_kernel(const LogitsParams p, 
     const unsigned c = s_count[i];
     if (!(c & kInTree) && (c || (p.num_bias && s_entry[i]))) s_list[atomicAdd(&s_listed, 1)] = (uint16_t)i;
   }
-  const T* in = static_cast<const T*>(p.logits) + (size_t)b * p.stride[0] + v0;
-  T* out = static_cast<T*>(p.out) + (size_t)b * p.out_stride[0] + v0;
-  const bool in_place = p.logits == p.out;
-  const int words = (p.V + 31) / 32;
-  // a row's mask: -1 for none, num_masks for one past the last, which allows nothing
-  auto mask_of = [&](int t) {
-    if (!p.mask) return -1;
-    const int row = b * p.T + t;
-    return p.mask_index ? min(max(p.mask_index[row], -1), p.num_masks) : row;
-  };
-  for (int t = t0; t < t1; ++t) {
-    const int which = mask_of(t);
-    if (in_place && which < 0) continue;
-    const bool none = which == p.num_masks && which >= 0;
-    const int* mask = which >= 0 ? p.mask + (size_t)which * words : nullptr;
-    const T* src = in + (size_t)t * p.stride[1];
-    T* dst = out + (size_t)t * p.out_stride[1];
-    // elements up to the first 16-byte boundary of both, whole vectors, the rest
-    const unsigned off = (unsigned)(reinterpret_cast<uintptr_t>(dst) & 15);
-    int head = (int)((16 - off) & 15) / (int)sizeof(T), vecs = 0;
-    if ((reinterpret_cast<uintptr_t>(src) & 15) == off && head < n) vecs = (n - head) / N;
-    else head = n;
-    auto one = [&](int i) {
-      const bool no = none || (mask && !(mask_bits<1>(mask, v0 + i) & 1u));
-      if (no) dst[i] = minus_inf<T>();
-      else if (!in_place) dst[i] = src[i];
-    };
-    for (int i = tid; i < head; i += kThreads) one(i);
-    for (int i = head + vecs * N + tid; i < n; i += kThreads) one(i);
-#pragma unroll 4
-    for (int i = tid; i < vecs; i += kThreads) {
-      const int at = head + i * N;
-      const unsigned yes = none ? 0u : mask ? mask_bits<N>(mask, v0 + at) : (1u << N) - 1u;
-      uint4* d = reinterpret_cast<uint4*>(dst + at);
-      constexpr uint32_t low = Lowest<T>::word;
-      if (yes == 0) {
-        *d = make_uint4(low, low, low, low);
-      } else if (yes != (1u << N) - 1u || !in_place) {
-        T x[N];
-        const uint4 w = *reinterpret_cast<const uint4*>(src + at);
-        memcpy(x, &w, 16);
-#pragma unroll
-        for (int e = 0; e < N; ++e)
-          if (!(yes >> e & 1u)) x[e] = minus_inf<T>();
-        uint4 y;
-        memcpy(&y, x, 16);
-        *d = y;
-      }
-    }
-  }
-  __syncthreads();  // the list is whole, and the rows are copied
   const float rep = p.repetition ? p.repetition[b] : 1.f, pres = p.presence ? p.presence[b] : 0.f;
   const float freq = p.frequency ? p.frequency[b] : 0.f;
   const float* bias = p.bias_values + (size_t)b * p.num_bias;
-  const int listed = s_listed, trees = s_trees;
-  for (int t = t0 + warp; t < t1; t += kWarps) {
-    const int which = mask_of(t);
-    if (which >= 0 && which == p.num_masks) continue;
-    const int* mask = which >= 0 ? p.mask + (size_t)which * words : nullptr;
-    const T* src = in + (size_t)t * p.stride[1];
-    T* dst = out + (size_t)t * p.out_stride[1];
-    auto change = [&](int at, bool seen, unsigned count) {
-      if (mask && !(mask_bits<1>(mask, v0 + at) & 1u)) return;
-      float x = Act<T>::to_f(src[at]);
-      if (seen) x = x > 0.f ? __fdiv_rn(x, rep) : __fmul_rn(x, rep);
-      if (count) x = __fsub_rn(__fsub_rn(x, __fmul_rn(freq, (float)count)), pres);
-      if (p.num_bias && s_entry[at]) x = __fadd_rn(x, bias[s_entry[at] - 1]);
-      dst[at] = Act<T>::from_f(x);
-    };
-#pragma unroll 2
-    for (int i = lane; i < listed; i += 32) {
-      const int at = s_list[i];
-      const unsigned c = s_count[at];
-      change(at, c != 0, c & kCount);
-    }
-    if (trees) {
-      const unsigned long long anc = s_anc[t];
-      for (int i = lane; i < trees; i += 32) {
-        const int at = s_at[i];
-        const unsigned c = s_count[at] & ~kInTree, path = (unsigned)__popcll(anc & s_nodes[i]);
-        const unsigned count = (c & kCount) + path;
-        if (c || path || (p.num_bias && s_entry[at])) change(at, c || path, count);
+
+  // ---- the rows, a part of a row at a time: through shared memory where it is copied or masked ----
+  const int per = (n + kPart - 1) / kPart, items = rows * per;
+  uint8_t* place = smem + warp * (2 * kPlace);
+  const uint32_t place_u = static_cast<uint32_t>(__cvta_generic_to_shared(place));
+  // Element i of a part lies at its place as it lies to a 16-byte boundary in memory.
+  auto bring = [&](int item, int turn) {
+    if (item < items) {
+      const int t = item / per, c0 = item % per * kPart, m = min(kPart, n - c0), which = s_which[t];
+      if (!(in_place && which < 0) && !(which >= 0 && which == p.num_masks)) {
+        const T* src = in + (size_t)t * p.stride[1] + c0;
+        const unsigned off = (unsigned)(reinterpret_cast<uintptr_t>(src) & 15);
+        const int head = min(m, (int)((16 - off) & 15) / (int)sizeof(T)), vecs = (m - head) / N;
+        const uint32_t to = place_u + turn * kPlace + off + head * (int)sizeof(T);
+#pragma unroll
+        for (int k = 0; k < kPartBytes / 512; ++k) {
+          const int i = k * 32 + lane;
+          if (i < vecs) cp_async16(to + i * 16, src + head + i * N);
+        }
+        T* x = reinterpret_cast<T*>(place + turn * kPlace + off);
+        for (int i = lane; i < head; i += 32) x[i] = src[i];
+        for (int i = head + vecs * N + lane; i < m; i += 32) x[i] = src[i];
       }
     }
+    cp_commit();
+  };
+  // One of the tokens that matter in row t (entry e, token `at` of the slice).
+  auto change = [&](float y, int t, int e, int at, bool& same) {
+    const unsigned c = s_count[at] & ~kInTree, entry = p.num_bias ? s_entry[at] : 0u;
+    unsigned path = 0;
+    if (e >= s_listed) path = (unsigned)__popcll(s_anc[t0 + t] & s_nodes[e - s_listed]);
+    same = !(c | path | entry);
+    const unsigned count = (c & kCount) + path;
+    if (rep != 1.f && (c | path)) y = y > 0.f ? __fdiv_rn(y, rep) : __fmul_rn(y, rep);
+    if (count) y = __fsub_rn(__fsub_rn(y, __fmul_rn(freq, (float)count)), pres);
+    if (entry) y = __fadd_rn(y, bias[entry - 1]);
+    return y;
+  };
+  __syncthreads();  // the rows' masks, and the list, are whole
+  bring(warp, 0);
+  const int listed = s_listed, entries = listed + s_trees;
+  auto token = [&](int e) { return e < listed ? (int)s_list[e] : s_at[e - listed]; };
+  int turn = 0;
+#pragma unroll 1
+  for (int item = warp; item < items; item += kWarps, turn ^= 1) {
+    bring(item + kWarps, turn ^ 1);
+    cp_wait<1>();
+    __syncwarp();
+    const int t = item / per, c0 = item % per * kPart, m = min(kPart, n - c0), which = s_which[t];
+    const T* src = in + (size_t)t * p.stride[1] + c0;
+    T* dst = out + (size_t)t * p.out_stride[1] + c0;
+    if (in_place && which < 0) {  // nothing but those tokens
+#pragma unroll 2
+      for (int e = lane; e < entries; e += 32) {
+        const int at = token(e) - c0;
+        if (at < 0 || at >= m) continue;
+        bool same;
+        const float y = change(Act<T>::to_f(src[at]), t, e, at + c0, same);
+        if (!same) dst[at] = Act<T>::from_f(y);
+      }
+      continue;
+    }
+    const bool none = which >= 0 && which == p.num_masks;
+    const int* mask = which >= 0 && !none ? p.mask + (size_t)which * words : nullptr;
+    const unsigned off = (unsigned)(reinterpret_cast<uintptr_t>(src) & 15);
+    T* x = reinterpret_cast<T*>(place + turn * kPlace + off);
+    const int first = v0 + c0;
+    const int head = min(m, (int)((16 - off) & 15) / (int)sizeof(T)), vecs = (m - head) / N;
+    unsigned yes[kPartBytes / 512];
+#pragma unroll
+    for (int k = 0; k < kPartBytes / 512; ++k) {
+      const int i = k * 32 + lane;
+      yes[k] = none ? 0u : mask && i < vecs ? mask_bits<N>(mask, first + head + i * N) : kAll;
+    }
+    if (!none) {
+#pragma unroll 2
+      for (int e = lane; e < entries; e += 32) {
+        const int at = token(e) - c0;
+        if (at < 0 || at >= m) continue;
+        bool same;
+        const float y = change(Act<T>::to_f(x[at]), t, e, at + c0, same);
+        if (!same) x[at] = Act<T>::from_f(y);
+      }
+      __syncwarp();
+    }
+    auto one = [&](int i) {
+      dst[i] = none || (mask && !(mask_bits<1>(mask, first + i) & 1u)) ? minus_inf<T>() : x[i];
+    };
+    if ((reinterpret_cast<uintptr_t>(dst) & 15) == off) {
+#pragma unroll
+      for (int k = 0; k < kPartBytes / 512; ++k) {
+        const int i = k * 32 + lane;
+        if (i >= vecs) continue;
+        constexpr uint32_t low = Lowest<T>::word;
+        uint4 w = make_uint4(low, low, low, low);
+        if (yes[k] != 0u) w = *reinterpret_cast<const uint4*>(x + head + i * N);
+        if (yes[k] != 0u && yes[k] != kAll) {
+          T e[N];
+          memcpy(e, &w, 16);
+#pragma unroll
+          for (int q = 0; q < N; ++q)
+            if (!(yes[k] >> q & 1u)) e[q] = minus_inf<T>();
+          memcpy(&w, e, 16);
+        }
+        *reinterpret_cast<uint4*>(dst + head + i * N) = w;
+      }
+      for (int i = lane; i < head; i += 32) one(i);
+      for (int i = head + vecs * N + lane; i < m; i += 32) one(i);
+    } else {
+      for (int i = lane; i < m; i += 32) one(i);
+    }
+    __syncwarp();  // the place is filled again
   }
+  cp_wait<0>();
 }
 
 template <typename T>
 cudaError_t launch_t(const LogitsParams& p, cudaStream_t stream) {
-  int dev = 0, sms = 0;
+  static std::atomic<int> sms_of[kMaxDevices];
+  int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
-  e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-  if (e != cudaSuccess) return e;
-  int slice = kMaxSlice, groups = 1;
-  auto slices = [&] { return (p.V + slice - 1) / slice; };
-  auto ctas = [&] { return (long long)p.B * slices() * groups; };
-  while (ctas() < 4LL * sms && groups < p.T) groups = groups * 2 < p.T ? groups * 2 : p.T;
-  while (ctas() < 2LL * sms && slice > 1024) slice /= 2;
+  int sms = dev >= 0 && dev < kMaxDevices ? sms_of[dev].load(std::memory_order_acquire) : 0;
+  if (!sms) {
+    e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    if (e != cudaSuccess) return e;
+    e = cudaFuncSetAttribute(logits_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             kWarps * 2 * kPlace + (kMaxSlice + 64) * 10);
+    if (e != cudaSuccess) return e;
+    if (dev >= 0 && dev < kMaxDevices) sms_of[dev].store(sms, std::memory_order_release);
+  }
+  // Rows are shared out where even the smallest slices, a warp's part, would leave SMs without
+  // work; then a sequence's slices, so many that the CTAs fill the SMs once.  With few rows a
+  // slice is as long as shared memory allows: every slice goes over the whole history.
+  constexpr int kPart = kPartBytes / (int)sizeof(T);
+  int groups = (p.T + kMaxRows - 1) / kMaxRows;
+  const int parts = (p.V + kPart - 1) / kPart;
+  while ((long long)p.B * parts * groups < 2LL * sms && groups < p.T) groups = groups * 2 < p.T ? groups * 2 : p.T;
   const int group_rows = (p.T + groups - 1) / groups;
   groups = (p.T + group_rows - 1) / group_rows;
-  const long long blocks = ctas();
+  const int least = group_rows >= kWarps ? parts : (p.V + kMaxSlice - 1) / kMaxSlice;
+  const long long fill = (long long)kCtas * sms / ((long long)p.B * groups);
+  int slices = (int)(fill < least ? least : fill > 2 * parts ? 2 * parts : fill);
+  const int slice = ((p.V + slices - 1) / slices + 63) / 64 * 64;
+  slices = (p.V + slice - 1) / slice;
+  const long long blocks = (long long)p.B * groups * slices;
   if (blocks >= (1ll << 31)) return cudaErrorInvalidValue;
-  const size_t smem = (size_t)slice * ((p.num_bias ? 8 : 4) + 2);
-  return launch_pdl(logits_kernel<T>, dim3((unsigned)blocks), dim3(kThreads), smem, stream, p, slice, slices(), groups,
+  const size_t smem = kWarps * 2 * kPlace + (size_t)slice * ((p.num_bias ? 8 : 4) + 2);
+  return launch_pdl(logits_kernel<T>, dim3((unsigned)blocks), dim3(kThreads), smem, stream, p, slice, slices, groups,
                     group_rows);
 }
 
