@@ -7,15 +7,21 @@
 //   x_v = -inf                                             where the row's mask says no
 // in 32 bits with one rounding to the logits' type; other entries keep their bits.
 //
-// Bound by memory, and few entries change: a CTA takes a slice of the vocabulary and some of
-// a sequence's rows.  It counts the slice's tokens of the history in shared memory (integer
-// atomics: any order gives the same counts), lists the tokens that matter once, and then
-//   - goes over the rows in 16-byte vectors where something has to be copied or masked (in
-//     place, a row without a mask is not touched, and whole vectors of masked tokens are
-//     written without being read);
-//   - changes the listed tokens of every row, a warp a row.
-// A node's path is a bit mask of its ancestors, and a tree token has the bit mask of the
-// nodes that hold it, so its count in a row is a population count.
+// Few entries change, and the rest is a copy: a CTA takes a slice of the vocabulary and some
+// of a sequence's rows.  It counts the slice's tokens of the history in shared memory (integer
+// atomics: any order gives the same counts) and lists the tokens that matter, once for all
+// rows.  Then a warp takes a part of a row at a time through shared memory: brought
+// asynchronously while the one before is worked on, the tokens that matter changed where they
+// lie, written in 16-byte vectors with -inf where the mask says so.  In place, a row without a
+// mask is not copied; its listed tokens alone are read and written.  A node's path is a bit
+// mask of its ancestors, and a tree token has the bit mask of the nodes that hold it, so its
+// count in a row is a population count.
+//
+// 16 trees of 64 nodes, 32000 bf16 logits, histories of 2048 to 4096 tokens, a third of the
+// rows under a mask: 36 us for 133 MB, 3.7 TB/s (54 % of a copy): 6 for the lists, 25 for the
+// copy, the rest instructions of the 1600 tokens a row that change.  With the changes made in
+// global memory behind the copy it took 42, with eight rows a thread on their way 47.  One row
+// of 32000 fp32 logits: 3.8 us, a launch and three dependent trips to memory.
 #include <atomic>
 #include <cmath>
 
@@ -34,6 +40,7 @@ constexpr int kMaxRows = 64;  // of a CTA
 constexpr unsigned kSeen = 0x80000000u;    // in a slice's count word: in the history
 constexpr unsigned kInTree = 0x40000000u;  // a tree token: listed apart
 constexpr unsigned kCount = 0x3fffffffu;
+constexpr int kBiased = 1 << 16;           // in a token's place: it has a bias
 constexpr int kPartBytes = 2048;           // of a row, that a warp takes at a time: four 16-byte vectors a lane
 constexpr int kPlace = kPartBytes + 16;    // its place in shared memory
 
@@ -71,6 +78,7 @@ __device__ __forceinline__ void cp_wait() {
 template <typename T>
 __global__ void __launch_bounds__(kThreads, kCtas) logits_kernel(const LogitsParams p, int slice, int slices, int groups, int group_rows) {
   constexpr int N = 16 / (int)sizeof(T), kPart = kPartBytes / (int)sizeof(T);  // tokens of a vector, of a part
+  constexpr int K = kPartBytes / 512;  // vectors of a part per lane
   constexpr unsigned kAll = (1u << N) - 1u;
   extern __shared__ __align__(16) uint8_t smem[];  // the warps' parts
   unsigned* s_count = reinterpret_cast<unsigned*>(smem + kWarps * 2 * kPlace);  // [slice]
@@ -122,6 +130,33 @@ __global__ void __launch_bounds__(kThreads, kCtas) logits_kernel(const LogitsPar
   };
   fetch(0);
   __syncthreads();
+  // The rows go through shared memory where they are copied or masked, a warp a part of a row at
+  // a time, the next one on its way: element i of a part lies at its place as it lies to a
+  // 16-byte boundary in memory.
+  const int per = (n + kPart - 1) / kPart, items = rows * per;
+  uint8_t* place = smem + warp * (2 * kPlace);
+  const uint32_t place_u = static_cast<uint32_t>(__cvta_generic_to_shared(place));
+  auto bring = [&](int item, int turn) {
+    if (item < items) {
+      const int t = item / per, c0 = item % per * kPart, m = min(kPart, n - c0), which = s_which[t];
+      if (!(in_place && which < 0) && !(which >= 0 && which == p.num_masks)) {
+        const T* src = in + (size_t)t * p.stride[1] + c0;
+        const unsigned off = (unsigned)(reinterpret_cast<uintptr_t>(src) & 15);
+        const int head = min(m, (int)((16 - off) & 15) / (int)sizeof(T)), vecs = (m - head) / N;
+        const uint32_t to = place_u + turn * kPlace + off + head * (int)sizeof(T);
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+          const int i = k * 32 + lane;
+          if (i < vecs) cp_async16(to + i * 16, src + head + i * N);
+        }
+        T* x = reinterpret_cast<T*>(place + turn * kPlace + off);
+        for (int i = lane; i < head; i += 32) x[i] = src[i];
+        for (int i = head + vecs * N + lane; i < m; i += 32) x[i] = src[i];
+      }
+    }
+    cp_commit();
+  };
+  bring(warp, 0);
 #pragma unroll 1
   for (int i0 = 0; i0 < len; i0 += 16 * kThreads) {
     if (i0) fetch(i0);
@@ -164,65 +199,66 @@ __global__ void __launch_bounds__(kThreads, kCtas) logits_kernel(const LogitsPar
   const float freq = p.frequency ? p.frequency[b] : 0.f;
   const float* bias = p.bias_values + (size_t)b * p.num_bias;
 
-  // ---- the rows, a part of a row at a time: through shared memory where it is copied or masked ----
-  const int per = (n + kPart - 1) / kPart, items = rows * per;
-  uint8_t* place = smem + warp * (2 * kPlace);
-  const uint32_t place_u = static_cast<uint32_t>(__cvta_generic_to_shared(place));
-  // Element i of a part lies at its place as it lies to a 16-byte boundary in memory.
-  auto bring = [&](int item, int turn) {
-    if (item < items) {
-      const int t = item / per, c0 = item % per * kPart, m = min(kPart, n - c0), which = s_which[t];
-      if (!(in_place && which < 0) && !(which >= 0 && which == p.num_masks)) {
-        const T* src = in + (size_t)t * p.stride[1] + c0;
-        const unsigned off = (unsigned)(reinterpret_cast<uintptr_t>(src) & 15);
-        const int head = min(m, (int)((16 - off) & 15) / (int)sizeof(T)), vecs = (m - head) / N;
-        const uint32_t to = place_u + turn * kPlace + off + head * (int)sizeof(T);
-#pragma unroll
-        for (int k = 0; k < kPartBytes / 512; ++k) {
-          const int i = k * 32 + lane;
-          if (i < vecs) cp_async16(to + i * 16, src + head + i * N);
-        }
-        T* x = reinterpret_cast<T*>(place + turn * kPlace + off);
-        for (int i = lane; i < head; i += 32) x[i] = src[i];
-        for (int i = head + vecs * N + lane; i < m; i += 32) x[i] = src[i];
-      }
-    }
-    cp_commit();
-  };
-  // One of the tokens that matter in row t (entry e, token `at` of the slice).
-  auto change = [&](float y, int t, int e, int at, bool& same) {
-    const unsigned c = s_count[at] & ~kInTree, entry = p.num_bias ? s_entry[at] : 0u;
-    unsigned path = 0;
-    if (e >= s_listed) path = (unsigned)__popcll(s_anc[t0 + t] & s_nodes[e - s_listed]);
-    same = !(c | path | entry);
-    const unsigned count = (c & kCount) + path;
-    if (rep != 1.f && (c | path)) y = y > 0.f ? __fdiv_rn(y, rep) : __fmul_rn(y, rep);
-    if (count) y = __fsub_rn(__fsub_rn(y, __fmul_rn(freq, (float)count)), pres);
-    if (entry) y = __fadd_rn(y, bias[entry - 1]);
-    return y;
-  };
-  __syncthreads();  // the rows' masks, and the list, are whole
-  bring(warp, 0);
+  __syncthreads();  // the list is whole
   const int listed = s_listed, entries = listed + s_trees;
-  auto token = [&](int e) { return e < listed ? (int)s_list[e] : s_at[e - listed]; };
+  // One of the tokens that matter: its place in the slice (-1: none), what it is, what is
+  // taken off for its count, its bias.  A tree token's count is the row's.
+  struct Token {
+    int at;
+    unsigned what;  // kSeen, and the count that is not a path's; kInTree: and a path's
+    float sub, add;
+  };
+  auto token = [&](int e) {
+    Token k{-1, 0u, 0.f, 0.f};
+    if (e >= entries) return k;
+    k.at = e < listed ? (int)s_list[e] : s_at[e - listed];
+    k.what = s_count[k.at];
+    k.sub = __fmul_rn(freq, (float)(k.what & kCount));
+    const unsigned entry = p.num_bias ? s_entry[k.at] : 0u;
+    if (entry) k.add = bias[entry - 1];
+    if (entry) k.at |= kBiased;
+    return k;
+  };
+  // Its new value in row t; false: as it was.
+  auto change = [&](const Token& k, int e, int t, float& y) {
+    unsigned c = k.what & ~kInTree;
+    float sub = k.sub;
+    if (k.what & kInTree) {
+      const unsigned path = (unsigned)__popcll(s_anc[t0 + t] & s_nodes[e - listed]);
+      c += path;
+      sub = __fmul_rn(freq, (float)(c & kCount));
+    }
+    if (rep != 1.f && c) y = y > 0.f ? __fdiv_rn(y, rep) : __fmul_rn(y, rep);
+    if (c & kCount) y = __fsub_rn(__fsub_rn(y, sub), pres);
+    if (k.at & kBiased) y = __fadd_rn(y, k.add);
+    return c || (k.at & kBiased);
+  };
+  // The first of them stay with their lanes for all rows.
+  constexpr int kHeld = 2;
+  Token held[kHeld];
+#pragma unroll
+  for (int q = 0; q < kHeld; ++q) held[q] = token(q * 32 + lane);
+  // All of them that lie in tokens c0 .. c0 + m - 1 of row t, from `x` to `y`.
+  auto change_all = [&](int t, int c0, int m, const T* x, T* y) {
+    auto one = [&](const Token& k, int e) {
+      const int at = k.at < 0 ? -1 : (k.at & ~kBiased) - c0;
+      if (at < 0 || at >= m) return;
+      float v = Act<T>::to_f(x[at]);
+      if (change(k, e, t, v)) y[at] = Act<T>::from_f(v);
+    };
+#pragma unroll
+    for (int q = 0; q < kHeld; ++q) one(held[q], q * 32 + lane);
+    for (int e = kHeld * 32 + lane; e < entries; e += 32) one(token(e), e);
+  };
   int turn = 0;
 #pragma unroll 1
   for (int item = warp; item < items; item += kWarps, turn ^= 1) {
     bring(item + kWarps, turn ^ 1);
-    cp_wait<1>();
-    __syncwarp();
     const int t = item / per, c0 = item % per * kPart, m = min(kPart, n - c0), which = s_which[t];
     const T* src = in + (size_t)t * p.stride[1] + c0;
     T* dst = out + (size_t)t * p.out_stride[1] + c0;
     if (in_place && which < 0) {  // nothing but those tokens
-#pragma unroll 2
-      for (int e = lane; e < entries; e += 32) {
-        const int at = token(e) - c0;
-        if (at < 0 || at >= m) continue;
-        bool same;
-        const float y = change(Act<T>::to_f(src[at]), t, e, at + c0, same);
-        if (!same) dst[at] = Act<T>::from_f(y);
-      }
+      change_all(t, c0, m, src, dst);
       continue;
     }
     const bool none = which >= 0 && which == p.num_masks;
@@ -231,21 +267,16 @@ __global__ void __launch_bounds__(kThreads, kCtas) logits_kernel(const LogitsPar
     T* x = reinterpret_cast<T*>(place + turn * kPlace + off);
     const int first = v0 + c0;
     const int head = min(m, (int)((16 - off) & 15) / (int)sizeof(T)), vecs = (m - head) / N;
-    unsigned yes[kPartBytes / 512];
+    unsigned yes[K];
 #pragma unroll
-    for (int k = 0; k < kPartBytes / 512; ++k) {
+    for (int k = 0; k < K; ++k) {
       const int i = k * 32 + lane;
       yes[k] = none ? 0u : mask && i < vecs ? mask_bits<N>(mask, first + head + i * N) : kAll;
     }
+    cp_wait<1>();
+    __syncwarp();
     if (!none) {
-#pragma unroll 2
-      for (int e = lane; e < entries; e += 32) {
-        const int at = token(e) - c0;
-        if (at < 0 || at >= m) continue;
-        bool same;
-        const float y = change(Act<T>::to_f(x[at]), t, e, at + c0, same);
-        if (!same) x[at] = Act<T>::from_f(y);
-      }
+      change_all(t, c0, m, x, x);
       __syncwarp();
     }
     auto one = [&](int i) {
@@ -253,7 +284,7 @@ __global__ void __launch_bounds__(kThreads, kCtas) logits_kernel(const LogitsPar
     };
     if ((reinterpret_cast<uintptr_t>(dst) & 15) == off) {
 #pragma unroll
-      for (int k = 0; k < kPartBytes / 512; ++k) {
+      for (int k = 0; k < K; ++k) {
         const int i = k * 32 + lane;
         if (i >= vecs) continue;
         constexpr uint32_t low = Lowest<T>::word;
