@@ -14,6 +14,7 @@
 // is encoded again, value / new scale, which loses only codes that underflow.
 //
 // Bound by memory: every kept row is read and written once, the weights are read once.
+#include <atomic>
 #include <cmath>
 
 #include "serve.cuh"
@@ -23,10 +24,9 @@ namespace mt {
 namespace {
 
 constexpr int kP = 16;
-constexpr int kSelWarps = 16;
-constexpr int kSelThreads = kSelWarps * 32;
+constexpr int kMaxDevices = 64;
 constexpr int kBins = 2048;
-constexpr int kMaxKeys = 40960;  // in shared memory
+constexpr int kMaxKeys = 24576;  // in shared memory: two CTAs of 1024 threads an SM
 
 // Keys in the order of the weights: NaN lowest, -0 as +0.
 __device__ __forceinline__ uint32_t key_of(float w) {
@@ -35,10 +35,13 @@ __device__ __forceinline__ uint32_t key_of(float w) {
   return (b & 0x80000000u) ? ~b : (b | 0x80000000u);
 }
 
-__global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictParams p, int max_keys) {
-  extern __shared__ uint32_t s_keys[];  // [max_keys]
+// THREADS: 512 or 1024.
+template <int THREADS>
+__global__ void __launch_bounds__(THREADS) evict_select_kernel(const EvictParams p, int max_keys) {
+  constexpr int WARPS = THREADS / 32, PER = kBins / THREADS;
+  extern __shared__ uint4 s_keys[];  // [max_keys / 4], four slots each
   __shared__ unsigned s_bins[kBins];
-  __shared__ int s_warp[kSelWarps], s_warp2[kSelWarps];
+  __shared__ int s_warp[WARPS], s_warp2[WARPS];
   __shared__ unsigned s_bin;
   __shared__ int s_left;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -50,25 +53,61 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictPa
     if (tid == 0) set_status(p.status, kStPages);
     return;
   }
+  if (tid == 0) {
+    s_bin = 0;
+    s_left = 0;
+  }
   int* kept = p.kept + ((size_t)b * p.Hkv + h) * p.budget;
   if (L <= p.budget) {
-    for (int i = tid; i < p.budget; i += kSelThreads) kept[i] = i < L ? i : -1;
+    for (int i = tid; i < p.budget; i += THREADS) kept[i] = i < L ? i : -1;
     return;
   }
-  // the slots between: count of them, and how many stay
-  const int lo = p.sinks, count = L - p.recent - lo, stay = p.budget - p.sinks - p.recent;
+  // the slots between, lo .. hi - 1, and how many of them stay
+  const int lo = p.sinks, hi = L - p.recent, stay = p.budget - p.sinks - p.recent;
+  const int quads = (hi + 3) / 4, q_lo = lo / 4;
   const int* bt = p.block_tables + (size_t)b * p.max_blocks;
-  auto fetch = [&](int i) {
-    const int slot = lo + i, page = bt[slot / kP];
-    if (page < 0 || page >= p.num_pages) return 0u;  // reported by whoever moves it or its neighbours
-    return key_of(p.weights[((size_t)page * p.Hkv + h) * kP + slot % kP]);
+  auto keys_of = [&](int page, int q) {
+    if (page < 0 || page >= p.num_pages) return make_uint4(0, 0, 0, 0);  // reported by whoever moves it
+    const float4 w = *reinterpret_cast<const float4*>(p.weights + ((size_t)page * p.Hkv + h) * kP + q % 4 * 4);
+    return make_uint4(key_of(w.x), key_of(w.y), key_of(w.z), key_of(w.w));
   };
-  const bool held = count <= max_keys;
+  const bool held = quads * 4 <= max_keys;
   if (held) {
-#pragma unroll 4
-    for (int i = tid; i < count; i += kSelThreads) s_keys[i] = fetch(i);
+    for (int q0 = q_lo + tid; q0 < quads; q0 += 4 * THREADS) {  // four pages' numbers, then their weights on their way
+      int page[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) page[e] = q0 + e * THREADS < quads ? bt[(q0 + e * THREADS) / 4] : -1;
+      uint4 k[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) k[e] = keys_of(page[e], q0 + e * THREADS);
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        if (q0 + e * THREADS < quads) s_keys[q0 + e * THREADS] = k[e];
+    }
   }
-  auto key = [&](int i) { return held ? s_keys[i] : fetch(i); };
+  // the keys of slots 4 q .. 4 q + 3, and which of them are between
+  auto quad = [&](int q, uint32_t (&k)[4]) {
+    const uint4 v = held ? s_keys[q] : keys_of(bt[q / 4], q);
+    k[0] = v.x;
+    k[1] = v.y;
+    k[2] = v.z;
+    k[3] = v.w;
+    unsigned in = 0;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) in |= (4 * q + e >= lo && 4 * q + e < hi ? 1u : 0u) << e;
+    return in;
+  };
+  auto scan = [&](unsigned v) {  // of a warp, inclusive
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const unsigned u = __shfl_up_sync(0xffffffffu, v, o);
+      if (lane >= o) v += u;
+    }
+    return v;
+  };
+  auto before_warp = [&](const int* x) {  // sum of the warps before this one
+    return __reduce_add_sync(0xffffffffu, lane < warp ? (unsigned)x[lane] : 0u);
+  };
   // the key of the last that stays, by digits; `left`: how many of its equals stay
   uint32_t cut = 0;
   int left = stay;
@@ -76,33 +115,30 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictPa
 #pragma unroll 1
     for (int pass = 0; pass < 3; ++pass) {
       const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0, bits = pass == 2 ? 10 : 11;
-      for (int i = tid; i < kBins; i += kSelThreads) s_bins[i] = 0;
-      __syncthreads();
-      for (int i = tid; i < count; i += kSelThreads) {
-        const uint32_t k = key(i);
-        if (pass == 0 || (k >> (shift + bits)) == (cut >> (shift + bits)))
-          atomicAdd(&s_bins[(k >> shift) & ((1u << bits) - 1u)], 1u);
+      for (int i = tid; i < kBins; i += THREADS) s_bins[i] = 0;
+      __syncthreads();  // (the keys are there, too)
+      for (int q = q_lo + tid; q < quads; q += THREADS) {
+        uint32_t k[4];
+        const unsigned in = quad(q, k);
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if ((in >> e & 1u) && (pass == 0 || (k[e] >> (shift + bits)) == (cut >> (shift + bits))))
+            atomicAdd(&s_bins[(k[e] >> shift) & ((1u << bits) - 1u)], 1u);
       }
       __syncthreads();
-      // bins from the top: a thread has four neighbours, thread 0 the highest
-      unsigned c[4], sum = 0;
+      // bins from the top: a thread has PER neighbours, thread 0 the highest
+      unsigned c[PER], sum = 0;
 #pragma unroll
-      for (int e = 0; e < 4; ++e) sum += c[e] = s_bins[kBins - 1 - 4 * tid - e];
-      unsigned incl = sum;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const unsigned v = __shfl_up_sync(0xffffffffu, incl, o);
-        if (lane >= o) incl += v;
-      }
+      for (int e = 0; e < PER; ++e) sum += c[e] = s_bins[kBins - 1 - PER * tid - e];
+      const unsigned incl = scan(sum);
       if (lane == 31) s_warp[warp] = (int)incl;
       __syncthreads();
-      unsigned before = incl - sum;
-      for (int w = 0; w < warp; ++w) before += (unsigned)s_warp[w];
+      unsigned before = incl - sum + before_warp(s_warp);
       if (before < (unsigned)left && before + sum >= (unsigned)left) {
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
+        for (int e = 0; e < PER; ++e) {
           if (before < (unsigned)left && before + c[e] >= (unsigned)left) {
-            s_bin = kBins - 1 - 4 * tid - e;
+            s_bin = kBins - 1 - PER * tid - e;
             s_left = left - (int)before;
           }
           before += c[e];
@@ -111,46 +147,66 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictPa
       __syncthreads();
       cut |= s_bin << shift;
       left = s_left;
-      __syncthreads();
     }
   }
   // which stay: every warp counts those of its range above the cut and on it
-  const int per = ((count + kSelWarps - 1) / kSelWarps + 31) / 32 * 32;
-  const int i0 = min(warp * per, count), i1 = min(i0 + per, count);
+  const int per = ((quads - q_lo + WARPS - 1) / WARPS + 31) / 32 * 32;
+  const int i0 = min(q_lo + warp * per, quads), i1 = min(i0 + per, quads);
   int above = 0, equal = 0;
   if (stay > 0) {
-    for (int i = i0 + lane; i < i1; i += 32) {
-      const uint32_t k = key(i);
-      above += k > cut;
-      equal += k == cut;
+    for (int q = i0 + lane; q < i1; q += 32) {
+      uint32_t k[4];
+      const unsigned in = quad(q, k);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        above += (in >> e & 1u) && k[e] > cut;
+        equal += (in >> e & 1u) && k[e] == cut;
+      }
     }
     above = __reduce_add_sync(0xffffffffu, above);
     equal = __reduce_add_sync(0xffffffffu, equal);
   }
+  __syncthreads();  // everybody has read s_warp
   if (lane == 0) {
     s_warp[warp] = above;
     s_warp2[warp] = equal;
   }
   __syncthreads();
-  int eq_before = 0, at = p.sinks;  // places: the sinks first
-  for (int w = 0; w < warp; ++w) {
-    at += s_warp[w] + max(min(s_warp2[w], left - eq_before), 0);
-    eq_before += s_warp2[w];
-  }
+  // places: the sinks first, then what is above the cut and the first `left` on it
+  int eq_before = (int)before_warp(s_warp2);
+  int at = p.sinks + (int)before_warp(s_warp) + min(eq_before, left);
   if (stay > 0) {
-    for (int i = i0; i < i1; i += 32) {
-      const bool in = i + lane < i1;
-      const uint32_t k = in ? key(i + lane) : 0u;
-      const unsigned eq = __ballot_sync(0xffffffffu, in && k == cut), below = (1u << lane) - 1u;
-      const bool stays = in && (k > cut || (k == cut && eq_before + __popc(eq & below) < left));
-      const unsigned all = __ballot_sync(0xffffffffu, stays);
-      if (stays) kept[at + __popc(all & below)] = lo + i + lane;
-      at += __popc(all);
-      eq_before += __popc(eq);
+    for (int q0 = i0; q0 < i1; q0 += 32) {
+      uint32_t k[4] = {0, 0, 0, 0};
+      const unsigned in = q0 + lane < i1 ? quad(q0 + lane, k) : 0u;
+      unsigned eq = 0, gt = 0;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        gt |= ((in >> e & 1u) && k[e] > cut ? 1u : 0u) << e;
+        eq |= ((in >> e & 1u) && k[e] == cut ? 1u : 0u) << e;
+      }
+      // equals in the lanes before, then places: two counts in one scan each
+      const int n = (int)scan(__popc(eq));
+      const int eq_all = __shfl_sync(0xffffffffu, n, 31);
+      int rank = eq_before + n - __popc(eq);
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        if (eq >> e & 1u) gt |= (rank++ < left ? 1u : 0u) << e;  // from here on: all that stay
+      const int m = (int)scan(__popc(gt));
+      int to = at + m - __popc(gt);
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        if (gt >> e & 1u) {
+          // (always: but where the weights lie in memory only, somebody may change them meanwhile)
+          if (to < p.budget - p.recent) kept[to] = 4 * (q0 + lane) + e;
+          ++to;
+        }
+      at += __shfl_sync(0xffffffffu, m, 31);
+      eq_before += eq_all;
     }
   }
-  for (int i = tid; i < p.sinks; i += kSelThreads) kept[i] = i;
-  for (int i = tid; i < p.recent; i += kSelThreads) kept[p.budget - p.recent + i] = L - p.recent + i;
+  for (int i = tid; i < p.sinks; i += THREADS) kept[i] = i;
+  for (int i = tid; i < p.recent; i += THREADS) kept[p.budget - p.recent + i] = L - p.recent + i;
 }
 
 constexpr int kMoveWarps = 4;
@@ -171,10 +227,12 @@ __global__ void __launch_bounds__(kMoveWarps * 32) evict_move_kernel(const Evict
   if (n <= 0) return;
   // lane r < 16: where row r comes from
   const int r = lane & 15;
-  const int slot = r < n ? p.kept[((size_t)b * p.Hkv + h) * p.budget + j * kP + r] : 0;
+  int slot = r < n ? p.kept[((size_t)b * p.Hkv + h) * p.budget + j * kP + r] : 0;
+  const bool stray = slot < 0 || slot >= L;  // not as select leaves it
+  if (stray) slot = 0;
   const int to = p.new_tables[(size_t)b * p.new_blocks + j];
   const int from = p.block_tables[(size_t)b * p.max_blocks + slot / kP];
-  if (__any_sync(0xffffffffu, (r < n && (from < 0 || from >= p.num_pages)) || to < 0 || to >= p.num_pages)) {
+  if (__any_sync(0xffffffffu, stray || (r < n && (from < 0 || from >= p.num_pages)) || to < 0 || to >= p.num_pages)) {
     if (lane == 0) set_status(p.status, kStPages);
     return;
   }
@@ -259,11 +317,27 @@ cudaError_t launch_move(const EvictParams& p, cudaStream_t stream) {
 cudaError_t launch_kv_evict(const EvictParams& p, cudaStream_t stream) {
   const long long rows = (long long)p.B * p.Hkv;
   if (rows >= (1ll << 31)) return cudaErrorInvalidValue;
-  const long long slots = (long long)p.max_blocks * kP - p.sinks - p.recent;
-  const int keys = (int)(slots < 0 ? 0 : slots < kMaxKeys ? slots : kMaxKeys);
-  cudaError_t e = cudaFuncSetAttribute(evict_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxKeys * 4);
+  static std::atomic<int> sms_of[kMaxDevices];
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
-  e = launch_pdl(evict_select_kernel, dim3((unsigned)rows), dim3(kSelThreads), (size_t)keys * 4, stream, p, keys);
+  int sms = dev >= 0 && dev < kMaxDevices ? sms_of[dev].load(std::memory_order_acquire) : 0;
+  if (!sms) {
+    e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    if (e == cudaSuccess)
+      e = cudaFuncSetAttribute(evict_select_kernel<512>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxKeys * 4);
+    if (e == cudaSuccess)
+      e = cudaFuncSetAttribute(evict_select_kernel<1024>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxKeys * 4);
+    if (e != cudaSuccess) return e;
+    if (dev >= 0 && dev < kMaxDevices) sms_of[dev].store(sms, std::memory_order_release);
+  }
+  const long long slots = (long long)p.max_blocks * kP;
+  const int keys = (int)(slots < kMaxKeys ? slots : kMaxKeys);
+  // few rows: as many threads as there are for each; more: all rows at once
+  if (rows <= 2LL * sms)
+    e = launch_pdl(evict_select_kernel<1024>, dim3((unsigned)rows), dim3(1024), (size_t)keys * 4, stream, p, keys);
+  else
+    e = launch_pdl(evict_select_kernel<512>, dim3((unsigned)rows), dim3(512), (size_t)keys * 4, stream, p, keys);
   if (e != cudaSuccess) return e;
   if (p.k_scales) return p.row_bytes == 64 ? launch_move<64, true>(p, stream) : launch_move<128, true>(p, stream);
   switch (p.row_bytes) {
