@@ -572,7 +572,7 @@ def _invoke(fn, what, dev, stream, *args):
         stream = torch._C._cuda_getCurrentRawStream(dev.index)
     elif hasattr(stream, "cuda_stream"):
         stream = stream.cuda_stream
-    if torch.cuda.current_device() == dev.index:
+    if torch._C._cuda_getDevice() == dev.index:
         st = fn(*args, stream)
     else:
         with torch.cuda.device(dev):
@@ -868,32 +868,46 @@ def process_logits(logits, out, *, status_ws: torch.Tensor, history=None, histor
         if v > 1 and st[-1] != 1:
             raise ValueError(f"{name} must have dense rows")
         strides += [st[0] if b > 1 else 0, 0 if two or t <= 1 else st[1]]
-    f32, i32, rows = torch.float32, torch.int32, (b,) if two else (b, t)
-    opt = lambda x, name, ty, shp: None if x is None else _arg(x, name, ty, shp, dev)  # noqa: E731
-    width = lambda x, name: x.shape[1] if isinstance(x, torch.Tensor) and x.dim() == 2 else _two_dims(x, name)  # noqa: E731
-    h, k, m = width(history, "history"), width(bias_tokens, "bias_tokens"), 0
-    for x, y, names in ((history, history_lens, "history and history_lens"), (bias_tokens, bias_values, "bias_tokens and bias_values")):
-        if (x is None) != (y is None):
-            raise ValueError(f"{names} go together")
+    f32, i32, one, rows = torch.float32, torch.int32, (b,), (b,) if two else (b, t)
+    # (no helper between: this call has the most arguments)
+    h = k = m = 0
+    hist = lens = starts = rep = pres = freq = tok = val = msk = idx = tree = par = None
+    if (history is None) != (history_lens is None) or (bias_tokens is None) != (bias_values is None):
+        raise ValueError("history and history_lens go together, and bias_tokens and bias_values")
+    if history is not None:
+        h = _width(history, "history")
+        hist, lens = _arg(history, "history", i32, (b, h), dev), _arg(history_lens, "history_lens", i32, one, dev)
+    if output_starts is not None:
+        starts = _arg(output_starts, "output_starts", i32, one, dev)
+    if repetition is not None:
+        rep = _arg(repetition, "repetition", f32, one, dev)
+    if presence is not None:
+        pres = _arg(presence, "presence", f32, one, dev)
+    if frequency is not None:
+        freq = _arg(frequency, "frequency", f32, one, dev)
+    if bias_tokens is not None:
+        k = _width(bias_tokens, "bias_tokens")
+        tok, val = _arg(bias_tokens, "bias_tokens", i32, (b, k), dev), _arg(bias_values, "bias_values", f32, (b, k), dev)
     if mask is not None:
-        width(mask, "mask")
+        _width(mask, "mask")
         m = mask.shape[0]
-    desc = _LOGITS_DESC.pack(b, t, v, dt, h, k, m, *strides)
-    _invoke(_load().mt_process_logits, "mt_process_logits", dev, stream, desc, logits.data_ptr(), out.data_ptr(),
-            opt(history, "history", i32, (b, h)), opt(history_lens, "history_lens", i32, (b,)),
-            opt(output_starts, "output_starts", i32, (b,)), opt(repetition, "repetition", f32, (b,)),
-            opt(presence, "presence", f32, (b,)), opt(frequency, "frequency", f32, (b,)),
-            opt(bias_tokens, "bias_tokens", i32, (b, k)), opt(bias_values, "bias_values", f32, (b, k)),
-            opt(mask, "mask", i32, (m, (v + 31) // 32)), opt(mask_index, "mask_index", i32, rows),
-            opt(tree_tokens, "tree_tokens", i32, rows), opt(tree_parents, "tree_parents", i32, rows),
-            _status_arg(status_ws, "status_ws", dev))
+        msk = _arg(mask, "mask", i32, (m, (v + 31) // 32), dev)
+    if mask_index is not None:
+        idx = _arg(mask_index, "mask_index", i32, rows, dev)
+    if tree_tokens is not None:
+        tree = _arg(tree_tokens, "tree_tokens", i32, rows, dev)
+    if tree_parents is not None:
+        par = _arg(tree_parents, "tree_parents", i32, rows, dev)
+    _invoke(_load().mt_process_logits, "mt_process_logits", dev, stream,
+            _LOGITS_DESC.pack(b, t, v, dt, h, k, m, *strides), logits.data_ptr(), out.data_ptr(), hist, lens, starts, rep,
+            pres, freq, tok, val, msk, idx, tree, par, _status_arg(status_ws, "status_ws", dev))
     return out
 
 
-def _two_dims(x, name):
-    if x is not None:
+def _width(x, name):
+    if not isinstance(x, torch.Tensor) or x.dim() != 2:
         raise ValueError(f"{name} must be a tensor of 2 dims")
-    return 0
+    return x.shape[1]
 
 
 def sample_tokens(logits, uniforms, tokens, *, temperature=None, top_k=None, top_p=None, min_p=None,
