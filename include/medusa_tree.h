@@ -525,7 +525,8 @@ int mt_kv_attn_weights(const mt_attn_desc* desc, int max_depth, float decay, con
  * for itself.  The kept slots in ascending order become slots 0 .. n-1 of the pages
  * new_tables[b][0 ..]: their keys, values and weights are copied there.
  *   kept int32 [B][Hkv][budget] out: the old slot of each new one, -1 from n on
- *   weights fp32 [num_pages][Hkv][16], as mt_kv_attn_weights writes them
+ *   weights fp32 [num_pages][Hkv][16], as mt_kv_attn_weights writes them; slots appended
+ *   since have none of their own yet, and belong among the `recent` ones
  *   new_tables int32 [B][new_blocks_per_seq], new_blocks_per_seq * 16 >= budget: pages
  *   that no sequence of the call is read from, each listed once; entries behind the
  *   ceil(n / 16)-th are not used

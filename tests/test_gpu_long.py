@@ -799,3 +799,115 @@ def test_slot_weights_wait_bound():
     finally:
         mt.debug_set_wait()
     _weights_check(c, None, None, 1.0, True)
+
+
+# ---- the operators together ---------------------------------------------------------
+
+def test_a_long_conversation_in_a_bounded_cache():
+    """Two layers, three turns: a tree step over the cache with its log-sum-exp, acceptance, the accepted path's weights,
+    the path appended, the cache brought back to its budget, the next token drawn from processed logits; each result
+    against the plain implementations, and the next turn on what this one left."""
+    rng = np.random.default_rng(70)
+    b, t, hq, hkv, d, v, dt = 2, 8, 8, 2, 128, 500, torch.bfloat16
+    budget, sinks, recent = 48, 2, 12
+    lens, blocks, pages = [61, 40], 6, 60
+    free = [int(p) for p in rng.permutation(pages)]
+    table = np.full((b, blocks), -1, np.int32)
+    for i, n in enumerate(lens):
+        for j in range(-(-(n + t) // P)):
+            table[i, j] = free.pop()
+    parents = np.array([[-1, 0, 0, 1, 1, 2, 3, 3]] * b)
+    history = np.full((b, 40), -1, np.int32)
+    history[:, :10] = rng.integers(0, v, (b, 10))
+    said = [10, 10]  # tokens of each history; the first ten are the prompt's
+    ws = _status()
+
+    def cache():
+        c = dict(k=np.zeros((pages, hkv, P, d), np.uint8), v=np.zeros((pages, hkv, P, d), np.uint8), ks=np.ones((pages, hkv)), vs=np.ones((pages, hkv)))
+        for x, s in (("k", "ks"), ("v", "vs")):
+            for i, n in enumerate(lens):
+                for p in range(-(-n // P)):
+                    for h in range(hkv):
+                        m = min(P, n - p * P)
+                        c[x][table[i, p], h, :m], c[s][table[i, p], h] = ref.block_codes(rng.standard_normal((m, d)))
+        c |= dict(K=_f8(c["k"]), V=_f8(c["v"]), KS=torch.from_numpy(c["ks"]).float().cuda(), VS=torch.from_numpy(c["vs"]).float().cuda(),
+                  W=torch.rand(pages, hkv, P, device="cuda"), prev=list(lens))
+        return c
+
+    def back(c):
+        """The layer's state on the host, as the last call left it."""
+        c["k"], c["v"] = _codes(c["K"]).copy(), _codes(c["V"]).copy()
+        c["ks"], c["vs"] = c["KS"].cpu().double().numpy(), c["VS"].cpu().double().numpy()
+
+    layers = [cache() for _ in range(2)]
+    for turn in range(3):
+        tokens = rng.integers(0, v, (b, t))
+        logits = _rand(rng, b, t, v, scale=2.0)
+        end = [5, 3]
+        for i, e in enumerate(end):  # the path to node e is accepted
+            n = e
+            while parents[i, n] >= 0:
+                logits[i, parents[i, n], tokens[i, n]] = 30.0
+                n = parents[i, n]
+            for c in range(t):
+                if parents[i, c] == e:
+                    logits[i, e, tokens[i, c]] = -30.0
+        alen, path = torch.zeros(b, dtype=torch.int32, device="cuda"), torch.zeros(b, 4, dtype=torch.int32, device="cuda")
+        mt.tree_accept_greedy(_i32(tokens).cuda(), logits.cuda(), _i32(parents).cuda(), alen, path, argmax_out=torch.zeros(b, t, dtype=torch.int32, device="cuda"),
+                              next_token=torch.zeros(b, dtype=torch.int32, device="cuda"), workspace=mt.alloc_accept_workspace(b, t))
+        hpath, hlen = path.cpu().numpy(), alen.cpu().numpy()
+        assert hlen.tolist() == [2, 2] and [hpath[i, 2] for i in range(b)] == end
+        dlens, dtab = _i32(lens).cuda(), _i32(table).cuda()
+        grown = [n + int(m) + 1 for n, m in zip(lens, hlen)]
+        new_table = np.full((b, blocks), -1, np.int32)
+        for i, n in enumerate(grown):
+            for j in range(-(-min(n, budget) // P)):
+                new_table[i, j] = free.pop()
+        for c in layers:
+            q, kn, vn = (_rand(rng, b, t, h, d, dtype=dt, scale=s) for h, s in ((hq, 2.0), (hkv, 1.0), (hkv, 1.0)))
+            step = dict(c, q=q, kn=kn, vn=vn, table=table, lens=lens, parents=parents)
+            out, lse = torch.empty(b, t, hq, d, dtype=dt, device="cuda"), torch.empty(b, t, hq, device="cuda")
+            aws = mt.alloc_block8_workspace(out, c["K"], dtab)
+            attn = (q.cuda(), c["K"], c["V"], c["KS"], c["VS"], dtab, dlens, _i32(parents).cuda(), out)
+            mt.tree_attn_paged_block8(*attn, k_new=kn.cuda(), v_new=vn.cuda(), workspace=aws, window=20, sinks=sinks)  # a windowed layer's view of it
+            _window_check(step, out, None, 20, sinks)
+            mt.tree_attn_paged_block8(*attn, k_new=kn.cuda(), v_new=vn.cuda(), workspace=aws, lse=lse)
+            assert mt.read_status(aws) == 0
+            _window_check(step, out, lse, 0, 0)
+            old = c["W"].cpu().numpy()
+            mt.kv_attn_weights(q.cuda(), c["K"], c["KS"], dtab, dlens, lse, c["W"], prev_lens=_i32(c["prev"]).cuda(), accept_path=path, accept_len=alen, decay=0.9, status_ws=ws)
+            want, tol = lref.weights64(step, old, lse.cpu().double().numpy(), lens, c["prev"], lambda i: hpath[i][:hlen[i] + 1], 0.9, d ** -0.5)
+            assert (np.abs(c["W"].cpu().double().numpy() - want) <= tol + 2.0 ** -24 * np.abs(want)).all()
+            mt.kv_append_accepted(kn.cuda(), vn.cuda(), path, alen, c["K"], c["V"], dtab, dlens, status_ws=ws, k_scales=c["KS"], v_scales=c["VS"])
+            back(c)
+            weights, kept = c["W"].cpu().numpy(), torch.empty(b, hkv, budget, dtype=torch.int32, device="cuda")
+            mt.kv_evict(c["K"], c["V"], c["W"], dtab, _i32(grown).cuda(), _i32(new_table).cuda(), kept, sinks=sinks, recent=recent, k_scales=c["KS"], v_scales=c["VS"], status_ws=ws)
+            want = lref.evict("block8", [c["k"], c["v"]], [c["ks"], c["vs"]], weights, table, grown, new_table, budget, sinks, recent)
+            assert np.array_equal(kept.cpu().numpy(), want)
+            assert np.array_equal(_codes(c["K"]), c["k"]) and np.array_equal(_codes(c["V"]), c["v"]) and np.array_equal(c["W"].cpu().numpy(), weights)
+            assert np.array_equal(c["KS"].cpu().double().numpy(), c["ks"]) and np.array_equal(c["VS"].cpu().double().numpy(), c["vs"])
+            c["prev"] = [min(n, budget) for n in grown]
+        free += [int(p) for p in table.ravel() if p >= 0]
+        table, lens = new_table, [min(n, budget) for n in grown]
+        for i, n in enumerate(lens):  # room for the next tree
+            for j in range(-(-n // P), -(-(n + t) // P)):
+                table[i, j] = free.pop()
+        # the next token: from the end nodes' logits, the path's tokens penalised, a grammar over one of them
+        x = logits.cuda().clone()
+        case = dict(x=logits, history=history, lens=np.array(said), starts=np.array([10, 10]), rep=np.float32([1.2, 1.0]), pres=np.float32([0.5, 0.0]), freq=np.float32([0.0, 0.3]),
+                    bias=(np.array([[7], [8]]), np.float32([[2.0], [-1.0]])), mask=rng.random((1, v)) < 0.5, index=np.where(np.arange(t) == end[0], 0, -1)[None].repeat(b, 0),
+                    tokens=tokens, parents=parents)
+        mt.process_logits(x, x, **_logits_kw(case, ws))
+        _logits_check(case, x)
+        rows, u = [int(end[i]) + i * t for i in range(b)], rng.random(b)
+        got = torch.empty(b, dtype=torch.int32, device="cuda")
+        f32 = lambda a: torch.tensor(a, dtype=torch.float32, device="cuda")  # noqa: E731
+        mt.sample_tokens(x.view(b * t, v), f32(u), got, temperature=f32([0.8] * b), top_k=_i32([40] * b).cuda(), row_index=_i32(rows).cuda())
+        f = lambda a: np.float64(np.float32(a))  # noqa: E731
+        y = x.view(b * t, v).cpu().double().numpy()
+        assert got.tolist() == [ref.sample64(y[rows[i]], f(u[i]), f(0.8), 40, 1.0, 0.0) for i in range(b)]
+        for i in range(b):
+            new = [int(tokens[i, n]) for n in hpath[i][:hlen[i] + 1]]
+            history[i, said[i]:said[i] + len(new)] = new
+            said[i] += len(new)
+    assert mt.read_status(ws) == 0
