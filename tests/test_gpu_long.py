@@ -410,7 +410,7 @@ def test_evict(kind, dtype, case):
 
 
 @pytest.mark.parametrize("what", ["equal", "zero", "negative", "odd", "close", "two"])
-@pytest.mark.parametrize("longest", [700, 44000])  # keys in shared memory, and more of them
+@pytest.mark.parametrize("longest", [700, 44000, 60000])  # keys in shared memory, and more of them
 def test_evict_ties_and_odd_weights(what, longest):
     rng = np.random.default_rng(50)
     e = Evict(rng, "e4m3", torch.bfloat16, 2, 64, [longest, 600], 500)
@@ -911,3 +911,14 @@ def test_a_long_conversation_in_a_bounded_cache():
             history[i, said[i]:said[i] + len(new)] = new
             said[i] += len(new)
     assert mt.read_status(ws) == 0
+
+
+@pytest.mark.parametrize("b, hkv, longest", [(100, 4, 300), (200, 2, 2500), (50, 8, 30000)])
+def test_evict_many_rows(b, hkv, longest):
+    # more rows than SMs: fewer threads for short tables, less shared memory for long ones
+    rng = np.random.default_rng(59)
+    lens = [int(n) for n in rng.integers(-1, 90, b)]
+    lens[3], lens[b - 1] = longest, longest - 7
+    e = Evict(rng, "e4m3", torch.bfloat16, hkv, 64, lens, 40)
+    e.run(3, 9)
+    e.check(3, 9)
