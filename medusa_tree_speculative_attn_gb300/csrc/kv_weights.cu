@@ -96,17 +96,25 @@ __global__ void __launch_bounds__(kThreads, Cfg<D>::CTAS) kv_weights_kernel(cons
   a.max_blocks = p.max_blocks;
   a.seq_lens = p.seq_lens;
   a.status = p.status;
-  block8_prefix<kWarps>(a, s_pfx, s_warp, blockIdx.x == 0);
+  const int total = block8_prefix<kWarps>(a, s_pfx, s_warp, blockIdx.x == 0);
   Sched sc = sched;
   sc.tile_pfx = s_pfx;
-  PieceIter it;
-  it.init(sc, blockIdx.x);
+  __shared__ PieceRec s_pieces[kMaxPieceRecs];
+  __shared__ int s_npieces;
+  if (warp == 0) {
+    const int n = list_pieces(sc, total, s_pieces, p.seq_lens);
+    if (lane == 0) s_npieces = n;
+  }
+  __syncthreads();
+  PieceSrc it;
+  it.init(s_pieces, s_npieces, sc, blockIdx.x, p.seq_lens);
+  int L = 0;
   uint8_t* ring = smem + warp * (DEPTH * C::kSlot);
   const uint32_t ring_u = static_cast<uint32_t>(__cvta_generic_to_shared(ring));
   Piece pc;
-  while (it.next(pc)) {  // every thread walks with the same values
+  while (it.next(pc, L)) {  // every thread walks with the same values
     const int b = pc.b, h = pc.kvh;
-    const int L = p.seq_lens[b], npages = (L + kP - 1) / kP;
+    const int npages = (L + kP - 1) / kP;
     int nodes = p.T;
     const int* path = nullptr;
     if (p.accept_path) {
@@ -290,7 +298,7 @@ cudaError_t launch_t(const WeightsParams& p, cudaStream_t stream) {
   }
   const int most = p.rows < kMaxRows ? (p.rows + 7) & ~7 : kMaxRows;
   const size_t smem = C::kRing + (size_t)most * (D * 2 + sizeof(float2)) + 4 * ((size_t)p.B + 1);
-  int per_sm = (int)(232448 / (smem + 1024));
+  int per_sm = (int)(232448 / (smem + 2304));  // and 1280 bytes of static memory, and the system's 1024
   per_sm = per_sm < 1 ? 1 : per_sm < C::CTAS ? per_sm : C::CTAS;
   // no more CTAs than tiles that the tables can hold
   const long long tiles = (long long)p.B * p.Hkv * ((p.max_blocks + 3) / 4);

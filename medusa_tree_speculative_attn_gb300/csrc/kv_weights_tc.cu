@@ -229,25 +229,6 @@ __device__ __forceinline__ float place_query(const QueryPart<T>& q, float scale_
   return amax < INFINITY ? scale * scale_log2 : __int_as_float(0x7fffffff);
 }
 
-// The pieces of this CTA, by a whole warp with the same values in every lane; their number,
-// -1 for more than a list holds.
-template <typename I>
-__device__ __forceinline__ int list_pieces(const Sched& sc, PieceRec* recs, const int* seq_lens) {
-  PieceIterT<I> it;
-  it.init(sc, blockIdx.x);
-  Piece pc;
-  int n = 0;
-  while (it.next(pc)) {
-    if (n == kMaxPieceRecs) return -1;
-    PieceRec r;
-    r.b = pc.b; r.kvh = pc.kvh; r.rg = pc.rg; r.seg = pc.seg;
-    r.tile_begin = pc.tile_begin; r.tile_end = pc.tile_end; r.slot = pc.slot;
-    r.L = seq_lens[pc.b];
-    recs[n++] = r;
-  }
-  return n;
-}
-
 template <typename T, int D, int NP>
 __global__ void __launch_bounds__(kThreads, 1)
     kv_weights_tc_kernel(const __grid_constant__ CUtensorMap map_k, const WeightsParams p, const Sched sched) {
@@ -316,9 +297,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   // this CTA's pieces, listed once by a warp (the walk's divisions are slow in 64 bits)
   __shared__ int s_npieces;
   if (warp == kCopyWarp) {
-    const long long nseg = (long long)sc.B * sc.Hkv;
-    const bool small = ((long long)total * sc.Hkv + sc.seg_cost * nseg) * (sc.G + 1) < (1LL << 31);
-    const int n = small ? list_pieces<int>(sc, s_pieces, p.seq_lens) : list_pieces<long long>(sc, s_pieces, p.seq_lens);
+    const int n = list_pieces(sc, total, s_pieces, p.seq_lens);
     if (lane == 0) s_npieces = n;
   }
   __syncthreads();

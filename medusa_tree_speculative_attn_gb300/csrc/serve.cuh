@@ -370,6 +370,32 @@ __device__ __forceinline__ int block8_prefix(const AttnParams& a, int* pfx, int*
   return carry;
 }
 
+// The pieces of this CTA, by a whole warp with the same values in every lane; their number,
+// -1 for more than a list holds.  `total`: the tiles of all sequences (the walk's divisions are
+// slow in 64 bits, and not needed where its products fit in 32).
+template <typename I>
+__device__ __forceinline__ int list_pieces_as(const Sched& sc, PieceRec* recs, const int* seq_lens) {
+  PieceIterT<I> it;
+  it.init(sc, blockIdx.x);
+  Piece pc;
+  int n = 0;
+  while (it.next(pc)) {
+    if (n == kMaxPieceRecs) return -1;
+    PieceRec r;
+    r.b = pc.b; r.kvh = pc.kvh; r.rg = pc.rg; r.seg = pc.seg;
+    r.tile_begin = pc.tile_begin; r.tile_end = pc.tile_end; r.slot = pc.slot;
+    r.L = seq_lens[pc.b];
+    recs[n++] = r;
+  }
+  return n;
+}
+
+__device__ __forceinline__ int list_pieces(const Sched& sc, int total, PieceRec* recs, const int* seq_lens) {
+  const long long segs = (long long)sc.B * sc.Hkv * sc.nrg;
+  const bool small = ((long long)total * sc.Hkv * sc.nrg + sc.seg_cost * segs) * (sc.G + 1) < (1LL << 31);
+  return small ? list_pieces_as<int>(sc, recs, seq_lens) : list_pieces_as<long long>(sc, recs, seq_lens);
+}
+
 // How a call runs: the tensor-core kernel or the register-fragment kernel, its
 // row group, row groups per KV head, persistent CTAs, and the cost of starting a
 // piece (in 64-slot tiles).
