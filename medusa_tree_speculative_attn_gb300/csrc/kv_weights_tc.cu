@@ -488,12 +488,26 @@ __global__ void __launch_bounds__(kThreads, 1)
         // one page's (a half-warp adds a unit's), a pair later, so that nobody waits.
         const int units = (cols + kUnit - 1) / kUnit;
         size_t at = 0;
-        bool writes = false;
+        bool writes = false, known = false;
         float old = 0.f;
+        int last_j = 0;
+        uint32_t last_pos = 0;
+        // What this warp writes of the pair that begins with tile j, and the old weight.  The
+        // pair's pages may be looked at by who has seen its scores, or the others' sums of it.
+        auto look = [&](int j, uint32_t ps) {
+          const int x = warp >> 3, id = j + x < tiles ? s_page[(ps + x) % kInfo * kPages + (warp & 7)].x : kNone;
+          const int slot = (pc.tile_begin + j + x) * kTile + (warp & 7) * kP + (lane & 15);
+          const bool good = id >= 0 && id < p.num_pages;
+          writes = good && lane < kP && slot < L;
+          at = ((size_t)(good ? id : 0) * p.Hkv + h) * kP + (lane & 15);
+          old = writes && slot < had ? before[at] : 0.f;
+          if (id != kNone && !good && lane == 0) set_status(p.status, kStPages);
+        };
         auto finish = [&](uint32_t pr) {
           const uint32_t side = pr % kAcc;
           wait_all(&parts[side], (pr / kAcc) & 1);
           if (!ok) return;
+          if (!known) look(last_j, last_pos);
           const float* part = s_part + (size_t)((side * 4 + (lane >> 4) * 2) * 2 + (warp >> 3)) * kTile + (warp & 7) * kP + (lane & 15);
           const int first = (lane >> 4) * 2;
           float all = first < 2 * units ? part[0] + part[2 * kTile] : 0.f;
@@ -561,14 +575,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           __syncwarp();
           if (lane == 0) tc::mbar_arrive(&parts[side]);
           if (j > 0) finish(pair - 1);
-          // what this warp will write, and the old weight
-          const int x = warp >> 3, id = j + x < tiles ? s_page[(pos + x) % kInfo * kPages + (warp & 7)].x : kNone;
-          const int slot = (pc.tile_begin + j + x) * kTile + (warp & 7) * kP + (lane & 15);
-          const bool good = id >= 0 && id < p.num_pages;
-          writes = good && lane < kP && slot < L;
-          at = ((size_t)(good ? id : 0) * p.Hkv + h) * kP + (lane & 15);
-          old = writes && slot < had ? before[at] : 0.f;
-          if (id != kNone && !good && lane == 0) set_status(p.status, kStPages);
+          known = u < units;
+          if (known) look(j, pos);
+          last_j = j;
+          last_pos = pos;
           pos += (uint32_t)min(2, tiles - j);
         }
         if (ok) finish(pair - 1);

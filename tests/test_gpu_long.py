@@ -922,3 +922,20 @@ def test_evict_many_rows(b, hkv, longest):
     e = Evict(rng, "e4m3", torch.bfloat16, hkv, 64, lens, 40)
     e.run(3, 9)
     e.check(3, 9)
+
+
+@pytest.mark.parametrize("t, hq, hkv", [(41, 4, 2), (33, 2, 1), (16, 16, 2)])  # 82, 66 and 128 rows a head: a unit a pair of tiles
+def test_slot_weights_of_one_unit_a_pair_of_tiles(t, hq, hkv):
+    c = _attn_case(np.random.default_rng(68), 1, t, hq, hkv, 64, [9000], "bf16", "chain")
+    lse = torch.zeros(1, t, hq, device="cuda")
+    args = (c["q"].cuda() * 0.1, _f8(c["k"]), torch.from_numpy(c["ks"]).float().cuda(), _i32(c["table"]).cuda(), _i32(c["lens"]).cuda(), lse)
+    ws, w = _status(), torch.zeros(c["k"].shape[0], hkv, P, device="cuda")
+    mt.kv_attn_weights(*args, w, status_ws=ws)
+    for _ in range(50):  # the CTAs' roles meet in another order every time
+        again = torch.zeros_like(w)
+        mt.kv_attn_weights(*args, again, status_ws=ws)
+        assert torch.equal(again, w)
+    assert mt.read_status(ws) == 0
+    c["q"] = (c["q"].cuda() * 0.1).cpu()
+    want, tol = lref.weights64(c, np.zeros(w.shape, np.float32), lse.cpu().double().numpy(), c["lens"], [0], lambda i: range(t), 1.0, 64 ** -0.5)
+    assert (np.abs(w.cpu().double().numpy() - want) <= tol).all()
