@@ -5,7 +5,7 @@
 // Into new pages and not in place, so that a prompt's pages that other sequences share stay
 // whole, no row waits for another to be read, and a call that is repeated gives the same.
 //
-// Two kernels.  select: a CTA per (sequence, KV head) finds the weight that the cut falls on
+// Two kernels, and one that does both for few short rows.  select: a CTA per (sequence, KV head) finds the weight that the cut falls on
 // by a radix select over order-preserving keys (11, 11 and 10 bits), which lie in shared
 // memory as far as they fit, and lists the kept slots; every warp has a contiguous range of
 // slots, so their order costs one scan over warps.  move: a warp per (new page, KV head)
@@ -18,7 +18,7 @@
 // 160 us for 966 MB, 6.0 TB/s (88 % of a copy), of which select takes 17 and move, at a copy's
 // rate, 142; 16 prompts of 4000 to 16384 to 2048 slots of a 16-bit cache: 60 us, select 18 for
 // 128 CTAs of up to 16k keys, which three passes of a digit and two of counting go over; one
-// sequence of 4224: 11 us, two launches and their chains.  (A slot a thread and 512 threads:
+// sequence of 4224: 10.5 us, a chain of passes.  (A slot a thread and 512 threads:
 // select 37 us for the prompts.)  Rows of 64 bytes: 55 % of a copy, two pages a warp no faster.
 #include <atomic>
 #include <cmath>
@@ -41,31 +41,23 @@ __device__ __forceinline__ uint32_t key_of(float w) {
   return (b & 0x80000000u) ? ~b : (b | 0x80000000u);
 }
 
-// THREADS: 256, 512 or 1024.
-template <int THREADS>
-__global__ void __launch_bounds__(THREADS) evict_select_kernel(const EvictParams p, int max_keys) {
+// The slots of (sequence b, KV head h) that stay, by a block of THREADS threads: keep(i, slot)
+// is called for every place i of the first min(L, budget), by some thread.  L: the sequence's
+// slots, within the table.  s_keys: [max_keys / 4], four slots each.
+template <int THREADS, typename Keep>
+__device__ __forceinline__ void select_slots(const EvictParams& p, int b, int h, int L, uint4* s_keys, int max_keys, Keep keep) {
   constexpr int WARPS = THREADS / 32, PER = kBins / THREADS;
-  extern __shared__ uint4 s_keys[];  // [max_keys / 4], four slots each
   __shared__ unsigned s_bins[kBins];
   __shared__ int s_warp[WARPS], s_warp2[WARPS];
   __shared__ unsigned s_bin;
   __shared__ int s_left;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int h = blockIdx.x % p.Hkv, b = blockIdx.x / p.Hkv;
-  pdl_wait();
-  const int L = p.seq_lens[b];
-  if (L < 0) return;
-  if ((long long)L > (long long)p.max_blocks * kP) {
-    if (tid == 0) set_status(p.status, kStPages);
-    return;
-  }
   if (tid == 0) {
     s_bin = 0;
     s_left = 0;
   }
-  int* kept = p.kept + ((size_t)b * p.Hkv + h) * p.budget;
   if (L <= p.budget) {
-    for (int i = tid; i < p.budget; i += THREADS) kept[i] = i < L ? i : -1;
+    for (int i = tid; i < L; i += THREADS) keep(i, i);
     return;
   }
   // the slots between, lo .. hi - 1, and how many of them stay
@@ -204,36 +196,48 @@ __global__ void __launch_bounds__(THREADS) evict_select_kernel(const EvictParams
       for (int e = 0; e < 4; ++e)
         if (gt >> e & 1u) {
           // (always: but where the weights lie in memory only, somebody may change them meanwhile)
-          if (to < p.budget - p.recent) kept[to] = 4 * (q0 + lane) + e;
+          if (to < p.budget - p.recent) keep(to, 4 * (q0 + lane) + e);
           ++to;
         }
       at += __shfl_sync(0xffffffffu, m, 31);
       eq_before += eq_all;
     }
   }
-  for (int i = tid; i < p.sinks; i += THREADS) kept[i] = i;
-  for (int i = tid; i < p.recent; i += THREADS) kept[p.budget - p.recent + i] = L - p.recent + i;
+  for (int i = tid; i < p.sinks; i += THREADS) keep(i, i);
+  for (int i = tid; i < p.recent; i += THREADS) keep(p.budget - p.recent + i, L - p.recent + i);
+}
+
+// THREADS: 256, 512 or 1024.
+template <int THREADS>
+__global__ void __launch_bounds__(THREADS) evict_select_kernel(const EvictParams p, int max_keys) {
+  extern __shared__ uint4 s_keys[];
+  const int h = blockIdx.x % p.Hkv, b = blockIdx.x / p.Hkv;
+  pdl_wait();
+  const int L = p.seq_lens[b];
+  if (L < 0) return;
+  if ((long long)L > (long long)p.max_blocks * kP) {
+    if (threadIdx.x == 0) set_status(p.status, kStPages);
+    return;
+  }
+  int* kept = p.kept + ((size_t)b * p.Hkv + h) * p.budget;
+  select_slots<THREADS>(p, b, h, L, s_keys, max_keys, [&](int i, int slot) { kept[i] = slot; });
+  for (int i = L + threadIdx.x; i < p.budget; i += THREADS) kept[i] = -1;
 }
 
 constexpr int kMoveWarps = 4;
 
-// RB: bytes of a row.
+// New page j of (sequence b, KV head h), by a warp.  RB: bytes of a row.  L: the sequence's
+// slots; kept: where the page's rows come from.
 template <int RB, bool SCALED>
-__global__ void __launch_bounds__(kMoveWarps * 32) evict_move_kernel(const EvictParams p, int pages_out, long long items) {
+__device__ __forceinline__ void move_page(const EvictParams& p, int b, int h, int j, int L, const int* kept) {
   constexpr int LPR = RB / 16;                       // lanes per row (16-byte words), at most 32
   constexpr int RPS = 32 / LPR, STEPS = kP / RPS;    // rows a step
   const int lane = threadIdx.x & 31;
-  const long long item = (long long)blockIdx.x * kMoveWarps + (threadIdx.x >> 5);
-  if (item >= items) return;
-  pdl_wait();
-  const int h = (int)(item % p.Hkv), j = (int)(item / p.Hkv % pages_out), b = (int)(item / p.Hkv / pages_out);
-  const int L = p.seq_lens[b];
-  if (L < 0 || (long long)L > (long long)p.max_blocks * kP) return;
   const int n = min(L, p.budget) - j * kP;  // rows of this page
   if (n <= 0) return;
   // lane r < 16: where row r comes from
   const int r = lane & 15;
-  int slot = r < n ? p.kept[((size_t)b * p.Hkv + h) * p.budget + j * kP + r] : 0;
+  int slot = r < n ? kept[r] : 0;
   const bool stray = slot < 0 || slot >= L;  // not as select leaves it
   if (stray) slot = 0;
   const int to = p.new_tables[(size_t)b * p.new_blocks + j];
@@ -310,6 +314,69 @@ __global__ void __launch_bounds__(kMoveWarps * 32) evict_move_kernel(const Evict
 }
 
 template <int RB, bool SCALED>
+__global__ void __launch_bounds__(kMoveWarps * 32) evict_move_kernel(const EvictParams p, int pages_out, long long items) {
+  const long long item = (long long)blockIdx.x * kMoveWarps + (threadIdx.x >> 5);
+  if (item >= items) return;
+  pdl_wait();
+  const int h = (int)(item % p.Hkv), j = (int)(item / p.Hkv % pages_out), b = (int)(item / p.Hkv / pages_out);
+  const int L = p.seq_lens[b];
+  if (L < 0 || (long long)L > (long long)p.max_blocks * kP) return;
+  move_page<RB, SCALED>(p, b, h, j, L, p.kept + ((size_t)b * p.Hkv + h) * p.budget + j * kP);
+}
+
+// Both in one launch, where the rows are few and their pages too: `parts` CTAs a (sequence, KV
+// head) select, each for itself (SMs would idle otherwise), and move a part of the pages.  One
+// sequence of 4224 slots, 8 heads: 10.5 us against 11.7 in two launches (with 1024 threads
+// 11.4), and 2.7 us less of the host; 15 of up to 7812, 8 heads: 20.3 against 17.3, two of
+// 32441, two heads: 79 against 38.
+constexpr int kBothPages = 32;    // of a part, at most
+constexpr int kBothSlots = 6144;  // the widest table
+constexpr int kBothThreads = 512;
+
+template <int RB, bool SCALED>
+__global__ void __launch_bounds__(kBothThreads) evict_both_kernel(const EvictParams p, int max_keys, int parts, int part_pages) {
+  extern __shared__ uint4 s_keys[];
+  __shared__ int s_kept[kBothPages * kP];
+  const int h = blockIdx.x % p.Hkv, part = blockIdx.x / p.Hkv % parts, b = blockIdx.x / p.Hkv / parts;
+  pdl_wait();
+  const int L = p.seq_lens[b];
+  if (L < 0) return;
+  if ((long long)L > (long long)p.max_blocks * kP) {
+    if (threadIdx.x == 0) set_status(p.status, kStPages);
+    return;
+  }
+  int* kept = p.kept + ((size_t)b * p.Hkv + h) * p.budget;
+  const int first = part * part_pages * kP, last = min(first + part_pages * kP, p.budget);
+  select_slots<kBothThreads>(p, b, h, L, s_keys, max_keys, [&](int i, int slot) {
+    if (i < first || i >= last) return;
+    s_kept[i - first] = slot;
+    kept[i] = slot;
+  });
+  for (int i = max(L, first) + threadIdx.x; i < last; i += kBothThreads) kept[i] = -1;
+  __syncthreads();
+  for (int j = threadIdx.x >> 5; j < part_pages; j += kBothThreads / 32)
+    move_page<RB, SCALED>(p, b, h, part * part_pages + j, L, s_kept + j * kP);
+}
+
+// Launches evict_both_kernel if it is its case.
+template <int RB, bool SCALED>
+cudaError_t launch_both(const EvictParams& p, int sms, bool* done, cudaStream_t stream) {
+  const long long rows = (long long)p.B * p.Hkv, slots = (long long)p.max_blocks * kP;
+  const int pages_out = (p.budget + kP - 1) / kP;
+  *done = false;
+  if (slots > kBothSlots) return cudaSuccess;
+  // a page a warp if SMs are left for that
+  long long parts = (pages_out + kBothThreads / 32 - 1) / (kBothThreads / 32);
+  if (parts > 2LL * sms / rows) parts = 2LL * sms / rows;
+  if (parts < 1 || (pages_out + parts - 1) / parts > kBothPages) return cudaSuccess;
+  const int part_pages = (int)((pages_out + parts - 1) / parts);
+  parts = (pages_out + part_pages - 1) / part_pages;
+  *done = true;
+  return launch_pdl(evict_both_kernel<RB, SCALED>, dim3((unsigned)(rows * parts)), dim3(kBothThreads), (size_t)slots * 4,
+                    stream, p, (int)slots, (int)parts, part_pages);
+}
+
+template <int RB, bool SCALED>
 cudaError_t launch_move(const EvictParams& p, cudaStream_t stream) {
   const int pages_out = (p.budget + kP - 1) / kP;
   const long long items = (long long)p.B * pages_out * p.Hkv, blocks = (items + kMoveWarps - 1) / kMoveWarps;
@@ -337,6 +404,18 @@ cudaError_t launch_kv_evict(const EvictParams& p, cudaStream_t stream) {
     if (e != cudaSuccess) return e;
     if (dev >= 0 && dev < kMaxDevices) sms_of[dev].store(sms, std::memory_order_release);
   }
+  bool done = false;
+  if (p.k_scales)
+    e = p.row_bytes == 64 ? launch_both<64, true>(p, sms, &done, stream) : launch_both<128, true>(p, sms, &done, stream);
+  else if (p.row_bytes == 64)
+    e = launch_both<64, false>(p, sms, &done, stream);
+  else if (p.row_bytes == 128)
+    e = launch_both<128, false>(p, sms, &done, stream);
+  else if (p.row_bytes == 256)
+    e = launch_both<256, false>(p, sms, &done, stream);
+  else
+    e = launch_both<512, false>(p, sms, &done, stream);
+  if (done || e != cudaSuccess) return e;
   // few rows: as many threads and as much shared memory as there are for each; many: all rows
   // at once, or nearly, with fewer threads for short tables
   const long long slots = (long long)p.max_blocks * kP, most = rows <= sms ? kMaxKeys : kManyKeys;

@@ -357,12 +357,12 @@ def test_slot_weights_far_pages():
 class Evict:
     """A cache of one kind with weights, tables and new pages, on both sides."""
 
-    def __init__(self, rng, kind, dt, hkv, d, lens, budget, spread=2.0):
+    def __init__(self, rng, kind, dt, hkv, d, lens, budget, spread=2.0, width=1):
         self.cache, self.lens, self.budget, self.kind = None, lens, budget, kind
         need, after = [-(-max(n, 0) // P) for n in lens], [-(-min(max(n, 0), budget) // P) for n in lens]
         self.pages = sum(need) + sum(after) + 3
         perm, at = rng.permutation(self.pages), 0
-        self.table, self.new = np.full((len(lens), max(1, *need)), -1, np.int32), np.full((len(lens), -(-budget // P) + 1), -1, np.int32)
+        self.table, self.new = np.full((len(lens), max(width, *need)), -1, np.int32), np.full((len(lens), -(-budget // P) + 1), -1, np.int32)
         for b in range(len(lens)):
             for t, n in ((self.table, need[b]), (self.new, after[b])):
                 t[b, :n] = perm[at:at + n]
@@ -398,9 +398,10 @@ EVICTS = [  # heads, D, lengths, budget, sinks, recent
 
 @pytest.mark.parametrize("kind, dtype", [("act", "f32"), ("act", "f16"), ("act", "bf16"), ("e4m3", "bf16"), ("block8", "bf16")])
 @pytest.mark.parametrize("case", range(len(EVICTS)))
-def test_evict(kind, dtype, case):
+@pytest.mark.parametrize("width", [1, 400])  # few rows of short tables go through one kernel, of wide ones through two
+def test_evict(kind, dtype, case, width):
     hkv, d, lens, budget, sinks, recent = EVICTS[case]
-    e = Evict(np.random.default_rng(3000 + case), kind, DT[dtype], hkv, d, lens, budget)
+    e = Evict(np.random.default_rng(3000 + case), kind, DT[dtype], hkv, d, lens, budget, width=width)
     if kind == "block8":  # no NaN codes: a re-encoded one keeps no sign
         for c, h in zip((e.cache.k, e.cache.v), e.cache.host):
             h.view(torch.uint8).numpy()[...] &= 0xF7
