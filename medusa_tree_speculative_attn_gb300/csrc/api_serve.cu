@@ -327,7 +327,8 @@ int mt_kv_attn_weights(const mt_attn_desc* d, int max_depth, float decay, const 
   if (st != MT_OK) return st;
   if (!q || !lse || !k_cache || !k_scales || !block_tables || !seq_lens || !weights || !out || !status_ws)
     return MT_ERR_INVALID_ARG;
-  if (!aligned16(q) || !aligned16(k_cache) || !aligned16(weights) || !aligned16(out) || !aligned16(status_ws))
+  if (!aligned16(q) || !aligned16(k_cache) || !aligned16(weights) || !aligned16(out) || !aligned16(status_ws) ||
+      reinterpret_cast<uintptr_t>(lse) % 4)
     return MT_ERR_INVALID_ARG;
   if ((accept_path == nullptr) != (accept_len == nullptr)) return MT_ERR_INVALID_ARG;
   if (accept_path && (max_depth < 0 || max_depth >= kMaxTree)) return MT_ERR_INVALID_ARG;
@@ -373,7 +374,8 @@ int mt_kv_evict(const mt_attn_desc* d, int new_blocks_per_seq, int budget, int s
     return MT_ERR_INVALID_ARG;
   if (!k_cache || !v_cache || !weights || !block_tables || !seq_lens || !new_tables || !kept || !status_ws)
     return MT_ERR_INVALID_ARG;
-  if (!aligned16(k_cache) || !aligned16(v_cache) || !aligned16(weights) || !aligned16(status_ws))
+  if (!aligned16(k_cache) || !aligned16(v_cache) || !aligned16(weights) || !aligned16(status_ws) ||
+      reinterpret_cast<uintptr_t>(kept) % 4)
     return MT_ERR_INVALID_ARG;
   EvictParams p{};
   p.B = d->batch; p.Hkv = d->num_kv_heads; p.max_blocks = d->max_blocks_per_seq; p.new_blocks = new_blocks_per_seq;
@@ -400,7 +402,7 @@ int mt_process_logits(const mt_logits_desc* d, const void* logits, void* out, co
   const long long rows = (long long)d->batch * d->tree_size;
   if (rows > (1 << 24)) return MT_ERR_INVALID_ARG;
   for (const long long s : {d->stride[0], d->stride[1], d->out_stride[0], d->out_stride[1]})
-    if (s < 0) return MT_ERR_INVALID_ARG;
+    if (s < 0 || s > (1ll << 38)) return MT_ERR_INVALID_ARG;  // (their sums over 2^24 rows fit)
   if ((history && !history_lens) || (history_lens && !history && d->history_width > 0) || (output_starts && !history_lens))
     return MT_ERR_INVALID_ARG;
   if ((bias_tokens == nullptr) != (bias_values == nullptr) || (mask_index && !mask) || (tree_parents && !tree_tokens))

@@ -339,8 +339,9 @@ def test_slot_weights_in_a_graph_on_another_stream_and_the_same_twice():
     assert torch.equal(other, want)
 
 
-def test_slot_weights_far_pages():
-    c = _attn_case(np.random.default_rng(46), 2, 1, 16, 8, 128, [200, 77], "bf16", "chain")
+@pytest.mark.parametrize("t", [1, 40])  # both kernels
+def test_slot_weights_far_pages(t):
+    c = _attn_case(np.random.default_rng(46), 2, t, 16, 8, 128, [200, 77], "bf16", "chain")
     lse, far, n = _lse_of(c), 300000, c["k"].shape[0]  # a page behind byte 2^32
     table, ws = _i32(c["table"]).cuda(), _status()
     k, ks = torch.empty((far + n, 8, P, 128), dtype=torch.uint8, device="cuda"), torch.empty((far + n, 8), device="cuda")

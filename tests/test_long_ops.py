@@ -73,7 +73,7 @@ def test_weights_pointers(lib):  # noqa: F811
         args = [PTR] * 12
         args[i] = None
         assert lib.mt_kv_attn_weights(_attn_desc(), 3, 1.0, *args, None) == INVALID, i
-    for i in (0, 2, 9, 10, 11):
+    for i in (0, 1, 2, 9, 10, 11):
         args = [PTR] * 12
         args[i] = ODD
         assert lib.mt_kv_attn_weights(_attn_desc(), 3, 1.0, *args, None) == INVALID, i
@@ -125,7 +125,7 @@ def test_evict_pointers(lib):  # noqa: F811
         args = [PTR] * 10
         args[i] = None
         assert _evict(lib, args) == INVALID, i
-    for i in (0, 1, 4, 9):
+    for i in (0, 1, 4, 8, 9):
         args = [PTR] * 10
         args[i] = ODD
         assert _evict(lib, args) == INVALID, i
@@ -164,7 +164,7 @@ def _logits_desc(**kw):
     (dict(history_width=-1), INVALID), (dict(history_width=1 << 30), INVALID), (dict(num_bias=-1), INVALID), (dict(num_masks=-1), INVALID), (dict(stride=(-400, 100)), INVALID),
     (dict(out_stride=(400, 99)), INVALID), (dict(out_stride=(399, 100)), INVALID), (dict(out_stride=(0, 100)), INVALID), (dict(out_stride=(150, 200)), INVALID),
     (dict(tree_size=65, stride=(6500, 100), out_stride=(6500, 100)), UNSUPPORTED), (dict(batch=1 << 24), INVALID), (dict(batch=0), OK), (dict(tree_size=0), OK),
-    (dict(stride=(800, 100)), INVALID),  # the same place under other strides
+    (dict(stride=(1 << 39, 100)), INVALID), (dict(out_stride=(400, 1 << 40)), INVALID), (dict(stride=(800, 100)), INVALID),  # the same place under other strides
 ])
 def test_logits_sizes(lib, desc, want):  # noqa: F811
     assert lib.mt_process_logits(_logits_desc(**desc), *[PTR] * 15, None) == want
