@@ -13,7 +13,7 @@
 // lie in shared memory in that order, one 16-byte read for two k-steps.  Persistent CTAs walk
 // the balanced schedule of 64-slot tiles; a warp takes a page of each and brings the pages,
 // with their old weights, into a ring of its own.  A slot's sum over rows is two shuffles.
-// Up to 56 rows a KV head: beyond, the tensor-core path (kv_weights_tc.cu).
+// Up to 32 or 48 rows a KV head: beyond, the tensor-core path (kv_weights_tc.cu).
 //
 // Bound by the keys' bytes: 64 sequences of 256 to 8192 tokens, one query each, 32 query and 8
 // KV heads: 54 us for 291 MB, 5.4 TB/s (79 % of a copy; six pages in flight instead of four 57,
@@ -316,10 +316,12 @@ cudaError_t launch_t(const WeightsParams& p, cudaStream_t stream) {
 }  // namespace
 
 cudaError_t launch_kv_weights(const WeightsParams& p, int dtype, cudaStream_t stream) {
-  // 16 sequences of 512 to 8192 slots, 8 KV heads: 48 rows 35.6 us here against 36.2 there, 64
-  // 41.4 against 36.2, 96 55.3 against 40.4; 64 of 256 to 4096: 48 rows 58.6 against 70.4, 64
-  // 70.3 against 71.0, 96 98.3 against 81.1; 4 of 2000: 64 rows 10.1 against 10.6.
-  if (p.rows > 56) return launch_kv_weights_tc(p, dtype, stream);
+  // Here against there, in us, 8 KV heads: 64 sequences of 256 to 4096 slots, 32 rows 46 against
+  // 50, 40 53 against 50, 64 68 against 51; 16 of 512 to 8192, 32 rows 28 against 29, 40 32 against
+  // 29, 64 40 against 29.  Short work has its start, which is longer there: 8 of 4000, 36 rows 16.2
+  // against 17.0, 48 17.4 against 17.3; 4 of 2000, 48 rows 8.6 against 10.4, 64 9.4 against 10.4.
+  const bool lots = (long long)p.B * p.Hkv * p.max_blocks > 32768;  // pages
+  if (p.rows > (lots ? 32 : 48)) return launch_kv_weights_tc(p, dtype, stream);
   if (p.D == 64)
     return dtype == 1 ? launch_t<__half, 64>(p, stream) : launch_t<__nv_bfloat16, 64>(p, stream);
   return dtype == 1 ? launch_t<__half, 128>(p, stream) : launch_t<__nv_bfloat16, 128>(p, stream);

@@ -4,29 +4,30 @@
 // A slot's weight is a sum over query rows, so the keys are the M side: a tile of 128 slots
 // (eight pages) by up to 256 query rows, S^T = K Q^T, has a key per TMEM lane, and the thread
 // that owns the lane adds up its row of exp2(S * scale - lse) in registers, with no reduction
-// between threads.  What belongs to a column (the query's scale and its lse) comes from shared
+// between threads.  What belongs to a column (its lse, and the query's scale) comes from shared
 // memory, the same address for all lanes; what belongs to a key (its page's scale) is the
 // thread's own.
 //
 // Operands stay in 8 bits (kind::f8f6f4): key codes go by TMA straight into the tile, and a
-// query row enters as the sum of two (bf16) or three (fp16) E4M3 parts, as in block8_prep.cu,
+// query row enters as the sum of two (bf16) or three (fp16) parts, E4M3 and the last E5M2,
 // worked out by the CTA when it takes up a segment and kept for all of its tiles.
 //
-// Roles: a warp issues the copies (a lane per page), one the products, sixteen add up.  A
-// constant from shared memory costs a 16-byte read for every two columns and warp, so a thread
-// takes a key of two tiles at once: a unit is two tiles by 128 columns, two units fill TMEM,
-// and each has a group of eight warps, 64 columns a warp.  The sums of a pair of tiles meet in
-// shared memory.  Every mbarrier wait is bounded (as in attn_block8_tc.cu), and the sums'
-// warps meet by mbarriers too, so that a timeout leaves nobody waiting.
+// Roles: a warp issues the copies (a lane per page), one the products, sixteen add up, two
+// write the weights.  Two accumulators of 256 columns fill TMEM, for even and odd tiles; each
+// has a group of eight summing warps, 128 columns a warp, whose two sums of a key meet in
+// shared memory, and a writing warp.  Every mbarrier wait is bounded (as in attn_block8_tc.cu),
+// and the warps of a role meet by mbarriers too, so that a timeout leaves nobody waiting.
 //
 // More than 256 query rows of a KV head are taken in passes over the segment's tiles.
 //
-// Bound by a unit's chain, products (16 of 100 cycles) then sums (2800 cycles with both groups
-// at work, of which the exponentials' unit is busy 2050), one accumulator a group.  Chunks of
-// 64 tokens for 8 sequences of 4096 to 16384, 32 query and 8 KV heads, bf16: 69 us, 39 % of the
-// products' rate; 4.0 of 5.2 thousand cycles a pair of tiles for the chain, 8000 cycles to
-// begin and 7000 to change a segment.  A tile at a time with eight warps took 80 us, with
-// sixteen 75; four groups of 64 columns 81 (a product of 64 columns takes 80 cycles).
+// Bound by shared memory: of two tiles, the products read 1540 cycles of operands, the sums
+// 2050 of constants (a 16-byte read gives every lane its copy: 4 cycles), the copies write 260;
+// the exponentials' unit works 2050 of the same 4000.  Chunks of 64 tokens for 8 sequences of
+// 4096 to 16384, 32 query and 8 KV heads, bf16: 60 us, 44 % of the products' rate; 7000 cycles
+// to begin and 10000 to take up a segment's queries are 14 of them.  Measured and worse: a unit of
+// two tiles by 128 columns, whose products read 2050 cycles (68 us: half the constants' reads, but
+// both tiles wait for one another), tile by tile (67); a scale for every 16 columns (66); the
+// weights written by the summing warps (69); the parts by integer arithmetic (60).
 #include <cudaTypedefs.h>
 
 #include <atomic>
@@ -47,16 +48,19 @@ constexpr int kInfo = 32;  // tiles whose pages' numbers and scales are kept: mo
 constexpr int kSmemLimit = 232448;
 constexpr int kMaxDevices = 64;
 constexpr int kNone = INT_MIN;  // no page
-constexpr int kUnit = 128;  // query rows of a unit: an accumulator has them for two tiles
-constexpr int kAcc = 2;     // accumulators, each of a group of eight warps
-constexpr int kSumWarps = 16, kCopyWarp = 16, kMmaWarp = 17, kThreads = 18 * 32;
+// Query rows whose scales are within 2^kSpan share the largest, and the sums read 4 bytes a column,
+// not 8 (60 against 79 us).  The smallest row's largest value then is 3.5 or more where its own
+// scale makes it 224, and what the parts leave of a value 2^-15 of it at most.
+constexpr int kSpan = 6;
+constexpr int kAcc = 2;  // accumulators, each of a group of eight warps: even and odd tiles
+constexpr int kSumWarps = 16, kCopyWarp = 16, kMmaWarp = 17, kWriteWarp = 18, kThreads = 20 * 32;
 
 template <int D, int NP>
 struct Cfg {
   static constexpr int kQPart = kCols * D;
   static constexpr int kQ = NP * kQPart;
   static constexpr int kStage = kTile * D;
-  static constexpr int kPart = kAcc * 4 * 2 * kTile * 4;
+  static constexpr int kPart = kAcc * 2 * kTile * 4;
   static constexpr int kMeta = 1024 + kCols * 8 + kPart + kInfo * kPages * 8 +
                                kMaxPieceRecs * (int)sizeof(PieceRec);  // barriers, columns, parts of sums, pages, pieces
   static constexpr int kFit = (kSmemLimit - 1024 - kMeta - kQ - 4 * (8192 + 4)) / kStage;
@@ -71,17 +75,19 @@ __device__ __forceinline__ float fast_exp2(float x) {
   return y;
 }
 
-// 32 lanes x 32 bits, eight consecutive columns per thread of two accumulators; and the
-// wait, through which the registers pass so that no use of them can move ahead of it.
-__device__ __forceinline__ void tmem_ld_x8(uint32_t taddr, uint32_t (&r)[8]) {
-  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
-               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
-               : "r"(taddr));
+// 32 lanes x 32 bits, 16 consecutive columns per thread; and the wait, through which the
+// registers pass so that no use of them can move ahead of it.
+__device__ __forceinline__ void tmem_ld_x16(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr));
 }
-__device__ __forceinline__ void tmem_ld_wait(uint32_t (&r)[8], uint32_t (&s)[8]) {
+__device__ __forceinline__ void tmem_ld_wait(uint32_t (&r)[16]) {
   asm volatile("tcgen05.wait::ld.sync.aligned;"
                : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
-                 "+r"(s[0]), "+r"(s[1]), "+r"(s[2]), "+r"(s[3]), "+r"(s[4]), "+r"(s[5]), "+r"(s[6]), "+r"(s[7])
+                 "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])
                :
                : "memory");
 }
@@ -111,7 +117,7 @@ __device__ __forceinline__ F2 f2_add(F2 a, F2 b) {
   return r;
 }
 
-// D[tmem] (+)= A[smem] * B[smem]: E4M3 both, K-major, fp32 accumulator.
+// D[tmem] (+)= A[smem] * B[smem]: 8 bits both, K-major, fp32 accumulator.
 template <bool ACC>
 __device__ __forceinline__ void mma_f8_ss(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc) {
   if (ACC) {
@@ -129,10 +135,10 @@ __device__ __forceinline__ void mma_f8_ss(uint32_t d_tmem, uint64_t a_desc, uint
   }
 }
 
-// Instruction descriptor of kind::f8f6f4 with E4M3 operands (format 0), both
-// K-major, fp32 accumulator (1 at bits 4-5), N >> 3 at bit 17, M >> 4 at bit 24.
-__device__ __forceinline__ uint32_t idesc_f8(int M, int N) {
-  return (1u << 4) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
+// Instruction descriptor of kind::f8f6f4 with A in E4M3 (format 0), B in E4M3 or E5M2 (0 or 1 at
+// bits 10-12), both K-major, fp32 accumulator (1 at bits 4-5), N >> 3 at bit 17, M >> 4 at bit 24.
+__device__ __forceinline__ uint32_t idesc_f8(int M, int N, bool b_e5m2) {
+  return (1u << 4) | ((b_e5m2 ? 1u : 0u) << 10) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
 }
 
 // K-major matrix of rows of D bytes, swizzled over 128 (D = 128) or 64 bytes: eight-row
@@ -184,18 +190,25 @@ struct QueryPart {
   }
 };
 
-// Columns 16 c .. 16 c + 15 of query row `row` of this pass as E4M3 parts in their places;
-// returns the row's scale (scores of the parts -> base 2).  Scaled to 448 at most, an fp16
-// holds all of a query's bits above 2^-24, far below the last part's smallest step (2^-9).
-template <typename T, int D, int NP>
-__device__ __forceinline__ float place_query(const QueryPart<T>& q, float scale_log2, uint8_t* sq, int row, int c) {
+// The largest magnitude of a row, NaN left out.
+template <typename T, int D>
+__device__ __forceinline__ float row_max(const QueryPart<T>& q) {
   AbsMax<T> top;
   top.add(q.r0);
   top.add(q.r1);
   float amax = top.get();
 #pragma unroll
   for (int off = 1; off < D / 16; off <<= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, off));
-  const float scale = block_scale(amax), inv = 1.f / scale;
+  return amax;
+}
+
+// Columns 16 c .. 16 c + 15 of query row `row` of this pass, divided by `scale`, as parts in their
+// places (an fp16 holds all of a query's bits above 2^-24 once it is 448 at most).  What E4M3 parts
+// leave of 8 bits (bf16) or 11 (fp16) is at most 8 of the last bit's steps, so 3 bits, which E5M2
+// holds down to 2^-14: the parts are off by at most 2^-14, and exact for a bf16 of 2^-6 and more.
+template <typename T, int D, int NP>
+__device__ __forceinline__ void place_query(const QueryPart<T>& q, float scale, uint8_t* sq, int row, int c) {
+  const float inv = 1.f / scale;
   __half2 x[8];
   {
     float t[8];
@@ -214,7 +227,8 @@ __device__ __forceinline__ float place_query(const QueryPart<T>& q, float scale_
       uint32_t bits;
       memcpy(&bits, &x[e], 4);
       uint16_t code;
-      asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(code) : "r"(bits));
+      if (part + 1 < NP) asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(code) : "r"(bits));
+      else asm("cvt.rn.satfinite.e5m2x2.f16x2 %0, %1;" : "=h"(code) : "r"(bits));
       if (e & 1) w[e / 2] |= (uint32_t)code << 16; else w[e / 2] = code;
       if (part + 1 < NP) {  // what the part leaves, exactly
         const uint32_t h = e4m3x2_to_h2(code);
@@ -225,8 +239,6 @@ __device__ __forceinline__ float place_query(const QueryPart<T>& q, float scale_
     }
     *reinterpret_cast<uint4*>(sq + part * (kCols * D) + row_off<D>(row, c)) = make_uint4(w[0], w[1], w[2], w[3]);
   }
-  // an infinity has no parts: the row's weights become NaN, as they would be
-  return amax < INFINITY ? scale * scale_log2 : __int_as_float(0x7fffffff);
 }
 
 template <typename T, int D, int NP>
@@ -238,23 +250,25 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* sQ = smem;             // [part][256 rows] swizzled
   uint8_t* sK = sQ + C::kQ;       // [stage][128 rows] swizzled
-  float4* s_col = reinterpret_cast<float4*>(sK + S * C::kStage);  // of two columns: their scales, minus their lse
-  float* s_part = reinterpret_cast<float*>(s_col + kCols / 2);  // [pair's turn][half unit][tile][key]
+  float* s_minus = reinterpret_cast<float*>(sK + S * C::kStage);  // [256] of a column: minus its lse
+  float* s_scale = s_minus + kCols;                               // [256] its scale (scores of the parts -> base 2)
+  float* s_part = s_scale + kCols;  // [accumulator][half of the columns][key]
   int2* s_page = reinterpret_cast<int2*>(s_part + C::kPart / 4);  // [kInfo][8] a tile's pages: number, scale
   uint64_t* bars = reinterpret_cast<uint64_t*>(s_page + kInfo * kPages);
   uint64_t* full = bars;           // [S] a tile's codes have landed
   uint64_t* empty = full + S;      // [S] and are multiplied
-  uint64_t* acc_full = empty + S;         // [kAcc] a unit's scores are there
+  uint64_t* acc_full = empty + S;         // [kAcc] a tile's scores are there
   uint64_t* acc_empty = acc_full + kAcc;  // [kAcc] and read out
-  uint64_t* parts = acc_empty + kAcc;     // [kAcc] the units' sums of a pair are there
+  uint64_t* parts = acc_empty + kAcc;     // [kAcc] the sums of a tile are there
   uint64_t* parts_read = parts + kAcc;    // [kAcc] and read
-  uint64_t* idle = parts_read + kAcc;     // the sums' warps have left the pass before
+  uint64_t* idle = parts_read + kAcc;     // the warps of sums and weights have left the pass before
   uint64_t* q_full = idle + 1;         // the pass's queries are in place
   uint64_t* fin = q_full + 1;          // every product done
   uint64_t* never = fin + 1;           // nothing arrives here (timeout test hook)
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(never + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   static_assert((2 * 6 + 4 * kAcc + 4) * 8 + 8 <= 1024, "barrier area");
+  __shared__ int2 s_span[2 * kSumWarps];  // largest and smallest exponent of each warp's query rows, by pass
   PieceRec* s_pieces = reinterpret_cast<PieceRec*>(reinterpret_cast<uint8_t*>(bars) + 1024);
   int* s_pfx = reinterpret_cast<int*>(s_pieces + kMaxPieceRecs);  // [B + 1]
   __shared__ int s_warp[kThreads / 32];
@@ -268,10 +282,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int s = 0; s < kAcc; ++s) {
       tc::mbar_init(&acc_full[s], 2);  // the products, and their issuer itself (below)
       tc::mbar_init(&acc_empty[s], kSumWarps / kAcc);
-      tc::mbar_init(&parts[s], kSumWarps);
-      tc::mbar_init(&parts_read[s], kSumWarps);
+      tc::mbar_init(&parts[s], kSumWarps / kAcc);
+      tc::mbar_init(&parts_read[s], 1);
     }
-    tc::mbar_init(idle, kSumWarps);
+    tc::mbar_init(idle, kSumWarps + 2);
     tc::mbar_init(q_full, kSumWarps);
     tc::mbar_init(fin, 1);
     tc::mbar_init(never, 1);
@@ -359,8 +373,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           const float ks = __shfl_sync(0xffffffffu, ks0, (j * kPages - base) + (lane & 7));
           if (pos >= (uint32_t)S) wait_all(&empty[st], ((pos / S) - 1) & 1);
           if (!ok) break;
-          // (the place is free: the products of the tile S before are done, so every group has
-          // left the pair eight before that tile's, which holds tiles after the one kInfo back)
+          // (the place is free: the products of the tile S before are done, so the sums' groups have
+          // left the tiles of their accumulators before it, and the writers of a group the one
+          // before that, or the whole pass before: fewer than kInfo tiles back)
           if (lane < kPages) s_page[pos % kInfo * kPages + lane] = make_int2(id, __float_as_int(ks));
           __syncwarp();
           if (lane == 0) tc::mbar_arrive_expect_tx(&full[st], C::kStage);
@@ -379,46 +394,41 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else if (warp == kMmaWarp) {
     // ------------------------------------------------------------ products
     const uint32_t sQ_u = tc::smem_u32(sQ), sK_u = tc::smem_u32(sK);
-    uint32_t pos = 0, unit = 0, pass = 0;
+    uint32_t pos = 0, pass = 0, uses[kAcc] = {};
+    static_assert(kAcc == 2, "accumulators");
     if (p.test_stall) wait_all(never, 0);  // test hook: a wait that can only time out
     while (ok && it.next(pc, L)) {
       const int rows = rows_of(pc.b);
       for (int r0 = 0; ok && r0 < rows; r0 += kCols, ++pass) {
         const int cols = (min(kCols, rows - r0) + 31) / 32 * 32;
         wait_all(q_full, pass & 1);
-        for (int j = pc.tile_begin; ok && j < pc.tile_end; j += 2) {
-          const int two = min(2, pc.tile_end - j);
-          for (int x = 0; x < two; ++x) wait_all(&full[(pos + x) % S], ((pos + x) / S) & 1);
-          for (int c0 = 0; ok && c0 < cols; c0 += kUnit, ++unit) {
-            const uint32_t buf = unit % kAcc;
-            if (unit >= kAcc) wait_all(&acc_empty[buf], ((unit / kAcc) - 1) & 1);
-            if (!ok) break;
-            tc::tc_fence_after();
-            const uint32_t idesc = idesc_f8(kTile, min(kUnit, cols - c0));
-#pragma unroll 1
-            for (int x = 0; x < two; ++x) {
-              const uint64_t kd = desc_rows8<D>(sK_u + (pos + x) % S * C::kStage);
-              const uint32_t d = tmem + buf * (2 * kUnit) + x * kUnit;
-              if (tc::elect_one()) {
+        const uint32_t idesc_part = idesc_f8(kTile, cols, false), idesc_last = idesc_f8(kTile, cols, true);
+        for (int j = pc.tile_begin; j < pc.tile_end; ++j, ++pos) {
+          const uint32_t st = pos % S, buf = j & 1, use = buf ? uses[1]++ : uses[0]++;
+          wait_all(&full[st], (pos / S) & 1);
+          if (use >= 1) wait_all(&acc_empty[buf], (use - 1) & 1);
+          if (!ok) break;
+          tc::tc_fence_after();
+          const uint64_t kd = desc_rows8<D>(sK_u + st * C::kStage);
+          const uint32_t d = tmem + buf * kCols;
+          if (tc::elect_one()) {
 #pragma unroll
-                for (int part = 0; part < NP; ++part) {
-                  const uint64_t qd = desc_rows8<D>(sQ_u + part * C::kQPart + c0 * D);
+            for (int part = 0; part < NP; ++part) {
+              const uint64_t qd = desc_rows8<D>(sQ_u + part * C::kQPart);
+              const uint32_t idesc = part + 1 < NP ? idesc_part : idesc_last;
 #pragma unroll
-                  for (int kk = 0; kk < D / 32; ++kk) {  // 32 codes: 2 descriptor units
-                    if (part == 0 && kk == 0) mma_f8_ss<false>(d, kd, qd, idesc);
-                    else mma_f8_ss<true>(d, kd + (uint64_t)(kk * 2), qd + (uint64_t)(kk * 2), idesc);
-                  }
-                }
-                if (c0 + kUnit >= cols) tc::mma_commit(&empty[(pos + x) % S]);
-                if (x == two - 1) tc::mma_commit(&acc_full[buf]);
+              for (int kk = 0; kk < D / 32; ++kk) {  // 32 codes: 2 descriptor units
+                if (part == 0 && kk == 0) mma_f8_ss<false>(d, kd, qd, idesc);
+                else mma_f8_ss<true>(d, kd + (uint64_t)(kk * 2), qd + (uint64_t)(kk * 2), idesc);
               }
-              __syncwarp();
             }
-            // passes on what this warp acquired with the tiles: their pages
-            if (lane == 0) tc::mbar_arrive(&acc_full[buf]);
-            __syncwarp();
+            tc::mma_commit(&empty[st]);
+            tc::mma_commit(&acc_full[buf]);
           }
-          pos += (uint32_t)two;
+          __syncwarp();
+          // passes on what this warp acquired with the tile: its pages
+          if (lane == 0) tc::mbar_arrive(&acc_full[buf]);
+          __syncwarp();
         }
       }
     }
@@ -426,20 +436,61 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncwarp();
     if (lane == 0) drain_wait(fin, 0, p.status);
     __syncwarp();
+  } else if (warp >= kWriteWarp) {
+    // -------------------------------------------------------------- weights
+    // A warp writes the tiles of one group, a lane every 32nd slot.  In every pass over a segment
+    // a slot is the same thread's, which reads back what it wrote.
+    const int x = warp - kWriteWarp;
+    uint32_t pos = 0, use = 0, pass = 0;
+    while (ok && it.next(pc, L)) {
+      const int rows = rows_of(pc.b), prev = p.prev_lens ? p.prev_lens[pc.b] : L;
+      for (int r0 = 0; ok && r0 < rows; r0 += kCols, ++pass) {
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(idle);
+        wait_all(idle, pass & 1);
+        if (!ok) break;
+        const float* before = r0 == 0 ? p.weights : p.out;  // later rows add to what the earlier ones left
+        const int had = r0 == 0 ? prev : L;
+        const float decay = r0 == 0 ? p.decay : 1.f;
+        for (int j = pc.tile_begin; j < pc.tile_end; ++j, ++pos) {
+          if ((j & 1) != x) continue;
+          wait_all(&parts[x], use & 1);
+          if (!ok) break;
+          ++use;
+          float all[kTile / 32], old[kTile / 32];
+          size_t at[kTile / 32];
+          bool writes[kTile / 32];
+#pragma unroll
+          for (int i = 0; i < kTile / 32; ++i) {
+            const int key = i * 32 + lane, slot = j * kTile + key;
+            const int id = s_page[pos % kInfo * kPages + key / kP].x;
+            const bool good = id >= 0 && id < p.num_pages;
+            writes[i] = good && slot < L;
+            at[i] = ((size_t)(good ? id : 0) * p.Hkv + pc.kvh) * kP + key % kP;
+            old[i] = writes[i] && slot < had ? before[at[i]] : 0.f;
+            if (id != kNone && !good) set_status(p.status, kStPages);
+            all[i] = s_part[x * 2 * kTile + key] + s_part[(x * 2 + 1) * kTile + key];
+          }
+          __syncwarp();
+          if (lane == 0) tc::mbar_arrive(&parts_read[x]);
+#pragma unroll
+          for (int i = 0; i < kTile / 32; ++i)
+            if (writes[i]) p.out[at[i]] = fmaf(old[i], decay, all[i]);
+        }
+      }
+    }
   } else {
     // ---------------------------------------------------------------- sums
-    const int quad = warp & 3, half = warp >> 2 & 1;  // TMEM lanes 32 quad ..; 64 columns of a unit
-    const uint32_t group = warp >> 3;                 // units of this number modulo kAcc
+    const int quad = warp & 3, half = warp >> 2 & 1;  // TMEM lanes 32 quad ..; half of the columns
+    const int group = warp >> 3;                      // tiles of this parity
     const int key = quad * 32 + lane;                 // of a tile
-    const uint32_t addr = tmem + ((uint32_t)(quad * 32) << 16) + group * (2 * kUnit) + (uint32_t)(half * 64);
+    const uint32_t addr = tmem + ((uint32_t)(quad * 32) << 16) + group * kCols;
     const float inv_g = 1.f / (float)p.g;
-    uint32_t unit = 0, pair = 0, pos = 0, pass = 0;
+    uint32_t pos = 0, use = 0, pass = 0;
     while (ok && it.next(pc, L)) {
       const int b = pc.b, h = pc.kvh, rows = rows_of(b);
       if (rows == 0 && threadIdx.x == 0) set_status(p.status, kStPages);
-      const int prev = p.prev_lens ? p.prev_lens[b] : L;
       const int* path = p.accept_path ? p.accept_path + (size_t)b * (p.max_depth + 1) : nullptr;
-      const int tiles = pc.tile_end - pc.tile_begin;
       for (int r0 = 0; ok && r0 < rows; r0 += kCols, ++pass) {
         // the queries and the columns' constants, asked for together, and put in their places
         // once nobody uses the pass before's
@@ -462,126 +513,108 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           raw[i].load(src);
         }
+        // each row's scale is a power of two of its own, unless all can share the largest
+        float amax[IT];
+        int top = INT_MIN, low = INT_MAX;
+#pragma unroll
+        for (int i = 0; i < IT; ++i) {
+          amax[i] = row_max<T, D>(raw[i]);
+          const int e = (int)(__float_as_uint(block_scale(amax[i])) >> 23);
+          if (amax[i] > 0.f) {
+            top = max(top, e);
+            low = min(low, amax[i] < INFINITY ? e : -1000);
+          }
+        }
+        top = __reduce_max_sync(0xffffffffu, top);
+        low = __reduce_min_sync(0xffffffffu, low);
+        if (lane == 0) s_span[(pass & 1) * kSumWarps + warp] = make_int2(top, low);
         __syncwarp();
         if (lane == 0) tc::mbar_arrive(idle);
         wait_all(idle, pass & 1);
         if (!ok) break;
+        {
+          const int2 span = s_span[(pass & 1) * kSumWarps + (lane & (kSumWarps - 1))];
+          top = __reduce_max_sync(0xffffffffu, span.x);
+          low = __reduce_min_sync(0xffffffffu, span.y);
+        }
+        // (no row above 0: any scale; and times the largest of a page, 2^119, it stays finite)
+        const float shared = top == INT_MIN ? 1.f : __uint_as_float((uint32_t)top << 23);
+        const bool same = (top == INT_MIN || top - low <= kSpan) && shared * p.scale_log2 <= 256.f;
 #pragma unroll
         for (int i = 0; i < IT; ++i) {
           const int row = (i * kSumWarps + warp) * RPW + lane / LPR;
           if ((i * kSumWarps + warp) * RPW >= cols) break;  // the same for the warp
-          const float c = place_query<T, D, NP>(raw[i], p.scale_log2, sQ, row, lane % LPR);
+          const float scale = same ? shared : block_scale(amax[i]);
+          place_query<T, D, NP>(raw[i], scale, sQ, row, lane % LPR);
           if (lane % LPR == 0) {
-            float* col = reinterpret_cast<float*>(s_col + row / 2) + (row & 1);
-            col[0] = row < n ? c : 0.f;
-            col[2] = -l2[i] * 1.4426950408889634f;
+            s_minus[row] = -l2[i] * 1.4426950408889634f;
+            // an infinity has no parts: the row's weights become NaN, as they would be
+            s_scale[row] = row >= n ? 0.f : amax[i] < INFINITY ? scale * p.scale_log2 : __int_as_float(0x7fffffff);
           }
         }
         tc::fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) tc::mbar_arrive(q_full);
-        const float* before = r0 == 0 ? p.weights : p.out;  // later rows add to what the earlier ones left
-        const int had = r0 == 0 ? prev : L;
-        const float decay = r0 == 0 ? p.decay : 1.f;
         wait_all(q_full, pass & 1);
-        // A pair's sums: a unit's group leaves its own, and when all are there each warp writes
-        // one page's (a half-warp adds a unit's), a pair later, so that nobody waits.
-        const int units = (cols + kUnit - 1) / kUnit;
-        size_t at = 0;
-        bool writes = false, known = false;
-        float old = 0.f;
-        int last_j = 0;
-        uint32_t last_pos = 0;
-        // What this warp writes of the pair that begins with tile j, and the old weight.  The
-        // pair's pages may be looked at by who has seen its scores, or the others' sums of it.
-        auto look = [&](int j, uint32_t ps) {
-          const int x = warp >> 3, id = j + x < tiles ? s_page[(ps + x) % kInfo * kPages + (warp & 7)].x : kNone;
-          const int slot = (pc.tile_begin + j + x) * kTile + (warp & 7) * kP + (lane & 15);
-          const bool good = id >= 0 && id < p.num_pages;
-          writes = good && lane < kP && slot < L;
-          at = ((size_t)(good ? id : 0) * p.Hkv + h) * kP + (lane & 15);
-          old = writes && slot < had ? before[at] : 0.f;
-          if (id != kNone && !good && lane == 0) set_status(p.status, kStPages);
-        };
-        auto finish = [&](uint32_t pr) {
-          const uint32_t side = pr % kAcc;
-          wait_all(&parts[side], (pr / kAcc) & 1);
-          if (!ok) return;
-          if (!known) look(last_j, last_pos);
-          const float* part = s_part + (size_t)((side * 4 + (lane >> 4) * 2) * 2 + (warp >> 3)) * kTile + (warp & 7) * kP + (lane & 15);
-          const int first = (lane >> 4) * 2;
-          float all = first < 2 * units ? part[0] + part[2 * kTile] : 0.f;
-          all += __shfl_xor_sync(0xffffffffu, all, 16);
-          if (lane == 0) tc::mbar_arrive(&parts_read[side]);
-          if (writes) p.out[at] = fmaf(old, decay, all);
-        };
-        for (int j = 0; ok && j < tiles; j += 2, ++pair, unit += (uint32_t)units) {
-          const uint32_t side = pair % kAcc;
-          const int u = (int)((group - unit) % kAcc);  // the pair's unit that is this group's, if there is one
-          if (u < units) {
-            F2 k[2], sum[2][2];
-            wait_all(&acc_full[group], ((unit + (uint32_t)u) / kAcc) & 1);
-            if (!ok) break;
-            tc::tc_fence_after();
-#pragma unroll
-            for (int x = 0; x < 2; ++x) {
-              const float ks = __int_as_float(s_page[(pos + x) % kInfo * kPages + key / kP].y);
-              k[x] = f2_of(ks, ks);
-              sum[x][0] = sum[x][1] = f2_of(0.f, 0.f);
-            }
-            const int c0 = u * kUnit + half * 64, steps = max(0, min(8, (cols - c0) / 8));  // whole fours: cols are
-            const float4* col = s_col + c0 / 2;
-            uint32_t s[2][2][8];  // [turn][tile]: eight columns are added while eight are on their way
-            auto load = [&](int y, int turn) {  // (no second tile: what is left over there, and not used)
-              tmem_ld_x8(addr + y * 8, s[turn][0]);
-              tmem_ld_x8(addr + kUnit + y * 8, s[turn][1]);
-            };
-            auto add = [&](int y, int turn) {
-#pragma unroll
-              for (int i = 0; i < 8; i += 2) {
-                const float4 c = col[y * 4 + i / 2];
-#pragma unroll
-                for (int x = 0; x < 2; ++x) {
-                  const uint32_t* v = s[turn][x] + i;
-                  const F2 z = f2_fma(f2_mul(f2_of(__uint_as_float(v[0]), __uint_as_float(v[1])), k[x]), f2_of(c.x, c.y),
-                                      f2_of(c.z, c.w));
-                  sum[x][i / 2 & 1] = f2_add(sum[x][i / 2 & 1], f2_of(fast_exp2(f2_lo(z)), fast_exp2(f2_hi(z))));
-                }
-              }
-            };
-            if (steps > 0) load(0, 0);
+        const int c0 = half * (cols / 2), steps = cols / 32;  // sixteens of a half
+        const uint32_t from = addr + c0;
+        for (int j = pc.tile_begin; j < pc.tile_end; ++j, ++pos) {
+          if ((j & 1) != group) continue;
+          wait_all(&acc_full[group], use & 1);
+          if (!ok) break;
+          tc::tc_fence_after();
+          const float ks = __int_as_float(s_page[pos % kInfo * kPages + key / kP].y);
+          F2 sum0 = f2_of(0.f, 0.f), sum1 = sum0;
+          uint32_t s[2][16];  // sixteen columns are added while sixteen are on their way
+          auto walk = [&](auto add16) {
+            tmem_ld_x16(from, s[0]);
 #pragma unroll 1
             for (int y = 0; y < steps; y += 2) {
-              tmem_ld_wait(s[0][0], s[0][1]);
-              load(y + 1, 1);
-              add(y, 0);
-              tmem_ld_wait(s[1][0], s[1][1]);
-              if (y + 2 < steps) load(y + 2, 0);
-              add(y + 1, 1);
+              tmem_ld_wait(s[0]);
+              if (y + 1 < steps) tmem_ld_x16(from + (y + 1) * 16, s[1]);
+              add16(s[0], y);
+              if (y + 1 == steps) break;
+              tmem_ld_wait(s[1]);
+              if (y + 2 < steps) tmem_ld_x16(from + (y + 2) * 16, s[0]);
+              add16(s[1], y + 1);
             }
-            tc::tc_fence_before();
-            __syncwarp();
-            if (lane == 0) tc::mbar_arrive(&acc_empty[group]);
-            if (pair >= kAcc) wait_all(&parts_read[side], ((pair / kAcc) - 1) & 1);
-            if (!ok) break;
+          };
+          auto take = [&](F2 z, F2& to) { to = f2_add(to, f2_of(fast_exp2(f2_lo(z)), fast_exp2(f2_hi(z)))); };
+          auto two = [](const uint32_t* v) { return f2_of(__uint_as_float(v[0]), __uint_as_float(v[1])); };
+          const float4* minus = reinterpret_cast<const float4*>(s_minus + c0);
+          if (same) {
+            const float k1 = ks * (shared * p.scale_log2);
+            const F2 k = f2_of(k1, k1);
+            walk([&](const uint32_t (&v)[16], int y) {
 #pragma unroll
-            for (int x = 0; x < 2; ++x)
-              s_part[((side * 4 + u * 2 + half) * 2 + x) * kTile + key] =
-                  (f2_lo(sum[x][0]) + f2_hi(sum[x][0])) + (f2_lo(sum[x][1]) + f2_hi(sum[x][1]));
-          } else if (pair >= kAcc) {
-            wait_all(&parts_read[side], ((pair / kAcc) - 1) & 1);
-            if (!ok) break;
+              for (int i = 0; i < 16; i += 4) {
+                const float4 c = minus[y * 4 + i / 4];
+                take(f2_fma(two(v + i), k, f2_of(c.x, c.y)), sum0);
+                take(f2_fma(two(v + i + 2), k, f2_of(c.z, c.w)), sum1);
+              }
+            });
+          } else {
+            const F2 k = f2_of(ks, ks);
+            const float4* scale = reinterpret_cast<const float4*>(s_scale + c0);
+            walk([&](const uint32_t (&v)[16], int y) {
+#pragma unroll
+              for (int i = 0; i < 16; i += 4) {
+                const float4 c = minus[y * 4 + i / 4], e = scale[y * 4 + i / 4];
+                take(f2_fma(f2_mul(two(v + i), k), f2_of(e.x, e.y), f2_of(c.x, c.y)), sum0);
+                take(f2_fma(f2_mul(two(v + i + 2), k), f2_of(e.z, e.w), f2_of(c.z, c.w)), sum1);
+              }
+            });
           }
+          tc::tc_fence_before();
           __syncwarp();
-          if (lane == 0) tc::mbar_arrive(&parts[side]);
-          if (j > 0) finish(pair - 1);
-          known = u < units;
-          if (known) look(j, pos);
-          last_j = j;
-          last_pos = pos;
-          pos += (uint32_t)min(2, tiles - j);
+          if (lane == 0) tc::mbar_arrive(&acc_empty[group]);
+          if (use >= 1) wait_all(&parts_read[group], (use - 1) & 1);
+          if (!ok) break;
+          ++use;
+          s_part[(group * 2 + half) * kTile + key] = (f2_lo(sum0) + f2_hi(sum0)) + (f2_lo(sum1) + f2_hi(sum1));
+          __syncwarp();
+          if (lane == 0) tc::mbar_arrive(&parts[group]);
         }
-        if (ok) finish(pair - 1);
       }
     }
   }
@@ -639,7 +672,7 @@ cudaError_t launch_t(const WeightsParams& p, cudaStream_t stream) {
   s.nrg = 1;
   s.G = (int)(tiles < sms ? tiles : sms);
   s.splits = 0;
-  s.seg_cost = 3;
+  s.seg_cost = 5;
   return launch_pdl(kv_weights_tc_kernel<T, D, NP>, dim3(s.G), dim3(kThreads), (size_t)C::kSmem + 4 * ((size_t)p.B + 1),
                     stream, map, p, s);
 }

@@ -788,6 +788,31 @@ def test_slot_weights_nan_among_chunks():
     assert np.array_equal(w.isnan().cpu().numpy(), want)
 
 
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("span", [3, 5, 7, 12])
+def test_slot_weights_rows_of_unlike_size(dtype, d, span):
+    # rows' largest values 2^0 to 2^-span, some rows of zeros; the second pass has like ones, or the other way round
+    rng = np.random.default_rng(61)
+    c = _attn_case(rng, 2, 40, 16, 2, d, [300, 129], dtype, "chain")
+    size = torch.from_numpy(2.0 ** -rng.integers(0, span + 1, (2, 40, 16)))
+    size[torch.from_numpy(rng.random((2, 40, 16)) < 0.02)] = 0
+    size[0, 33:], size[1, :31] = 0.5, 0.25
+    c["q"] = (c["q"].double() * size[..., None]).to(c["q"].dtype)
+    _weights_check(c, None, None, 1.0, False)
+
+
+def test_slot_weights_of_zero_keys_behind_large_scales():
+    c = _attn_case(np.random.default_rng(62), 1, 64, 4, 1, 128, [100], "bf16", "chain")
+    c["q"] = (c["q"].float() * 2.0 ** 100).to(torch.bfloat16)
+    lse = torch.zeros(1, 64, 4, device="cuda")
+    w, ws = torch.zeros(c["k"].shape[0], 1, P, device="cuda"), _status()
+    ks = torch.full((c["k"].shape[0], 1), 2.0 ** 100, device="cuda")
+    mt.kv_attn_weights(c["q"].cuda(), torch.zeros_like(_f8(c["k"])), ks, _i32(c["table"]).cuda(), _i32(c["lens"]).cuda(), lse, w, status_ws=ws)
+    pages, at = c["table"][0][np.arange(100) // P], np.arange(100) % P
+    assert (w.cpu().numpy()[pages, 0, at] == 256).all() and float(w.sum()) == 25600
+
+
 def test_slot_weights_wait_bound():
     """A pipeline wait that only its bound ends: the status says so, and the next call is right."""
     c = _attn_case(np.random.default_rng(58), 2, 32, 8, 2, 128, [100, 400], "bf16", "chain")
