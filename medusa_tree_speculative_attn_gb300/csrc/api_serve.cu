@@ -56,7 +56,7 @@ struct Block8Ws {
 };
 
 // visible_blocks: the most pages that a sequence's new tokens see
-int block8_ws(const mt_attn_desc* d, int visible_blocks, Block8Ws* w) {
+int block8_ws(const mt_attn_desc* d, int visible_blocks, bool windowed, Block8Ws* w) {
   int dev = 0, sms = 0;
   if (cudaGetDevice(&dev) != cudaSuccess ||
       cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
@@ -65,7 +65,7 @@ int block8_ws(const mt_attn_desc* d, int visible_blocks, Block8Ws* w) {
   if (rows > (1 << 20)) return MT_ERR_UNSUPPORTED;
   w->rows = (int)rows;
   w->plan = block8_plan(d->batch, d->num_kv_heads, w->rows, d->num_q_heads / d->num_kv_heads, visible_blocks, d->tree_size,
-                        d->dtype, sms);
+                        d->dtype, windowed, sms);
   w->nrg = w->plan.nrg;
   w->part_rows = w->rows < w->plan.rows_per_group ? w->rows : w->plan.rows_per_group;
   w->G = w->plan.ctas;
@@ -133,7 +133,8 @@ int attn_block8(const mt_attn_desc* d, int window, int sinks, const void* q, con
   if (window > 0 && ((long long)sinks + 15) / 16 + ((long long)window + 15) / 16 + 1 < blocks)
     blocks = ((long long)sinks + 15) / 16 + ((long long)window + 15) / 16 + 1;
   Block8Ws w;
-  st = block8_ws(d, (int)blocks, &w);
+  // (a log-sum-exp alone leaves the output as the call without one has it, so with its kernel)
+  st = block8_ws(d, (int)blocks, window > 0 && window < INT_MAX, &w);
   if (st != MT_OK) return st;
   if (ws_bytes < w.total) return MT_ERR_INVALID_ARG;
   char* ws = static_cast<char*>(workspace);
@@ -292,9 +293,11 @@ int mt_kv_append_accepted(const mt_append_desc* d, int tree_size, int max_depth,
 }
 
 size_t mt_tree_attn_block8_workspace_size(const mt_attn_desc* d) {
-  Block8Ws w;
-  if (check_block8(d) != MT_OK || block8_ws(d, d->max_blocks_per_seq, &w) != MT_OK) return 0;
-  return w.total;
+  Block8Ws w, r;  // of either form
+  if (check_block8(d) != MT_OK || block8_ws(d, d->max_blocks_per_seq, false, &w) != MT_OK ||
+      block8_ws(d, d->max_blocks_per_seq, true, &r) != MT_OK)
+    return 0;
+  return w.total > r.total ? w.total : r.total;
 }
 
 int mt_tree_attn_paged_block8(const mt_attn_desc* d, const void* q, const void* k_new, const void* v_new,

@@ -830,7 +830,8 @@ cudaError_t launch_d(const Block8Params& p, cudaStream_t stream) {
 
 }  // namespace
 
-Block8Plan block8_plan(int batch, int kv_heads, int rows, int g, int max_blocks, int tree_size, int dtype, int sms) {
+Block8Plan block8_plan(int batch, int kv_heads, int rows, int g, int max_blocks, int tree_size, int dtype, bool windowed,
+                       int sms) {
   Block8Plan p{};
   // Up to 16 rows the register-fragment kernel, which wastes no rows; from 17 on the
   // tensor-core kernel, whose tile has 128 (256) rows.  64 sequences of 256 to 8192
@@ -839,13 +840,16 @@ Block8Plan block8_plan(int batch, int kv_heads, int rows, int g, int max_blocks,
   // The latter's tiles are built for g that divides 128; for any other g the former
   // takes every count, and streams a KV head's cache once per 32 rows: 16 sequences of
   // 512 to 8192 tokens, 64 nodes, 24, 28 and 40 query heads for 8, 4 and 8 KV heads 321,
-  // 348 and 518 us, where 32 for 8 take 95.  (A tile of 128 / g * g rows would hold whole
-  // tokens of any g.)  fp16 queries fill three operand parts, and with those two tiles
-  // do not fit in TMEM: the same trees 119 us.
-  if (rows > 16 && tc_supported(128, g)) {
+  // 348 and 518 us, where 32 for 8 take 95.  fp16 queries fill three operand parts, and
+  // with those two tiles do not fit in TMEM: the same trees 119 us.
+  // Under a window the tiles take any g, with 128 / g * g rows: whole nodes.  Trees of 64 nodes as
+  // above, up to 32768 tokens, window 4096, 24 and 56 heads for 8: 86 and 151 us, the
+  // register-fragment kernel 352 and 759; 18 rows of 4 sequences, window 1024, 19 against 26.
+  if (rows > 16 && (tc_supported(128, g) || (windowed && g <= 128))) {
+    const int tile = 128 / g * g;
     p.tc = true;
     p.parts = dtype == 1 ? 3 : 2;
-    p.rows_per_group = p.parts == 2 && rows > 128 ? 256 : 128;
+    p.rows_per_group = p.parts == 2 && rows > tile ? 2 * tile : tile;
     p.ctas = sms;
     p.seg_cost = 5;  // 16 sequences of 64 nodes: 3 98 us, 5 95, 8 97, 12 100
   } else {

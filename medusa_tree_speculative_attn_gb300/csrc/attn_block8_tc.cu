@@ -247,6 +247,9 @@ __global__ void __launch_bounds__(Cfg<D, MT, NP>::kThreads, 1)
   using C = Cfg<D, MT, NP>;
   constexpr int S = C::STAGES, PB = C::PB;
   constexpr uint32_t kIdescQK = idesc_f8(128, kTileKeys);
+  // Rows of an M tile: whole nodes.  Where g does not divide 128 the rest of a tile's rows are what
+  // was left in their place; no row's result depends on another's.
+  const int RT = REACH ? p.a.rows_per_group / MT : 128;
   constexpr uint32_t kIdescPV = tc::idesc_f16(false, true, 128, D);
   const AttnParams& a = p.a;
 
@@ -359,9 +362,9 @@ __global__ void __launch_bounds__(Cfg<D, MT, NP>::kThreads, 1)
         if (!ok) break;
         if (lane == 0) {
           const int m = s / NP, part = s % NP;
-          tc::mbar_arrive_expect_tx(&land[st], 128 * D);
+          tc::mbar_arrive_expect_tx(&land[st], RT * D);
           tc::tma_load_3d(sKV + st * C::kStage, &map_q, 0, pc.kvh * a.g,
-                          (part * a.B + pc.b) * a.T + (pc.rg * a.rows_per_group + m * 128) / a.g, &land[st], q_policy);
+                          (part * a.B + pc.b) * a.T + (pc.rg * a.rows_per_group + m * RT) / a.g, &land[st], q_policy);
         }
         __syncwarp();
       }
@@ -617,8 +620,8 @@ __global__ void __launch_bounds__(Cfg<D, MT, NP>::kThreads, 1)
     uint32_t it = 0, pos = 0;
     while (ok && pi.next(pc, L)) {
       pos += C::kQSlots;
-      const int row = pc.rg * a.rows_per_group + m * 128 + r;
-      const bool row_ok = row < a.rows;
+      const int row = pc.rg * a.rows_per_group + m * RT + r;
+      const bool row_ok = row < a.rows && r < RT;
       const int node = row_ok ? row / a.g : 0, h = pc.kvh * a.g + (row_ok ? row % a.g : 0);
       const unsigned long long anc = p.anc[(size_t)pc.b * a.T + node];
       const float qs = p.q_scale[((size_t)pc.b * a.T + node) * a.Hq + h];
@@ -733,7 +736,7 @@ __global__ void __launch_bounds__(Cfg<D, MT, NP>::kThreads, 1)
       wait_all(&pv_done[m * PB + (it - 1) % PB], ((it - 1) / PB) & 1);
       if (!ok) break;
       tc::tc_fence_after();
-      const int seg_row = m * 128 + r;
+      const int seg_row = m * RT + r;
       // NaN values at the window's edge, for the columns col .. col + 31 of a row that sees them
       auto edge_nan = [&](uint32_t (&o)[32], int col) {
         const int last = min(reach.edge + a.T - 1, min(reach.Lv, pc.tile_end * kTileKeys));
@@ -900,8 +903,7 @@ bool map_pages(CUtensorMap* map, const void* base, long long rows, int D, bool k
              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// Query parts [parts * B * T][Hq][D]: boxes of one 128-row M tile (128 / g nodes
-// x g heads).
+// Query parts [parts * B * T][Hq][D]: boxes of one M tile (128 / g nodes x g heads).
 bool map_queries(CUtensorMap* map, const void* base, long long nodes, int Hq, int g, int D) {
   auto enc = get_encode();
   if (!enc) return false;
@@ -946,7 +948,7 @@ cudaError_t launch_t(const Block8Params& p, cudaStream_t stream) {
 template <int D>
 cudaError_t launch_d(const Block8Params& p, int dtype, cudaStream_t stream) {
   if (dtype == 1) return launch_t<__half, D, 1, 3>(p, stream);
-  if (p.a.rows_per_group == 128) return launch_t<__nv_bfloat16, D, 1, 2>(p, stream);
+  if (p.a.rows_per_group <= 128) return launch_t<__nv_bfloat16, D, 1, 2>(p, stream);
   return launch_t<__nv_bfloat16, D, 2, 2>(p, stream);
 }
 

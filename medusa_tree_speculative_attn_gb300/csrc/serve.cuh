@@ -403,7 +403,9 @@ struct Block8Plan {
   bool tc;
   int rows_per_group, nrg, ctas, seg_cost, parts;
 };
-Block8Plan block8_plan(int batch, int kv_heads, int rows, int g, int max_blocks, int tree_size, int dtype, int sms);
+// windowed: the tensor-core kernel takes any g.
+Block8Plan block8_plan(int batch, int kv_heads, int rows, int g, int max_blocks, int tree_size, int dtype, bool windowed,
+                       int sms);
 cudaError_t launch_attn_block8(const Block8Params& p, int dtype, cudaStream_t stream);
 cudaError_t launch_block8_prep(const Block8Params& p, int dtype, cudaStream_t stream);
 cudaError_t launch_block8_combine(const Block8Params& p, int dtype, cudaStream_t stream);

@@ -94,6 +94,31 @@ def test_window_attention_long_sequences_in_pieces(t, hq, hkv, window, sinks):
     _window_check(c, out, lse, window, sinks)
 
 
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("t, hq, hkv, d", [(6, 6, 2, 128), (44, 12, 4, 64), (64, 7, 1, 128), (61, 14, 2, 64), (9, 24, 1, 128), (3, 200, 2, 64),
+                                           (64, 5, 1, 128), (26, 5, 1, 64), (64, 3, 1, 128), (33, 65, 1, 64), (2, 127, 1, 128)])
+@pytest.mark.parametrize("lens", [[40, 0, 300], [2500, 700]])
+def test_window_attention_of_trees_with_odd_groups(dtype, t, hq, hkv, d, lens):
+    # query heads a KV head that do not divide a tile's 128 rows: tiles of whole nodes, one or more a head
+    c = _attn_case(np.random.default_rng(63), len(lens), t, hq, hkv, d, lens, dtype, "tree")
+    window = 200 if d == 64 else 1000
+    _hide(c, window, 5)
+    out, lse, ws, _, _ = _window_run(c, window, 5)
+    assert mt.read_status(ws) == 0
+    _window_check(c, out, lse, window, 5)
+    other, lse2, _, _, _ = _window_run(c, window, 5, ws=ws)
+    assert torch.equal(other, out) and torch.equal(lse, lse2)
+
+
+@pytest.mark.parametrize("t, hq, hkv", [(20, 6, 2), (64, 7, 1)])
+def test_a_log_sum_exp_leaves_the_output_of_odd_groups(t, hq, hkv):
+    c = _attn_case(np.random.default_rng(64), 3, t, hq, hkv, 128, [700, 20, 64], "bf16")
+    out, _, _, args, kw = _window_run(c, 0, 0)
+    plain = torch.full_like(out, 5.0)
+    mt.tree_attn_paged_block8(*args[:8], plain, **{k: kw[k] for k in ("k_new", "v_new", "workspace")})
+    assert torch.equal(out, plain)
+
+
 @pytest.mark.parametrize("t, hq, hkv", [(3, 8, 2), (24, 8, 2)])
 def test_window_zero_is_the_call_without_one(t, hq, hkv):
     c = _attn_case(np.random.default_rng(31), 3, t, hq, hkv, 128, [700, 20, 64], "bf16")
