@@ -157,23 +157,6 @@ __global__ void __launch_bounds__(kThreads, kCtas) logits_kernel(const LogitsPar
     cp_commit();
   };
   bring(warp, 0);
-#pragma unroll 1
-  for (int i0 = 0; i0 < len; i0 += 16 * kThreads) {
-    if (i0) fetch(i0);
-#pragma unroll
-    for (int e = 0; e < 16; ++e) {
-      const unsigned at = (unsigned)tok[e] - (unsigned)v0;
-      if (tok[e] >= 0 && at < (unsigned)n) {
-        if (i0 + e * kThreads + tid >= start) atomicAdd(&s_count[at], 1u);
-        else atomicOr(&s_count[at], kSeen);
-      }
-    }
-  }
-  for (int i = tid; i < p.num_bias; i += kThreads) {
-    const int token = p.bias_tokens[(size_t)b * p.num_bias + i];
-    const unsigned at = (unsigned)token - (unsigned)v0;
-    if (token >= 0 && at < (unsigned)n) atomicMax(&s_entry[at], (unsigned)i + 1u);
-  }
   if (p.tree_tokens && tid < p.T) {
     unsigned long long anc = 0, nodes = 0;
     for (int a = tid; a >= 0; a = s_par[a]) anc |= 1ull << a;  // parents are earlier: at most T steps
@@ -190,10 +173,26 @@ __global__ void __launch_bounds__(kThreads, kCtas) logits_kernel(const LogitsPar
       }
     }
   }
-  __syncthreads();
-  for (int i = tid; i < n; i += kThreads) {
-    const unsigned c = s_count[i];
-    if (!(c & kInTree) && (c || (p.num_bias && s_entry[i]))) s_list[atomicAdd(&s_listed, 1)] = (uint16_t)i;
+  if (p.tree_tokens) __syncthreads();
+#pragma unroll 1
+  for (int i0 = 0; i0 < len; i0 += 16 * kThreads) {
+    if (i0) fetch(i0);
+#pragma unroll
+    for (int e = 0; e < 16; ++e) {
+      if (i0 + e * kThreads >= len) break;
+      const unsigned at = (unsigned)tok[e] - (unsigned)v0;
+      if (tok[e] >= 0 && at < (unsigned)n) {
+        const unsigned was = i0 + e * kThreads + tid >= start ? atomicAdd(&s_count[at], 1u) : atomicOr(&s_count[at], kSeen);
+        if (was == 0) s_list[atomicAdd(&s_listed, 1)] = (uint16_t)at;  // its first
+      }
+    }
+  }
+  if (p.num_bias) __syncthreads();
+  for (int i = tid; i < p.num_bias; i += kThreads) {
+    const int token = p.bias_tokens[(size_t)b * p.num_bias + i];
+    const unsigned at = (unsigned)token - (unsigned)v0;
+    if (token >= 0 && at < (unsigned)n && atomicMax(&s_entry[at], (unsigned)i + 1u) == 0 && s_count[at] == 0)
+      s_list[atomicAdd(&s_listed, 1)] = (uint16_t)at;
   }
   const float rep = p.repetition ? p.repetition[b] : 1.f, pres = p.presence ? p.presence[b] : 0.f;
   const float freq = p.frequency ? p.frequency[b] : 0.f;
