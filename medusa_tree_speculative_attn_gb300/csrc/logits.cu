@@ -9,8 +9,8 @@
 //
 // Few entries change, and the rest is a copy: a CTA takes a slice of the vocabulary and some
 // of a sequence's rows.  It counts the slice's tokens of the history in shared memory (integer
-// atomics: any order gives the same counts) and lists the tokens that matter, once for all
-// rows.  Then a warp takes a part of a row at a time through shared memory: brought
+// atomics: any order gives the same counts) and lists the tokens that matter as it first meets
+// them, once for all rows (the list's order is any, and no result depends on it).  Then a warp takes a part of a row at a time through shared memory: brought
 // asynchronously while the one before is worked on, the tokens that matter changed where they
 // lie, written in 16-byte vectors with -inf where the mask says so.  In place, a row without a
 // mask is not copied; its listed tokens alone are read and written.  A node's path is a bit
@@ -18,10 +18,11 @@
 // count in a row is a population count.
 //
 // 16 trees of 64 nodes, 32000 bf16 logits, histories of 2048 to 4096 tokens, a third of the
-// rows under a mask: 36 us for 133 MB, 3.7 TB/s (54 % of a copy): 6 for the lists, 25 for the
-// copy, the rest instructions of the 1600 tokens a row that change.  With the changes made in
-// global memory behind the copy it took 42, with eight rows a thread on their way 47.  One row
-// of 32000 fp32 logits: 3.8 us, a launch and three dependent trips to memory.
+// rows under a mask: 33 us for 133 MB, 4.0 TB/s (59 % of a copy): 3 for the lists, 25 for the
+// copy, the rest instructions of the 1600 tokens a row that change.  Listed by a look at every
+// word of the slice it took 36, with the changes made in global memory behind the copy 42, with
+// eight rows a thread on their way 47.  One row of 32000 fp32 logits: 3.5 us, a launch and three
+// dependent trips to memory.  Single rows of many sequences: a slice's chain of steps.
 #include <atomic>
 #include <cmath>
 
@@ -33,7 +34,7 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
-constexpr int kMaxSlice = 4096;
+constexpr int kMaxSlice = 6144;  // 120 rows of 102136, fp16: 2048 31 us, 4096 22, 6144 18 (three CTAs an SM), 8192 21
 constexpr int kMaxDevices = 64;
 constexpr int kCtas = 4;      // per SM, by registers
 constexpr int kMaxRows = 64;  // of a CTA
