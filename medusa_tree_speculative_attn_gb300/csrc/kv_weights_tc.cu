@@ -20,14 +20,15 @@
 //
 // More than 256 query rows of a KV head are taken in passes over the segment's tiles.
 //
-// Bound by shared memory more than by any other unit: of two tiles' 4400 cycles, the products read
-// 1540 of operands, the sums 2050 of constants (a 16-byte read gives every lane its copy: 4
-// cycles), the copies write 260; the exponentials' unit works 2050.  Chunks of 64 tokens for 8 sequences of
-// 4096 to 16384, 32 query and 8 KV heads, bf16: 60 us, 44 % of the products' rate; 7000 cycles
-// to begin and 10000 to take up a segment's queries are 14 of them.  Measured and worse: a unit of
-// two tiles by 128 columns, whose products read 2050 cycles (68 us: half the constants' reads, but
-// both tiles wait for one another), tile by tile (67); a scale for every 16 columns (66); the
-// weights written by the summing warps (69); the parts by integer arithmetic (60).
+// Bound by shared memory more than by any other unit: of two tiles' 4400 cycles, the products
+// read 1540 of operands, the sums 2050 of constants (a 16-byte read gives every lane its copy:
+// 4 cycles), the copies write 260; the exponentials' unit works 2050.  Chunks of 64 tokens for
+// 8 sequences of 4096 to 16384, 32 query and 8 KV heads, bf16: 60 us, 44 % of the products'
+// rate; 7000 cycles to begin and 10000 to take up a segment's queries are 14 of them.
+// Measured and worse: a unit of two tiles by 128 columns, whose products read 2050 cycles (68
+// us: half the constants' reads, but both tiles wait for one another), tile by tile (67); a
+// scale for every 16 columns (66); the weights written by the summing warps (69); the parts by
+// integer arithmetic (60).
 #include <cudaTypedefs.h>
 
 #include <atomic>

@@ -10,12 +10,13 @@
 // Few entries change, and the rest is a copy: a CTA takes a slice of the vocabulary and some
 // of a sequence's rows.  It counts the slice's tokens of the history in shared memory (integer
 // atomics: any order gives the same counts) and lists the tokens that matter as it first meets
-// them, once for all rows (the list's order is any, and no result depends on it).  Then a warp takes a part of a row at a time through shared memory: brought
-// asynchronously while the one before is worked on, the tokens that matter changed where they
-// lie, written in 16-byte vectors with -inf where the mask says so.  In place, a row without a
-// mask is not copied; its listed tokens alone are read and written.  A node's path is a bit
-// mask of its ancestors, and a tree token has the bit mask of the nodes that hold it, so its
-// count in a row is a population count.
+// them, once for all rows (the list's order is any, and no result depends on it).  Then a warp
+// takes a part of a row at a time through shared memory: brought asynchronously while the one
+// before is worked on, the tokens that matter changed where they lie, written in 16-byte
+// vectors with -inf where the mask says so.  In place, a row without a mask is not copied; its
+// listed tokens alone are read and written.  A node's path is a bit mask of its ancestors, and
+// a tree token has the bit mask of the nodes that hold it, so its count in a row is a
+// population count.
 //
 // 16 trees of 64 nodes, 32000 bf16 logits, histories of 2048 to 4096 tokens, a third of the
 // rows under a mask: 33 us for 133 MB, 4.0 TB/s (59 % of a copy): 3 for the lists, 25 for the
