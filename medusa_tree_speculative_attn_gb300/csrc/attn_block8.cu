@@ -300,7 +300,8 @@ __device__ __forceinline__ void partial_step(State<D, NT>& st, const uint8_t* kp
       odd = odd || nan;
     }
   }
-  odd = __any_sync(0xffffffffu, odd);  // (and a barrier)
+  odd = __any_sync(0xffffffffu, odd);
+  __syncwarp();  // page_step's lanes read rows that other lanes have changed; a vote orders no memory
   unsigned see[NT][2];
 #pragma unroll
   for (int i = 0; i < NT; ++i)
