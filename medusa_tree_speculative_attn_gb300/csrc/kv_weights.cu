@@ -252,7 +252,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D>::CTAS) kv_weights_kernel(cons
             mma(s, k[x / 2][2 * (x % 2) + 1], q.z, q.w);
           }
           // element e: row 2 tig + (e & 1), key gid + 8 (e >> 1)
-          const float c0 = rc.x * scale, c1 = rc.z * scale;
+          const float c0 = score_factor(rc.x, scale), c1 = score_factor(rc.z, scale);
           sum[0] += fast_exp2(fmaf(s[0], c0, -rc.y)) + fast_exp2(fmaf(s[1], c1, -rc.w));
           sum[1] += fast_exp2(fmaf(s[2], c0, -rc.y)) + fast_exp2(fmaf(s[3], c1, -rc.w));
         }

@@ -434,6 +434,16 @@ struct WeightsParams {
   unsigned long long wait_limit_ns;  // as in AttnParams
   int test_stall;
 };
+
+// What a score's product of codes is multiplied by: a query row's constant and a page's scale,
+// which each may be as large as 2^127.  Finite, so that a key of zeros has the score 0; where the
+// cut takes effect any other key's score is beyond 2^90, of whatever it is cut to.  A NaN (a query
+// with an infinity) stays one.
+__device__ __forceinline__ float score_factor(float row, float page) {
+  float f;
+  asm("min.NaN.f32 %0, %1, %2;" : "=f"(f) : "f"(row * page), "f"(3.402823466e38f));
+  return f;
+}
 cudaError_t launch_kv_weights_tc(const WeightsParams& p, int dtype, cudaStream_t stream);
 cudaError_t launch_kv_weights(const WeightsParams& p, int dtype, cudaStream_t stream);
 

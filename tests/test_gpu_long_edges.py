@@ -39,3 +39,23 @@ def test_window_values_that_one_lane_changes_for_another(d, t, hq, hkv):
         mt.tree_attn_paged_block8(*args[:8], again, **kw)
         assert torch.equal(again, out)
     assert mt.read_status(ws) == 0
+
+
+# ---- weights of cached slots ---------------------------------------------------
+
+KERNELS = [(1, 4, 1), (4, 8, 2), (64, 4, 1)]  # T, Hq, Hkv: a few rows a head, and many
+
+
+@pytest.mark.parametrize("dtype, exponent", [("bf16", 100), ("bf16", 118), ("f16", 15)])
+@pytest.mark.parametrize("t, hq, hkv", KERNELS)
+def test_slot_weights_of_zero_keys_behind_the_largest_scales(dtype, exponent, t, hq, hkv):
+    # queries and page scales whose product is no 32-bit number: a key of zeros has the score 0 all the same
+    c = _attn_case(np.random.default_rng(71), 1, t, hq, hkv, 128, [100], dtype, "chain")
+    c["q"] = (torch.sign(c["q"].float()) * 2.0 ** exponent).to(c["q"].dtype)
+    lse = torch.zeros(1, t, hq, device="cuda")
+    w, ws = torch.zeros(c["k"].shape[0], hkv, P, device="cuda"), _status()
+    ks = torch.full((c["k"].shape[0], hkv), 2.0 ** 119, device="cuda")
+    mt.kv_attn_weights(c["q"].cuda(), torch.zeros_like(_f8(c["k"])), ks, _i32(c["table"]).cuda(), _i32(c["lens"]).cuda(), lse, w, status_ws=ws)
+    pages, at = c["table"][0][np.arange(100) // P], np.arange(100) % P
+    rows = t * hq // hkv
+    assert (w.cpu().numpy()[pages, :, at] == rows).all() and float(w.sum()) == 100 * hkv * rows
