@@ -230,15 +230,15 @@ __device__ __forceinline__ bool drop_nan(uint4& c) {
   return nan;
 }
 
+// Columns of tile j (from k0) that are cached pages'.
+__device__ __forceinline__ unsigned long long cached(int npre, int k0) { return Reach::below64(npre * 16 - k0); }
+
 // REACH: with a window and sinks, and the rows' log-sum-exp.  Only the visible pages are
 // streamed.  A value row of the window's edge, which not every node sees, must not bring a
 // NaN to those that do not: its NaN codes are 0 in the products, and each row that sees it
 // looks for them itself at its end (a CTA that has met one).  16 sequences of 512 to 32768
 // keys under a window of 4096, 64 nodes, 32 query and 8 KV heads: 88 us, 40 % of the
 // products' rate, as without a window.
-// Columns of tile j (from k0) that are cached pages'.
-__device__ __forceinline__ unsigned long long cached(int npre, int k0) { return Reach::below64(npre * 16 - k0); }
-
 template <typename T, int D, int MT, int NP, bool REACH>
 __global__ void __launch_bounds__(Cfg<D, MT, NP>::kThreads, 1)
     attn_block8_tc_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v,
@@ -639,7 +639,7 @@ __global__ void __launch_bounds__(Cfg<D, MT, NP>::kThreads, 1)
         const float4 ks = *reinterpret_cast<const float4*>(s_scale + st * 16);
         const float4 lv = *reinterpret_cast<const float4*>(s_scale + st * 16 + 4);
         const float4 iv = *reinterpret_cast<const float4*>(s_scale + st * 16 + 8);
-        const float c4[4] = {ks.x * qs, ks.y * qs, ks.z * qs, ks.w * qs};
+        float c4[4] = {ks.x * qs, ks.y * qs, ks.z * qs, ks.w * qs};
         const float l4[4] = {lv.x, lv.y, lv.z, lv.w}, i4[4] = {iv.x, iv.y, iv.z, iv.w};
         tc::tmem_ld_wait();
         // the scores are in registers: S may take the next tile's scores
@@ -657,6 +657,12 @@ __global__ void __launch_bounds__(Cfg<D, MT, NP>::kThreads, 1)
 #pragma unroll
             for (int c = 0; c < 32; ++c)
               if (!((bits >> c) & 1u)) sr[32 * hw + c] = 0xff800000u;  // -inf
+          }
+          // -inf comes through the factor: of a page that the row does not see, any will do
+          if (REACH) {
+#pragma unroll
+            for (int g = 0; g < 4; ++g)
+              if (!((uint32_t)(see >> (16 * g)) & 0xffffu)) c4[g] = 1.f;
           }
         }
         // maximum of score + lv: per page of the raw products, then scaled

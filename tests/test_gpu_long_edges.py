@@ -41,6 +41,31 @@ def test_window_values_that_one_lane_changes_for_another(d, t, hq, hkv):
     assert mt.read_status(ws) == 0
 
 
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+@pytest.mark.parametrize("t, hq, hkv, n, window", [(3, 4, 2, 300, 30), (6, 6, 2, 2007, 700), (20, 4, 1, 300, 36), (40, 8, 2, 150, 40), (64, 7, 1, 2000, 1000)])
+def test_window_attention_of_a_key_scale_that_some_rows_do_not_see(dtype, bad, t, hq, hkv, n, window):
+    # the page at the window's edge has a key scale that is no number: rows that see one of its slots are none either (under
+    # an infinity a score may be -inf, and its weight 0), and the deeper nodes, which see none, have what they would have
+    c = _attn_case(np.random.default_rng(73), 1, t, hq, hkv, 128, [n], dtype, "chain")
+    far = n - window + 1
+    edge = [d for d in range(t) if (far + d) // P == far // P]  # depths that see a slot of that page
+    assert edge and len(edge) < t
+    want, mag, wlse = lref.window_attn64(c, window, 0, 128 ** -0.5)
+    c["ks"][c["table"][0, far // P], 0] = bad
+    _hide(c, window, 0)
+    out, lse, ws, _, _ = _window_run(c, window, 0)
+    got, glse = out.cpu().double().numpy(), lse.cpu().double().numpy()
+    g = hq // hkv
+    assert np.isnan(got[:, edge, :g]).all() or bad == float("inf")
+    calm = np.ones(got.shape[:3], bool)
+    calm[:, edge, :g] = False
+    tol = ref.HALF_STEP[c["q"].dtype] * np.abs(want) + (2.0 ** -11 + 2.0 ** -8) * mag + 1e-7  # as test_gpu_long's
+    assert (np.abs(got - want) <= tol)[calm].all()
+    assert (np.abs(glse - wlse) <= 2.0 ** -9 + 2.0 ** -20 * (1 + np.abs(wlse)))[calm].all()
+    assert mt.read_status(ws) == 0
+
+
 # ---- weights of cached slots ---------------------------------------------------
 
 KERNELS = [(1, 4, 1), (4, 8, 2), (64, 4, 1)]  # T, Hq, Hkv: a few rows a head, and many
