@@ -496,7 +496,9 @@ int mt_tree_attn_paged_block8_window(const mt_attn_desc* desc, int window, int s
  * (window 0: a slot's weight is its share of the softmax over the whole cache):
  *   out[slot] = decay * (s < prev_lens[b] ? weights[slot] : 0)
  *               + sum_r exp(q_r . k_s * sm_scale - lse_r)
- * in fp32; a slot's sum has one order, so results are the same in every run.
+ * in fp32; a slot's sum has one order, so results are the same in every run.  A query's
+ * elements keep all their bits down to 2^-20 of the row's largest; what is lost of a
+ * smaller one is at most 2^-31 of the largest.
  * Rows: all tree_size nodes (a decoding step, a chunk of a prompt), or with accept_path
  * and accept_len the nodes accept_path[b][0 .. accept_len[b]], as the acceptance calls
  * give them; accept_path int32 [B][max_depth + 1].

@@ -9,8 +9,12 @@
 // thread's own.
 //
 // Operands stay in 8 bits (kind::f8f6f4): key codes go by TMA straight into the tile, and a
-// query row enters as the sum of two (bf16) or three (fp16) parts, E4M3 and the last E5M2,
-// worked out by the CTA when it takes up a segment and kept for all of its tiles.
+// query row enters as the sum of three (bf16) or four (fp16) E5M2 parts, worked out by the CTA
+// when it takes up a segment and kept for all of its tiles.  They hold an element's every bit down
+// to 2^-23 (bf16) or 2^-20 (fp16) of its row's largest, and leave at most 2^-31 of that of a smaller
+// one, so that keys that miss a query's dominant channel get their scores in 32 bits, too.  Two E4M3
+// and E5M2 parts of a bf16 are quicker (60 us for the chunks below) but lose bits from 2^-14 of the
+// largest on.
 //
 // Roles: a warp issues the copies (a lane per page), one the products, sixteen add up, two
 // write the weights.  Two accumulators of 256 columns fill TMEM, for even and odd tiles; each
@@ -20,15 +24,14 @@
 //
 // More than 256 query rows of a KV head are taken in passes over the segment's tiles.
 //
-// Bound by shared memory more than by any other unit: of two tiles' 4400 cycles, the products
-// read 1540 of operands, the sums 2050 of constants (a 16-byte read gives every lane its copy:
-// 4 cycles), the copies write 260; the exponentials' unit works 2050.  Chunks of 64 tokens for
-// 8 sequences of 4096 to 16384, 32 query and 8 KV heads, bf16: 60 us, 44 % of the products'
-// rate; 7000 cycles to begin and 10000 to take up a segment's queries are 14 of them.
-// Measured and worse: a unit of two tiles by 128 columns, whose products read 2050 cycles (68
-// us: half the constants' reads, but both tiles wait for one another), tile by tile (67); a
-// scale for every 16 columns (66); the weights written by the summing warps (69); the parts by
-// integer arithmetic (60).
+// Bound by shared memory more than by any other unit, as counted from the code: of two tiles' 5000
+// cycles the products read 2310 of operands, the sums 2050 of constants (a 16-byte read gives every
+// lane its copy: 4 cycles), the copies write 260; the exponentials' unit works 2050.  Chunks of 64
+// tokens for 8 sequences of 4096 to 16384, 32 query and 8 KV heads, bf16: 69 us, 38 % of the
+// products' rate; 7000 cycles to begin and 10000 to take up a segment's queries are 14 of them.
+// Measured and worse, against 60 us with two parts: a unit of two tiles by 128 columns (68: half
+// the constants' reads, but both tiles wait for one another), tile by tile (67); a scale for every
+// 16 columns (66), for every column (79); the weights written by the summing warps (69).
 #include <cudaTypedefs.h>
 
 #include <atomic>
@@ -49,15 +52,12 @@ constexpr int kInfo = 32;  // tiles whose pages' numbers and scales are kept: mo
 constexpr int kSmemLimit = 232448;
 constexpr int kMaxDevices = 64;
 constexpr int kNone = INT_MIN;  // no page
-// Query rows whose scales are within 2^kSpan share the largest, and the sums read 4 bytes a column,
-// not 8 (60 against 79 us).  The smallest row's largest value then is 3.5 or more where its own
-// scale makes it 224, and what the parts leave of a value 2^-15 of it at most.
-constexpr int kSpan = 6;
 constexpr int kAcc = 2;  // accumulators, each of a group of eight warps: even and odd tiles
 constexpr int kSumWarps = 16, kCopyWarp = 16, kMmaWarp = 17, kWriteWarp = 18, kThreads = 20 * 32;
 
 template <int D, int NP>
 struct Cfg {
+  static constexpr int kWhole = NP == 3 ? 9 : 6;  // elements of 2^-kWhole and more keep all bits in their parts
   static constexpr int kQPart = kCols * D;
   static constexpr int kQ = NP * kQPart;
   static constexpr int kStage = kTile * D;
@@ -107,11 +107,6 @@ __device__ __forceinline__ F2 f2_fma(F2 a, F2 b, F2 c) {
   asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
   return r;
 }
-__device__ __forceinline__ F2 f2_mul(F2 a, F2 b) {
-  F2 r;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
 __device__ __forceinline__ F2 f2_add(F2 a, F2 b) {
   F2 r;
   asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
@@ -136,10 +131,10 @@ __device__ __forceinline__ void mma_f8_ss(uint32_t d_tmem, uint64_t a_desc, uint
   }
 }
 
-// Instruction descriptor of kind::f8f6f4 with A in E4M3 (format 0), B in E4M3 or E5M2 (0 or 1 at
-// bits 10-12), both K-major, fp32 accumulator (1 at bits 4-5), N >> 3 at bit 17, M >> 4 at bit 24.
-__device__ __forceinline__ uint32_t idesc_f8(int M, int N, bool b_e5m2) {
-  return (1u << 4) | ((b_e5m2 ? 1u : 0u) << 10) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
+// Instruction descriptor of kind::f8f6f4 with A in E4M3 (format 0 at bits 7-9), B in E5M2 (format 1
+// at bits 10-12), both K-major, fp32 accumulator (1 at bits 4-5), N >> 3 at bit 17, M >> 4 at bit 24.
+__device__ __forceinline__ uint32_t idesc_f8(int M, int N) {
+  return (1u << 4) | (1u << 10) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
 }
 
 // K-major matrix of rows of D bytes, swizzled over 128 (D = 128) or 64 bytes: eight-row
@@ -203,10 +198,35 @@ __device__ __forceinline__ float row_max(const QueryPart<T>& q) {
   return amax;
 }
 
-// Columns 16 c .. 16 c + 15 of query row `row` of this pass, divided by `scale`, as parts in their
-// places (an fp16 holds all of a query's bits above 2^-24 once it is 448 at most).  What E4M3 parts
-// leave of 8 bits (bf16) or 11 (fp16) is at most 8 of the last bit's steps, so 3 bits, which E5M2
-// holds down to 2^-14: the parts are off by at most 2^-14, and exact for a bf16 of 2^-6 and more.
+// Biased exponent (in 32 bits) of the smallest magnitude above 0 of a lane's 16 columns, at least
+// 255 where there is none.
+template <typename T>
+__device__ __forceinline__ int least_exponent(const QueryPart<T>& q) {
+  const uint4 w0 = q.r0.w[0], w1 = q.r1.w[0];
+  const uint32_t w[8] = {w0.x, w0.y, w0.z, w0.w, w1.x, w1.y, w1.z, w1.w};
+  uint32_t least = 0xffffffffu;  // of both halves, less 1: zeros are largest
+#pragma unroll
+  for (int e = 0; e < 8; ++e) least = __vminu2(least, __vsub2(w[e] & 0x7fff7fffu, 0x00010001u));
+  const uint32_t bits = min(least & 0xffffu, least >> 16) + 1;
+  if (bits > 0x7fffu) return 255;
+  const uint16_t half = (uint16_t)bits;
+  T v;
+  memcpy(&v, &half, 2);
+  return (int)(__float_as_uint(Act<T>::to_f(v)) >> 23);
+}
+
+// A row's scale: the smallest power of two under which its largest magnitude is 57344 = 1.75 * 2^15
+// at most, the largest E5M2 (down to 2^-120: it and its inverse are normal numbers).
+__device__ __forceinline__ float query_scale(float amax) {
+  const uint32_t bits = __float_as_uint(amax);
+  const int k = (int)(bits >> 23) - 127 - ((bits & 0x7fffffu) <= 0x600000u ? 15 : 14);
+  return __uint_as_float((uint32_t)(max(k, -120) + 127) << 23);
+}
+
+// Columns 16 c .. 16 c + 15 of query row `row` of this pass, divided by `scale`, as E5M2 parts in
+// their places.  A part is the nearest of 3 bits to what the ones before it leave, so NP of them
+// hold 3 NP bits: an element's 8 (bf16, 3 parts) or 11 (fp16, 4 parts), all of them, down to a last
+// bit of 2^-16, the smallest E5M2.  What they leave of smaller elements is 2^-17 at most.
 template <typename T, int D, int NP>
 __device__ __forceinline__ void place_query(const QueryPart<T>& q, float scale, uint8_t* sq, int row, int c) {
   const float inv = 1.f / scale;
@@ -228,11 +248,10 @@ __device__ __forceinline__ void place_query(const QueryPart<T>& q, float scale, 
       uint32_t bits;
       memcpy(&bits, &x[e], 4);
       uint16_t code;
-      if (part + 1 < NP) asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(code) : "r"(bits));
-      else asm("cvt.rn.satfinite.e5m2x2.f16x2 %0, %1;" : "=h"(code) : "r"(bits));
+      asm("cvt.rn.satfinite.e5m2x2.f16x2 %0, %1;" : "=h"(code) : "r"(bits));
       if (e & 1) w[e / 2] |= (uint32_t)code << 16; else w[e / 2] = code;
-      if (part + 1 < NP) {  // what the part leaves, exactly
-        const uint32_t h = e4m3x2_to_h2(code);
+      if (part + 1 < NP) {  // what the part leaves, exactly: an E5M2 is the upper byte of an fp16
+        const uint32_t h = __byte_perm((uint32_t)code, 0u, 0x1404);
         __half2 v;
         memcpy(&v, &h, 4);
         x[e] = __hsub2(x[e], v);
@@ -403,7 +422,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int r0 = 0; ok && r0 < rows; r0 += kCols, ++pass) {
         const int cols = (min(kCols, rows - r0) + 31) / 32 * 32;
         wait_all(q_full, pass & 1);
-        const uint32_t idesc_part = idesc_f8(kTile, cols, false), idesc_last = idesc_f8(kTile, cols, true);
+        const uint32_t idesc = idesc_f8(kTile, cols);
         for (int j = pc.tile_begin; j < pc.tile_end; ++j, ++pos) {
           const uint32_t st = pos % S, buf = j & 1, use = buf ? uses[1]++ : uses[0]++;
           wait_all(&full[st], (pos / S) & 1);
@@ -416,7 +435,6 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int part = 0; part < NP; ++part) {
               const uint64_t qd = desc_rows8<D>(sQ_u + part * C::kQPart);
-              const uint32_t idesc = part + 1 < NP ? idesc_part : idesc_last;
 #pragma unroll
               for (int kk = 0; kk < D / 32; ++kk) {  // 32 codes: 2 descriptor units
                 if (part == 0 && kk == 0) mma_f8_ss<false>(d, kd, qd, idesc);
@@ -514,17 +532,16 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           raw[i].load(src);
         }
-        // each row's scale is a power of two of its own, unless all can share the largest
+        // each row's scale is a power of two of its own, unless all elements keep their bits under
+        // the largest one
         float amax[IT];
         int top = INT_MIN, low = INT_MAX;
 #pragma unroll
         for (int i = 0; i < IT; ++i) {
           amax[i] = row_max<T, D>(raw[i]);
-          const int e = (int)(__float_as_uint(block_scale(amax[i])) >> 23);
-          if (amax[i] > 0.f) {
-            top = max(top, e);
-            low = min(low, amax[i] < INFINITY ? e : -1000);
-          }
+          low = min(low, least_exponent(raw[i]));
+          if (amax[i] > 0.f) top = max(top, (int)(__float_as_uint(query_scale(amax[i])) >> 23));
+          if (!(amax[i] < INFINITY)) low = -1000;
         }
         top = __reduce_max_sync(0xffffffffu, top);
         low = __reduce_min_sync(0xffffffffu, low);
@@ -538,14 +555,14 @@ __global__ void __launch_bounds__(kThreads, 1)
           top = __reduce_max_sync(0xffffffffu, span.x);
           low = __reduce_min_sync(0xffffffffu, span.y);
         }
-        // (no row above 0: any scale; and times the largest of a page, 2^119, it stays finite)
+        // (no row above 0: any scale)
         const float shared = top == INT_MIN ? 1.f : __uint_as_float((uint32_t)top << 23);
-        const bool same = (top == INT_MIN || top - low <= kSpan) && shared * p.scale_log2 <= 256.f;
+        const bool same = top == INT_MIN || top - low <= C::kWhole;
 #pragma unroll
         for (int i = 0; i < IT; ++i) {
           const int row = (i * kSumWarps + warp) * RPW + lane / LPR;
           if ((i * kSumWarps + warp) * RPW >= cols) break;  // the same for the warp
-          const float scale = same ? shared : block_scale(amax[i]);
+          const float scale = same ? shared : query_scale(amax[i]);
           place_query<T, D, NP>(raw[i], scale, sQ, row, lane % LPR);
           if (lane % LPR == 0) {
             s_minus[row] = -l2[i] * 1.4426950408889634f;
@@ -584,7 +601,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           auto two = [](const uint32_t* v) { return f2_of(__uint_as_float(v[0]), __uint_as_float(v[1])); };
           const float4* minus = reinterpret_cast<const float4*>(s_minus + c0);
           if (same) {
-            const float k1 = ks * (shared * p.scale_log2);
+            const float k1 = score_factor(shared * p.scale_log2, ks);
             const F2 k = f2_of(k1, k1);
             walk([&](const uint32_t (&v)[16], int y) {
 #pragma unroll
@@ -595,14 +612,13 @@ __global__ void __launch_bounds__(kThreads, 1)
               }
             });
           } else {
-            const F2 k = f2_of(ks, ks);
             const float4* scale = reinterpret_cast<const float4*>(s_scale + c0);
             walk([&](const uint32_t (&v)[16], int y) {
 #pragma unroll
               for (int i = 0; i < 16; i += 4) {
                 const float4 c = minus[y * 4 + i / 4], e = scale[y * 4 + i / 4];
-                take(f2_fma(f2_mul(two(v + i), k), f2_of(e.x, e.y), f2_of(c.x, c.y)), sum0);
-                take(f2_fma(f2_mul(two(v + i + 2), k), f2_of(e.z, e.w), f2_of(c.z, c.w)), sum1);
+                take(f2_fma(two(v + i), f2_of(score_factor(e.x, ks), score_factor(e.y, ks)), f2_of(c.x, c.y)), sum0);
+                take(f2_fma(two(v + i + 2), f2_of(score_factor(e.z, ks), score_factor(e.w, ks)), f2_of(c.z, c.w)), sum1);
               }
             });
           }
@@ -681,8 +697,8 @@ cudaError_t launch_t(const WeightsParams& p, cudaStream_t stream) {
 }  // namespace
 
 cudaError_t launch_kv_weights_tc(const WeightsParams& p, int dtype, cudaStream_t stream) {
-  if (p.D == 64) return dtype == 1 ? launch_t<__half, 64, 3>(p, stream) : launch_t<__nv_bfloat16, 64, 2>(p, stream);
-  return dtype == 1 ? launch_t<__half, 128, 3>(p, stream) : launch_t<__nv_bfloat16, 128, 2>(p, stream);
+  if (p.D == 64) return dtype == 1 ? launch_t<__half, 64, 4>(p, stream) : launch_t<__nv_bfloat16, 64, 3>(p, stream);
+  return dtype == 1 ? launch_t<__half, 128, 4>(p, stream) : launch_t<__nv_bfloat16, 128, 3>(p, stream);
 }
 
 }  // namespace mt

@@ -84,3 +84,37 @@ def test_slot_weights_of_zero_keys_behind_the_largest_scales(dtype, exponent, t,
     pages, at = c["table"][0][np.arange(100) // P], np.arange(100) % P
     rows = t * hq // hkv
     assert (w.cpu().numpy()[pages, :, at] == rows).all() and float(w.sum()) == 100 * hkv * rows
+
+
+@pytest.mark.parametrize("t, hq, hkv", KERNELS)
+def test_slot_weights_of_small_queries_behind_large_scales(t, hq, hkv):
+    # the other way round: codes and a page's scale whose product is no 32-bit number, and queries so small that the scores
+    # are of ordinary size.  Some rows are of ordinary size themselves, with a log-sum-exp beyond all their scores.
+    c = _attn_case(np.random.default_rng(72), 2, t, hq, hkv, 128, [100, 37], "bf16", "chain")
+    lse = torch.zeros(2, t, hq, device="cuda")
+    small = torch.ones(2, t, hq, dtype=torch.bool)
+    small[:, ::3, 1::2] = False
+    c["q"] = torch.where(small[..., None], c["q"].double() * 2.0 ** -121, c["q"].double()).to(torch.bfloat16)
+    lse[~small.cuda()] = 2.0 ** 126
+    c["ks"][:] = 2.0 ** 119
+    got = _weights_check(c, None, None, 1.0, False, lse=lse)
+    assert np.isfinite(got).all()
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("t, hq, hkv", KERNELS + [(40, 16, 2)])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("dominant, apart", [(8, 0), (8, 6), (12, 3), (12, 6)])
+def test_slot_weights_of_queries_with_a_dominant_channel(dtype, t, hq, hkv, d, dominant, apart):
+    # one channel of a query is 2^dominant times the others, and the keys have nothing there, so that the scores come from
+    # the small ones alone; rows are up to 2^apart apart.  (The tolerance counts 32 bits of what enters a score.)  The new
+    # tokens' keys have nothing there either: with them a log-sum-exp of 577 leaves weights of 10^-63, which no 32 bits hold.
+    rng = np.random.default_rng(74)
+    c = _attn_case(rng, 2, t, hq, hkv, d, [200, 37], dtype, "chain")
+    q = c["q"].double()
+    q[..., 11] = 2.0 ** dominant * torch.sign(q[..., 11])
+    q *= torch.from_numpy(2.0 ** -rng.integers(0, apart + 1, (2, t, hq, 1)))
+    c["q"] = q.to(c["q"].dtype)
+    c["k"][..., 11] = 0
+    c["kn"][..., 11] = 0
+    _weights_check(c, [150, 20], None, 0.9, False)
