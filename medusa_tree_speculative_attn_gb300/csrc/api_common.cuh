@@ -32,6 +32,12 @@ inline size_t align_up(size_t x) { return (x + kAlign - 1) / kAlign * kAlign; }
 
 inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
 
+// Of 32-bit arrays; a null pointer is aligned.
+template <typename... P>
+inline bool aligned4(const P*... p) {
+  return ((reinterpret_cast<uintptr_t>(p) % 4 == 0) && ...);
+}
+
 // The bound of the tensor-core kernels' waits and the timeout test hook, as
 // mt_debug_set_wait left them.
 void wait_bound(unsigned long long* limit_ns, int* stall);

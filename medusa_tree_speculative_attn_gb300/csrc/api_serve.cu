@@ -113,7 +113,8 @@ int attn_block8(const mt_attn_desc* d, int window, int sinks, const void* q, con
       !workspace)
     return MT_ERR_INVALID_ARG;
   if (!aligned16(q) || !aligned16(k_new) || !aligned16(v_new) || !aligned16(k_cache) || !aligned16(v_cache) ||
-      !aligned16(out) || reinterpret_cast<uintptr_t>(workspace) % kAlign)
+      !aligned16(out) || reinterpret_cast<uintptr_t>(workspace) % kAlign ||
+      !aligned4(k_scales, v_scales, block_tables, seq_lens, tree_parents, lse))
     return MT_ERR_INVALID_ARG;
   // the output is written while other blocks still read the inputs
   const size_t tokens = (size_t)d->batch * d->tree_size, q_bytes = tokens * d->num_q_heads * d->head_dim * 2;
@@ -123,7 +124,7 @@ int attn_block8(const mt_attn_desc* d, int window, int sinks, const void* q, con
     return MT_ERR_INVALID_ARG;
   if (lse) {
     const size_t lse_bytes = tokens * d->num_q_heads * 4;
-    if (reinterpret_cast<uintptr_t>(lse) % 4 || overlap(lse, lse_bytes, q, q_bytes) ||
+    if (overlap(lse, lse_bytes, q, q_bytes) ||
         overlap(lse, lse_bytes, k_new, new_bytes) || overlap(lse, lse_bytes, v_new, new_bytes) ||
         overlap(lse, lse_bytes, out, q_bytes))
       return MT_ERR_INVALID_ARG;
@@ -198,7 +199,8 @@ int append(const mt_append_desc* d, AppendParams& a, const void* k, const void* 
   if (!k || !v || !k_cache || !v_cache || !block_tables || !seq_lens || !status_ws) return MT_ERR_INVALID_ARG;
   const int eb = act_bytes(d->dtype);
   if (!aligned16(k) || !aligned16(v) || !aligned16(k_cache) || !aligned16(v_cache) || !aligned16(status_ws) ||
-      !strides_ok(d->k_stride, eb) || !strides_ok(d->v_stride, eb))
+      !strides_ok(d->k_stride, eb) || !strides_ok(d->v_stride, eb) ||
+      !aligned4(k_scales, v_scales, block_tables, seq_lens, a.row_offsets, a.accept_path, a.accept_len))
     return MT_ERR_INVALID_ARG;
   a.mode = d->cache_dtype == 0 ? kCacheAct : k_scales ? kCacheBlock8 : kCacheE4m3;
   if (a.mode == kCacheE4m3 && (!(d->k_scale > 0.f) || std::isinf(d->k_scale) || !(d->v_scale > 0.f) ||
@@ -241,7 +243,7 @@ int mt_qk_norm_rope(const mt_norm_rope_desc* d, const void* q, const void* k, co
   const int eb = act_bytes(d->dtype);
   if (!aligned16(q) || !aligned16(k) || !aligned16(q_out) || !aligned16(k_out) || !aligned16(status_ws) ||
       !aligned16(q_weight) || !aligned16(k_weight) || !strides_ok(d->q_stride, eb) || !strides_ok(d->k_stride, eb) ||
-      !strides_ok(d->q_out_stride, eb) || !strides_ok(d->k_out_stride, eb))
+      !strides_ok(d->q_out_stride, eb) || !strides_ok(d->k_out_stride, eb) || !aligned4(positions))
     return MT_ERR_INVALID_ARG;
   NormRopeParams a{};
   if (rope) {
@@ -331,7 +333,7 @@ int mt_kv_attn_weights(const mt_attn_desc* d, int max_depth, float decay, const 
   if (!q || !lse || !k_cache || !k_scales || !block_tables || !seq_lens || !weights || !out || !status_ws)
     return MT_ERR_INVALID_ARG;
   if (!aligned16(q) || !aligned16(k_cache) || !aligned16(weights) || !aligned16(out) || !aligned16(status_ws) ||
-      reinterpret_cast<uintptr_t>(lse) % 4)
+      !aligned4(lse, k_scales, block_tables, seq_lens, prev_lens, accept_path, accept_len))
     return MT_ERR_INVALID_ARG;
   if ((accept_path == nullptr) != (accept_len == nullptr)) return MT_ERR_INVALID_ARG;
   if (accept_path && (max_depth < 0 || max_depth >= kMaxTree)) return MT_ERR_INVALID_ARG;
@@ -378,7 +380,7 @@ int mt_kv_evict(const mt_attn_desc* d, int new_blocks_per_seq, int budget, int s
   if (!k_cache || !v_cache || !weights || !block_tables || !seq_lens || !new_tables || !kept || !status_ws)
     return MT_ERR_INVALID_ARG;
   if (!aligned16(k_cache) || !aligned16(v_cache) || !aligned16(weights) || !aligned16(status_ws) ||
-      reinterpret_cast<uintptr_t>(kept) % 4)
+      !aligned4(k_scales, v_scales, block_tables, seq_lens, new_tables, kept))
     return MT_ERR_INVALID_ARG;
   EvictParams p{};
   p.B = d->batch; p.Hkv = d->num_kv_heads; p.max_blocks = d->max_blocks_per_seq; p.new_blocks = new_blocks_per_seq;
@@ -415,7 +417,9 @@ int mt_process_logits(const mt_logits_desc* d, const void* logits, void* out, co
   if (rows == 0) return MT_OK;
   const size_t eb = (size_t)act_bytes(d->dtype);
   if (!logits || !out || !status_ws || reinterpret_cast<uintptr_t>(logits) % eb ||
-      reinterpret_cast<uintptr_t>(out) % eb || !aligned16(status_ws))
+      reinterpret_cast<uintptr_t>(out) % eb || !aligned16(status_ws) ||
+      !aligned4(history, history_lens, output_starts, repetition, presence, frequency, bias_tokens, bias_values, mask,
+                mask_index, tree_tokens, tree_parents))
     return MT_ERR_INVALID_ARG;
   // rows of `out` apart from one another, and `out` the logits themselves or apart from them
   const long long b1 = d->batch - 1, t1 = d->tree_size - 1, v = d->vocab;
@@ -455,7 +459,8 @@ int mt_sample_tokens(int num_rows, int vocab, mt_dtype logits_dtype, const void*
   if (!row_index && num_logit_rows != num_rows) return MT_ERR_INVALID_ARG;
   if (num_rows == 0) return MT_OK;
   if ((!logits && num_logit_rows > 0) || !uniforms || !tokens ||
-      reinterpret_cast<uintptr_t>(logits) % act_bytes(logits_dtype))
+      reinterpret_cast<uintptr_t>(logits) % act_bytes(logits_dtype) ||
+      !aligned4(row_index, uniforms, temperature, top_k, top_p, min_p, tokens))
     return MT_ERR_INVALID_ARG;
   SampleParams a{};
   a.N = num_rows; a.V = vocab; a.rows = num_logit_rows; a.row_stride = row_stride;
