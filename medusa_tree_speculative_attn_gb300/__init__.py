@@ -25,6 +25,7 @@ Calls (same names as the C ABI without the ``mt_`` prefix):
 from __future__ import annotations
 
 import ctypes
+import operator
 import os
 import struct
 from typing import Optional
@@ -552,10 +553,14 @@ def _act(t, name, kinds=_DTYPES):
 
 
 def _int32(x, name):
-    """A count: a whole number of 0 .. 2^31 - 1 (ctypes would cut a larger one)."""
-    if not 0 <= x < 2 ** 31:
+    """A count: a whole number of 0 .. 2^31 - 1 (ctypes would cut a larger one).  A TypeError for what is no integer."""
+    try:
+        n = operator.index(x)
+    except TypeError:
+        raise TypeError(f"{name} must be an integer, got {x!r}") from None
+    if not 0 <= n < 2 ** 31:
         raise ValueError(f"{name} must be in [0, 2^31), got {x}")
-    return int(x)
+    return n
 
 
 def _status_arg(t, name, dev, nbytes=256):
@@ -750,11 +755,13 @@ def tree_attn_paged_block8(q, k_cache, v_cache, k_scales, v_scales, block_tables
             _arg(out, "out", dt, rows, dev))
     desc = _block8_desc(q, k_cache, block_tables, sm_scale)
     ws = _status_arg(workspace, "workspace", dev), workspace.numel() * workspace.element_size()
-    if window == 0 and lse is None:
+    if window or sinks:
+        window, sinks = _int32(window, "window"), _int32(sinks, "sinks")
+    if not window and lse is None:
         _invoke(_load().mt_tree_attn_paged_block8, "mt_tree_attn_paged_block8", dev, stream, desc, *args, *ws)
     else:
         _invoke(_load().mt_tree_attn_paged_block8_window, "mt_tree_attn_paged_block8_window", dev, stream, desc,
-                _int32(window, "window"), _int32(sinks, "sinks"), *args,
+                window, sinks, *args,
                 None if lse is None else _arg(lse, "lse", f32, (b, t, hq), dev), *ws)
     return out
 

@@ -1,9 +1,11 @@
 """Host-side checks, without a GPU: a misaligned pointer to a 32-bit array is refused by the call (on the device it would be a
-fault)."""
+fault), and a count that is no whole number by the binding."""
+import numpy as np
 import pytest
 
-pytest.importorskip("torch")
+torch = pytest.importorskip("torch")
 
+import medusa_tree_speculative_attn_gb300 as mt
 from test_long_ops import _logits_desc
 from test_serve_ops import INVALID, _append_desc, _attn_desc, _norm_desc, lib  # noqa: F401 (lib: the fixture)
 
@@ -57,3 +59,28 @@ def test_norm_positions(lib):  # noqa: F811
 def test_sampling(lib):  # noqa: F811
     # logits, row index, uniforms, temperature, top_k, top_p, min_p, tokens
     _odd(lambda x, i, *a: lib.mt_sample_tokens(4, 10, 2, x, 4, 10, i, *a, None), 8, range(1, 8))
+
+
+def test_counts_of_the_binding():
+    for good in (0, 7, 2 ** 31 - 1, np.int32(5), True):
+        assert mt._int32(good, "n") == int(good) and type(mt._int32(good, "n")) is int
+    for bad in (2.5, 2.0, "3", None, np.float32(1)):
+        with pytest.raises(TypeError, match="window must be an integer"):
+            mt._int32(bad, "window")
+    for bad in (-1, 2 ** 31, 2 ** 40):
+        with pytest.raises(ValueError, match="window must be in"):
+            mt._int32(bad, "window")
+
+
+@pytest.mark.gpu
+def test_counts_of_the_calls():
+    cu = lambda *s, dtype=torch.bfloat16: torch.zeros(*s, dtype=dtype, device="cuda")  # noqa: E731
+    q, n, cache, table = cu(3, 4, 8, 128), cu(3, 4, 2, 128), cu(6, 2, 16, 128, dtype=torch.float8_e4m3fn), cu(3, 2, dtype=torch.int32)
+    scales, ws, lens, out = cu(6, 2, dtype=torch.float32) + 1, mt.alloc_block8_workspace(q, cache, table), cu(3, dtype=torch.int32), torch.empty_like(q)
+    for kw in (dict(window=2.5), dict(window=5, sinks=1.5), dict(window=5.0), dict(sinks=-1), dict(window="5")):
+        with pytest.raises((TypeError, ValueError)):
+            mt.tree_attn_paged_block8(q, cache, cache, scales, scales, table, lens, None, out, k_new=n, v_new=n, workspace=ws, **kw)
+    kept, weights = cu(3, 2, 20, dtype=torch.int32), cu(6, 2, 16, dtype=torch.float32)
+    for kw in (dict(sinks=1.5), dict(recent=2.0)):
+        with pytest.raises(TypeError):
+            mt.kv_evict(cache, cache, weights, table, lens, table, kept, status_ws=ws, **kw)
