@@ -538,9 +538,11 @@ int mt_kv_attn_weights(const mt_attn_desc* desc, int max_depth, float decay, con
  * rotated at the positions they had: a slot's number is no longer its position, and the new
  * tokens' positions have to be counted apart (mt_qk_norm_rope takes any).
  * The cache holds dtype's elements (cache_dtype 0) or E4M3 codes (MT_E4M3), copied as they
- * are; with k_scales and v_scales (fp32 [num_pages][Hkv], positive) a new page's scale is
- * the largest of its rows' pages', and a row from a page of a smaller scale has the codes of
- * (its value / the new scale), rounded to nearest even; a NaN stays one.
+ * are; with k_scales and v_scales (fp32 [num_pages][Hkv], 2^-64 to 2^119, powers of two or
+ * not) a new page's scale is the largest of its rows' pages', and a row from a page of a
+ * smaller scale has the codes of (its value / the new scale), rounded once, to nearest even;
+ * a NaN stays one.  (The largest of the pages', not of the rows: a scale stays when the row
+ * that made it goes, and values below 2^-10 of it become 0, until the appends fill new pages.)
  * desc: batch, num_kv_heads, head_dim, page_size, max_blocks_per_seq (of block_tables),
  * num_pages, dtype, cache_dtype; the rest is not used.  budget >= 1, sinks + recent <=
  * budget.  A sequence with seq_lens[b] < 0 is no sequence: nothing is written for it.

@@ -1,7 +1,8 @@
 """Places of the operators for long sequences where a result could go wrong without a size or a mask being odd: what one
 lane leaves for another, extreme scales, queries with a dominant channel, scales that are not powers of two.  Against the
 plain implementations in 64 bits (long_reference)."""
-import ctypes
+import bisect
+from fractions import Fraction
 
 import numpy as np
 import pytest
@@ -11,8 +12,8 @@ torch = pytest.importorskip("torch")
 import long_reference as lref
 import medusa_tree_speculative_attn_gb300 as mt
 import serve_reference as ref
-from test_gpu_long import _f8, _hide, _lse_of, _weights_check, _window_check, _window_run
-from test_gpu_serve import P, _attn_case, _i32, _status
+from test_gpu_long import Evict, _f8, _hide, _lse_of, _weights_check, _window_check, _window_run
+from test_gpu_serve import P, _attn_case, _codes, _i32, _status
 
 pytestmark = pytest.mark.gpu
 
@@ -118,3 +119,86 @@ def test_slot_weights_of_queries_with_a_dominant_channel(dtype, t, hq, hkv, d, d
     c["k"][..., 11] = 0
     c["kn"][..., 11] = 0
     _weights_check(c, [150, 20], None, 0.9, False)
+
+
+# ---- eviction -------------------------------------------------------------------
+
+def _reencoded(old, new):
+    """The code of (value * old / new) for each of the 256 codes, by exact arithmetic: nearest, ties to the even code."""
+    out = np.zeros(256, np.uint8)
+    f = Fraction(float(old)) / Fraction(float(new))
+    values = [Fraction(float(v)) for v in ref.VALUES]
+    for code, v in enumerate(values):
+        x = v * f
+        at = min(bisect.bisect_left(values, x), 126)  # the first value >= x
+        if values[at] != x and at > 0:
+            lo, hi = x - values[at - 1], values[at] - x
+            at -= lo < hi or (lo == hi and at % 2 == 1)
+        out[code] = at
+    out[0x7F] = 0x7F
+    out[128:] = out[:128] | 0x80
+    return out
+
+
+def test_reencoding_of_powers_of_two():
+    for k in range(12):
+        want = ref.encode(ref.decode(np.arange(256)) * 2.0 ** -k)
+        got = _reencoded(1.0, 2.0 ** k)
+        nan = np.arange(256) & 0x7F == 0x7F
+        assert np.array_equal(got[~nan], want[~nan])
+
+
+def _borders(rng, shape):
+    """Scales of which one in three is the largest, and the others put some code's value on the border of two codes under
+    it, or just beside: old / new = m / c with c a code's four bits and m a border's five, up to a power of two."""
+    new = 45045 * 16  # every c divides it
+    out = np.full(shape, new, np.float32)
+    for at in np.ndindex(*shape):
+        if at[0] % 3:
+            c, m = 8 + int(rng.integers(0, 8)), 17 + 2 * int(rng.integers(0, 8))
+            out[at] = new // c * m / 2.0 ** rng.integers(2, 6)
+            if at[0] % 3 == 2:
+                out[at] = np.nextafter(out[at], np.float32(rng.choice([0, 2e9])))
+    return out
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("what", ["any", "borders", "near 1", "far apart"])
+def test_evict_scales_that_are_not_powers_of_two(d, what):
+    rng = np.random.default_rng(75)
+    e = Evict(rng, "block8", torch.bfloat16, 2, d, [500, 64, 201], 100)
+    for x in range(2):
+        s = e.cache.host_scales[x]
+        if what == "any":
+            s[...] = np.exp(2 * rng.standard_normal(s.shape)).astype(np.float32)
+        elif what == "near 1":
+            s[...] = (np.float32(1) + rng.integers(0, 4, s.shape).astype(np.float32) * np.float32(2.0 ** -23)).astype(np.float32)
+        elif what == "far apart":
+            s[...] = np.float32(1.7) * 2.0 ** rng.integers(-64, 119, s.shape).astype(np.float32)
+        else:
+            s[...] = _borders(rng, s.shape)
+        e.cache.scales[x].copy_(torch.from_numpy(s).float())
+        s[...] = e.cache.scales[x].cpu().numpy()
+        assert s.max() <= 2.0 ** 119
+    e.run(3, 10)
+    kept = e.kept.cpu().numpy()
+    tables = {}
+    for x, cache in enumerate((e.cache.k, e.cache.v)):
+        got, src, new_scales = _codes(cache), e.cache.host[x].view(torch.uint8).numpy(), e.cache.scales[x].cpu().numpy()
+        for b in range(len(e.lens)):
+            for h in range(2):
+                stay = kept[b, h][kept[b, h] >= 0]
+                for j in range(0, len(stay), P):
+                    slots = stay[j:j + P]
+                    pages = e.table[b][slots // P]
+                    old, to = e.cache.host_scales[x][pages, h].astype(np.float32), e.new[b][j // P]
+                    assert new_scales[to, h] == old.max()
+                    for r, (slot, page) in enumerate(zip(slots, pages)):
+                        key = (float(old[r]), float(old.max()))
+                        if key not in tables:
+                            tables[key] = _reencoded(*key)
+                        row = src[page, h, slot % P]
+                        want = row if key[0] == key[1] else tables[key][row]
+                        nan = row & 0x7F == 0x7F
+                        assert np.array_equal(got[to, h, r][~nan], want[~nan]) and (got[to, h, r][nan] & 0x7F == 0x7F).all()
+    assert len(tables) > 20 or what == "near 1"
