@@ -55,8 +55,8 @@ struct Block8Ws {
   Block8Plan plan;
 };
 
-// visible_blocks: the most pages that a sequence's new tokens see
-int block8_ws(const mt_attn_desc* d, int visible_blocks, bool windowed, Block8Ws* w) {
+// visible_blocks: the most pages that a sequence's new tokens see; reach: with a window or a log-sum-exp
+int block8_ws(const mt_attn_desc* d, int visible_blocks, bool windowed, bool reach, Block8Ws* w) {
   int dev = 0, sms = 0;
   if (cudaGetDevice(&dev) != cudaSuccess ||
       cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
@@ -96,7 +96,7 @@ int block8_ws(const mt_attn_desc* d, int visible_blocks, bool windowed, Block8Ws
     w->k_blocks = take(blocks * 16 * d->head_dim);
     w->v_blocks = take(blocks * 16 * d->head_dim);
     w->block_scales = take(2 * blocks * sizeof(float));
-    w->depth = take(nodes * sizeof(int));
+    w->depth = reach ? take(nodes * sizeof(int)) : 0;
   }
   w->total = off;
   return MT_OK;
@@ -135,7 +135,7 @@ int attn_block8(const mt_attn_desc* d, int window, int sinks, const void* q, con
     blocks = ((long long)sinks + 15) / 16 + ((long long)window + 15) / 16 + 1;
   Block8Ws w;
   // (a log-sum-exp alone leaves the output as the call without one has it, so with its kernel)
-  st = block8_ws(d, (int)blocks, window > 0 && window < INT_MAX, &w);
+  st = block8_ws(d, (int)blocks, window > 0 && window < INT_MAX, window > 0, &w);
   if (st != MT_OK) return st;
   if (ws_bytes < w.total) return MT_ERR_INVALID_ARG;
   char* ws = static_cast<char*>(workspace);
@@ -172,7 +172,7 @@ int attn_block8(const mt_attn_desc* d, int window, int sinks, const void* q, con
   p.k_block_scales = reinterpret_cast<float*>(ws + w.block_scales);
   p.v_block_scales = p.k_block_scales + (size_t)d->batch * d->num_kv_heads * ((d->tree_size + 15) / 16);
   p.anc = reinterpret_cast<unsigned long long*>(ws + w.anc);
-  p.depth = reinterpret_cast<int*>(ws + w.depth);
+  p.depth = window > 0 ? reinterpret_cast<int*>(ws + w.depth) : nullptr;
   p.pieces = reinterpret_cast<int*>(ws + w.pieces);
   wait_bound(&a.wait_limit_ns, &a.test_stall);
   st = cuda_status(launch_block8_prep(p, d->dtype, stream));
@@ -295,9 +295,9 @@ int mt_kv_append_accepted(const mt_append_desc* d, int tree_size, int max_depth,
 }
 
 size_t mt_tree_attn_block8_workspace_size(const mt_attn_desc* d) {
-  Block8Ws w, r;  // of either form
-  if (check_block8(d) != MT_OK || block8_ws(d, d->max_blocks_per_seq, false, &w) != MT_OK ||
-      block8_ws(d, d->max_blocks_per_seq, true, &r) != MT_OK)
+  Block8Ws w, r;  // of either form (without a window or a log-sum-exp the nodes' depths are not needed)
+  if (check_block8(d) != MT_OK || block8_ws(d, d->max_blocks_per_seq, false, true, &w) != MT_OK ||
+      block8_ws(d, d->max_blocks_per_seq, true, true, &r) != MT_OK)
     return 0;
   return w.total > r.total ? w.total : r.total;
 }

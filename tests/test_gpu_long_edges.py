@@ -67,6 +67,21 @@ def test_window_attention_of_a_key_scale_that_some_rows_do_not_see(dtype, bad, t
     assert mt.read_status(ws) == 0
 
 
+@pytest.mark.parametrize("t, hq, hkv", [(24, 8, 2), (64, 32, 8)])
+def test_a_workspace_without_room_for_depths_serves_the_call_that_has_none(t, hq, hkv):
+    # what the call without a window asked for before there was one: all but the last part, the nodes' depths
+    c = _attn_case(np.random.default_rng(76), 3, t, hq, hkv, 128, [300, 20, 64], "bf16", "tree")
+    want, _, ws, args, kw = _window_run(c, 0, 0)
+    room = ws.numel() * ws.element_size() - -(-3 * t * 4 // 256) * 256
+    less = torch.zeros(room, dtype=torch.uint8, device="cuda")
+    out, kw = torch.full_like(want, 5.0), {k: kw[k] for k in ("k_new", "v_new")}
+    mt.tree_attn_paged_block8(*args[:8], out, workspace=less, **kw)
+    assert torch.equal(out, want) and mt.read_status(less) == 0
+    for more in (dict(workspace=less, window=9), dict(workspace=less, lse=torch.zeros(3, t, hq, device="cuda")), dict(workspace=less[:-256])):
+        with pytest.raises(mt.MedusaTreeError):
+            mt.tree_attn_paged_block8(*args[:8], out, **kw, **more)
+
+
 # ---- weights of cached slots ---------------------------------------------------
 
 KERNELS = [(1, 4, 1), (4, 8, 2), (64, 4, 1)]  # T, Hq, Hkv: a few rows a head, and many
