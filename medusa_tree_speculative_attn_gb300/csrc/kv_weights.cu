@@ -13,7 +13,7 @@
 // lie in shared memory in that order, one 16-byte read for two k-steps.  Persistent CTAs walk
 // the balanced schedule of 64-slot tiles; a warp takes a page of each and brings the pages,
 // with their old weights, into a ring of its own.  A slot's sum over rows is two shuffles.
-// Up to 32 or 48 rows a KV head: beyond, the tensor-core path (kv_weights_tc.cu).
+// Up to 48 rows a KV head: beyond, the tensor-core path (kv_weights_tc.cu).
 //
 // Bound by the keys' bytes: 64 sequences of 256 to 8192 tokens, one query each, 32 query and 8
 // KV heads: 54 us for 291 MB, 5.4 TB/s (79 % of a copy; six pages in flight instead of four 57,
@@ -31,7 +31,7 @@ namespace {
 constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
 constexpr int kP = 16;
-constexpr int kMaxRows = 256;  // query rows in shared memory at a time
+constexpr int kMaxRows = 48;  // query rows of a KV head: more go to the tensor-core path
 constexpr int kMaxDevices = 64;
 
 template <int D>
@@ -83,7 +83,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D>::CTAS) kv_weights_kernel(cons
   using C = Cfg<D>;
   constexpr int NC = D / 64, DEPTH = C::DEPTH;
   extern __shared__ __align__(128) uint8_t smem[];
-  const int most = min(kMaxRows, (p.rows + 7) & ~7);
+  const int most = (p.rows + 7) & ~7;
   uint4* s_q = reinterpret_cast<uint4*>(smem + C::kRing);                   // [tile of 8 rows][chunk][half][lane]
   float2* s_row = reinterpret_cast<float2*>(smem + C::kRing + most * D * 2);  // score -> base 2, lse in base 2
   int* s_pfx = reinterpret_cast<int*>(s_row + most);                        // [B + 1]
@@ -133,150 +133,145 @@ __global__ void __launch_bounds__(kThreads, Cfg<D>::CTAS) kv_weights_kernel(cons
     const int first = 4 * pc.tile_begin + warp;
     const int mine = min(pc.tile_end - pc.tile_begin, max(0, (npages - first + kWarps - 1) / kWarps));
     const int* bt = p.block_tables + (size_t)b * p.max_blocks;
-    for (int r0 = 0; r0 < rows; r0 += kMaxRows) {
-      const int n = min(kMaxRows, rows - r0), tiles = (n + 7) / 8;
-      const float* before = r0 == 0 ? p.weights : p.out;  // later rows add to what the earlier ones left
-      const int had = r0 == 0 ? prev : L;
-      const float decay = r0 == 0 ? p.decay : 1.f;
-      // page ids and scales of 32 pages, a lane each; the next 32 ids are fetched while
-      // these are used, their scales half way
-      auto fetch_id = [&](int i) { return i < mine ? bt[first + 4 * i] : -1; };
-      auto fetch_scale = [&](int id) {
-        return id >= 0 && id < p.num_pages ? __ldg(p.k_scales + (size_t)id * p.Hkv + h) : 0.f;
-      };
-      int id_cur = fetch_id(lane), id_nxt = -1, id_iss = id_cur, iss_base = 0;
-      float ks_cur = fetch_scale(id_cur), ks_nxt = 0.f;
-      auto issue = [&](int i) {
-        if (i < mine) {
-          if (i - iss_base >= 32) {
-            iss_base += 32;
-            id_iss = id_nxt;
-          }
-          const int id = __shfl_sync(0xffffffffu, id_iss, i - iss_base);
-          if (id >= 0 && id < p.num_pages) {
-            const size_t page = (size_t)id * p.Hkv + h;
-            const uint8_t* src = static_cast<const uint8_t*>(p.k_cache) + page * C::kKeys;
-            const uint32_t dst = ring_u + (i % DEPTH) * C::kSlot;
-            constexpr int CPR = D / 16;  // chunks per row
-#pragma unroll
-            for (int x = 0; x < kP * CPR / 32; ++x) {
-              const int q = x * 32 + lane;
-              cp_async16(dst + k_off<D>(q / CPR, q % CPR), src + q * 16);
-            }
-            if (lane < 4 && (first + 4 * i) * kP < had) cp_async16(dst + C::kKeys + lane * 16, before + page * kP + lane * 4);
-          }
+    const int tiles = (rows + 7) / 8;
+    // page ids and scales of 32 pages, a lane each; the next 32 ids are fetched while
+    // these are used, their scales half way
+    auto fetch_id = [&](int i) { return i < mine ? bt[first + 4 * i] : -1; };
+    auto fetch_scale = [&](int id) {
+      return id >= 0 && id < p.num_pages ? __ldg(p.k_scales + (size_t)id * p.Hkv + h) : 0.f;
+    };
+    int id_cur = fetch_id(lane), id_nxt = -1, id_iss = id_cur, iss_base = 0;
+    float ks_cur = fetch_scale(id_cur), ks_nxt = 0.f;
+    auto issue = [&](int i) {
+      if (i < mine) {
+        if (i - iss_base >= 32) {
+          iss_base += 32;
+          id_iss = id_nxt;
         }
-        cp_commit();
-      };
+        const int id = __shfl_sync(0xffffffffu, id_iss, i - iss_base);
+        if (id >= 0 && id < p.num_pages) {
+          const size_t page = (size_t)id * p.Hkv + h;
+          const uint8_t* src = static_cast<const uint8_t*>(p.k_cache) + page * C::kKeys;
+          const uint32_t dst = ring_u + (i % DEPTH) * C::kSlot;
+          constexpr int CPR = D / 16;  // chunks per row
 #pragma unroll
-      for (int i = 0; i < DEPTH - 1; ++i) issue(i);
-      // the queries: a warp eight rows, lanes as they multiply
-      __syncthreads();  // those of the piece before are no longer read
-      for (int t = warp; t < tiles; t += kWarps) {
-        const int row = t * 8 + gid;
-        Row8<T> raw[2 * NC];
-#pragma unroll
-        for (int x = 0; x < 2 * NC; ++x) raw[x].zero();
-        float l2 = INFINITY;
-        if (row < n) {
-          const int at = (r0 + row) / p.g, node = path ? path[at] : at, head = h * p.g + (r0 + row) % p.g;
-          const size_t q = ((size_t)b * p.T + node) * p.Hq + head;
-#pragma unroll
-          for (int x = 0; x < 2 * NC; ++x)
-            raw[x].load(static_cast<const T*>(p.q) + q * D + (x / 2) * 64 + tig * 16 + (x % 2) * 8);
-          l2 = p.lse[q] * 1.4426950408889634f;
-        }
-        AbsMax<T> top;
-#pragma unroll
-        for (int x = 0; x < 2 * NC; ++x) top.add(raw[x]);
-        float amax = top.get();
-        amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
-        amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
-        // 2^8 <= scaled maximum < 2^9: a bf16 keeps its bits down to 2^-25 of it, an fp16 to 2^-22
-        const int ex = amax > 0.f ? (int)(__float_as_uint(amax) >> 23) - 127 : 0;
-        const int k = min(max(8 - ex, -120), 120);
-        const float f2 = __uint_as_float((uint32_t)(127 + k) << 23);
-        const float c = amax < INFINITY ? p.scale_log2 * __uint_as_float((uint32_t)(127 - k) << 23)
-                                        : __int_as_float(0x7fffffff);
-        if (tig == 0) s_row[row] = make_float2(row < n ? c : 0.f, l2);
-#pragma unroll
-        for (int x = 0; x < 2 * NC; ++x) {  // 8 columns: two k-steps of four
-          float f[8];
-          raw[x].to_f(f);
-          s_q[(t * 2 * NC + x) * 32 + lane] = make_uint4(pack_h2(f[0] * f2, f[1] * f2), pack_h2(f[2] * f2, f[3] * f2),
-                                                         pack_h2(f[4] * f2, f[5] * f2), pack_h2(f[6] * f2, f[7] * f2));
+          for (int x = 0; x < kP * CPR / 32; ++x) {
+            const int q = x * 32 + lane;
+            cp_async16(dst + k_off<D>(q / CPR, q % CPR), src + q * 16);
+          }
+          if (lane < 4 && (first + 4 * i) * kP < prev) cp_async16(dst + C::kKeys + lane * 16, p.weights + page * kP + lane * 4);
         }
       }
-      __syncthreads();
-#pragma unroll 1
-      for (int i = 0; i < mine; ++i) {
-        const int at = i & 31;
-        if (at == 0) {
-          if (i > 0) {
-            id_cur = id_nxt;
-            ks_cur = ks_nxt;
-          }
-          id_nxt = fetch_id(i + 32 + lane);
-        } else if (at == 16) {
-          ks_nxt = fetch_scale(id_nxt);
-        }
-        issue(i + DEPTH - 1);
-        cp_wait<DEPTH - 1>();
-        __syncwarp();
-        const uint8_t* kp = ring + (i % DEPTH) * C::kSlot;
-        const int pg = __shfl_sync(0xffffffffu, id_cur, at);
-        const float scale = __shfl_sync(0xffffffffu, ks_cur, at);
-        uint32_t k[NC][4][4];
+      cp_commit();
+    };
 #pragma unroll
-        for (int c = 0; c < NC; ++c) {
-          const uint4 w0 = *reinterpret_cast<const uint4*>(kp + k_off<D>(gid, c * 4 + tig));
-          const uint4 w1 = *reinterpret_cast<const uint4*>(kp + k_off<D>(gid + 8, c * 4 + tig));
-          const uint32_t x0[4] = {w0.x, w0.y, w0.z, w0.w}, x1[4] = {w1.x, w1.y, w1.z, w1.w};
+    for (int i = 0; i < DEPTH - 1; ++i) issue(i);
+    // the queries: a warp eight rows, lanes as they multiply
+    __syncthreads();  // those of the piece before are no longer read
+    for (int t = warp; t < tiles; t += kWarps) {
+      const int row = t * 8 + gid;
+      Row8<T> raw[2 * NC];
 #pragma unroll
-          for (int x = 0; x < 4; ++x) {
-            k[c][x][0] = e4m3x2_to_h2(x0[x] & 0xffffu);
-            k[c][x][1] = e4m3x2_to_h2(x1[x] & 0xffffu);
-            k[c][x][2] = e4m3x2_to_h2(x0[x] >> 16);
-            k[c][x][3] = e4m3x2_to_h2(x1[x] >> 16);
-          }
-        }
-        float sum[2] = {0.f, 0.f};
-#pragma unroll 2
-        for (int t = 0; t < tiles; ++t) {
-          float s[4] = {0.f, 0.f, 0.f, 0.f};
-          const float4 rc = *reinterpret_cast<const float4*>(s_row + t * 8 + 2 * tig);
+      for (int x = 0; x < 2 * NC; ++x) raw[x].zero();
+      float l2 = INFINITY;
+      if (row < rows) {
+        const int at = row / p.g, node = path ? path[at] : at, head = h * p.g + row % p.g;
+        const size_t q = ((size_t)b * p.T + node) * p.Hq + head;
 #pragma unroll
-          for (int x = 0; x < 2 * NC; ++x) {
-            const uint4 q = s_q[(t * 2 * NC + x) * 32 + lane];
-            mma(s, k[x / 2][2 * (x % 2)], q.x, q.y);
-            mma(s, k[x / 2][2 * (x % 2) + 1], q.z, q.w);
-          }
-          // element e: row 2 tig + (e & 1), key gid + 8 (e >> 1)
-          const float c0 = score_factor(rc.x, scale), c1 = score_factor(rc.z, scale);
-          sum[0] += fast_exp2(fmaf(s[0], c0, -rc.y)) + fast_exp2(fmaf(s[1], c1, -rc.w));
-          sum[1] += fast_exp2(fmaf(s[2], c0, -rc.y)) + fast_exp2(fmaf(s[3], c1, -rc.w));
-        }
-#pragma unroll
-        for (int r = 0; r < 2; ++r) {
-          sum[r] += __shfl_xor_sync(0xffffffffu, sum[r], 1);
-          sum[r] += __shfl_xor_sync(0xffffffffu, sum[r], 2);
-        }
-        // lanes 0 .. 15: a slot each
-        const float lo = __shfl_sync(0xffffffffu, sum[0], 4 * (lane & 7)), hi = __shfl_sync(0xffffffffu, sum[1], 4 * (lane & 7));
-        const int slot = (first + 4 * i) * kP + lane;
-        if (lane < kP && slot < L) {
-          if (pg >= 0 && pg < p.num_pages) {
-            const float old = slot < had ? reinterpret_cast<const float*>(kp + C::kKeys)[lane] * decay : 0.f;
-            p.out[((size_t)pg * p.Hkv + h) * kP + lane] = old + (lane < 8 ? lo : hi);
-          } else {
-            set_status(p.status, kStPages);
-          }
-        }
-        __syncwarp();  // every lane has read the slot before it is filled again
+        for (int x = 0; x < 2 * NC; ++x)
+          raw[x].load(static_cast<const T*>(p.q) + q * D + (x / 2) * 64 + tig * 16 + (x % 2) * 8);
+        l2 = p.lse[q] * 1.4426950408889634f;
       }
-      cp_wait<0>();
-      __syncwarp();
+      AbsMax<T> top;
+#pragma unroll
+      for (int x = 0; x < 2 * NC; ++x) top.add(raw[x]);
+      float amax = top.get();
+      amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+      amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+      // 2^8 <= scaled maximum < 2^9: a bf16 keeps its bits down to 2^-25 of it, an fp16 to 2^-22
+      const int ex = amax > 0.f ? (int)(__float_as_uint(amax) >> 23) - 127 : 0;
+      const int k = min(max(8 - ex, -120), 120);
+      const float f2 = __uint_as_float((uint32_t)(127 + k) << 23);
+      const float c = amax < INFINITY ? p.scale_log2 * __uint_as_float((uint32_t)(127 - k) << 23)
+                                      : __int_as_float(0x7fffffff);
+      if (tig == 0) s_row[row] = make_float2(row < rows ? c : 0.f, l2);
+#pragma unroll
+      for (int x = 0; x < 2 * NC; ++x) {  // 8 columns: two k-steps of four
+        float f[8];
+        raw[x].to_f(f);
+        s_q[(t * 2 * NC + x) * 32 + lane] = make_uint4(pack_h2(f[0] * f2, f[1] * f2), pack_h2(f[2] * f2, f[3] * f2),
+                                                       pack_h2(f[4] * f2, f[5] * f2), pack_h2(f[6] * f2, f[7] * f2));
+      }
     }
+    __syncthreads();
+#pragma unroll 1
+    for (int i = 0; i < mine; ++i) {
+      const int at = i & 31;
+      if (at == 0) {
+        if (i > 0) {
+          id_cur = id_nxt;
+          ks_cur = ks_nxt;
+        }
+        id_nxt = fetch_id(i + 32 + lane);
+      } else if (at == 16) {
+        ks_nxt = fetch_scale(id_nxt);
+      }
+      issue(i + DEPTH - 1);
+      cp_wait<DEPTH - 1>();
+      __syncwarp();
+      const uint8_t* kp = ring + (i % DEPTH) * C::kSlot;
+      const int pg = __shfl_sync(0xffffffffu, id_cur, at);
+      const float scale = __shfl_sync(0xffffffffu, ks_cur, at);
+      uint32_t k[NC][4][4];
+#pragma unroll
+      for (int c = 0; c < NC; ++c) {
+        const uint4 w0 = *reinterpret_cast<const uint4*>(kp + k_off<D>(gid, c * 4 + tig));
+        const uint4 w1 = *reinterpret_cast<const uint4*>(kp + k_off<D>(gid + 8, c * 4 + tig));
+        const uint32_t x0[4] = {w0.x, w0.y, w0.z, w0.w}, x1[4] = {w1.x, w1.y, w1.z, w1.w};
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+          k[c][x][0] = e4m3x2_to_h2(x0[x] & 0xffffu);
+          k[c][x][1] = e4m3x2_to_h2(x1[x] & 0xffffu);
+          k[c][x][2] = e4m3x2_to_h2(x0[x] >> 16);
+          k[c][x][3] = e4m3x2_to_h2(x1[x] >> 16);
+        }
+      }
+      float sum[2] = {0.f, 0.f};
+#pragma unroll 2
+      for (int t = 0; t < tiles; ++t) {
+        float s[4] = {0.f, 0.f, 0.f, 0.f};
+        const float4 rc = *reinterpret_cast<const float4*>(s_row + t * 8 + 2 * tig);
+#pragma unroll
+        for (int x = 0; x < 2 * NC; ++x) {
+          const uint4 q = s_q[(t * 2 * NC + x) * 32 + lane];
+          mma(s, k[x / 2][2 * (x % 2)], q.x, q.y);
+          mma(s, k[x / 2][2 * (x % 2) + 1], q.z, q.w);
+        }
+        // element e: row 2 tig + (e & 1), key gid + 8 (e >> 1)
+        const float c0 = score_factor(rc.x, scale), c1 = score_factor(rc.z, scale);
+        sum[0] += fast_exp2(fmaf(s[0], c0, -rc.y)) + fast_exp2(fmaf(s[1], c1, -rc.w));
+        sum[1] += fast_exp2(fmaf(s[2], c0, -rc.y)) + fast_exp2(fmaf(s[3], c1, -rc.w));
+      }
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        sum[r] += __shfl_xor_sync(0xffffffffu, sum[r], 1);
+        sum[r] += __shfl_xor_sync(0xffffffffu, sum[r], 2);
+      }
+      // lanes 0 .. 15: a slot each
+      const float lo = __shfl_sync(0xffffffffu, sum[0], 4 * (lane & 7)), hi = __shfl_sync(0xffffffffu, sum[1], 4 * (lane & 7));
+      const int slot = (first + 4 * i) * kP + lane;
+      if (lane < kP && slot < L) {
+        if (pg >= 0 && pg < p.num_pages) {
+          const float old = slot < prev ? reinterpret_cast<const float*>(kp + C::kKeys)[lane] * p.decay : 0.f;
+          p.out[((size_t)pg * p.Hkv + h) * kP + lane] = old + (lane < 8 ? lo : hi);
+        } else {
+          set_status(p.status, kStPages);
+        }
+      }
+      __syncwarp();  // every lane has read the slot before it is filled again
+    }
+    cp_wait<0>();
+    __syncwarp();
   }
 }
 
@@ -296,7 +291,7 @@ cudaError_t launch_t(const WeightsParams& p, cudaStream_t stream) {
     if (e != cudaSuccess) return e;
     if (dev >= 0 && dev < kMaxDevices) sms_of[dev].store(sms, std::memory_order_release);
   }
-  const int most = p.rows < kMaxRows ? (p.rows + 7) & ~7 : kMaxRows;
+  const int most = (p.rows + 7) & ~7;
   const size_t smem = C::kRing + (size_t)most * (D * 2 + sizeof(float2)) + 4 * ((size_t)p.B + 1);
   int per_sm = (int)(232448 / (smem + 2304));  // and 1280 bytes of static memory, and the system's 1024
   per_sm = per_sm < 1 ? 1 : per_sm < C::CTAS ? per_sm : C::CTAS;
@@ -316,12 +311,12 @@ cudaError_t launch_t(const WeightsParams& p, cudaStream_t stream) {
 }  // namespace
 
 cudaError_t launch_kv_weights(const WeightsParams& p, int dtype, cudaStream_t stream) {
-  // Here against there, in us, 8 KV heads: 64 sequences of 256 to 4096 slots, 32 rows 46 against
-  // 50, 40 53 against 50, 64 68 against 51; 16 of 512 to 8192, 32 rows 28 against 29, 40 32 against
-  // 29, 64 40 against 29.  Short work has its start, which is longer there: 8 of 4000, 36 rows 16.2
-  // against 17.0, 48 17.4 against 17.3; 4 of 2000, 48 rows 8.6 against 10.4, 64 9.4 against 10.4.
-  const bool lots = (long long)p.B * p.Hkv * p.max_blocks > 32768;  // pages
-  if (p.rows > (lots ? 32 : 48)) return launch_kv_weights_tc(p, dtype, stream);
+  // Here against there, in us, cold caches, 8 KV heads of 128 columns, bf16: 64 sequences of 256 to
+  // 4096 slots, 48 rows 47 against 52, 64 55 against 53; 16 of 512 to 8192, 48 rows 29 against 29, 64
+  // 33 against 29; 8 of 4000, 40 rows 22.5 against 22.6, 48 24.6 against 23.0.  Short work has its
+  // start, which is longer there: 4 of 2000, 48 rows 14.3 against 16.5, 64 15.0 against 16.8, 128 20.5
+  // against 19.1; but what a sequence holds is not known here, and the table may be much wider.
+  if (p.rows > kMaxRows) return launch_kv_weights_tc(p, dtype, stream);
   if (p.D == 64)
     return dtype == 1 ? launch_t<__half, 64>(p, stream) : launch_t<__nv_bfloat16, 64>(p, stream);
   return dtype == 1 ? launch_t<__half, 128>(p, stream) : launch_t<__nv_bfloat16, 128>(p, stream);
