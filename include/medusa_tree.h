@@ -493,12 +493,15 @@ int mt_tree_attn_paged_block8_window(const mt_attn_desc* desc, int window, int s
  * What a cache of bounded size can go by: how much attention each slot has received.
  * For every cached slot s < seq_lens[b] of sequence b and KV head h, with the query rows
  * r of the call under that head and lse_r as mt_tree_attn_paged_block8_window returned it
- * (window 0: a slot's weight is its share of the softmax over the whole cache):
+ * for window 0:
  *   out[slot] = decay * (s < prev_lens[b] ? weights[slot] : 0)
  *               + sum_r exp(q_r . k_s * sm_scale - lse_r)
- * in fp32; a slot's sum has one order, so results are the same in every run.  A query's
- * elements keep all their bits down to 2^-20 of the row's largest; what is lost of a
- * smaller one is at most 2^-31 of the largest.
+ * in fp32: each row adds a slot's share of its softmax over the whole cache.  There is no
+ * window here, and the log-sum-exp of a call with one must not be passed (slots that no row
+ * saw would get weights, without a bound, and the pages that it let go are read).  A slot's
+ * sum has one order, so results are the same in every run.  A query's elements keep all
+ * their bits down to 2^-20 of the row's largest; what is lost of a smaller one is at most
+ * 2^-31 of the largest.
  * Rows: all tree_size nodes (a decoding step, a chunk of a prompt), or with accept_path
  * and accept_len the nodes accept_path[b][0 .. accept_len[b]], as the acceptance calls
  * give them; accept_path int32 [B][max_depth + 1].

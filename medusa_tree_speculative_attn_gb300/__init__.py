@@ -771,9 +771,10 @@ def kv_attn_weights(q, k_cache, k_scales, block_tables, seq_lens, lse, weights, 
                     sm_scale: float = 0.0, stream=None):
     """Adds to weights [pages,Hkv,16] (float32; or writes the sums to `out`, of that
     shape) what the rows of q [B,T,Hq,D] give to each cached slot: exp(score - lse),
-    with lse [B,T,Hq] from tree_attn_paged_block8 over the whole cache.  The rows are
-    all T nodes', or the accepted path's.  What a slot had before counts `decay`
-    times; slots from prev_lens[b] on (None: none) are new and had nothing."""
+    with lse [B,T,Hq] from tree_attn_paged_block8 over the whole cache (not from a call
+    with a window).  The rows are all T nodes', or the accepted path's.  What a slot had
+    before counts `decay` times; slots from prev_lens[b] on (None: none) are new and had
+    nothing."""
     dev = _cuda_device(q, "q")
     dt = q.dtype
     _act(q, "q", (torch.float16, torch.bfloat16))

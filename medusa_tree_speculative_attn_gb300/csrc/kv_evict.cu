@@ -5,13 +5,15 @@
 // Into new pages and not in place, so that a prompt's pages that other sequences share stay
 // whole, no row waits for another to be read, and a call that is repeated gives the same.
 //
-// Two kernels, and one that does both for few short rows.  select: a CTA per (sequence, KV head) finds the weight that the cut falls on
-// by a radix select over order-preserving keys (11, 11 and 10 bits), which lie in shared
-// memory as far as they fit, and lists the kept slots; every warp has a contiguous range of
-// slots, so their order costs one scan over warps.  move: a warp per (new page, KV head)
+// Two kernels, and one that does both for few short rows.  select: a CTA per (sequence, KV head)
+// finds the weight that the cut falls on by a radix select over order-preserving keys (11, 11 and
+// 10 bits), which lie in shared memory where all of a row's fit, and are read again for each pass
+// where not, and lists the kept slots; every warp has a contiguous range of slots, so their order
+// costs one scan over warps.  move: a warp per (new page, KV head)
 // gathers the page's 16 keys and values, all in flight together, and their weights.  A
 // block-scaled page takes the largest of its rows' scales; a row from a page of a smaller one
-// is encoded again, value / new scale, which loses only codes that underflow.
+// is encoded again, value / new scale, rounded once; between powers of two that loses only codes
+// that underflow.
 //
 // Bound by memory: every kept row is read and written once, the weights are read once.  64
 // sequences of 3000 to 4224 slots back to 4096, 8 heads of 128 columns in block-scaled codes:

@@ -24,11 +24,12 @@
 //
 // More than 256 query rows of a KV head are taken in passes over the segment's tiles.
 //
-// Bound by shared memory more than by any other unit, as counted from the code: of two tiles' 5000
-// cycles the products read 2310 of operands, the sums 2050 of constants (a 16-byte read gives every
-// lane its copy: 4 cycles), the copies write 260; the exponentials' unit works 2050.  Chunks of 64
-// tokens for 8 sequences of 4096 to 16384, 32 query and 8 KV heads, bf16: 69 us, 38 % of the
-// products' rate; 7000 cycles to begin and 10000 to take up a segment's queries are 14 of them.
+// Bound by turns: an accumulator is filled, then read out, and two of them are not enough to keep
+// either the products or the sums at work all the time.  Chunks of 64 tokens for 8 sequences of 4096
+// to 16384, 32 query and 8 KV heads, bf16: 69 us, 38 % of the products' rate; counters: tensor pipe
+// 45 % active, shared memory's load path 38 % (a column's constant is an address common to a warp,
+// but every lane gets its copy), issue 40 %, the exponentials' unit 30 %.  7000 cycles to begin and
+// 10000 to take up a segment's queries are 14 of them.
 // Measured and worse, against 60 us with two parts: a unit of two tiles by 128 columns (68: half
 // the constants' reads, but both tiles wait for one another), tile by tile (67); a scale for every
 // 16 columns (66), for every column (79); the weights written by the summing warps (69).

@@ -67,6 +67,29 @@ def test_window_attention_of_a_key_scale_that_some_rows_do_not_see(dtype, bad, t
     assert mt.read_status(ws) == 0
 
 
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("t, hq, hkv, d, lens", [(1, 8, 2, 128, [0, 40, 700]), (4, 4, 2, 64, [2000, 1]), (6, 6, 2, 128, [333]), (24, 8, 2, 128, [90, 1500]), (64, 4, 1, 64, [500])])
+@pytest.mark.parametrize("window, sinks, spread", [(0, 0, 2.0), (50, 4, 0.5), (300, 0, 6.0)])
+def test_log_sum_exp_in_32_bits(dtype, t, hq, hkv, d, lens, window, sinks, spread):
+    # Off by what a score is off by: 2 D 2^-24 sum |q k| for products and sums in 32 bits, and for each channel 2^-17 of the
+    # row's largest |q| for what the parts of a query leave; and by 2^-20 of itself, the largest score and 1 for the units,
+    # the exponentials, their sum and its logarithm.  The largest sum |q k| is at most the log-sum-exp of the magnitudes,
+    # sum |k| that of queries of ones.
+    c = _attn_case(np.random.default_rng(77), len(lens), t, hq, hkv, d, lens, dtype, "tree", spread=spread)
+    sm = d ** -0.5
+    for i, n in enumerate(lens):  # no NaN codes in sight of a row, or of its page
+        c["k"][c["table"][i][:-(-n // P)]] &= 0xF7
+    _, _, want = lref.window_attn64(c, window, sinks, sm)
+    mags = dict(c, q=c["q"].abs(), kn=c["kn"].abs(), k=c["k"] & 0x7F)
+    _, _, products = lref.window_attn64(mags, window, sinks, sm)
+    _, _, keys = lref.window_attn64(dict(mags, q=torch.ones_like(c["q"])), window, sinks, sm)
+    top = c["q"].double().abs().amax(-1).numpy()
+    tol = 2 * d * 2.0 ** -24 * products + 2.0 ** -17 * top * keys + 2.0 ** -20 * (1 + np.abs(want) + products)
+    _, lse, ws, _, _ = _window_run(c, window, sinks)
+    off = np.abs(lse.cpu().double().numpy() - want)
+    assert (off <= tol).all(), (np.argwhere(off > tol)[:4], (off / tol).max())
+    assert mt.read_status(ws) == 0
+
 @pytest.mark.parametrize("t, hq, hkv", [(24, 8, 2), (64, 32, 8)])
 def test_a_workspace_without_room_for_depths_serves_the_call_that_has_none(t, hq, hkv):
     # what the call without a window asked for before there was one: all but the last part, the nodes' depths
