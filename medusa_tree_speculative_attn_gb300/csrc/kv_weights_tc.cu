@@ -26,8 +26,8 @@
 //
 // Bound by turns: an accumulator is filled, then read out, and two of them are not enough to keep
 // either the products or the sums at work all the time.  Chunks of 64 tokens for 8 sequences of 4096
-// to 16384, 32 query and 8 KV heads, bf16: 69 us, 38 % of the products' rate; counters: tensor pipe
-// 45 % active, shared memory's load path 38 % (a column's constant is an address common to a warp,
+// to 16384, 32 query and 8 KV heads, bf16: 64 us (in some processes up to 73, by where the buffers
+// lie), 41 % of the products' rate; counters: tensor pipe 45 % active, shared memory's load path 38 % (a column's constant is an address common to a warp,
 // but every lane gets its copy), issue 40 %, the exponentials' unit 30 %.  7000 cycles to begin and
 // 10000 to take up a segment's queries are 14 of them.
 // Measured and worse, against 60 us with two parts: a unit of two tiles by 128 columns (68: half
@@ -433,12 +433,14 @@ __global__ void __launch_bounds__(kThreads, 1)
           const uint64_t kd = desc_rows8<D>(sK_u + st * C::kStage);
           const uint32_t d = tmem + buf * kCols;
           if (tc::elect_one()) {
+            // the smallest parts first: the accumulator cuts what an addition leaves over, and a small
+            // sum loses less (the weights' error 5.0e-7 of the norm with the largest first)
 #pragma unroll
-            for (int part = 0; part < NP; ++part) {
+            for (int part = NP - 1; part >= 0; --part) {
               const uint64_t qd = desc_rows8<D>(sQ_u + part * C::kQPart);
 #pragma unroll
               for (int kk = 0; kk < D / 32; ++kk) {  // 32 codes: 2 descriptor units
-                if (part == 0 && kk == 0) mma_f8_ss<false>(d, kd, qd, idesc);
+                if (part == NP - 1 && kk == 0) mma_f8_ss<false>(d, kd, qd, idesc);
                 else mma_f8_ss<true>(d, kd + (uint64_t)(kk * 2), qd + (uint64_t)(kk * 2), idesc);
               }
             }
