@@ -26,10 +26,10 @@
 //
 // Bound by turns: an accumulator is filled, then read out, and two of them are not enough to keep
 // either the products or the sums at work all the time.  Chunks of 64 tokens for 8 sequences of 4096
-// to 16384, 32 query and 8 KV heads, bf16: 64 us (in some processes up to 73, by where the buffers
-// lie), 41 % of the products' rate; counters: tensor pipe 45 % active, shared memory's load path 38 % (a column's constant is an address common to a warp,
-// but every lane gets its copy), issue 40 %, the exponentials' unit 30 %.  7000 cycles to begin and
-// 10000 to take up a segment's queries are 14 of them.
+// to 16384, 32 query and 8 KV heads, bf16: 64 us (up to 73 in some processes), 41 % of the products'
+// rate; counters: tensor pipe 45 % active, issue 40 %, shared memory's load path 38 % (a column's
+// constant is an address common to a warp, but every lane gets its copy), the exponentials' unit
+// 30 %.  7000 cycles to begin and 10000 to take up a segment's queries are 14 of them.
 // Measured and worse, against 60 us with two parts: a unit of two tiles by 128 columns (68: half
 // the constants' reads, but both tiles wait for one another), tile by tile (67); a scale for every
 // 16 columns (66), for every column (79); the weights written by the summing warps (69).

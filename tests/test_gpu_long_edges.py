@@ -240,3 +240,33 @@ def test_evict_scales_that_are_not_powers_of_two(d, what):
                         nan = row & 0x7F == 0x7F
                         assert np.array_equal(got[to, h, r][~nan], want[~nan]) and (got[to, h, r][nan] & 0x7F == 0x7F).all()
     assert len(tables) > 20 or what == "near 1"
+
+
+def test_evict_again_and_again():
+    # a scale stays when the row that made it goes: over three evictions a value loses no more than what falls below the
+    # smallest code under the largest scale on its way, half of 2^-9 of it each time
+    rng = np.random.default_rng(78)
+    e = Evict(rng, "block8", torch.bfloat16, 2, 64, [700, 333], 256)
+    for x in range(2):
+        e.cache.host[x].view(torch.uint8).numpy()[...] &= 0xF7  # no NaN codes
+        (e.cache.k, e.cache.v)[x].view(torch.uint8).copy_(e.cache.host[x].view(torch.uint8).cuda())
+    value = lambda x, page, h, at: ref.decode(e.cache.host[x].view(torch.uint8).numpy()[page, h, at]) * e.cache.host_scales[x][page, h][..., None]  # noqa: E731
+    first, first_lens = e.table.copy(), list(e.lens)
+    start = [[[value(x, first[b][np.arange(n) // P], h, np.arange(n) % P) for h in range(2)] for b, n in enumerate(first_lens)] for x in range(2)]
+    slots = [[np.arange(n)] * 2 for n in first_lens]  # what is left, by its first slot
+    for budget in (256, 100, 33):
+        e.budget = budget
+        e.run(2, 9)
+        e.check(2, 9)
+        kept = e.kept.cpu().numpy()
+        e.lens = [min(n, budget) for n in e.lens]
+        slots = [[slots[b][h][kept[b, h][:n]] for h in range(2)] for b, n in enumerate(e.lens)]
+        e.table, e.new = e.new, e.table  # the pages that are free again
+    for x in range(2):
+        for b, n in enumerate(e.lens):
+            for h in range(2):
+                at = np.arange(n)
+                pages = e.table[b][at // P]
+                now, then = value(x, pages, h, at % P), start[x][b][h][slots[b][h]]
+                assert (np.abs(now - then) <= 3 * 2.0 ** -10 * e.cache.host_scales[x][pages, h][:, None]).all()
+                assert (np.abs(now - then) > 0).any() or x  # (some did fall below)
